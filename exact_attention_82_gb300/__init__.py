@@ -22,7 +22,9 @@ __all__ = ["fa_fwd", "fa_fwd_raw", "fa_fwd_window", "fa_fwd_window_raw", "fa_str
            "fa_fwd_splitkv", "fa_fwd_splitkv_raw", "fa_fwd_splitkv_workspace_bytes",
            "fa_splitkv_num_splits", "FA_ERR_SCRATCH_LIMIT",
            "fa_bwd", "fa_bwd_raw", "fa_fwd_fp8", "fa_fwd_fp8_raw",
-           "fa_fwd_blockmask", "fa_fwd_blockmask_raw", "FA_ERR_BAD_MASK", "FA_BLOCK_M", "FA_BLOCK_N"]
+           "fa_fwd_blockmask", "fa_fwd_blockmask_raw", "FA_ERR_BAD_MASK", "FA_BLOCK_M", "FA_BLOCK_N",
+           "fa_kv_plan", "fa_kv_plan_raw", "fa_kv_append", "fa_kv_append_raw", "fa_page_select", "fa_page_select_raw",
+           "fa_fwd_paged", "fa_fwd_paged_raw", "fa_fwd_paged_workspace_bytes", "FA_ERR_BAD_PAGE", "FA_PAGE_SIZES"]
 
 FA_OK = 0
 FA_ERR_NULLPTR = -1
@@ -38,14 +40,17 @@ FA_ERR_BAD_WINDOW = -10
 FA_ERR_WORKSPACE = -11
 FA_ERR_SCRATCH_LIMIT = -12
 FA_ERR_BAD_MASK = -13
+FA_ERR_BAD_PAGE = -14
 FA_BLOCK_M = 128  # query rows per block-mask row
 FA_BLOCK_N = 128  # keys per block-mask column
+FA_PAGE_SIZES = (16, 32, 64, 128)  # tokens per page of the paged cache
 
 _lock = threading.Lock()
 _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes), mirroring include/fa.h
 _SIGNATURES = {
@@ -63,6 +68,11 @@ _SIGNATURES = {
     "fa_bwd": (_i, [_vp] * 10 + [_i, _i, _i, _i, _i, ctypes.c_float, _i, _vp]),
     "fa_fwd_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _i,
                         ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp]),
+    "fa_kv_plan": (_i, [_vp] * 9 + [_i] * 6 + [_vp]),
+    "fa_kv_append": (_i, [_vp] * 9 + [_i] * 3 + [_ll] * 2 + [_i] * 2 + [_vp]),
+    "fa_page_select": (_i, [_vp] * 8 + [_i] * 5 + [_ll] + [_i] * 6 + [_vp]),
+    "fa_fwd_paged": (_i, [_vp] * 12 + [_i] * 5 + [ctypes.c_float, _ll] + [_i] * 4 + [_vp, ctypes.c_size_t, _vp]),
+    "fa_fwd_paged_workspace_bytes": (ctypes.c_size_t, [_i] * 5),
     "fa_strerror": (ctypes.c_char_p, [_i]),
     "fa_device_status": (_i, [_vp]),
     "fa_selftest_bounded_wait": (_i, [_i, _vp]),
@@ -346,6 +356,247 @@ def fa_bwd(q, k, v, o, lse, dout, dq=None, dk=None, dv=None, delta=None,
     if st != FA_OK:
         raise FAError(st, "fa_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------ the paged 8-bit cache
+def fa_kv_plan_raw(cached_ptr, new_ptr, free_ptr, count_ptr, table_ptr, cu_q_ptr, lens_ptr, slots_ptr, left_ptr, B, T,
+                   max_pages, num_free, num_pages, page_size, stream_ptr) -> int:
+    """The plan C call with raw device pointers; returns the status code."""
+    return lib().fa_kv_plan(cached_ptr, new_ptr, free_ptr, count_ptr, table_ptr, cu_q_ptr, lens_ptr, slots_ptr, left_ptr,
+                            B, T, max_pages, num_free, num_pages, page_size, stream_ptr)
+
+
+def fa_kv_append_raw(k_ptr, v_ptr, slots_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr, k_mean_ptr,
+                     k_mean_scale_ptr, T, Hkv, D, k_stride, v_stride, num_pages, page_size, stream_ptr) -> int:
+    """The append C call with raw device pointers; returns the status code."""
+    return lib().fa_kv_append(k_ptr, v_ptr, slots_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr, k_mean_ptr,
+                              k_mean_scale_ptr, T, Hkv, D, k_stride, v_stride, num_pages, page_size, stream_ptr)
+
+
+def fa_page_select_raw(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_mean_ptr, k_mean_scale_ptr, sel_ptr, count_ptr, B, T, Hq,
+                       Hkv, D, q_stride, max_pages, num_pages, page_size, top_k, keep_first, keep_last,
+                       stream_ptr) -> int:
+    """The page selection C call with raw device pointers; returns the status code."""
+    return lib().fa_page_select(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_mean_ptr, k_mean_scale_ptr, sel_ptr, count_ptr, B,
+                                T, Hq, Hkv, D, q_stride, max_pages, num_pages, page_size, top_k, keep_first, keep_last,
+                                stream_ptr)
+
+
+def fa_fwd_paged_raw(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr, sel_ptr,
+                     count_ptr, o_ptr, lse_ptr, B, T, Hq, Hkv, D, scale, q_stride, max_pages, num_pages, page_size,
+                     sel_width, ws_ptr, ws_bytes, stream_ptr) -> int:
+    """The paged attention C call with raw device pointers; returns the status code."""
+    return lib().fa_fwd_paged(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr,
+                              sel_ptr, count_ptr, o_ptr, lse_ptr, B, T, Hq, Hkv, D, scale, q_stride, max_pages, num_pages,
+                              page_size, sel_width, ws_ptr, ws_bytes, stream_ptr)
+
+
+def fa_fwd_paged_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> int:
+    return lib().fa_fwd_paged_workspace_bytes(B, T, Hq, Hkv, D)
+
+
+def _check(name, t, dtypes, shape, device, strided=False):
+    """t is a CUDA tensor on `device` of one of `dtypes` and of `shape` (None: any size), contiguous
+    (strided: in all but its first dimension)."""
+    if t.dtype not in dtypes or t.device != device or t.dim() != len(shape):
+        raise ValueError(f"{name} must be a {len(shape)}-dimensional {' or '.join(map(str, dtypes))} tensor on {device}")
+    for n, m in zip(t.shape, shape):
+        if m is not None and n != m:
+            raise ValueError(f"{name} must have the shape {tuple('*' if m is None else m for m in shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous() and not (strided and t.shape[0] > 0 and t[0].is_contiguous()):
+        raise ValueError(f"{name} must be contiguous" + (" but for the stride of its first dimension" if strided else ""))
+
+
+def _token_stride(t) -> int:
+    """Elements between tokens of a [T, H, D] tensor (one token: its own size)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+class _Launch:
+    """A call's device and stream: the device of its tensors is made the current one,
+    and what the call allocates belongs to the stream that it is launched on."""
+
+    def __init__(self, device, stream):
+        import torch
+
+        if device.type != "cuda":
+            raise ValueError("the tensors must be CUDA tensors")
+        self._ctx = []
+        if torch.cuda.current_device() != device.index:
+            self._ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self._ctx.append(torch.cuda.stream(stream))
+        self._device = device
+        self._torch = torch
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        return self._torch.cuda.current_stream(self._device).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def fa_kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_pages: int, page_size: int, cu_q=None,
+               seq_lens=None, slot_map=None, free_left=None, num_tokens: int | None = None, stream=None):
+    """Block tables and slot maps from request lengths, first come, first served.
+
+    cached_lens, new_lens: int32 [B]; free_pages: int32 [num_free], of which the first free_count
+    (int32 [1]) are free and are taken from the end; block_table: int32 [B, max_pages], to which the
+    new pages are added.  slot_map (int32 [T]) or num_tokens says how many tokens there are room for.
+    Returns (cu_q [B+1], seq_lens [B], slot_map [T], free_left [1]), all int32, without synchronising;
+    a request that is not served gets seq_lens 0 and slots of -1."""
+    import torch
+
+    dev, i32 = cached_lens.device, (torch.int32,)
+    with _Launch(dev, stream) as st:
+        B = cached_lens.shape[0]
+        if slot_map is None:
+            if num_tokens is None:
+                raise ValueError("give slot_map or num_tokens")
+            slot_map = torch.empty(num_tokens, dtype=torch.int32, device=dev)
+        T = slot_map.shape[0]
+        cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev) if cu_q is None else cu_q
+        seq_lens = torch.empty(B, dtype=torch.int32, device=dev) if seq_lens is None else seq_lens
+        free_left = torch.empty(1, dtype=torch.int32, device=dev) if free_left is None else free_left
+        for name, t, shape in (("cached_lens", cached_lens, (B,)), ("new_lens", new_lens, (B,)), ("free_pages", free_pages, (None,)),
+                               ("free_count", free_count, (1,)), ("block_table", block_table, (B, None)), ("cu_q", cu_q, (B + 1,)),
+                               ("seq_lens", seq_lens, (B,)), ("slot_map", slot_map, (T,)), ("free_left", free_left, (1,))):
+            _check(name, t, i32, shape, dev)
+        rc = lib().fa_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                              block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), slot_map.data_ptr(),
+                              free_left.data_ptr(), B, T, block_table.shape[1], free_pages.shape[0], num_pages, page_size, st)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_kv_plan")
+    return cu_q, seq_lens, slot_map, free_left
+
+
+def _check_pages(pages, dev):
+    """The shape (num_pages, Hkv, page_size, D) of a cache whose (name, codes, scale) are in `pages`."""
+    import torch
+
+    shape = tuple(pages[0][1].shape)
+    if len(shape) != 4:
+        raise ValueError("pages must be [num_pages, Hkv, page_size, D]")
+    for name, codes, scale in pages:
+        _check(name + "_pages", codes, (torch.float8_e4m3fn, torch.uint8), shape, dev)
+        _check(name + "_scale", scale, (torch.float32,), shape[:2], dev)
+    return shape
+
+
+def fa_kv_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean=None, k_mean_scale=None, stream=None):
+    """Rounds a step's keys and values into the paged 8-bit cache, in place.
+
+    k, v: bf16 [T, Hkv, D], strided over tokens or contiguous; slot_map: int32 [T] (negative: skipped);
+    k_pages, v_pages: uint8 or float8_e4m3fn [num_pages, Hkv, page_size, D]; k_scale, v_scale: fp32
+    [num_pages, Hkv]; k_mean (int8 [num_pages, Hkv, D]) and k_mean_scale (fp32 [num_pages, Hkv]), both or
+    neither, are the pages' mean keys for fa_page_select.  Does not synchronise."""
+    import torch
+
+    dev = k.device
+    with _Launch(dev, stream) as st:
+        num_pages, Hkv, page_size, D = _check_pages((("k", k_pages, k_scale), ("v", v_pages, v_scale)), dev)
+        T = slot_map.shape[0]
+        _check("slot_map", slot_map, (torch.int32,), (None,), dev)
+        _check("k", k, (torch.bfloat16,), (T, Hkv, D), dev, strided=True)
+        _check("v", v, (torch.bfloat16,), (T, Hkv, D), dev, strided=True)
+        if (k_mean is None) != (k_mean_scale is None):
+            raise ValueError("give both of k_mean and k_mean_scale, or neither")
+        if k_mean is not None:
+            _check("k_mean", k_mean, (torch.int8,), (num_pages, Hkv, D), dev)
+            _check("k_mean_scale", k_mean_scale, (torch.float32,), (num_pages, Hkv), dev)
+        rc = lib().fa_kv_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                k_scale.data_ptr(), v_scale.data_ptr(), None if k_mean is None else k_mean.data_ptr(),
+                                None if k_mean is None else k_mean_scale.data_ptr(), T, Hkv, D, _token_stride(k),
+                                _token_stride(v), num_pages, page_size, st)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_kv_append")
+
+
+def _check_queries(q, cu_q, seq_lens, block_table, D):
+    import torch
+
+    T, Hq, B = q.shape[0], q.shape[1], seq_lens.shape[0]
+    dev, i32 = q.device, (torch.int32,)
+    _check("q", q, (torch.bfloat16,), (None, None, D), dev, strided=True)
+    _check("cu_q", cu_q, i32, (B + 1,), dev)
+    _check("seq_lens", seq_lens, i32, (None,), dev)
+    _check("block_table", block_table, i32, (B, None), dev)
+    return B, T, Hq, block_table.shape[1]
+
+
+def fa_page_select(q, cu_q, seq_lens, block_table, k_mean, k_mean_scale, page_size: int, top_k: int, keep_first: int = 1,
+                   keep_last: int = 1, sel=None, sel_count=None, stream=None):
+    """The top_k pages of each sequence and key/value head by the 8-bit score of its queries against
+    the pages' mean keys; the first keep_first and the last keep_last pages are always among them.
+
+    q: bf16 [T, Hq, D], strided over tokens or contiguous; cu_q: int32 [B+1]; seq_lens: int32 [B];
+    block_table: int32 [B, max_pages]; k_mean, k_mean_scale: fa_kv_append's.  Returns (sel, sel_count):
+    int32 [B, Hkv, top_k] of positions in the block table, ascending, -1 behind the last, and int32
+    [B, Hkv].  Does not synchronise."""
+    import torch
+
+    dev = q.device
+    with _Launch(dev, stream) as st:
+        _check("k_mean", k_mean, (torch.int8,), (None, None, None), dev)
+        num_pages, Hkv, D = k_mean.shape
+        _check("k_mean_scale", k_mean_scale, (torch.float32,), (num_pages, Hkv), dev)
+        B, T, Hq, max_pages = _check_queries(q, cu_q, seq_lens, block_table, D)
+        sel = torch.empty((B, Hkv, top_k), dtype=torch.int32, device=dev) if sel is None else sel
+        sel_count = torch.empty((B, Hkv), dtype=torch.int32, device=dev) if sel_count is None else sel_count
+        _check("sel", sel, (torch.int32,), (B, Hkv, top_k), dev)
+        _check("sel_count", sel_count, (torch.int32,), (B, Hkv), dev)
+        rc = lib().fa_page_select(q.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                                  k_mean.data_ptr(), k_mean_scale.data_ptr(), sel.data_ptr(), sel_count.data_ptr(), B, T, Hq,
+                                  Hkv, D, _token_stride(q), max_pages, num_pages, page_size, top_k, keep_first, keep_last, st)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_page_select")
+    return sel, sel_count
+
+
+def fa_fwd_paged(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, sel=None, sel_count=None, o=None,
+                 lse=None, scale: float | None = None, workspace=None, stream=None):
+    """Attention of a step's query tokens (the last ones of their sequences, causal) over the paged
+    8-bit cache, or over the pages that fa_page_select chose.
+
+    q: bf16 [T, Hq, D], strided over tokens or contiguous; cu_q: int32 [B+1]; seq_lens: int32 [B], this
+    step's tokens included; block_table: int32 [B, max_pages]; the cache as in fa_kv_append; sel,
+    sel_count: both or neither.  o (bf16 [T, Hq, D]), lse (fp32 [T, Hq]) and workspace (a CUDA uint8
+    tensor of at least fa_fwd_paged_workspace_bytes(...) bytes) are allocated if not given; rows from
+    cu_q[B] on are not written.  Returns (o, lse) without synchronising."""
+    import torch
+
+    dev = q.device
+    with _Launch(dev, stream) as st:
+        num_pages, Hkv, page_size, D = _check_pages((("k", k_pages, k_scale), ("v", v_pages, v_scale)), dev)
+        B, T, Hq, max_pages = _check_queries(q, cu_q, seq_lens, block_table, D)
+        if (sel is None) != (sel_count is None):
+            raise ValueError("give both of sel and sel_count, or neither")
+        if sel is not None:
+            _check("sel", sel, (torch.int32,), (B, Hkv, None), dev)
+            _check("sel_count", sel_count, (torch.int32,), (B, Hkv), dev)
+        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if o is None else o
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+        _check("o", o, (torch.bfloat16,), (T, Hq, D), dev)
+        _check("lse", lse, (torch.float32,), (T, Hq), dev)
+        if workspace is None:
+            workspace = torch.empty(max(fa_fwd_paged_workspace_bytes(B, T, Hq, Hkv, D), 16), dtype=torch.uint8, device=dev)
+        _check("workspace", workspace, (torch.uint8,), (None,), dev)
+        rc = lib().fa_fwd_paged(q.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                                k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                None if sel is None else sel.data_ptr(), None if sel is None else sel_count.data_ptr(),
+                                o.data_ptr(), lse.data_ptr(), B, T, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale),
+                                _token_stride(q), max_pages, num_pages, page_size, 0 if sel is None else sel.shape[2],
+                                workspace.data_ptr(), workspace.numel(), st)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_fwd_paged")
+    return o, lse
 
 
 def fa_device_status(stream=None) -> int:

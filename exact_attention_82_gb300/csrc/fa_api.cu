@@ -19,6 +19,7 @@ using std::min;
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "fa_paged.h"
 
 namespace {
 
@@ -90,6 +91,9 @@ extern "C" const char *fa_strerror(int status) {
         case FA_ERR_BAD_WINDOW: s = "window bounds must be >= -1, and a bounded window needs Sq == Sk"; break;
         case FA_ERR_WORKSPACE: s = "workspace missing, not 16-byte aligned, or smaller than required"; break;
         case FA_ERR_BAD_MASK: s = "mask_heads must be 1 or B * H, and pair_stride >= 1"; break;
+        case FA_ERR_BAD_PAGE:
+            s = "page size must be 16, 32, 64 or 128 (or, from the status word: a page or position outside the cache)";
+            break;
         case FA_ERR_SCRATCH_LIMIT:
             s = "needs more scratch than the built-in 16 MiB buffer of fa_fwd_splitkv_noalloc holds; "
                 "pass a workspace to fa_fwd_splitkv instead";
@@ -464,12 +468,250 @@ extern "C" int fa_selftest_bwd_timeout(const void *q, const void *k, const void 
     return bwd_checked(q, k, v, o, lse, dout, dq, dk, dv, delta, B, H, Sq, Sk, D, scale, causal, stream, timeout_ns);
 }
 
+// --------------------------------------------------- the paged 8-bit cache
+namespace {
+
+struct Span {
+    const void *ptr;
+    size_t bytes;
+};
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Whether an output overlaps an input or another output.
+template <int NO, int NI>
+bool any_alias(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (int a = 0; a < NO; ++a) {
+        if (!outs[a].ptr) continue;
+        for (int b = 0; b < NI; ++b)
+            if (ins[b].ptr && overlaps(outs[a].ptr, outs[a].bytes, ins[b].ptr, ins[b].bytes)) return true;
+        for (int b = a + 1; b < NO; ++b)
+            if (outs[b].ptr && overlaps(outs[a].ptr, outs[a].bytes, outs[b].ptr, outs[b].bytes)) return true;
+    }
+    return false;
+}
+
+// log2 of the page size, or -1.
+int page_log2_of(int page_size) {
+    return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : page_size == 128 ? 7 : -1;
+}
+
+// What the cache's entry points share; FA_OK when the sizes are in range.
+int check_cache(int B, int T, int Hkv, int D, int max_pages, int num_pages, int page_size) {
+    if (B < 1 || B > 8192 || T < 1 || Hkv < 1 || Hkv > 1024 || max_pages < 1 || num_pages < 1)
+        return FA_ERR_BAD_SHAPE;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED_D;
+    if (page_log2_of(page_size) < 0) return FA_ERR_BAD_PAGE;
+    if ((long long)num_pages * page_size > 0x7fffffffll || (long long)max_pages * page_size > 0x7fffffffll)
+        return FA_ERR_BAD_SHAPE;
+    return FA_OK;
+}
+
+// The stride between tokens of H heads of D elements each.
+bool stride_ok(long long stride, int H, int D) {
+    return stride >= (long long)H * D && stride % 8 == 0 && stride < (1ll << 40);
+}
+
+size_t strided_bytes(int T, long long stride, int H, int D) {
+    return ((size_t)(T - 1) * (size_t)stride + (size_t)H * D) * 2;
+}
+
+}  // namespace
+
+extern "C" int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_count,
+                          int *block_table, int *cu_q, int *seq_lens, int *slot_map, int *free_left, int B, int T,
+                          int max_pages, int num_free, int num_pages, int page_size, void *stream) {
+    const void *ptrs[9] = {cached_lens, new_lens, free_pages, free_count, block_table, cu_q, seq_lens, slot_map, free_left};
+    for (const void *ptr : ptrs)
+        if (!ptr) return FA_ERR_NULLPTR;
+    for (const void *ptr : ptrs)
+        if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
+    if (num_free < 1) return FA_ERR_BAD_SHAPE;
+    const int st = check_cache(B, T, 1, 64, max_pages, num_pages, page_size);
+    if (st != FA_OK) return st;
+    const Span outs[5] = {{block_table, (size_t)B * max_pages * 4}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
+                          {slot_map, (size_t)T * 4}, {free_left, 4}};
+    const Span ins[4] = {{cached_lens, (size_t)B * 4}, {new_lens, (size_t)B * 4}, {free_pages, (size_t)num_free * 4}, {free_count, 4}};
+    if (any_alias(outs, ins)) return FA_ERR_ALIAS;
+    fa::PlanParams p;
+    p.cached = cached_lens;
+    p.fresh = new_lens;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.table = block_table;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.slots = slot_map;
+    p.free_left = free_left;
+    p.B = B;
+    p.T = T;
+    p.max_pages = max_pages;
+    p.num_free = num_free;
+    p.num_pages = num_pages;
+    p.page_log2 = page_log2_of(page_size);
+    const cudaError_t e = fa::launch_kv_plan(p, sm_count(), (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+extern "C" int fa_kv_append(const void *k, const void *v, const int *slot_map, void *k_pages, void *v_pages,
+                            float *k_scale, float *v_scale, signed char *k_mean, float *k_mean_scale, int T, int Hkv,
+                            int D, long long k_stride, long long v_stride, int num_pages, int page_size,
+                            void *stream) {
+    if (!k || !v || !slot_map || !k_pages || !v_pages || !k_scale || !v_scale || (!k_mean != !k_mean_scale))
+        return FA_ERR_NULLPTR;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_mean) ||
+        !aligned4(slot_map) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(k_mean_scale))
+        return FA_ERR_MISALIGNED;
+    const int st = check_cache(1, T, Hkv, D, 1, num_pages, page_size);
+    if (st != FA_OK) return st;
+    if (!stride_ok(k_stride, Hkv, D) || !stride_ok(v_stride, Hkv, D)) return FA_ERR_BAD_SHAPE;
+    const size_t heads = (size_t)num_pages * Hkv, codes = heads * page_size * D;
+    const Span outs[6] = {{k_pages, codes}, {v_pages, codes}, {k_scale, heads * 4}, {v_scale, heads * 4},
+                          {k_mean, heads * D}, {k_mean_scale, heads * 4}};
+    const Span ins[3] = {{k, strided_bytes(T, k_stride, Hkv, D)}, {v, strided_bytes(T, v_stride, Hkv, D)},
+                         {slot_map, (size_t)T * 4}};
+    if (any_alias(outs, ins)) return FA_ERR_ALIAS;
+    fa::AppendParams p;
+    p.x[0] = k;
+    p.x[1] = v;
+    p.stride[0] = k_stride;
+    p.stride[1] = v_stride;
+    p.slots = slot_map;
+    p.pages[0] = static_cast<uint8_t *>(k_pages);
+    p.pages[1] = static_cast<uint8_t *>(v_pages);
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.mean = reinterpret_cast<int8_t *>(k_mean);
+    p.mean_scale = k_mean_scale;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.num_pages = num_pages;
+    p.page_log2 = page_log2_of(page_size);
+    const cudaError_t e = fa::launch_kv_append(D, p, sm_count(), (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+extern "C" int fa_page_select(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                              const signed char *k_mean, const float *k_mean_scale, int *sel, int *sel_count, int B,
+                              int T, int Hq, int Hkv, int D, long long q_stride, int max_pages, int num_pages,
+                              int page_size, int top_k, int keep_first, int keep_last, void *stream) {
+    if (!q || !cu_q || !seq_lens || !block_table || !k_mean || !k_mean_scale || !sel || !sel_count)
+        return FA_ERR_NULLPTR;
+    const void *ints[6] = {cu_q, seq_lens, block_table, k_mean_scale, sel, sel_count};
+    for (const void *ptr : ints)
+        if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned16(k_mean)) return FA_ERR_MISALIGNED;
+    const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
+    if (st != FA_OK) return st;
+    if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || !stride_ok(q_stride, Hq, D) || max_pages > fa::kSelectMaxPages ||
+        top_k < 1 || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > top_k)
+        return FA_ERR_BAD_SHAPE;
+    const Span outs[2] = {{sel, (size_t)B * Hkv * top_k * 4}, {sel_count, (size_t)B * Hkv * 4}};
+    const Span ins[6] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
+                         {block_table, (size_t)B * max_pages * 4}, {k_mean, (size_t)num_pages * Hkv * D},
+                         {k_mean_scale, (size_t)num_pages * Hkv * 4}};
+    if (any_alias(outs, ins)) return FA_ERR_ALIAS;
+    fa::SelectParams p;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.table = block_table;
+    p.mean = reinterpret_cast<const int8_t *>(k_mean);
+    p.mean_scale = k_mean_scale;
+    p.sel = sel;
+    p.sel_count = sel_count;
+    p.B = B;
+    p.T = T;
+    p.G = Hq / Hkv;
+    p.Hkv = Hkv;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.page_log2 = page_log2_of(page_size);
+    p.top_k = top_k;
+    p.keep_first = keep_first;
+    p.keep_last = keep_last;
+    const cudaError_t e = fa::launch_page_select(D, p, (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+static bool paged_shape_ok(int B, int T, int Hq, int Hkv, int D) {
+    return B >= 1 && B <= 8192 && T >= 1 && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
+           (D == 64 || D == 128);
+}
+
+extern "C" size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+    if (!paged_shape_ok(B, T, Hq, Hkv, D)) return 0;
+    return fa::paged_workspace_bytes(B, T, Hq, Hkv, D, sm_count());
+}
+
+extern "C" int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                            const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                            const int *sel, const int *sel_count, void *o, float *lse, int B, int T, int Hq, int Hkv,
+                            int D, float scale, long long q_stride, int max_pages, int num_pages, int page_size,
+                            int sel_width, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !cu_q || !seq_lens || !block_table || !k_pages || !v_pages || !k_scale || !v_scale || !o || !lse ||
+        (!sel != !sel_count))
+        return FA_ERR_NULLPTR;
+    const void *ints[8] = {cu_q, seq_lens, block_table, k_scale, v_scale, sel, sel_count, lse};
+    for (const void *ptr : ints)
+        if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o)) return FA_ERR_MISALIGNED;
+    const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
+    if (st != FA_OK) return st;
+    if (!paged_shape_ok(B, T, Hq, Hkv, D) || !stride_ok(q_stride, Hq, D) || (sel && sel_width < 1))
+        return FA_ERR_BAD_SHAPE;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!isfinite(scale) || !(scale > 0.f) || !isfinite(scale_log2)) return FA_ERR_BAD_SCALE;
+    const size_t need = fa::paged_workspace_bytes(B, T, Hq, Hkv, D, sm_count());
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return FA_ERR_WORKSPACE;
+    const size_t heads = (size_t)num_pages * Hkv, codes = heads * page_size * D;
+    const Span outs[3] = {{o, (size_t)T * Hq * D * 2}, {lse, (size_t)T * Hq * 4}, {workspace, need}};
+    const Span ins[10] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
+                          {block_table, (size_t)B * max_pages * 4}, {k_pages, codes}, {v_pages, codes},
+                          {k_scale, heads * 4}, {v_scale, heads * 4}, {sel, (size_t)B * Hkv * (sel ? sel_width : 0) * 4},
+                          {sel_count, (size_t)B * Hkv * 4}};
+    if (any_alias(outs, ins)) return FA_ERR_ALIAS;
+    fa::PagedParams p;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.table = block_table;
+    p.k_pages = static_cast<const uint8_t *>(k_pages);
+    p.v_pages = static_cast<const uint8_t *>(v_pages);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.sel = sel;
+    p.sel_count = sel_count;
+    p.o = o;
+    p.lse = lse;
+    p.ws = static_cast<float *>(workspace);
+    p.B = B;
+    p.T = T;
+    p.G = Hq / Hkv;
+    p.Hkv = Hkv;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.page_log2 = page_log2_of(page_size);
+    p.sel_width = sel ? sel_width : 0;
+    p.scale_log2 = scale_log2;
+    const cudaError_t e = fa::launch_fwd_paged(D, p, sm_count(), (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
 extern "C" int fa_device_status(void *stream) {
     int v = 0, w = 0, x = 0;
     cudaError_t e = fa::status_read_and_clear(&v, (cudaStream_t)stream);
     if (e == cudaSuccess) e = fa::splitkv_status_read_and_clear(&w);
     if (e == cudaSuccess) e = fa::bwd_status_read_and_clear(&x);
+    int cache[3] = {0, 0, 0};  // the paged cache's kernels
+    if (e == cudaSuccess) e = fa::kv_cache_status_read_and_clear(&cache[0]);
+    if (e == cudaSuccess) e = fa::page_select_status_read_and_clear(&cache[1]);
+    if (e == cudaSuccess) e = fa::paged_status_read_and_clear(&cache[2]);
     if (e != cudaSuccess) return fail_cuda(e);
+    for (int c : cache)
+        if (x == FA_OK) x = c;
     return v != FA_OK ? v : (w != FA_OK ? w : x);
 }
 

@@ -1,0 +1,65 @@
+// fa_paged.h -- declarations of the paged 8-bit cache's kernels, shared by
+// the C-ABI layer and their translation units.  Not part of the public interface.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fa {
+
+struct PlanParams {
+    const int *cached, *fresh;   // [B] tokens in the cache, tokens of this step
+    const int *free_pages, *free_count;
+    int *table;                  // [B, max_pages]
+    int *cu_q, *seq_lens, *slots, *free_left;
+    int B, T, max_pages, num_free, num_pages, page_log2;
+};
+cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream);
+
+struct AppendParams {
+    const void *x[2];            // k, v: bf16 [T, Hkv, D]
+    long long stride[2];         // elements between tokens
+    const int *slots;
+    uint8_t *pages[2];           // k_pages, v_pages
+    float *scale[2];
+    int8_t *mean;                // null: no means are kept
+    float *mean_scale;
+    int T, Hkv, num_pages, page_log2;
+};
+cudaError_t launch_kv_append(int D, const AppendParams &p, int num_sms, cudaStream_t stream);
+
+struct SelectParams {
+    const void *q;               // bf16 [T, Hq, D]
+    long long q_stride;
+    const int *cu_q, *seq_lens, *table;
+    const int8_t *mean;
+    const float *mean_scale;
+    int *sel, *sel_count;
+    int B, T, G, Hkv, max_pages, num_pages, page_log2;
+    int top_k, keep_first, keep_last;
+};
+constexpr int kSelectMaxPages = 49152;  // scores of one (sequence, head) stay in shared memory
+cudaError_t launch_page_select(int D, const SelectParams &p, cudaStream_t stream);
+
+struct PagedParams {
+    const void *q;               // bf16 [T, Hq, D]
+    long long q_stride;
+    const int *cu_q, *seq_lens, *table;
+    const uint8_t *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const int *sel, *sel_count;  // null: every page
+    void *o;                     // bf16 [T, Hq, D]
+    float *lse;                  // fp32 [T, Hq]
+    float *ws;
+    int B, T, G, Hkv, max_pages, num_pages, page_log2, sel_width;
+    float scale_log2;            // scale * log2(e)
+};
+size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms);
+cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream);
+
+// Each translation unit's device status word: read it and reset it.
+cudaError_t kv_cache_status_read_and_clear(int *out);
+cudaError_t page_select_status_read_and_clear(int *out);
+cudaError_t paged_status_read_and_clear(int *out);
+
+}  // namespace fa

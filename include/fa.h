@@ -54,7 +54,9 @@ typedef enum {
     FA_ERR_BAD_WINDOW = -10,        /* window bound below -1, or band with Sq != Sk  */
     FA_ERR_WORKSPACE = -11,         /* workspace missing, misaligned or too small    */
     FA_ERR_SCRATCH_LIMIT = -12,     /* more scratch than the built-in buffer holds   */
-    FA_ERR_BAD_MASK = -13           /* mask heads not 1 or B * H, or pair stride < 1 */
+    FA_ERR_BAD_MASK = -13,          /* mask heads not 1 or B * H, or pair stride < 1 */
+    FA_ERR_BAD_PAGE = -14           /* page size not 16/32/64/128, or (status word) a
+                                       page or position outside the cache             */
 } fa_status;
 
 /*
@@ -257,6 +259,164 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *o,
 int fa_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
            const void *dout, void *dq, void *dk, void *dv, float *delta, int B, int H, int Sq,
            int Sk, int D, float scale, int causal, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The paged 8-bit key/value cache: decode serving.
+ *
+ * A cache holds num_pages pages of page_size tokens (16, 32, 64 or 128) for
+ * each key/value head, in e4m3 codes with one fp32 scale per page and head:
+ *
+ *   k_pages, v_pages   e4m3 [num_pages, Hkv, page_size, D]   value = code * scale
+ *   k_scale, v_scale   fp32 [num_pages, Hkv], finite and > 0
+ *   k_mean             int8 [num_pages, Hkv, D]  and
+ *   k_mean_scale       fp32 [num_pages, Hkv]: the page's mean key, m * scale
+ *                      (only fa_page_select reads them)
+ *
+ * Token t of sequence b is row t % page_size of page block_table[b][t / page_size]
+ * (int32 [B, max_pages]; entries past a sequence's last page are never read).
+ * The step's tokens of all sequences are packed: q [T, Hq, D], o [T, Hq, D],
+ * lse [T, Hq]; those of sequence b are rows cu_q[b] .. cu_q[b+1]-1 (int32
+ * [B+1], ascending from 0) and are its last tokens: with L = seq_lens[b] (int32
+ * [B], this step's tokens included) and n = cu_q[b+1] - cu_q[b], row i of them
+ * is at position L - n + i and sees the keys 0 .. L - n + i.  Rows from cu_q[B]
+ * on (padding) are left as they were.  Query head h reads key/value head
+ * h / (Hq / Hkv).
+ *
+ * One step:  fa_kv_plan -> fa_kv_append -> [fa_page_select ->] fa_fwd_paged.
+ *
+ * Lengths and tables are read on the device, so that a step can be captured in
+ * a graph and replayed with other lengths.  What they hold is checked there:
+ * lengths are clamped to what the table and T hold; a page or position outside
+ * the cache is never read or written, sets FA_ERR_BAD_PAGE in the status word
+ * (fa_device_status), and the rows that would have read it come out NaN.
+ * D is 64 or 128; q, k and v may be strided over tokens (strides in elements,
+ * multiples of 8, each token's heads contiguous).  Tensors of codes and bf16 are
+ * 16-byte aligned, int32 and fp32 arrays 4-byte aligned (FA_ERR_MISALIGNED).
+ * num_pages * page_size < 2^31, B <= 8192, Hkv <= 1024, Hq a multiple of Hkv.
+ * These operations have no counterpart in the pages.
+ */
+
+/*
+ * fa_kv_plan -- block tables and slot maps from request lengths: gives the
+ * pages that a step's new tokens need, first come, first served.
+ *
+ *   cached_lens, new_lens  int32 [B]: tokens in the cache, and of this step
+ *   free_pages             int32 [num_free] page numbers, of which the first
+ *   free_count             int32 [1] are free; pages are taken from the end:
+ *                          the i-th one taken is free_pages[free_count - 1 - i]
+ *   block_table            int32 [B, max_pages], read and written: row b holds
+ *                          ceil(cached/page_size) pages; the new ones are added
+ *   cu_q                   int32 [B+1] written: 0, and the running sums of
+ *                          new_lens (at most T)
+ *   seq_lens               int32 [B] written: cached + new
+ *   slot_map               int32 [T] written: page * page_size + row of each new
+ *                          token; -1 behind the last token
+ *   free_left              int32 [1] written: pages still free
+ *
+ * Request b is served when its lengths are >= 0, cached + new fits in max_pages
+ * pages, and it needs no page or the pages that requests 0 .. b need are free
+ * (a request that does not fit thus keeps later ones from taking pages).  One
+ * that is not served keeps its row of block_table, gets slots of -1 and
+ * seq_lens[b] = 0 (attention writes O = 0, LSE = -inf for its rows); its rows of
+ * q, k and v stay counted in cu_q.  A slot whose page is outside the cache is -1.
+ * Outputs may not overlap inputs or one another (free_left is not free_count).
+ * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE (B, T, max_pages,
+ * num_free or num_pages < 1, or out of range), FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
+ */
+int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_count,
+               int *block_table, int *cu_q, int *seq_lens, int *slot_map, int *free_left, int B, int T,
+               int max_pages, int num_free, int num_pages, int page_size, void *stream);
+
+/*
+ * fa_kv_append -- rounds a step's keys and values into the cache.
+ *
+ *   k, v        bf16 [T, Hkv, D], token strides k_stride, v_stride
+ *   slot_map    int32 [T]; tokens with a negative slot are skipped
+ *   k_pages .. v_scale, k_mean, k_mean_scale   the cache, read and written
+ *               (k_mean and k_mean_scale both NULL: no means are kept)
+ *
+ * Consecutive tokens with consecutive slots in one page are a run.  For each run
+ * and head, with amax = max |x| over its finite values,
+ *   scale = 2^ceil(log2(amax / 448))   (1 for amax = 0; exponent in [-100, 120]),
+ * and, where the run does not begin at row 0 of its page, at least the page's
+ * scale; the rows before it are then rounded again, to code * old / scale.  Codes
+ * are x / scale rounded to nearest even; +-inf become +-448, NaN stays NaN.
+ * The mean is over the page's rows up to the run's last one:
+ *   S_d = sum of codes (NaN as 0), A = max_d |S_d|,
+ *   k_mean_d = rint(S_d * (127 / A)),  k_mean_scale = A * scale / (127 * rows).
+ * Rows behind the run are left as they were.  A page may be in one run of a call
+ * only; with more, what it holds afterwards is undefined.  A slot past the cache
+ * is skipped and sets FA_ERR_BAD_PAGE in the status word.
+ * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
+ * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
+ */
+int fa_kv_append(const void *k, const void *v, const int *slot_map, void *k_pages, void *v_pages,
+                 float *k_scale, float *v_scale, signed char *k_mean, float *k_mean_scale, int T, int Hkv,
+                 int D, long long k_stride, long long v_stride, int num_pages, int page_size, void *stream);
+
+/*
+ * fa_page_select -- the pages that a sequence's queries attend to: the top_k
+ * that an 8-bit score puts first, per sequence and key/value head.
+ *
+ *   q, cu_q, seq_lens, block_table, k_mean, k_mean_scale   as above
+ *   sel        int32 [B, Hkv, top_k] written: positions in the block table,
+ *              ascending; -1 behind the last one
+ *   sel_count  int32 [B, Hkv] written: how many; 0 for a sequence without queries
+ *
+ * Each query row is rounded to 8 bits, q8 = rint(q * (127 / max|q|)) over its
+ * finite values (others count as 0), and
+ *   score(page) = max over the sequence's rows r of the head's query heads of
+ *                 (sum_d q8_rd * k_mean_d) * (max|q_r| / 127) * k_mean_scale,
+ * the sum in integers, so that it is the same whatever its order.  The first
+ * keep_first and the last keep_last pages come before all others, then higher
+ * scores, and the lower position among equals; pages outside the cache last.
+ * top_k >= 1, keep_first, keep_last >= 0, keep_first + keep_last <= top_k.
+ * max_pages <= 49152.
+ * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
+ * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
+ */
+int fa_page_select(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                   const signed char *k_mean, const float *k_mean_scale, int *sel, int *sel_count, int B,
+                   int T, int Hq, int Hkv, int D, long long q_stride, int max_pages, int num_pages,
+                   int page_size, int top_k, int keep_first, int keep_last, void *stream);
+
+/*
+ * fa_fwd_paged -- attention of a step's query tokens over the cache:
+ *   O = softmax(scale q K^T) V,  LSE = ln sum exp(scale q.k_j)  over the keys that
+ * the row sees (above), or those among them in the selected pages.
+ *
+ *   sel, sel_count  both NULL: every page; else int32 [B, Hkv, sel_width] and
+ *                   [B, Hkv], as fa_page_select writes them (any order; a
+ *                   position that is there twice counts twice)
+ *   o               bf16 [T, Hq, D] contiguous, written
+ *   lse             fp32 [T, Hq] contiguous, written
+ *   workspace       caller-owned DEVICE scratch of at least
+ *                   fa_fwd_paged_workspace_bytes(...) bytes, 16-byte aligned; it
+ *                   holds partial results within the call, needs no
+ *                   initialisation, and must not be used by another call until
+ *                   the stream has run past this one
+ *
+ * A row that sees no key gets O = 0, LSE = -inf.  Keys a row does not see never
+ * touch it, whatever their codes are (NaN included).  Scores and sums are fp32;
+ * q and K enter the products exactly (q as bf16 scaled by a power of two to fp16:
+ * a value below 2^-24 of its row's largest is rounded), the softmax weights are
+ * rounded to fp16, O once to bf16.  Any number of query tokens a sequence is
+ * taken; the kernel is made for a few (decode, drafts).  Deterministic; no atomics
+ * on results.
+ * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
+ * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_BAD_SCALE, FA_ERR_WORKSPACE,
+ * FA_ERR_ALIAS; FA_ERR_CUDA if a launch fails.
+ */
+int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                 const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                 const int *sel, const int *sel_count, void *o, float *lse, int B, int T, int Hq, int Hkv,
+                 int D, float scale, long long q_stride, int max_pages, int num_pages, int page_size,
+                 int sel_width, void *workspace, size_t workspace_bytes, void *stream);
+
+/* fa_fwd_paged_workspace_bytes -- bytes of workspace fa_fwd_paged needs on the
+ * current device for these sizes (the same for all lengths); 0 for unsupported sizes. */
+size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 
 /*
  * fa_strerror -- static English text for a status code.  For FA_ERR_CUDA

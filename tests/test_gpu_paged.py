@@ -1,0 +1,490 @@
+"""GPU parity of the paged 8-bit cache's operators (fa_kv_plan, fa_kv_append,
+fa_page_select, fa_fwd_paged) against plain 64-bit implementations of their
+definitions, at the sizes and contents where they can go wrong, and a run of them
+together as a serving loop uses them."""
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_82_gb300 as fa
+import paged_util as pu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status_clean():
+    yield
+    assert fa.fa_device_status() == fa.FA_OK
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# -------------------------------------------------------------------- plan
+def run_plan(cached, new, free, count, table, T, num_pages, page):
+    d_table = i32(table.tolist())
+    cu, lens, slots, left = fa.fa_kv_plan(i32(cached), i32(new), i32(free), i32([count]), d_table, num_pages, page, num_tokens=T)
+    ref = pu.plan(cached, new, free, count, table, T, num_pages, page)
+    for name, a, r in zip(("cu_q", "seq_lens", "slot_map", "left", "table"), (cu, lens, slots, left, d_table), ref):
+        assert np.array_equal(a.cpu().numpy().reshape(np.shape(r)), np.array(r)), name
+
+
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+@pytest.mark.parametrize("B,short", [(1, 1.0), (7, 1.0), (64, 0.6), (300, 1.0), (1025, 0.9), (8192, 0.5)])
+def test_plan(page, B, short):
+    rng = np.random.default_rng(B * 1000 + page)
+    cached = rng.integers(0, 300, size=B)
+    new = np.where(rng.random(B) < 0.5, 1, rng.integers(0, 90 if B > 1000 else 400, size=B))
+    held, need = -(-cached // page), -(-(cached + new) // page)
+    width = int(need.max()) + 1
+    num_pages = int(need.sum()) + 5
+    ids = rng.permutation(num_pages)
+    table = np.full((B, width), -1)
+    for b in range(B):
+        table[b, :held[b]], ids = ids[:held[b]], ids[held[b]:]
+    count = int(short * (need - held).sum())
+    run_plan(cached.tolist(), new.tolist(), ids.tolist(), count, table, int(new.sum()) + 17, num_pages, page)
+
+
+def test_plan_invalid_requests():
+    """Negative lengths, a request longer than its table row, pages outside the cache, too few token slots,
+    and more free pages claimed than the list holds."""
+    table = np.array([[3, -1, -1], [-1] * 3, [40, -1, -1], [2, 6, -1], [-9, -1, -1], [-1] * 3, [-1] * 3])
+    cached, new = [5, -4, 9, 30, 3, 0, 0], [20, 9, 12, 40, 2, 0, 30]
+    for count in (0, 1, 2, 3, 6, 99, -5):
+        run_plan(cached, new, [10, 11, 70, -3, 12, 13], count, table, 118, 30, 16)
+    run_plan(cached, new, [10, 11, 9, 8, 12, 13], 6, table, 20, 30, 16)  # tokens behind T are dropped
+    run_plan([0] * 4, [0] * 4, [1], 1, np.full((4, 1), -1), 3, 4, 128)  # nothing to do
+    big = 2 ** 31 - 1
+    run_plan([big, 0, 1], [big, big, 5], [1, 2], 2, np.full((3, 2), 0), 12, 4, 64)  # sums past 32 bits
+
+
+# ------------------------------------------------------------------ append
+def run_append(lens, new, Hkv, page, D, seed, pad=0, means=True, change=None, gap=False):
+    """Appends `new` tokens behind `lens` cached ones and compares every page and scale."""
+    c = pu.Cache([a + b for a, b in zip(lens, new)], Hkv, page, D, seed)
+    rng = np.random.default_rng(seed)
+    T = sum(new) + pad
+    slots = []
+    for b, (a, n) in enumerate(zip(lens, new)):
+        slots += [int(c.table[b, t // page]) * page + t % page for t in range(a, a + n)]
+    slots = np.array(slots + [-1] * pad, np.int32)
+    if gap:
+        slots[rng.integers(0, T, size=max(1, T // 9))] = -1
+    g = torch.Generator().manual_seed(seed)
+    wide = (torch.randn((T, 2 * Hkv, D), generator=g) * torch.exp(torch.randn((T, 2 * Hkv, 1), generator=g))).to(torch.bfloat16)
+    if change:
+        change(wide)
+    k, v = wide[:, :Hkv], wide[:, Hkv:]
+    dw = wide.cuda()
+    fa.fa_kv_append(dw[:, :Hkv], dw[:, Hkv:], torch.from_numpy(slots).cuda(), *c.pages, k_mean=c.d_mean if means else None,
+                    k_mean_scale=c.d_ms if means else None)
+    mean, ms = c.mean.copy(), c.ms.copy()
+    pu.append(pu.f64(k), slots, c.kc, c.ks, page, *((mean, ms) if means else ()))
+    pu.append(pu.f64(v), slots, c.vc, c.vs, page)
+    for name, a, r in (("k", c.d_kc, c.kc), ("v", c.d_vc, c.vc)):
+        a = pu.codes_of(a)
+        same = (a == r) | (np.isnan(pu.E4M3[a]) & np.isnan(pu.E4M3[r]))
+        assert same.all(), f"{name} codes: {np.argwhere(~same)[:4].tolist()}"
+    assert np.array_equal(pu.f64(c.d_ks), c.ks) and np.array_equal(pu.f64(c.d_vs), c.vs)
+    assert np.array_equal(c.d_mean.cpu().numpy(), mean) and np.array_equal(c.d_ms.cpu().numpy(), ms)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+def test_append_ragged(page, D):
+    lens = [0, 0, 5, page - 1, page, 3 * page + 1, 2 * page - 1, 0, 7]
+    new = [1, 2 * page + 3, 1, 1, 1, page - 1, 2, page, 0]
+    run_append(lens, new, 3, page, D, seed=page + D, pad=5)
+
+
+def test_append_decode_and_prompt_shapes():
+    run_append([i * 3 for i in range(100)], [1] * 100, 2, 64, 128, seed=1)
+    run_append([0], [1500], 1, 64, 64, seed=2)
+    run_append([17], [1500], 2, 16, 128, seed=3, pad=100)
+    run_append([0, 9], [1, 1], 1, 128, 64, seed=4, means=False)
+
+
+def test_append_skipped_tokens_inside_a_batch():
+    run_append([0], [1], 1, 16, 64, seed=5)
+    run_append([3, 40, 0, 11, 16, 20] * 4, [1] * 24, 2, 32, 64, seed=6, gap=True)
+
+
+def test_append_special_values():
+    def change(w):
+        w[0] = 0.0                                  # a page of zeros has scale 1
+        w[1, :, 3], w[1, :, 4] = float("inf"), float("-inf")
+        w[2, :, 5] = float("nan")
+        w[3] = float("nan")
+        w[4] = 1.75 * 2.0 ** -12                    # exactly 448 * 2^-20
+        w[5] = 1e-38                                # below what the smallest scale holds
+        w[6] = 3e38
+        w[7, :, 0] = 1.7578125                      # one step above 448 * 2^-8
+
+    for page in (16, 64):
+        run_append([0, 5, 0, 7, 0, 9, 0, 0], [1] * 8, 2, page, 64, seed=7, change=change)
+    run_append([0, 3], [8, 8], 1, 16, 128, seed=8, change=change)
+
+
+def test_append_bad_slots_are_skipped_and_reported():
+    c = pu.Cache([20], 2, 16, 64, seed=9)
+    before = [t.clone() for t in c.pages]
+    x = torch.randn((4, 2, 64), device="cuda").to(torch.bfloat16)
+    slots = i32([c.num_pages * 16, 2 ** 31 - 1, -1, -2 ** 31])
+    fa.fa_kv_append(x, x.clone(), slots, *c.pages)
+    assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
+    assert all(torch.equal(a, b) for a, b in zip(before, c.pages))
+
+
+# ------------------------------------------------------------------ select
+def run_select(c, q, cu, d_cu, top, first, last):
+    sel, count = fa.fa_page_select(q, d_cu, c.d_lens, c.d_table, c.d_mean, c.d_ms, c.page, top, first, last)
+    rs, rc = pu.select(pu.f64(q), cu, c.lens, c.table, c.mean, c.ms, c.page, top, first, last)
+    assert np.array_equal(count.cpu().numpy(), rc)
+    assert np.array_equal(sel.cpu().numpy(), rs)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 4), (3, 16)])
+@pytest.mark.parametrize("top,first,last", [(1, 0, 0), (4, 1, 1), (8, 0, 8), (33, 2, 1)])
+def test_select(D, Hkv, G, top, first, last):
+    lens = [0, 1, 16, 17, 300, 0, 1600, 16 * top, 16 * top + 1]
+    counts = [0, 1, 1, 2, 1, 1, 5, 1, 2]
+    c = pu.Cache(lens, Hkv, 16, D, seed=D + top)
+    q, cu, d_cu = pu.queries(counts, Hkv * G, D, seed=G, pad=2)
+    run_select(c, q, cu, d_cu, top, first, last)
+
+
+def test_select_ties_and_special_queries():
+    c = pu.Cache([3000, 3000, 900, 640], 2, 16, 64, seed=3)
+    q, cu, d_cu = pu.queries([1, 2, 1, 1], 4, 64, seed=4)
+    c.mean[:] = c.mean[:1, :1]
+    c.ms[:] = 0.25
+    c.mean[::3] = -c.mean[::3]                      # two values: ties all along
+    q[1] = 0.0                                      # every score 0
+    q[3, 0, 5], q[3, 1, 6] = float("nan"), float("inf")
+    q[4] = float("nan")
+    c.d_mean, c.d_ms = torch.from_numpy(c.mean).cuda(), torch.from_numpy(c.ms).cuda()
+    run_select(c, q, cu, d_cu, 20, 1, 2)
+
+
+def test_select_long_sequence():
+    c = pu.Cache([49000], 1, 16, 64, seed=5, num_pages=4000)
+    q, cu, d_cu = pu.queries([1], 8, 64, seed=6)
+    for top in (5, 64, 1000):
+        run_select(c, q, cu, d_cu, top, 1, 2)
+
+
+def test_select_pages_outside_the_cache_come_last():
+    c = pu.Cache([800], 1, 16, 64, seed=5)
+    q, cu, d_cu = pu.queries([1], 2, 64, seed=6)
+    c.table[0, 5:40:3] = [c.num_pages, -1, 2 ** 31 - 1, -2 ** 31] * 3
+    c.d_table = torch.from_numpy(c.table).cuda()
+    run_select(c, q, cu, d_cu, 45, 1, 2)
+    assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
+
+
+# ------------------------------------------------------------------ attend
+def run_attend(c, q, cu, d_cu, sel=None, count=None, scale=None, what="", **kw):
+    T, Hq, D = q.shape
+    o = torch.full((T, Hq, D), 777.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), 777.0, device="cuda")
+    d = {} if sel is None else dict(sel=torch.from_numpy(np.ascontiguousarray(sel, np.int32)).cuda(),
+                                    sel_count=torch.from_numpy(np.ascontiguousarray(count, np.int32)).cuda())
+    fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages, o=o, lse=lse, scale=scale, **d, **kw)
+    torch.cuda.synchronize()
+    rows = int(cu[-1])
+    assert bool((o[rows:] == 777).all()) and bool((lse[rows:] == 777).all()), "padding rows were written"
+    ref = pu.attend(pu.f64(q), cu, c.lens, c.table, c.kc, c.vc, c.ks, c.vs, scale or D ** -0.5, c.page, sel, count)
+    pu.check_attend(o, lse, ref, what, rows)
+    return o, lse
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 3), (1, 8), (2, 16), (1, 40)])
+def test_attend_decode(D, page, Hkv, G):
+    lens = [1, 0, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 700]
+    c = pu.Cache(lens, Hkv, page, D, seed=D + page + G)
+    q, cu, d_cu = pu.queries([0 if L == 0 else 1 for L in lens], Hkv * G, D, seed=G, pad=3)
+    run_attend(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 8, 5])
+def test_attend_several_tokens(D, G):
+    """Causal among a sequence's query tokens; more of them than keys, so that rows see none."""
+    lens, counts = [1, 7, 40, 64, 500, 3, 0, 2, 129, 33], [1, 8, 3, 5, 8, 6, 2, 0, 2, 33]
+    for page in (16, 64):
+        c = pu.Cache(lens, 2, page, D, seed=D + G + page)
+        q, cu, d_cu = pu.queries(counts, 2 * G, D, seed=G, pad=1)
+        run_attend(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+def test_attend_long_and_ragged(page):
+    lens = [5000, 1, 2500, 77, 9001]
+    c = pu.Cache(lens, 2, page, 128, seed=page)
+    q, cu, d_cu = pu.queries([1, 1, 4, 1, 2], 8, 128, seed=page)
+    o1, l1 = run_attend(c, q, cu, d_cu)
+    o2, l2 = run_attend(c, q, cu, d_cu)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2), "not deterministic"
+
+
+def test_attend_many_sequences():
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 150, size=700).tolist()
+    c = pu.Cache(lens, 1, 16, 64, seed=1)
+    q, cu, d_cu = pu.queries(rng.integers(0, 3, size=700).tolist(), 2, 64, seed=2, pad=9)
+    run_attend(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_selected_pages(page, D):
+    rng = np.random.default_rng(page)
+    lens, counts = [1000, page, 3 * page - 1, 0, 777, 5 * page + 1], [1, 1, 2, 1, 3, 1]
+    c = pu.Cache(lens, 2, page, D, seed=D + page)
+    q, cu, d_cu = pu.queries(counts, 8, D, seed=page, pad=2)
+    W = 7
+    sel, count = np.full((6, 2, W), -5), np.zeros((6, 2), int)
+    for b, L in enumerate(lens):
+        n = -(-L // page)
+        for h in range(2):
+            k = int(rng.integers(0, min(n, W) + 1)) if b != 1 else 1
+            sel[b, h, :k], count[b, h] = rng.permutation(n)[:k], k
+    run_attend(c, q, cu, d_cu, sel, count)
+    full = np.full((6, 2, 70), -1)
+    for b, L in enumerate(lens):
+        n = -(-L // page)
+        full[b, :, :n] = np.arange(n)
+    o1, l1 = run_attend(c, q, cu, d_cu, full, np.array([[-(-L // page)] * 2 for L in lens]))
+
+
+def test_attend_masked_values_never_touch_a_row():
+    """NaN codes behind the last key (every Cache holds them), and NaN keys and values that only a
+    sequence's later query tokens see."""
+    lens, counts = [40, 16, 129, 70], [3, 2, 4, 8]
+    for D in (64, 128):
+        c = pu.Cache(lens, 1, 16, D, seed=D)
+        for b, (L, n) in enumerate(zip(lens, counts)):
+            t = L - 1 - b % 2                       # the last or last but one key
+            c.kc[c.table[b, t // 16], 0, t % 16, 3] = 0x7F if b < 2 else c.kc[c.table[b, t // 16], 0, t % 16, 3]
+            c.vc[c.table[b, t // 16], 0, t % 16, 5:9] = 0xFF
+        c.d_kc, c.d_vc = torch.from_numpy(c.kc).cuda(), torch.from_numpy(c.vc).cuda()
+        q, cu, d_cu = pu.queries(counts, 4, D, seed=D)
+        run_attend(c, q, cu, d_cu)
+
+
+def test_attend_peaky_and_uneven_scales():
+    """Scores in the hundreds, and pages whose scales differ by 2^40."""
+    for seed, mult in ((1, 30.0), (2, 1.0)):
+        c = pu.Cache([900, 64, 333], 2, 32, 128, seed=seed)
+        rng = np.random.default_rng(seed)
+        c.vs *= 2.0 ** rng.integers(-20, 20, size=c.vs.shape)
+        c.ks *= 2.0 ** rng.integers(-2, 3, size=c.ks.shape)
+        c.ks[::3] *= 1.37                            # scales need not be powers of two
+        c.ks, c.vs = c.ks.astype(np.float32).astype(np.float64), (c.vs * 1.1).astype(np.float32).astype(np.float64)
+        c.d_ks, c.d_vs = torch.from_numpy(c.ks).float().cuda(), torch.from_numpy(c.vs).float().cuda()
+        q, cu, d_cu = pu.queries([1, 1, 2], 4, 128, seed=seed, mult=mult)
+        run_attend(c, q, cu, d_cu)
+
+
+def test_attend_tiny_and_huge_queries():
+    c = pu.Cache([200, 90], 1, 64, 64, seed=11)
+    q, cu, d_cu = pu.queries([1, 1], 4, 64, seed=11)
+    q[0, 0] *= 2.0 ** -100
+    q[0, 1] = 0.0
+    q[0, 2] *= 2.0 ** 90
+    run_attend(c, q[:1].contiguous(), np.array([0, 1, 1]), i32([0, 1, 1]), scale=2.0 ** -92)
+    q[1, 1, 3] = float("nan")                       # one row's NaN stays in that row
+    o, lse = fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages)
+    assert bool(torch.isnan(o[1, 1]).all()) and bool(torch.isnan(lse[1, 1]))
+    assert bool(torch.isfinite(o[1, [0, 2, 3]]).all()) and bool(torch.isfinite(lse[1, [0, 2, 3]]).all())
+
+
+def test_attend_pages_and_positions_outside_the_cache():
+    c = pu.Cache([100, 100, 100, 100], 2, 16, 64, seed=12)
+    q, cu, d_cu = pu.queries([1, 1, 2, 1], 4, 64, seed=12)
+    c.table[1, 3], c.table[2, 6], c.table[3, 0] = c.num_pages, -1, -2 ** 31
+    c.d_table = torch.from_numpy(c.table).cuda()
+    run_attend(c, q, cu, d_cu)
+    assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
+    sel = np.tile(np.array([0, 2, 5, 6]), (4, 2, 1))
+    sel[0, 0, 1], sel[0, 1, 2] = 7, -1              # behind the sequence, negative
+    sel[2, 0, 3], sel[3, 1, 0] = 2 ** 31 - 1, 1
+    run_attend(c, q, cu, d_cu, sel, np.full((4, 2), 4))
+    assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
+
+
+def test_attend_lengths_past_the_table_are_held_to_it():
+    c = pu.Cache([64, 30], 1, 16, 64, seed=13, extra_cols=0)
+    q, cu, d_cu = pu.queries([1, 1], 2, 64, seed=13)
+    c.lens = [64, -3]
+    c.d_lens = i32([2 ** 31 - 1, -3])
+    run_attend(c, q, cu, d_cu)
+    d_cu = i32([0, 900, 2 ** 31 - 1])               # sums past T: the first sequence has every row
+    o, lse = fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages)
+    ref = pu.attend(pu.f64(q), np.array([0, 2, 2]), [64, 0], c.table, c.kc, c.vc, c.ks, c.vs, 0.125, 16)
+    pu.check_attend(o, lse, ref)
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond 4 GiB of a cache, written and read."""
+    Hkv, page, D, N = 8, 128, 128, 34000
+    kc, vc = (torch.zeros((N, Hkv, page, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones((N, Hkv), device="cuda") for _ in range(2))
+    mean, ms = torch.zeros((N, Hkv, D), dtype=torch.int8, device="cuda"), torch.zeros((N, Hkv), device="cuda")
+    table = i32([[N - 1, 32768, 5]])
+    x = torch.randn((300, 2 * Hkv, D), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    slots = torch.cat([table[0, t // 128] * 128 + t % 128 for t in range(300)][:0] + [table[0].repeat_interleave(128)[:300] * 128 +
+                                                                                  torch.arange(300, device="cuda", dtype=torch.int32) % 128])
+    fa.fa_kv_append(x[:, :Hkv], x[:, Hkv:], slots.to(torch.int32), kc, vc, ks, vs, mean, ms)
+    q, cu, d_cu = pu.queries([2], Hkv * 2, D, seed=3)
+    o, lse = fa.fa_fwd_paged(q, d_cu, i32([300]), table, kc, vc, ks, vs)
+    at = table[0].long()
+    small = [t[at].contiguous() for t in (kc, vc, ks, vs)]
+    ref = pu.attend(pu.f64(q), cu, [300], np.array([[0, 1, 2]]), small[0].cpu().numpy(), small[1].cpu().numpy(), pu.f64(small[2]),
+                    pu.f64(small[3]), D ** -0.5, page)
+    pu.check_attend(o, lse, ref)
+    assert bool((ms[at] > 0).all()) and int(mean[at].abs().amax()) == 127
+    sel, count = fa.fa_page_select(q, d_cu, i32([300]), table, mean, ms, page, 2, 0, 1)
+    rs, _ = pu.select(pu.f64(q), cu, [300], np.array([[0, 1, 2]]), mean[at].cpu().numpy(), ms[at].cpu().numpy(), page, 2, 0, 1)
+    assert np.array_equal(sel.cpu().numpy(), rs)
+
+
+# ------------------------------------------------- streams, graphs, a whole run
+class Serving:
+    """A serving loop over one cache: host-side copies advance by the plain implementations."""
+
+    def __init__(self, B, Hkv, G, page, D, num_pages, width, seed):
+        self.B, self.Hkv, self.G, self.page, self.D, self.N, self.W = B, Hkv, G, page, D, num_pages, width
+        self.rng = np.random.default_rng(seed)
+        shape = (num_pages, Hkv, page, D)
+        self.kc, self.vc = (np.full(shape, 0x7F, np.uint8) for _ in range(2))
+        self.ks, self.vs = (np.ones(shape[:2]) for _ in range(2))
+        self.mean, self.ms = np.zeros((num_pages, Hkv, D), np.int8), np.zeros(shape[:2], np.float32)
+        self.table, self.cached = np.full((B, width), -1), [0] * B
+        self.free, self.count = self.rng.permutation(num_pages).tolist(), num_pages
+        t = lambda a, dt=None: torch.from_numpy(a).to(device="cuda", dtype=dt)  # noqa: E731
+        self.dev = [t(self.kc), t(self.vc), t(self.ks, torch.float32), t(self.vs, torch.float32)]
+        self.d_mean, self.d_ms, self.d_table = t(self.mean), t(self.ms), t(self.table, torch.int32)
+        self.d_free = i32(self.free)
+
+    def tokens(self, T, seed):
+        g = torch.Generator().manual_seed(seed)
+        w = torch.randn((T, (self.G + 2) * self.Hkv, self.D), generator=g).to(torch.bfloat16)
+        a = self.Hkv * self.G
+        return w, (slice(None), slice(0, a)), (slice(None), slice(a, a + self.Hkv)), (slice(None), slice(a + self.Hkv, None))
+
+    def launch(self, cached, new, count, w, slots, top, out, stream=None):
+        """One step on the device, into `out`'s tensors."""
+        a = self.Hkv * self.G
+        q, k, v = w[:, :a], w[:, a:a + self.Hkv], w[:, a + self.Hkv:]
+        fa.fa_kv_plan(cached, new, self.d_free, count, self.d_table, self.N, self.page, cu_q=out["cu"], seq_lens=out["lens"], slot_map=slots,
+                      free_left=out["left"], stream=stream)
+        fa.fa_kv_append(k, v, slots, *self.dev, k_mean=self.d_mean, k_mean_scale=self.d_ms, stream=stream)
+        fa.fa_page_select(q, out["cu"], out["lens"], self.d_table, self.d_mean, self.d_ms, self.page, top, 1, 1, sel=out["sel"],
+                          sel_count=out["count"], stream=stream)
+        fa.fa_fwd_paged(q, out["cu"], out["lens"], self.d_table, *self.dev, o=out["o"], lse=out["lse"], workspace=out["ws"], stream=stream)
+        fa.fa_fwd_paged(q, out["cu"], out["lens"], self.d_table, *self.dev, sel=out["sel"], sel_count=out["count"], o=out["os"],
+                        lse=out["ls"], workspace=out["ws"], stream=stream)
+
+    def outputs(self, T, top):
+        Hq = self.Hkv * self.G
+        z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+        return dict(cu=z(self.B + 1), lens=z(self.B), left=z(1), sel=z(self.B, self.Hkv, top), count=z(self.B, self.Hkv),
+                    o=z(T, Hq, self.D, dt=torch.bfloat16), os=z(T, Hq, self.D, dt=torch.bfloat16), lse=z(T, Hq, dt=torch.float32),
+                    ls=z(T, Hq, dt=torch.float32), ws=z(fa.fa_fwd_paged_workspace_bytes(self.B, T, Hq, self.Hkv, self.D), dt=torch.uint8))
+
+    def check(self, new, w, T, top, out):
+        """The same step by the plain implementations, and the comparison."""
+        cu, lens, slots, left, self.table = pu.plan(self.cached, new, self.free, self.count, self.table, T, self.N, self.page)
+        _, qs, kk, vv = self.tokens(1, 0)
+        x = pu.f64(w)
+        pu.append(x[kk], slots, self.kc, self.ks, self.page, self.mean, self.ms)
+        pu.append(x[vv], slots, self.vc, self.vs, self.page)
+        assert out["cu"].tolist() == cu and out["lens"].tolist() == lens and int(out["left"]) == left
+        assert np.array_equal(self.d_table.cpu().numpy(), self.table)
+        sel, count = pu.select(x[qs], cu, lens, self.table, self.mean, self.ms, self.page, top, 1, 1)
+        assert np.array_equal(out["sel"].cpu().numpy(), sel) and np.array_equal(out["count"].cpu().numpy(), count)
+        args = (x[qs], cu, lens, self.table, self.kc, self.vc, self.ks, self.vs, self.D ** -0.5, self.page)
+        pu.check_attend(out["o"], out["lse"], pu.attend(*args), "all pages", cu[-1])
+        pu.check_attend(out["os"], out["ls"], pu.attend(*args, sel, count), "selected", cu[-1])
+        self.cached = [L if L else c for L, c in zip(lens, self.cached)]
+        self.count = left
+
+
+@pytest.mark.parametrize("page,D", [(16, 64), (64, 128)])
+def test_serving_run(page, D):
+    """Prompts, then decode steps, drafts and a late prompt; pages run out at the end."""
+    s = Serving(5, 2, 4, page, D, num_pages=11 + 224 // page, width=2 + 160 // page, seed=page)
+    steps = [[40, 3, 90, 0, 17], [1, 1, 1, 0, 1], [1, 0, 1, 30, 1], [3, 1, 2, 1, 4], [1, 1, 1, 1, 1], [20, 20, 20, 60, 20]]
+    for i, new in enumerate(steps):
+        T = sum(new) + (3 if i % 2 else 0)
+        w = s.tokens(T, i)[0]
+        out = s.outputs(T, 3)
+        s.launch(i32(s.cached), i32(new), i32([s.count]), w.cuda(), torch.zeros(T, dtype=torch.int32, device="cuda"), 3, out)
+        torch.cuda.synchronize()
+        s.check(new, w, T, 3, out)
+
+
+def test_captured_steps_replayed_with_other_lengths():
+    """One graph of a whole step, replayed while the lengths, tokens and free pages change."""
+    s = Serving(4, 1, 8, 16, 128, num_pages=60, width=12, seed=1)
+    T, top = 64, 4
+    w, slots = s.tokens(T, 0)[0].cuda(), torch.zeros(T, dtype=torch.int32, device="cuda")
+    cached, new, count, out = i32([0] * 4), i32([0] * 4), i32([60]), s.outputs(T, top)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s.launch(cached, new, count, w, slots, top, out, stream=side)   # nothing to do: loads the kernels
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.launch(cached, new, count, w, slots, top, out)
+    for i, step in enumerate([[30, 1, 0, 20], [1, 1, 1, 1], [2, 0, 50, 1], [1, 1, 1, 1], [0, 0, 0, 0]]):
+        hw = s.tokens(T, 10 + i)[0]
+        w.copy_(hw)
+        cached.copy_(i32(s.cached)), new.copy_(i32(step)), count.fill_(s.count)
+        graph.replay()
+        torch.cuda.synchronize()
+        s.check(step, hw, T, top, out)
+
+
+def test_calls_on_several_streams():
+    """Independent calls at the same time, each with its own workspace, give what each gives alone."""
+    made = []
+    for i in range(4):
+        c = pu.Cache([3000 + 100 * i, 17], 2, 64, 128, seed=i)
+        q, cu, d_cu = pu.queries([1, 1], 8, 128, seed=i)
+        made.append((c, q, d_cu, fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(5):
+        got = []
+        for st, (c, q, d_cu, _) in zip(streams, made):
+            st.wait_stream(torch.cuda.current_stream())
+            got.append(fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages, stream=st))
+        torch.cuda.synchronize()
+        for (o, lse), (_, _, _, (ro, rl)) in zip(got, made):
+            assert torch.equal(o, ro) and torch.equal(lse, rl)
+
+
+def test_wrappers_check_their_tensors():
+    c = pu.Cache([40], 2, 16, 64, seed=1)
+    q, cu, d_cu = pu.queries([1], 4, 64, seed=1)
+    ok = dict(q=q, cu_q=d_cu, seq_lens=c.d_lens, block_table=c.d_table, k_pages=c.d_kc, v_pages=c.d_vc, k_scale=c.d_ks, v_scale=c.d_vs)
+    fa.fa_fwd_paged(**ok)
+    for name, bad in (("q", q.float()), ("q", q[:, :, :32]), ("q", q[0]), ("cu_q", d_cu.long()), ("cu_q", d_cu[:1]), ("seq_lens", c.d_lens.cpu()),
+                      ("block_table", c.d_table[0]), ("k_pages", c.d_kc[:, :1]), ("v_pages", c.d_vc.to(torch.int8)), ("k_scale", c.d_ks[:1]),
+                      ("v_scale", c.d_vs.double()), ("sel", i32([[[0], [0]]])), ("workspace", torch.zeros(4, device="cuda"))):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_paged(**{**ok, name: bad})
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_fwd_paged(**ok, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == fa.FA_ERR_WORKSPACE
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_fwd_paged(**{**ok, "q": torch.zeros(1, 3, 64, dtype=torch.bfloat16, device="cuda")})
+    assert e.value.status == fa.FA_ERR_BAD_SHAPE
