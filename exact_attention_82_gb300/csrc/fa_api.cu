@@ -502,7 +502,7 @@ int check_cache(int B, int T, int Hkv, int D, int max_pages, int num_pages, int 
         return FA_ERR_BAD_SHAPE;
     if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED_D;
     if (page_log2_of(page_size) < 0) return FA_ERR_BAD_PAGE;
-    if ((long long)num_pages * page_size > 0x7fffffffll || (long long)max_pages * page_size > 0x7fffffffll)
+    if ((long long)num_pages * Hkv > 0x7fffffffll || (long long)num_pages * page_size > 0x7fffffffll || (long long)max_pages * page_size > 0x7fffffffll)
         return FA_ERR_BAD_SHAPE;
     return FA_OK;
 }

@@ -29,11 +29,14 @@
 // item.
 //
 // Split.  The tiles of all items (sequence, key/value head, 8 or 16 query rows)
-// are laid end to end and cut into equal shares, one a CTA, whatever the lengths:
-// a long sequence is cut over many CTAs, short ones are packed into one.  Lengths
-// are read on the device (a scan of a few hundred integers).  An item that is cut
-// leaves partial results in the workspace, which a second kernel joins; a CTA has
-// at most two of them (the item that it continues, the item that it leaves off).
+// are laid end to end, each item behind a few places that stand for its fixed
+// cost, and the line is cut into equal shares, one a warp, whatever the lengths: a
+// long sequence is cut over many warps, short ones follow one another in one.
+// Lengths are read on the device (a scan of a few hundred integers).  A warp's ring
+// runs on across its items, so that the next one's keys arrive while it writes
+// out the last one's rows.  An item that is cut leaves partial results in the
+// workspace, which a second kernel joins; a warp has at most two of them (the item
+// that it continues, the item that it leaves off).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -51,7 +54,8 @@ constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgTile = 32;         // keys a tile; two halves of 16, each in one page
 constexpr int kPgCtasPerSm = 2;
-constexpr int kPgMinShare = 8;      // tiles: two for each warp
+constexpr int kPgFixed = 2;         // places of the line that an item's fixed cost takes
+constexpr int kPgMinShare = 4;      // places
 constexpr int kPgMaxLen = 0x7fffff00;
 constexpr float kPgShift = 14.f;
 
@@ -64,7 +68,6 @@ struct PgCfg {
     static constexpr int META = 8;                           // words a stage
     static constexpr int OFF_META = kPgWarps * ST * STAGE_BYTES;
     static constexpr int SMEM = OFF_META + kPgWarps * ST * META * 4;
-    static constexpr int ROW = D + 4;                        // floats a row of the join buffers
 };
 
 // A place in the line of tiles.
@@ -98,18 +101,16 @@ __device__ __forceinline__ long long entry_weight(const PagedParams &p, int e, i
     const Seq s = sequence(p, b);
     if (s.nq == 0) return 0;
     const long long rt = ((long long)s.nq * p.G + nr - 1) / nr;
-    return rt * (p.sel ? 1 : p.Hkv) * item_tiles(p, b, h, s.len);
+    return rt * (p.sel ? 1 : p.Hkv) * (kPgFixed + item_tiles(p, b, h, s.len));
 }
 
-// The line of tiles, known to every thread of a block: total and share, and the
-// place of one position (given as a function of the share).
+// Scans the line.  Returns its length and the share of each of `workers` warps,
+// and leaves in found[w] the place where the block's warp w begins.
 struct Line {
     long long total, share;
 };
 
-template <class PosOf>
-__device__ __forceinline__ Line scan_line(const PagedParams &p, int nr, int ctas, PosOf pos_of, Place &place,
-                                          long long *warp_sums, Place *found) {
+__device__ __forceinline__ Line scan_line(const PagedParams &p, int nr, int workers, long long *warp_sums, Place *found) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = p.sel ? p.B * p.Hkv : p.B;
     const int per = (n + kPgThreads - 1) / kPgThreads;
@@ -131,23 +132,57 @@ __device__ __forceinline__ Line scan_line(const PagedParams &p, int nr, int ctas
         if (w < warp) x += warp_sums[w];
         line.total += warp_sums[w];
     }
-    line.share = (line.total + ctas - 1) / ctas;
+    line.share = (line.total + workers - 1) / workers;
     if (line.share < kPgMinShare) line.share = kPgMinShare;
-    const long long pos = pos_of(line);
-    long long lo = x - mine;
-    if (pos >= lo && pos < x) {
-        int e = e0;
-        for (; e < e1 - 1; ++e) {
-            const long long w = entry_weight(p, e, nr);
-            if (pos < lo + w) break;
-            lo += w;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) {
+        const long long pos = (blockIdx.x * kPgWarps + w) * line.share;
+        long long lo = x - mine;
+        if (pos >= lo && pos < x) {
+            int e = e0;
+            for (; e < e1 - 1; ++e) {
+                const long long q = entry_weight(p, e, nr);
+                if (pos < lo + q) break;
+                lo += q;
+            }
+            found[w].entry = e;
+            found[w].base = lo;
         }
-        found->entry = e;
-        found->base = lo;
     }
     __syncthreads();
-    place = *found;
     return line;
+}
+
+// What the line holds at a position.
+struct Item {
+    Seq s;
+    int b, h, tiles;
+    long long first;        // its first place: kPgFixed of them, then its tiles
+    long long row0, rows;   // its first query row, and how many the sequence has for this head
+    int t0, t1;             // the tiles from the position to `end`
+};
+
+__device__ __forceinline__ Item item_at(const PagedParams &p, Place &place, long long pos, long long end, int nr) {
+    Item it;
+    for (;;) {
+        const long long w = entry_weight(p, place.entry, nr);
+        if (pos < place.base + w) break;
+        place.base += w;
+        ++place.entry;
+    }
+    it.b = p.sel ? place.entry / p.Hkv : place.entry;
+    it.h = p.sel ? place.entry % p.Hkv : 0;
+    it.s = sequence(p, it.b);
+    it.tiles = item_tiles(p, it.b, it.h, it.s.len);
+    it.rows = (long long)it.s.nq * p.G;
+    const long long w = kPgFixed + it.tiles, rts = (it.rows + nr - 1) / nr, nth = (pos - place.base) / w;
+    it.first = place.base + nth * w;
+    long long rt = nth;
+    if (!p.sel) it.h = (int)(nth / rts), rt = nth % rts;
+    it.row0 = rt * nr;
+    it.t0 = (int)max(0ll, pos - it.first - kPgFixed);
+    it.t1 = (int)max(0ll, min((long long)it.tiles, end - it.first - kPgFixed));
+    return it;
 }
 
 // ------------------------------------------------------------- instructions
@@ -196,27 +231,31 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Where partial results of CTA c lie: slot 0 for the item that it continues, 1
-// for the one that it leaves off.  [rows] m, [rows] l, [rows][D] sums.
-__device__ __forceinline__ float *slot_of(float *ws, int c, int slot, int nr, int D) {
-    return ws + (2ll * c + slot) * nr * (D + 2);
+// The workspace: for each worker (a warp) what the item that it leaves off needs
+// to be joined, then two slots of partial results: 0 for the item that it continues, 1
+// for the one that it leaves off.  A slot is [rows][D] sums, [rows] m, [rows] l.
+struct Tail {
+    int parts, b, h, tile_of_rows;  // parts 0: no item is left off
+};
+__device__ __forceinline__ Tail *tail_of(float *ws, int worker) { return reinterpret_cast<Tail *>(ws) + worker; }
+__device__ __forceinline__ float *slot_of(float *ws, int workers, int worker, int slot, int nr, int D) {
+    return ws + 4ll * workers + (2ll * worker + slot) * nr * (D + 2);
 }
 
-__device__ __forceinline__ void write_row(const PagedParams &p, const Seq &s, int h, long long row, int D, int d,
-                                          float o, float m, float l) {
-    const long long at = (s.q0 + row / p.G) * ((long long)p.Hkv * p.G) + (long long)h * p.G + row % p.G;
-    static_cast<__nv_bfloat16 *>(p.o)[at * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-    if (d == 0) {
-        // l's exponent is added to m before its mantissa's logarithm: both are near
-        // what LSE is not, and would cost it their rounding
-        const uint32_t u = __float_as_uint(l);
-        const float whole = (float)((int)(u >> 23) - 127) - kPgShift;
-        const float frac = log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
-        float y = ((m + whole) + frac) * 0.69314718055994531f;
-        if (l == 0.f) y = -INFINITY;
-        if (!(l < INFINITY)) y = m + l;
-        p.lse[at] = y;
-    }
+// m - 14 + log2 l in base e.  l's exponent is added to m before its mantissa's
+// logarithm: both are near what LSE is not, and would cost it their rounding.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    const uint32_t u = __float_as_uint(l);
+    const float whole = (float)((int)(u >> 23) - 127) - kPgShift;
+    const float frac = log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+    if (l == 0.f) return -INFINITY;
+    if (!(l < INFINITY)) return m + l;
+    return ((m + whole) + frac) * 0.69314718055994531f;
+}
+
+// The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
+__device__ __forceinline__ long long out_row(const PagedParams &p, const Seq &s, int h, long long row) {
+    return (s.q0 + row / p.G) * ((long long)p.Hkv * p.G) + (long long)h * p.G + row % p.G;
 }
 
 // --------------------------------------------------------------- the kernel
@@ -227,111 +266,120 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
     constexpr int KG = D / 64;  // groups of four 16-byte pieces of a row
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ long long warp_sums[kPgWarps];
-    __shared__ Place found;
-    __shared__ float join_m[kPgWarps][NR], join_l[kPgWarps][NR];
+    __shared__ Place found[kPgWarps];
     grid_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int page = 1 << p.page_log2;
     const uint32_t ring = smem_u32(sm) + warp * C::ST * C::STAGE_BYTES;
     int *const meta_of = reinterpret_cast<int *>(sm + C::OFF_META) + warp * C::ST * C::META;
+    const int workers = gridDim.x * kPgWarps, worker = blockIdx.x * kPgWarps + warp;
 
-    Place place;
-    const Line line = scan_line(
-        p, NR, gridDim.x, [](const Line &l) { return (long long)blockIdx.x * l.share; }, place, warp_sums, &found);
-    long long pos = blockIdx.x * line.share;
+    const Line line = scan_line(p, NR, workers, warp_sums, found);
+    long long pos = worker * line.share;
     const long long end = min(pos + line.share, line.total);
-    while (pos < end) {
-        // ---- the item at pos
-        int b = place.entry, h = 0;
-        if (p.sel) b = place.entry / p.Hkv, h = place.entry % p.Hkv;
-        const Seq s = sequence(p, b);
-        const long long weight = entry_weight(p, place.entry, NR);
-        if (pos >= place.base + weight) {
-            place.base += weight;
-            ++place.entry;
-            continue;
-        }
-        const int tiles = item_tiles(p, b, h, s.len);
-        const long long rts = ((long long)s.nq * p.G + NR - 1) / NR, nth = (pos - place.base) / tiles;
-        const int t0 = (int)((pos - place.base) - nth * tiles), t1 = (int)min((long long)tiles, t0 + (end - pos));
-        long long rt = nth;
-        if (!p.sel) h = (int)(nth / rts), rt = nth % rts;
-        const long long row0 = rt * NR, rows = (long long)s.nq * p.G;
-        const int n_pages = (s.len + page - 1) >> p.page_log2;
-        const long long bh = (long long)b * p.Hkv + h;
-        const int n_sel = p.sel ? max(0, min(p.sel_count[bh], p.sel_width)) : 0;
-        const int *const table = p.table + (long long)b * p.max_pages;
-        const int *const sel = p.sel ? p.sel + bh * p.sel_width : nullptr;
-        const int mine = t1 - t0 > warp ? (t1 - t0 - warp + kPgWarps - 1) / kPgWarps : 0;  // this warp's tiles
+    if (lane == 0) tail_of(p.ws, worker)->parts = 0;
+    if (pos >= end) return;  // no block-wide barrier from here on
+    Place place = found[warp];
 
-        // ---- pages: 16 tiles (32 halves) looked up at a time, a half a lane
-        // key: the half's first key, kPgMaxLen for none; pg: its page, -1 for one outside the cache
-        auto look_up = [&](int i, int &pg, int &key) {
-            const int tile = t0 + warp + (i + (lane >> 1)) * kPgWarps;
+    // ---- pages: up to 16 tiles (32 halves) of one item looked up at a time, a half a
+    // lane, one such batch ahead of the copies
+    // key: the half's first key, kPgMaxLen for none; ph: its page * Hkv + head, -1 for
+    // a page outside the cache; nv: its rows before the end of the sequence
+    Place ahead = place;
+    long long pos_ahead = pos;
+    int ph_now = 0, key_now = 0, nv_now = 0, n_now = 0, at_now = 0;
+    int ph_next, key_next, nv_next, n_next = 0;
+    auto look_up = [&]() {
+        n_next = 0;
+        ph_next = 0, key_next = kPgMaxLen, nv_next = 0;
+        while (pos_ahead < end) {
+            const Item it = item_at(p, ahead, pos_ahead, end, NR);
+            n_next = min(16, it.t1 - it.t0);
+            pos_ahead = it.first + kPgFixed + it.t0 + max(n_next, 0);
+            if (n_next <= 0) {  // the share ends within the item's fixed places
+                n_next = 0;
+                break;
+            }
+            const int tile = it.t0 + (lane >> 1);
             const long long at = (long long)tile * kPgTile + (lane & 1) * 16;
-            pg = 0;
-            key = kPgMaxLen;
-            if (tile >= t1) return;
-            int pos_in = (int)(at >> p.page_log2);
-            if (sel) {
-                if (pos_in >= n_sel) return;
-                pos_in = sel[pos_in];
-                if (pos_in < 0 || pos_in >= n_pages) {
-                    pg = -1, key = 0;
-                    return;
-                }
-                key = (pos_in << p.page_log2) + (int)(at & (page - 1));
-                if (key >= s.len) {
-                    key = kPgMaxLen;
-                    return;
-                }
-            } else {
-                if (at >= s.len) return;
-                key = (int)at;
-            }
-            pg = table[pos_in];
-            if (pg < 0 || pg >= p.num_pages) pg = -1;
-        };
-        int pg_now, key_now, pg_next, key_next;
-        look_up(0, pg_now, key_now);
-        look_up(16, pg_next, key_next);
-        int issued = 0;
-        auto issue = [&]() {
-            if (issued < mine) {
-                const uint32_t st = ring + (issued % C::ST) * C::STAGE_BYTES;
-                int *const meta = meta_of + (issued % C::ST) * C::META;
-                if (issued > 0 && (issued & 15) == 0) {
-                    pg_now = pg_next, key_now = key_next;
-                    look_up(issued + 16, pg_next, key_next);
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int src = ((issued & 15) << 1) + half;
-                    const int pg = __shfl_sync(0xffffffffu, pg_now, src), key = __shfl_sync(0xffffffffu, key_now, src);
-                    const long long ph = (long long)max(pg, 0) * p.Hkv + h;
-                    const long long at = ((ph << p.page_log2) + (key & (page - 1))) * D + lane * 16;
-                    const bool none = pg < 0 || key == kPgMaxLen;
-                    constexpr int PER = C::HALF_BYTES / 512;
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        const int r = j * (16 / PER) + lane / C::CHUNKS, c = lane % C::CHUNKS;
-                        const int n = !none && key + r < s.len ? 16 : 0;  // rows behind the sequence read as 0
-                        const int kx = D == 128 ? c ^ ((r & 1) << 2) : c;
-                        const int vx = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-                        cp_async16(st + half * C::HALF_BYTES + r * D + kx * 16, p.k_pages + (none ? 0 : at + j * 512), n);
-                        cp_async16(st + (2 + half) * C::HALF_BYTES + r * D + vx * 16, p.v_pages + (none ? 0 : at + j * 512), n);
+            if ((lane >> 1) < n_next) {
+                const long long bh = (long long)it.b * p.Hkv + it.h;
+                const int n_pages = (it.s.len + page - 1) >> p.page_log2;
+                long long of = at >> p.page_log2;  // position in the block table
+                bool some = p.sel || at < it.s.len;
+                key_next = some ? (int)at : kPgMaxLen;
+                if (p.sel) {
+                    some = of < min(p.sel_count[bh], p.sel_width);
+                    key_next = kPgMaxLen;
+                    if (some) {
+                        of = p.sel[bh * p.sel_width + of];
+                        if (of < 0 || of >= n_pages) {
+                            some = false;
+                            ph_next = -1, key_next = 0;
+                        } else {
+                            const long long k = (of << p.page_log2) + (at & (page - 1));
+                            some = k < it.s.len;
+                            if (some) key_next = (int)k;
+                        }
                     }
-                    if (lane < 2) cp_async4(smem_u32(meta + 4 + half * 2 + lane), (lane ? p.v_scale : p.k_scale) + ph);
-                    if (lane == 2) meta[half * 2] = key;
-                    if (lane == 3) meta[half * 2 + 1] = pg;
+                }
+                if (some) {
+                    const int pg = p.table[(long long)it.b * p.max_pages + of];
+                    const bool good = pg >= 0 && pg < p.num_pages;
+                    ph_next = good ? pg * p.Hkv + it.h : -1;
+                    nv_next = good ? min(16, it.s.len - key_next) : 0;
                 }
             }
-            cp_commit();
-            ++issued;
-        };
+            break;
+        }
+    };
+    look_up();
+    int stage_in = 0, stage_out = 0;
+    auto issue = [&]() {
+        if (at_now == n_now) {
+            ph_now = ph_next, key_now = key_next, nv_now = nv_next, n_now = n_next;
+            at_now = 0;
+            if (n_now > 0) look_up();
+        }
+        if (at_now < n_now) {
+            const uint32_t st = ring + stage_in * C::STAGE_BYTES;
+            int *const meta = meta_of + stage_in * C::META;
 #pragma unroll
-        for (int i = 0; i < C::ST - 1; ++i) issue();
+            for (int half = 0; half < 2; ++half) {
+                const int src = (at_now << 1) + half;
+                const int ph = __shfl_sync(0xffffffffu, ph_now, src), key = __shfl_sync(0xffffffffu, key_now, src);
+                const int nv = __shfl_sync(0xffffffffu, nv_now, src);
+                const long long at = (((long long)max(ph, 0) << p.page_log2) + (key & (page - 1))) * D + lane * 16;
+                constexpr int PER = C::HALF_BYTES / 512;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int r = j * (16 / PER) + lane / C::CHUNKS, c = lane % C::CHUNKS;
+                    const int n = r < nv ? 16 : 0;  // rows behind the sequence read as 0
+                    const int kx = D == 128 ? c ^ ((r & 1) << 2) : c;
+                    const int vx = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+                    cp_async16(st + half * C::HALF_BYTES + r * D + kx * 16, p.k_pages + at + j * 512, n);
+                    cp_async16(st + (2 + half) * C::HALF_BYTES + r * D + vx * 16, p.v_pages + at + j * 512, n);
+                }
+                if (lane < 2) cp_async4(smem_u32(meta + 4 + half * 2 + lane), (lane ? p.v_scale : p.k_scale) + max(ph, 0));
+                if (lane == 2) meta[half * 2] = key;
+                if (lane == 3) meta[half * 2 + 1] = ph;
+            }
+            ++at_now;
+            stage_in = stage_in + 1 == C::ST ? 0 : stage_in + 1;
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::ST - 1; ++i) issue();
+
+    while (pos < end) {
+        const Item it = item_at(p, place, pos, end, NR);
+        const Seq s = it.s;
+        const int h = it.h, t0 = it.t0, t1 = it.t1;
+        const long long row0 = it.row0, rows = it.rows;
+        pos = it.first + kPgFixed + t1;
+        if (t1 <= t0) break;  // the share ends within the item's fixed places
 
         // ---- query rows: fragments of Q^T (lane: row g of each tile of 8)
         uint32_t qf[NT][KG][4][2];
@@ -391,12 +439,13 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 for (int j = 0; j < 4; ++j) acc[c][nt][j] = 0.f;
         }
 
-        for (int i = 0; i < mine; ++i) {
+        for (int i = t0; i < t1; ++i) {
             cp_wait<C::ST - 2>();
             __syncwarp();
             issue();  // into the stage that the tile before was read from
-            const uint32_t st = ring + (i % C::ST) * C::STAGE_BYTES;
-            const int *const meta = meta_of + (i % C::ST) * C::META;
+            const uint32_t st = ring + stage_out * C::STAGE_BYTES;
+            const int *const meta = meta_of + stage_out * C::META;
+            stage_out = stage_out + 1 == C::ST ? 0 : stage_out + 1;
 
             // ---- S^T = K Q^T: a half of 16 keys an MMA tile.  The order of d within the
             // contraction is free as long as Q's is the same: lane t takes whole 16-byte
@@ -550,11 +599,10 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 }
             }
         }
-        cp_wait<0>();
 
-        // ---- join the warps
-        __syncthreads();
-        float *const join = reinterpret_cast<float *>(sm);  // [warp][NR][ROW], over the ring
+        // ---- write the rows out, or what is known of them
+        const bool whole = t0 == 0 && t1 == it.tiles;
+        float *const part = slot_of(p.ws, workers, worker, t0 == 0 ? 1 : 0, NR, D);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -563,100 +611,126 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 y += __shfl_xor_sync(0xffffffffu, y, 4);
                 y += __shfl_xor_sync(0xffffffffu, y, 8);
                 y += __shfl_xor_sync(0xffffffffu, y, 16);
+                const float base = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
                 const int r = nt * 8 + 2 * t + j;
-                if (g == 0) {
-                    join_m[warp][r] = m[nt][j];
-                    join_l[warp][r] = y;
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < C::CHUNKS; ++c)
+                        *reinterpret_cast<float2 *>(part + r * D + 16 * c + 2 * g) =
+                            make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
+                    if (g == 0) part[NR * D + r] = base, part[NR * D + NR + r] = y;
+                } else if (row0 + r < rows) {
+                    const float inv = y == 0.f ? 0.f : 1.f / y;
+                    const long long at = out_row(p, s, h, row0 + r);
+                    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D + 2 * g);
+#pragma unroll
+                    for (int c = 0; c < C::CHUNKS; ++c)
+                        o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
+                    if (g == 0) p.lse[at] = lse_of(base, y);
                 }
-#pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c)
-                    *reinterpret_cast<float2 *>(join + (warp * NR + r) * C::ROW + 16 * c + 2 * g) =
-                        make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
             }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == tiles;
-        float *const part = slot_of(p.ws, blockIdx.x, t0 == 0 ? 1 : 0, NR, D);
-        for (int i = tid; i < NR * D; i += kPgThreads) {
-            const int r = i / D, d = i % D;
-            float M = -INFINITY, L = 0.f, O = 0.f;
-#pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, join_m[w][r]);
-            const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) {
-                const float f = ex2_approx(join_m[w][r] - base);
-                L = fmaf(join_l[w][r], f, L);
-                O = fmaf(join[(w * NR + r) * C::ROW + d], f, O);
-            }
-            if (whole) {
-                if (row0 + r < rows) write_row(p, s, h, row0 + r, D, d, O, base, L);
-            } else {
-                part[2 * NR + i] = O;
-                if (d == 0) part[r] = base, part[NR + r] = L;
-            }
+        if (t0 == 0 && !whole && lane == 0) {
+            const long long last = (it.first + kPgFixed + it.tiles - 1) / line.share;
+            *tail_of(p.ws, worker) = Tail{(int)last - worker + 1, it.b, h, (int)(row0 / NR)};
         }
-        __syncthreads();
-        pos += t1 - t0;
     }
+    cp_wait<0>();
 }
 
-// Joins the partial results of an item that was cut: block (c, r) has row r of
-// the item that CTA c left off, whose other parts are with the CTAs behind it.
+// Joins the partial results of the items that were cut: a block takes one row of
+// the item that a worker left off at a time, whose other parts are with the
+// workers behind it.  Its warps share the parts.
 template <int D, int NT>
-__global__ void __launch_bounds__(kPgThreads) fa_paged_join_kernel(const PagedParams p, int ctas) {
-    constexpr int NR = 8 * NT;
-    extern __shared__ float weight_of[];  // [ctas]
-    __shared__ long long warp_sums[kPgWarps];
-    __shared__ Place found;
-    __shared__ float red[kPgWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, r = blockIdx.y;
-    Place place;
-    const Line line = scan_line(
-        p, NR, ctas, [c](const Line &l) { return (c + 1) * l.share - 1; }, place, warp_sums, &found);
+__global__ void __launch_bounds__(kPgThreads) fa_paged_join_kernel(const PagedParams p, int workers) {
+    constexpr int NR = 8 * NT, E = D / 32;
+    __shared__ float red_m[kPgWarps], red_l[kPgWarps], red_o[kPgWarps][D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_wait();
-    const long long edge = (c + 1) * line.share;  // where CTA c ends
-    if (edge >= line.total) return;
-    int b = place.entry, h = 0;
-    if (p.sel) b = place.entry / p.Hkv, h = place.entry % p.Hkv;
-    const Seq s = sequence(p, b);
-    const int tiles = item_tiles(p, b, h, s.len);
-    const long long rts = ((long long)s.nq * p.G + NR - 1) / NR, nth = (edge - 1 - place.base) / tiles;
-    const long long first = place.base + nth * tiles, last = first + tiles;  // the item
-    if (first < edge - line.share || last <= edge) return;
-    long long rt = nth;
-    if (!p.sel) h = (int)(nth / rts), rt = nth % rts;
-    const long long row = rt * NR + r;
-    if (row >= (long long)s.nq * p.G) return;
-    const int n = (int)((last - 1) / line.share) - c + 1;  // parts
-    float M = -INFINITY;
-    for (int i = tid; i < n; i += kPgThreads) {
-        const float *part = slot_of(p.ws, c + i, i == 0, NR, D);
-        // a part without keys does not count
-        const float m = part[NR + r] == 0.f ? -INFINITY : part[r];
-        weight_of[i] = m;
-        M = fmaxf(M, m);
-    }
+    // a lane looks at the tail of one of this block's next 32 rows
+    for (int i0 = blockIdx.x; i0 < workers * NR; i0 += 32 * gridDim.x) {
+        const int mine = i0 + lane * gridDim.x;
+        int parts = 0;
+        if (mine < workers * NR) parts = tail_of(p.ws, mine / NR)->parts;
+        uint32_t todo = __ballot_sync(0xffffffffu, parts > 0);
+        while (todo) {
+            const int k = __ffs((int)todo) - 1;
+            todo &= todo - 1;
+            const int i = i0 + k * gridDim.x, worker = i / NR, r = i % NR;
+            const Tail tail = *tail_of(p.ws, worker);
+            const Seq s = sequence(p, tail.b);
+            const long long row = (long long)tail.tile_of_rows * NR + r;
+            if (row >= (long long)s.nq * p.G) continue;
+            float M = -INFINITY, L = 0.f, O[E];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if (lane == 0) red[warp] = M;
-    __syncthreads();
+            for (int e = 0; e < E; ++e) O[e] = 0.f;
+            constexpr int UN = 4;  // parts in flight
+            for (int j0 = warp; j0 < tail.parts; j0 += UN * kPgWarps) {
+                float m[UN], l[UN], o[UN][E];
 #pragma unroll
-    for (int w = 0; w < kPgWarps; ++w) M = fmaxf(M, red[w]);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, O = 0.f;
-    const int d = tid;
-    for (int i = 0; i < n; ++i) {
-        const float *part = slot_of(p.ws, c + i, i == 0, NR, D);
-        const float f = ex2_approx(weight_of[i] - base);
-        L = fmaf(part[NR + r], f, L);
-        if (d < D) O = fmaf(part[2 * NR + r * D + d], f, O);
+                for (int u = 0; u < UN; ++u) {
+                    const int j = j0 + u * kPgWarps;
+                    m[u] = -INFINITY, l[u] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+                    if (j < tail.parts) {
+                        const float *part = slot_of(p.ws, workers, worker + j, j == 0, NR, D);
+                        m[u] = part[NR * D + r];
+                        l[u] = part[NR * D + NR + r];
+                        if (E == 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(part + r * D + 4 * lane);
+                            o[u][0] = x.x, o[u][1] = x.y, o[u][E - 2] = x.z, o[u][E - 1] = x.w;
+                        } else {
+                            const float2 x = *reinterpret_cast<const float2 *>(part + r * D + 2 * lane);
+                            o[u][0] = x.x, o[u][1] = x.y;
+                        }
+                    }
+                }
+                float now = M;
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    if (l[u] == 0.f) m[u] = -INFINITY;  // a part without keys does not count
+                    now = fmaxf(now, m[u]);
+                }
+                const float base = now == -INFINITY ? 0.f : now, f0 = ex2_approx(M - base);
+                M = now;
+                L *= f0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) O[e] *= f0;
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    const float f = ex2_approx(m[u] - base);
+                    L = fmaf(l[u], f, L);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) O[e] = fmaf(o[u][e], f, O[e]);
+                }
+            }
+            __syncthreads();  // the row before is read
+            if (lane == 0) red_m[warp] = M, red_l[warp] = L;
+#pragma unroll
+            for (int e = 0; e < E; ++e) red_o[warp][lane * E + e] = O[e];
+            __syncthreads();
+            float all = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) all = fmaxf(all, red_m[w]);
+            const float base = all == -INFINITY ? 0.f : all;
+            float l = 0.f, o = 0.f;
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) {
+                const float f = ex2_approx(red_m[w] - base);
+                l = fmaf(red_l[w], f, l);
+                if (tid < D) o = fmaf(red_o[w][tid], f, o);
+            }
+            const long long at = out_row(p, s, tail.h, row);
+            if (tid < D) static_cast<__nv_bfloat16 *>(p.o)[at * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+            if (tid == 0) p.lse[at] = lse_of(base, l);
+        }
     }
-    if (d < D) write_row(p, s, h, row, D, d, O, base, L);
 }
 
 size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms) {
     (void)B, (void)T, (void)Hq, (void)Hkv;
-    return (size_t)num_sms * kPgCtasPerSm * 2 * 16 * (D + 2) * sizeof(float);
+    const size_t workers = (size_t)num_sms * kPgCtasPerSm * kPgWarps;
+    return workers * (sizeof(Tail) + 2 * 16 * (D + 2) * sizeof(float));
 }
 
 template <int D, int NT>
@@ -670,21 +744,22 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     // the join is launched while the first kernel still runs, and waits for its end
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, 8 * NT);
+    cfg.gridDim = dim3(4 * num_sms);
     cfg.blockDim = dim3(kPgThreads);
-    cfg.dynamicSmemBytes = ctas * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p, ctas);
+    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p, ctas * kPgWarps);
 }
 
 cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream) {
-    // Rows of an item: 8 while a sequence has no more on average, 16 beyond.
-    const bool wide = (long long)p.T * p.G > 8ll * p.B;
+    // Rows of an item: 8 while a sequence's query rows are no more (by the mean
+    // number of its tokens, padding rounded off), 16 beyond.
+    const long long tokens = (2ll * p.T + p.B) / (2ll * p.B);
+    const bool wide = (tokens > 1 ? tokens : 1) * p.G > 8;
     if (D == 64) return wide ? launch_paged<64, 2>(p, num_sms, stream) : launch_paged<64, 1>(p, num_sms, stream);
     return wide ? launch_paged<128, 2>(p, num_sms, stream) : launch_paged<128, 1>(p, num_sms, stream);
 }

@@ -293,7 +293,7 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * D is 64 or 128; q, k and v may be strided over tokens (strides in elements,
  * multiples of 8, each token's heads contiguous).  Tensors of codes and bf16 are
  * 16-byte aligned, int32 and fp32 arrays 4-byte aligned (FA_ERR_MISALIGNED).
- * num_pages * page_size < 2^31, B <= 8192, Hkv <= 1024, Hq a multiple of Hkv.
+ * num_pages * page_size and num_pages * Hkv < 2^31, B <= 8192, Hkv <= 1024, Hq a multiple of Hkv.
  * These operations have no counterpart in the pages.
  */
 
