@@ -666,6 +666,7 @@ extern "C" int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens,
     const size_t need = fa::paged_workspace_bytes(B, T, Hq, Hkv, D, sm_count());
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return FA_ERR_WORKSPACE;
     const size_t heads = (size_t)num_pages * Hkv, codes = heads * page_size * D;
+    if (heads * page_size > 0xffffffffull) return FA_ERR_BAD_SHAPE;  // rows of a cache: more than memory holds
     const Span outs[3] = {{o, (size_t)T * Hq * D * 2}, {lse, (size_t)T * Hq * 4}, {workspace, need}};
     const Span ins[10] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
                           {block_table, (size_t)B * max_pages * 4}, {k_pages, codes}, {v_pages, codes},

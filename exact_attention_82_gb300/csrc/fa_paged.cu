@@ -4,18 +4,18 @@
 //
 // Mathematics.  For a query row r and key j with codes k_j, v_j and their pages'
 // scales ks_j, vs_j, in base 2 (c = scale log2 e):
-//   x_rj = c ks_j (q_r . k_j) + log2 vs_j,      m_r = max_j x_rj,
-//   w_rj = 2^(x_rj - m_r + 14)                   (the weight of the CODES v_j)
+//   x_rj = c ks_j (q_r . k_j) + log2 vs_j,
+//   w_rj = 2^(x_rj - m_r + 8)                    (the weight of the CODES v_j)
 //   O_r  = sum_j w_rj v_j / l_r,   l_r = sum_j w_rj / vs_j,
-//   LSE_r = ln2 (m_r - 14 + log2 l_r).
-// With the value scale inside the exponent the weights are at most 2^14 however
-// unevenly the pages are scaled, so they can be rounded to fp16 (to 2^-12 of
-// each) with the smallest ones still above fp16's subnormals 2^-24, i.e. 2^-38 of
-// the largest; bf16 would keep three bits less.  l sums the unrounded weights in
-// fp32.  e4m3 codes are exact in fp16, and a query row is scaled by a power of two
-// to a largest element in [1, 2), so that its bf16 values are exact too: both
-// products run on fp16 operands with fp32 accumulators, and nothing but w and O is
-// rounded.
+//   LSE_r = ln2 (m_r - 8 + log2 l_r),
+// for any m_r.  m_r is the largest x_rj so far when it was last taken, and is taken
+// again when some x_rj exceeds it by more than 7, so w is at most 2^15 however
+// unevenly the pages are scaled and can be rounded to fp16 (to 2^-11 of each), whose
+// smallest subnormal is then 2^-32 of the row's largest weight or less; bf16 would
+// keep three bits less.  l sums the unrounded weights in fp32.  e4m3 codes are exact
+// in fp16, and a query row is scaled by a power of two to a largest element in
+// [1, 2), so that its bf16 values are exact too: both products run on fp16 operands
+// with fp32 accumulators, and nothing but w and O is rounded.
 //
 // What bounds it: 2 D bytes read for a key and key/value head and 2 FLOP a byte
 // for each query row, so for a few rows (grouped heads, drafts) the HBM stream.
@@ -57,7 +57,9 @@ constexpr int kPgCtasPerSm = 2;
 constexpr int kPgFixed = 2;         // places of the line that an item's fixed cost takes
 constexpr int kPgMinShare = 4;      // places
 constexpr int kPgMaxLen = 0x7fffff00;
-constexpr float kPgShift = 14.f;
+constexpr float kPgShift = 8.f;    // exponent of a weight at x = m
+constexpr float kPgMost = 15.f;    // and the largest one
+constexpr float kPgNone = -3e38f;  // m before any key
 
 template <int D>
 struct PgCfg {
@@ -65,9 +67,16 @@ struct PgCfg {
     static constexpr int HALF_BYTES = 16 * D;                // 16 rows of K or of V
     static constexpr int STAGE_BYTES = 4 * HALF_BYTES;       // K and V of a tile
     static constexpr int ST = D == 128 ? 3 : 6;              // stages a warp: 96 KB a CTA
-    static constexpr int META = 8;                           // words a stage
-    static constexpr int OFF_META = kPgWarps * ST * STAGE_BYTES;
-    static constexpr int SMEM = OFF_META + kPgWarps * ST * META * 4;
+    static constexpr int OFF_META = kPgWarps * ST * STAGE_BYTES;  // 2 float4 a stage
+    static constexpr int SMEM = OFF_META + kPgWarps * ST * 2 * 16;
+    // Where a 16-byte piece of a row lies: pieces are swapped within 128 bytes so that
+    // eight rows' same piece (ldmatrix) falls into different banks.
+    static __device__ __forceinline__ int swap(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
+    // The key of MMA row g of a half: with bits 0 and 2 of g exchanged, two neighbouring
+    // lanes' rows (D = 128) fall into different banks in 16-byte loads too.
+    static __device__ __forceinline__ int key_of(int g) {
+        return D == 128 ? (g & 2) | ((g & 1) << 2) | (g >> 2) : g;
+    }
 };
 
 // A place in the line of tiles.
@@ -189,8 +198,8 @@ __device__ __forceinline__ Item item_at(const PagedParams &p, Place &place, long
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -242,7 +251,7 @@ __device__ __forceinline__ float *slot_of(float *ws, int workers, int worker, in
     return ws + 4ll * workers + (2ll * worker + slot) * nr * (D + 2);
 }
 
-// m - 14 + log2 l in base e.  l's exponent is added to m before its mantissa's
+// m - 8 + log2 l in base e.  l's exponent is added to m before its mantissa's
 // logarithm: both are near what LSE is not, and would cost it their rounding.
 __device__ __forceinline__ float lse_of(float m, float l) {
     const uint32_t u = __float_as_uint(l);
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
     const int g = lane >> 2, t = lane & 3;
     const int page = 1 << p.page_log2;
     const uint32_t ring = smem_u32(sm) + warp * C::ST * C::STAGE_BYTES;
-    int *const meta_of = reinterpret_cast<int *>(sm + C::OFF_META) + warp * C::ST * C::META;
+    float4 *const meta_of = reinterpret_cast<float4 *>(sm + C::OFF_META) + warp * C::ST * 2;
     const int workers = gridDim.x * kPgWarps, worker = blockIdx.x * kPgWarps + warp;
 
     const Line line = scan_line(p, NR, workers, warp_sums, found);
@@ -284,94 +293,111 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
 
     // ---- pages: up to 16 tiles (32 halves) of one item looked up at a time, a half a
     // lane, one such batch ahead of the copies
-    // key: the half's first key, kPgMaxLen for none; ph: its page * Hkv + head, -1 for
-    // a page outside the cache; nv: its rows before the end of the sequence
     Place ahead = place;
     long long pos_ahead = pos;
-    int ph_now = 0, key_now = 0, nv_now = 0, n_now = 0, at_now = 0;
-    int ph_next, key_next, nv_next, n_next = 0;
+    int ph_next, key_next, nv_next, n_next;  // page * Hkv + head (-1: outside the cache), first key, keys there
     auto look_up = [&]() {
         n_next = 0;
         ph_next = 0, key_next = kPgMaxLen, nv_next = 0;
-        while (pos_ahead < end) {
-            const Item it = item_at(p, ahead, pos_ahead, end, NR);
-            n_next = min(16, it.t1 - it.t0);
-            pos_ahead = it.first + kPgFixed + it.t0 + max(n_next, 0);
-            if (n_next <= 0) {  // the share ends within the item's fixed places
-                n_next = 0;
-                break;
+        if (pos_ahead >= end) return;
+        const Item it = item_at(p, ahead, pos_ahead, end, NR);
+        n_next = max(0, min(16, it.t1 - it.t0));  // 0: the share ends within the item's fixed places
+        pos_ahead = it.first + kPgFixed + it.t0 + n_next;
+        if ((lane >> 1) >= n_next) return;
+        const long long at = (long long)(it.t0 + (lane >> 1)) * kPgTile + (lane & 1) * 16;
+        long long of = at >> p.page_log2;  // position in the block table
+        if (p.sel) {
+            const long long bh = (long long)it.b * p.Hkv + it.h;
+            if (of >= min(p.sel_count[bh], p.sel_width)) return;
+            of = p.sel[bh * p.sel_width + of];
+            const long long k = (of << p.page_log2) + (at & (page - 1));
+            if (of < 0 || of >= (it.s.len + page - 1) >> p.page_log2) {
+                ph_next = -1, key_next = 0;
+                return;
             }
-            const int tile = it.t0 + (lane >> 1);
-            const long long at = (long long)tile * kPgTile + (lane & 1) * 16;
-            if ((lane >> 1) < n_next) {
-                const long long bh = (long long)it.b * p.Hkv + it.h;
-                const int n_pages = (it.s.len + page - 1) >> p.page_log2;
-                long long of = at >> p.page_log2;  // position in the block table
-                bool some = p.sel || at < it.s.len;
-                key_next = some ? (int)at : kPgMaxLen;
-                if (p.sel) {
-                    some = of < min(p.sel_count[bh], p.sel_width);
-                    key_next = kPgMaxLen;
-                    if (some) {
-                        of = p.sel[bh * p.sel_width + of];
-                        if (of < 0 || of >= n_pages) {
-                            some = false;
-                            ph_next = -1, key_next = 0;
-                        } else {
-                            const long long k = (of << p.page_log2) + (at & (page - 1));
-                            some = k < it.s.len;
-                            if (some) key_next = (int)k;
-                        }
-                    }
-                }
-                if (some) {
-                    const int pg = p.table[(long long)it.b * p.max_pages + of];
-                    const bool good = pg >= 0 && pg < p.num_pages;
-                    ph_next = good ? pg * p.Hkv + it.h : -1;
-                    nv_next = good ? min(16, it.s.len - key_next) : 0;
-                }
-            }
-            break;
+            if (k >= it.s.len) return;
+            key_next = (int)k;
+        } else {
+            if (at >= it.s.len) return;
+            key_next = (int)at;
         }
+        const int pg = p.table[(long long)it.b * p.max_pages + of];
+        const bool good = pg >= 0 && pg < p.num_pages;
+        ph_next = good ? pg * p.Hkv + it.h : -1;
+        nv_next = good ? min(16, it.s.len - key_next) : 0;
     };
     look_up();
-    int stage_in = 0, stage_out = 0;
+    // The batch being copied: each lane's half as a row of the cache, and what its
+    // consumer needs (first key, c's key scale or NaN, log2 of the value scale and its
+    // inverse).
+    uint32_t row_now = 0, full_now = 0;
+    int nv_now = 0, n_now = 0, at_now = 0, stage_in = 0;
+    float4 meta_now = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint8_t *const k_lane = p.k_pages + lane * 16, *const v_lane = p.v_pages + lane * 16;
+    const int r_lane = lane / C::CHUNKS;  // row of this lane's piece among those of one copy
+    const uint32_t dst_lane = ring + r_lane * D + ((lane % C::CHUNKS) ^ C::swap(r_lane)) * 16;
+    constexpr int PER = C::HALF_BYTES / 512;           // copies a half
+    constexpr uint32_t ODD = D == 128 ? 64u : 0u;      // every other copy's rows are 4 further
     auto issue = [&]() {
         if (at_now == n_now) {
-            ph_now = ph_next, key_now = key_next, nv_now = nv_next, n_now = n_next;
             at_now = 0;
-            if (n_now > 0) look_up();
+            n_now = n_next;
+            if (n_now > 0) {
+                const bool bad = ph_next < 0;
+                const int ph = max(ph_next, 0);
+                row_now = ((uint32_t)ph << p.page_log2) + (key_next & (page - 1));
+                nv_now = nv_next;
+                full_now = __ballot_sync(0xffffffffu, nv_now == 16);
+                float ks = p.k_scale[ph], vs = p.v_scale[ph];
+                if (bad) {
+                    ks = __int_as_float(0x7fc00000), vs = 1.f;
+                    atomicExch(&g_status_paged, (int)FA_ERR_BAD_PAGE);
+                }
+                const int u = __float_as_int(vs);  // its logarithm, exact for powers of two
+                const float lv = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
+                meta_now = make_float4(__int_as_float(key_next), ks, lv, ex2_approx(-lv));
+                look_up();
+            }
         }
         if (at_now < n_now) {
-            const uint32_t st = ring + stage_in * C::STAGE_BYTES;
-            int *const meta = meta_of + stage_in * C::META;
+            const uint32_t st = dst_lane + stage_in * C::STAGE_BYTES;
+            if ((lane >> 1) == at_now) meta_of[stage_in * 2 + (lane & 1)] = meta_now;
+            const bool full = ((full_now >> (2 * at_now)) & 3u) == 3u;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int src = (at_now << 1) + half;
-                const int ph = __shfl_sync(0xffffffffu, ph_now, src), key = __shfl_sync(0xffffffffu, key_now, src);
-                const int nv = __shfl_sync(0xffffffffu, nv_now, src);
-                const long long at = (((long long)max(ph, 0) << p.page_log2) + (key & (page - 1))) * D + lane * 16;
-                constexpr int PER = C::HALF_BYTES / 512;
+                const uint32_t row = __shfl_sync(0xffffffffu, row_now, 2 * at_now + half);
+                const uint8_t *const ks = k_lane + (unsigned long long)row * D, *const vs = v_lane + (unsigned long long)row * D;
+                if (full) {
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const int r = j * (16 / PER) + lane / C::CHUNKS, c = lane % C::CHUNKS;
-                    const int n = r < nv ? 16 : 0;  // rows behind the sequence read as 0
-                    const int kx = D == 128 ? c ^ ((r & 1) << 2) : c;
-                    const int vx = D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
-                    cp_async16(st + half * C::HALF_BYTES + r * D + kx * 16, p.k_pages + at + j * 512, n);
-                    cp_async16(st + (2 + half) * C::HALF_BYTES + r * D + vx * 16, p.v_pages + at + j * 512, n);
+                    for (int j = 0; j < PER; ++j) {
+                        const uint32_t dst = ((j & 1) ? st ^ ODD : st) + half * C::HALF_BYTES + j * 512;
+                        cp_async16(dst, ks + j * 512);
+                        cp_async16(dst + 2 * C::HALF_BYTES, vs + j * 512);
+                    }
+                } else {  // rows behind the sequence read as 0
+                    const int nv = __shfl_sync(0xffffffffu, nv_now, 2 * at_now + half);
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const uint32_t dst = ((j & 1) ? st ^ ODD : st) + half * C::HALF_BYTES + j * 512;
+                        const int n = j * (16 / PER) + r_lane < nv ? 16 : 0;
+                        cp_async16(dst, ks + j * 512, n);
+                        cp_async16(dst + 2 * C::HALF_BYTES, vs + j * 512, n);
+                    }
                 }
-                if (lane < 2) cp_async4(smem_u32(meta + 4 + half * 2 + lane), (lane ? p.v_scale : p.k_scale) + max(ph, 0));
-                if (lane == 2) meta[half * 2] = key;
-                if (lane == 3) meta[half * 2 + 1] = ph;
             }
             ++at_now;
             stage_in = stage_in + 1 == C::ST ? 0 : stage_in + 1;
         }
         cp_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < C::ST - 1; ++i) issue();
+    // where this lane reads: K rows by 16-byte loads, V rows by ldmatrix
+    const int gk = C::key_of(g);
+    const uint32_t k_read = ring + gk * D + (t ^ C::swap(gk)) * 16;
+    const int v_row = (lane & 24) + C::key_of(lane & 7);
+    const uint32_t v_read = ring + 2 * C::HALF_BYTES + v_row * D + C::swap(v_row) * 16;
+    int stage_out = 0;
 
     while (pos < end) {
         const Item it = item_at(p, place, pos, end, NR);
@@ -407,7 +433,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 }
             am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
             am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            const int e = max(-126, min(126, (int)(am >> 7) - 127));
+            const int e = am ? max(-126, min(126, (int)(am >> 7) - 127)) : 0;
             const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
             for (int i = 0; i < KG; ++i)
@@ -431,7 +457,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
         float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
+            m[nt][0] = m[nt][1] = kPgNone;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c)
@@ -439,23 +465,20 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 for (int j = 0; j < 4; ++j) acc[c][nt][j] = 0.f;
         }
 
+#pragma unroll 1
         for (int i = t0; i < t1; ++i) {
             cp_wait<C::ST - 2>();
             __syncwarp();
             issue();  // into the stage that the tile before was read from
-            const uint32_t st = ring + stage_out * C::STAGE_BYTES;
-            const int *const meta = meta_of + stage_out * C::META;
+            const uint32_t st = stage_out * C::STAGE_BYTES;
+            const float4 meta[2] = {meta_of[stage_out * 2], meta_of[stage_out * 2 + 1]};
+            const int key[2] = {__float_as_int(meta[0].x), __float_as_int(meta[1].x)};
             stage_out = stage_out + 1 == C::ST ? 0 : stage_out + 1;
 
             // ---- S^T = K Q^T: a half of 16 keys an MMA tile.  The order of d within the
             // contraction is free as long as Q's is the same: lane t takes whole 16-byte
             // pieces t and t + 4 of its keys' rows, four MMAs' worth each.
             float sc[2][NT][4];
-            float lv[2], inv_vs[2];
-            int key[2];
-            float mx[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -464,8 +487,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                     for (int j = 0; j < 4; ++j) sc[half][nt][j] = 0.f;
 #pragma unroll
                 for (int kg = 0; kg < KG; ++kg) {
-                    const int c = t + 4 * kg, x = D == 128 ? c ^ ((g & 1) << 2) : c;
-                    const uint32_t at = st + half * C::HALF_BYTES + g * D + x * 16;
+                    const uint32_t at = ((k_read + st) ^ (kg * 64)) + half * C::HALF_BYTES;
                     uint32_t a[4], b8[4];
                     ld_shared_v4(at, a[0], a[1], a[2], a[3]);
                     ld_shared_v4(at + 8 * D, b8[0], b8[1], b8[2], b8[3]);
@@ -478,57 +500,52 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                             mma_f16(sc[half][nt], a0, a1, a2, a3, qf[nt][kg][w][0], qf[nt][kg][w][1]);
                     }
                 }
-                key[half] = meta[half * 2];
-                const bool bad = meta[half * 2 + 1] < 0;
-                float ks = __int_as_float(meta[4 + half * 2]);
-                if (bad) {
-                    ks = __int_as_float(0x7fc00000);
-                    if (lane == 0) atomicExch(&g_status_paged, (int)FA_ERR_BAD_PAGE);
-                }
-                {   // log2 of the value scale, exact for powers of two
-                    const int u = bad ? 0x3f800000 : meta[5 + half * 2];
-                    lv[half] = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
-                }
-                inv_vs[half] = ex2_approx(-lv[half]);
-                const bool masked = key[half] + 16 > lim_min;
+            }
+            // ---- exponents of the weights, against the maximum in use
+            const bool edge = max(key[0], key[1]) + 16 > lim_min;  // some row does not see some key
+            float y[2][NT][4], top = kPgNone;
+            auto exponents = [&](int half, int nt, int j, float off) {
+                float x = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y, meta[half].z + off);
+                if (edge && key[half] + gk + (j >> 1) * 8 >= lim[nt][j & 1]) x = -INFINITY;
+                return x;
+            };
+            if (!edge) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            y[half][nt][j] = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y,
+                                                  meta[half].z + (kPgShift - m[nt][j & 1]));
+                            top = fmaxf(top, y[half][nt][j]);
+                        }
+            }
+            if (__any_sync(0xffffffffu, edge || top > kPgMost)) {
+                // a new maximum: the sums so far are scaled to it
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float y = fmaf(sc[half][nt][j], fac[nt][j & 1] * ks, lv[half]);
-                        if (masked && key[half] + g + (j >> 1) * 8 >= lim[nt][j & 1]) y = -INFINITY;
-                        sc[half][nt][j] = y;
-                        mx[nt][j & 1] = fmaxf(mx[nt][j & 1], y);
+                    for (int j = 0; j < 2; ++j) {
+                        float x = kPgNone;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            x = fmaxf(x, fmaxf(exponents(half, nt, j, 0.f), exponents(half, nt, j + 2, 0.f)));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        x = fmaxf(x, m[nt][j]);
+                        const float f = ex2_approx(m[nt][j] - x);
+                        m[nt][j] = x;
+                        l[nt][j] *= f;
+#pragma unroll
+                        for (int c = 0; c < C::CHUNKS; ++c) acc[c][nt][j] *= f, acc[c][nt][j + 2] *= f;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            y[half][nt][j] = exponents(half, nt, j, kPgShift - x);
+                            y[half][nt][j + 2] = exponents(half, nt, j + 2, kPgShift - x);
+                        }
                     }
-            }
-            // ---- running maximum; the sums are scaled where it grew
-            bool grew = false;
-            float corr[NT][2], off[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float y = mx[nt][j];
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                    y = fmaxf(y, m[nt][j]);
-                    const float base = y == -INFINITY ? 0.f : y;
-                    grew |= y > m[nt][j];
-                    corr[nt][j] = ex2_approx(m[nt][j] - base);
-                    off[nt][j] = kPgShift - base;
-                    m[nt][j] = y;
-                }
-            if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    l[nt][0] *= corr[nt][0];
-                    l[nt][1] *= corr[nt][1];
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[c][nt][j] *= corr[nt][j & 1];
-                }
             }
             // ---- weights, and their transpose as the B operand (keys x rows)
             uint32_t wf[2][NT][2];
@@ -539,15 +556,15 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                     float w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        w[j] = ex2_approx(sc[half][nt][j] + off[nt][j & 1]);
-                        l[nt][j & 1] = fmaf(w[j], inv_vs[half], l[nt][j & 1]);
+                        w[j] = ex2_approx(y[half][nt][j]);
+                        l[nt][j & 1] = fmaf(w[j], meta[half].w, l[nt][j & 1]);
                     }
                     wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
                     wf[half][nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
                 }
             // ---- O^T += V^T W^T.  A pair of bytes is one 16-bit element for ldmatrix, so
-            // a transposed tile holds d = 2g, 2g+1 of two neighbouring keys in a register;
-            // their bytes are sorted by d before the conversion.
+            // a transposed tile holds d = 2g, 2g+1 of two keys in a register; their bytes
+            // are sorted by d before the conversion.
             auto accumulate = [&](auto keep, auto settle) {
 #pragma unroll
                 for (int c = 0; c < C::CHUNKS; ++c) {
@@ -556,9 +573,8 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) was[nt][j] = acc[c][nt][j];
-                    const int x = D == 128 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3);
                     uint32_t r[4];
-                    ldmatrix_x4_trans(st + 2 * C::HALF_BYTES + lane * D + x * 16, r);
+                    ldmatrix_x4_trans((v_read + st) ^ (c * 16), r);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t lo = __byte_perm(keep(r[2 * half], half, 0), 0, 0x3120);
@@ -575,7 +591,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                         for (int j = 0; j < 4; ++j) acc[c][nt][j] = settle(acc[c][nt][j], was[nt][j], nt, j & 1);
                 }
             };
-            if (max(key[0], key[1]) + 16 <= lim_min || lim_min >= s.len) {
+            if (!edge || lim_min >= s.len) {
                 accumulate([](uint32_t r, int, int) { return r; }, [](float now, float, int, int) { return now; });
             } else {
                 // Some rows do not see all of these keys: a weight of 0 would still turn a
@@ -583,6 +599,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 // are cleared, a token at a time, and only that token's rows take the
                 // result (only the last tiles of a sequence come here).
                 const int tok0 = (int)(row0 / p.G), tok1 = (int)min((long long)s.nq - 1, (row0 + NR - 1) / p.G);
+#pragma unroll 1
                 for (int tok = tok0; tok <= tok1; ++tok) {
                     const int limit = s.len - s.nq + tok + 1;
                     bool my[NT][2];
@@ -592,8 +609,9 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                         for (int j = 0; j < 2; ++j) my[nt][j] = (row0 + nt * 8 + 2 * t + j) / p.G == tok;
                     accumulate(
                         [&](uint32_t r, int half, int up) {
-                            const int k = key[half] + up * 8 + 2 * t;
-                            return r & ((k < limit ? 0xffffu : 0u) | (k + 1 < limit ? 0xffff0000u : 0u));
+                            const int k = key[half] + up * 8;
+                            return r & ((k + C::key_of(2 * t) < limit ? 0xffffu : 0u) |
+                                        (k + C::key_of(2 * t + 1) < limit ? 0xffff0000u : 0u));
                         },
                         [&](float now, float before, int nt, int j) { return my[nt][j] ? now : before; });
                 }
@@ -611,7 +629,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 y += __shfl_xor_sync(0xffffffffu, y, 4);
                 y += __shfl_xor_sync(0xffffffffu, y, 8);
                 y += __shfl_xor_sync(0xffffffffu, y, 16);
-                const float base = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+                const float base = m[nt][j];
                 const int r = nt * 8 + 2 * t + j;
                 if (!whole) {
 #pragma unroll
