@@ -126,8 +126,13 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const PlanPara
             const Request r = plan_request(p, b);
             if (r.valid && (r.need == 0 || (long long)pc[b] + r.need <= free_count)) {
                 const int pos = r.cached + (i - cu[b]), ord = pos >> p.page_log2;
-                const int pg = ord < r.held ? p.table[(long long)b * p.max_pages + ord]
-                                            : p.free_pages[free_count - 1 - (pc[b] + ord - r.held)];
+                // (in range, unless the caller changes the lengths during the call)
+                const int of = free_count - 1 - (pc[b] + ord - r.held);
+                int pg = -1;
+                if (ord < r.held && ord < p.max_pages)
+                    pg = p.table[(long long)b * p.max_pages + ord];
+                else if (of >= 0 && of < free_count)
+                    pg = p.free_pages[of];
                 if (pg >= 0 && pg < p.num_pages) slot = pg * page + (pos & (page - 1));
             }
         }
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const PlanPara
     for (int i = me; i < min(pc[p.B], free_count); i += step) {
         const int b = count_le(pc + 1, p.B, i);
         const Request r = plan_request(p, b);
-        if ((long long)pc[b] + r.need <= free_count)
+        if ((long long)pc[b] + r.need <= free_count && r.held + (i - pc[b]) < p.max_pages)
             p.table[(long long)b * p.max_pages + r.held + (i - pc[b])] = p.free_pages[free_count - 1 - i];
     }
 }

@@ -172,22 +172,24 @@ struct Item {
 };
 
 __device__ __forceinline__ Item item_at(const PagedParams &p, Place &place, long long pos, long long end, int nr) {
+    // The scan's lengths and these are the same unless the caller changes them during
+    // the call; the bounds on entry, head and parts keep every access inside even then.
     Item it;
-    for (;;) {
+    const int n = p.sel ? p.B * p.Hkv : p.B;
+    for (; place.entry < n - 1; ++place.entry) {
         const long long w = entry_weight(p, place.entry, nr);
         if (pos < place.base + w) break;
         place.base += w;
-        ++place.entry;
     }
     it.b = p.sel ? place.entry / p.Hkv : place.entry;
     it.h = p.sel ? place.entry % p.Hkv : 0;
     it.s = sequence(p, it.b);
     it.tiles = item_tiles(p, it.b, it.h, it.s.len);
     it.rows = (long long)it.s.nq * p.G;
-    const long long w = kPgFixed + it.tiles, rts = (it.rows + nr - 1) / nr, nth = (pos - place.base) / w;
+    const long long w = kPgFixed + it.tiles, rts = max(1ll, (it.rows + nr - 1) / nr), nth = (pos - place.base) / w;
     it.first = place.base + nth * w;
     long long rt = nth;
-    if (!p.sel) it.h = (int)(nth / rts), rt = nth % rts;
+    if (!p.sel) it.h = (int)min(nth / rts, p.Hkv - 1ll), rt = nth % rts;
     it.row0 = rt * nr;
     it.t0 = (int)max(0ll, pos - it.first - kPgFixed);
     it.t1 = (int)max(0ll, min((long long)it.tiles, end - it.first - kPgFixed));
@@ -649,7 +651,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
             }
         if (t0 == 0 && !whole && lane == 0) {
             const long long last = (it.first + kPgFixed + it.tiles - 1) / line.share;
-            *tail_of(p.ws, worker) = Tail{(int)last - worker + 1, it.b, h, (int)(row0 / NR)};
+            *tail_of(p.ws, worker) = Tail{min((int)last, workers - 1) - worker + 1, it.b, h, (int)(row0 / NR)};
         }
     }
     cp_wait<0>();
