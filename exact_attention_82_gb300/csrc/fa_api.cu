@@ -659,7 +659,8 @@ extern "C" int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens,
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o)) return FA_ERR_MISALIGNED;
     const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
     if (st != FA_OK) return st;
-    if (!paged_shape_ok(B, T, Hq, Hkv, D) || !stride_ok(q_stride, Hq, D) || (sel && sel_width < 1))
+    if (!paged_shape_ok(B, T, Hq, Hkv, D) || !stride_ok(q_stride, Hq, D) || (sel && sel_width < 1) ||
+        (long long)T * Hq > 0x7fffffff)
         return FA_ERR_BAD_SHAPE;
     const float scale_log2 = scale * 1.4426950408889634f;
     if (!isfinite(scale) || !(scale > 0.f) || !isfinite(scale_log2)) return FA_ERR_BAD_SCALE;

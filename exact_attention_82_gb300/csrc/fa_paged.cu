@@ -31,12 +31,14 @@
 // Split.  The tiles of all items (sequence, key/value head, 8 or 16 query rows)
 // are laid end to end, each item behind a few places that stand for its fixed
 // cost, and the line is cut into equal shares, one a warp, whatever the lengths: a
-// long sequence is cut over many warps, short ones follow one another in one.
-// Lengths are read on the device (a scan of a few hundred integers).  A warp's ring
-// runs on across its items, so that the next one's keys arrive while it writes
-// out the last one's rows.  An item that is cut leaves partial results in the
-// workspace, which a second kernel joins; a warp has at most two of them (the item
-// that it continues, the item that it leaves off).
+// long sequence is cut over many warps, short ones follow one another in one (and
+// are not cut at all where a share holds two of them).  Lengths are read on the
+// device (a scan of a few hundred integers).  A warp's ring runs on across its
+// items, so that the next one's keys arrive while it writes out the last one's rows.
+// Warps of a block whose whole share lies in one item are joined in shared memory;
+// what is still cut leaves partial results in the workspace, which a second kernel
+// joins.  A warp leaves at most two of them (for the item that it continues, and the
+// one that it leaves off).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -50,10 +52,7 @@ namespace fa {
 
 static __device__ int g_status_paged = 0;
 
-constexpr int kPgWarps = 4;
-constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgTile = 32;         // keys a tile; two halves of 16, each in one page
-constexpr int kPgCtasPerSm = 2;
 constexpr int kPgFixed = 2;         // places of the line that an item's fixed cost takes
 constexpr int kPgMinShare = 4;      // places
 constexpr int kPgMaxLen = 0x7fffff00;
@@ -61,14 +60,17 @@ constexpr float kPgShift = 8.f;    // exponent of a weight at x = m
 constexpr float kPgMost = 15.f;    // and the largest one
 constexpr float kPgNone = -3e38f;  // m before any key
 
-template <int D>
+template <int D, int NT>
 struct PgCfg {
     static constexpr int CHUNKS = D / 16;                    // 16-byte pieces of a row
     static constexpr int HALF_BYTES = 16 * D;                // 16 rows of K or of V
     static constexpr int STAGE_BYTES = 4 * HALF_BYTES;       // K and V of a tile
-    static constexpr int ST = D == 128 ? 3 : 6;              // stages a warp: 96 KB a CTA
-    static constexpr int OFF_META = kPgWarps * ST * STAGE_BYTES;  // 2 float4 a stage
-    static constexpr int SMEM = OFF_META + kPgWarps * ST * 2 * 16;
+    static constexpr int WARPS = NT == 1 ? 12 : 8;           // one block an SM
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int ST = (D == 128 ? 2 : 4) + (NT == 1 ? 0 : D == 128 ? 1 : 2);  // stages a warp: 192 KB
+    static constexpr int OFF_META = WARPS * ST * STAGE_BYTES;  // 2 float4 a stage
+    static constexpr int SMEM = OFF_META + WARPS * ST * 2 * 16;
+    static constexpr int UNITS = CHUNKS * NT * 2;            // float2 of sums that a lane holds
     // Where a 16-byte piece of a row lies: pieces are swapped within 128 bytes so that
     // eight rows' same piece (ldmatrix) falls into different banks.
     static __device__ __forceinline__ int swap(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
@@ -82,7 +84,8 @@ struct PgCfg {
 // A place in the line of tiles.
 struct Place {
     int entry;        // sequence, or sequence * Hkv + head where pages are selected
-    long long base;   // first tile of the entry
+    long long base;   // first place of the entry
+    long long pos;
 };
 
 struct Seq {
@@ -105,24 +108,36 @@ __device__ __forceinline__ int item_tiles(const PagedParams &p, int b, int h, in
     return max(1, (int)((keys + kPgTile - 1) / kPgTile));
 }
 
-__device__ __forceinline__ long long entry_weight(const PagedParams &p, int e, int nr) {
+// Rare work (once a share, an item or sixteen tiles) is kept out of line, so that the
+// loop over tiles stays within the instruction cache: with the 64-bit divisions of it
+// inlined everywhere the kernel was 192 KB long and spent 25 us on fetching itself.
+__device__ __noinline__ long long entry_weight(const PagedParams &p, int e, int nr) {
     const int b = p.sel ? e / p.Hkv : e, h = p.sel ? e % p.Hkv : 0;
     const Seq s = sequence(p, b);
     if (s.nq == 0) return 0;
-    const long long rt = ((long long)s.nq * p.G + nr - 1) / nr;
+    const long long rt = (s.nq * p.G + nr - 1) / nr;
     return rt * (p.sel ? 1 : p.Hkv) * (kPgFixed + item_tiles(p, b, h, s.len));
 }
 
+// x / y for x >= 0, y > 0
+__device__ __noinline__ long long quotient(long long x, long long y) {
+    if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+
 // Scans the line.  Returns its length and the share of each of `workers` warps,
-// and leaves in found[w] the place where the block's warp w begins.
+// and leaves in found[w] where the block's warp w begins, found[w + 1] where it ends.
+// A boundary that falls into an item of half a share at most, or into an item's fixed
+// places, is moved to the item's nearer end or its beginning.
 struct Line {
     long long total, share;
 };
 
+template <int WARPS>
 __device__ __forceinline__ Line scan_line(const PagedParams &p, int nr, int workers, long long *warp_sums, Place *found) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = p.sel ? p.B * p.Hkv : p.B;
-    const int per = (n + kPgThreads - 1) / kPgThreads;
+    const int per = (n + 32 * WARPS - 1) / (32 * WARPS);
     const int e0 = min(n, tid * per), e1 = min(n, e0 + per);
     long long mine = 0;
     for (int e = e0; e < e1; ++e) mine += entry_weight(p, e, nr);
@@ -137,25 +152,37 @@ __device__ __forceinline__ Line scan_line(const PagedParams &p, int nr, int work
     Line line;
     line.total = 0;
 #pragma unroll
-    for (int w = 0; w < kPgWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) x += warp_sums[w];
         line.total += warp_sums[w];
     }
-    line.share = (line.total + workers - 1) / workers;
+    line.share = quotient(line.total + workers - 1, workers);
     if (line.share < kPgMinShare) line.share = kPgMinShare;
-#pragma unroll
-    for (int w = 0; w < kPgWarps; ++w) {
-        const long long pos = (blockIdx.x * kPgWarps + w) * line.share;
-        long long lo = x - mine;
-        if (pos >= lo && pos < x) {
+    if (tid <= WARPS) {
+        const long long pos = ((long long)blockIdx.x * WARPS + tid) * line.share;
+        if (pos >= line.total) found[tid] = Place{0, 0, line.total};
+    }
+    if (mine > 0) {
+#pragma unroll 1
+        for (int w = 0; w <= WARPS; ++w) {
+            const long long pos = ((long long)blockIdx.x * WARPS + w) * line.share;
+            long long lo = x - mine;
+            if (pos < lo || pos >= x) continue;
             int e = e0;
             for (; e < e1 - 1; ++e) {
                 const long long q = entry_weight(p, e, nr);
                 if (pos < lo + q) break;
                 lo += q;
             }
-            found[w].entry = e;
-            found[w].base = lo;
+            const int b = p.sel ? e / p.Hkv : e, h = p.sel ? e % p.Hkv : 0;
+            const long long size = kPgFixed + item_tiles(p, b, h, sequence(p, b).len);
+            const long long in = (pos - lo) - quotient(pos - lo, size) * size;
+            long long at = pos;
+            if (in <= kPgFixed || (2 * size <= line.share && 2 * in < size))
+                at = pos - in;
+            else if (2 * size <= line.share)
+                at = pos - in + size;
+            found[w] = Place{e, lo, at};
         }
     }
     __syncthreads();
@@ -167,11 +194,11 @@ struct Item {
     Seq s;
     int b, h, tiles;
     long long first;        // its first place: kPgFixed of them, then its tiles
-    long long row0, rows;   // its first query row, and how many the sequence has for this head
+    int row0, rows;         // its first query row, and how many the sequence has for this head
     int t0, t1;             // the tiles from the position to `end`
 };
 
-__device__ __forceinline__ Item item_at(const PagedParams &p, Place &place, long long pos, long long end, int nr) {
+__device__ __noinline__ Item item_at(const PagedParams &p, Place &place, long long pos, long long end, int nr) {
     // The scan's lengths and these are the same unless the caller changes them during
     // the call; the bounds on entry, head and parts keep every access inside even then.
     Item it;
@@ -185,11 +212,12 @@ __device__ __forceinline__ Item item_at(const PagedParams &p, Place &place, long
     it.h = p.sel ? place.entry % p.Hkv : 0;
     it.s = sequence(p, it.b);
     it.tiles = item_tiles(p, it.b, it.h, it.s.len);
-    it.rows = (long long)it.s.nq * p.G;
-    const long long w = kPgFixed + it.tiles, rts = max(1ll, (it.rows + nr - 1) / nr), nth = (pos - place.base) / w;
+    it.rows = it.s.nq * p.G;
+    const long long w = kPgFixed + it.tiles, nth = quotient(pos - place.base, w);
     it.first = place.base + nth * w;
-    long long rt = nth;
-    if (!p.sel) it.h = (int)min(nth / rts, p.Hkv - 1ll), rt = nth % rts;
+    const int rts = max(1, (it.rows + nr - 1) / nr);
+    int rt = (int)nth;  // items of an entry: fewer than 2^31
+    if (!p.sel) it.h = min(rt / rts, p.Hkv - 1), rt = rt % rts;
     it.row0 = rt * nr;
     it.t0 = (int)max(0ll, pos - it.first - kPgFixed);
     it.t1 = (int)max(0ll, min((long long)it.tiles, end - it.first - kPgFixed));
@@ -245,12 +273,15 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 // The workspace: for each worker (a warp) what the item that it leaves off needs
 // to be joined, then two slots of partial results: 0 for the item that it continues, 1
 // for the one that it leaves off.  A slot is [rows][D] sums, [rows] m, [rows] l.
-struct Tail {
-    int parts, b, h, tile_of_rows;  // parts 0: no item is left off
+struct __align__(16) Tail {
+    int parts;               // 0: no item is left off
+    int b, h, tile_of_rows;
+    int from, step, last;    // part 0 is slot 1 of this worker, part j slot 0 of worker from + j * step,
+    int pad;                 // but the last one's of worker `last`
 };
 __device__ __forceinline__ Tail *tail_of(float *ws, int worker) { return reinterpret_cast<Tail *>(ws) + worker; }
 __device__ __forceinline__ float *slot_of(float *ws, int workers, int worker, int slot, int nr, int D) {
-    return ws + 4ll * workers + (2ll * worker + slot) * nr * (D + 2);
+    return ws + (long long)workers * (sizeof(Tail) / 4) + (2ll * worker + slot) * nr * (D + 2);
 }
 
 // m - 8 + log2 l in base e.  l's exponent is added to m before its mantissa's
@@ -265,33 +296,37 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
-__device__ __forceinline__ long long out_row(const PagedParams &p, const Seq &s, int h, long long row) {
-    return (s.q0 + row / p.G) * ((long long)p.Hkv * p.G) + (long long)h * p.G + row % p.G;
+__device__ __forceinline__ long long out_row(const PagedParams &p, const Seq &s, int h, int row) {
+    return (long long)(s.q0 + row / p.G) * (p.Hkv * p.G) + h * p.G + row % p.G;
 }
 
 // --------------------------------------------------------------- the kernel
 template <int D, int NT>
-__global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(const PagedParams p) {
-    using C = PgCfg<D>;
+__global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(const __grid_constant__ PagedParams p) {
+    using C = PgCfg<D, NT>;
     constexpr int NR = 8 * NT;
     constexpr int KG = D / 64;  // groups of four 16-byte pieces of a row
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ long long warp_sums[kPgWarps];
-    __shared__ Place found[kPgWarps];
+    __shared__ long long warp_sums[C::WARPS];
+    __shared__ Place found[C::WARPS + 1];
+    __shared__ int flag_of[C::WARPS];
+    __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR];
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int page = 1 << p.page_log2;
     const uint32_t ring = smem_u32(sm) + warp * C::ST * C::STAGE_BYTES;
     float4 *const meta_of = reinterpret_cast<float4 *>(sm + C::OFF_META) + warp * C::ST * 2;
-    const int workers = gridDim.x * kPgWarps, worker = blockIdx.x * kPgWarps + warp;
+    const int workers = gridDim.x * C::WARPS, worker = blockIdx.x * C::WARPS + warp;
 
-    const Line line = scan_line(p, NR, workers, warp_sums, found);
-    long long pos = worker * line.share;
-    const long long end = min(pos + line.share, line.total);
-    if (lane == 0) tail_of(p.ws, worker)->parts = 0;
-    if (pos >= end) return;  // no block-wide barrier from here on
+    const Line line = scan_line<C::WARPS>(p, NR, workers, warp_sums, found);
     Place place = found[warp];
+    long long pos = place.pos;
+    const long long end = found[warp + 1].pos;
+    if (lane == 0) {
+        tail_of(p.ws, worker)->parts = 0;
+        flag_of[warp] = 0;
+    }
 
     // ---- pages: up to 16 tiles (32 halves) of one item looked up at a time, a half a
     // lane, one such batch ahead of the copies
@@ -333,7 +368,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
     // consumer needs (first key, c's key scale or NaN, log2 of the value scale and its
     // inverse).
     uint32_t row_now = 0, full_now = 0;
-    int nv_now = 0, n_now = 0, at_now = 0, stage_in = 0;
+    int ph_now = 0, nv_now = 0, n_now = 0, at_now = 0, stage_in = 0;
     float4 meta_now = make_float4(0.f, 0.f, 0.f, 0.f);
     const uint8_t *const k_lane = p.k_pages + lane * 16, *const v_lane = p.v_pages + lane * 16;
     const int r_lane = lane / C::CHUNKS;  // row of this lane's piece among those of one copy
@@ -345,25 +380,14 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
             at_now = 0;
             n_now = n_next;
             if (n_now > 0) {
-                const bool bad = ph_next < 0;
-                const int ph = max(ph_next, 0);
-                row_now = ((uint32_t)ph << p.page_log2) + (key_next & (page - 1));
+                ph_now = ph_next;
+                row_now = ((uint32_t)max(ph_now, 0) << p.page_log2) + (key_next & (page - 1));
                 nv_now = nv_next;
                 full_now = __ballot_sync(0xffffffffu, nv_now == 16);
-                float ks = p.k_scale[ph], vs = p.v_scale[ph];
-                if (bad) {
-                    ks = __int_as_float(0x7fc00000), vs = 1.f;
-                    atomicExch(&g_status_paged, (int)FA_ERR_BAD_PAGE);
-                }
-                const int u = __float_as_int(vs);  // its logarithm, exact for powers of two
-                const float lv = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
-                meta_now = make_float4(__int_as_float(key_next), ks, lv, ex2_approx(-lv));
-                look_up();
             }
         }
         if (at_now < n_now) {
             const uint32_t st = dst_lane + stage_in * C::STAGE_BYTES;
-            if ((lane >> 1) == at_now) meta_of[stage_in * 2 + (lane & 1)] = meta_now;
             const bool full = ((full_now >> (2 * at_now)) & 3u) == 3u;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -387,6 +411,19 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                     }
                 }
             }
+            if (at_now == 0) {  // a new batch: its scales, and the next one's pages, while the copies run
+                float ks = p.k_scale[max(ph_now, 0)], vs = p.v_scale[max(ph_now, 0)];
+                if (ph_now < 0) {
+                    ks = __int_as_float(0x7fc00000), vs = 1.f;
+                    atomicExch(&g_status_paged, (int)FA_ERR_BAD_PAGE);
+                }
+                const int key = key_next;
+                look_up();
+                const int u = __float_as_int(vs);  // its logarithm, exact for powers of two
+                const float lv = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
+                meta_now = make_float4(__int_as_float(key), ks, lv, ex2_approx(-lv));
+            }
+            if ((lane >> 1) == at_now) meta_of[stage_in * 2 + (lane & 1)] = meta_now;
             ++at_now;
             stage_in = stage_in + 1 == C::ST ? 0 : stage_in + 1;
         }
@@ -401,13 +438,17 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
     const uint32_t v_read = ring + 2 * C::HALF_BYTES + v_row * D + C::swap(v_row) * 16;
     int stage_out = 0;
 
+    if (pos >= end) {  // nothing to do, but the others wait for every warp's flag
+        named_bar_sync(1, C::THREADS);
+        named_bar_sync(1, C::THREADS);
+    }
+    bool first_item = true;
     while (pos < end) {
         const Item it = item_at(p, place, pos, end, NR);
         const Seq s = it.s;
         const int h = it.h, t0 = it.t0, t1 = it.t1;
-        const long long row0 = it.row0, rows = it.rows;
+        const int row0 = it.row0, rows = it.rows;
         pos = it.first + kPgFixed + t1;
-        if (t1 <= t0) break;  // the share ends within the item's fixed places
 
         // ---- query rows: fragments of Q^T (lane: row g of each tile of 8)
         uint32_t qf[NT][KG][4][2];
@@ -415,7 +456,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
         int lim[NT][2];     // the first key that they do not see
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const long long row = row0 + nt * 8 + g;
+            const int row = row0 + nt * 8 + g;
             uint4 w[KG][2];
             uint32_t am = 0;
 #pragma unroll
@@ -425,8 +466,8 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                     w[i][j] = make_uint4(0, 0, 0, 0);
                     if (row < rows) {
                         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                                 (s.q0 + row / p.G) * p.q_stride +
-                                                 ((long long)h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
+                                                 (long long)(s.q0 + row / p.G) * p.q_stride +
+                                                 (long long)(h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
                         w[i][j] = __ldg(reinterpret_cast<const uint4 *>(q));
                     }
                     const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
@@ -450,11 +491,11 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 fac[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-                const long long r = row0 + nt * 8 + 2 * t + j;
-                lim[nt][j] = r < rows ? s.len - s.nq + (int)(r / p.G) + 1 : s.len;
+                const int r = row0 + nt * 8 + 2 * t + j;
+                lim[nt][j] = r < rows ? s.len - s.nq + r / p.G + 1 : s.len;
             }
         }
-        const int lim_min = s.len - s.nq + (int)(row0 / p.G) + 1;
+        const int lim_min = s.len - s.nq + row0 / p.G + 1;
 
         float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
 #pragma unroll
@@ -600,7 +641,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
                 // NaN among the values into NaN, so the values that a token does not see
                 // are cleared, a token at a time, and only that token's rows take the
                 // result (only the last tiles of a sequence come here).
-                const int tok0 = (int)(row0 / p.G), tok1 = (int)min((long long)s.nq - 1, (row0 + NR - 1) / p.G);
+                const int tok0 = row0 / p.G, tok1 = min(s.nq - 1, (row0 + NR - 1) / p.G);
 #pragma unroll 1
                 for (int tok = tok0; tok <= tok1; ++tok) {
                     const int limit = s.len - s.nq + tok + 1;
@@ -620,159 +661,286 @@ __global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm) fa_fwd_paged_kernel(
             }
         }
 
+        // ---- the block's last items: warps whose whole share lies in the item of the warp
+        // before are joined with it.  (For the last of an item's warps that is so only
+        // where its share before moving boundaries ends with the item: the warp that
+        // describes the parts has to know.)
+        int group = 1, in_group = 0;      // warps of this warp's group, its own place among them
+        bool open = t1 < it.tiles;        // the item goes on behind them
+        bool begins = t0 == 0;
+        if (pos >= end) {
+            const long long it_end = it.first + kPgFixed + it.tiles;
+            const bool sole = warp > 0 && first_item && t0 > 0 &&
+                              (open || it_end == min((worker + 1) * line.share, line.total));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+                    if (g == 0) {
+                        join_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
+                        join_l[warp][nt * 8 + 2 * t + j] = l[nt][j];
+                    }
+                }
+            cp_wait<0>();
+            __syncwarp();
+            float2 *const mine = reinterpret_cast<float2 *>(sm + warp * C::ST * C::STAGE_BYTES) + lane;  // over the ring
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mine[((c * NT + nt) * 2 + j) * 32] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
+            if (lane == 0) flag_of[warp] = (sole ? 1 : 0) | (open ? 2 : 0) | (begins ? 4 : 0);
+            named_bar_sync(1, C::THREADS);
+            int lead = warp, last = warp;
+            while (flag_of[lead] & 1) --lead;
+            while (last + 1 < C::WARPS && (flag_of[last + 1] & 1)) ++last;
+            group = last - lead + 1;
+            in_group = warp - lead;
+            open = flag_of[last] & 2;
+            begins = flag_of[lead] & 4;
+            // every row's maximum over the group, and this warp's sums' factor to it
+            if (lane < NR) {
+                float M = kPgNone;
+                for (int w = lead; w <= last; ++w) M = fmaxf(M, join_m[w][lane]);
+                join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
+            }
+            named_bar_sync(1, C::THREADS);
+        }
+        first_item = false;
+
         // ---- write the rows out, or what is known of them
-        const bool whole = t0 == 0 && t1 == it.tiles;
-        float *const part = slot_of(p.ws, workers, worker, t0 == 0 ? 1 : 0, NR, D);
+        const int lead = worker - in_group;
+        const bool whole = begins && !open;
+        float *const part = slot_of(p.ws, workers, lead, begins ? 1 : 0, NR, D);
+        if (group == 1) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float y = l[nt][j];
-                y += __shfl_xor_sync(0xffffffffu, y, 4);
-                y += __shfl_xor_sync(0xffffffffu, y, 8);
-                y += __shfl_xor_sync(0xffffffffu, y, 16);
-                const float base = m[nt][j];
-                const int r = nt * 8 + 2 * t + j;
+                for (int j = 0; j < 2; ++j) {
+                    float y = l[nt][j];
+                    if (pos < end) {  // (otherwise summed above)
+                        y += __shfl_xor_sync(0xffffffffu, y, 4);
+                        y += __shfl_xor_sync(0xffffffffu, y, 8);
+                        y += __shfl_xor_sync(0xffffffffu, y, 16);
+                    }
+                    const int r = nt * 8 + 2 * t + j;
+                    if (!whole) {
+                        float2 *const o = reinterpret_cast<float2 *>(part + r * D) + g;
+#pragma unroll
+                        for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
+                        if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = y;
+                    } else if (row0 + r < rows) {
+                        const float inv = y == 0.f ? 0.f : 1.f / y;
+                        const long long at = out_row(p, s, h, row0 + r);
+                        uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + g;
+#pragma unroll
+                        for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
+                        if (g == 0) p.lse[at] = lse_of(m[nt][j], y);
+                    }
+                }
+        } else {  // each warp of the group writes every group-th piece of the sums
+            const int w0 = warp - in_group;
+#pragma unroll 1
+            for (int u = in_group; u < C::UNITS; u += group) {
+                const int c = u / (2 * NT), r = (u / 2 % NT) * 8 + 2 * t + (u & 1);
+                float2 o = make_float2(0.f, 0.f);
+                float y = 0.f;
+                for (int w = w0; w < w0 + group; ++w) {
+                    const float f = join_f[w][r];
+                    const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[u * 32 + lane];
+                    o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y);
+                    y = fmaf(join_l[w][r], f, y);
+                }
+                float M = kPgNone;
+                if (c == 0)
+                    for (int w = w0; w < w0 + group; ++w) M = fmaxf(M, join_m[w][r]);
                 if (!whole) {
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; ++c)
-                        *reinterpret_cast<float2 *>(part + r * D + 16 * c + 2 * g) =
-                            make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
-                    if (g == 0) part[NR * D + r] = base, part[NR * D + NR + r] = y;
+                    reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
+                    if (c == 0 && g == 0) part[NR * D + r] = M, part[NR * D + NR + r] = y;
                 } else if (row0 + r < rows) {
                     const float inv = y == 0.f ? 0.f : 1.f / y;
                     const long long at = out_row(p, s, h, row0 + r);
-                    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D + 2 * g);
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; ++c)
-                        o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
-                    if (g == 0) p.lse[at] = lse_of(base, y);
+                    reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D)[8 * c + g] = pack_bf16x2(o.x * inv, o.y * inv);
+                    if (c == 0 && g == 0) p.lse[at] = lse_of(M, y);
                 }
             }
-        if (t0 == 0 && !whole && lane == 0) {
-            const long long last = (it.first + kPgFixed + it.tiles - 1) / line.share;
-            *tail_of(p.ws, worker) = Tail{min((int)last, workers - 1) - worker + 1, it.b, h, (int)(row0 / NR)};
+        }
+        if (begins && open && in_group == 0 && lane == 0) {
+            // the parts behind this one: the first warp of every further block, and the
+            // item's last warp unless it is in a group
+            const long long it_last = it.first + kPgFixed + it.tiles - 1;
+            const int last = (int)min(quotient(it_last, line.share), workers - 1ll), blk = last / C::WARPS;
+            const bool grouped = last % C::WARPS == 0 || it_last + 1 == min((last + 1) * line.share, line.total);
+            Tail tail;
+            tail.parts = 1 + (blk - blockIdx.x) + (grouped ? 0 : 1);
+            tail.b = it.b, tail.h = h, tail.tile_of_rows = row0 / NR;
+            tail.from = blockIdx.x * C::WARPS, tail.step = C::WARPS;
+            tail.last = grouped ? blk * C::WARPS : last;
+            tail.pad = 0;
+            *tail_of(p.ws, lead) = tail;
         }
     }
-    cp_wait<0>();
 }
 
-// Joins the partial results of the items that were cut: a block takes one row of
-// the item that a worker left off at a time, whose other parts are with the
-// workers behind it.  Its warps share the parts.
-template <int D, int NT>
-__global__ void __launch_bounds__(kPgThreads) fa_paged_join_kernel(const PagedParams p, int workers) {
-    constexpr int NR = 8 * NT, E = D / 32;
-    __shared__ float red_m[kPgWarps], red_l[kPgWarps], red_o[kPgWarps][D];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    grid_wait();
-    // a lane looks at the tail of one of this block's next 32 rows
-    for (int i0 = blockIdx.x; i0 < workers * NR; i0 += 32 * gridDim.x) {
-        const int mine = i0 + lane * gridDim.x;
-        int parts = 0;
-        if (mine < workers * NR) parts = tail_of(p.ws, mine / NR)->parts;
-        uint32_t todo = __ballot_sync(0xffffffffu, parts > 0);
-        while (todo) {
-            const int k = __ffs((int)todo) - 1;
-            todo &= todo - 1;
-            const int i = i0 + k * gridDim.x, worker = i / NR, r = i % NR;
-            const Tail tail = *tail_of(p.ws, worker);
-            const Seq s = sequence(p, tail.b);
-            const long long row = (long long)tail.tile_of_rows * NR + r;
-            if (row >= (long long)s.nq * p.G) continue;
-            float M = -INFINITY, L = 0.f, O[E];
+// Joins the partial results of the items that were cut: a warp, or where there are
+// many parts a block, takes one row of the item that a worker left off at a time.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinMany = 12;  // parts
+
+template <int D, int NR>
+struct JoinRow {
+    static constexpr int E = D / 32;
+    float M, L, O[E];
+
+    // parts j0, j0 + step, ..
+    __device__ __forceinline__ void sum(const PagedParams &p, const Tail &tail, int workers, int worker, int r, int j0, int step) {
+        const int lane = threadIdx.x & 31;
+        M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] = 0.f;
-            constexpr int UN = 4;  // parts in flight
-            for (int j0 = warp; j0 < tail.parts; j0 += UN * kPgWarps) {
-                float m[UN], l[UN], o[UN][E];
+        for (int e = 0; e < E; ++e) O[e] = 0.f;
+        constexpr int UN = 4;  // parts in flight
+        for (; j0 < tail.parts; j0 += UN * step) {
+            float m[UN], l[UN], o[UN][E];
 #pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    const int j = j0 + u * kPgWarps;
-                    m[u] = -INFINITY, l[u] = 0.f;
+            for (int u = 0; u < UN; ++u) {
+                const int j = j0 + u * step;
+                m[u] = -INFINITY, l[u] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[u][e] = 0.f;
-                    if (j < tail.parts) {
-                        const float *part = slot_of(p.ws, workers, worker + j, j == 0, NR, D);
-                        m[u] = part[NR * D + r];
-                        l[u] = part[NR * D + NR + r];
-                        if (E == 4) {
-                            const float4 x = *reinterpret_cast<const float4 *>(part + r * D + 4 * lane);
-                            o[u][0] = x.x, o[u][1] = x.y, o[u][E - 2] = x.z, o[u][E - 1] = x.w;
-                        } else {
-                            const float2 x = *reinterpret_cast<const float2 *>(part + r * D + 2 * lane);
-                            o[u][0] = x.x, o[u][1] = x.y;
-                        }
+                for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+                if (j < tail.parts) {
+                    const int from = j == 0 ? worker : j == tail.parts - 1 ? tail.last : tail.from + j * tail.step;
+                    const float *part = slot_of(p.ws, workers, from, j == 0, NR, D);
+                    m[u] = part[NR * D + r];
+                    l[u] = part[NR * D + NR + r];
+                    if (E == 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(part + r * D + 4 * lane);
+                        o[u][0] = x.x, o[u][1] = x.y, o[u][E - 2] = x.z, o[u][E - 1] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2 *>(part + r * D + 2 * lane);
+                        o[u][0] = x.x, o[u][1] = x.y;
                     }
                 }
-                float now = M;
-#pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    if (l[u] == 0.f) m[u] = -INFINITY;  // a part without keys does not count
-                    now = fmaxf(now, m[u]);
-                }
-                const float base = now == -INFINITY ? 0.f : now, f0 = ex2_approx(M - base);
-                M = now;
-                L *= f0;
-#pragma unroll
-                for (int e = 0; e < E; ++e) O[e] *= f0;
-#pragma unroll
-                for (int u = 0; u < UN; ++u) {
-                    const float f = ex2_approx(m[u] - base);
-                    L = fmaf(l[u], f, L);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) O[e] = fmaf(o[u][e], f, O[e]);
-                }
             }
-            __syncthreads();  // the row before is read
-            if (lane == 0) red_m[warp] = M, red_l[warp] = L;
+            float now = M;
 #pragma unroll
-            for (int e = 0; e < E; ++e) red_o[warp][lane * E + e] = O[e];
-            __syncthreads();
-            float all = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) all = fmaxf(all, red_m[w]);
-            const float base = all == -INFINITY ? 0.f : all;
-            float l = 0.f, o = 0.f;
-#pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) {
-                const float f = ex2_approx(red_m[w] - base);
-                l = fmaf(red_l[w], f, l);
-                if (tid < D) o = fmaf(red_o[w][tid], f, o);
+            for (int u = 0; u < UN; ++u) {
+                if (l[u] == 0.f) m[u] = -INFINITY;  // a part without keys does not count
+                now = fmaxf(now, m[u]);
             }
-            const long long at = out_row(p, s, tail.h, row);
-            if (tid < D) static_cast<__nv_bfloat16 *>(p.o)[at * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-            if (tid == 0) p.lse[at] = lse_of(base, l);
+            const float base = now == -INFINITY ? 0.f : now, f0 = ex2_approx(M - base);
+            M = now;
+            L *= f0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] *= f0;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const float f = ex2_approx(m[u] - base);
+                L = fmaf(l[u], f, L);
+#pragma unroll
+                for (int e = 0; e < E; ++e) O[e] = fmaf(o[u][e], f, O[e]);
+            }
         }
     }
+    __device__ __forceinline__ void add(float m, float l, const float *o) {
+        const float now = fmaxf(M, m), base = now == -INFINITY ? 0.f : now;
+        const float f0 = ex2_approx(M - base), f = ex2_approx(m - base);
+        M = now, L = fmaf(L, f0, l * f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] = fmaf(O[e], f0, o[e] * f);
+    }
+    __device__ __forceinline__ void write(const PagedParams &p, long long at) {
+        const int lane = threadIdx.x & 31;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + lane * (E / 2);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) o[e] = pack_bf16x2(O[2 * e] * inv, O[2 * e + 1] * inv);
+        if (lane == 0) p.lse[at] = lse_of(M == -INFINITY ? 0.f : M, L);
+    }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __grid_constant__ PagedParams p, int workers) {
+    constexpr int NR = 8 * NT, E = D / 32;
+    __shared__ float red_m[kJoinWarps], red_l[kJoinWarps], red_o[kJoinWarps][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    JoinRow<D, NR> row_of;
+    grid_wait();
+    // A block takes every gridDim-th worker, a lane looks at the tail of one of the next
+    // 32; a warp takes every fourth row of a tail.
+    for (int i0 = blockIdx.x; i0 < workers; i0 += 32 * gridDim.x) {
+        const int mine = i0 + lane * gridDim.x;
+        int parts = 0;
+        if (mine < workers) parts = tail_of(p.ws, mine)->parts;
+        uint32_t todo = __ballot_sync(0xffffffffu, parts > 0);
+        while (todo) {
+            const int k = __ffs((int)todo) - 1, worker = i0 + k * gridDim.x;
+            todo &= todo - 1;
+            const Tail tail = *tail_of(p.ws, worker);
+            const Seq s = sequence(p, tail.b);
+            const int row0 = tail.tile_of_rows * NR;
+            const int rows = max(0, min(NR, s.nq * p.G - row0));
+            if (tail.parts <= kJoinMany) {
+                for (int r = warp; r < rows; r += kJoinWarps) {
+                    row_of.sum(p, tail, workers, worker, r, 0, 1);
+                    row_of.write(p, out_row(p, s, tail.h, row0 + r));
+                }
+            } else {
+                for (int r = 0; r < rows; ++r) {
+                    row_of.sum(p, tail, workers, worker, r, warp, kJoinWarps);
+                    __syncthreads();  // the row before is read
+                    if (lane == 0) red_m[warp] = row_of.M, red_l[warp] = row_of.L;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) red_o[warp][lane * E + e] = row_of.O[e];
+                    __syncthreads();
+                    if (warp != r % kJoinWarps) continue;
+#pragma unroll
+                    for (int w = 1; w < kJoinWarps; ++w) {
+                        const int v = (warp + w) % kJoinWarps;
+                        row_of.add(red_m[v], red_l[v], &red_o[v][lane * E]);
+                    }
+                    row_of.write(p, out_row(p, s, tail.h, row0 + r));
+                }
+            }
+        }
+    }
+}
+
+template <int D, int NT>
+static size_t workspace_of(int num_sms) {
+    return (size_t)num_sms * PgCfg<D, NT>::WARPS * (sizeof(Tail) + 2 * 8 * NT * (D + 2) * sizeof(float));
 }
 
 size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms) {
-    (void)B, (void)T, (void)Hq, (void)Hkv;
-    const size_t workers = (size_t)num_sms * kPgCtasPerSm * kPgWarps;
-    return workers * (sizeof(Tail) + 2 * 16 * (D + 2) * sizeof(float));
+    (void)B, (void)T, (void)Hq, (void)Hkv;  // the same for all: what of the two forms needs more
+    const size_t a = D == 64 ? workspace_of<64, 1>(num_sms) : workspace_of<128, 1>(num_sms);
+    const size_t b = D == 64 ? workspace_of<64, 2>(num_sms) : workspace_of<128, 2>(num_sms);
+    return a > b ? a : b;
 }
 
 template <int D, int NT>
 static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t stream) {
-    const int ctas = kPgCtasPerSm * num_sms;
-    cudaError_t e = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PgCfg<D>::SMEM);
+    using C = PgCfg<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    fa_fwd_paged_kernel<D, NT><<<ctas, kPgThreads, PgCfg<D>::SMEM, stream>>>(p);
+    fa_fwd_paged_kernel<D, NT><<<num_sms, C::THREADS, C::SMEM, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // the join is launched while the first kernel still runs, and waits for its end
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4 * num_sms);
-    cfg.blockDim = dim3(kPgThreads);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p, ctas * kPgWarps);
+    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p, num_sms * C::WARPS);
 }
 
 cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream) {
