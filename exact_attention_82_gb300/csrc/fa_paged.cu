@@ -30,15 +30,14 @@
 //
 // Split.  The tiles of all items (sequence, key/value head, 8 or 16 query rows)
 // are laid end to end, each item behind a few places that stand for its fixed
-// cost, and the line is cut into equal shares, one a warp, whatever the lengths: a
-// long sequence is cut over many warps, short ones follow one another in one (and
-// are not cut at all where a share holds two of them).  Lengths are read on the
-// device (a scan of a few hundred integers).  A warp's ring runs on across its
-// items, so that the next one's keys arrive while it writes out the last one's rows.
-// Warps of a block whose whole share lies in one item are joined in shared memory;
-// what is still cut leaves partial results in the workspace, which a second kernel
-// joins.  A warp leaves at most two of them (for the item that it continues, and the
-// one that it leaves off).
+// cost, and the line is cut into equal shares, one a block (an SM), and each of
+// them again into equal ones, one a warp, whatever the lengths: a long sequence is
+// cut over many warps, short ones follow one another in one (small items are not cut
+// at all).  Lengths are read on the device (a scan of a few hundred integers).  A
+// warp's ring runs on across its items, so that the next one's keys arrive while it
+// writes out the last one's rows.  What a block's warps have of an item is joined
+// within the block, in shared memory; an item that crosses blocks leaves one partial
+// result a block in the workspace, which a second kernel joins.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -54,7 +53,7 @@ static __device__ int g_status_paged = 0;
 
 constexpr int kPgTile = 32;         // keys a tile; two halves of 16, each in one page
 constexpr int kPgFixed = 2;         // places of the line that an item's fixed cost takes
-constexpr int kPgMinShare = 4;      // places
+constexpr int kPgMinShare = 36;     // places of a block: three tiles a warp
 constexpr int kPgMaxLen = 0x7fffff00;
 constexpr float kPgShift = 8.f;    // exponent of a weight at x = m
 constexpr float kPgMost = 15.f;    // and the largest one
@@ -69,7 +68,10 @@ struct PgCfg {
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int ST = (D == 128 ? 2 : 4) + (NT == 1 ? 0 : D == 128 ? 1 : 2);  // stages a warp: 192 KB
     static constexpr int OFF_META = WARPS * ST * STAGE_BYTES;  // 2 float4 a stage
-    static constexpr int SMEM = OFF_META + WARPS * ST * 2 * 16;
+    static constexpr int OFF_WORK = OFF_META + WARPS * ST * 2 * 16;
+    static constexpr int WORKS = 8;                          // items looked up ahead: ST + 1 at most
+    static constexpr int OFF_SUMS = OFF_WORK + WARPS * WORKS * 48;
+    static constexpr int SMEM = OFF_SUMS + THREADS * 8;
     static constexpr int UNITS = CHUNKS * NT * 2;            // float2 of sums that a lane holds
     // Where a 16-byte piece of a row lies: pieces are swapped within 128 bytes so that
     // eight rows' same piece (ldmatrix) falls into different banks.
@@ -125,111 +127,133 @@ __device__ __noinline__ long long quotient(long long x, long long y) {
     return x / y;
 }
 
-// Scans the line.  Returns its length and the share of each of `workers` warps,
-// and leaves in found[w] where the block's warp w begins, found[w + 1] where it ends.
-// A boundary that falls into an item of half a share at most, or into an item's fixed
-// places, is moved to the item's nearer end or its beginning.
-struct Line {
-    long long total, share;
-};
+// Finds the place of `pos` from the sums over the threads' entries.  Where it falls
+// into an item's fixed places, or into an item of at most `small` places, it is moved
+// to the item's beginning or its nearer end.
+__device__ __noinline__ Place place_of(const PagedParams &p, const long long *sums, int threads, int per, int n, int nr,
+                                       long long pos, long long small) {
+    int lo = 0, hi = threads - 1;  // the first thread whose sum is above pos
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] > pos)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    Place f;
+    f.entry = min(lo * per, n - 1);
+    f.base = lo ? sums[lo - 1] : 0;
+    f.pos = pos;
+    for (const int e1 = min(n, f.entry + per); f.entry < e1 - 1; ++f.entry) {
+        const long long w = entry_weight(p, f.entry, nr);
+        if (pos < f.base + w) break;
+        f.base += w;
+    }
+    const int b = p.sel ? f.entry / p.Hkv : f.entry, h = p.sel ? f.entry % p.Hkv : 0;
+    const long long size = kPgFixed + item_tiles(p, b, h, sequence(p, b).len);
+    const long long in = (pos - f.base) - quotient(pos - f.base, size) * size;
+    if (in <= kPgFixed || (size <= small && 2 * in < size))
+        f.pos -= in;
+    else if (size <= small)
+        f.pos += size - in;
+    return f;
+}
 
+// Scans the line.  Returns the share of a block, and leaves in found[w] where the
+// block's warp w begins, in found[w + 1] where it ends.
 template <int WARPS>
-__device__ __forceinline__ Line scan_line(const PagedParams &p, int nr, int workers, long long *warp_sums, Place *found) {
+__device__ __forceinline__ long long scan_line(const PagedParams &p, int nr, long long *sums, Place *found) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int THREADS = 32 * WARPS;
     const int n = p.sel ? p.B * p.Hkv : p.B;
-    const int per = (n + 32 * WARPS - 1) / (32 * WARPS);
-    const int e0 = min(n, tid * per), e1 = min(n, e0 + per);
-    long long mine = 0;
-    for (int e = e0; e < e1; ++e) mine += entry_weight(p, e, nr);
-    long long x = mine;
+    const int per = (n + THREADS - 1) / THREADS;
+    long long x = 0;
+    for (int e = min(n, tid * per); e < min(n, tid * per + per); ++e) x += entry_weight(p, e, nr);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, d);
         if (lane >= d) x += y;
     }
-    if (lane == 31) warp_sums[warp] = x;
+    sums[tid] = x;
     __syncthreads();
-    Line line;
-    line.total = 0;
+    long long before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) x += warp_sums[w];
-        line.total += warp_sums[w];
-    }
-    line.share = quotient(line.total + workers - 1, workers);
-    if (line.share < kPgMinShare) line.share = kPgMinShare;
-    if (tid <= WARPS) {
-        const long long pos = ((long long)blockIdx.x * WARPS + tid) * line.share;
-        if (pos >= line.total) found[tid] = Place{0, 0, line.total};
-    }
-    if (mine > 0) {
-#pragma unroll 1
-        for (int w = 0; w <= WARPS; ++w) {
-            const long long pos = ((long long)blockIdx.x * WARPS + w) * line.share;
-            long long lo = x - mine;
-            if (pos < lo || pos >= x) continue;
-            int e = e0;
-            for (; e < e1 - 1; ++e) {
-                const long long q = entry_weight(p, e, nr);
-                if (pos < lo + q) break;
-                lo += q;
-            }
-            const int b = p.sel ? e / p.Hkv : e, h = p.sel ? e % p.Hkv : 0;
-            const long long size = kPgFixed + item_tiles(p, b, h, sequence(p, b).len);
-            const long long in = (pos - lo) - quotient(pos - lo, size) * size;
-            long long at = pos;
-            if (in <= kPgFixed || (2 * size <= line.share && 2 * in < size))
-                at = pos - in;
-            else if (2 * size <= line.share)
-                at = pos - in + size;
-            found[w] = Place{e, lo, at};
-        }
+        const long long y = sums[w * 32 + 31];
+        if (w < warp) before += y;
+        total += y;
     }
     __syncthreads();
-    return line;
+    sums[tid] = x + before;
+    long long share = quotient(total + gridDim.x - 1, gridDim.x);
+    // With less work than the chip has room for, items of up to two least shares stay whole.
+    const long long small = share <= kPgMinShare ? 2 * kPgMinShare : share / 2;
+    if (share < kPgMinShare) share = kPgMinShare;
+    __syncthreads();
+    if (warp == 0) {
+        Place f{0, 0, total};
+        const long long cut = (long long)(blockIdx.x + (lane == WARPS)) * share;
+        if ((lane == 0 || lane == WARPS) && cut < total) f = place_of(p, sums, THREADS, per, n, nr, cut, small);
+        const long long begin = __shfl_sync(0xffffffffu, f.pos, 0), end = __shfl_sync(0xffffffffu, f.pos, WARPS);
+        const long long part = quotient(end - begin + WARPS - 1, WARPS), pos = begin + lane * part;
+        if (lane > 0 && lane < WARPS) {
+            f.pos = end;
+            if (pos < end) f = place_of(p, sums, THREADS, per, n, nr, pos, part / 2);
+        }
+        if (lane <= WARPS) found[lane] = f;
+    }
+    __syncthreads();
+    return share;
 }
 
-// What the line holds at a position.
-struct Item {
-    Seq s;
-    int b, h, tiles;
-    long long first;        // its first place: kPgFixed of them, then its tiles
-    int row0, rows;         // its first query row, and how many the sequence has for this head
-    int t0, t1;             // the tiles from the position to `end`
+// What a warp does for one item.
+struct Work {
+    int q0, nq, len;
+    int b, h, row0, rows;     // its first query row, and how many the sequence has for this head
+    int tiles, t0, t1;        // tiles of the item, and this warp's of them
+    int last;                 // whether the warp's share ends with it
+    int end_block;            // the block that has the item's last tile
 };
+static_assert(sizeof(Work) == 48, "");
 
-__device__ __noinline__ Item item_at(const PagedParams &p, Place &place, long long pos, long long end, int nr) {
+// The item at place.pos, which is moved behind the warp's tiles of it.
+__device__ __noinline__ Work work_at(const PagedParams &p, Place &place, long long end, long long share, int nr) {
     // The scan's lengths and these are the same unless the caller changes them during
-    // the call; the bounds on entry, head and parts keep every access inside even then.
-    Item it;
+    // the call; the bounds on entry, head and block keep every access inside even then.
     const int n = p.sel ? p.B * p.Hkv : p.B;
     for (; place.entry < n - 1; ++place.entry) {
         const long long w = entry_weight(p, place.entry, nr);
-        if (pos < place.base + w) break;
+        if (place.pos < place.base + w) break;
         place.base += w;
     }
+    Work it;
     it.b = p.sel ? place.entry / p.Hkv : place.entry;
     it.h = p.sel ? place.entry % p.Hkv : 0;
-    it.s = sequence(p, it.b);
-    it.tiles = item_tiles(p, it.b, it.h, it.s.len);
-    it.rows = it.s.nq * p.G;
-    const long long w = kPgFixed + it.tiles, nth = quotient(pos - place.base, w);
-    it.first = place.base + nth * w;
+    const Seq s = sequence(p, it.b);
+    it.q0 = s.q0, it.nq = s.nq, it.len = s.len;
+    it.tiles = item_tiles(p, it.b, it.h, s.len);
+    it.rows = s.nq * p.G;
+    const long long w = kPgFixed + it.tiles, nth = quotient(place.pos - place.base, w), first = place.base + nth * w;
     const int rts = max(1, (it.rows + nr - 1) / nr);
     int rt = (int)nth;  // items of an entry: fewer than 2^31
     if (!p.sel) it.h = min(rt / rts, p.Hkv - 1), rt = rt % rts;
     it.row0 = rt * nr;
-    it.t0 = (int)max(0ll, pos - it.first - kPgFixed);
-    it.t1 = (int)max(0ll, min((long long)it.tiles, end - it.first - kPgFixed));
+    it.t0 = (int)max(0ll, place.pos - first - kPgFixed);
+    it.t1 = max(it.t0 + 1, (int)min((long long)it.tiles, end - first - kPgFixed));
+    place.pos = first + kPgFixed + it.t1;
+    it.last = place.pos >= end;
+    it.end_block = (int)min(quotient(first + w - 1, share), gridDim.x - 1ll);
     return it;
 }
 
 // ------------------------------------------------------------- instructions
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes, or zeros for bytes = 0; read once, so the first to leave the L2
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy)
+                 : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -270,18 +294,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The workspace: for each worker (a warp) what the item that it leaves off needs
-// to be joined, then two slots of partial results: 0 for the item that it continues, 1
-// for the one that it leaves off.  A slot is [rows][D] sums, [rows] m, [rows] l.
+// The workspace: for each block what the item that it leaves off needs to be
+// joined, then two slots of partial results for each warp: 0 for an item that was begun
+// before the warp, 1 for the one that the block leaves off.  A slot is [rows][D] sums,
+// [rows] m, [rows] l.
 struct __align__(16) Tail {
-    int parts;               // 0: no item is left off
-    int b, h, tile_of_rows;
-    int from, step, last;    // part 0 is slot 1 of this worker, part j slot 0 of worker from + j * step,
-    int pad;                 // but the last one's of worker `last`
+    int parts;               // 0: no item is left off.  Part 0 is slot 1 of warp `lead`,
+    int lead;                // part j slot 0 of the first warp of the j-th block behind
+    int b, h, row0, pad[3];
 };
-__device__ __forceinline__ Tail *tail_of(float *ws, int worker) { return reinterpret_cast<Tail *>(ws) + worker; }
-__device__ __forceinline__ float *slot_of(float *ws, int workers, int worker, int slot, int nr, int D) {
-    return ws + (long long)workers * (sizeof(Tail) / 4) + (2ll * worker + slot) * nr * (D + 2);
+__device__ __forceinline__ Tail *tail_of(float *ws, int block) { return reinterpret_cast<Tail *>(ws) + block; }
+__device__ __forceinline__ float *slot_of(float *ws, int blocks, int worker, int slot, int nr, int D) {
+    return ws + (long long)blocks * (sizeof(Tail) / 4) + (2ll * worker + slot) * nr * (D + 2);
 }
 
 // m - 8 + log2 l in base e.  l's exponent is added to m before its mantissa's
@@ -296,8 +320,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
-__device__ __forceinline__ long long out_row(const PagedParams &p, const Seq &s, int h, int row) {
-    return (long long)(s.q0 + row / p.G) * (p.Hkv * p.G) + h * p.G + row % p.G;
+__device__ __forceinline__ long long out_row(const PagedParams &p, int q0, int h, int row) {
+    return (long long)(q0 + row / p.G) * (p.Hkv * p.G) + h * p.G + row % p.G;
 }
 
 // --------------------------------------------------------------- the kernel
@@ -307,61 +331,67 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     constexpr int NR = 8 * NT;
     constexpr int KG = D / 64;  // groups of four 16-byte pieces of a row
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ long long warp_sums[C::WARPS];
     __shared__ Place found[C::WARPS + 1];
     __shared__ int flag_of[C::WARPS];
-    __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR];
+    __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR], close_f[C::WARPS][NR];
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int page = 1 << p.page_log2;
     const uint32_t ring = smem_u32(sm) + warp * C::ST * C::STAGE_BYTES;
     float4 *const meta_of = reinterpret_cast<float4 *>(sm + C::OFF_META) + warp * C::ST * 2;
-    const int workers = gridDim.x * C::WARPS, worker = blockIdx.x * C::WARPS + warp;
+    Work *const work_of = reinterpret_cast<Work *>(sm + C::OFF_WORK) + warp * C::WORKS;
+    const uint64_t policy = l2_policy_evict_first();
 
-    const Line line = scan_line<C::WARPS>(p, NR, workers, warp_sums, found);
-    Place place = found[warp];
-    long long pos = place.pos;
+    const long long share = scan_line<C::WARPS>(p, NR, reinterpret_cast<long long *>(sm + C::OFF_SUMS), found);
+    Place ahead = found[warp];
     const long long end = found[warp + 1].pos;
+    const bool busy = ahead.pos < end;
     if (lane == 0) {
-        tail_of(p.ws, worker)->parts = 0;
+        if (warp == 0) tail_of(p.ws, blockIdx.x)->parts = 0;
         flag_of[warp] = 0;
     }
 
     // ---- pages: up to 16 tiles (32 halves) of one item looked up at a time, a half a
-    // lane, one such batch ahead of the copies
-    Place ahead = place;
-    long long pos_ahead = pos;
+    // lane, one such batch ahead of the copies; the items go into a ring for the loop below
+    Work next;              // the item being looked up
+    int t_next = 0, works = 0;
+    next.t1 = 0;
     int ph_next, key_next, nv_next, n_next;  // page * Hkv + head (-1: outside the cache), first key, keys there
     auto look_up = [&]() {
         n_next = 0;
         ph_next = 0, key_next = kPgMaxLen, nv_next = 0;
-        if (pos_ahead >= end) return;
-        const Item it = item_at(p, ahead, pos_ahead, end, NR);
-        n_next = max(0, min(16, it.t1 - it.t0));  // 0: the share ends within the item's fixed places
-        pos_ahead = it.first + kPgFixed + it.t0 + n_next;
+        if (t_next == next.t1) {
+            if (ahead.pos >= end) return;
+            next = work_at(p, ahead, end, share, NR);
+            t_next = next.t0;
+            if (lane == 0) work_of[works & (C::WORKS - 1)] = next;
+            ++works;
+        }
+        n_next = min(16, next.t1 - t_next);
+        const long long at = (long long)(t_next + (lane >> 1)) * kPgTile + (lane & 1) * 16;
+        t_next += n_next;
         if ((lane >> 1) >= n_next) return;
-        const long long at = (long long)(it.t0 + (lane >> 1)) * kPgTile + (lane & 1) * 16;
         long long of = at >> p.page_log2;  // position in the block table
         if (p.sel) {
-            const long long bh = (long long)it.b * p.Hkv + it.h;
+            const long long bh = (long long)next.b * p.Hkv + next.h;
             if (of >= min(p.sel_count[bh], p.sel_width)) return;
             of = p.sel[bh * p.sel_width + of];
             const long long k = (of << p.page_log2) + (at & (page - 1));
-            if (of < 0 || of >= (it.s.len + page - 1) >> p.page_log2) {
+            if (of < 0 || of >= (next.len + page - 1) >> p.page_log2) {
                 ph_next = -1, key_next = 0;
                 return;
             }
-            if (k >= it.s.len) return;
+            if (k >= next.len) return;
             key_next = (int)k;
         } else {
-            if (at >= it.s.len) return;
+            if (at >= next.len) return;
             key_next = (int)at;
         }
-        const int pg = p.table[(long long)it.b * p.max_pages + of];
+        const int pg = p.table[(long long)next.b * p.max_pages + of];
         const bool good = pg >= 0 && pg < p.num_pages;
-        ph_next = good ? pg * p.Hkv + it.h : -1;
-        nv_next = good ? min(16, it.s.len - key_next) : 0;
+        ph_next = good ? pg * p.Hkv + next.h : -1;
+        nv_next = good ? min(16, next.len - key_next) : 0;
     };
     look_up();
     // The batch being copied: each lane's half as a row of the cache, and what its
@@ -397,8 +427,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
                         const uint32_t dst = ((j & 1) ? st ^ ODD : st) + half * C::HALF_BYTES + j * 512;
-                        cp_async16(dst, ks + j * 512);
-                        cp_async16(dst + 2 * C::HALF_BYTES, vs + j * 512);
+                        cp_async16(dst, ks + j * 512, policy);
+                        cp_async16(dst + 2 * C::HALF_BYTES, vs + j * 512, policy);
                     }
                 } else {  // rows behind the sequence read as 0
                     const int nv = __shfl_sync(0xffffffffu, nv_now, 2 * at_now + half);
@@ -406,8 +436,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                     for (int j = 0; j < PER; ++j) {
                         const uint32_t dst = ((j & 1) ? st ^ ODD : st) + half * C::HALF_BYTES + j * 512;
                         const int n = j * (16 / PER) + r_lane < nv ? 16 : 0;
-                        cp_async16(dst, ks + j * 512, n);
-                        cp_async16(dst + 2 * C::HALF_BYTES, vs + j * 512, n);
+                        cp_async16(dst, ks + j * 512, n, policy);
+                        cp_async16(dst + 2 * C::HALF_BYTES, vs + j * 512, n, policy);
                     }
                 }
             }
@@ -429,8 +459,6 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
         }
         cp_commit();
     };
-#pragma unroll 1
-    for (int i = 0; i < C::ST - 1; ++i) issue();
     // where this lane reads: K rows by 16-byte loads, V rows by ldmatrix
     const int gk = C::key_of(g);
     const uint32_t k_read = ring + gk * D + (t ^ C::swap(gk)) * 16;
@@ -438,81 +466,84 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     const uint32_t v_read = ring + 2 * C::HALF_BYTES + v_row * D + C::swap(v_row) * 16;
     int stage_out = 0;
 
-    if (pos >= end) {  // nothing to do, but the others wait for every warp's flag
-        named_bar_sync(1, C::THREADS);
-        named_bar_sync(1, C::THREADS);
-    }
-    bool first_item = true;
-    while (pos < end) {
-        const Item it = item_at(p, place, pos, end, NR);
-        const Seq s = it.s;
-        const int h = it.h, t0 = it.t0, t1 = it.t1;
-        const int row0 = it.row0, rows = it.rows;
-        pos = it.first + kPgFixed + t1;
-
-        // ---- query rows: fragments of Q^T (lane: row g of each tile of 8)
-        uint32_t qf[NT][KG][4][2];
-        float fac[NT][2];   // c 2^e of the rows 2t, 2t+1, which this lane holds in accumulators
-        int lim[NT][2];     // the first key that they do not see
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = row0 + nt * 8 + g;
-            uint4 w[KG][2];
-            uint32_t am = 0;
-#pragma unroll
-            for (int i = 0; i < KG; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    w[i][j] = make_uint4(0, 0, 0, 0);
-                    if (row < rows) {
-                        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                                 (long long)(s.q0 + row / p.G) * p.q_stride +
-                                                 (long long)(h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
-                        w[i][j] = __ldg(reinterpret_cast<const uint4 *>(q));
-                    }
-                    const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) am = max(am, max(u[c] & 0x7fffu, (u[c] >> 16) & 0x7fffu));
-                }
-            am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-            am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            const int e = am ? max(-126, min(126, (int)(am >> 7) - 127)) : 0;
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-            for (int i = 0; i < KG; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        qf[nt][i][2 * j + c / 2][c & 1] =
-                            pack_f16x2(__uint_as_float(u[c] << 16) * down, __uint_as_float(u[c] & 0xffff0000u) * down);
-                }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                fac[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-                const int r = row0 + nt * 8 + 2 * t + j;
-                lim[nt][j] = r < rows ? s.len - s.nq + r / p.G + 1 : s.len;
-            }
-        }
-        const int lim_min = s.len - s.nq + row0 / p.G + 1;
-
-        float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = kPgNone;
-            l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[c][nt][j] = 0.f;
-        }
-
+    // ---- the warp's tiles, item after item
+    Work it;
+    int i = 0, done = 0, fill = C::ST - 1;
+    it.t1 = 0;
+    uint32_t qf[NT][KG][4][2];  // fragments of Q^T (lane: row g of each tile of 8)
+    float fac[NT][2];           // c 2^e of the rows 2t, 2t+1, which this lane holds in accumulators
+    int lim[NT][2], lim_min = 0;  // the first key that they do not see, and the least of them
+    float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
+    if (busy) {
 #pragma unroll 1
-        for (int i = t0; i < t1; ++i) {
-            cp_wait<C::ST - 2>();
-            __syncwarp();
+        for (;;) {
+            if (fill == 0) {
+                cp_wait<C::ST - 2>();
+                __syncwarp();
+            }
             issue();  // into the stage that the tile before was read from
+            if (fill > 0) {
+                --fill;
+                continue;
+            }
+            if (i == it.t1) {  // the next item
+                __syncwarp();
+                it = work_of[done & (C::WORKS - 1)];
+                ++done;
+                i = it.t0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int row = it.row0 + nt * 8 + g;
+                uint4 w[KG][2];
+                uint32_t am = 0;
+#pragma unroll
+                for (int i = 0; i < KG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        w[i][j] = make_uint4(0, 0, 0, 0);
+                        if (row < it.rows) {
+                            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
+                                                     (long long)(it.q0 + row / p.G) * p.q_stride +
+                                                     (long long)(it.h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
+                            w[i][j] = __ldg(reinterpret_cast<const uint4 *>(q));
+                        }
+                        const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) am = max(am, max(u[c] & 0x7fffu, (u[c] >> 16) & 0x7fffu));
+                    }
+                am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+                am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+                const int e = am ? max(-126, min(126, (int)(am >> 7) - 127)) : 0;
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int i = 0; i < KG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            qf[nt][i][2 * j + c / 2][c & 1] =
+                                pack_f16x2(__uint_as_float(u[c] << 16) * down, __uint_as_float(u[c] & 0xffff0000u) * down);
+                    }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    fac[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
+                    const int r = it.row0 + nt * 8 + 2 * t + j;
+                    lim[nt][j] = r < it.rows ? it.len - it.nq + r / p.G + 1 : it.len;
+                }
+            }
+            lim_min = it.len - it.nq + it.row0 / p.G + 1;
+
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    m[nt][0] = m[nt][1] = kPgNone;
+                    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[c][nt][j] = 0.f;
+                }
+            }
             const uint32_t st = stage_out * C::STAGE_BYTES;
             const float4 meta[2] = {meta_of[stage_out * 2], meta_of[stage_out * 2 + 1]};
             const int key[2] = {__float_as_int(meta[0].x), __float_as_int(meta[1].x)};
@@ -634,22 +665,22 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         for (int j = 0; j < 4; ++j) acc[c][nt][j] = settle(acc[c][nt][j], was[nt][j], nt, j & 1);
                 }
             };
-            if (!edge || lim_min >= s.len) {
+            if (!edge || lim_min >= it.len) {
                 accumulate([](uint32_t r, int, int) { return r; }, [](float now, float, int, int) { return now; });
             } else {
                 // Some rows do not see all of these keys: a weight of 0 would still turn a
                 // NaN among the values into NaN, so the values that a token does not see
                 // are cleared, a token at a time, and only that token's rows take the
                 // result (only the last tiles of a sequence come here).
-                const int tok0 = row0 / p.G, tok1 = min(s.nq - 1, (row0 + NR - 1) / p.G);
+                const int tok0 = it.row0 / p.G, tok1 = min(it.nq - 1, (it.row0 + NR - 1) / p.G);
 #pragma unroll 1
                 for (int tok = tok0; tok <= tok1; ++tok) {
-                    const int limit = s.len - s.nq + tok + 1;
+                    const int limit = it.len - it.nq + tok + 1;
                     bool my[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) my[nt][j] = (row0 + nt * 8 + 2 * t + j) / p.G == tok;
+                        for (int j = 0; j < 2; ++j) my[nt][j] = (it.row0 + nt * 8 + 2 * t + j) / p.G == tok;
                     accumulate(
                         [&](uint32_t r, int half, int up) {
                             const int k = key[half] + up * 8;
@@ -659,138 +690,127 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         [&](float now, float before, int nt, int j) { return my[nt][j] ? now : before; });
                 }
             }
-        }
 
-        // ---- the block's last items: warps whose whole share lies in the item of the warp
-        // before are joined with it.  (For the last of an item's warps that is so only
-        // where its share before moving boundaries ends with the item: the warp that
-        // describes the parts has to know.)
-        int group = 1, in_group = 0;      // warps of this warp's group, its own place among them
-        bool open = t1 < it.tiles;        // the item goes on behind them
-        bool begins = t0 == 0;
-        if (pos >= end) {
-            const long long it_end = it.first + kPgFixed + it.tiles;
-            const bool sole = warp > 0 && first_item && t0 > 0 &&
-                              (open || it_end == min((worker + 1) * line.share, line.total));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
-                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
-                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
-                    if (g == 0) {
-                        join_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
-                        join_l[warp][nt * 8 + 2 * t + j] = l[nt][j];
-                    }
-                }
-            cp_wait<0>();
-            __syncwarp();
-            float2 *const mine = reinterpret_cast<float2 *>(sm + warp * C::ST * C::STAGE_BYTES) + lane;  // over the ring
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        mine[((c * NT + nt) * 2 + j) * 32] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
-            if (lane == 0) flag_of[warp] = (sole ? 1 : 0) | (open ? 2 : 0) | (begins ? 4 : 0);
-            named_bar_sync(1, C::THREADS);
-            int lead = warp, last = warp;
-            while (flag_of[lead] & 1) --lead;
-            while (last + 1 < C::WARPS && (flag_of[last + 1] & 1)) ++last;
-            group = last - lead + 1;
-            in_group = warp - lead;
-            open = flag_of[last] & 2;
-            begins = flag_of[lead] & 4;
-            // every row's maximum over the group, and this warp's sums' factor to it
-            if (lane < NR) {
-                float M = kPgNone;
-                for (int w = lead; w <= last; ++w) M = fmaxf(M, join_m[w][lane]);
-                join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
-            }
-            named_bar_sync(1, C::THREADS);
-        }
-        first_item = false;
-
-        // ---- write the rows out, or what is known of them
-        const int lead = worker - in_group;
-        const bool whole = begins && !open;
-        float *const part = slot_of(p.ws, workers, lead, begins ? 1 : 0, NR, D);
-        if (group == 1) {
+            if (++i < it.t1) continue;
+            if (it.last) break;
+            // ---- an item that ends here, with others behind it: written out, or where it
+            // was begun before this warp, what is known of it
+            float *const part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + warp, 0, NR, D);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float y = l[nt][j];
-                    if (pos < end) {  // (otherwise summed above)
-                        y += __shfl_xor_sync(0xffffffffu, y, 4);
-                        y += __shfl_xor_sync(0xffffffffu, y, 8);
-                        y += __shfl_xor_sync(0xffffffffu, y, 16);
-                    }
+                    y += __shfl_xor_sync(0xffffffffu, y, 4);
+                    y += __shfl_xor_sync(0xffffffffu, y, 8);
+                    y += __shfl_xor_sync(0xffffffffu, y, 16);
                     const int r = nt * 8 + 2 * t + j;
-                    if (!whole) {
+                    if (it.t0 > 0) {
                         float2 *const o = reinterpret_cast<float2 *>(part + r * D) + g;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
                         if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = y;
-                    } else if (row0 + r < rows) {
+                    } else if (it.row0 + r < it.rows) {
                         const float inv = y == 0.f ? 0.f : 1.f / y;
-                        const long long at = out_row(p, s, h, row0 + r);
+                        const long long at = out_row(p, it.q0, it.h, it.row0 + r);
                         uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + g;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
                         if (g == 0) p.lse[at] = lse_of(m[nt][j], y);
                     }
                 }
-        } else {  // each warp of the group writes every group-th piece of the sums
-            const int w0 = warp - in_group;
-#pragma unroll 1
-            for (int u = in_group; u < C::UNITS; u += group) {
-                const int c = u / (2 * NT), r = (u / 2 % NT) * 8 + 2 * t + (u & 1);
-                float2 o = make_float2(0.f, 0.f);
-                float y = 0.f;
-                for (int w = w0; w < w0 + group; ++w) {
-                    const float f = join_f[w][r];
-                    const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[u * 32 + lane];
-                    o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y);
-                    y = fmaf(join_l[w][r], f, y);
-                }
-                float M = kPgNone;
-                if (c == 0)
-                    for (int w = w0; w < w0 + group; ++w) M = fmaxf(M, join_m[w][r]);
-                if (!whole) {
-                    reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
-                    if (c == 0 && g == 0) part[NR * D + r] = M, part[NR * D + NR + r] = y;
-                } else if (row0 + r < rows) {
-                    const float inv = y == 0.f ? 0.f : 1.f / y;
-                    const long long at = out_row(p, s, h, row0 + r);
-                    reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D)[8 * c + g] = pack_bf16x2(o.x * inv, o.y * inv);
-                    if (c == 0 && g == 0) p.lse[at] = lse_of(M, y);
-                }
-            }
-        }
-        if (begins && open && in_group == 0 && lane == 0) {
-            // the parts behind this one: the first warp of every further block, and the
-            // item's last warp unless it is in a group
-            const long long it_last = it.first + kPgFixed + it.tiles - 1;
-            const int last = (int)min(quotient(it_last, line.share), workers - 1ll), blk = last / C::WARPS;
-            const bool grouped = last % C::WARPS == 0 || it_last + 1 == min((last + 1) * line.share, line.total);
-            Tail tail;
-            tail.parts = 1 + (blk - blockIdx.x) + (grouped ? 0 : 1);
-            tail.b = it.b, tail.h = h, tail.tile_of_rows = row0 / NR;
-            tail.from = blockIdx.x * C::WARPS, tail.step = C::WARPS;
-            tail.last = grouped ? blk * C::WARPS : last;
-            tail.pad = 0;
-            *tail_of(p.ws, lead) = tail;
         }
     }
+
+    // ---- the warps' last items.  Warps that had nothing else than more of the item of
+    // the warp before them form a group with it, and so does, if the item still goes
+    // on, what the next warp left of its first item in its slot 0.  (That warp had
+    // other items behind it, so the item ended there.)
+    float2 *const sums_of = reinterpret_cast<float2 *>(sm + warp * C::ST * C::STAGE_BYTES) + lane;  // over the ring
+    if (busy) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float y = l[nt][j];
+                y += __shfl_xor_sync(0xffffffffu, y, 4);
+                y += __shfl_xor_sync(0xffffffffu, y, 8);
+                y += __shfl_xor_sync(0xffffffffu, y, 16);
+                if (g == 0) {
+                    join_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
+                    join_l[warp][nt * 8 + 2 * t + j] = y;
+                }
+            }
+        cp_wait<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    sums_of[((c * NT + nt) * 2 + j) * 32] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
+        if (lane == 0)
+            flag_of[warp] = (warp > 0 && done == 1 && it.t0 > 0 ? 1 : 0) | (it.t1 < it.tiles ? 2 : 0) | (it.t0 == 0 ? 4 : 0) | 8;
+    }
+    __syncthreads();
+    int lead = warp, last = warp;
+    while (lead > 0 && (flag_of[lead] & 1)) --lead;
+    while (last + 1 < C::WARPS && (flag_of[last + 1] & 1)) ++last;
+    bool open = flag_of[last] & 2;
+    const bool begins = flag_of[lead] & 4;
+    const bool closes = open && last + 1 < C::WARPS && (flag_of[last + 1] & 8);
+    const float *const closing = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + min(last + 1, C::WARPS - 1), 0, NR, D);
+    if (closes) open = false;
+    // every row's maximum over the group, and the factors of its parts to it
+    if (busy && lane < NR) {
+        float M = closes ? closing[NR * D + lane] : kPgNone;
+        for (int w = lead; w <= last; ++w) M = fmaxf(M, join_m[w][lane]);
+        join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
+        close_f[warp][lane] = closes ? ex2_approx(closing[NR * D + lane] - M) : 0.f;
+    }
+    __syncthreads();
+    if (!busy) return;
+    const bool whole = begins && !open;
+    float *const part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + lead, begins ? 1 : 0, NR, D);
+#pragma unroll 1
+    for (int u = warp - lead; u < C::UNITS; u += last - lead + 1) {  // a group's warps share the sums
+        const int c = u / (2 * NT), r = (u / 2 % NT) * 8 + 2 * t + (u & 1);
+        float2 o = make_float2(0.f, 0.f);
+        float y = 0.f, M = kPgNone;
+        if (closes) {
+            const float f = close_f[warp][r];
+            o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + g];
+            o.x *= f, o.y *= f;
+            y = closing[NR * D + NR + r] * f;
+            M = closing[NR * D + r];
+        }
+        for (int w = lead; w <= last; ++w) {
+            const float f = join_f[w][r];
+            const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[u * 32 + lane];
+            o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y);
+            y = fmaf(join_l[w][r], f, y);
+            M = fmaxf(M, join_m[w][r]);
+        }
+        if (!whole) {
+            reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
+            if (c == 0 && g == 0) part[NR * D + r] = M, part[NR * D + NR + r] = y;
+        } else if (it.row0 + r < it.rows) {
+            const float inv = y == 0.f ? 0.f : 1.f / y;
+            const long long at = out_row(p, it.q0, it.h, it.row0 + r);
+            reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D)[8 * c + g] = pack_bf16x2(o.x * inv, o.y * inv);
+            if (c == 0 && g == 0) p.lse[at] = lse_of(M, y);
+        }
+    }
+    if (begins && open && warp == lead && lane == 0)
+        *tail_of(p.ws, blockIdx.x) = Tail{it.end_block - (int)blockIdx.x + 1, lead, it.b, it.h, it.row0, {0, 0, 0}};
 }
 
-// Joins the partial results of the items that were cut: a warp, or where there are
-// many parts a block, takes one row of the item that a worker left off at a time.
+// Joins the partial results of the items that cross blocks: each block of this kernel
+// takes every fourth row of the item that one of them left off, a warp a row, or the
+// whole block where there are many parts.
 constexpr int kJoinWarps = 4;
-constexpr int kJoinMany = 12;  // parts
+constexpr int kJoinMany = 8;  // parts
 
 template <int D, int NR>
 struct JoinRow {
@@ -798,12 +818,13 @@ struct JoinRow {
     float M, L, O[E];
 
     // parts j0, j0 + step, ..
-    __device__ __forceinline__ void sum(const PagedParams &p, const Tail &tail, int workers, int worker, int r, int j0, int step) {
+    __device__ __forceinline__ void sum(const PagedParams &p, const Tail &tail, int blocks, int warps, int block, int r, int j0, int step) {
         const int lane = threadIdx.x & 31;
         M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) O[e] = 0.f;
         constexpr int UN = 4;  // parts in flight
+#pragma unroll 1
         for (; j0 < tail.parts; j0 += UN * step) {
             float m[UN], l[UN], o[UN][E];
 #pragma unroll
@@ -813,8 +834,7 @@ struct JoinRow {
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[u][e] = 0.f;
                 if (j < tail.parts) {
-                    const int from = j == 0 ? worker : j == tail.parts - 1 ? tail.last : tail.from + j * tail.step;
-                    const float *part = slot_of(p.ws, workers, from, j == 0, NR, D);
+                    const float *part = slot_of(p.ws, blocks, (block + j) * warps + (j == 0 ? tail.lead : 0), j == 0, NR, D);
                     m[u] = part[NR * D + r];
                     l[u] = part[NR * D + NR + r];
                     if (E == 4) {
@@ -864,55 +884,41 @@ struct JoinRow {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __grid_constant__ PagedParams p, int workers) {
-    constexpr int NR = 8 * NT, E = D / 32;
+__global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int NR = 8 * NT, E = D / 32, WARPS = PgCfg<D, NT>::WARPS;
     __shared__ float red_m[kJoinWarps], red_l[kJoinWarps], red_o[kJoinWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x, blocks = gridDim.x;
     JoinRow<D, NR> row_of;
     grid_wait();
-    // A block takes every gridDim-th worker, a lane looks at the tail of one of the next
-    // 32; a warp takes every fourth row of a tail.
-    for (int i0 = blockIdx.x; i0 < workers; i0 += 32 * gridDim.x) {
-        const int mine = i0 + lane * gridDim.x;
-        int parts = 0;
-        if (mine < workers) parts = tail_of(p.ws, mine)->parts;
-        uint32_t todo = __ballot_sync(0xffffffffu, parts > 0);
-        while (todo) {
-            const int k = __ffs((int)todo) - 1, worker = i0 + k * gridDim.x;
-            todo &= todo - 1;
-            const Tail tail = *tail_of(p.ws, worker);
-            const Seq s = sequence(p, tail.b);
-            const int row0 = tail.tile_of_rows * NR;
-            const int rows = max(0, min(NR, s.nq * p.G - row0));
-            if (tail.parts <= kJoinMany) {
-                for (int r = warp; r < rows; r += kJoinWarps) {
-                    row_of.sum(p, tail, workers, worker, r, 0, 1);
-                    row_of.write(p, out_row(p, s, tail.h, row0 + r));
-                }
-            } else {
-                for (int r = 0; r < rows; ++r) {
-                    row_of.sum(p, tail, workers, worker, r, warp, kJoinWarps);
-                    __syncthreads();  // the row before is read
-                    if (lane == 0) red_m[warp] = row_of.M, red_l[warp] = row_of.L;
+    const Tail tail = *tail_of(p.ws, block);
+    if (tail.parts == 0) return;
+    const Seq s = sequence(p, tail.b);
+    const int rows = min(NR, s.nq * p.G - tail.row0);
+    if (tail.parts <= kJoinMany) {
+        const int r = blockIdx.y * kJoinWarps + warp;
+        if (r >= rows) return;
+        row_of.sum(p, tail, blocks, WARPS, block, r, 0, 1);
+        row_of.write(p, out_row(p, s.q0, tail.h, tail.row0 + r));
+        return;
+    }
+#pragma unroll 1
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        row_of.sum(p, tail, blocks, WARPS, block, r, warp, kJoinWarps);
+        __syncthreads();  // the row before is read
+        if (lane == 0) red_m[warp] = row_of.M, red_l[warp] = row_of.L;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) red_o[warp][lane * E + e] = row_of.O[e];
-                    __syncthreads();
-                    if (warp != r % kJoinWarps) continue;
+        for (int e = 0; e < E; ++e) red_o[warp][lane * E + e] = row_of.O[e];
+        __syncthreads();
+        if (warp != 0) continue;
 #pragma unroll
-                    for (int w = 1; w < kJoinWarps; ++w) {
-                        const int v = (warp + w) % kJoinWarps;
-                        row_of.add(red_m[v], red_l[v], &red_o[v][lane * E]);
-                    }
-                    row_of.write(p, out_row(p, s, tail.h, row0 + r));
-                }
-            }
-        }
+        for (int v = 1; v < kJoinWarps; ++v) row_of.add(red_m[v], red_l[v], &red_o[v][lane * E]);
+        row_of.write(p, out_row(p, s.q0, tail.h, tail.row0 + r));
     }
 }
 
 template <int D, int NT>
 static size_t workspace_of(int num_sms) {
-    return (size_t)num_sms * PgCfg<D, NT>::WARPS * (sizeof(Tail) + 2 * 8 * NT * (D + 2) * sizeof(float));
+    return num_sms * (sizeof(Tail) + (size_t)PgCfg<D, NT>::WARPS * 2 * 8 * NT * (D + 2) * sizeof(float));
 }
 
 size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms) {
@@ -932,7 +938,7 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     // the join is launched while the first kernel still runs, and waits for its end
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4 * num_sms);
+    cfg.gridDim = dim3(num_sms, 8 * NT / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -940,7 +946,7 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p, num_sms * C::WARPS);
+    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p);
 }
 
 cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream) {
