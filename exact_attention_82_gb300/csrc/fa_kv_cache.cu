@@ -161,13 +161,15 @@ cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream
 
 // ------------------------------------------------------------------ append
 // Bound by HBM: 4 bytes of bf16 read and 2 bytes of codes written for a key and
-// a value element.  One CTA takes one run (consecutive tokens in one page: a
-// whole page of a prompt, or one token of a decode step) of one head, of K or of
-// V: its tokens stay in registers between the pass that takes the largest
-// magnitude and the one that writes codes, so that they are read once.  Eight
-// elements a thread: 16-byte loads, 8-byte stores.
-constexpr int kAppendThreads = 128;
-constexpr int kWindow = 64;  // tokens whose runs one set of CTAs shares
+// a value element.  A team of 1 to 8 warps takes one run (consecutive tokens in one
+// page: a whole page of a prompt, or one token of a decode step) of one head, of K or
+// of V.  The page's rows are spread over its threads, eight elements each, eight times
+// at most, and stay in registers between the pass that takes the largest magnitude and
+// the one that writes codes: the run's rows as bf16, and where the page's mean is kept the
+// rows before them as codes, so that everything a team reads is asked for at once.
+// The size of the team follows from the page's: small pages go to single warps, which
+// meet no barrier.
+constexpr int kWindow = 64;  // tokens whose runs one set of blocks shares
 
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     uint32_t h;
@@ -203,159 +205,209 @@ __device__ __forceinline__ float pow2_scale(float amax) {
     return __uint_as_float((uint32_t)(max(-100, min(120, e)) + 127) << 23);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const AppendParams p, int share) {
-    constexpr int TPT = D / 8;                     // threads a token
-    constexpr int ROWS = kAppendThreads / TPT;     // tokens a pass
-    constexpr int PASSES = 128 / ROWS;             // passes over the largest page
-    __shared__ unsigned long long starts;
-    __shared__ uint32_t match[kAppendThreads / 32];
-    __shared__ uint32_t amax_sm[kAppendThreads / 32];
-    __shared__ int sums[D];
+template <int D, int PAGE>
+struct AppendCfg {
+    static constexpr int TEAM = PAGE * D < 2048 ? 1 : PAGE * D / 2048;  // warps
+    static constexpr int WARPS = TEAM > 4 ? TEAM : 4;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int TEAMS = WARPS / TEAM;
+    static constexpr int TPT = D / 8;                                 // threads a token
+    static constexpr int ROWS = 32 * TEAM / TPT;                      // tokens a pass
+    static constexpr int PASSES = PAGE / ROWS;
+};
+
+template <int D, int PAGE>
+__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
+    using C = AppendCfg<D, PAGE>;
+    __shared__ int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
+    __shared__ uint32_t starts[kWindow / 32];
+    __shared__ uint32_t amax_sm[2][C::WARPS];
+    __shared__ int sums[C::WARPS][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
     const int h = blockIdx.y, kv = blockIdx.z;
     const int win = blockIdx.x / share, part = blockIdx.x % share;
-    const int t0 = win * kWindow, page = 1 << p.page_log2;
-    const long long limit = (long long)p.num_pages << p.page_log2;
-    const __nv_bfloat16 *const x_of = static_cast<const __nv_bfloat16 *>(kv ? p.x[1] : p.x[0]);
+    const int t0 = win * kWindow;
+    const int limit = p.num_pages * PAGE;  // fewer than 2^31
+    const __nv_bfloat16 *const x_of = static_cast<const __nv_bfloat16 *>(kv ? p.x[1] : p.x[0]) + h * D;
     const long long stride = kv ? p.stride[1] : p.stride[0];
     float *const scale_of = kv ? p.scale[1] : p.scale[0];
     uint8_t *const pages_of = kv ? p.pages[1] : p.pages[0];
+    auto team_sync = [&]() {
+        if (C::TEAM == 1)
+            __syncwarp();
+        else
+            named_bar_sync(1 + team, C::TEAM * 32);
+    };
 
-    // run starts of the window
-    {
-        bool start = false;
-        const int t = t0 + tid;
-        if (tid < kWindow && t < p.T) {
-            const int s = p.slots[t];
-            start = s >= 0 && s < limit && (t == 0 || p.slots[t - 1] != s - 1 || (s & (page - 1)) == 0);
-            if (s >= limit) atomicExch(&g_status_kv_cache, (int)FA_ERR_BAD_PAGE);
-        }
+    // ---- the runs that begin in the window
+    for (int i = tid; i < kWindow + PAGE; i += C::THREADS) slot_of[i] = t0 + i < p.T ? p.slots[t0 + i] : -1;
+    int before = -2;
+    if (tid == 0 && t0 > 0) before = p.slots[t0 - 1];
+    __syncthreads();
+    for (int i = warp * 32; i < kWindow; i += C::THREADS) {
+        const int s = slot_of[i + lane], prev = i + lane > 0 ? slot_of[i + lane - 1] : before;
+        const bool start = s >= 0 && s < limit && (prev != s - 1 || s % PAGE == 0);
+        if (s >= limit) atomicExch(&g_status_kv_cache, (int)FA_ERR_BAD_PAGE);
         const uint32_t m = __ballot_sync(0xffffffffu, start);
-        if (lane == 0 && warp < 2) reinterpret_cast<uint32_t *>(&starts)[warp] = m;
-        __syncthreads();
+        if (lane == 0) starts[i / 32] = m;
     }
-    unsigned long long todo = starts;
-    for (int ordinal = 0; todo; ++ordinal) {
-        const int t = t0 + __ffsll((long long)todo) - 1;
-        todo &= todo - 1;
-        if (ordinal % share != part) continue;
-        const int slot = p.slots[t], off = slot & (page - 1), pg = slot >> p.page_log2;
-        const bool same = tid < page - off && t + tid < p.T && p.slots[t + tid] == slot + tid;
-        const uint32_t m = __ballot_sync(0xffffffffu, same);
-        __syncthreads();  // the shared words of the run before are read
-        if (lane == 0) match[warp] = m;
-        if (tid < D) sums[tid] = 0;
-        __syncthreads();
+    __syncthreads();
+    // this lane's two tokens, and how many runs begin before each
+    const uint32_t s0 = starts[0], s1 = starts[1], lt = (1u << lane) - 1;
+    const int rank0 = (s0 >> lane) & 1u ? __popc(s0 & lt) : -1, rank1 = (s1 >> lane) & 1u ? __popc(s0) + __popc(s1 & lt) : -1;
+    const int runs = __popc(s0) + __popc(s1);
+    for (int run = part * C::TEAMS + team; run < runs; run += share * C::TEAMS) {
+        const uint32_t m0 = __ballot_sync(0xffffffffu, rank0 == run), m1 = __ballot_sync(0xffffffffu, rank1 == run);
+        const int i0 = m0 ? __ffs((int)m0) - 1 : 31 + __ffs((int)m1);
+        const int slot = slot_of[i0], off = slot % PAGE, pg = slot / PAGE;
         int n = 0;  // tokens of the run
 #pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w) {
-            if (n == 32 * w) n += match[w] == 0xffffffffu ? 32 : __ffs((int)~match[w]) - 1;
+        for (int w = 0; w < (PAGE + 31) / 32; ++w) {
+            const int i = w * 32 + lane;
+            const uint32_t m = __ballot_sync(0xffffffffu, i < PAGE - off && slot_of[i0 + min(i, PAGE - 1)] == slot + i);
+            if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
         }
 
-        const int sub = tid % TPT, row0 = tid / TPT;
-        const __nv_bfloat16 *x = x_of + h * D + sub * 8;
-        uint4 w[PASSES];
+        // ---- everything that is read, at once: row r0 + i ROWS of the page in slot i
+        const int sub = tt % C::TPT, r0 = tt / C::TPT;
+        const long long ph = (long long)pg * p.Hkv + h;
+        const float was = scale_of[ph];
+        uint8_t *const codes = pages_of + ph * PAGE * D + sub * 8;
+        const __nv_bfloat16 *const x = x_of + (long long)(t0 + i0 - off) * stride + sub * 8;  // row 0's token
+        const bool mean = kv == 0 && p.mean != nullptr;
+        uint4 w[C::PASSES];
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
+        for (int i = 0; i < C::PASSES; ++i) {
+            const int r = r0 + i * C::ROWS;
             w[i] = make_uint4(0, 0, 0, 0);
-            if (row0 + i * ROWS < n)
-                w[i] = __ldg(reinterpret_cast<const uint4 *>(x + (long long)(t + row0 + i * ROWS) * stride));
+            if (r >= off && r < off + n) {
+                w[i] = __ldg(reinterpret_cast<const uint4 *>(x + r * stride));
+            } else if (mean && r < off) {
+                const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                w[i].x = c.x, w[i].y = c.y;
+            }
         }
         // magnitudes of bf16 compare as integers; those of exponent 255 do not count
         uint32_t am = 0;
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
+        for (int i = 0; i < C::PASSES; ++i) {
+            const int r = r0 + i * C::ROWS;
             const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
-                am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                if (r >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
             }
         }
         am = __reduce_max_sync(0xffffffffu, am);
-        if (lane == 0) amax_sm[warp] = am;
-        const long long ph = (long long)pg * p.Hkv + h;
-        const float was = scale_of[ph];
-        __syncthreads();
+        if (C::TEAM > 1) {
+            if (lane == 0) amax_sm[0][warp] = am;
+            team_sync();
 #pragma unroll
-        for (int v = 0; v < kAppendThreads / 32; ++v) am = max(am, amax_sm[v]);
+            for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
+        } else {
+            team_sync();
+        }
         float scale = pow2_scale(__uint_as_float(am << 16));
         if (off > 0) scale = fmaxf(scale, was);
-        if (tid == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
-
-        uint8_t *codes = pages_of + ((ph << p.page_log2) * D) + sub * 8;
-        const bool mean = kv == 0 && p.mean != nullptr;
-        int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
         // x / scale is x * (1 / scale) exactly where the scale is a power of two
         // (always, unless the caller put another one there)
         const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-        const float inv_scale = 1.f / scale;
-        // the rows before the run, rounded again where the scale has grown
-        if (off > 0 && (mean || scale != was)) {
-            const float f = was / scale;
-            for (int r = row0; r < off; r += ROWS) {
-                uint2 c = *reinterpret_cast<const uint2 *>(codes + (long long)r * D);
-                float y[8];
-                decode8(c, y);
-                if (scale != was) {
+        const float inv_scale = 1.f / scale, shrink = was / scale;
+        const bool grown = off > 0 && scale != was;  // the rows before the run are rounded again
+        int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] *= f;
-                    c = encode8(y);
-                    *reinterpret_cast<uint2 *>(codes + (long long)r * D) = c;
-                    decode8(c, y);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] += y[i] == y[i] ? (int)(y[i] * 512.f) : 0;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int r = row0 + i * ROWS;
-            if (r < n) {
-                float y[8];
+        for (int i = 0; i < C::PASSES; ++i) {
+            const int r = r0 + i * C::ROWS;
+            if (r >= off + n) continue;
+            uint2 c = make_uint2(w[i].x, w[i].y);
+            float y[8];
+            if (r >= off) {
                 bf16x8(w[i], y);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) y[c] = pow2 ? y[c] * inv_scale : y[c] / scale;
-                const uint2 c = encode8(y);
-                *reinterpret_cast<uint2 *>(codes + (long long)(off + r) * D) = c;
-                if (mean) {
-                    decode8(c, y);
+                for (int j = 0; j < 8; ++j) y[j] = pow2 ? y[j] * inv_scale : y[j] / scale;
+            } else if (grown) {
+                if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                decode8(c, y);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += y[j] == y[j] ? (int)(y[j] * 512.f) : 0;
-                }
+                for (int j = 0; j < 8; ++j) y[j] *= shrink;
+            }
+            if (r >= off || grown) {
+                c = encode8(y);
+                *reinterpret_cast<uint2 *>(codes + r * D) = c;
+            }
+            if (mean) {
+                decode8(c, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += y[j] == y[j] ? (int)(y[j] * 512.f) : 0;
             }
         }
         if (mean) {  // integer sums: the same in any order
 #pragma unroll
-            for (int j = 0; j < 8; ++j) atomicAdd(&sums[sub * 8 + j], sum[j]);
-            __syncthreads();
-            int a = tid < D ? abs(sums[tid]) : 0;
-            a = __reduce_max_sync(0xffffffffu, a);
-            if (lane == 0) amax_sm[warp] = (uint32_t)a;
-            __syncthreads();
+            for (int j = 0; j < 8; ++j) {
 #pragma unroll
-            for (int v = 0; v < kAppendThreads / 32; ++v) a = max(a, (int)amax_sm[v]);
+                for (int d = C::TPT; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+                if (lane < C::TPT) sums[warp][lane * 8 + j] = sum[j];
+            }
+            team_sync();
+            constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
+            int total[PER], a = 0;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int d = tt + c * 32 * C::TEAM;
+                total[c] = 0;
+                if (d < D)
+#pragma unroll
+                    for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
+                a = max(a, abs(total[c]));
+            }
+            a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
+            if (C::TEAM > 1) {
+                if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
+                team_sync();
+#pragma unroll
+                for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
+            }
             const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
-            if (tid < D) p.mean[ph * D + tid] = (int8_t)__float2int_rn((float)sums[tid] * inv);
-            if (tid == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (off + n));
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int d = tt + c * 32 * C::TEAM;
+                if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
+            }
+            if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (off + n));
         }
+        team_sync();  // the next run overwrites the shared words
+    }
+}
+
+template <int D, int PAGE>
+static cudaError_t launch_append(const AppendParams &p, int num_sms, cudaStream_t stream) {
+    const int windows = (p.T + kWindow - 1) / kWindow;
+    // Blocks that share a window's runs: as many as a decode step has (64 of one
+    // token each) while there are few windows, one where a prompt fills the chip.
+    const long long per = (long long)windows * p.Hkv * 2;
+    constexpr int most = kWindow / AppendCfg<D, PAGE>::TEAMS;
+    long long share = 32ll * num_sms / per;
+    share = share < 1 ? 1 : (share > most ? most : share);
+    const dim3 grid((unsigned)(windows * share), p.Hkv, 2);
+    fa_kv_append_kernel<D, PAGE><<<grid, AppendCfg<D, PAGE>::THREADS, 0, stream>>>(p, (int)share);
+    return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_append_page(const AppendParams &p, int num_sms, cudaStream_t stream) {
+    switch (p.page_log2) {
+        case 4: return launch_append<D, 16>(p, num_sms, stream);
+        case 5: return launch_append<D, 32>(p, num_sms, stream);
+        case 6: return launch_append<D, 64>(p, num_sms, stream);
+        default: return launch_append<D, 128>(p, num_sms, stream);
     }
 }
 
 cudaError_t launch_kv_append(int D, const AppendParams &p, int num_sms, cudaStream_t stream) {
-    const int windows = (p.T + kWindow - 1) / kWindow;
-    // CTAs that share a window's runs: as many as a decode step has (64 of one
-    // token each) while there are few windows, one when a prompt fills the chip
-    const long long per = (long long)windows * p.Hkv * 2;
-    int share = (int)((32ll * num_sms + per - 1) / per);
-    share = share < 1 ? 1 : (share > kWindow ? kWindow : share);
-    const dim3 grid((unsigned)(windows * share), p.Hkv, 2);
-    if (D == 64)
-        fa_kv_append_kernel<64><<<grid, kAppendThreads, 0, stream>>>(p, share);
-    else
-        fa_kv_append_kernel<128><<<grid, kAppendThreads, 0, stream>>>(p, share);
-    return cudaGetLastError();
+    return D == 64 ? launch_append_page<64>(p, num_sms, stream) : launch_append_page<128>(p, num_sms, stream);
 }
 
 cudaError_t kv_cache_status_read_and_clear(int *out) {
