@@ -183,6 +183,13 @@ __device__ __forceinline__ void decode8(const uint2 w, float (&f)[8]) {
     f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
 }
 
+// NaN codes (0x7f and 0xff) as 0
+__device__ __forceinline__ uint32_t without_nan(uint32_t c) {
+    const uint32_t nan = ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    return nan ? c & ~((nan >> 7) * 0xffu) : c;
+}
+__device__ __forceinline__ uint2 without_nan(uint2 c) { return make_uint2(without_nan(c.x), without_nan(c.y)); }
+
 __device__ __forceinline__ uint2 encode8(const float (&f)[8]) {
     return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
@@ -288,16 +295,26 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kern
                 w[i].x = c.x, w[i].y = c.y;
             }
         }
-        // magnitudes of bf16 compare as integers; those of exponent 255 do not count
-        uint32_t am = 0;
+        // magnitudes of bf16 compare as integers, two at a time
+        uint32_t am2 = 0;
 #pragma unroll
         for (int i = 0; i < C::PASSES; ++i) {
-            const int r = r0 + i * C::ROWS;
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t u = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                  __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+            if (r0 + i * C::ROWS < off) u = 0;
+            am2 = __vmaxu2(am2, u);
+        }
+        uint32_t am = max(am2 & 0xffffu, am2 >> 16);
+        if (am >= 0x7f80u) {  // infinities and NaN do not count
+            am = 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
-                if (r >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            for (int i = 0; i < C::PASSES; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
+                    if (r0 + i * C::ROWS >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                }
             }
         }
         am = __reduce_max_sync(0xffffffffu, am);
@@ -317,7 +334,9 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kern
         const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
         const float inv_scale = 1.f / scale, shrink = was / scale;
         const bool grown = off > 0 && scale != was;  // the rows before the run are rounded again
-        int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        // the codes' sums: multiples of 2^-9, at most 8 of them of at most 448 a thread, are exact in fp32
+        static_assert(C::PASSES <= 8, "");
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < C::PASSES; ++i) {
             const int r = r0 + i * C::ROWS;
@@ -339,17 +358,18 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kern
                 *reinterpret_cast<uint2 *>(codes + r * D) = c;
             }
             if (mean) {
-                decode8(c, y);
+                decode8(without_nan(c), y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] += y[j] == y[j] ? (int)(y[j] * 512.f) : 0;
+                for (int j = 0; j < 8; ++j) sum[j] += y[j];
             }
         }
         if (mean) {  // integer sums: the same in any order
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                int x = (int)(sum[j] * 512.f);
 #pragma unroll
-                for (int d = C::TPT; d < 32; d <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-                if (lane < C::TPT) sums[warp][lane * 8 + j] = sum[j];
+                for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
             }
             team_sync();
             constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
