@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kern
         float scale = pow2_scale(__uint_as_float(am << 16));
         if (off > 0) scale = fmaxf(scale, was);
         if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
-        // x / scale is x * (1 / scale) exactly where the scale is a power of two
-        // (always, unless the caller put another one there)
+        // x / scale is x * (1 / scale) exactly where the scale is a power of two (always,
+        // unless the caller put another one there; the remainder corrects it then)
         const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
         const float inv_scale = 1.f / scale, shrink = was / scale;
         const bool grown = off > 0 && scale != was;  // the rows before the run are rounded again
@@ -340,24 +340,38 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kern
 #pragma unroll
         for (int i = 0; i < C::PASSES; ++i) {
             const int r = r0 + i * C::ROWS;
-            if (r >= off + n) continue;
-            uint2 c = make_uint2(w[i].x, w[i].y);
+            if (r < off || r >= off + n) continue;
             float y[8];
-            if (r >= off) {
-                bf16x8(w[i], y);
+            bf16x8(w[i], y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = pow2 ? y[j] * inv_scale : y[j] / scale;
-            } else if (grown) {
-                if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                decode8(c, y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= shrink;
+            for (int j = 0; j < 8; ++j) {
+                const float x = y[j];
+                y[j] = x * inv_scale;
+                if (!pow2) y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
             }
-            if (r >= off || grown) {
-                c = encode8(y);
-                *reinterpret_cast<uint2 *>(codes + r * D) = c;
-            }
+            const uint2 c = encode8(y);
+            *reinterpret_cast<uint2 *>(codes + r * D) = c;
             if (mean) {
+                decode8(without_nan(c), y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += y[j];
+            }
+        }
+        if (off > 0 && (mean || grown)) {  // apart, so that prompts' whole pages skip it
+#pragma unroll
+            for (int i = 0; i < C::PASSES; ++i) {
+                const int r = r0 + i * C::ROWS;
+                if (r >= off) continue;
+                uint2 c = make_uint2(w[i].x, w[i].y);
+                float y[8];
+                if (grown) {
+                    if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                    decode8(c, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] *= shrink;
+                    c = encode8(y);
+                    *reinterpret_cast<uint2 *>(codes + r * D) = c;
+                }
                 decode8(without_nan(c), y);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[j] += y[j];
