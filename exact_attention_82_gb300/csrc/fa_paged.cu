@@ -71,8 +71,7 @@ struct PgCfg {
     static constexpr int OFF_WORK = OFF_META + WARPS * ST * 2 * 16;
     static constexpr int WORKS = 8;                          // items looked up ahead: ST + 1 at most
     static constexpr int OFF_SUMS = OFF_WORK + WARPS * WORKS * 48;
-    static constexpr int SMEM = OFF_SUMS + THREADS * 8;
-    static constexpr int UNITS = CHUNKS * NT * 2;            // float2 of sums that a lane holds
+    static constexpr int SMEM = OFF_SUMS + THREADS * 4;
     // Where a 16-byte piece of a row lies: pieces are swapped within 128 bytes so that
     // eight rows' same piece (ldmatrix) falls into different banks.
     static __device__ __forceinline__ int swap(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
@@ -83,11 +82,11 @@ struct PgCfg {
     }
 };
 
-// A place in the line of tiles.
+// A place in the line of tiles (32 bits: the caller has checked that they do).
 struct Place {
-    int entry;        // sequence, or sequence * Hkv + head where pages are selected
-    long long base;   // first place of the entry
-    long long pos;
+    int entry;   // sequence, or sequence * Hkv + head where pages are selected
+    int base;    // first place of the entry
+    int pos;
 };
 
 struct Seq {
@@ -110,28 +109,18 @@ __device__ __forceinline__ int item_tiles(const PagedParams &p, int b, int h, in
     return max(1, (int)((keys + kPgTile - 1) / kPgTile));
 }
 
-// Rare work (once a share, an item or sixteen tiles) is kept out of line, so that the
-// loop over tiles stays within the instruction cache: with the 64-bit divisions of it
-// inlined everywhere the kernel was 192 KB long and spent 25 us on fetching itself.
-__device__ __noinline__ long long entry_weight(const PagedParams &p, int e, int nr) {
+__device__ __forceinline__ int entry_weight(const PagedParams &p, int e, int nr) {
     const int b = p.sel ? e / p.Hkv : e, h = p.sel ? e % p.Hkv : 0;
     const Seq s = sequence(p, b);
-    if (s.nq == 0) return 0;
-    const long long rt = (s.nq * p.G + nr - 1) / nr;
+    const int rt = (s.nq * p.G + nr - 1) / nr;
     return rt * (p.sel ? 1 : p.Hkv) * (kPgFixed + item_tiles(p, b, h, s.len));
 }
 
-// x / y for x >= 0, y > 0
-__device__ __noinline__ long long quotient(long long x, long long y) {
-    if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
-    return x / y;
-}
-
-// Finds the place of `pos` from the sums over the threads' entries.  Where it falls
-// into an item's fixed places, or into an item of at most `small` places, it is moved
-// to the item's beginning or its nearer end.
-__device__ __noinline__ Place place_of(const PagedParams &p, const long long *sums, int threads, int per, int n, int nr,
-                                       long long pos, long long small) {
+// The place of `pos`, from the sums up to the end of each thread's entries.  Where it
+// falls into an item's fixed places, or into an item of at most `small` places, it is
+// moved to the item's beginning or its nearer end.
+__device__ __forceinline__ Place place_of(const PagedParams &p, const int *sums, int threads, int per, int n, int nr, int pos,
+                                          int small) {
     int lo = 0, hi = threads - 1;  // the first thread whose sum is above pos
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -140,70 +129,20 @@ __device__ __noinline__ Place place_of(const PagedParams &p, const long long *su
         else
             lo = mid + 1;
     }
-    Place f;
-    f.entry = min(lo * per, n - 1);
-    f.base = lo ? sums[lo - 1] : 0;
-    f.pos = pos;
+    Place f{min(lo * per, n - 1), lo ? sums[lo - 1] : 0, pos};
+#pragma unroll 1
     for (const int e1 = min(n, f.entry + per); f.entry < e1 - 1; ++f.entry) {
-        const long long w = entry_weight(p, f.entry, nr);
+        const int w = entry_weight(p, f.entry, nr);
         if (pos < f.base + w) break;
         f.base += w;
     }
     const int b = p.sel ? f.entry / p.Hkv : f.entry, h = p.sel ? f.entry % p.Hkv : 0;
-    const long long size = kPgFixed + item_tiles(p, b, h, sequence(p, b).len);
-    const long long in = (pos - f.base) - quotient(pos - f.base, size) * size;
+    const int size = kPgFixed + item_tiles(p, b, h, sequence(p, b).len), in = (uint32_t)(pos - f.base) % (uint32_t)size;
     if (in <= kPgFixed || (size <= small && 2 * in < size))
         f.pos -= in;
     else if (size <= small)
         f.pos += size - in;
     return f;
-}
-
-// Scans the line.  Returns the share of a block, and leaves in found[w] where the
-// block's warp w begins, in found[w + 1] where it ends.
-template <int WARPS>
-__device__ __forceinline__ long long scan_line(const PagedParams &p, int nr, long long *sums, Place *found) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int THREADS = 32 * WARPS;
-    const int n = p.sel ? p.B * p.Hkv : p.B;
-    const int per = (n + THREADS - 1) / THREADS;
-    long long x = 0;
-    for (int e = min(n, tid * per); e < min(n, tid * per + per); ++e) x += entry_weight(p, e, nr);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    sums[tid] = x;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const long long y = sums[w * 32 + 31];
-        if (w < warp) before += y;
-        total += y;
-    }
-    __syncthreads();
-    sums[tid] = x + before;
-    long long share = quotient(total + gridDim.x - 1, gridDim.x);
-    // With less work than the chip has room for, items of up to two least shares stay whole.
-    const long long small = share <= kPgMinShare ? 2 * kPgMinShare : share / 2;
-    if (share < kPgMinShare) share = kPgMinShare;
-    __syncthreads();
-    if (warp == 0) {
-        Place f{0, 0, total};
-        const long long cut = (long long)(blockIdx.x + (lane == WARPS)) * share;
-        if ((lane == 0 || lane == WARPS) && cut < total) f = place_of(p, sums, THREADS, per, n, nr, cut, small);
-        const long long begin = __shfl_sync(0xffffffffu, f.pos, 0), end = __shfl_sync(0xffffffffu, f.pos, WARPS);
-        const long long part = quotient(end - begin + WARPS - 1, WARPS), pos = begin + lane * part;
-        if (lane > 0 && lane < WARPS) {
-            f.pos = end;
-            if (pos < end) f = place_of(p, sums, THREADS, per, n, nr, pos, part / 2);
-        }
-        if (lane <= WARPS) found[lane] = f;
-    }
-    __syncthreads();
-    return share;
 }
 
 // What a warp does for one item.
@@ -216,13 +155,17 @@ struct Work {
 };
 static_assert(sizeof(Work) == 48, "");
 
-// The item at place.pos, which is moved behind the warp's tiles of it.
-__device__ __noinline__ Work work_at(const PagedParams &p, Place &place, long long end, long long share, int nr) {
+// The item at place.pos, which is moved behind the warp's tiles of it.  (Rare work like
+// this is kept out of line, so that the loop over tiles stays within the instruction
+// cache: with all of it inlined, in 64 bits, the kernel was 192 KB long and spent 25 us on
+// fetching itself.)
+__device__ __noinline__ Work work_at(const PagedParams &p, Place &place, int end, int share, int nr) {
     // The scan's lengths and these are the same unless the caller changes them during
     // the call; the bounds on entry, head and block keep every access inside even then.
     const int n = p.sel ? p.B * p.Hkv : p.B;
+#pragma unroll 1
     for (; place.entry < n - 1; ++place.entry) {
-        const long long w = entry_weight(p, place.entry, nr);
+        const int w = entry_weight(p, place.entry, nr);
         if (place.pos < place.base + w) break;
         place.base += w;
     }
@@ -233,17 +176,90 @@ __device__ __noinline__ Work work_at(const PagedParams &p, Place &place, long lo
     it.q0 = s.q0, it.nq = s.nq, it.len = s.len;
     it.tiles = item_tiles(p, it.b, it.h, s.len);
     it.rows = s.nq * p.G;
-    const long long w = kPgFixed + it.tiles, nth = quotient(place.pos - place.base, w), first = place.base + nth * w;
-    const int rts = max(1, (it.rows + nr - 1) / nr);
-    int rt = (int)nth;  // items of an entry: fewer than 2^31
-    if (!p.sel) it.h = min(rt / rts, p.Hkv - 1), rt = rt % rts;
+    const int w = kPgFixed + it.tiles;
+    int rt = (int)((uint32_t)(place.pos - place.base) / (uint32_t)w);
+    const int first = place.base + rt * w;
+    if (!p.sel) {
+        const int rts = max(1, (it.rows + nr - 1) / nr);
+        it.h = min(rt / rts, p.Hkv - 1), rt = rt % rts;
+    }
     it.row0 = rt * nr;
-    it.t0 = (int)max(0ll, place.pos - first - kPgFixed);
-    it.t1 = max(it.t0 + 1, (int)min((long long)it.tiles, end - first - kPgFixed));
+    it.t0 = max(0, place.pos - first - kPgFixed);
+    it.t1 = max(it.t0 + 1, min(it.tiles, end - first - kPgFixed));
     place.pos = first + kPgFixed + it.t1;
     it.last = place.pos >= end;
-    it.end_block = (int)min(quotient(first + w - 1, share), gridDim.x - 1ll);
+    it.end_block = min((first + w - 1) / share, (int)gridDim.x - 1);
     return it;
+}
+
+// Where a warp is after the scan: behind its first item, which lies in its ring.
+struct Start {
+    Place ahead;   // entry -1: no work
+    int end;       // of the warp's share
+};
+
+// Scans the line and starts every warp of the block.  Returns the share of a block.
+template <int WARPS>
+__device__ __forceinline__ int scan_line(const PagedParams &p, int nr, int *sums, Start *start, Work *work_of, int works) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int THREADS = 32 * WARPS;
+    __shared__ int share_sm;
+    const int n = p.sel ? p.B * p.Hkv : p.B;
+    const int per = (n + THREADS - 1) / THREADS;
+    long long x = 0;
+#pragma unroll 4
+    for (int e = min(n, tid * per); e < min(n, tid * per + per); ++e) x += entry_weight(p, e, nr);
+    sums[tid] = (int)min(x, 0x7fffffffll);
+    __syncthreads();
+    if (warp == 0) {  // a lane takes WARPS threads' sums, then a boundary between warps, then a warp's first item
+        int sum[WARPS];
+        long long all = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            all += sums[lane * WARPS + w];
+            sum[w] = (int)all;
+        }
+        x = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        const long long all_places = __shfl_sync(0xffffffffu, x, 31);
+        int total = (int)all_places;
+        if (all_places >= 0x7ff00000ll) {  // cu_q does not ascend: more tokens than T
+            total = 0;
+            if (lane == 0) atomicExch(&g_status_paged, (int)FA_ERR_BAD_SHAPE);
+        }
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) sums[lane * WARPS + w] = sum[w] + (int)(x - all);
+        __syncwarp();
+        int share = (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x);
+        // With less work than the chip has room for, items of up to two least shares stay whole.
+        const int small = share <= kPgMinShare ? 2 * kPgMinShare : share / 2;
+        share = max(share, kPgMinShare);
+        // the block's ends, then the warps'
+        Place f{0, 0, total};
+        const long long cut = (long long)(blockIdx.x + (lane == WARPS)) * share;
+        if (cut < total) f = place_of(p, sums, THREADS, per, n, nr, (int)cut, small);
+        const int begin = __shfl_sync(0xffffffffu, f.pos, 0), end = __shfl_sync(0xffffffffu, f.pos, WARPS);
+        const int part = (end - begin + WARPS - 1) / WARPS, pos = begin + lane * part;
+        if (lane > 0 && lane < WARPS) {
+            f.pos = end;
+            if (pos < end) f = place_of(p, sums, THREADS, per, n, nr, pos, part / 2);
+        }
+        Start st{f, __shfl_down_sync(0xffffffffu, f.pos, 1)};
+        if (lane < WARPS) {
+            if (f.pos < st.end)
+                work_of[lane * works] = work_at(p, st.ahead, st.end, share, nr);
+            else
+                st.ahead.entry = -1;
+            start[lane] = st;
+        }
+        if (lane == 0) share_sm = share;
+    }
+    __syncthreads();
+    return share_sm;
 }
 
 // ------------------------------------------------------------- instructions
@@ -331,9 +347,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     constexpr int NR = 8 * NT;
     constexpr int KG = D / 64;  // groups of four 16-byte pieces of a row
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ Place found[C::WARPS + 1];
+    __shared__ Start start[C::WARPS];
     __shared__ int flag_of[C::WARPS];
-    __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR], close_f[C::WARPS][NR];
+    __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR];
+    __shared__ float close_f[C::WARPS][NR], inv_of[C::WARPS][NR];
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -343,10 +360,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     Work *const work_of = reinterpret_cast<Work *>(sm + C::OFF_WORK) + warp * C::WORKS;
     const uint64_t policy = l2_policy_evict_first();
 
-    const long long share = scan_line<C::WARPS>(p, NR, reinterpret_cast<long long *>(sm + C::OFF_SUMS), found);
-    Place ahead = found[warp];
-    const long long end = found[warp + 1].pos;
-    const bool busy = ahead.pos < end;
+    const int share = scan_line<C::WARPS>(p, NR, reinterpret_cast<int *>(sm + C::OFF_SUMS), start, reinterpret_cast<Work *>(sm + C::OFF_WORK), C::WORKS);
+    Place ahead = start[warp].ahead;
+    const int end = start[warp].end;
+    const bool busy = ahead.entry >= 0;
     if (lane == 0) {
         if (warp == 0) tail_of(p.ws, blockIdx.x)->parts = 0;
         flag_of[warp] = 0;
@@ -354,39 +371,39 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 
     // ---- pages: up to 16 tiles (32 halves) of one item looked up at a time, a half a
     // lane, one such batch ahead of the copies; the items go into a ring for the loop below
-    Work next;              // the item being looked up
-    int t_next = 0, works = 0;
-    next.t1 = 0;
+    Work next = work_of[0];  // the item being looked up
+    if (!busy) next.t0 = next.t1 = 0;
+    int t_next = next.t0, works = 1;
     int ph_next, key_next, nv_next, n_next;  // page * Hkv + head (-1: outside the cache), first key, keys there
     auto look_up = [&]() {
         n_next = 0;
         ph_next = 0, key_next = kPgMaxLen, nv_next = 0;
         if (t_next == next.t1) {
-            if (ahead.pos >= end) return;
+            if (!busy || ahead.pos >= end) return;
             next = work_at(p, ahead, end, share, NR);
             t_next = next.t0;
             if (lane == 0) work_of[works & (C::WORKS - 1)] = next;
             ++works;
         }
         n_next = min(16, next.t1 - t_next);
-        const long long at = (long long)(t_next + (lane >> 1)) * kPgTile + (lane & 1) * 16;
+        const int at = (t_next + (lane >> 1)) * kPgTile + (lane & 1) * 16;
         t_next += n_next;
         if ((lane >> 1) >= n_next) return;
-        long long of = at >> p.page_log2;  // position in the block table
+        int of = at >> p.page_log2;  // position in the block table
         if (p.sel) {
             const long long bh = (long long)next.b * p.Hkv + next.h;
-            if (of >= min(p.sel_count[bh], p.sel_width)) return;
+            if ((uint32_t)of >= (uint32_t)max(0, min(p.sel_count[bh], p.sel_width))) return;
             of = p.sel[bh * p.sel_width + of];
-            const long long k = (of << p.page_log2) + (at & (page - 1));
             if (of < 0 || of >= (next.len + page - 1) >> p.page_log2) {
                 ph_next = -1, key_next = 0;
                 return;
             }
+            const int k = (of << p.page_log2) + (at & (page - 1));
             if (k >= next.len) return;
-            key_next = (int)k;
+            key_next = k;
         } else {
-            if (at >= next.len) return;
-            key_next = (int)at;
+            if ((uint32_t)at >= (uint32_t)next.len) return;
+            key_next = at;
         }
         const int pg = p.table[(long long)next.b * p.max_pages + of];
         const bool good = pg >= 0 && pg < p.num_pages;
@@ -482,10 +499,6 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 __syncwarp();
             }
             issue();  // into the stage that the tile before was read from
-            if (fill > 0) {
-                --fill;
-                continue;
-            }
             if (i == it.t1) {  // the next item
                 __syncwarp();
                 it = work_of[done & (C::WORKS - 1)];
@@ -543,6 +556,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[c][nt][j] = 0.f;
                 }
+            }
+            if (fill > 0) {
+                --fill;
+                continue;
             }
             const uint32_t st = stage_out * C::STAGE_BYTES;
             const float4 meta[2] = {meta_of[stage_out * 2], meta_of[stage_out * 2 + 1]};
@@ -692,118 +709,138 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
             }
 
             if (++i < it.t1) continue;
-            if (it.last) break;
-            // ---- an item that ends here, with others behind it: written out, or where it
-            // was begun before this warp, what is known of it
-            float *const part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + warp, 0, NR, D);
+
+            // ---- an item ends here, or the warp's share of it
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float y = l[nt][j];
-                    y += __shfl_xor_sync(0xffffffffu, y, 4);
-                    y += __shfl_xor_sync(0xffffffffu, y, 8);
-                    y += __shfl_xor_sync(0xffffffffu, y, 16);
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+                }
+            bool whole = it.t0 == 0;
+            float *part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + warp, 0, NR, D);
+            if (it.last) {
+                // Warps that had nothing else than more of the item of the warp before them
+                // form a group with it, and so does, if the item still goes on, what the next
+                // warp left of its first item in its slot 0.  (That warp had other items
+                // behind it, so the item ended there.)
+                float2 *const sums_of = reinterpret_cast<float2 *>(sm + warp * C::ST * C::STAGE_BYTES) + lane;  // over the ring
+                cp_wait<0>();
+                __syncwarp();
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (g == 0) {
+                            join_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
+                            join_l[warp][nt * 8 + 2 * t + j] = l[nt][j];
+                        }
+#pragma unroll
+                        for (int c = 0; c < C::CHUNKS; ++c)
+                            sums_of[((c * NT + nt) * 2 + j) * 32] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
+                    }
+                if (lane == 0)
+                    flag_of[warp] = (warp > 0 && done == 1 && it.t0 > 0 ? 1 : 0) | (it.t1 < it.tiles ? 2 : 0) | (it.t0 == 0 ? 4 : 0) | 8;
+                named_bar_sync(1, C::THREADS);
+                int lead = warp, last = warp;
+                while (lead > 0 && (flag_of[lead] & 1)) --lead;
+                while (last + 1 < C::WARPS && (flag_of[last + 1] & 1)) ++last;
+                bool open = flag_of[last] & 2;
+                const bool begins = flag_of[lead] & 4;
+                const bool closes = open && last + 1 < C::WARPS && (flag_of[last + 1] & 8);
+                const float *const closing = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + min(last + 1, C::WARPS - 1), 0, NR, D);
+                if (closes) open = false;
+                whole = begins && !open;
+                part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + lead, begins ? 1 : 0, NR, D);
+                if (begins && open && warp == lead && lane == 0)
+                    *tail_of(p.ws, blockIdx.x) = Tail{it.end_block - (int)blockIdx.x + 1, lead, it.b, it.h, it.row0, {0, 0, 0}};
+                if (lead != last || closes) {
+                    if (lane < NR) {  // a row's maximum over the group, and the factors of its parts to it
+                        float M = closes ? closing[NR * D + lane] : kPgNone, L = 0.f, f = 0.f;
+#pragma unroll 1
+                        for (int w = lead; w <= last; ++w) M = fmaxf(M, join_m[w][lane]);
+                        if (closes) {
+                            f = ex2_approx(closing[NR * D + lane] - M);
+                            L = closing[NR * D + NR + lane] * f;
+                        }
+                        close_f[warp][lane] = f;
+#pragma unroll 1
+                        for (int w = lead; w <= last; ++w) L = fmaf(join_l[w][lane], ex2_approx(join_m[w][lane] - M), L);
+                        join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
+                        inv_of[warp][lane] = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+                        if (warp == lead) {
+                            if (!whole)
+                                part[NR * D + lane] = M, part[NR * D + NR + lane] = L;
+                            else if (it.row0 + lane < it.rows)
+                                p.lse[out_row(p, it.q0, it.h, it.row0 + lane)] = lse_of(M, L);
+                        }
+                    }
+                    named_bar_sync(1, C::THREADS);
+                    long long at[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = nt * 8 + 2 * t + j;
+                            at[nt][j] = it.row0 + r < it.rows ? out_row(p, it.q0, it.h, it.row0 + r) : -1;
+                        }
+#pragma unroll 1
+                    for (int c = warp - lead; c < C::CHUNKS; c += last - lead + 1) {  // the group's warps share the sums
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int r = nt * 8 + 2 * t + j;
+                                float2 o = make_float2(0.f, 0.f);
+                                if (closes) {
+                                    o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + g];
+                                    o.x *= close_f[warp][r], o.y *= close_f[warp][r];
+                                }
+#pragma unroll 1
+                                for (int w = lead; w <= last; ++w) {
+                                    const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[((c * NT + nt) * 2 + j) * 32 + lane];
+                                    o.x = fmaf(x.x, join_f[w][r], o.x), o.y = fmaf(x.y, join_f[w][r], o.y);
+                                }
+                                const float inv = inv_of[warp][r];
+                                if (!whole)
+                                    reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
+                                else if (at[nt][j] >= 0)
+                                    reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at[nt][j] * D)[8 * c + g] =
+                                        pack_bf16x2(o.x * inv, o.y * inv);
+                            }
+                    }
+                    return;
+                }
+                named_bar_sync(1, C::THREADS);
+            }
+            // ---- written out, or what is known of it
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
                     const int r = nt * 8 + 2 * t + j;
-                    if (it.t0 > 0) {
+                    if (!whole) {
                         float2 *const o = reinterpret_cast<float2 *>(part + r * D) + g;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
-                        if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = y;
+                        if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = l[nt][j];
                     } else if (it.row0 + r < it.rows) {
-                        const float inv = y == 0.f ? 0.f : 1.f / y;
+                        const float inv = l[nt][j] == 0.f ? 0.f : 1.f / l[nt][j];
                         const long long at = out_row(p, it.q0, it.h, it.row0 + r);
                         uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + g;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
-                        if (g == 0) p.lse[at] = lse_of(m[nt][j], y);
+                        if (g == 0) p.lse[at] = lse_of(m[nt][j], l[nt][j]);
                     }
                 }
+            if (it.last) return;
         }
     }
-
-    // ---- the warps' last items.  Warps that had nothing else than more of the item of
-    // the warp before them form a group with it, and so does, if the item still goes
-    // on, what the next warp left of its first item in its slot 0.  (That warp had
-    // other items behind it, so the item ended there.)
-    float2 *const sums_of = reinterpret_cast<float2 *>(sm + warp * C::ST * C::STAGE_BYTES) + lane;  // over the ring
-    if (busy) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float y = l[nt][j];
-                y += __shfl_xor_sync(0xffffffffu, y, 4);
-                y += __shfl_xor_sync(0xffffffffu, y, 8);
-                y += __shfl_xor_sync(0xffffffffu, y, 16);
-                if (g == 0) {
-                    join_m[warp][nt * 8 + 2 * t + j] = m[nt][j];
-                    join_l[warp][nt * 8 + 2 * t + j] = y;
-                }
-            }
-        cp_wait<0>();
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    sums_of[((c * NT + nt) * 2 + j) * 32] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
-        if (lane == 0)
-            flag_of[warp] = (warp > 0 && done == 1 && it.t0 > 0 ? 1 : 0) | (it.t1 < it.tiles ? 2 : 0) | (it.t0 == 0 ? 4 : 0) | 8;
-    }
-    __syncthreads();
-    int lead = warp, last = warp;
-    while (lead > 0 && (flag_of[lead] & 1)) --lead;
-    while (last + 1 < C::WARPS && (flag_of[last + 1] & 1)) ++last;
-    bool open = flag_of[last] & 2;
-    const bool begins = flag_of[lead] & 4;
-    const bool closes = open && last + 1 < C::WARPS && (flag_of[last + 1] & 8);
-    const float *const closing = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + min(last + 1, C::WARPS - 1), 0, NR, D);
-    if (closes) open = false;
-    // every row's maximum over the group, and the factors of its parts to it
-    if (busy && lane < NR) {
-        float M = closes ? closing[NR * D + lane] : kPgNone;
-        for (int w = lead; w <= last; ++w) M = fmaxf(M, join_m[w][lane]);
-        join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
-        close_f[warp][lane] = closes ? ex2_approx(closing[NR * D + lane] - M) : 0.f;
-    }
-    __syncthreads();
-    if (!busy) return;
-    const bool whole = begins && !open;
-    float *const part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + lead, begins ? 1 : 0, NR, D);
-#pragma unroll 1
-    for (int u = warp - lead; u < C::UNITS; u += last - lead + 1) {  // a group's warps share the sums
-        const int c = u / (2 * NT), r = (u / 2 % NT) * 8 + 2 * t + (u & 1);
-        float2 o = make_float2(0.f, 0.f);
-        float y = 0.f, M = kPgNone;
-        if (closes) {
-            const float f = close_f[warp][r];
-            o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + g];
-            o.x *= f, o.y *= f;
-            y = closing[NR * D + NR + r] * f;
-            M = closing[NR * D + r];
-        }
-        for (int w = lead; w <= last; ++w) {
-            const float f = join_f[w][r];
-            const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[u * 32 + lane];
-            o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y);
-            y = fmaf(join_l[w][r], f, y);
-            M = fmaxf(M, join_m[w][r]);
-        }
-        if (!whole) {
-            reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
-            if (c == 0 && g == 0) part[NR * D + r] = M, part[NR * D + NR + r] = y;
-        } else if (it.row0 + r < it.rows) {
-            const float inv = y == 0.f ? 0.f : 1.f / y;
-            const long long at = out_row(p, it.q0, it.h, it.row0 + r);
-            reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D)[8 * c + g] = pack_bf16x2(o.x * inv, o.y * inv);
-            if (c == 0 && g == 0) p.lse[at] = lse_of(M, y);
-        }
-    }
-    if (begins && open && warp == lead && lane == 0)
-        *tail_of(p.ws, blockIdx.x) = Tail{it.end_block - (int)blockIdx.x + 1, lead, it.b, it.h, it.row0, {0, 0, 0}};
+    // a warp without tiles: the others wait for it
+    named_bar_sync(1, C::THREADS);
+    named_bar_sync(1, C::THREADS);
 }
 
 // Joins the partial results of the items that cross blocks: each block of this kernel
@@ -949,11 +986,22 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p);
 }
 
-cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream) {
-    // Rows of an item: 8 while a sequence's query rows are no more (by the mean
-    // number of its tokens, padding rounded off), 16 beyond.
+// Rows of an item: 8 while a sequence's query rows are no more (by the mean
+// number of its tokens, padding rounded off), 16 beyond.
+static bool wide_items(const PagedParams &p) {
     const long long tokens = (2ll * p.T + p.B) / (2ll * p.B);
-    const bool wide = (tokens > 1 ? tokens : 1) * p.G > 8;
+    return (tokens > 1 ? tokens : 1) * p.G > 8;
+}
+
+bool paged_fits(const PagedParams &p) {
+    const long long keys = (long long)(p.sel_width > p.max_pages ? p.sel_width : p.max_pages) << p.page_log2;
+    const long long items = ((long long)p.T * p.G / (wide_items(p) ? 16 : 8) + p.B) * p.Hkv;
+    const long long places = keys / kPgTile + 1 + kPgFixed;
+    return keys <= 0x7fffffff && items < (1ll << 31) && items * places < (1ll << 31) - (1 << 20);
+}
+
+cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream) {
+    const bool wide = wide_items(p);
     if (D == 64) return wide ? launch_paged<64, 2>(p, num_sms, stream) : launch_paged<64, 1>(p, num_sms, stream);
     return wide ? launch_paged<128, 2>(p, num_sms, stream) : launch_paged<128, 1>(p, num_sms, stream);
 }
