@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR];
     __shared__ float close_f[C::WARPS][NR], inv_of[C::WARPS][NR];
     grid_launch_dependents();
+    grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int page = 1 << p.page_log2;
@@ -361,9 +362,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     const uint64_t policy = l2_policy_evict_first();
 
     const int share = scan_line<C::WARPS>(p, NR, reinterpret_cast<int *>(sm + C::OFF_SUMS), start, reinterpret_cast<Work *>(sm + C::OFF_WORK), C::WORKS);
-    Place ahead = start[warp].ahead;
-    const int end = start[warp].end;
-    const bool busy = ahead.entry >= 0;
+    const bool busy = start[warp].ahead.entry >= 0;
     if (lane == 0) {
         if (warp == 0) tail_of(p.ws, blockIdx.x)->parts = 0;
         flag_of[warp] = 0;
@@ -371,44 +370,52 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 
     // ---- pages: up to 16 tiles (32 halves) of one item looked up at a time, a half a
     // lane, one such batch ahead of the copies; the items go into a ring for the loop below
-    Work next = work_of[0];  // the item being looked up
-    if (!busy) next.t0 = next.t1 = 0;
-    int t_next = next.t0, works = 1;
+    // (What is used once an item stays in shared memory: the loop needs the registers.)
+    const Work *next = work_of;  // the item being looked up
+    int t_next = busy ? next->t0 : 0, works = 1;
     int ph_next, key_next, nv_next, n_next;  // page * Hkv + head (-1: outside the cache), first key, keys there
     auto look_up = [&]() {
         n_next = 0;
         ph_next = 0, key_next = kPgMaxLen, nv_next = 0;
-        if (t_next == next.t1) {
-            if (!busy || ahead.pos >= end) return;
-            next = work_at(p, ahead, end, share, NR);
-            t_next = next.t0;
-            if (lane == 0) work_of[works & (C::WORKS - 1)] = next;
+        if (!busy) return;
+        if (t_next == next->t1) {
+            if (next->last) return;
+            next = work_of + (works & (C::WORKS - 1));
             ++works;
+            Place ahead = start[warp].ahead;
+            const Work made = work_at(p, ahead, start[warp].end, share, NR);
+            __syncwarp();
+            if (lane == 0) {
+                start[warp].ahead = ahead;
+                *const_cast<Work *>(next) = made;
+            }
+            __syncwarp();
+            t_next = next->t0;
         }
-        n_next = min(16, next.t1 - t_next);
+        n_next = min(16, next->t1 - t_next);
         const int at = (t_next + (lane >> 1)) * kPgTile + (lane & 1) * 16;
         t_next += n_next;
         if ((lane >> 1) >= n_next) return;
         int of = at >> p.page_log2;  // position in the block table
         if (p.sel) {
-            const long long bh = (long long)next.b * p.Hkv + next.h;
+            const long long bh = (long long)next->b * p.Hkv + next->h;
             if ((uint32_t)of >= (uint32_t)max(0, min(p.sel_count[bh], p.sel_width))) return;
             of = p.sel[bh * p.sel_width + of];
-            if (of < 0 || of >= (next.len + page - 1) >> p.page_log2) {
+            if (of < 0 || of >= (next->len + page - 1) >> p.page_log2) {
                 ph_next = -1, key_next = 0;
                 return;
             }
             const int k = (of << p.page_log2) + (at & (page - 1));
-            if (k >= next.len) return;
+            if (k >= next->len) return;
             key_next = k;
         } else {
-            if ((uint32_t)at >= (uint32_t)next.len) return;
+            if ((uint32_t)at >= (uint32_t)next->len) return;
             key_next = at;
         }
-        const int pg = p.table[(long long)next.b * p.max_pages + of];
+        const int pg = p.table[(long long)next->b * p.max_pages + of];
         const bool good = pg >= 0 && pg < p.num_pages;
-        ph_next = good ? pg * p.Hkv + next.h : -1;
-        nv_next = good ? min(16, next.len - key_next) : 0;
+        ph_next = good ? pg * p.Hkv + next->h : -1;
+        nv_next = good ? min(16, next->len - key_next) : 0;
     };
     look_up();
     // The batch being copied: each lane's half as a row of the cache, and what its
@@ -484,9 +491,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     int stage_out = 0;
 
     // ---- the warp's tiles, item after item
-    Work it;
+    const Work *it = work_of;
     int i = 0, done = 0, fill = C::ST - 1;
-    it.t1 = 0;
+    int t1 = 0;  // where the item's tiles end
     uint32_t qf[NT][KG][4][2];  // fragments of Q^T (lane: row g of each tile of 8)
     float fac[NT][2];           // c 2^e of the rows 2t, 2t+1, which this lane holds in accumulators
     int lim[NT][2], lim_min = 0;  // the first key that they do not see, and the least of them
@@ -499,14 +506,14 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 __syncwarp();
             }
             issue();  // into the stage that the tile before was read from
-            if (i == it.t1) {  // the next item
+            if (i == t1) {  // the next item
                 __syncwarp();
-                it = work_of[done & (C::WORKS - 1)];
+                it = work_of + (done & (C::WORKS - 1));
                 ++done;
-                i = it.t0;
+                i = it->t0, t1 = it->t1;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int row = it.row0 + nt * 8 + g;
+                const int row = it->row0 + nt * 8 + g;
                 uint4 w[KG][2];
                 uint32_t am = 0;
 #pragma unroll
@@ -514,10 +521,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         w[i][j] = make_uint4(0, 0, 0, 0);
-                        if (row < it.rows) {
+                        if (row < it->rows) {
                             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                                     (long long)(it.q0 + row / p.G) * p.q_stride +
-                                                     (long long)(it.h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
+                                                     (long long)(it->q0 + row / p.G) * p.q_stride +
+                                                     (long long)(it->h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
                             w[i][j] = __ldg(reinterpret_cast<const uint4 *>(q));
                         }
                         const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
@@ -541,11 +548,11 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     fac[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-                    const int r = it.row0 + nt * 8 + 2 * t + j;
-                    lim[nt][j] = r < it.rows ? it.len - it.nq + r / p.G + 1 : it.len;
+                    const int r = it->row0 + nt * 8 + 2 * t + j;
+                    lim[nt][j] = r < it->rows ? it->len - it->nq + r / p.G + 1 : it->len;
                 }
             }
-            lim_min = it.len - it.nq + it.row0 / p.G + 1;
+            lim_min = it->len - it->nq + it->row0 / p.G + 1;
 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -682,22 +689,22 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         for (int j = 0; j < 4; ++j) acc[c][nt][j] = settle(acc[c][nt][j], was[nt][j], nt, j & 1);
                 }
             };
-            if (!edge || lim_min >= it.len) {
+            if (!edge || lim_min >= it->len) {
                 accumulate([](uint32_t r, int, int) { return r; }, [](float now, float, int, int) { return now; });
             } else {
                 // Some rows do not see all of these keys: a weight of 0 would still turn a
                 // NaN among the values into NaN, so the values that a token does not see
                 // are cleared, a token at a time, and only that token's rows take the
                 // result (only the last tiles of a sequence come here).
-                const int tok0 = it.row0 / p.G, tok1 = min(it.nq - 1, (it.row0 + NR - 1) / p.G);
+                const int tok0 = it->row0 / p.G, tok1 = min(it->nq - 1, (it->row0 + NR - 1) / p.G);
 #pragma unroll 1
                 for (int tok = tok0; tok <= tok1; ++tok) {
-                    const int limit = it.len - it.nq + tok + 1;
+                    const int limit = it->len - it->nq + tok + 1;
                     bool my[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) my[nt][j] = (it.row0 + nt * 8 + 2 * t + j) / p.G == tok;
+                        for (int j = 0; j < 2; ++j) my[nt][j] = (it->row0 + nt * 8 + 2 * t + j) / p.G == tok;
                     accumulate(
                         [&](uint32_t r, int half, int up) {
                             const int k = key[half] + up * 8;
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 }
             }
 
-            if (++i < it.t1) continue;
+            if (++i < t1) continue;
 
             // ---- an item ends here, or the warp's share of it
 #pragma unroll
@@ -719,9 +726,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                     l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
                     l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
                 }
-            bool whole = it.t0 == 0;
+            bool whole = it->t0 == 0;
             float *part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + warp, 0, NR, D);
-            if (it.last) {
+            if (it->last) {
                 // Warps that had nothing else than more of the item of the warp before them
                 // form a group with it, and so does, if the item still goes on, what the next
                 // warp left of its first item in its slot 0.  (That warp had other items
@@ -742,7 +749,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                             sums_of[((c * NT + nt) * 2 + j) * 32] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
                     }
                 if (lane == 0)
-                    flag_of[warp] = (warp > 0 && done == 1 && it.t0 > 0 ? 1 : 0) | (it.t1 < it.tiles ? 2 : 0) | (it.t0 == 0 ? 4 : 0) | 8;
+                    flag_of[warp] = (warp > 0 && done == 1 && it->t0 > 0 ? 1 : 0) | (it->t1 < it->tiles ? 2 : 0) | (it->t0 == 0 ? 4 : 0) | 8;
                 named_bar_sync(1, C::THREADS);
                 int lead = warp, last = warp;
                 while (lead > 0 && (flag_of[lead] & 1)) --lead;
@@ -755,7 +762,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 whole = begins && !open;
                 part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + lead, begins ? 1 : 0, NR, D);
                 if (begins && open && warp == lead && lane == 0)
-                    *tail_of(p.ws, blockIdx.x) = Tail{it.end_block - (int)blockIdx.x + 1, lead, it.b, it.h, it.row0, {0, 0, 0}};
+                    *tail_of(p.ws, blockIdx.x) = Tail{it->end_block - (int)blockIdx.x + 1, lead, it->b, it->h, it->row0, {0, 0, 0}};
                 if (lead != last || closes) {
                     if (lane < NR) {  // a row's maximum over the group, and the factors of its parts to it
                         float M = closes ? closing[NR * D + lane] : kPgNone, L = 0.f, f = 0.f;
@@ -773,8 +780,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         if (warp == lead) {
                             if (!whole)
                                 part[NR * D + lane] = M, part[NR * D + NR + lane] = L;
-                            else if (it.row0 + lane < it.rows)
-                                p.lse[out_row(p, it.q0, it.h, it.row0 + lane)] = lse_of(M, L);
+                            else if (it->row0 + lane < it->rows)
+                                p.lse[out_row(p, it->q0, it->h, it->row0 + lane)] = lse_of(M, L);
                         }
                     }
                     named_bar_sync(1, C::THREADS);
@@ -784,7 +791,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const int r = nt * 8 + 2 * t + j;
-                            at[nt][j] = it.row0 + r < it.rows ? out_row(p, it.q0, it.h, it.row0 + r) : -1;
+                            at[nt][j] = it->row0 + r < it->rows ? out_row(p, it->q0, it->h, it->row0 + r) : -1;
                         }
 #pragma unroll 1
                     for (int c = warp - lead; c < C::CHUNKS; c += last - lead + 1) {  // the group's warps share the sums
@@ -826,16 +833,16 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
                         if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = l[nt][j];
-                    } else if (it.row0 + r < it.rows) {
+                    } else if (it->row0 + r < it->rows) {
                         const float inv = l[nt][j] == 0.f ? 0.f : 1.f / l[nt][j];
-                        const long long at = out_row(p, it.q0, it.h, it.row0 + r);
+                        const long long at = out_row(p, it->q0, it->h, it->row0 + r);
                         uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + g;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
                         if (g == 0) p.lse[at] = lse_of(m[nt][j], l[nt][j]);
                     }
                 }
-            if (it.last) return;
+            if (it->last) return;
         }
     }
     // a warp without tiles: the others wait for it
@@ -926,6 +933,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
     __shared__ float red_m[kJoinWarps], red_l[kJoinWarps], red_o[kJoinWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x, blocks = gridDim.x;
     JoinRow<D, NR> row_of;
+    grid_launch_dependents();
     grid_wait();
     const Tail tail = *tail_of(p.ws, block);
     if (tail.parts == 0) return;
@@ -970,19 +978,22 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     using C = PgCfg<D, NT>;
     cudaError_t e = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    fa_fwd_paged_kernel<D, NT><<<num_sms, C::THREADS, C::SMEM, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // the join is launched while the first kernel still runs, and waits for its end
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms, 8 * NT / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.stream = stream;
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    e = cudaLaunchKernelEx(&cfg, fa_fwd_paged_kernel<D, NT>, p);
+    if (e != cudaSuccess) return e;
+    // the join is launched while the first kernel still runs, and waits for its end
+    cfg.gridDim = dim3(num_sms, 8 * NT / kJoinWarps);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p);
 }
 
