@@ -43,6 +43,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/fa.h"
 #include "fa_paged.h"
 #include "sm103_ptx.cuh"
@@ -97,30 +99,30 @@ __device__ __forceinline__ Seq sequence(const PagedParams &p, int b) {
     Seq s;
     s.q0 = max(0, min(p.cu_q[b], p.T));
     s.nq = max(s.q0, min(p.cu_q[b + 1], p.T)) - s.q0;
-    const long long most = min((long long)p.max_pages << p.page_log2, (long long)kPgMaxLen);
-    s.len = (int)max(0ll, min((long long)p.seq_lens[b], most));
+    s.len = max(0, min(p.seq_lens[b], p.max_len));
     return s;
 }
 
 // Tiles of one item of (b, h), at least one: an item without keys still writes its rows.
 __device__ __forceinline__ int item_tiles(const PagedParams &p, int b, int h, int len) {
-    long long keys = len;
-    if (p.sel) keys = (long long)max(0, min(p.sel_count[(long long)b * p.Hkv + h], p.sel_width)) << p.page_log2;
-    return max(1, (int)((keys + kPgTile - 1) / kPgTile));
+    int keys = len;
+    if (p.sel) keys = max(0, min(p.sel_count[(long long)b * p.Hkv + h], p.sel_width)) << p.page_log2;
+    return max(1, (int)((uint32_t)(keys + kPgTile - 1) / kPgTile));
 }
 
-__device__ __forceinline__ int entry_weight(const PagedParams &p, int e, int nr) {
+template <int NR>
+__device__ __forceinline__ int entry_weight(const PagedParams &p, int e) {
     const int b = p.sel ? e / p.Hkv : e, h = p.sel ? e % p.Hkv : 0;
     const Seq s = sequence(p, b);
-    const int rt = (s.nq * p.G + nr - 1) / nr;
+    const int rt = (uint32_t)(s.nq * p.G + NR - 1) / NR;
     return rt * (p.sel ? 1 : p.Hkv) * (kPgFixed + item_tiles(p, b, h, s.len));
 }
 
 // The place of `pos`, from the sums up to the end of each thread's entries.  Where it
 // falls into an item's fixed places, or into an item of at most `small` places, it is
 // moved to the item's beginning or its nearer end.
-__device__ __forceinline__ Place place_of(const PagedParams &p, const int *sums, int threads, int per, int n, int nr, int pos,
-                                          int small) {
+template <int NR>
+__device__ __forceinline__ Place place_of(const PagedParams &p, const int *sums, int threads, int per, int n, int pos, int small) {
     int lo = 0, hi = threads - 1;  // the first thread whose sum is above pos
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -132,7 +134,7 @@ __device__ __forceinline__ Place place_of(const PagedParams &p, const int *sums,
     Place f{min(lo * per, n - 1), lo ? sums[lo - 1] : 0, pos};
 #pragma unroll 1
     for (const int e1 = min(n, f.entry + per); f.entry < e1 - 1; ++f.entry) {
-        const int w = entry_weight(p, f.entry, nr);
+        const int w = entry_weight<NR>(p, f.entry);
         if (pos < f.base + w) break;
         f.base += w;
     }
@@ -151,7 +153,7 @@ struct Work {
     int b, h, row0, rows;     // its first query row, and how many the sequence has for this head
     int tiles, t0, t1;        // tiles of the item, and this warp's of them
     int last;                 // whether the warp's share ends with it
-    int end_block;            // the block that has the item's last tile
+    int end;                  // the place behind its last tile
 };
 static_assert(sizeof(Work) == 48, "");
 
@@ -159,13 +161,14 @@ static_assert(sizeof(Work) == 48, "");
 // this is kept out of line, so that the loop over tiles stays within the instruction
 // cache: with all of it inlined, in 64 bits, the kernel was 192 KB long and spent 25 us on
 // fetching itself.)
-__device__ __noinline__ Work work_at(const PagedParams &p, Place &place, int end, int share, int nr) {
+template <int NR>
+__device__ __noinline__ Work work_at(const PagedParams &p, Place &place, int end) {
     // The scan's lengths and these are the same unless the caller changes them during
     // the call; the bounds on entry, head and block keep every access inside even then.
     const int n = p.sel ? p.B * p.Hkv : p.B;
 #pragma unroll 1
     for (; place.entry < n - 1; ++place.entry) {
-        const int w = entry_weight(p, place.entry, nr);
+        const int w = entry_weight<NR>(p, place.entry);
         if (place.pos < place.base + w) break;
         place.base += w;
     }
@@ -180,15 +183,18 @@ __device__ __noinline__ Work work_at(const PagedParams &p, Place &place, int end
     int rt = (int)((uint32_t)(place.pos - place.base) / (uint32_t)w);
     const int first = place.base + rt * w;
     if (!p.sel) {
-        const int rts = max(1, (it.rows + nr - 1) / nr);
-        it.h = min(rt / rts, p.Hkv - 1), rt = rt % rts;
+        const int rts = (uint32_t)(it.rows + NR - 1) / NR;
+        it.h = rt;
+        if (rts > 1) it.h = rt / rts, rt %= rts;
+        else rt = 0;
+        it.h = min(it.h, p.Hkv - 1);
     }
-    it.row0 = rt * nr;
+    it.row0 = rt * NR;
     it.t0 = max(0, place.pos - first - kPgFixed);
     it.t1 = max(it.t0 + 1, min(it.tiles, end - first - kPgFixed));
     place.pos = first + kPgFixed + it.t1;
     it.last = place.pos >= end;
-    it.end_block = min((first + w - 1) / share, (int)gridDim.x - 1);
+    it.end = first + w;
     return it;
 }
 
@@ -199,8 +205,8 @@ struct Start {
 };
 
 // Scans the line and starts every warp of the block.  Returns the share of a block.
-template <int WARPS>
-__device__ __forceinline__ int scan_line(const PagedParams &p, int nr, int *sums, Start *start, Work *work_of, int works) {
+template <int WARPS, int NR>
+__device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start *start, Work *work_of, int works) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int THREADS = 32 * WARPS;
     __shared__ int share_sm;
@@ -208,7 +214,7 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int nr, int *sums
     const int per = (n + THREADS - 1) / THREADS;
     long long x = 0;
 #pragma unroll 4
-    for (int e = min(n, tid * per); e < min(n, tid * per + per); ++e) x += entry_weight(p, e, nr);
+    for (int e = min(n, tid * per); e < min(n, tid * per + per); ++e) x += entry_weight<NR>(p, e);
     sums[tid] = (int)min(x, 0x7fffffffll);
     __syncthreads();
     if (warp == 0) {  // a lane takes WARPS threads' sums, then a boundary between warps, then a warp's first item
@@ -241,17 +247,17 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int nr, int *sums
         // the block's ends, then the warps'
         Place f{0, 0, total};
         const long long cut = (long long)(blockIdx.x + (lane == WARPS)) * share;
-        if (cut < total) f = place_of(p, sums, THREADS, per, n, nr, (int)cut, small);
+        if (cut < total) f = place_of<NR>(p, sums, THREADS, per, n, (int)cut, small);
         const int begin = __shfl_sync(0xffffffffu, f.pos, 0), end = __shfl_sync(0xffffffffu, f.pos, WARPS);
         const int part = (end - begin + WARPS - 1) / WARPS, pos = begin + lane * part;
         if (lane > 0 && lane < WARPS) {
             f.pos = end;
-            if (pos < end) f = place_of(p, sums, THREADS, per, n, nr, pos, part / 2);
+            if (pos < end) f = place_of<NR>(p, sums, THREADS, per, n, pos, part / 2);
         }
         Start st{f, __shfl_down_sync(0xffffffffu, f.pos, 1)};
         if (lane < WARPS) {
             if (f.pos < st.end)
-                work_of[lane * works] = work_at(p, st.ahead, st.end, share, nr);
+                work_of[lane * works] = work_at<NR>(p, st.ahead, st.end);
             else
                 st.ahead.entry = -1;
             start[lane] = st;
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     Work *const work_of = reinterpret_cast<Work *>(sm + C::OFF_WORK) + warp * C::WORKS;
     const uint64_t policy = l2_policy_evict_first();
 
-    const int share = scan_line<C::WARPS>(p, NR, reinterpret_cast<int *>(sm + C::OFF_SUMS), start, reinterpret_cast<Work *>(sm + C::OFF_WORK), C::WORKS);
+    const int share = scan_line<C::WARPS, NR>(p, reinterpret_cast<int *>(sm + C::OFF_SUMS), start, reinterpret_cast<Work *>(sm + C::OFF_WORK), C::WORKS);
     const bool busy = start[warp].ahead.entry >= 0;
     if (lane == 0) {
         if (warp == 0) tail_of(p.ws, blockIdx.x)->parts = 0;
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
             next = work_of + (works & (C::WORKS - 1));
             ++works;
             Place ahead = start[warp].ahead;
-            const Work made = work_at(p, ahead, start[warp].end, share, NR);
+            const Work made = work_at<NR>(p, ahead, start[warp].end);
             __syncwarp();
             if (lane == 0) {
                 start[warp].ahead = ahead;
@@ -762,7 +768,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 whole = begins && !open;
                 part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + lead, begins ? 1 : 0, NR, D);
                 if (begins && open && warp == lead && lane == 0)
-                    *tail_of(p.ws, blockIdx.x) = Tail{it->end_block - (int)blockIdx.x + 1, lead, it->b, it->h, it->row0, {0, 0, 0}};
+                    *tail_of(p.ws, blockIdx.x) = Tail{min((it->end - 1) / share, (int)gridDim.x - 1) - (int)blockIdx.x + 1, lead, it->b, it->h, it->row0, {0, 0, 0}};
                 if (lead != last || closes) {
                     if (lane < NR) {  // a row's maximum over the group, and the factors of its parts to it
                         float M = closes ? closing[NR * D + lane] : kPgNone, L = 0.f, f = 0.f;
@@ -1011,7 +1017,9 @@ bool paged_fits(const PagedParams &p) {
     return keys <= 0x7fffffff && items < (1ll << 31) && items * places < (1ll << 31) - (1 << 20);
 }
 
-cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_fwd_paged(int D, const PagedParams &params, int num_sms, cudaStream_t stream) {
+    PagedParams p = params;
+    p.max_len = (int)std::min<long long>((long long)p.max_pages << p.page_log2, kPgMaxLen);
     const bool wide = wide_items(p);
     if (D == 64) return wide ? launch_paged<64, 2>(p, num_sms, stream) : launch_paged<64, 1>(p, num_sms, stream);
     return wide ? launch_paged<128, 2>(p, num_sms, stream) : launch_paged<128, 1>(p, num_sms, stream);

@@ -52,6 +52,7 @@ struct PagedParams {
     float *lse;                  // fp32 [T, Hq]
     float *ws;
     int B, T, G, Hkv, max_pages, num_pages, page_log2, sel_width;
+    int max_len;                 // tokens that a table row holds (set by the launch)
     float scale_log2;            // scale * log2(e)
 };
 // Whether the work of these sizes, at most, can be laid out in 32-bit places.
