@@ -392,55 +392,54 @@ def fa_fwd_paged_raw(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_pages_ptr, v_pages_
 
 
 def fa_fwd_paged_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace that fa_fwd_paged needs for these sizes on the current device."""
     return lib().fa_fwd_paged_workspace_bytes(B, T, Hq, Hkv, D)
 
 
-def _check(name, t, dtypes, shape, device, strided=False):
-    """t is a CUDA tensor on `device` of one of `dtypes` and of `shape` (None: any size), contiguous
-    (strided: in all but its first dimension)."""
-    if t.dtype not in dtypes or t.device != device or t.dim() != len(shape):
-        raise ValueError(f"{name} must be a {len(shape)}-dimensional {' or '.join(map(str, dtypes))} tensor on {device}")
-    for n, m in zip(t.shape, shape):
-        if m is not None and n != m:
-            raise ValueError(f"{name} must have the shape {tuple('*' if m is None else m for m in shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous() and not (strided and t.shape[0] > 0 and t[0].is_contiguous()):
-        raise ValueError(f"{name} must be contiguous" + (" but for the stride of its first dimension" if strided else ""))
+_binding_module = None
 
 
-def _token_stride(t) -> int:
-    """Elements between tokens of a [T, H, D] tensor (one token: its own size)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _binding():
+    """The extension module that makes the paged cache's calls on tensors."""
+    global _binding_module
+    if _binding_module is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries, which the module links, are loaded)
+
+        lib()
+        with _lock:
+            if _binding_module is None:
+                loader = importlib.machinery.ExtensionFileLoader("fa_binding", _build.BINDING_PATH)
+                module = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_binding", loader))
+                loader.exec_module(module)
+                _binding_module = module
+    return _binding_module
 
 
-class _Launch:
-    """A call's device and stream: the device of its tensors is made the current one,
-    and what the call allocates belongs to the stream that it is launched on."""
+def _stream_of(stream, device):
+    """A stream argument as the extension takes it: None (torch's current one) or an address."""
+    if stream is None or isinstance(stream, int):
+        return stream
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream
 
-    def __init__(self, device, stream):
-        import torch
 
-        if device.type != "cuda":
-            raise ValueError("the tensors must be CUDA tensors")
-        self._ctx = []
-        if torch.cuda.current_device() != device.index:
-            self._ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self._ctx.append(torch.cuda.stream(stream))
-        self._device = device
-        self._torch = torch
+def _allocating(device, stream):
+    """A context in which new tensors belong to the stream that the call is launched on."""
+    import contextlib
 
-    def __enter__(self):
-        for c in self._ctx:
-            c.__enter__()
-        return self._torch.cuda.current_stream(self._device).cuda_stream
+    import torch
 
-    def __exit__(self, *exc):
-        for c in reversed(self._ctx):
-            c.__exit__(*exc)
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def fa_kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_pages: int, page_size: int, cu_q=None,
@@ -452,42 +451,22 @@ def fa_kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_p
     new pages are added.  slot_map (int32 [T]) or num_tokens says how many tokens there are room for.
     Returns (cu_q [B+1], seq_lens [B], slot_map [T], free_left [1]), all int32, without synchronising;
     a request that is not served gets seq_lens 0 and slots of -1."""
-    import torch
+    if cu_q is None or seq_lens is None or slot_map is None or free_left is None:
+        import torch
 
-    dev, i32 = cached_lens.device, (torch.int32,)
-    with _Launch(dev, stream) as st:
-        B = cached_lens.shape[0]
-        if slot_map is None:
-            if num_tokens is None:
-                raise ValueError("give slot_map or num_tokens")
-            slot_map = torch.empty(num_tokens, dtype=torch.int32, device=dev)
-        T = slot_map.shape[0]
-        cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev) if cu_q is None else cu_q
-        seq_lens = torch.empty(B, dtype=torch.int32, device=dev) if seq_lens is None else seq_lens
-        free_left = torch.empty(1, dtype=torch.int32, device=dev) if free_left is None else free_left
-        for name, t, shape in (("cached_lens", cached_lens, (B,)), ("new_lens", new_lens, (B,)), ("free_pages", free_pages, (None,)),
-                               ("free_count", free_count, (1,)), ("block_table", block_table, (B, None)), ("cu_q", cu_q, (B + 1,)),
-                               ("seq_lens", seq_lens, (B,)), ("slot_map", slot_map, (T,)), ("free_left", free_left, (1,))):
-            _check(name, t, i32, shape, dev)
-        rc = lib().fa_kv_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                              block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), slot_map.data_ptr(),
-                              free_left.data_ptr(), B, T, block_table.shape[1], free_pages.shape[0], num_pages, page_size, st)
+        dev, B = cached_lens.device, cached_lens.shape[0]
+        if slot_map is None and num_tokens is None:
+            raise ValueError("give slot_map or num_tokens")
+        with _allocating(dev, stream):
+            cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev) if cu_q is None else cu_q
+            seq_lens = torch.empty(B, dtype=torch.int32, device=dev) if seq_lens is None else seq_lens
+            slot_map = torch.empty(num_tokens, dtype=torch.int32, device=dev) if slot_map is None else slot_map
+            free_left = torch.empty(1, dtype=torch.int32, device=dev) if free_left is None else free_left
+    rc = _binding().kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_pages, page_size, cu_q, seq_lens,
+                            slot_map, free_left, stream if stream is None else _stream_of(stream, cached_lens.device))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv_plan")
     return cu_q, seq_lens, slot_map, free_left
-
-
-def _check_pages(pages, dev):
-    """The shape (num_pages, Hkv, page_size, D) of a cache whose (name, codes, scale) are in `pages`."""
-    import torch
-
-    shape = tuple(pages[0][1].shape)
-    if len(shape) != 4:
-        raise ValueError("pages must be [num_pages, Hkv, page_size, D]")
-    for name, codes, scale in pages:
-        _check(name + "_pages", codes, (torch.float8_e4m3fn, torch.uint8), shape, dev)
-        _check(name + "_scale", scale, (torch.float32,), shape[:2], dev)
-    return shape
 
 
 def fa_kv_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean=None, k_mean_scale=None, stream=None):
@@ -497,38 +476,10 @@ def fa_kv_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean=None
     k_pages, v_pages: uint8 or float8_e4m3fn [num_pages, Hkv, page_size, D]; k_scale, v_scale: fp32
     [num_pages, Hkv]; k_mean (int8 [num_pages, Hkv, D]) and k_mean_scale (fp32 [num_pages, Hkv]), both or
     neither, are the pages' mean keys for fa_page_select.  Does not synchronise."""
-    import torch
-
-    dev = k.device
-    with _Launch(dev, stream) as st:
-        num_pages, Hkv, page_size, D = _check_pages((("k", k_pages, k_scale), ("v", v_pages, v_scale)), dev)
-        T = slot_map.shape[0]
-        _check("slot_map", slot_map, (torch.int32,), (None,), dev)
-        _check("k", k, (torch.bfloat16,), (T, Hkv, D), dev, strided=True)
-        _check("v", v, (torch.bfloat16,), (T, Hkv, D), dev, strided=True)
-        if (k_mean is None) != (k_mean_scale is None):
-            raise ValueError("give both of k_mean and k_mean_scale, or neither")
-        if k_mean is not None:
-            _check("k_mean", k_mean, (torch.int8,), (num_pages, Hkv, D), dev)
-            _check("k_mean_scale", k_mean_scale, (torch.float32,), (num_pages, Hkv), dev)
-        rc = lib().fa_kv_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                k_scale.data_ptr(), v_scale.data_ptr(), None if k_mean is None else k_mean.data_ptr(),
-                                None if k_mean is None else k_mean_scale.data_ptr(), T, Hkv, D, _token_stride(k),
-                                _token_stride(v), num_pages, page_size, st)
+    rc = _binding().kv_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean, k_mean_scale,
+                              stream if stream is None else _stream_of(stream, k.device))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv_append")
-
-
-def _check_queries(q, cu_q, seq_lens, block_table, D):
-    import torch
-
-    T, Hq, B = q.shape[0], q.shape[1], seq_lens.shape[0]
-    dev, i32 = q.device, (torch.int32,)
-    _check("q", q, (torch.bfloat16,), (None, None, D), dev, strided=True)
-    _check("cu_q", cu_q, i32, (B + 1,), dev)
-    _check("seq_lens", seq_lens, i32, (None,), dev)
-    _check("block_table", block_table, i32, (B, None), dev)
-    return B, T, Hq, block_table.shape[1]
 
 
 def fa_page_select(q, cu_q, seq_lens, block_table, k_mean, k_mean_scale, page_size: int, top_k: int, keep_first: int = 1,
@@ -540,21 +491,15 @@ def fa_page_select(q, cu_q, seq_lens, block_table, k_mean, k_mean_scale, page_si
     block_table: int32 [B, max_pages]; k_mean, k_mean_scale: fa_kv_append's.  Returns (sel, sel_count):
     int32 [B, Hkv, top_k] of positions in the block table, ascending, -1 behind the last, and int32
     [B, Hkv].  Does not synchronise."""
-    import torch
+    if sel is None or sel_count is None:
+        import torch
 
-    dev = q.device
-    with _Launch(dev, stream) as st:
-        _check("k_mean", k_mean, (torch.int8,), (None, None, None), dev)
-        num_pages, Hkv, D = k_mean.shape
-        _check("k_mean_scale", k_mean_scale, (torch.float32,), (num_pages, Hkv), dev)
-        B, T, Hq, max_pages = _check_queries(q, cu_q, seq_lens, block_table, D)
-        sel = torch.empty((B, Hkv, top_k), dtype=torch.int32, device=dev) if sel is None else sel
-        sel_count = torch.empty((B, Hkv), dtype=torch.int32, device=dev) if sel_count is None else sel_count
-        _check("sel", sel, (torch.int32,), (B, Hkv, top_k), dev)
-        _check("sel_count", sel_count, (torch.int32,), (B, Hkv), dev)
-        rc = lib().fa_page_select(q.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-                                  k_mean.data_ptr(), k_mean_scale.data_ptr(), sel.data_ptr(), sel_count.data_ptr(), B, T, Hq,
-                                  Hkv, D, _token_stride(q), max_pages, num_pages, page_size, top_k, keep_first, keep_last, st)
+        shape = (seq_lens.shape[0], k_mean.shape[1])
+        with _allocating(q.device, stream):
+            sel = torch.empty((*shape, top_k), dtype=torch.int32, device=q.device) if sel is None else sel
+            sel_count = torch.empty(shape, dtype=torch.int32, device=q.device) if sel_count is None else sel_count
+    rc = _binding().page_select(q, cu_q, seq_lens, block_table, k_mean, k_mean_scale, page_size, top_k, keep_first, keep_last, sel,
+                                sel_count, stream if stream is None else _stream_of(stream, q.device))
     if rc != FA_OK:
         raise FAError(rc, "fa_page_select")
     return sel, sel_count
@@ -570,30 +515,21 @@ def fa_fwd_paged(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_sc
     sel_count: both or neither.  o (bf16 [T, Hq, D]), lse (fp32 [T, Hq]) and workspace (a CUDA uint8
     tensor of at least fa_fwd_paged_workspace_bytes(...) bytes) are allocated if not given; rows from
     cu_q[B] on are not written.  Returns (o, lse) without synchronising."""
-    import torch
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if o is None or lse is None or workspace is None:
+        import torch
 
-    dev = q.device
-    with _Launch(dev, stream) as st:
-        num_pages, Hkv, page_size, D = _check_pages((("k", k_pages, k_scale), ("v", v_pages, v_scale)), dev)
-        B, T, Hq, max_pages = _check_queries(q, cu_q, seq_lens, block_table, D)
-        if (sel is None) != (sel_count is None):
-            raise ValueError("give both of sel and sel_count, or neither")
-        if sel is not None:
-            _check("sel", sel, (torch.int32,), (B, Hkv, None), dev)
-            _check("sel_count", sel_count, (torch.int32,), (B, Hkv), dev)
-        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if o is None else o
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        _check("o", o, (torch.bfloat16,), (T, Hq, D), dev)
-        _check("lse", lse, (torch.float32,), (T, Hq), dev)
-        if workspace is None:
-            workspace = torch.empty(max(fa_fwd_paged_workspace_bytes(B, T, Hq, Hkv, D), 16), dtype=torch.uint8, device=dev)
-        _check("workspace", workspace, (torch.uint8,), (None,), dev)
-        rc = lib().fa_fwd_paged(q.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-                                k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                None if sel is None else sel.data_ptr(), None if sel is None else sel_count.data_ptr(),
-                                o.data_ptr(), lse.data_ptr(), B, T, Hq, Hkv, D, D ** -0.5 if scale is None else float(scale),
-                                _token_stride(q), max_pages, num_pages, page_size, 0 if sel is None else sel.shape[2],
-                                workspace.data_ptr(), workspace.numel(), st)
+        dev = q.device
+        with _allocating(dev, stream):
+            o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if o is None else o
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
+            if workspace is None:
+                with torch.cuda.device(dev):
+                    need = fa_fwd_paged_workspace_bytes(seq_lens.shape[0], q.shape[0], q.shape[1], k_pages.shape[1], q.shape[-1])
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    rc = _binding().fwd_paged(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, sel, sel_count, o, lse, scale,
+                              workspace, stream if stream is None else _stream_of(stream, q.device))
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_paged")
     return o, lse

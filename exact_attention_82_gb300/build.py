@@ -1,7 +1,9 @@
 """Build the sm_103a shared library in-tree with nvcc (no cmake, no torch
 extension machinery): each .cu is compiled in parallel, then linked with the
 static CUDA runtime into ``_build/libfa_gb300.so``.  The driver's tensor-map
-encoder is looked up at run time, so the library does not link libcuda.
+encoder is looked up at run time, so the library does not link libcuda.  The
+paged cache's calls for torch tensors are a small CPython extension beside it
+(``fa_binding.cpp``, compiled with g++ against torch's headers).
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
+BINDING_SOURCE = "fa_binding.cpp"
+BINDING_PATH = os.path.join(OUT_DIR, "fa_binding.so")
 
 SOURCES = ["fa_fwd_kernel.cu", "fa_splitkv.cu", "fa_bwd.cu", "fa_kv_cache.cu", "fa_page_select.cu",
            "fa_paged.cu", "fa_api.cu"]
@@ -34,16 +39,16 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES + [BINDING_SOURCE]]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "fa.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -67,15 +72,50 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
+    cmd = [cc, *ARCH, "-shared", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj)
     return LIB_PATH
+
+
+def _torch_dir() -> str:
+    import importlib.util
+
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _run(cmd, what: str, verbose: bool = False):
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding(verbose: bool) -> str:
+    obj = os.path.join(OUT_DIR, "fa_binding.o")
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_path("include"), "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-c",
+          os.path.join(CSRC, BINDING_SOURCE), "-o", obj], f"g++ on {BINDING_SOURCE}", verbose)
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    libs = os.path.join(_torch_dir(), "lib")
+    _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, LIB_PATH, "-L", libs, "-ltorch_python", "-lc10_cuda", "-lc10",
+          "-ltorch_cpu", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], "linking the binding")
+    os.replace(tmp, BINDING_PATH)
 
 
 if __name__ == "__main__":
