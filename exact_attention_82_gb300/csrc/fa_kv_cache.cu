@@ -79,7 +79,8 @@ __device__ __forceinline__ int count_le(const int *a, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const PlanParams p) {
+__global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const __grid_constant__ PlanParams p) {
+    grid_wait();
     extern __shared__ int sm_plan[];
     __shared__ long long warp_sums[kPlanThreads / 32];
     int *cu = sm_plan;              // [B+1] first token of each request, at most T
@@ -152,11 +153,11 @@ cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream
     long long grid = ((most > p.T ? most : p.T) + kPlanThreads - 1) / kPlanThreads;
     if (grid > 4ll * num_sms) grid = 4ll * num_sms;
     const int smem = 2 * (p.B + 1) * (int)sizeof(int);
-    const cudaError_t e =
-        cudaFuncSetAttribute(fa_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    fa_kv_plan_kernel<<<(unsigned)grid, kPlanThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    if (smem > 48 * 1024) {  // beyond what a kernel may have without asking
+        const cudaError_t e = cudaFuncSetAttribute(fa_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_early(fa_kv_plan_kernel, dim3((unsigned)grid), kPlanThreads, smem, stream, 1, p);
 }
 
 // ------------------------------------------------------------------ append
@@ -226,6 +227,7 @@ struct AppendCfg {
 template <int D, int PAGE>
 __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
     using C = AppendCfg<D, PAGE>;
+    grid_wait();
     __shared__ int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
     __shared__ uint32_t starts[kWindow / 32];
     __shared__ uint32_t amax_sm[2][C::WARPS];
@@ -426,8 +428,7 @@ static cudaError_t launch_append(const AppendParams &p, int num_sms, cudaStream_
     long long share = 32ll * num_sms / per;
     share = share < 1 ? 1 : (share > most ? most : share);
     const dim3 grid((unsigned)(windows * share), p.Hkv, 2);
-    fa_kv_append_kernel<D, PAGE><<<grid, AppendCfg<D, PAGE>::THREADS, 0, stream>>>(p, (int)share);
-    return cudaGetLastError();
+    return launch_early(fa_kv_append_kernel<D, PAGE>, grid, AppendCfg<D, PAGE>::THREADS, 0, stream, 1, p, (int)share);
 }
 
 template <int D>

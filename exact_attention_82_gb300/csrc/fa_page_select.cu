@@ -62,6 +62,7 @@ __device__ __forceinline__ void store_cluster(uint32_t a, uint32_t v) {
 
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __grid_constant__ SelectParams p) {
+    grid_wait();
     extern __shared__ uint32_t key[];  // [max_pages] the order of each page's score, in the first block
     __shared__ __align__(16) int q8[kSelRows][D / 4];
     __shared__ float qs[kSelRows];
@@ -232,21 +233,12 @@ cudaError_t launch_page_select(int D, const SelectParams &p, cudaStream_t stream
     int size = 1;
     while (size < 8 && size * kSelShare < p.max_pages) size *= 2;
     void (*const f)(SelectParams) = D == 64 ? fa_page_select_kernel<64> : fa_page_select_kernel<128>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(size, p.Hkv, p.B);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = p.max_pages * sizeof(uint32_t);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = size;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaFuncSetAttribute((const void *)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
-    if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, f, p);
+    const size_t smem = p.max_pages * sizeof(uint32_t);
+    if (smem > 40 * 1024) {  // beyond what a kernel may have, beside its own arrays, without asking
+        const cudaError_t e = cudaFuncSetAttribute((const void *)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_early(f, dim3(size, p.Hkv, p.B), kSelThreads, smem, stream, size, p);
 }
 
 cudaError_t page_select_status_read_and_clear(int *out) {

@@ -313,8 +313,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&h);
 }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The workspace: for each block what the item that it leaves off needs to be
 // joined, then two slots of partial results for each warp: 0 for an item that was begun
@@ -357,7 +355,6 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     __shared__ int flag_of[C::WARPS];
     __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR];
     __shared__ float close_f[C::WARPS][NR], inv_of[C::WARPS][NR];
-    grid_launch_dependents();
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -939,7 +936,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
     __shared__ float red_m[kJoinWarps], red_l[kJoinWarps], red_o[kJoinWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x, blocks = gridDim.x;
     JoinRow<D, NR> row_of;
-    grid_launch_dependents();
     grid_wait();
     const Tail tail = *tail_of(p.ws, block);
     if (tail.parts == 0) return;
@@ -984,23 +980,9 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     using C = PgCfg<D, NT>;
     cudaError_t e = cudaFuncSetAttribute(fa_fwd_paged_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(num_sms);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    e = cudaLaunchKernelEx(&cfg, fa_fwd_paged_kernel<D, NT>, p);
+    e = launch_early(fa_fwd_paged_kernel<D, NT>, dim3(num_sms), C::THREADS, C::SMEM, stream, 1, p);
     if (e != cudaSuccess) return e;
-    // the join is launched while the first kernel still runs, and waits for its end
-    cfg.gridDim = dim3(num_sms, 8 * NT / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, NT>, p);
+    return launch_early(fa_paged_join_kernel<D, NT>, dim3(num_sms, 8 * NT / kJoinWarps), 32 * kJoinWarps, 0, stream, 1, p);
 }
 
 // Rows of an item: 8 while a sequence's query rows are no more (by the mean

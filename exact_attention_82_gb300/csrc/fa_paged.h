@@ -65,4 +65,33 @@ cudaError_t kv_cache_status_read_and_clear(int *out);
 cudaError_t page_select_status_read_and_clear(int *out);
 cudaError_t paged_status_read_and_clear(int *out);
 
+// A launch whose blocks may be made ready while the kernel before it in the stream
+// ends: every kernel of the paged cache begins by waiting for the one before it to have
+// ended and its writes to be seen (grid_wait).  Back to back calls of fa_kv_plan: 5.8 us with
+// plain launches, 3.1 us with these.  (None lets the next one in before its own end: blocks
+// that wait take the place of blocks that work, 4.3 -> 7.1 us where there are many.)
+// `cluster`: blocks of a cluster along x.
+template <class... A>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 }  // namespace fa
