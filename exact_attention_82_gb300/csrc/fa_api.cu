@@ -698,7 +698,7 @@ extern "C" int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens,
     p.page_log2 = page_log2_of(page_size);
     p.sel_width = sel ? sel_width : 0;
     p.scale_log2 = scale_log2;
-    if (!fa::paged_fits(p)) return FA_ERR_BAD_SHAPE;
+    if (!fa::paged_fits(D, p)) return FA_ERR_BAD_SHAPE;
     const cudaError_t e = fa::launch_fwd_paged(D, p, sm_count(), (cudaStream_t)stream);
     return e == cudaSuccess ? FA_OK : fail_cuda(e);
 }

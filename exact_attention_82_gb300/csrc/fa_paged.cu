@@ -28,7 +28,7 @@
 // running maximum and sums: nothing waits for another warp before the end of an
 // item.
 //
-// Split.  The tiles of all items (sequence, key/value head, 8 or 16 query rows)
+// Split.  The tiles of all items (sequence, key/value head, 8 to 32 query rows)
 // are laid end to end, each item behind a few places that stand for its fixed
 // cost, and the line is cut into equal shares, one a block (an SM), and each of
 // them again into equal ones, one a warp, whatever the lengths: a long sequence is
@@ -68,12 +68,16 @@ struct PgCfg {
     static constexpr int STAGE_BYTES = 4 * HALF_BYTES;       // K and V of a tile
     static constexpr int WARPS = NT == 1 ? 12 : 8;           // one block an SM
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int ST = (D == 128 ? 2 : 4) + (NT == 1 ? 0 : D == 128 ? 1 : 2);  // stages a warp: 192 KB
+    // Beside 32 rows the registers are full of sums, and the query fragments lie in shared
+    // memory, each lane's apart (32 KB of the 192; the ring has the rest).
+    static constexpr bool Q_SHARED = NT > 2;
+    static constexpr int ST = D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 4 : NT == 2 ? 6 : 5);  // stages a warp
     static constexpr int OFF_META = WARPS * ST * STAGE_BYTES;  // 2 float4 a stage
     static constexpr int OFF_WORK = OFF_META + WARPS * ST * 2 * 16;
     static constexpr int WORKS = 8;                          // items looked up ahead: ST + 1 at most
     static constexpr int OFF_SUMS = OFF_WORK + WARPS * WORKS * 48;
-    static constexpr int SMEM = OFF_SUMS + THREADS * 4;
+    static constexpr int OFF_Q = (OFF_SUMS + THREADS * 4 + 127) / 128 * 128;
+    static constexpr int SMEM = OFF_Q + (Q_SHARED ? WARPS * 8 * NT * D * 2 : 0);
     // Where a 16-byte piece of a row lies: pieces are swapped within 128 bytes so that
     // eight rows' same piece (ldmatrix) falls into different banks.
     static __device__ __forceinline__ int swap(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
@@ -497,7 +501,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     const Work *it = work_of;
     int i = 0, done = 0, fill = C::ST - 1;
     int t1 = 0;  // where the item's tiles end
-    uint32_t qf[NT][KG][4][2];  // fragments of Q^T (lane: row g of each tile of 8)
+    uint32_t qf[C::Q_SHARED ? 1 : NT][KG][4][2];  // fragments of Q^T (lane: row g of each tile of 8)
+    uint2 *const q_sm = reinterpret_cast<uint2 *>(sm + C::OFF_Q) + warp * (KG * 4 * NT * 32) + lane;  // or here, [kg][w][nt]
     float fac[NT][2];           // c 2^e of the rows 2t, 2t+1, which this lane holds in accumulators
     int lim[NT][2], lim_min = 0;  // the first key that they do not see, and the least of them
     float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
@@ -543,10 +548,17 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+                        uint32_t f[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            qf[nt][i][2 * j + c / 2][c & 1] =
-                                pack_f16x2(__uint_as_float(u[c] << 16) * down, __uint_as_float(u[c] & 0xffff0000u) * down);
+                            f[c] = pack_f16x2(__uint_as_float(u[c] << 16) * down, __uint_as_float(u[c] & 0xffff0000u) * down);
+                        if (C::Q_SHARED) {
+                            q_sm[((i * 4 + 2 * j) * NT + nt) * 32] = make_uint2(f[0], f[1]);
+                            q_sm[((i * 4 + 2 * j + 1) * NT + nt) * 32] = make_uint2(f[2], f[3]);
+                        } else {
+                            qf[C::Q_SHARED ? 0 : nt][i][2 * j][0] = f[0], qf[C::Q_SHARED ? 0 : nt][i][2 * j][1] = f[1];
+                            qf[C::Q_SHARED ? 0 : nt][i][2 * j + 1][0] = f[2], qf[C::Q_SHARED ? 0 : nt][i][2 * j + 1][1] = f[3];
+                        }
                     }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -581,24 +593,51 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
             // pieces t and t + 4 of its keys' rows, four MMAs' worth each.
             float sc[2][NT][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sc[half][nt][j] = 0.f;
+            if (!C::Q_SHARED) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int kg = 0; kg < KG; ++kg) {
+                        const uint32_t at = ((k_read + st) ^ (kg * 64)) + half * C::HALF_BYTES;
+                        uint32_t a[4], b8[4];
+                        ld_shared_v4(at, a[0], a[1], a[2], a[3]);
+                        ld_shared_v4(at + 8 * D, b8[0], b8[1], b8[2], b8[3]);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t a0 = codes_f16x2(a[w]), a1 = codes_f16x2(b8[w]);
+                            const uint32_t a2 = codes_f16x2(a[w] >> 16), a3 = codes_f16x2(b8[w] >> 16);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(sc[half][nt], a0, a1, a2, a3, qf[C::Q_SHARED ? 0 : nt][kg][w][0], qf[C::Q_SHARED ? 0 : nt][kg][w][1]);
+                        }
+                    }
+            } else {  // both halves together, so that a fragment of Q is read once a tile
 #pragma unroll
                 for (int kg = 0; kg < KG; ++kg) {
-                    const uint32_t at = ((k_read + st) ^ (kg * 64)) + half * C::HALF_BYTES;
-                    uint32_t a[4], b8[4];
-                    ld_shared_v4(at, a[0], a[1], a[2], a[3]);
-                    ld_shared_v4(at + 8 * D, b8[0], b8[1], b8[2], b8[3]);
+                    uint32_t a[2][4], b8[2][4];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t at = ((k_read + st) ^ (kg * 64)) + half * C::HALF_BYTES;
+                        ld_shared_v4(at, a[half][0], a[half][1], a[half][2], a[half][3]);
+                        ld_shared_v4(at + 8 * D, b8[half][0], b8[half][1], b8[half][2], b8[half][3]);
+                    }
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const uint32_t a0 = codes_f16x2(a[w]), a1 = codes_f16x2(b8[w]);
-                        const uint32_t a2 = codes_f16x2(a[w] >> 16), a3 = codes_f16x2(b8[w] >> 16);
+                        uint2 q[NT];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(sc[half][nt], a0, a1, a2, a3, qf[nt][kg][w][0], qf[nt][kg][w][1]);
+                        for (int nt = 0; nt < NT; ++nt) q[nt] = q_sm[((kg * 4 + w) * NT + nt) * 32];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t a0 = codes_f16x2(a[half][w]), a1 = codes_f16x2(b8[half][w]);
+                            const uint32_t a2 = codes_f16x2(a[half][w] >> 16), a3 = codes_f16x2(b8[half][w] >> 16);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma_f16(sc[half][nt], a0, a1, a2, a3, q[nt].x, q[nt].y);
+                        }
                     }
                 }
             }
@@ -969,10 +1008,10 @@ static size_t workspace_of(int num_sms) {
 }
 
 size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms) {
-    (void)B, (void)T, (void)Hq, (void)Hkv;  // the same for all: what of the two forms needs more
-    const size_t a = D == 64 ? workspace_of<64, 1>(num_sms) : workspace_of<128, 1>(num_sms);
-    const size_t b = D == 64 ? workspace_of<64, 2>(num_sms) : workspace_of<128, 2>(num_sms);
-    return a > b ? a : b;
+    (void)B, (void)T, (void)Hq, (void)Hkv;  // the same for all: what of the forms needs most
+    if (D == 64)
+        return std::max(workspace_of<64, 1>(num_sms), std::max(workspace_of<64, 2>(num_sms), workspace_of<64, 4>(num_sms)));
+    return std::max(workspace_of<128, 1>(num_sms), workspace_of<128, 2>(num_sms));
 }
 
 template <int D, int NT>
@@ -985,16 +1024,18 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
     return launch_early(fa_paged_join_kernel<D, NT>, dim3(num_sms, 8 * NT / kJoinWarps), 32 * kJoinWarps, 0, stream, 1, p);
 }
 
-// Rows of an item: 8 while a sequence's query rows are no more (by the mean
-// number of its tokens, padding rounded off), 16 beyond.
-static bool wide_items(const PagedParams &p) {
-    const long long tokens = (2ll * p.T + p.B) / (2ll * p.B);
-    return (tokens > 1 ? tokens : 1) * p.G > 8;
+// Rows of an item: 8 or 16 while a sequence's query rows are no more (by the mean
+// number of its tokens, padding rounded off).  Beyond, 32 at D = 64 (16 sequences of 16384
+// keys, 32 rows: 97 us, 118 us in two items of 16) and 16 at D = 128, where the sums of 32
+// rows leave too few registers (8 sequences, 32 rows: 116 us, 100 us in two items).
+static int item_rows(int D, const PagedParams &p) {
+    const long long tokens = (2ll * p.T + p.B) / (2ll * p.B), rows = (tokens > 1 ? tokens : 1) * p.G;
+    return rows <= 8 ? 8 : rows <= 16 || D == 128 ? 16 : 32;
 }
 
-bool paged_fits(const PagedParams &p) {
+bool paged_fits(int D, const PagedParams &p) {
     const long long keys = (long long)(p.sel_width > p.max_pages ? p.sel_width : p.max_pages) << p.page_log2;
-    const long long items = ((long long)p.T * p.G / (wide_items(p) ? 16 : 8) + p.B) * p.Hkv;
+    const long long items = ((long long)p.T * p.G / item_rows(D, p) + p.B) * p.Hkv;
     const long long places = keys / kPgTile + 1 + kPgFixed;
     return keys <= 0x7fffffff && items < (1ll << 31) && items * places < (1ll << 31) - (1 << 20);
 }
@@ -1002,9 +1043,11 @@ bool paged_fits(const PagedParams &p) {
 cudaError_t launch_fwd_paged(int D, const PagedParams &params, int num_sms, cudaStream_t stream) {
     PagedParams p = params;
     p.max_len = (int)std::min<long long>((long long)p.max_pages << p.page_log2, kPgMaxLen);
-    const bool wide = wide_items(p);
-    if (D == 64) return wide ? launch_paged<64, 2>(p, num_sms, stream) : launch_paged<64, 1>(p, num_sms, stream);
-    return wide ? launch_paged<128, 2>(p, num_sms, stream) : launch_paged<128, 1>(p, num_sms, stream);
+    const int rows = item_rows(D, p);
+    if (D == 64)
+        return rows == 8 ? launch_paged<64, 1>(p, num_sms, stream)
+                         : rows == 16 ? launch_paged<64, 2>(p, num_sms, stream) : launch_paged<64, 4>(p, num_sms, stream);
+    return rows == 8 ? launch_paged<128, 1>(p, num_sms, stream) : launch_paged<128, 2>(p, num_sms, stream);
 }
 
 cudaError_t paged_status_read_and_clear(int *out) {

@@ -56,7 +56,7 @@ struct PagedParams {
     float scale_log2;            // scale * log2(e)
 };
 // Whether the work of these sizes, at most, can be laid out in 32-bit places.
-bool paged_fits(const PagedParams &p);
+bool paged_fits(int D, const PagedParams &p);
 size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream);
 
