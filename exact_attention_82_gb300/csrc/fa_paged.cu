@@ -122,20 +122,12 @@ __device__ __forceinline__ int entry_weight(const PagedParams &p, int e) {
     return rt * (p.sel ? 1 : p.Hkv) * (kPgFixed + item_tiles(p, b, h, s.len));
 }
 
-// The place of `pos`, from the sums up to the end of each thread's entries.  Where it
-// falls into an item's fixed places, or into an item of at most `small` places, it is
-// moved to the item's beginning or its nearer end.
+// The place of `pos`, which thread `at`'s entries contain (`base`: the places before
+// them).  Where it falls into an item's fixed places, or into an item of at most `small`
+// places, it is moved to the item's beginning or its nearer end.
 template <int NR>
-__device__ __forceinline__ Place place_of(const PagedParams &p, const int *sums, int threads, int per, int n, int pos, int small) {
-    int lo = 0, hi = threads - 1;  // the first thread whose sum is above pos
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] > pos)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    Place f{min(lo * per, n - 1), lo ? sums[lo - 1] : 0, pos};
+__device__ __forceinline__ Place place_of(const PagedParams &p, int at, int base, int per, int n, int pos, int small) {
+    Place f{min(at * per, n - 1), base, pos};
 #pragma unroll 1
     for (const int e1 = min(n, f.entry + per); f.entry < e1 - 1; ++f.entry) {
         const int w = entry_weight<NR>(p, f.entry);
@@ -161,52 +153,52 @@ struct Work {
 };
 static_assert(sizeof(Work) == 48, "");
 
-// The item at place.pos, which is moved behind the warp's tiles of it.  (Rare work like
-// this is kept out of line, so that the loop over tiles stays within the instruction
-// cache: with all of it inlined, in 64 bits, the kernel was 192 KB long and spent 25 us on
-// fetching itself.)
-template <int NR>
-__device__ __noinline__ Work work_at(const PagedParams &p, Place &place, int end) {
-    // The scan's lengths and these are the same unless the caller changes them during
-    // the call; the bounds on entry, head and block keep every access inside even then.
-    const int n = p.sel ? p.B * p.Hkv : p.B;
-#pragma unroll 1
-    for (; place.entry < n - 1; ++place.entry) {
-        const int w = entry_weight<NR>(p, place.entry);
-        if (place.pos < place.base + w) break;
-        place.base += w;
-    }
-    Work it;
-    it.b = p.sel ? place.entry / p.Hkv : place.entry;
-    it.h = p.sel ? place.entry % p.Hkv : 0;
-    const Seq s = sequence(p, it.b);
-    it.q0 = s.q0, it.nq = s.nq, it.len = s.len;
-    it.tiles = item_tiles(p, it.b, it.h, s.len);
-    it.rows = s.nq * p.G;
-    const int w = kPgFixed + it.tiles;
-    int rt = (int)((uint32_t)(place.pos - place.base) / (uint32_t)w);
-    const int first = place.base + rt * w;
-    if (!p.sel) {
-        const int rts = (uint32_t)(it.rows + NR - 1) / NR;
-        it.h = rt;
-        if (rts > 1) it.h = rt / rts, rt %= rts;
-        else rt = 0;
-        it.h = min(it.h, p.Hkv - 1);
-    }
-    it.row0 = rt * NR;
-    it.t0 = max(0, place.pos - first - kPgFixed);
-    it.t1 = max(it.t0 + 1, min(it.tiles, end - first - kPgFixed));
-    place.pos = first + kPgFixed + it.t1;
-    it.last = place.pos >= end;
-    it.end = first + w;
-    return it;
-}
-
-// Where a warp is after the scan: behind its first item, which lies in its ring.
+// Where a warp is: behind the last item that it has looked up.
 struct Start {
     Place ahead;   // entry -1: no work
     int end;       // of the warp's share
 };
+
+// The next item of a warp, into `it`; `at` moves behind the warp's tiles of it.  Called
+// by one lane or by a whole warp (whose lanes then write the same), with both in shared
+// memory.  (Rare work like this is kept out of line, so that the loop over tiles stays
+// within the instruction cache: with all of it inlined, in 64 bits, the kernel was 192 KB
+// long and spent 25 us on fetching itself.)
+template <int NR>
+__device__ __noinline__ void work_at(const PagedParams &p, Start *at, Work *it) {
+    // The scan's lengths and these are the same unless the caller changes them during
+    // the call; the bounds on entry, head and block keep every access inside even then.
+    const int n = p.sel ? p.B * p.Hkv : p.B, pos = at->ahead.pos, end = at->end;
+    int entry = at->ahead.entry, base = at->ahead.base;
+#pragma unroll 1
+    for (; entry < n - 1; ++entry) {
+        const int w = entry_weight<NR>(p, entry);
+        if (pos < base + w) break;
+        base += w;
+    }
+    const int b = p.sel ? entry / p.Hkv : entry;
+    int h = p.sel ? entry % p.Hkv : 0;
+    const Seq s = sequence(p, b);
+    const int tiles = item_tiles(p, b, h, s.len), w = kPgFixed + tiles, rows = s.nq * p.G;
+    int rt = (int)((uint32_t)(pos - base) / (uint32_t)w);
+    const int first = base + rt * w;
+    if (!p.sel) {
+        const int rts = (uint32_t)(rows + NR - 1) / NR;
+        h = rt;
+        if (rts > 1)
+            h = rt / rts, rt %= rts;
+        else
+            rt = 0;
+        h = min(h, p.Hkv - 1);
+    }
+    const int t0 = max(0, pos - first - kPgFixed), t1 = max(t0 + 1, min(tiles, end - first - kPgFixed));
+    it->q0 = s.q0, it->nq = s.nq, it->len = s.len;
+    it->b = b, it->h = h, it->row0 = rt * NR, it->rows = rows;
+    it->tiles = tiles, it->t0 = t0, it->t1 = t1;
+    it->last = first + kPgFixed + t1 >= end;
+    it->end = first + w;
+    at->ahead = Place{entry, base, first + kPgFixed + t1};
+}
 
 // Scans the line and starts every warp of the block.  Returns the share of a block.
 template <int WARPS, int NR>
@@ -248,23 +240,45 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start 
         // With less work than the chip has room for, items of up to two least shares stay whole.
         const int small = share <= kPgMinShare ? 2 * kPgMinShare : share / 2;
         share = max(share, kPgMinShare);
-        // the block's ends, then the warps'
+        // The block's ends.  Which thread's entries hold them: a lane's twelve or eight sums,
+        // then one of those.
+        auto holder = [&](int pos) {
+            const int in = max(0, __ffs((int)__ballot_sync(0xffffffffu, x > pos)) - 1);
+            const uint32_t above = __ballot_sync(0xffffffffu, lane < WARPS && sums[in * WARPS + min(lane, WARPS - 1)] > pos);
+            return in * WARPS + max(0, __ffs((int)above) - 1);
+        };
+        const long long cut0 = (long long)blockIdx.x * share, cut1 = cut0 + share;
+        const int at0 = holder((int)min(cut0, total - 1ll)), at1 = holder((int)min(cut1, total - 1ll));
         Place f{0, 0, total};
-        const long long cut = (long long)(blockIdx.x + (lane == WARPS)) * share;
-        if (cut < total) f = place_of<NR>(p, sums, THREADS, per, n, (int)cut, small);
+        {
+            const long long cut = lane == WARPS ? cut1 : cut0;
+            const int at = lane == WARPS ? at1 : at0;
+            if (cut < total) f = place_of<NR>(p, at, at ? sums[at - 1] : 0, per, n, (int)cut, small);
+        }
+        // the warps' ends, between them
         const int begin = __shfl_sync(0xffffffffu, f.pos, 0), end = __shfl_sync(0xffffffffu, f.pos, WARPS);
         const int part = (end - begin + WARPS - 1) / WARPS, pos = begin + lane * part;
         if (lane > 0 && lane < WARPS) {
             f.pos = end;
-            if (pos < end) f = place_of<NR>(p, sums, THREADS, per, n, pos, part / 2);
+            if (pos < end) {
+                int lo = at0, hi = at1;  // the first thread whose sum is above pos
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (sums[mid] > pos)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                f = place_of<NR>(p, lo, lo ? sums[lo - 1] : 0, per, n, pos, part / 2);
+            }
         }
-        Start st{f, __shfl_down_sync(0xffffffffu, f.pos, 1)};
+        const int mine = __shfl_down_sync(0xffffffffu, f.pos, 1);
         if (lane < WARPS) {
-            if (f.pos < st.end)
-                work_of[lane * works] = work_at<NR>(p, st.ahead, st.end);
+            start[lane] = Start{f, mine};
+            if (f.pos < mine)
+                work_at<NR>(p, start + lane, work_of + lane * works);
             else
-                st.ahead.entry = -1;
-            start[lane] = st;
+                start[lane].ahead.entry = -1;
         }
         if (lane == 0) share_sm = share;
     }
@@ -344,8 +358,12 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
-__device__ __forceinline__ long long out_row(const PagedParams &p, int q0, int h, int row) {
-    return (long long)(q0 + row / p.G) * (p.Hkv * p.G) + h * p.G + row % p.G;
+// The token of a sequence that a row belongs to.
+__device__ __forceinline__ int token_of(const PagedParams &p, int nq, int row) { return nq > 1 ? row / p.G : 0; }
+
+__device__ __forceinline__ long long out_row(const PagedParams &p, int q0, int nq, int h, int row) {
+    const int tok = token_of(p, nq, row);
+    return (long long)(q0 + tok) * (p.Hkv * p.G) + h * p.G + (row - tok * p.G);
 }
 
 // --------------------------------------------------------------- the kernel
@@ -389,13 +407,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
             if (next->last) return;
             next = work_of + (works & (C::WORKS - 1));
             ++works;
-            Place ahead = start[warp].ahead;
-            const Work made = work_at<NR>(p, ahead, start[warp].end);
             __syncwarp();
-            if (lane == 0) {
-                start[warp].ahead = ahead;
-                *const_cast<Work *>(next) = made;
-            }
+            if (lane == 0) work_at<NR>(p, start + warp, const_cast<Work *>(next));
             __syncwarp();
             t_next = next->t0;
         }
@@ -521,7 +534,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 i = it->t0, t1 = it->t1;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int row = it->row0 + nt * 8 + g;
+                const int row = it->row0 + nt * 8 + g, tok = token_of(p, it->nq, row);
+                const __nv_bfloat16 *const q = static_cast<const __nv_bfloat16 *>(p.q) + (long long)(it->q0 + tok) * p.q_stride +
+                                               (long long)(it->h * p.G + row - tok * p.G) * D + 16 * t;
                 uint4 w[KG][2];
                 uint32_t am = 0;
 #pragma unroll
@@ -530,10 +545,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                     for (int j = 0; j < 2; ++j) {
                         w[i][j] = make_uint4(0, 0, 0, 0);
                         if (row < it->rows) {
-                            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                                     (long long)(it->q0 + row / p.G) * p.q_stride +
-                                                     (long long)(it->h * p.G + row % p.G) * D + 16 * (t + 4 * i) + 8 * j;
-                            w[i][j] = __ldg(reinterpret_cast<const uint4 *>(q));
+                            w[i][j] = __ldg(reinterpret_cast<const uint4 *>(q + 64 * i + 8 * j));
                         }
                         const uint32_t u[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
 #pragma unroll
@@ -564,10 +576,10 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 for (int j = 0; j < 2; ++j) {
                     fac[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
                     const int r = it->row0 + nt * 8 + 2 * t + j;
-                    lim[nt][j] = r < it->rows ? it->len - it->nq + r / p.G + 1 : it->len;
+                    lim[nt][j] = r < it->rows ? it->len - it->nq + token_of(p, it->nq, r) + 1 : it->len;
                 }
             }
-            lim_min = it->len - it->nq + it->row0 / p.G + 1;
+            lim_min = it->len - it->nq + token_of(p, it->nq, it->row0) + 1;
 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -808,14 +820,14 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 if (lead != last || closes) {
                     if (lane < NR) {  // a row's maximum over the group, and the factors of its parts to it
                         float M = closes ? closing[NR * D + lane] : kPgNone, L = 0.f, f = 0.f;
-#pragma unroll 1
+#pragma unroll 4
                         for (int w = lead; w <= last; ++w) M = fmaxf(M, join_m[w][lane]);
                         if (closes) {
                             f = ex2_approx(closing[NR * D + lane] - M);
                             L = closing[NR * D + NR + lane] * f;
                         }
                         close_f[warp][lane] = f;
-#pragma unroll 1
+#pragma unroll 4
                         for (int w = lead; w <= last; ++w) L = fmaf(join_l[w][lane], ex2_approx(join_m[w][lane] - M), L);
                         join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
                         inv_of[warp][lane] = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
@@ -823,42 +835,29 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                             if (!whole)
                                 part[NR * D + lane] = M, part[NR * D + NR + lane] = L;
                             else if (it->row0 + lane < it->rows)
-                                p.lse[out_row(p, it->q0, it->h, it->row0 + lane)] = lse_of(M, L);
+                                p.lse[out_row(p, it->q0, it->nq, it->h, it->row0 + lane)] = lse_of(M, L);
                         }
                     }
                     named_bar_sync(1, C::THREADS);
-                    long long at[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int r = nt * 8 + 2 * t + j;
-                            at[nt][j] = it->row0 + r < it->rows ? out_row(p, it->q0, it->h, it->row0 + r) : -1;
+#pragma unroll 1
+                    for (int u = warp - lead; u < C::CHUNKS * NT * 2; u += last - lead + 1) {  // the group's warps share the sums
+                        const int c = u / (2 * NT), r = (u / 2 % NT) * 8 + 2 * t + (u & 1);
+                        float2 o = make_float2(0.f, 0.f);
+                        if (closes) {
+                            o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + g];
+                            o.x *= close_f[warp][r], o.y *= close_f[warp][r];
                         }
-#pragma unroll 1
-                    for (int c = warp - lead; c < C::CHUNKS; c += last - lead + 1) {  // the group's warps share the sums
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int r = nt * 8 + 2 * t + j;
-                                float2 o = make_float2(0.f, 0.f);
-                                if (closes) {
-                                    o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + g];
-                                    o.x *= close_f[warp][r], o.y *= close_f[warp][r];
-                                }
-#pragma unroll 1
-                                for (int w = lead; w <= last; ++w) {
-                                    const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[((c * NT + nt) * 2 + j) * 32 + lane];
-                                    o.x = fmaf(x.x, join_f[w][r], o.x), o.y = fmaf(x.y, join_f[w][r], o.y);
-                                }
-                                const float inv = inv_of[warp][r];
-                                if (!whole)
-                                    reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
-                                else if (at[nt][j] >= 0)
-                                    reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at[nt][j] * D)[8 * c + g] =
-                                        pack_bf16x2(o.x * inv, o.y * inv);
-                            }
+#pragma unroll 4
+                        for (int w = lead; w <= last; ++w) {
+                            const float2 x = reinterpret_cast<const float2 *>(sm + w * C::ST * C::STAGE_BYTES)[u * 32 + lane];
+                            o.x = fmaf(x.x, join_f[w][r], o.x), o.y = fmaf(x.y, join_f[w][r], o.y);
+                        }
+                        const float inv = inv_of[warp][r];
+                        if (!whole)
+                            reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
+                        else if (it->row0 + r < it->rows)
+                            reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + out_row(p, it->q0, it->nq, it->h, it->row0 + r) * D)[8 * c + g] =
+                                pack_bf16x2(o.x * inv, o.y * inv);
                     }
                     return;
                 }
@@ -877,7 +876,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = l[nt][j];
                     } else if (it->row0 + r < it->rows) {
                         const float inv = l[nt][j] == 0.f ? 0.f : 1.f / l[nt][j];
-                        const long long at = out_row(p, it->q0, it->h, it->row0 + r);
+                        const long long at = out_row(p, it->q0, it->nq, it->h, it->row0 + r);
                         uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + g;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
@@ -984,7 +983,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
         const int r = blockIdx.y * kJoinWarps + warp;
         if (r >= rows) return;
         row_of.sum(p, tail, blocks, WARPS, block, r, 0, 1);
-        row_of.write(p, out_row(p, s.q0, tail.h, tail.row0 + r));
+        row_of.write(p, out_row(p, s.q0, s.nq, tail.h, tail.row0 + r));
         return;
     }
 #pragma unroll 1
@@ -998,7 +997,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
         if (warp != 0) continue;
 #pragma unroll
         for (int v = 1; v < kJoinWarps; ++v) row_of.add(red_m[v], red_l[v], &red_o[v][lane * E]);
-        row_of.write(p, out_row(p, s.q0, tail.h, tail.row0 + r));
+        row_of.write(p, out_row(p, s.q0, s.nq, tail.h, tail.row0 + r));
     }
 }
 
