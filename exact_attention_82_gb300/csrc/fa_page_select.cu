@@ -10,11 +10,12 @@
 //
 // Bound by latency: a page's mean key is 68 or 132 bytes, so even 131072 tokens have
 // some MB to read, and the answer is a few hundred numbers.  So it is one launch: a
-// cluster of 1 to 8 blocks takes one (sequence, head), each block scores its share of
-// the pages (a page a thread, its mean key in registers, the 8-bit queries read from
-// shared memory by all threads at once, four products an instruction) and writes the
-// scores' bits into the first block's shared memory, which finds the k-th largest by its
-// bits, eight at a time from the highest, without sorting.
+// cluster of 1 to 8 blocks takes one (sequence, head), and each block scores its share
+// of the pages.  The products run on the tensor cores in integers (16 pages by 8 rows by
+// 32 elements an instruction; four products a lane and instruction took twice as long,
+// most of it to read the queries from shared memory).  The scores' bits are
+// written into the first block's shared memory, which finds the k-th largest by its bits,
+// eleven at a time from the highest, without sorting.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -47,8 +48,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// c (16 x 8, int32) += a (16 x 32, int8) b (32 x 8, int8)
+__device__ __forceinline__ void mma_s8(int (&c)[4], int a0, int a1, int a2, int a3, int b0, int b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // the address of `p` in the cluster's first block
 __device__ __forceinline__ uint32_t in_first_block(const void *p) {
@@ -66,9 +73,9 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
     extern __shared__ uint32_t key[];  // [max_pages] the order of each page's score, in the first block
     __shared__ __align__(16) int q8[kSelRows][D / 4];
     __shared__ float qs[kSelRows];
-    __shared__ int hist[256];
+    __shared__ __align__(16) int hist[2048];
     __shared__ int warp_sums[kSelWarps];
-    __shared__ uint32_t pick[2];
+    __shared__ uint32_t pick[3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int h = blockIdx.y, b = blockIdx.z;
@@ -83,28 +90,60 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
         if (tid == 0) p.sel_count[bh] = take;
         for (int i = take + tid; i < p.top_k; i += kSelThreads) sel[i] = -1;
     }
+    if (size > 1) cluster_arrive();      // this block's shared memory is there
     if (n <= p.top_k || take == 0) {  // every page, or none; the same in all blocks of the cluster
         if (rank == 0)
             for (int i = tid; i < take; i += kSelThreads) sel[i] = i;
+        if (size > 1) cluster_wait();
         return;
     }
-    if (size > 1) cluster_sync();  // the first block's shared memory is there
 
+    // ---- scores: 16 pages at a time a warp
     const int *const table = p.table + (long long)b * p.max_pages;
-    const int rows = (q1 - q0) * p.G;
-    const int chunk = (n + (int)size - 1) / (int)size, begin = min(n, (int)rank * chunk), end = min(n, begin + chunk);
+    const int rows = (q1 - q0) * p.G, g = lane >> 2, t = lane & 3;
+    const int chunk = (((n + (int)size - 1) / (int)size) + 15) & ~15, begin = min(n, (int)rank * chunk), end = min(n, begin + chunk);
+    constexpr int KS = D / 32;  // instructions along a row
+    bool waited = size == 1;
     for (int r0 = 0; r0 < rows; r0 += kSelRows) {
+        // The first pages are asked for before the queries are rounded.  Lane t takes
+        // 16-byte pieces t (and t + 4) of the mean keys of pages g and g + 8.
+        int4 w[2][D / 64];
+        float ms[2];
+        int pg[2];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = i0 + g + 8 * j;
+                pg[j] = i < end ? table[i] : 0;
+                const bool good = pg[j] >= 0 && pg[j] < p.num_pages;
+                if (!good) {
+                    if (r0 == 0) atomicExch(&g_status_page_select, (int)FA_ERR_BAD_PAGE);
+                    pg[j] = -1;
+                }
+                const long long ph = (long long)max(pg[j], 0) * p.Hkv + h;
+                const int4 *const m = reinterpret_cast<const int4 *>(p.mean + ph * D) + t;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) w[j][c] = __ldg(m + 4 * c);
+                ms[j] = p.mean_scale[ph];
+            }
+        };
+        int i0 = begin + warp * 16;
+        if (i0 < end) fetch(i0);
         if (r0 > 0) __syncthreads();
         const int some = min(kSelRows, rows - r0);
-        for (int r = warp; r < some; r += kSelWarps) {
-            const int t = q0 + (r0 + r) / p.G, g = (r0 + r) % p.G;
-            const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(
-                static_cast<const __nv_bfloat16 *>(p.q) + (long long)t * p.q_stride + (long long)(h * p.G + g) * D);
+        for (int r = warp; r < kSelRows; r += kSelWarps) {
             float x[D / 32], amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const float2 f = __bfloat1622float2(q[lane * (D / 64) + i]);
-                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            for (int i = 0; i < D / 32; ++i) x[i] = 0.f;
+            if (r < some) {
+                const int tok = q0 + (r0 + r) / p.G, gq = (r0 + r) % p.G;
+                const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(
+                    static_cast<const __nv_bfloat16 *>(p.q) + (long long)tok * p.q_stride + (long long)(h * p.G + gq) * D);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const float2 f = __bfloat1622float2(q[lane * (D / 64) + i]);
+                    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+                }
             }
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
@@ -119,71 +158,105 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
             if (lane == 0) qs[r] = amax / 127.f;
         }
         __syncthreads();
-        for (int i = begin + tid; i < end; i += kSelThreads) {
-            const int pg = table[i];
-            uint32_t k = 0;  // a page outside the cache: behind all others
-            if (pg >= 0 && pg < p.num_pages) {
-                const long long ph = (long long)pg * p.Hkv + h;
-                const int4 *m = reinterpret_cast<const int4 *>(p.mean + ph * D);
-                int4 w[D / 16];
+        // the order of a row's elements is free as long as both operands have the same
+        int qf[kSelRows / 8][KS][2];
+        float qscale[kSelRows / 8][2];
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) w[c] = __ldg(m + c);
-                const float ms = p.mean_scale[ph];
-#pragma unroll 2
-                for (int r = 0; r < some; ++r) {
-                    int dot[4] = {0, 0, 0, 0};
+        for (int nt = 0; nt < kSelRows / 8; ++nt) {
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        const int4 q = *reinterpret_cast<const int4 *>(&q8[r][4 * c]);
-                        dot[0] = __dp4a(w[c].x, q.x, dot[0]);
-                        dot[1] = __dp4a(w[c].y, q.y, dot[1]);
-                        dot[2] = __dp4a(w[c].z, q.z, dot[2]);
-                        dot[3] = __dp4a(w[c].w, q.w, dot[3]);
-                    }
-                    const uint32_t o = order_of(((float)(dot[0] + dot[1] + dot[2] + dot[3]) * qs[r]) * ms);
-                    k = max(k, min(max(o, 1u), 0xfffffffeu));
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) qf[nt][k][c] = q8[nt * 8 + g][D == 128 ? 4 * (t + 4 * c) + k : 4 * t + 2 * k + c];
+            qscale[nt][0] = qs[nt * 8 + 2 * t], qscale[nt][1] = qs[nt * 8 + 2 * t + 1];
+        }
+        for (; i0 < end; i0 += 16 * kSelWarps) {
+            uint32_t best[2] = {0, 0};
+#pragma unroll
+            for (int nt = 0; nt < kSelRows / 8; ++nt) {
+                if (nt * 8 >= some) continue;
+                int dot[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    int a[2][2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            a[j][c] = reinterpret_cast<const int *>(&w[j][D == 128 ? c : 0])[D == 128 ? k : 2 * k + c];
+                    mma_s8(dot, a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][k][0], qf[nt][k][1]);
                 }
-            } else if (r0 == 0) {
-                atomicExch(&g_status_page_select, (int)FA_ERR_BAD_PAGE);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (nt * 8 + 2 * t + (j & 1) < some) {
+                        const uint32_t o = order_of(((float)dot[j] * qscale[nt][j & 1]) * ms[j >> 1]);
+                        best[j >> 1] = max(best[j >> 1], min(max(o, 1u), 0xfffffffeu));
+                    }
             }
-            if (i < p.keep_first || i >= n - p.keep_last) k = 0xffffffffu;
-            if (size == 1) {
-                key[i] = r0 == 0 ? k : max(k, key[i]);
-            } else {  // this block's own copy holds the maximum over the rows so far
-                if (r0 > 0) k = max(k, key[i - begin]);
-                if (r0 + kSelRows < rows)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                best[j] = max(best[j], __shfl_xor_sync(0xffffffffu, best[j], 1));
+                best[j] = max(best[j], __shfl_xor_sync(0xffffffffu, best[j], 2));
+                if (pg[j] < 0) best[j] = 0;  // a page outside the cache: behind all others
+            }
+            if (!waited) {
+                cluster_wait();
+                waited = true;
+            }
+            const int i = i0 + g + 8 * t;  // lanes t = 0 and 1 write pages g and g + 8
+            uint32_t k = t == 0 ? best[0] : best[1];
+            if (t < 2 && i < end) {
+                if (i < p.keep_first || i >= n - p.keep_last) k = 0xffffffffu;
+                if (r0 > 0) k = max(k, key[i - begin]);  // this block's own copy: the maximum over the rows so far
+                if (rank == 0 || r0 + kSelRows < rows)
                     key[i - begin] = k;
-                else if (rank == 0)
-                    key[i] = k;
                 else
                     store_cluster(in_first_block(key + i), k);
             }
+            if (i0 + 16 * kSelWarps < end) fetch(i0 + 16 * kSelWarps);
         }
     }
-    if (size > 1)
-        cluster_sync();
-    else
+    if (size > 1) {
+        if (!waited) cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
+    }
     if (rank != 0) return;
 
-    // the take-th largest key, eight bits at a time from the top
+    // the take-th largest key, eleven bits at a time from the top
     uint32_t prefix = 0, known = 0;
     int left = take;  // how many of the keys that agree with the prefix are taken
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    bool all = false; // whether all of them are
+    for (int shift = 21; shift > -11 && !all; shift -= shift == 10 ? 10 : 11) {
+        const uint32_t digit = shift == 0 ? 1023u : 2047u;
+        *reinterpret_cast<int4 *>(&hist[4 * tid]) = make_int4(0, 0, 0, 0);
         __syncthreads();
-        for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-            const int i = i0 + tid;
-            const bool in = i < n && (key[min(i, n - 1)] & known) == prefix;
-            const uint32_t bin = in ? (key[i] >> shift) & 255u : 256u;
-            // scores are alike in their highest bits: equal bins of a warp are counted at once
-            const uint32_t same = __match_any_sync(0xffffffffu, bin);
-            if (in && lane == __ffs((int)same) - 1) atomicAdd(&hist[bin], __popc(same));
+        for (int i0 = 0; i0 < n; i0 += 4 * kSelThreads) {
+            uint32_t k[4];
+            bool in[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * kSelThreads + tid;
+                k[j] = i < n ? key[i] : 0u;
+                in[j] = i < n && (k[j] & known) == prefix;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t members = __ballot_sync(0xffffffffu, in[j]);
+                if (!members) continue;
+                // scores are alike in their highest bits: those in one bin with the first are counted at once
+                const uint32_t bin = (k[j] >> shift) & digit, first = __shfl_sync(0xffffffffu, bin, __ffs((int)members) - 1);
+                const uint32_t same = __ballot_sync(0xffffffffu, in[j] && bin == first);
+                if (lane == 0) atomicAdd(&hist[first], __popc(same));
+                if (in[j] && bin != first) atomicAdd(&hist[bin], 1);
+            }
         }
         __syncthreads();
-        // sums over the bins from the highest down: thread t has bin 255 - t
-        int s = tid < 256 ? hist[255 - tid] : 0;
-        const int mine = s;
+        // sums over the bins from the highest down: thread t has bin 2047 - 4 t and the three below
+        const int4 c4 = *reinterpret_cast<const int4 *>(&hist[2044 - 4 * tid]);
+        const int c[4] = {c4.w, c4.z, c4.y, c4.x}, mine = c[0] + c[1] + c[2] + c[3];
+        int s = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, s, d);
@@ -191,22 +264,45 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
         }
         if (lane == 31) warp_sums[warp] = s;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) s += warp_sums[w];
-        if (tid < 256 && s >= left && s - mine < left) {
-            pick[0] = 255 - tid;
-            pick[1] = left - (s - mine);
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w)
+            if (w < warp) s += warp_sums[w];
+        int before = s - mine;
+        if (before < left && s >= left) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before < left && before + c[j] >= left) {
+                    pick[0] = 2047 - 4 * tid - j;
+                    pick[1] = left - before;
+                    pick[2] = c[j];
+                }
+                before += c[j];
+            }
         }
         __syncthreads();
         prefix |= pick[0] << shift;
-        known |= 255u << shift;
+        known |= digit << shift;
         left = (int)pick[1];
+        all = left == (int)pick[2];
+        __syncthreads();
+        if (shift == 0) break;
+    }
+    if (all) {  // every key from the prefix on, whatever its other bits
+        prefix -= 1;
+        left = 0;
     }
     // Positions in ascending order: all keys above, and the first `left` equal ones.
     // A thread has a run of keys; one scan over the threads' counts.
     const int per = (n + kSelThreads - 1) / kSelThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    int g = 0, e = 0;
-    for (int i = i0; i < i1; ++i) g += key[i] > prefix, e += key[i] == prefix;
-    unsigned long long x = (unsigned long long)e << 32 | (uint32_t)g;
+    int gt = 0, eq = 0;
+    uint32_t marks = 0;  // of the first 32 keys: those that are not below
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key[i];
+        gt += k > prefix, eq += k == prefix;
+        if (k >= prefix && i - i0 < 32) marks |= 1u << (i - i0);
+    }
+    unsigned long long x = (unsigned long long)eq << 32 | (uint32_t)gt;
     const unsigned long long own = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -217,16 +313,20 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
     if (lane == 31) warp_counts[warp] = x;
     __syncthreads();
     x -= own;
-    for (int w = 0; w < warp; ++w) x += warp_counts[w];
-    g = (int)(uint32_t)x, e = (int)(x >> 32);
-    for (int i = i0; i < i1; ++i) {
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w)
+        if (w < warp) x += warp_counts[w];
+    gt = (int)(uint32_t)x, eq = (int)(x >> 32);
+    auto put = [&](int i) {
         if (key[i] > prefix)
-            sel[g++ + min(e, left)] = i;
+            sel[gt++ + min(eq, left)] = i;
         else if (key[i] == prefix) {
-            if (e < left) sel[g + e] = i;
-            ++e;
+            if (eq < left) sel[gt + eq] = i;
+            ++eq;
         }
-    }
+    };
+    for (; marks; marks &= marks - 1) put(i0 + __ffs((int)marks) - 1);
+    for (int i = i0 + 32; i < i1; ++i) put(i);
 }
 
 cudaError_t launch_page_select(int D, const SelectParams &p, cudaStream_t stream) {
@@ -234,7 +334,7 @@ cudaError_t launch_page_select(int D, const SelectParams &p, cudaStream_t stream
     while (size < 8 && size * kSelShare < p.max_pages) size *= 2;
     void (*const f)(SelectParams) = D == 64 ? fa_page_select_kernel<64> : fa_page_select_kernel<128>;
     const size_t smem = p.max_pages * sizeof(uint32_t);
-    if (smem > 40 * 1024) {  // beyond what a kernel may have, beside its own arrays, without asking
+    if (smem > 32 * 1024) {  // beyond what a kernel may have, beside its own arrays, without asking
         const cudaError_t e = cudaFuncSetAttribute((const void *)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
