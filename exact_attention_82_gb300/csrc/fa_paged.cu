@@ -56,6 +56,13 @@ static __device__ int g_status_paged = 0;
 constexpr int kPgTile = 32;         // keys a tile; two halves of 16, each in one page
 constexpr int kPgFixed = 2;         // places of the line that an item's fixed cost takes
 constexpr int kPgMinShare = 36;     // places of a block: three tiles a warp
+// An item of an eighth of a share is not cut (16 sequences of 2000 to 16000 keys: 88 us
+// with half a share, whose blocks have up to one and a half of it, 80 us with an eighth or
+// less), nor is one of 8 places (256 sequences of 100 keys: 27 us without this, 23 us with
+// it).  What is not cut between warps must not be between blocks: else a warp's end
+// could be moved past its block's.
+constexpr int kPgSmall = 8;
+constexpr int kPgWhole = 8;
 constexpr int kPgMaxLen = 0x7fffff00;
 constexpr float kPgShift = 8.f;    // exponent of a weight at x = m
 constexpr float kPgMost = 15.f;    // and the largest one
@@ -238,7 +245,7 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start 
         __syncwarp();
         int share = (int)((uint32_t)(total + gridDim.x - 1) / gridDim.x);
         // With less work than the chip has room for, items of up to two least shares stay whole.
-        const int small = share <= kPgMinShare ? 2 * kPgMinShare : share / 2;
+        const int small = share <= kPgMinShare ? 2 * kPgMinShare : max(share / kPgSmall, kPgWhole);
         share = max(share, kPgMinShare);
         // The block's ends.  Which thread's entries hold them: a lane's twelve or eight sums,
         // then one of those.
@@ -269,7 +276,7 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start 
                     else
                         lo = mid + 1;
                 }
-                f = place_of<NR>(p, lo, lo ? sums[lo - 1] : 0, per, n, pos, part / 2);
+                f = place_of<NR>(p, lo, lo ? sums[lo - 1] : 0, per, n, pos, max(part / kPgSmall, kPgWhole));
             }
         }
         const int mine = __shfl_down_sync(0xffffffffu, f.pos, 1);
@@ -299,6 +306,9 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // four 8x8 tiles of 16-bit pairs, transposed: lane l's address is row l of the 32
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
@@ -438,12 +448,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
         nv_next = good ? min(16, next->len - key_next) : 0;
     };
     look_up();
-    // The batch being copied: each lane's half as a row of the cache, and what its
-    // consumer needs (first key, c's key scale or NaN, log2 of the value scale and its
-    // inverse).
+    // The batch being copied: each lane's half as a row of the cache.
     uint32_t row_now = 0, full_now = 0;
-    int ph_now = 0, nv_now = 0, n_now = 0, at_now = 0, stage_in = 0;
-    float4 meta_now = make_float4(0.f, 0.f, 0.f, 0.f);
+    int ph_now = 0, key_now = 0, nv_now = 0, n_now = 0, at_now = 0, stage_in = 0;
     const uint8_t *const k_lane = p.k_pages + lane * 16, *const v_lane = p.v_pages + lane * 16;
     const int r_lane = lane / C::CHUNKS;  // row of this lane's piece among those of one copy
     const uint32_t dst_lane = ring + r_lane * D + ((lane % C::CHUNKS) ^ C::swap(r_lane)) * 16;
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
             at_now = 0;
             n_now = n_next;
             if (n_now > 0) {
-                ph_now = ph_next;
+                ph_now = ph_next, key_now = key_next;
                 row_now = ((uint32_t)max(ph_now, 0) << p.page_log2) + (key_next & (page - 1));
                 nv_now = nv_next;
                 full_now = __ballot_sync(0xffffffffu, nv_now == 16);
@@ -485,19 +492,18 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                     }
                 }
             }
-            if (at_now == 0) {  // a new batch: its scales, and the next one's pages, while the copies run
-                float ks = p.k_scale[max(ph_now, 0)], vs = p.v_scale[max(ph_now, 0)];
-                if (ph_now < 0) {
-                    ks = __int_as_float(0x7fc00000), vs = 1.f;
+            if ((lane >> 1) == at_now) {  // what the tile's consumer needs: the first key and the page's scales
+                float *const meta = reinterpret_cast<float *>(meta_of + stage_in * 2 + (lane & 1));
+                meta[0] = __int_as_float(key_now);
+                if (ph_now >= 0) {
+                    cp_async4(smem_u32(meta + 1), p.k_scale + ph_now);
+                    cp_async4(smem_u32(meta + 2), p.v_scale + ph_now);
+                } else {
+                    meta[1] = __int_as_float(0x7fc00000), meta[2] = 1.f;
                     atomicExch(&g_status_paged, (int)FA_ERR_BAD_PAGE);
                 }
-                const int key = key_next;
-                look_up();
-                const int u = __float_as_int(vs);  // its logarithm, exact for powers of two
-                const float lv = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
-                meta_now = make_float4(__int_as_float(key), ks, lv, ex2_approx(-lv));
             }
-            if ((lane >> 1) == at_now) meta_of[stage_in * 2 + (lane & 1)] = meta_now;
+            if (at_now == 0) look_up();  // the next batch's pages, while the copies run
             ++at_now;
             stage_in = stage_in + 1 == C::ST ? 0 : stage_in + 1;
         }
@@ -596,9 +602,15 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 continue;
             }
             const uint32_t st = stage_out * C::STAGE_BYTES;
-            const float4 meta[2] = {meta_of[stage_out * 2], meta_of[stage_out * 2 + 1]};
+            float4 meta[2] = {meta_of[stage_out * 2], meta_of[stage_out * 2 + 1]};  // first key, scales
             const int key[2] = {__float_as_int(meta[0].x), __float_as_int(meta[1].x)};
             stage_out = stage_out + 1 == C::ST ? 0 : stage_out + 1;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // the value scale's logarithm, exact for powers of two, and its inverse
+                const int u = __float_as_int(meta[half].z);
+                meta[half].z = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
+                meta[half].w = ex2_approx(-meta[half].z);
+            }
 
             // ---- S^T = K Q^T: a half of 16 keys an MMA tile.  The order of d within the
             // contraction is free as long as Q's is the same: lane t takes whole 16-byte
