@@ -400,10 +400,13 @@ int fa_page_select(const void *q, const int *cu_q, const int *seq_lens, const in
  * A row that sees no key gets O = 0, LSE = -inf.  Keys a row does not see never
  * touch it, whatever their codes are (NaN included).  Scores and sums are fp32;
  * q and K enter the products exactly (q as bf16 scaled by a power of two to fp16:
- * a value below 2^-24 of its row's largest is rounded), the softmax weights are
- * rounded to fp16, O once to bf16.  Any number of query tokens a sequence is
- * taken; the kernel is made for a few (decode, drafts).  Deterministic; no atomics
- * on results.
+ * elements below 2^-17 of their row's largest are rounded, to steps of 2^-24 of it),
+ * the softmax weights are rounded to fp16, O once to bf16.  Any number of query
+ * tokens a sequence is taken; the kernel is made for a few (decode, drafts): 8 to 32
+ * rows (query tokens times heads of the group) share a pass over the keys.
+ * T * Hq < 2^31, and so is, at most, (T * Hq / Hkv / 8 + B) * Hkv times the 32-key
+ * tiles of a full table row, plus 3 (FA_ERR_BAD_SHAPE).  Deterministic; no atomics on
+ * results.  Lengths and tables must not change while the call runs.
  * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
  * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_BAD_SCALE, FA_ERR_WORKSPACE,
  * FA_ERR_ALIAS; FA_ERR_CUDA if a launch fails.

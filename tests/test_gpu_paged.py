@@ -177,6 +177,20 @@ def test_select_long_sequence():
         run_select(c, q, cu, d_cu, top, 1, 2)
 
 
+@pytest.mark.parametrize("width,G,D", [(300, 4, 64), (700, 16, 128), (2100, 3, 64)])
+def test_select_wide_tables(width, G, D):
+    """Tables that several blocks score: long and short sequences beside one another, some shorter than
+    top_k, more query rows than are scored at a time."""
+    lens = [16 * width, 1, 0, 16 * 40, 16 * 60 + 5, 16 * (width - 13) + 3, 16 * 259]
+    c = pu.Cache(lens, 2, 16, D, seed=width, extra_cols=0)
+    q, cu, d_cu = pu.queries([3, 1, 1, 1, 0, 2, 4], 2 * G, D, seed=G, pad=1)
+    run_select(c, q, cu, d_cu, 50, 2, 3)
+    c.mean[:, :, :] = c.mean[:1, :1]
+    c.ms[:] = np.linspace(0.5, 2, 5).astype(np.float32)[np.arange(c.num_pages) % 5, None]   # five values: many ties
+    c.d_mean, c.d_ms = torch.from_numpy(c.mean).cuda(), torch.from_numpy(c.ms).cuda()
+    run_select(c, q, cu, d_cu, 64, 0, 0)
+
+
 def test_select_pages_outside_the_cache_come_last():
     c = pu.Cache([800], 1, 16, 64, seed=5)
     q, cu, d_cu = pu.queries([1], 2, 64, seed=6)
@@ -239,6 +253,52 @@ def test_attend_many_sequences():
     c = pu.Cache(lens, 1, 16, 64, seed=1)
     q, cu, d_cu = pu.queries(rng.integers(0, 3, size=700).tolist(), 2, 64, seed=2, pad=9)
     run_attend(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_attend_random_batches(seed):
+    """Batches of any mixture of lengths, tokens and heads: how the work is cut must not show."""
+    rng = np.random.default_rng(1000 + seed)
+    B = int(rng.choice([1, 2, 3, 17, 60, 150]))
+    top = int(rng.choice([20, 120, 700, 4000 if B < 10 else 700]))
+    Hkv, G, D = int(rng.choice([1, 2, 3])), int(rng.choice([1, 2, 4, 7, 8, 16])), int(rng.choice([64, 128]))
+    page = int(rng.choice(fa.FA_PAGE_SIZES))
+    lens = [int(rng.integers(0, 1 + (top if rng.random() < 0.3 else top // 8))) for _ in range(B)]
+    counts = [int(rng.choice([0, 1, 1, 1, 2, 5])) for _ in range(B)]
+    c = pu.Cache(lens, Hkv, page, D, seed=seed)
+    q, cu, d_cu = pu.queries(counts, Hkv * G, D, seed=seed, pad=int(rng.integers(0, 4)))
+    run_attend(c, q, cu, d_cu, what=f"{B} {top} {Hkv} {G} {D} {page}")
+
+
+def test_attend_heads_of_short_sequences():
+    """Thousands of items of a few tiles each."""
+    rng = np.random.default_rng(5)
+    for hi in (33, 97, 260):
+        lens = rng.integers(1, hi, size=180).tolist()
+        c = pu.Cache(lens, 8, 16, 64, seed=hi)
+        q, cu, d_cu = pu.queries([1] * 180, 8, 64, seed=hi)
+        run_attend(c, q, cu, d_cu, what=str(hi))
+
+
+def test_attend_types_streams_and_workspaces():
+    """Codes as float8 tensors, an exact workspace that held other things, streams as objects and addresses."""
+    c = pu.Cache([900, 40, 2000], 2, 32, 128, seed=8)
+    q, cu, d_cu = pu.queries([1, 2, 1], 8, 128, seed=8)
+    o, lse = run_attend(c, q, cu, d_cu)
+    T, Hq, _ = q.shape
+    ws = torch.full((fa.fa_fwd_paged_workspace_bytes(3, T, Hq, 2, 128),), 255, dtype=torch.uint8, device="cuda")
+    f8 = [t.view(torch.float8_e4m3fn) for t in c.pages[:2]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side, side.cuda_stream, 0):
+        o2, l2 = fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *f8, *c.pages[2:], workspace=ws, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    before = [t.clone() for t in c.pages]
+    x = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+    fa.fa_kv_append(x, x, i32([-1]), *f8, *c.pages[2:], stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, c.pages))
 
 
 @pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
