@@ -222,10 +222,15 @@ struct AppendCfg {
     static constexpr int TPT = D / 8;                                 // threads a token
     static constexpr int ROWS = 32 * TEAM / TPT;                      // tokens a pass
     static constexpr int PASSES = PAGE / ROWS;
+    // Blocks an SM that the registers are held to.  A team waits for memory three times
+    // (slots, rows, and to be written), so more of them side by side is faster, until they
+    // spill: a 16384-token prompt with 7, 8, 9 and 10 blocks 25.1, 23.2, 22.3 and 22.7 us, ragged
+    // prompts at 16 rows a page, D = 64, with 9, 10 and 12 blocks 19.1, 16.4 and 18.0 us.
+    static constexpr int BLOCKS = (PASSES <= 4 ? 10 : 9) * 128 / THREADS;
 };
 
 template <int D, int PAGE>
-__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
+__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE>::BLOCKS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
     using C = AppendCfg<D, PAGE>;
     grid_wait();
     __shared__ int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
