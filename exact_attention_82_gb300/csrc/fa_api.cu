@@ -496,9 +496,13 @@ int page_log2_of(int page_size) {
     return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : page_size == 128 ? 7 : -1;
 }
 
+// Tokens, free pages and chosen pages of a call: kernels count them in int, in steps
+// of up to 2^18 past the end.
+constexpr int kMostCounted = 1 << 30;
+
 // What the cache's entry points share; FA_OK when the sizes are in range.
 int check_cache(int B, int T, int Hkv, int D, int max_pages, int num_pages, int page_size) {
-    if (B < 1 || B > 8192 || T < 1 || Hkv < 1 || Hkv > 1024 || max_pages < 1 || num_pages < 1)
+    if (B < 1 || B > 8192 || T < 1 || T > kMostCounted || Hkv < 1 || Hkv > 1024 || max_pages < 1 || num_pages < 1)
         return FA_ERR_BAD_SHAPE;
     if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED_D;
     if (page_log2_of(page_size) < 0) return FA_ERR_BAD_PAGE;
@@ -526,7 +530,7 @@ extern "C" int fa_kv_plan(const int *cached_lens, const int *new_lens, const int
         if (!ptr) return FA_ERR_NULLPTR;
     for (const void *ptr : ptrs)
         if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
-    if (num_free < 1) return FA_ERR_BAD_SHAPE;
+    if (num_free < 1 || num_free > kMostCounted) return FA_ERR_BAD_SHAPE;
     const int st = check_cache(B, T, 1, 64, max_pages, num_pages, page_size);
     if (st != FA_OK) return st;
     const Span outs[5] = {{block_table, (size_t)B * max_pages * 4}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
@@ -604,7 +608,7 @@ extern "C" int fa_page_select(const void *q, const int *cu_q, const int *seq_len
     const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
     if (st != FA_OK) return st;
     if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || !stride_ok(q_stride, Hq, D) || max_pages > fa::kSelectMaxPages ||
-        top_k < 1 || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > top_k)
+        top_k < 1 || top_k > kMostCounted || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > top_k)
         return FA_ERR_BAD_SHAPE;
     const Span outs[2] = {{sel, (size_t)B * Hkv * top_k * 4}, {sel_count, (size_t)B * Hkv * 4}};
     const Span ins[6] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},

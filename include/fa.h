@@ -293,7 +293,7 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * D is 64 or 128; q, k and v may be strided over tokens (strides in elements,
  * multiples of 8, each token's heads contiguous).  Tensors of codes and bf16 are
  * 16-byte aligned, int32 and fp32 arrays 4-byte aligned (FA_ERR_MISALIGNED).
- * num_pages * page_size and num_pages * Hkv < 2^31, B <= 8192, Hkv <= 1024, Hq a multiple of Hkv.
+ * num_pages * page_size and num_pages * Hkv < 2^31, B <= 8192, T <= 2^30, Hkv <= 1024, Hq a multiple of Hkv.
  * These operations have no counterpart in the pages.
  */
 
@@ -322,7 +322,7 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * q, k and v stay counted in cu_q.  A slot whose page is outside the cache is -1.
  * Outputs may not overlap inputs or one another (free_left is not free_count).
  * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE (B, T, max_pages,
- * num_free or num_pages < 1, or out of range), FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
+ * num_free or num_pages < 1, or out of range: num_free <= 2^30), FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
  */
 int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_count,
                int *block_table, int *cu_q, int *seq_lens, int *slot_map, int *free_left, int B, int T,
@@ -371,7 +371,7 @@ int fa_kv_append(const void *k, const void *v, const int *slot_map, void *k_page
  * the sum in integers, so that it is the same whatever its order.  The first
  * keep_first and the last keep_last pages come before all others, then higher
  * scores, and the lower position among equals; pages outside the cache last.
- * top_k >= 1, keep_first, keep_last >= 0, keep_first + keep_last <= top_k.
+ * 1 <= top_k <= 2^30, keep_first, keep_last >= 0, keep_first + keep_last <= top_k.
  * max_pages <= 49152.
  * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
  * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_ALIAS.

@@ -79,6 +79,15 @@ def test_bad_shapes(call, kw):
     assert call(**kw) == fa.FA_ERR_BAD_SHAPE
 
 
+@pytest.mark.parametrize("call,name", [(plan, "T"), (plan, "num_free"), (append, "T"), (select, "T"), (select, "top"),
+                                       (attend, "T")])
+def test_counts_that_an_int_cannot_step_past(call, name):
+    """A loop that steps past the end of 2^31 - 1 items would go on at negative indexes."""
+    kw = dict(Hq=1, Hkv=1) if call in (select, attend) else {}
+    for n in (2 ** 31 - 1, 2 ** 31 - 2 ** 17, 2 ** 30 + 1):
+        assert call(**{**kw, name: n}) == fa.FA_ERR_BAD_SHAPE
+
+
 @pytest.mark.parametrize("scale", [float("nan"), float("inf"), 0.0, -0.5, 3e38])
 def test_attend_scale(scale):
     assert attend(scale=scale) == fa.FA_ERR_BAD_SCALE
