@@ -151,10 +151,11 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
                 amax = fmaxf(amax, fabsf(x[i]));
             }
             amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-            const float inv = amax > 0.f ? 127.f / amax : 0.f;
+            // 127 / amax is past the largest float below 2^-121: such rows are scaled, exactly
+            const float up = amax < 0x1p-100f ? 0x1p100f : 1.f, inv = amax > 0.f ? 127.f / (amax * up) : 0.f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
-                reinterpret_cast<int8_t *>(q8[r])[lane * (D / 32) + i] = (int8_t)__float2int_rn(x[i] * inv);
+                reinterpret_cast<int8_t *>(q8[r])[lane * (D / 32) + i] = (int8_t)__float2int_rn(x[i] * up * inv);
             if (lane == 0) qs[r] = amax / 127.f;
         }
         __syncthreads();

@@ -200,6 +200,27 @@ def test_select_pages_outside_the_cache_come_last():
     assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
 
 
+def test_select_tiny_queries():
+    """Queries down to bf16's smallest numbers are rounded like others: 127 / max|q| is past the largest float
+    below 2^-121.  The pages' scores lie in powers of two apart, so that their 32-bit products (which are
+    subnormal, with 10 bits or more) keep the order."""
+    c = pu.Cache([640], 1, 16, 64, seed=7)
+    rng = np.random.default_rng(8)
+    c.mean[:] = rng.integers(64, 128, size=c.mean.shape[:2])[..., None] * rng.choice([-1, 1], size=64)
+    c.ms[:, 0] = np.exp2(rng.permutation(c.num_pages)).astype(np.float32)
+    c.d_mean, c.d_ms = torch.from_numpy(c.mean).cuda(), torch.from_numpy(c.ms).cuda()
+    sign = torch.from_numpy(np.sign(c.mean[0, 0]).astype(np.float32)).cuda()
+    want = None
+    for e in (0, -100, -120, -121, -122, -126, -130, -133):
+        q = (sign * 2.0 ** e).to(torch.bfloat16).view(1, 1, 64).expand(1, 2, 64).contiguous()
+        sel, n = fa.fa_page_select(q, i32([0, 1]), c.d_lens, c.d_table, c.d_mean, c.d_ms, 16, 9)
+        assert int(n) == 9
+        want = sel if want is None else want
+        assert torch.equal(sel, want), e
+    ref = pu.select(pu.f64(sign.view(1, 1, 64).expand(1, 2, 64)), np.array([0, 1]), c.lens, c.table, c.mean, c.ms, 16, 9, 1, 1)
+    assert np.array_equal(want.cpu().numpy(), ref[0])
+
+
 # ------------------------------------------------------------------ attend
 def run_attend(c, q, cu, d_cu, sel=None, count=None, scale=None, what="", **kw):
     T, Hq, D = q.shape
