@@ -116,14 +116,16 @@ PyObject *call(Py_ssize_t given, Py_ssize_t wanted, F f) {
     return nullptr;
 }
 
-// The C call without the interpreter's lock, as ctypes makes its calls.
+// The C call without the interpreter's lock, as ctypes makes its calls.  The lock is
+// taken back by a destructor: a tensor without storage throws when it is asked for
+// its address, and the exception has to leave with the lock held.
 template <class F>
 int unlocked(F f) {
-    int rc;
-    Py_BEGIN_ALLOW_THREADS;
-    rc = f();
-    Py_END_ALLOW_THREADS;
-    return rc;
+    struct Unlock {
+        PyThreadState *const state = PyEval_SaveThread();
+        ~Unlock() { PyEval_RestoreThread(state); }
+    } unlock;
+    return f();
 }
 
 // cached_lens, new_lens, free_pages, free_count, block_table, num_pages, page_size, cu_q, seq_lens, slot_map, free_left, stream

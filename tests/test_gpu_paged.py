@@ -569,3 +569,27 @@ def test_wrappers_check_their_tensors():
     with pytest.raises(fa.FAError) as e:
         fa.fa_fwd_paged(**{**ok, "q": torch.zeros(1, 3, 64, dtype=torch.bfloat16, device="cuda")})
     assert e.value.status == fa.FA_ERR_BAD_SHAPE
+
+
+def test_tensors_without_storage_are_refused():
+    """A tensor that has no address raises where it is asked for it; the interpreter goes on."""
+    class NoStorage(torch.Tensor):
+        @staticmethod
+        def __new__(cls, like):
+            return torch.Tensor._make_wrapper_subclass(cls, like.shape, dtype=like.dtype, device=like.device)
+
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise NotImplementedError(func)
+
+    c = pu.Cache([40], 2, 16, 64, seed=1)
+    q, cu, d_cu = pu.queries([1], 4, 64, seed=1)
+    for name in ("q", "seq_lens", "k_pages", "o"):
+        a = dict(q=q, cu_q=d_cu, seq_lens=c.d_lens, block_table=c.d_table, k_pages=c.d_kc, v_pages=c.d_vc, k_scale=c.d_ks,
+                 v_scale=c.d_vs, o=torch.empty_like(q), lse=torch.empty(q.shape[:2], device="cuda"))
+        a[name] = NoStorage(a[name])
+        with pytest.raises((RuntimeError, ValueError, NotImplementedError)):
+            fa.fa_fwd_paged(**a)
+    with pytest.raises((RuntimeError, ValueError, NotImplementedError)):
+        fa.fa_kv_append(NoStorage(q[:, :2]), q[:, :2], i32([0]), *c.pages)
+    run_attend(c, q, cu, d_cu)
