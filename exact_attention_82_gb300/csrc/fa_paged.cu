@@ -76,9 +76,9 @@ struct PgCfg {
     static constexpr int WARPS = NT == 1 ? 12 : 8;           // one block an SM
     static constexpr int THREADS = 32 * WARPS;
     // Beside 32 rows the registers are full of sums, and the query fragments lie in shared
-    // memory, each lane's apart (32 KB of the 192; the ring has the rest).
+    // memory, each lane's apart (D / 2 KB of about 200; the ring has the rest).
     static constexpr bool Q_SHARED = NT > 2;
-    static constexpr int ST = D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 4 : NT == 2 ? 6 : 5);  // stages a warp
+    static constexpr int ST = D == 128 ? (NT == 2 ? 3 : 2) : (NT == 1 ? 4 : NT == 2 ? 6 : 5);  // stages a warp
     static constexpr int OFF_META = WARPS * ST * STAGE_BYTES;  // 2 float4 a stage
     static constexpr int OFF_WORK = OFF_META + WARPS * ST * 2 * 16;
     static constexpr int WORKS = 8;                          // items looked up ahead: ST + 1 at most
@@ -86,13 +86,15 @@ struct PgCfg {
     static constexpr int OFF_Q = (OFF_SUMS + THREADS * 4 + 127) / 128 * 128;
     static constexpr int SMEM = OFF_Q + (Q_SHARED ? WARPS * 8 * NT * D * 2 : 0);
     // Where a 16-byte piece of a row lies: pieces are swapped within 128 bytes so that
-    // eight rows' same piece (ldmatrix) falls into different banks.
-    static __device__ __forceinline__ int swap(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
-    // The key of MMA row g of a half: with bits 0 and 2 of g exchanged, two neighbouring
-    // lanes' rows (D = 128) fall into different banks in 16-byte loads too.
-    static __device__ __forceinline__ int key_of(int g) {
-        return D == 128 ? (g & 2) | ((g & 1) << 2) | (g >> 2) : g;
+    // eight rows' same piece (ldmatrix) falls into different banks, and so do pieces 0 to 3
+    // of two neighbouring rows (16-byte loads).
+    static __device__ __forceinline__ int swap(int row) {
+        return D == 128 ? (row & 2) | ((row & 1) << 2) | ((row >> 2) & 1) : (row >> 1) & 3;
     }
+    // The key of MMA row g of a half; row g + 8 has the key 2 further.  In this order the
+    // weights that the transposition leaves a lane are those of the four keys 4t .. 4t+3,
+    // whose values ldmatrix leaves it in one register.
+    static __device__ __forceinline__ int key_of(int g) { return 4 * (g >> 1) + (g & 1); }
 };
 
 // A place in the line of tiles (32 bits: the caller has checked that they do).
@@ -310,9 +312,10 @@ __device__ __forceinline__ void cp_wait() {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// four 8x8 tiles of 16-bit pairs, transposed: lane l's address is row l of the 32
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+// two 16x16 tiles of bytes, transposed: lane l's address is row l of the 32.  Of each tile
+// the lane gets bytes 4t .. 4t+3 of (transposed) rows g and g + 8.
+__device__ __forceinline__ void ldmatrix_b8_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
@@ -321,6 +324,10 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
+}
+// one such tile: lane l's address is row l of the 16
+__device__ __forceinline__ void ldmatrix_b8_trans(uint32_t addr, uint32_t (&r)[2]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
 }
 // two e4m3 codes -> two fp16
 __device__ __forceinline__ uint32_t codes_f16x2(uint32_t two) {
@@ -331,7 +338,7 @@ __device__ __forceinline__ uint32_t codes_f16x2(uint32_t two) {
 // c (16 x 8, fp32) += a (16 x 16, fp16) b (16 x 8, fp16)
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -382,6 +389,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     using C = PgCfg<D, NT>;
     constexpr int NR = 8 * NT;
     constexpr int KG = D / 64;  // groups of four 16-byte pieces of a row
+    // Halves of a tile at a time: one where the registers are full of sums.
+    constexpr int HB = D == 128 && NT == 4 ? 1 : 2;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ Start start[C::WARPS];
     __shared__ int flag_of[C::WARPS];
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     const int r_lane = lane / C::CHUNKS;  // row of this lane's piece among those of one copy
     const uint32_t dst_lane = ring + r_lane * D + ((lane % C::CHUNKS) ^ C::swap(r_lane)) * 16;
     constexpr int PER = C::HALF_BYTES / 512;           // copies a half
-    constexpr uint32_t ODD = D == 128 ? 64u : 0u;      // every other copy's rows are 4 further
+    constexpr uint32_t ODD = D == 128 ? 16u : 0u;      // every other copy's rows are 4 further
     auto issue = [&]() {
         if (at_now == n_now) {
             at_now = 0;
@@ -512,7 +521,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     // where this lane reads: K rows by 16-byte loads, V rows by ldmatrix
     const int gk = C::key_of(g);
     const uint32_t k_read = ring + gk * D + (t ^ C::swap(gk)) * 16;
-    const int v_row = (lane & 24) + C::key_of(lane & 7);
+    constexpr uint32_t TWO = D == 128 ? 32u : 16u;  // what two rows further changes of where a piece lies
+    const int v_row = HB == 2 ? lane : lane & 15;
     const uint32_t v_read = ring + 2 * C::HALF_BYTES + v_row * D + C::swap(v_row) * 16;
     int stage_out = 0;
 
@@ -602,61 +612,54 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 continue;
             }
             const uint32_t st = stage_out * C::STAGE_BYTES;
-            float4 meta[2] = {meta_of[stage_out * 2], meta_of[stage_out * 2 + 1]};  // first key, scales
-            const int key[2] = {__float_as_int(meta[0].x), __float_as_int(meta[1].x)};
+            const float4 *const stage_meta = meta_of + stage_out * 2;
             stage_out = stage_out + 1 == C::ST ? 0 : stage_out + 1;
+#pragma unroll 1
+            for (int h0 = 0; h0 < 2; h0 += HB) {
+                float4 meta[HB];  // first key, scales
+                int key[HB], key_max = 0;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // the value scale's logarithm, exact for powers of two, and its inverse
-                const int u = __float_as_int(meta[half].z);
-                meta[half].z = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
-                meta[half].w = ex2_approx(-meta[half].z);
-            }
+                for (int half = 0; half < HB; ++half) {
+                    meta[half] = stage_meta[h0 + half];
+                    key[half] = __float_as_int(meta[half].x);
+                    key_max = max(key_max, key[half]);
+                }
+#pragma unroll
+                for (int half = 0; half < HB; ++half) {  // the value scale's logarithm, exact for powers of two, and its inverse
+                    const int u = __float_as_int(meta[half].z);
+                    meta[half].z = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
+                    meta[half].w = ex2_approx(-meta[half].z);
+                }
 
-            // ---- S^T = K Q^T: a half of 16 keys an MMA tile.  The order of d within the
-            // contraction is free as long as Q's is the same: lane t takes whole 16-byte
-            // pieces t and t + 4 of its keys' rows, four MMAs' worth each.
-            float sc[2][NT][4];
+                // ---- S^T = K Q^T: a half of 16 keys an MMA tile.  The order of d within the
+                // contraction is free as long as Q's is the same: lane t takes whole 16-byte
+                // pieces t and t + 4 of its keys' rows, four MMAs' worth each.
+                float sc[HB][NT][4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+                for (int half = 0; half < HB; ++half)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sc[half][nt][j] = 0.f;
-            if (!C::Q_SHARED) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int kg = 0; kg < KG; ++kg) {
-                        const uint32_t at = ((k_read + st) ^ (kg * 64)) + half * C::HALF_BYTES;
-                        uint32_t a[4], b8[4];
-                        ld_shared_v4(at, a[0], a[1], a[2], a[3]);
-                        ld_shared_v4(at + 8 * D, b8[0], b8[1], b8[2], b8[3]);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t a0 = codes_f16x2(a[w]), a1 = codes_f16x2(b8[w]);
-                            const uint32_t a2 = codes_f16x2(a[w] >> 16), a3 = codes_f16x2(b8[w] >> 16);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(sc[half][nt], a0, a1, a2, a3, qf[C::Q_SHARED ? 0 : nt][kg][w][0], qf[C::Q_SHARED ? 0 : nt][kg][w][1]);
-                        }
-                    }
-            } else {  // both halves together, so that a fragment of Q is read once a tile
+                        for (int j = 0; j < 4; ++j) sc[half][nt][j] = 0.f;
+                // Both halves' MMAs take turns: one that adds to the sums of another waits for it.
 #pragma unroll
                 for (int kg = 0; kg < KG; ++kg) {
-                    uint32_t a[2][4], b8[2][4];
+                    uint32_t a[HB][4], b8[HB][4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t at = ((k_read + st) ^ (kg * 64)) + half * C::HALF_BYTES;
+                    for (int half = 0; half < HB; ++half) {
+                        const uint32_t at = ((k_read + st) ^ (kg * 64)) + (h0 + half) * C::HALF_BYTES;
                         ld_shared_v4(at, a[half][0], a[half][1], a[half][2], a[half][3]);
-                        ld_shared_v4(at + 8 * D, b8[half][0], b8[half][1], b8[half][2], b8[half][3]);
+                        ld_shared_v4((at ^ TWO) + 2 * D, b8[half][0], b8[half][1], b8[half][2], b8[half][3]);
                     }
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         uint2 q[NT];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) q[nt] = q_sm[((kg * 4 + w) * NT + nt) * 32];
+                        for (int nt = 0; nt < NT; ++nt)
+                            q[nt] = C::Q_SHARED ? q_sm[((kg * 4 + w) * NT + nt) * 32]
+                                                : make_uint2(qf[C::Q_SHARED ? 0 : nt][kg][w][0], qf[C::Q_SHARED ? 0 : nt][kg][w][1]);
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
+                        for (int half = 0; half < HB; ++half) {
                             const uint32_t a0 = codes_f16x2(a[half][w]), a1 = codes_f16x2(b8[half][w]);
                             const uint32_t a2 = codes_f16x2(a[half][w] >> 16), a3 = codes_f16x2(b8[half][w] >> 16);
 #pragma unroll
@@ -664,126 +667,146 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         }
                     }
                 }
-            }
-            // ---- exponents of the weights, against the maximum in use
-            const bool edge = max(key[0], key[1]) + 16 > lim_min;  // some row does not see some key
-            float y[2][NT][4], top = kPgNone;
-            auto exponents = [&](int half, int nt, int j, float off) {
-                float x = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y, meta[half].z + off);
-                if (edge && key[half] + gk + (j >> 1) * 8 >= lim[nt][j & 1]) x = -INFINITY;
-                return x;
-            };
-            if (!edge) {
+                // ---- exponents of the weights, against the maximum in use
+                const bool edge = key_max + 16 > lim_min;  // some row does not see some key
+                float y[HB][NT][4], top = kPgNone;
+                auto exponents = [&](int half, int nt, int j, float off) {
+                    float x = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y, meta[half].z + off);
+                    if (edge && key[half] + gk + (j >> 1) * 2 >= lim[nt][j & 1]) x = -INFINITY;
+                    return x;
+                };
+                if (!edge) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            y[half][nt][j] = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y,
-                                                  meta[half].z + (kPgShift - m[nt][j & 1]));
-                            top = fmaxf(top, y[half][nt][j]);
-                        }
-            }
-            if (__any_sync(0xffffffffu, edge || top > kPgMost)) {
-                // a new maximum: the sums so far are scaled to it
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float x = kPgNone;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            x = fmaxf(x, fmaxf(exponents(half, nt, j, 0.f), exponents(half, nt, j + 2, 0.f)));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        x = fmaxf(x, m[nt][j]);
-                        const float f = ex2_approx(m[nt][j] - x);
-                        m[nt][j] = x;
-                        l[nt][j] *= f;
-#pragma unroll
-                        for (int c = 0; c < C::CHUNKS; ++c) acc[c][nt][j] *= f, acc[c][nt][j + 2] *= f;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            y[half][nt][j] = exponents(half, nt, j, kPgShift - x);
-                            y[half][nt][j + 2] = exponents(half, nt, j + 2, kPgShift - x);
-                        }
-                    }
-            }
-            // ---- weights, and their transpose as the B operand (keys x rows)
-            uint32_t wf[2][NT][2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        w[j] = ex2_approx(y[half][nt][j]);
-                        l[nt][j & 1] = fmaf(w[j], meta[half].w, l[nt][j & 1]);
-                    }
-                    wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
-                    wf[half][nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
-                }
-            // ---- O^T += V^T W^T.  A pair of bytes is one 16-bit element for ldmatrix, so
-            // a transposed tile holds d = 2g, 2g+1 of two keys in a register; their bytes
-            // are sorted by d before the conversion.
-            auto accumulate = [&](auto keep, auto settle) {
-#pragma unroll
-                for (int c = 0; c < C::CHUNKS; ++c) {
-                    float was[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) was[nt][j] = acc[c][nt][j];
-                    uint32_t r[4];
-                    ldmatrix_x4_trans((v_read + st) ^ (c * 16), r);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t lo = __byte_perm(keep(r[2 * half], half, 0), 0, 0x3120);
-                        const uint32_t hi = __byte_perm(keep(r[2 * half + 1], half, 1), 0, 0x3120);
-                        const uint32_t a0 = codes_f16x2(lo), a1 = codes_f16x2(lo >> 16);
-                        const uint32_t a2 = codes_f16x2(hi), a3 = codes_f16x2(hi >> 16);
+                    for (int half = 0; half < HB; ++half)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(acc[c][nt], a0, a1, a2, a3, wf[half][nt][0], wf[half][nt][1]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                y[half][nt][j] = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y,
+                                                      meta[half].z + (kPgShift - m[nt][j & 1]));
+                                top = fmaxf(top, y[half][nt][j]);
+                            }
+                }
+                if (__any_sync(0xffffffffu, edge || top > kPgMost)) {
+                    // a new maximum: the sums so far are scaled to it
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float x = kPgNone;
+#pragma unroll
+                            for (int half = 0; half < HB; ++half)
+                                x = fmaxf(x, fmaxf(exponents(half, nt, j, 0.f), exponents(half, nt, j + 2, 0.f)));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, m[nt][j]);
+                            const float f = ex2_approx(m[nt][j] - x);
+                            m[nt][j] = x;
+                            l[nt][j] *= f;
+#pragma unroll
+                            for (int c = 0; c < C::CHUNKS; ++c) acc[c][nt][j] *= f, acc[c][nt][j + 2] *= f;
+#pragma unroll
+                            for (int half = 0; half < HB; ++half) {
+                                y[half][nt][j] = exponents(half, nt, j, kPgShift - x);
+                                y[half][nt][j + 2] = exponents(half, nt, j + 2, kPgShift - x);
+                            }
+                        }
+                }
+                // ---- weights, and their transpose as the B operand (keys x rows)
+                uint32_t wf[HB][NT][2];
+#pragma unroll
+                for (int half = 0; half < HB; ++half)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            w[j] = ex2_approx(y[half][nt][j]);
+                            l[nt][j & 1] = fmaf(w[j], meta[half].w, l[nt][j & 1]);
+                        }
+                        wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                        wf[half][nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
                     }
+                // ---- O^T += V^T W^T: a lane has the rows (of V^T) g and g + 8 of each tile of 16,
+                // four keys in a register.
+                auto accumulate = [&](auto keep, auto settle) {
+                    constexpr int CG = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // tiles whose MMAs take turns
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int c0 = 0; c0 < C::CHUNKS; c0 += CG) {
+                        uint32_t r[CG][2 * HB];
+                        float was[CG][NT][4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[c][nt][j] = settle(acc[c][nt][j], was[nt][j], nt, j & 1);
-                }
-            };
-            if (!edge || lim_min >= it->len) {
-                accumulate([](uint32_t r, int, int) { return r; }, [](float now, float, int, int) { return now; });
-            } else {
-                // Some rows do not see all of these keys: a weight of 0 would still turn a
-                // NaN among the values into NaN, so the values that a token does not see
-                // are cleared, a token at a time, and only that token's rows take the
-                // result (only the last tiles of a sequence come here).
-                const int tok0 = it->row0 / p.G, tok1 = min(it->nq - 1, (it->row0 + NR - 1) / p.G);
+                        for (int c = 0; c < CG; ++c) {
+                            ldmatrix_b8_trans(((v_read + st) ^ ((c0 + c) * 16)) + h0 * C::HALF_BYTES, r[c]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) was[c][nt][j] = acc[c0 + c][nt][j];
+                        }
+#pragma unroll
+                        for (int half = 0; half < HB; ++half)
+#pragma unroll
+                            for (int c = 0; c < CG; ++c) {
+                                const uint32_t lo = keep(r[c][2 * half], half), hi = keep(r[c][2 * half + 1], half);
+                                const uint32_t a0 = codes_f16x2(lo), a1 = codes_f16x2(hi);
+                                const uint32_t a2 = codes_f16x2(lo >> 16), a3 = codes_f16x2(hi >> 16);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_f16(acc[c0 + c][nt], a0, a1, a2, a3, wf[half][nt][0], wf[half][nt][1]);
+                            }
+#pragma unroll
+                        for (int c = 0; c < CG; ++c)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) acc[c0 + c][nt][j] = settle(acc[c0 + c][nt][j], was[c][nt][j], nt, j & 1);
+                    }
+                };
+                if (!edge || lim_min >= it->len) {
+                    accumulate([](uint32_t r, int) { return r; }, [](float now, float, int, int) { return now; });
+                } else {
+                    // Some rows do not see all of these keys: a weight of 0 would still turn a
+                    // NaN among the values into NaN, so the values that a token does not see
+                    // are cleared, a token at a time, and only that token's rows take the
+                    // result (only the last tiles of a sequence come here).
+                    const int tok0 = it->row0 / p.G, tok1 = min(it->nq - 1, (it->row0 + NR - 1) / p.G);
 #pragma unroll 1
-                for (int tok = tok0; tok <= tok1; ++tok) {
-                    const int limit = it->len - it->nq + tok + 1;
-                    bool my[NT][2];
+                    for (int tok = tok0; tok <= tok1; ++tok) {
+                        const int limit = it->len - it->nq + tok + 1;
+                        bool my[NT][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) my[nt][j] = (it->row0 + nt * 8 + 2 * t + j) / p.G == tok;
-                    accumulate(
-                        [&](uint32_t r, int half, int up) {
-                            const int k = key[half] + up * 8;
-                            return r & ((k + C::key_of(2 * t) < limit ? 0xffffu : 0u) |
-                                        (k + C::key_of(2 * t + 1) < limit ? 0xffff0000u : 0u));
-                        },
-                        [&](float now, float before, int nt, int j) { return my[nt][j] ? now : before; });
+                            for (int j = 0; j < 2; ++j) my[nt][j] = (it->row0 + nt * 8 + 2 * t + j) / p.G == tok;
+                        accumulate(
+                            [&](uint32_t r, int half) {
+                                const int k = key[half] + 4 * t;  // the first of the lane's four keys
+                                return k + 4 <= limit ? r : k >= limit ? 0u : r & ((1u << 8 * (limit - k)) - 1);
+                            },
+                            [&](float now, float before, int nt, int j) { return my[nt][j] ? now : before; });
+                    }
                 }
+
             }
 
             if (++i < t1) continue;
 
-            // ---- an item ends here, or the warp's share of it
+            // ---- an item ends here, or the warp's share of it.  Neighbouring lanes exchange
+            // halves, so that each has two neighbouring elements: pair `pg` of a tile's 8.
+            const int pg = (g >> 1) + 4 * (g & 1);
+#pragma unroll
+            for (int c = 0; c < C::CHUNKS; ++c)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float got = __shfl_xor_sync(0xffffffffu, (g & 1) ? acc[c][nt][j] : acc[c][nt][j + 2], 4);
+                        if (g & 1)
+                            acc[c][nt][j] = got;
+                        else
+                            acc[c][nt][j + 2] = got;
+                    }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -856,7 +879,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         const int c = u / (2 * NT), r = (u / 2 % NT) * 8 + 2 * t + (u & 1);
                         float2 o = make_float2(0.f, 0.f);
                         if (closes) {
-                            o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + g];
+                            o = reinterpret_cast<const float2 *>(closing + r * D)[8 * c + pg];
                             o.x *= close_f[warp][r], o.y *= close_f[warp][r];
                         }
 #pragma unroll 4
@@ -866,9 +889,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         }
                         const float inv = inv_of[warp][r];
                         if (!whole)
-                            reinterpret_cast<float2 *>(part + r * D)[8 * c + g] = o;
+                            reinterpret_cast<float2 *>(part + r * D)[8 * c + pg] = o;
                         else if (it->row0 + r < it->rows)
-                            reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + out_row(p, it->q0, it->nq, it->h, it->row0 + r) * D)[8 * c + g] =
+                            reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + out_row(p, it->q0, it->nq, it->h, it->row0 + r) * D)[8 * c + pg] =
                                 pack_bf16x2(o.x * inv, o.y * inv);
                     }
                     return;
@@ -882,14 +905,14 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 for (int j = 0; j < 2; ++j) {
                     const int r = nt * 8 + 2 * t + j;
                     if (!whole) {
-                        float2 *const o = reinterpret_cast<float2 *>(part + r * D) + g;
+                        float2 *const o = reinterpret_cast<float2 *>(part + r * D) + pg;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
                         if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = l[nt][j];
                     } else if (it->row0 + r < it->rows) {
                         const float inv = l[nt][j] == 0.f ? 0.f : 1.f / l[nt][j];
                         const long long at = out_row(p, it->q0, it->nq, it->h, it->row0 + r);
-                        uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + g;
+                        uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + pg;
 #pragma unroll
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = pack_bf16x2(acc[c][nt][j] * inv, acc[c][nt][j + 2] * inv);
                         if (g == 0) p.lse[at] = lse_of(m[nt][j], l[nt][j]);
@@ -1022,7 +1045,7 @@ size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms) 
     (void)B, (void)T, (void)Hq, (void)Hkv;  // the same for all: what of the forms needs most
     if (D == 64)
         return std::max(workspace_of<64, 1>(num_sms), std::max(workspace_of<64, 2>(num_sms), workspace_of<64, 4>(num_sms)));
-    return std::max(workspace_of<128, 1>(num_sms), workspace_of<128, 2>(num_sms));
+    return std::max(workspace_of<128, 1>(num_sms), std::max(workspace_of<128, 2>(num_sms), workspace_of<128, 4>(num_sms)));
 }
 
 template <int D, int NT>
@@ -1037,11 +1060,13 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
 
 // Rows of an item: 8 or 16 while a sequence's query rows are no more (by the mean
 // number of its tokens, padding rounded off).  Beyond, 32 at D = 64 (16 sequences of 16384
-// keys, 32 rows: 97 us, 118 us in two items of 16) and 16 at D = 128, where the sums of 32
-// rows leave too few registers (8 sequences, 32 rows: 116 us, 100 us in two items).
+// keys, 32 rows: 95 us, 118 us in two items of 16).  At D = 128 the sums of 32 rows leave
+// few registers, and items of 32 pay from more than 32 rows on: 8 sequences of 16384 keys with
+// 64 rows take 154 us, 174 us in items of 16; with 32 rows 97 and 100 us; but 16 ragged ones
+// with 16 to 40 rows 89 and 77 us.
 static int item_rows(int D, const PagedParams &p) {
     const long long tokens = (2ll * p.T + p.B) / (2ll * p.B), rows = (tokens > 1 ? tokens : 1) * p.G;
-    return rows <= 8 ? 8 : rows <= 16 || D == 128 ? 16 : 32;
+    return rows <= 8 ? 8 : rows <= (D == 128 ? 32 : 16) ? 16 : 32;
 }
 
 bool paged_fits(int D, const PagedParams &p) {
@@ -1058,7 +1083,8 @@ cudaError_t launch_fwd_paged(int D, const PagedParams &params, int num_sms, cuda
     if (D == 64)
         return rows == 8 ? launch_paged<64, 1>(p, num_sms, stream)
                          : rows == 16 ? launch_paged<64, 2>(p, num_sms, stream) : launch_paged<64, 4>(p, num_sms, stream);
-    return rows == 8 ? launch_paged<128, 1>(p, num_sms, stream) : launch_paged<128, 2>(p, num_sms, stream);
+    return rows == 8 ? launch_paged<128, 1>(p, num_sms, stream)
+                     : rows == 16 ? launch_paged<128, 2>(p, num_sms, stream) : launch_paged<128, 4>(p, num_sms, stream);
 }
 
 cudaError_t paged_status_read_and_clear(int *out) {

@@ -258,6 +258,20 @@ def test_attend_several_tokens(D, G):
         run_attend(c, q, cu, d_cu)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,page", [(1, 64), (16, 16)])
+def test_attend_prompts(D, G, page):
+    """As many query rows as a prompt has: several passes over the keys, masked tiles in most of them."""
+    lens, counts = [130, 61, 300, 47], [130, 61, 90, 5]
+    c = pu.Cache(lens, 1, page, D, seed=D + G)
+    q, cu, d_cu = pu.queries(counts, G, D, seed=G, pad=2)
+    run_attend(c, q, cu, d_cu)
+    chosen = [1, 0] if page == 16 else [0]  # in any order
+    sel = np.full((4, 1, 3), -1, np.int32)
+    sel[:, 0, :len(chosen)] = chosen
+    run_attend(c, q, cu, d_cu, sel=sel, count=np.full((4, 1), len(chosen), np.int32))
+
+
 @pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
 def test_attend_long_and_ragged(page):
     lens = [5000, 1, 2500, 77, 9001]
@@ -357,6 +371,18 @@ def test_attend_masked_values_never_touch_a_row():
         c.d_kc, c.d_vc = torch.from_numpy(c.kc).cuda(), torch.from_numpy(c.vc).cuda()
         q, cu, d_cu = pu.queries(counts, 4, D, seed=D)
         run_attend(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_masked_values_beside_many_rows(D):
+    lens, counts = [40, 16, 129, 70], [3, 2, 4, 8]
+    c = pu.Cache(lens, 1, 32, D, seed=D)
+    for b, L in enumerate(lens):
+        t = L - 1 - b % 2
+        c.vc[c.table[b, t // 32], 0, t % 32, 5:9] = 0xFF
+    c.d_vc = torch.from_numpy(c.vc).cuda()
+    q, cu, d_cu = pu.queries(counts, 20, D, seed=D)
+    run_attend(c, q, cu, d_cu)
 
 
 def test_attend_peaky_and_uneven_scales():
