@@ -289,7 +289,10 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * a graph and replayed with other lengths.  What they hold is checked there:
  * lengths are clamped to what the table and T hold; a page or position outside
  * the cache is never read or written, sets FA_ERR_BAD_PAGE in the status word
- * (fa_device_status), and the rows that would have read it come out NaN.
+ * (fa_device_status), and the rows that would have read it come out NaN.  Where
+ * cu_q does not ascend, so that its tokens exceed what T says, fa_fwd_paged writes
+ * nothing and sets FA_ERR_BAD_SHAPE there, or rows are written more than once.
+ * None of what a call reads may change while it runs, lengths and tables above all.
  * D is 64 or 128; q, k and v may be strided over tokens (strides in elements,
  * multiples of 8, each token's heads contiguous).  Tensors of codes and bf16 are
  * 16-byte aligned, int32 and fp32 arrays 4-byte aligned (FA_ERR_MISALIGNED).
@@ -344,7 +347,8 @@ int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_page
  * are x / scale rounded to nearest even; +-inf become +-448, NaN stays NaN.
  * The mean is over the page's rows up to the run's last one:
  *   S_d = sum of codes (NaN as 0), A = max_d |S_d|,
- *   k_mean_d = rint(S_d * (127 / A)),  k_mean_scale = A * scale / (127 * rows).
+ *   k_mean_d = rint(S_d * (127 / A)),  k_mean_scale = A * scale / (127 * rows)
+ * (left to right in fp32: infinite where A * scale is).
  * Rows behind the run are left as they were.  A page may be in one run of a call
  * only; with more, what it holds afterwards is undefined.  A slot past the cache
  * is skipped and sets FA_ERR_BAD_PAGE in the status word.
@@ -406,7 +410,7 @@ int fa_page_select(const void *q, const int *cu_q, const int *seq_lens, const in
  * rows (query tokens times heads of the group) share a pass over the keys.
  * T * Hq < 2^31, and so is, at most, (T * Hq / Hkv / 8 + B) * Hkv times the 32-key
  * tiles of a full table row, plus 3 (FA_ERR_BAD_SHAPE).  Deterministic; no atomics on
- * results.  Lengths and tables must not change while the call runs.
+ * results.
  * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
  * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_BAD_SCALE, FA_ERR_WORKSPACE,
  * FA_ERR_ALIAS; FA_ERR_CUDA if a launch fails.
@@ -434,7 +438,8 @@ const char *fa_strerror(int status);
  * a wait that gives up records FA_ERR_TIMEOUT there (instead of hanging or
  * trapping) and the kernel winds down.  This call synchronises `stream`,
  * reads and resets the word on the current device, and returns FA_OK,
- * FA_ERR_TIMEOUT or FA_ERR_CUDA.  Meant for tests and debugging; it is the
+ * FA_ERR_TIMEOUT, FA_ERR_BAD_PAGE or FA_ERR_BAD_SHAPE (the paged cache's calls:
+ * contents of tables that they could not use), or FA_ERR_CUDA.  Meant for tests and debugging; it is the
  * only call here that synchronises.
  */
 int fa_device_status(void *stream);
