@@ -14,10 +14,14 @@
 // of the pages.  The products run on the tensor cores in integers (16 pages by 8 rows by
 // 32 elements an instruction; four products a lane and instruction took twice as long,
 // most of it to read the queries from shared memory).  The scores' bits are
-// written into the first block's shared memory, which finds the k-th largest by its bits,
-// eleven at a time from the highest, without sorting.  8 sequences of 16384 tokens, 8 of 32
-// heads, pages of 64: 6.4 us; one of 131072, pages of 32: 10.5 us, most of it the counting
-// of 4096 keys in one block.
+// written into the first block's shared memory, which finds the k-th largest without
+// sorting: counted in 2048 equal steps from the least score to the largest, it is among
+// the few of one step, and is the one that has the right number of those above it.  Where
+// that does not tell them apart (ties, infinities) it is found by its bits, eleven at a time.
+// (By bits alone, whose highest are alike, so that counts collide: 6.2 and 10.3 us for 5.8 and
+// 9.7.)  8 sequences of 16384 tokens, 8 of 32 heads, pages of 64: 5.8 us; one of 131072, 8 of
+// 64 heads, pages of 32: 9.7 us, a chain of latencies: lengths 0.9, queries 1.4, table and
+// means twice 2.9, barrier 0.6, the k-th largest 2.7, the list 1.4.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -32,12 +36,16 @@ static __device__ int g_status_page_select = 0;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelRows = 16;   // query rows scored at a time
+constexpr int kSelBins = 2048;
 constexpr int kSelShare = 256; // pages of the table that make another block of the cluster worth its while
 
 // Unsigned numbers in the order of the floats; -0 counts as 0.
 __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float float_of(uint32_t order) {
+    return __uint_as_float((order & 0x80000000u) ? order & 0x7fffffffu : ~order);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -69,15 +77,23 @@ __device__ __forceinline__ void store_cluster(uint32_t a, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ void min_cluster(uint32_t a, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void max_cluster(uint32_t a, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __grid_constant__ SelectParams p) {
     grid_wait();
     extern __shared__ uint32_t key[];  // [max_pages] the order of each page's score, in the first block
     __shared__ __align__(16) int q8[kSelRows][D / 4];
     __shared__ float qs[kSelRows];
-    __shared__ __align__(16) int hist[2048];
+    __shared__ __align__(16) int hist[kSelBins];
     __shared__ int warp_sums[kSelWarps];
-    __shared__ uint32_t pick[3];
+    __shared__ uint32_t pick[3], key_min, key_max;  // of the keys that are scores
+    __shared__ int listed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int h = blockIdx.y, b = blockIdx.z;
@@ -89,7 +105,10 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
     const long long bh = (long long)b * p.Hkv + h;
     int *const sel = p.sel + bh * p.top_k;
     if (rank == 0) {
-        if (tid == 0) p.sel_count[bh] = take;
+        if (tid == 0) {
+            p.sel_count[bh] = take;
+            key_min = 0xffffffffu, key_max = 0, listed = 0;
+        }
         for (int i = take + tid; i < p.top_k; i += kSelThreads) sel[i] = -1;
     }
     if (size > 1) cluster_arrive();      // this block's shared memory is there
@@ -106,6 +125,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
     const int chunk = (((n + (int)size - 1) / (int)size) + 15) & ~15, begin = min(n, (int)rank * chunk), end = min(n, begin + chunk);
     constexpr int KS = D / 32;  // instructions along a row
     bool waited = size == 1;
+    uint32_t k_min = 0xffffffffu, k_max = 0;
     for (int r0 = 0; r0 < rows; r0 += kSelRows) {
         // The first pages are asked for before the queries are rounded.  Lane t takes
         // 16-byte pieces t (and t + 4) of the mean keys of pages g and g + 8.
@@ -172,6 +192,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
                 for (int c = 0; c < 2; ++c) qf[nt][k][c] = q8[nt * 8 + g][D == 128 ? 4 * (t + 4 * c) + k : 4 * t + 2 * k + c];
             qscale[nt][0] = qs[nt * 8 + 2 * t], qscale[nt][1] = qs[nt * 8 + 2 * t + 1];
         }
+        k_min = 0xffffffffu, k_max = 0;  // (the last rows' stay)
         for (; i0 < end; i0 += 16 * kSelWarps) {
             uint32_t best[2] = {0, 0};
 #pragma unroll
@@ -210,6 +231,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
             if (t < 2 && i < end) {
                 if (i < p.keep_first || i >= n - p.keep_last) k = 0xffffffffu;
                 if (r0 > 0) k = max(k, key[i - begin]);  // this block's own copy: the maximum over the rows so far
+                if (k != 0xffffffffu && k != 0) k_min = min(k_min, k), k_max = max(k_max, k);
                 if (rank == 0 || r0 + kSelRows < rows)
                     key[i - begin] = k;
                 else
@@ -217,6 +239,11 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
             }
             if (i0 + 16 * kSelWarps < end) fetch(i0 + 16 * kSelWarps);
         }
+    }
+    k_min = __reduce_min_sync(0xffffffffu, k_min), k_max = __reduce_max_sync(0xffffffffu, k_max);
+    if (lane == 0 && k_max > 0) {
+        min_cluster(in_first_block(&key_min), k_min);
+        max_cluster(in_first_block(&key_max), k_max);
     }
     if (size > 1) {
         if (!waited) cluster_wait();
@@ -227,10 +254,88 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
     }
     if (rank != 0) return;
 
-    // the take-th largest key, eleven bits at a time from the top
-    uint32_t prefix = 0, known = 0;
-    int left = take;  // how many of the keys that agree with the prefix are taken
-    bool all = false; // whether all of them are
+    // Finds in which bin of `hist`, counted from the highest down, the left-th member is:
+    // pick = {the bin, how many of its members are taken, how many it has}.
+    auto find_bin = [&](int left) {
+        // thread t has bin 2047 - 4 t and the three below
+        const int4 c4 = *reinterpret_cast<const int4 *>(&hist[kSelBins - 4 - 4 * tid]);
+        const int c[4] = {c4.w, c4.z, c4.y, c4.x}, mine = c[0] + c[1] + c[2] + c[3];
+        int s = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        if (lane == 31) warp_sums[warp] = s;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w)
+            if (w < warp) s += warp_sums[w];
+        int before = s - mine;
+        if (before < left && s >= left) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before < left && before + c[j] >= left) {
+                    pick[0] = kSelBins - 1 - 4 * tid - j;
+                    pick[1] = left - before;
+                    pick[2] = c[j];
+                }
+                before += c[j];
+            }
+        }
+        __syncthreads();
+    };
+    static_assert(kSelBins == 4 * kSelThreads, "");
+
+    // The take-th largest key, `prefix`, and how many of those equal to it are taken, `left`.
+    uint32_t prefix = 0;
+    int left = take;
+    const float low = float_of(key_min), range = float_of(key_max) - low;  // NaN where there is no score
+    const float per_bin = (kSelBins - 1) / range;
+    bool found = false;
+    const int scored_left = take - p.keep_first - p.keep_last;  // the kept pages' keys are above all others
+    if (scored_left == 0) {
+        prefix = 0xfffffffeu, left = 0;
+        found = true;
+    } else if (range > 0.f && per_bin < INFINITY && range < INFINITY) {
+        // no less for larger scores; pages outside the cache are in bin 0
+        auto bin_of = [&](uint32_t k) { return k ? min(kSelBins - 1, (int)((float_of(k) - low) * per_bin)) : 0; };
+        *reinterpret_cast<int4 *>(&hist[4 * tid]) = make_int4(0, 0, 0, 0);
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < n; i += kSelThreads) {
+            const uint32_t k = key[i];
+            if (k != 0xffffffffu) atomicAdd(&hist[bin_of(k)], 1);
+        }
+        __syncthreads();
+        find_bin(scored_left);
+        const int bin = (int)pick[0], in_bin = (int)pick[2];
+        left = (int)pick[1];
+        if (in_bin <= kSelThreads) {
+            uint32_t *const list = reinterpret_cast<uint32_t *>(hist);  // the bin's members, over the counts
+#pragma unroll 4
+            for (int i = tid; i < n; i += kSelThreads) {
+                const uint32_t k = key[i];
+                if (k != 0xffffffffu && bin_of(k) == bin) list[atomicAdd(&listed, 1)] = k;
+            }
+            __syncthreads();
+            if (tid < in_bin) {
+                const uint32_t mine = list[tid];
+                int above = 0, equal = 0;
+#pragma unroll 4
+                for (int i = 0; i < in_bin; ++i) above += list[i] > mine, equal += list[i] == mine;
+                if (above < left && left <= above + equal) pick[0] = mine, pick[1] = left - above;
+            }
+            __syncthreads();
+            prefix = pick[0], left = (int)pick[1];
+            found = true;
+        } else {
+            left = take;
+        }
+    }
+    // by its bits, eleven at a time from the top
+    uint32_t known = 0;
+    bool all = found;  // whether all that agree with the prefix are taken
     for (int shift = 21; shift > -11 && !all; shift -= shift == 10 ? 10 : 11) {
         const uint32_t digit = shift == 0 ? 1023u : 2047u;
         *reinterpret_cast<int4 *>(&hist[4 * tid]) = make_int4(0, 0, 0, 0);
@@ -256,33 +361,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
             }
         }
         __syncthreads();
-        // sums over the bins from the highest down: thread t has bin 2047 - 4 t and the three below
-        const int4 c4 = *reinterpret_cast<const int4 *>(&hist[2044 - 4 * tid]);
-        const int c[4] = {c4.w, c4.z, c4.y, c4.x}, mine = c[0] + c[1] + c[2] + c[3];
-        int s = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += y;
-        }
-        if (lane == 31) warp_sums[warp] = s;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w)
-            if (w < warp) s += warp_sums[w];
-        int before = s - mine;
-        if (before < left && s >= left) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (before < left && before + c[j] >= left) {
-                    pick[0] = 2047 - 4 * tid - j;
-                    pick[1] = left - before;
-                    pick[2] = c[j];
-                }
-                before += c[j];
-            }
-        }
-        __syncthreads();
+        find_bin(left);
         prefix |= pick[0] << shift;
         known |= digit << shift;
         left = (int)pick[1];
@@ -290,7 +369,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_page_select_kernel(const __gri
         __syncthreads();
         if (shift == 0) break;
     }
-    if (all) {  // every key from the prefix on, whatever its other bits
+    if (all && !found) {  // every key from the prefix on, whatever its other bits
         prefix -= 1;
         left = 0;
     }

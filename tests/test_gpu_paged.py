@@ -200,6 +200,23 @@ def test_select_pages_outside_the_cache_come_last():
     assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
 
 
+@pytest.mark.parametrize("outlier", [False, True])
+@pytest.mark.parametrize("top,first,last", [(64, 1, 1), (1500, 2, 3), (7, 3, 4), (2999, 0, 0)])
+def test_select_crowded_scores(top, first, last, outlier):
+    """Scores that steps from the least to the largest do not tell apart: two values all along, or one page
+    far above or below all others; and no room but for the pages that are kept anyway."""
+    c = pu.Cache([16 * 3000 - 5], 1, 16, 64, seed=top, num_pages=3100)
+    q, cu, d_cu = pu.queries([1], 2, 64, seed=top)
+    if outlier:
+        c.ms[c.table[0, 1234 + top % 2]] = 1e9
+    else:
+        c.mean[:] = c.mean[:1]
+        c.mean[1::2] = -c.mean[1::2]
+        c.ms[:] = 0.5
+    c.d_mean, c.d_ms = torch.from_numpy(c.mean).cuda(), torch.from_numpy(c.ms).cuda()
+    run_select(c, q, cu, d_cu, top, first, last)
+
+
 def test_select_tiny_queries():
     """Queries down to bf16's smallest numbers are rounded like others: 127 / max|q| is past the largest float
     below 2^-121.  The pages' scores lie in powers of two apart, so that their 32-bit products (which are
