@@ -375,6 +375,21 @@ def test_attend_selected_pages(page, D):
     o1, l1 = run_attend(c, q, cu, d_cu, full, np.array([[-(-L // page)] * 2 for L in lens]))
 
 
+def test_pages_shared_and_chosen_twice():
+    """Sequences with pages in common (the same prompt), a page twice in one row of the table, and a position
+    that is chosen twice, which counts twice."""
+    c = pu.Cache([200, 333, 333, 64], 2, 16, 64, seed=21)
+    c.table[1, :12] = c.table[0, :12]
+    c.table[2, :21] = c.table[1, :21]
+    c.table[2, 3] = c.table[2, 7]
+    c.d_table = torch.from_numpy(c.table).cuda()
+    q, cu, d_cu = pu.queries([2, 1, 1, 1], 8, 64, seed=21)
+    run_attend(c, q, cu, d_cu)
+    sel = np.tile(np.array([1, 0, 1, 3, 3, 2]), (4, 2, 1))
+    run_attend(c, q, cu, d_cu, sel, np.array([[6, 5], [3, 6], [0, 1], [4, 2]]))
+    run_select(c, q, cu, d_cu, 9, 1, 1)
+
+
 def test_attend_masked_values_never_touch_a_row():
     """NaN codes behind the last key (every Cache holds them), and NaN keys and values that only a
     sequence's later query tokens see."""
@@ -575,6 +590,47 @@ def test_captured_steps_replayed_with_other_lengths():
         graph.replay()
         torch.cuda.synchronize()
         s.check(step, hw, T, top, out)
+
+
+def test_captured_on_forked_streams():
+    """A graph whose calls follow copies, fills, one another and other streams' calls."""
+    c = pu.Cache([700, 90, 1500], 2, 32, 128, seed=31)
+    q, cu, d_cu = pu.queries([1, 3, 1], 16, 128, seed=31)
+    k, v = (torch.randn((6, 2, 128), device="cuda").to(torch.bfloat16) for _ in range(2))
+    free = [i for i in range(c.num_pages) if i not in c.table][:1]
+    slots = i32([free[0] * 32 + i for i in range(6)])
+    kc, vc, ks, vs = (x.clone() for x in c.pages)
+    mean, ms = c.d_mean.clone(), c.d_ms.clone()
+    want_pages = tuple(x.clone() for x in (kc, vc, ks, vs, mean, ms))
+    fa.fa_kv_append(k, v, slots, *want_pages)
+    want_sel = fa.fa_page_select(q, d_cu, c.d_lens, c.d_table, c.d_mean, c.d_ms, 32, 8)
+    want = fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages, *want_sel)
+    torch.cuda.synchronize()
+    q2, sel, n = torch.zeros_like(q), torch.zeros_like(want_sel[0]), torch.zeros_like(want_sel[1])
+    o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    ws = torch.empty(fa.fa_fwd_paged_workspace_bytes(3, q.shape[0], 16, 2, 128), dtype=torch.uint8, device="cuda")
+    graph, fork, done = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        q2.copy_(q)
+        fork.wait_stream(main)
+        with torch.cuda.stream(fork):
+            ks.mul_(1.0)
+            fa.fa_kv_append(k, v, slots, kc, vc, ks, vs, mean, ms, stream=fork)
+            done.record(fork)
+        sel.fill_(-9)
+        fa.fa_page_select(q2, d_cu, c.d_lens, c.d_table, c.d_mean, c.d_ms, 32, 8, sel=sel, sel_count=n)
+        o.zero_()
+        main.wait_event(done)
+        fa.fa_fwd_paged(q2, d_cu, c.d_lens, c.d_table, kc, vc, ks, vs, sel, n, o=o, lse=lse, workspace=ws)
+    for _ in range(3):
+        q2.zero_(), o.zero_(), lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(sel, want_sel[0]) and torch.equal(n, want_sel[1])
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        for got, ref in zip((kc, vc, ks, vs, mean, ms), want_pages):
+            assert torch.equal(got, ref)
 
 
 def test_calls_on_several_streams():
