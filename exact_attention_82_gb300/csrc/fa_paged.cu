@@ -351,12 +351,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // The workspace: for each block what the item that it leaves off needs to be
 // joined, then two slots of partial results for each warp: 0 for an item that was begun
-// before the warp, 1 for the one that the block leaves off.  A slot is [rows][D] sums,
-// [rows] m, [rows] l.
+// before the warp, 1 (the first warp's) for the one that the block leaves off.  A slot is
+// [rows][D] sums, [rows] m, [rows] l.
 struct __align__(16) Tail {
-    int parts;               // 0: no item is left off.  Part 0 is slot 1 of warp `lead`,
-    int lead;                // part j slot 0 of the first warp of the j-th block behind
-    int b, h, row0, pad[3];
+    int parts;               // 0: no item is left off.  Part 0 is slot 1 of this block's first
+    int q0, nq, h;           // warp, part j slot 0 of that of the j-th block behind
+    int row0, pad[3];
 };
 __device__ __forceinline__ Tail *tail_of(float *ws, int block) { return reinterpret_cast<Tail *>(ws) + block; }
 __device__ __forceinline__ float *slot_of(float *ws, int blocks, int worker, int slot, int nr, int D) {
@@ -381,6 +381,11 @@ __device__ __forceinline__ int token_of(const PagedParams &p, int nq, int row) {
 __device__ __forceinline__ long long out_row(const PagedParams &p, int q0, int nq, int h, int row) {
     const int tok = token_of(p, nq, row);
     return (long long)(q0 + tok) * (p.Hkv * p.G) + h * p.G + (row - tok * p.G);
+}
+
+__device__ __noinline__ void write_tail(float *ws, const Work *it, int share) {
+    const int parts = min((it->end - 1) / share, (int)gridDim.x - 1) - (int)blockIdx.x + 1;
+    *tail_of(ws, blockIdx.x) = Tail{parts, it->q0, it->nq, it->h, it->row0, {0, 0, 0}};
 }
 
 // --------------------------------------------------------------- the kernel
@@ -849,9 +854,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 const float *const closing = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + min(last + 1, C::WARPS - 1), 0, NR, D);
                 if (closes) open = false;
                 whole = begins && !open;
-                part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS + lead, begins ? 1 : 0, NR, D);
+                part = slot_of(p.ws, gridDim.x, blockIdx.x * C::WARPS, begins, NR, D);  // (begun before the block: by its first warp)
                 if (begins && open && warp == lead && lane == 0)
-                    *tail_of(p.ws, blockIdx.x) = Tail{min((it->end - 1) / share, (int)gridDim.x - 1) - (int)blockIdx.x + 1, lead, it->b, it->h, it->row0, {0, 0, 0}};
+                    write_tail(p.ws, it, share);
                 if (lead != last || closes) {
                     if (lane < NR) {  // a row's maximum over the group, and the factors of its parts to it
                         float M = closes ? closing[NR * D + lane] : kPgNone, L = 0.f, f = 0.f;
@@ -935,55 +940,58 @@ constexpr int kJoinMany = 8;  // parts
 template <int D, int NR>
 struct JoinRow {
     static constexpr int E = D / 32;
+    static constexpr int UN = 4;  // parts in flight
     float M, L, O[E];
+    float m[UN], l[UN], o[UN][E];
 
-    // parts j0, j0 + step, ..
-    __device__ __forceinline__ void sum(const PagedParams &p, const Tail &tail, int blocks, int warps, int block, int r, int j0, int step) {
-        const int lane = threadIdx.x & 31;
+    __device__ __forceinline__ void begin() {
         M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) O[e] = 0.f;
-        constexpr int UN = 4;  // parts in flight
-#pragma unroll 1
-        for (; j0 < tail.parts; j0 += UN * step) {
-            float m[UN], l[UN], o[UN][E];
+    }
+    // parts j0, j0 + step, .. of those below `limit`
+    __device__ __forceinline__ void fetch(const PagedParams &p, int blocks, int warps, int block, int r, int j0, int step, int limit) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const int j = j0 + u * step;
-                m[u] = -INFINITY, l[u] = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[u][e] = 0.f;
-                if (j < tail.parts) {
-                    const float *part = slot_of(p.ws, blocks, (block + j) * warps + (j == 0 ? tail.lead : 0), j == 0, NR, D);
-                    m[u] = part[NR * D + r];
-                    l[u] = part[NR * D + NR + r];
-                    if (E == 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(part + r * D + 4 * lane);
-                        o[u][0] = x.x, o[u][1] = x.y, o[u][E - 2] = x.z, o[u][E - 1] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2 *>(part + r * D + 2 * lane);
-                        o[u][0] = x.x, o[u][1] = x.y;
-                    }
-                }
+        for (int u = 0; u < UN; ++u) {
+            const int j = j0 + u * step;
+            if (j >= limit) continue;
+            const float *part = slot_of(p.ws, blocks, (block + j) * warps, j == 0, NR, D);
+            m[u] = part[NR * D + r];
+            l[u] = part[NR * D + NR + r];
+            if (E == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(part + r * D + 4 * lane);
+                o[u][0] = x.x, o[u][1] = x.y, o[u][E - 2] = x.z, o[u][E - 1] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(part + r * D + 2 * lane);
+                o[u][0] = x.x, o[u][1] = x.y;
             }
-            float now = M;
+        }
+    }
+    // what was fetched, as far as it is below `parts`
+    __device__ __forceinline__ void take(int j0, int step, int parts) {
+        float now = M;
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                if (l[u] == 0.f) m[u] = -INFINITY;  // a part without keys does not count
-                now = fmaxf(now, m[u]);
-            }
-            const float base = now == -INFINITY ? 0.f : now, f0 = ex2_approx(M - base);
-            M = now;
-            L *= f0;
+        for (int u = 0; u < UN; ++u) {
+            const bool is = j0 + u * step < parts;
+            if (!is || l[u] == 0.f) m[u] = -INFINITY;  // a part without keys does not count
+            if (!is) l[u] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) O[e] *= f0;
+            for (int e = 0; e < E; ++e)
+                if (!is) o[u][e] = 0.f;
+            now = fmaxf(now, m[u]);
+        }
+        const float base = now == -INFINITY ? 0.f : now, f0 = ex2_approx(M - base);
+        M = now;
+        L *= f0;
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                const float f = ex2_approx(m[u] - base);
-                L = fmaf(l[u], f, L);
+        for (int e = 0; e < E; ++e) O[e] *= f0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) O[e] = fmaf(o[u][e], f, O[e]);
-            }
+        for (int u = 0; u < UN; ++u) {
+            const float f = ex2_approx(m[u] - base);
+            L = fmaf(l[u], f, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] = fmaf(o[u][e], f, O[e]);
         }
     }
     __device__ __forceinline__ void add(float m, float l, const float *o) {
@@ -1010,20 +1018,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = blockIdx.x, blocks = gridDim.x;
     JoinRow<D, NR> row_of;
     grid_wait();
+    // The first parts that there may be are read with what says how many there are.
+    const int r0 = blockIdx.y * kJoinWarps + warp;
+    row_of.fetch(p, blocks, WARPS, block, r0, 0, 1, blocks - block);
     const Tail tail = *tail_of(p.ws, block);
     if (tail.parts == 0) return;
-    const Seq s = sequence(p, tail.b);
-    const int rows = min(NR, s.nq * p.G - tail.row0);
+    const int rows = min(NR, tail.nq * p.G - tail.row0);
+    row_of.begin();
     if (tail.parts <= kJoinMany) {
-        const int r = blockIdx.y * kJoinWarps + warp;
-        if (r >= rows) return;
-        row_of.sum(p, tail, blocks, WARPS, block, r, 0, 1);
-        row_of.write(p, out_row(p, s.q0, s.nq, tail.h, tail.row0 + r));
+        if (r0 >= rows) return;
+        row_of.take(0, 1, tail.parts);
+#pragma unroll 1
+        for (int j0 = row_of.UN; j0 < tail.parts; j0 += row_of.UN) {
+            row_of.fetch(p, blocks, WARPS, block, r0, j0, 1, tail.parts);
+            row_of.take(j0, 1, tail.parts);
+        }
+        row_of.write(p, out_row(p, tail.q0, tail.nq, tail.h, tail.row0 + r0));
         return;
     }
 #pragma unroll 1
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        row_of.sum(p, tail, blocks, WARPS, block, r, warp, kJoinWarps);
+        row_of.begin();
+#pragma unroll 1
+        for (int j0 = warp; j0 < tail.parts; j0 += row_of.UN * kJoinWarps) {
+            row_of.fetch(p, blocks, WARPS, block, r, j0, kJoinWarps, tail.parts);
+            row_of.take(j0, kJoinWarps, tail.parts);
+        }
         __syncthreads();  // the row before is read
         if (lane == 0) red_m[warp] = row_of.M, red_l[warp] = row_of.L;
 #pragma unroll
@@ -1032,7 +1052,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
         if (warp != 0) continue;
 #pragma unroll
         for (int v = 1; v < kJoinWarps; ++v) row_of.add(red_m[v], red_l[v], &red_o[v][lane * E]);
-        row_of.write(p, out_row(p, s.q0, s.nq, tail.h, tail.row0 + r));
+        row_of.write(p, out_row(p, tail.q0, tail.nq, tail.h, tail.row0 + r));
     }
 }
 
