@@ -40,6 +40,7 @@
 // result a block in the workspace, which a second kernel joins.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -108,7 +109,16 @@ struct Seq {
     int q0, nq, len;
 };
 
-__device__ __forceinline__ Seq sequence(const PagedParams &p, int b) {
+// What of the parameters says how the work is laid out, for shared memory: an out of line
+// function that is given the parameters themselves reads them as if from global memory
+// (work_at before the first copy took 1930 cycles so, and takes 1200).
+struct Layout {
+    const int *cu_q, *seq_lens, *sel, *sel_count;
+    int B, T, G, Hkv, sel_width, page_log2, max_len;
+};
+
+template <class P>
+__device__ __forceinline__ Seq sequence(const P &p, int b) {
     Seq s;
     s.q0 = max(0, min(p.cu_q[b], p.T));
     s.nq = max(s.q0, min(p.cu_q[b + 1], p.T)) - s.q0;
@@ -117,14 +127,15 @@ __device__ __forceinline__ Seq sequence(const PagedParams &p, int b) {
 }
 
 // Tiles of one item of (b, h), at least one: an item without keys still writes its rows.
-__device__ __forceinline__ int item_tiles(const PagedParams &p, int b, int h, int len) {
+template <class P>
+__device__ __forceinline__ int item_tiles(const P &p, int b, int h, int len) {
     int keys = len;
     if (p.sel) keys = max(0, min(p.sel_count[(long long)b * p.Hkv + h], p.sel_width)) << p.page_log2;
     return max(1, (int)((uint32_t)(keys + kPgTile - 1) / kPgTile));
 }
 
-template <int NR>
-__device__ __forceinline__ int entry_weight(const PagedParams &p, int e) {
+template <int NR, class P>
+__device__ __forceinline__ int entry_weight(const P &p, int e) {
     const int b = p.sel ? e / p.Hkv : e, h = p.sel ? e % p.Hkv : 0;
     const Seq s = sequence(p, b);
     const int rt = (uint32_t)(s.nq * p.G + NR - 1) / NR;
@@ -174,7 +185,7 @@ struct Start {
 // within the instruction cache: with all of it inlined, in 64 bits, the kernel was 192 KB
 // long and spent 25 us on fetching itself.)
 template <int NR>
-__device__ __noinline__ void work_at(const PagedParams &p, Start *at, Work *it) {
+__device__ __noinline__ void work_at(const Layout &p, Start *at, Work *it) {
     // The scan's lengths and these are the same unless the caller changes them during
     // the call; the bounds on entry, head and block keep every access inside even then.
     const int n = p.sel ? p.B * p.Hkv : p.B, pos = at->ahead.pos, end = at->end;
@@ -211,7 +222,7 @@ __device__ __noinline__ void work_at(const PagedParams &p, Start *at, Work *it) 
 
 // Scans the line and starts every warp of the block.  Returns the share of a block.
 template <int WARPS, int NR>
-__device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start *start, Work *work_of, int works) {
+__device__ __forceinline__ int scan_line(const PagedParams &p, Layout *layout, int *sums, Start *start, Work *work_of, int works) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int THREADS = 32 * WARPS;
     __shared__ int share_sm;
@@ -251,8 +262,9 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start 
         share = max(share, kPgMinShare);
         // The block's ends.  Which thread's entries hold them: a lane's twelve or eight sums,
         // then one of those.
+        const int x32 = (int)min(x, 0x7fffffffll);
         auto holder = [&](int pos) {
-            const int in = max(0, __ffs((int)__ballot_sync(0xffffffffu, x > pos)) - 1);
+            const int in = max(0, __ffs((int)__ballot_sync(0xffffffffu, x32 > pos)) - 1);
             const uint32_t above = __ballot_sync(0xffffffffu, lane < WARPS && sums[in * WARPS + min(lane, WARPS - 1)] > pos);
             return in * WARPS + max(0, __ffs((int)above) - 1);
         };
@@ -285,7 +297,7 @@ __device__ __forceinline__ int scan_line(const PagedParams &p, int *sums, Start 
         if (lane < WARPS) {
             start[lane] = Start{f, mine};
             if (f.pos < mine)
-                work_at<NR>(p, start + lane, work_of + lane * works);
+                work_at<NR>(*layout, start + lane, work_of + lane * works);
             else
                 start[lane].ahead.entry = -1;
         }
@@ -398,9 +410,12 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     constexpr int HB = D == 128 && NT == 4 ? 1 : 2;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ Start start[C::WARPS];
+    __shared__ Layout layout;
     __shared__ int flag_of[C::WARPS];
     __shared__ float join_m[C::WARPS][NR], join_l[C::WARPS][NR], join_f[C::WARPS][NR];
     __shared__ float close_f[C::WARPS][NR], inv_of[C::WARPS][NR];
+    // (the parameters are there before the kernel before this one has ended)
+    if (threadIdx.x == 0) layout = Layout{p.cu_q, p.seq_lens, p.sel, p.sel_count, p.B, p.T, p.G, p.Hkv, p.sel_width, p.page_log2, p.max_len};
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -410,7 +425,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     Work *const work_of = reinterpret_cast<Work *>(sm + C::OFF_WORK) + warp * C::WORKS;
     const uint64_t policy = l2_policy_evict_first();
 
-    const int share = scan_line<C::WARPS, NR>(p, reinterpret_cast<int *>(sm + C::OFF_SUMS), start, reinterpret_cast<Work *>(sm + C::OFF_WORK), C::WORKS);
+    const int share = scan_line<C::WARPS, NR>(p, &layout, reinterpret_cast<int *>(sm + C::OFF_SUMS), start,
+                                              reinterpret_cast<Work *>(sm + C::OFF_WORK), C::WORKS);
     const bool busy = start[warp].ahead.entry >= 0;
     if (lane == 0) {
         if (warp == 0) tail_of(p.ws, blockIdx.x)->parts = 0;
@@ -432,7 +448,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
             next = work_of + (works & (C::WORKS - 1));
             ++works;
             __syncwarp();
-            if (lane == 0) work_at<NR>(p, start + warp, const_cast<Work *>(next));
+            if (lane == 0) work_at<NR>(layout, start + warp, const_cast<Work *>(next));
             __syncwarp();
             t_next = next->t0;
         }
@@ -538,7 +554,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     uint32_t qf[C::Q_SHARED ? 1 : NT][KG][4][2];  // fragments of Q^T (lane: row g of each tile of 8)
     uint2 *const q_sm = reinterpret_cast<uint2 *>(sm + C::OFF_Q) + warp * (KG * 4 * NT * 32) + lane;  // or here, [kg][w][nt]
     float fac[NT][2];           // c 2^e of the rows 2t, 2t+1, which this lane holds in accumulators
-    int lim[NT][2], lim_min = 0;  // the first key that they do not see, and the least of them
+    int lim_min = 0;              // the first key that some row of the item does not see
     float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
     if (busy) {
 #pragma unroll 1
@@ -596,8 +612,6 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     fac[nt][j] = p.scale_log2 * __shfl_sync(0xffffffffu, up, (2 * t + j) * 4);
-                    const int r = it->row0 + nt * 8 + 2 * t + j;
-                    lim[nt][j] = r < it->rows ? it->len - it->nq + token_of(p, it->nq, r) + 1 : it->len;
                 }
             }
             lim_min = it->len - it->nq + token_of(p, it->nq, it->row0) + 1;
@@ -675,10 +689,9 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 // ---- exponents of the weights, against the maximum in use
                 const bool edge = key_max + 16 > lim_min;  // some row does not see some key
                 float y[HB][NT][4], top = kPgNone;
-                auto exponents = [&](int half, int nt, int j, float off) {
-                    float x = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y, meta[half].z + off);
-                    if (edge && key[half] + gk + (j >> 1) * 2 >= lim[nt][j & 1]) x = -INFINITY;
-                    return x;
+                auto exponents = [&](int half, int nt, int j, float off, int limit) {
+                    const float x = fmaf(sc[half][nt][j], fac[nt][j & 1] * meta[half].y, meta[half].z + off);
+                    return key[half] + gk + (j >> 1) * 2 < limit ? x : -INFINITY;
                 };
                 if (!edge) {
 #pragma unroll
@@ -698,10 +711,12 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
+                            const int row = it->row0 + nt * 8 + 2 * t + j;
+                            const int limit = !edge ? INT_MAX : row < it->rows ? it->len - it->nq + token_of(p, it->nq, row) + 1 : it->len;
                             float x = kPgNone;
 #pragma unroll
                             for (int half = 0; half < HB; ++half)
-                                x = fmaxf(x, fmaxf(exponents(half, nt, j, 0.f), exponents(half, nt, j + 2, 0.f)));
+                                x = fmaxf(x, fmaxf(exponents(half, nt, j, 0.f, limit), exponents(half, nt, j + 2, 0.f, limit)));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -713,8 +728,8 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                             for (int c = 0; c < C::CHUNKS; ++c) acc[c][nt][j] *= f, acc[c][nt][j + 2] *= f;
 #pragma unroll
                             for (int half = 0; half < HB; ++half) {
-                                y[half][nt][j] = exponents(half, nt, j, kPgShift - x);
-                                y[half][nt][j + 2] = exponents(half, nt, j + 2, kPgShift - x);
+                                y[half][nt][j] = exponents(half, nt, j, kPgShift - x, limit);
+                                y[half][nt][j + 2] = exponents(half, nt, j + 2, kPgShift - x, limit);
                             }
                         }
                 }
@@ -1080,7 +1095,7 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
 
 // Rows of an item: 8 or 16 while a sequence's query rows are no more (by the mean
 // number of its tokens, padding rounded off).  Beyond, 32 at D = 64 (16 sequences of 16384
-// keys, 32 rows: 95 us, 118 us in two items of 16).  At D = 128 the sums of 32 rows leave
+// keys, 32 rows: 98 us, 118 us in two items of 16).  At D = 128 the sums of 32 rows leave
 // few registers, and items of 32 pay from more than 32 rows on: 8 sequences of 16384 keys with
 // 64 rows take 154 us, 174 us in items of 16; with 32 rows 97 and 100 us; but 16 ragged ones
 // with 16 to 40 rows 89 and 77 us.
