@@ -8,6 +8,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/fa.h"
 #include "fa_paged.h"
 #include "sm103_ptx.cuh"
@@ -172,12 +174,12 @@ cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream
 // The size of the team follows from the page's: small pages go to single warps, which
 // meet no barrier.
 //
-// A prompt of 16384 tokens, 8 heads, D = 128: 20.9 us, 4,820 GB/s of reads and writes (72% of
-// the copy rate); D = 64 14.3 us; 64 single tokens 4.4 us, three latencies after one
-// another.  It issues 2.9 instructions a cycle of 4, so what an element costs counts:
-// bf16 times the inverse scale and fp16 plus a sum are instructions of mixed precision
-// (22.4 -> 21.4 us with both), and NaN among the codes is looked for only where the row
-// had one (20.9 us).
+// A prompt of 16384 tokens, 8 heads, D = 128: 17.3 us, 5,840 GB/s of reads and writes (87% of
+// the copy rate); D = 64 11.6 us; 64 single tokens 4.5 us, three latencies after one
+// another.  It issues more than 2.5 instructions a cycle of 4, so what an element costs
+// counts: bf16 times the inverse scale and fp16 plus a sum are instructions of mixed
+// precision (22.4 -> 21.4 us with both), NaN among the codes is looked for only where the
+// row had one (20.9 us), and whole pages have a pass of their own.
 constexpr int kWindow = 64;  // tokens whose runs one set of blocks shares
 
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
@@ -257,9 +259,9 @@ struct AppendCfg {
     static constexpr int PASSES = PAGE / ROWS;
     // Blocks an SM that the registers are held to.  A team waits for memory three times
     // (slots, rows, and to be written), so more of them side by side is faster, until they
-    // spill (much): a 16384-token prompt with 7, 8, 9 and 10 blocks 25.1, 23.2, 22.3 and 22.7 us, ragged
-    // prompts at 16 rows a page, D = 64, with 9, 10 and 12 blocks 19.1, 16.4 and 18.0 us.
-    static constexpr int BLOCKS = (PASSES <= 4 ? 10 : 9) * 128 / THREADS;
+    // spill (much): a 16384-token prompt with 7, 8, 9 and 10 blocks 18.4, 18.1, 17.8 and 17.3 us;
+    // ragged prompts at 16 rows a page, D = 64, with 8, 9, 10 and 12 blocks 15.0, 14.3, 13.7 and 14.1.
+    static constexpr int BLOCKS = 10 * 128 / THREADS;
 };
 
 template <int D, int PAGE>
@@ -318,146 +320,155 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
             if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
         }
 
-        // ---- everything that is read, at once: row r0 + i ROWS of the page in slot i
-        const int sub = tt % C::TPT, r0 = tt / C::TPT;
-        const long long ph = (long long)pg * p.Hkv + h;
-        const float was = scale_of[ph];
-        uint8_t *const codes = pages_of + ph * PAGE * D + sub * 8;
-        const __nv_bfloat16 *const x = x_of + (long long)(t0 + i0 - off) * stride + sub * 8;  // row 0's token
-        const bool mean = kv == 0 && p.mean != nullptr;
-        uint4 w[C::PASSES];
-#pragma unroll
-        for (int i = 0; i < C::PASSES; ++i) {
-            const int r = r0 + i * C::ROWS;
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (r >= off && r < off + n) {
-                w[i] = __ldg(reinterpret_cast<const uint4 *>(x + r * stride));
-            } else if (mean && r < off) {
-                const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                w[i].x = c.x, w[i].y = c.y;
-            }
-        }
-        // magnitudes of bf16 compare as integers, two at a time
-        uint32_t am2 = 0;
-#pragma unroll
-        for (int i = 0; i < C::PASSES; ++i) {
-            uint32_t u = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                  __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-            if (r0 + i * C::ROWS < off) u = 0;
-            am2 = __vmaxu2(am2, u);
-        }
-        uint32_t am = max(am2 & 0xffffu, am2 >> 16);
-        const bool special = am >= 0x7f80u;
-        if (special) {  // infinities and NaN do not count
-            am = 0;
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
-                    if (r0 + i * C::ROWS >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                }
-            }
-        }
-        am = __reduce_max_sync(0xffffffffu, am);
-        if (C::TEAM > 1) {
-            if (lane == 0) amax_sm[0][warp] = am;
-            team_sync();
-#pragma unroll
-            for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
-        } else {
-            team_sync();
-        }
-        float scale = pow2_scale(__uint_as_float(am << 16));
-        if (off > 0) scale = fmaxf(scale, was);
-        if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
-        // x / scale is x * (1 / scale) exactly where the scale is a power of two (always,
-        // unless the caller put another one there; the remainder corrects it then)
-        const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-        const float inv_scale = 1.f / scale, shrink = was / scale;
-        const uint16_t inv_bf16 = (uint16_t)(__float_as_uint(inv_scale) >> 16);  // exact, where it is used
-        const bool grown = off > 0 && scale != was;  // the rows before the run are rounded again
-        // the codes' sums: multiples of 2^-9, at most 8 of them of at most 448 a thread, are exact in fp32
-        static_assert(C::PASSES <= 8, "");
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < C::PASSES; ++i) {
-            const int r = r0 + i * C::ROWS;
-            if (r < off || r >= off + n) continue;
-            float y[8];
-            if (pow2) {
-                scaled8(w[i], inv_bf16, y);
-            } else {
-                bf16x8(w[i], y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = y[j];
-                    y[j] = x * inv_scale;
-                    y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
-                }
-            }
-            const uint2 c = encode8(y);
-            *reinterpret_cast<uint2 *>(codes + r * D) = c;
-            if (mean) {
-                add8(special ? without_nan(c) : c, sum);
-            }
-        }
-        if (off > 0 && (mean || grown)) {  // apart, so that prompts' whole pages skip it
+        // A whole page, the usual run of a prompt, does without what the ends of others need
+        // (20.9 -> 18.1 us) and always has a power of two for its scale (17.6 us).
+        auto append = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            // ---- everything that is read, at once: row r0 + i ROWS of the page in slot i
+            const int sub = tt % C::TPT, r0 = tt / C::TPT;
+            const long long ph = (long long)pg * p.Hkv + h;
+            const float was = W ? 0.f : scale_of[ph];
+            uint8_t *const codes = pages_of + ph * PAGE * D + sub * 8;
+            const __nv_bfloat16 *const x = x_of + (long long)(t0 + i0 - off) * stride + sub * 8;  // row 0's token
+            const bool mean = kv == 0 && p.mean != nullptr;
+            uint4 w[C::PASSES];
 #pragma unroll
             for (int i = 0; i < C::PASSES; ++i) {
                 const int r = r0 + i * C::ROWS;
-                if (r >= off) continue;
-                uint2 c = make_uint2(w[i].x, w[i].y);
-                float y[8];
-                if (grown) {
-                    if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                    decode8(c, y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] *= shrink;
-                    c = encode8(y);
-                    *reinterpret_cast<uint2 *>(codes + r * D) = c;
+                if (!W) w[i] = make_uint4(0, 0, 0, 0);
+                if (W || (r >= off && r < off + n)) {
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(x + r * stride));
+                } else if (mean && r < off) {
+                    const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                    w[i].x = c.x, w[i].y = c.y;
                 }
-                decode8(without_nan(c), y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] += y[j];
             }
-        }
-        if (mean) {  // integer sums: the same in any order
+            // magnitudes of bf16 compare as integers, two at a time
+            uint32_t am2 = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                int x = (int)(sum[j] * 512.f);
-#pragma unroll
-                for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
+            for (int i = 0; i < C::PASSES; ++i) {
+                uint32_t u = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                if (!W && r0 + i * C::ROWS < off) u = 0;
+                am2 = __vmaxu2(am2, u);
             }
-            team_sync();
-            constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
-            int total[PER], a = 0;
+            uint32_t am = max(am2 & 0xffffu, am2 >> 16);
+            const bool special = am >= 0x7f80u;
+            if (special) {  // infinities and NaN do not count
+                am = 0;
 #pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int d = tt + c * 32 * C::TEAM;
-                total[c] = 0;
-                if (d < D)
+                for (int i = 0; i < C::PASSES; ++i) {
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-                    for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
-                a = max(a, abs(total[c]));
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
+                        if (W || r0 + i * C::ROWS >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                    }
+                }
             }
-            a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
+            am = __reduce_max_sync(0xffffffffu, am);
             if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
+                if (lane == 0) amax_sm[0][warp] = am;
                 team_sync();
 #pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
+                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
+            } else {
+                team_sync();
             }
-            const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
+            float scale = pow2_scale(__uint_as_float(am << 16));
+            if (!W && off > 0) scale = fmaxf(scale, was);
+            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
+            // x / scale is x * (1 / scale) exactly where the scale is a power of two (always,
+            // unless the caller put another one there; the remainder corrects it then)
+            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+            const float inv_scale = 1.f / scale, shrink = was / scale;
+            const uint16_t inv_bf16 = (uint16_t)(__float_as_uint(inv_scale) >> 16);  // exact, where it is used
+            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
+            // the codes' sums: multiples of 2^-9, at most 8 of them of at most 448 a thread, are exact in fp32
+            static_assert(C::PASSES <= 8, "");
+            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int d = tt + c * 32 * C::TEAM;
-                if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
+            for (int i = 0; i < C::PASSES; ++i) {
+                const int r = r0 + i * C::ROWS;
+                if (!W && (r < off || r >= off + n)) continue;
+                float y[8];
+                if (W || pow2) {
+                    scaled8(w[i], inv_bf16, y);
+                } else {
+                    bf16x8(w[i], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float x = y[j];
+                        y[j] = x * inv_scale;
+                        y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
+                    }
+                }
+                const uint2 c = encode8(y);
+                *reinterpret_cast<uint2 *>(codes + r * D) = c;
+                if (mean) {
+                    add8(special ? without_nan(c) : c, sum);
+                }
             }
-            if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (off + n));
-        }
+            if (!W && off > 0 && (mean || grown)) {  // apart, so that prompts' whole pages skip it
+#pragma unroll
+                for (int i = 0; i < C::PASSES; ++i) {
+                    const int r = r0 + i * C::ROWS;
+                    if (r >= off) continue;
+                    uint2 c = make_uint2(w[i].x, w[i].y);
+                    float y[8];
+                    if (grown) {
+                        if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                        decode8(c, y);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] *= shrink;
+                        c = encode8(y);
+                        *reinterpret_cast<uint2 *>(codes + r * D) = c;
+                    }
+                    decode8(without_nan(c), y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += y[j];
+                }
+            }
+            if (mean) {  // integer sums: the same in any order
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    int x = (int)(sum[j] * 512.f);
+#pragma unroll
+                    for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
+                }
+                team_sync();
+                constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
+                int total[PER], a = 0;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) {
+                    const int d = tt + c * 32 * C::TEAM;
+                    total[c] = 0;
+                    if (d < D)
+#pragma unroll
+                        for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
+                    a = max(a, abs(total[c]));
+                }
+                a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
+                if (C::TEAM > 1) {
+                    if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
+                    team_sync();
+#pragma unroll
+                    for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
+                }
+                const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) {
+                    const int d = tt + c * 32 * C::TEAM;
+                    if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
+                }
+                if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (W ? PAGE : off + n));
+            }
+        };
+        if (n == PAGE)
+            append(std::true_type());
+        else
+            append(std::false_type());
         team_sync();  // the next run overwrites the shared words
     }
 }
