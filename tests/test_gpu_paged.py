@@ -128,6 +128,38 @@ def test_append_special_values():
     run_append([0, 3], [8, 8], 1, 16, 128, seed=8, change=change)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+def test_append_special_values_in_whole_pages(page, D):
+    """Pages that one run fills: a zero page, infinities, NaN, the smallest and the largest numbers, and a
+    page of one value; with and without means."""
+    def change(w):
+        w[:page] = 0.0
+        w[page + 3, :, 1], w[page + 4, :, 2], w[page + 5] = float("inf"), float("-inf"), float("nan")
+        w[2 * page:3 * page] = float("nan")
+        w[3 * page:4 * page] = 1e-38
+        w[4 * page:5 * page:2] = 3e38
+        w[5 * page:6 * page] = -1.75 * 2.0 ** -12
+
+    for means in (True, False):
+        run_append([0, 0], [7 * page, page], 2, page, D, seed=page, change=change, means=means)
+
+
+def test_append_beside_scales_that_are_no_powers_of_two():
+    """A page whose scale the caller has set: what is added to it is divided by that scale."""
+    c = pu.Cache([40, 24], 2, 16, 64, seed=9)
+    c.ks *= 1.5
+    c.vs *= 1.25
+    c.d_ks, c.d_vs = torch.from_numpy(c.ks).float().cuda(), torch.from_numpy(c.vs).float().cuda()
+    x = torch.randn((4, 2, 64), generator=torch.Generator().manual_seed(9)).to(torch.bfloat16) * 0.5
+    slots = np.array([int(c.table[0, 2]) * 16 + 5 + i for i in range(3)] + [int(c.table[1, 1]) * 16 + 3], np.int32)
+    fa.fa_kv_append(x.cuda(), x.cuda(), torch.from_numpy(slots).cuda(), *c.pages)
+    for codes, scale, got, got_scale in ((c.kc, c.ks, c.d_kc, c.d_ks), (c.vc, c.vs, c.d_vc, c.d_vs)):
+        pu.append(pu.f64(x), slots, codes, scale, 16)
+        assert np.array_equal(pu.f64(got_scale), scale)
+        assert np.array_equal(pu.codes_of(got), codes)
+
+
 def test_append_bad_slots_are_skipped_and_reported():
     c = pu.Cache([20], 2, 16, 64, seed=9)
     before = [t.clone() for t in c.pages]
