@@ -10,9 +10,13 @@
 //   LSE_r = ln2 (m_r - 8 + log2 l_r),
 // for any m_r.  m_r is the largest x_rj so far when it was last taken, and is taken
 // again when some x_rj exceeds it by more than 7, so w is at most 2^15 however
-// unevenly the pages are scaled and can be rounded to fp16 (to 2^-11 of each), whose
-// smallest subnormal is then 2^-32 of the row's largest weight or less; bf16 would
-// keep three bits less.  l sums the unrounded weights in fp32.  e4m3 codes are exact
+// unevenly the pages are scaled and can be rounded to fp16 (to 2^-11 of each; bf16 would
+// keep three bits less).  fp16's subnormal numbers end at 2^-24, which is 2^-32 of the largest
+// 2^x so far.  That may be a key's whose values are 0, for a page of zeros has scale 1, so
+// where a page's value scale is below 2^-4 of the largest before it (or beside it), its
+// 16 keys are a block of their own: weights rounded against their own maximum, and the sums scaled
+// to m_r in fp32.  So no softmax weight is off by more than 2^-11 of itself and 2^-29 of the
+// row's largest.  l sums the unrounded weights in fp32.  e4m3 codes are exact
 // in fp16, and a query row is scaled by a power of two to a largest element in
 // [1, 2), so that its bf16 values are exact too: both products run on fp16 operands
 // with fp32 accumulators, and nothing but w and O is rounded.
@@ -75,6 +79,10 @@ constexpr int kPgMaxLen = 0x7fffff00;
 constexpr float kPgShift = 8.f;    // exponent of a weight at x = m
 constexpr float kPgMost = 15.f;    // and the largest one
 constexpr float kPgNone = -3e38f;  // m before any key
+// log2 of how far value scales may lie apart before weights are rounded apart (see above).  Scales of pages
+// that hold like values differ by 1 or 2.  Where one page in 64 is zeros beside small values, 8 sequences of 16384
+// keys take 50.4 us for 49.6, drafts of 16 to 40 rows 92 for 75; every second page 51.1 and 85.
+constexpr float kPgApart = 4.f;
 
 template <int D, int NT>
 struct PgCfg {
@@ -562,6 +570,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
     uint2 *const q_sm = reinterpret_cast<uint2 *>(sm + C::OFF_Q) + warp * (KG * 4 * NT * 32) + lane;  // or here, [kg][w][nt]
     float fac[NT][2];           // c 2^e of the rows 2t, 2t+1, which this lane holds in accumulators
     int lim_min = 0;              // the first key that some row of the item does not see
+    float z_top = kPgNone;        // the largest value scale of the item so far, as a logarithm
     float m[NT][2], l[NT][2], acc[C::CHUNKS][NT][4];
     if (busy) {
 #pragma unroll 1
@@ -576,6 +585,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 it = work_of + (done & (C::WORKS - 1));
                 ++done;
                 i = it->t0, t1 = it->t1;
+                z_top = kPgNone;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = it->row0 + nt * 8 + g, tok = token_of(p, it->nq, row);
@@ -655,7 +665,11 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                     const int u = __float_as_int(meta[half].z);
                     meta[half].z = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
                     meta[half].w = ex2_approx(-meta[half].z);
+                    if (key[half] != kPgMaxLen) z_top = fmaxf(z_top, meta[half].z);
                 }
+                bool apart = false;  // whether some keys' value scale is far below one before
+#pragma unroll
+                for (int half = 0; half < HB; ++half) apart |= key[half] != kPgMaxLen && meta[half].z < z_top - kPgApart;
 
                 // ---- S^T = K Q^T: a half of 16 keys an MMA tile.  The order of d within the
                 // contraction is free as long as Q's is the same: lane t takes whole 16-byte
@@ -740,81 +754,109 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                             }
                         }
                 }
-                // ---- weights, and their transpose as the B operand (keys x rows)
-                uint32_t wf[HB][NT][2];
-#pragma unroll
-                for (int half = 0; half < HB; ++half)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            w[j] = ex2_approx(y[half][nt][j]);
-                            l[nt][j & 1] = fmaf(w[j], meta[half].w, l[nt][j & 1]);
-                        }
-                        wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
-                        wf[half][nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
-                    }
-                // ---- O^T += V^T W^T: a lane has the rows (of V^T) g and g + 8 of each tile of 16,
+                // ---- weights, and their transpose as the B operand (keys x rows); then
+                // O^T += V^T W^T: a lane has the rows (of V^T) g and g + 8 of each tile of 16,
                 // four keys in a register.
-                auto accumulate = [&](auto keep, auto settle) {
+                uint32_t wf[HB][NT][2];
+                if (!apart && (!edge || lim_min >= it->len)) {
+#pragma unroll
+                    for (int half = 0; half < HB; ++half)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                w[j] = ex2_approx(y[half][nt][j]);
+                                l[nt][j & 1] = fmaf(w[j], meta[half].w, l[nt][j & 1]);
+                            }
+                            wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                            wf[half][nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+                        }
                     constexpr int CG = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // tiles whose MMAs take turns
 #pragma unroll
                     for (int c0 = 0; c0 < C::CHUNKS; c0 += CG) {
                         uint32_t r[CG][2 * HB];
-                        float was[CG][NT][4];
 #pragma unroll
-                        for (int c = 0; c < CG; ++c) {
-                            ldmatrix_b8_trans(((v_read + st) ^ ((c0 + c) * 16)) + h0 * C::HALF_BYTES, r[c]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) was[c][nt][j] = acc[c0 + c][nt][j];
-                        }
+                        for (int c = 0; c < CG; ++c) ldmatrix_b8_trans(((v_read + st) ^ ((c0 + c) * 16)) + h0 * C::HALF_BYTES, r[c]);
 #pragma unroll
                         for (int half = 0; half < HB; ++half)
 #pragma unroll
                             for (int c = 0; c < CG; ++c) {
-                                const uint32_t lo = keep(r[c][2 * half], half), hi = keep(r[c][2 * half + 1], half);
+                                const uint32_t lo = r[c][2 * half], hi = r[c][2 * half + 1];
                                 const uint32_t a0 = codes_f16x2(lo), a1 = codes_f16x2(hi);
                                 const uint32_t a2 = codes_f16x2(lo >> 16), a3 = codes_f16x2(hi >> 16);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
                                     mma_f16(acc[c0 + c][nt], a0, a1, a2, a3, wf[half][nt][0], wf[half][nt][1]);
                             }
-#pragma unroll
-                        for (int c = 0; c < CG; ++c)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) acc[c0 + c][nt][j] = settle(acc[c0 + c][nt][j], was[c][nt][j], nt, j & 1);
                     }
-                };
-                if (!edge || lim_min >= it->len) {
-                    accumulate([](uint32_t r, int) { return r; }, [](float now, float, int, int) { return now; });
                 } else {
-                    // Some rows do not see all of these keys: a weight of 0 would still turn a
-                    // NaN among the values into NaN, so the values that a token does not see
-                    // are cleared, a token at a time, and only that token's rows take the
-                    // result (only the last tiles of a sequence come here).
-                    const int tok0 = it->row0 / p.G, tok1 = min(it->nq - 1, (it->row0 + NR - 1) / p.G);
+                    // Rare tiles: value scales far apart, or keys that some rows do not see.  Each half's
+                    // weights are rounded against their own maximum, and its sums scaled back in fp32.
+                    // A weight of 0 would still turn a NaN among the values into NaN, so the values that
+                    // a token does not see are cleared, a token at a time, and only that token's rows
+                    // take the result.
+                    const bool cut = edge && lim_min < it->len;
+                    const int tok0 = cut ? it->row0 / p.G : 0, tok1 = cut ? min(it->nq - 1, (it->row0 + NR - 1) / p.G) : 0;
+                    float back[HB][NT][2];
+#pragma unroll
+                    for (int half = 0; half < HB; ++half)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float(&yh)[4] = y[half][nt];
+                            float w[4];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                float x = fmaxf(yh[j], yh[j + 2]);
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                                x = x == -INFINITY ? 0.f : x - kPgShift;
+                                back[half][nt][j] = ex2_approx(x);
+#pragma unroll
+                                for (int e = j; e < 4; e += 2) {
+                                    w[e] = ex2_approx(yh[e] - x);
+                                    l[nt][j] = fmaf(w[e], back[half][nt][j] * meta[half].w, l[nt][j]);
+                                }
+                            }
+                            wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
+                            wf[half][nt][1] = movmatrix_trans(pack_f16x2(w[2], w[3]));
+                        }
 #pragma unroll 1
                     for (int tok = tok0; tok <= tok1; ++tok) {
-                        const int limit = it->len - it->nq + tok + 1;
+                        const int limit = cut ? it->len - it->nq + tok + 1 : INT_MAX, first = tok * p.G - it->row0;
                         bool my[NT][2];
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) my[nt][j] = (it->row0 + nt * 8 + 2 * t + j) / p.G == tok;
-                        accumulate(
-                            [&](uint32_t r, int half) {
-                                const int k = key[half] + 4 * t;  // the first of the lane's four keys
-                                return k + 4 <= limit ? r : k >= limit ? 0u : r & ((1u << 8 * (limit - k)) - 1);
-                            },
-                            [&](float now, float before, int nt, int j) { return my[nt][j] ? now : before; });
+                            for (int j = 0; j < 2; ++j) my[nt][j] = !cut || (uint32_t)(nt * 8 + 2 * t + j - first) < (uint32_t)p.G;
+                        uint32_t seen[HB];
+#pragma unroll
+                        for (int half = 0; half < HB; ++half) {
+                            const int k = key[half] + 4 * t;  // the first of the lane's four keys
+                            seen[half] = k + 4 <= limit ? 0xffffffffu : k >= limit ? 0u : (1u << 8 * (limit - k)) - 1;
+                        }
+#pragma unroll
+                        for (int c = 0; c < C::CHUNKS; ++c) {
+                            uint32_t r[2 * HB];
+                            ldmatrix_b8_trans(((v_read + st) ^ (c * 16)) + h0 * C::HALF_BYTES, r);
+#pragma unroll
+                            for (int half = 0; half < HB; ++half) {
+                                const uint32_t lo = r[2 * half] & seen[half], hi = r[2 * half + 1] & seen[half];
+                                const uint32_t a0 = codes_f16x2(lo), a1 = codes_f16x2(hi);
+                                const uint32_t a2 = codes_f16x2(lo >> 16), a3 = codes_f16x2(hi >> 16);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float o[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_f16(o, a0, a1, a2, a3, wf[half][nt][0], wf[half][nt][1]);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        if (my[nt][j & 1]) acc[c][nt][j] = fmaf(o[j], back[half][nt][j & 1], acc[c][nt][j]);
+                                }
+                            }
+                        }
                     }
                 }
-
             }
 
             if (++i < t1) continue;

@@ -405,7 +405,8 @@ int fa_page_select(const void *q, const int *cu_q, const int *seq_lens, const in
  * touch it, whatever their codes are (NaN included).  Scores and sums are fp32;
  * q and K enter the products exactly (q as bf16 scaled by a power of two to fp16:
  * elements below 2^-17 of their row's largest are rounded, to steps of 2^-24 of it),
- * the softmax weights are rounded to fp16, O once to bf16.  Any number of query
+ * the softmax weights are rounded to fp16 (each by at most 2^-11 of itself, or 2^-29 of
+ * the row's largest), O once to bf16.  Any number of query
  * tokens a sequence is taken; the kernel is made for a few (decode, drafts): 8 to 32
  * rows (query tokens times heads of the group) share a pass over the keys.
  * T * Hq < 2^31, and so is, at most, (T * Hq / Hkv / 8 + B) * Hkv times the 32-key

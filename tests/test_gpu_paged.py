@@ -463,6 +463,61 @@ def test_attend_peaky_and_uneven_scales():
         run_attend(c, q, cu, d_cu)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", fa.FA_PAGE_SIZES)
+@pytest.mark.parametrize("G", [1, 8, 20])
+def test_attend_small_values_beside_pages_of_zeros(page, D, G):
+    """A page of zeros has scale 1.  Its keys' scores are like the others', and add nothing to O: what the
+    others add keeps its accuracy however small their values are."""
+    for down in (8, 13, 20, 30, 60, 90):
+        lens, counts = [1024, 8 * page, 700, 5 * page + 3], [1, 1, 3, 2]
+        c = pu.Cache(lens, 1, page, D, seed=D + page + down)
+        c.vs *= 2.0 ** -down
+        for b, zero in enumerate(([0, 5], [1, 3, 5, 7], [0, 1, 700 // page], [2])):  # first, in turn, last, inside
+            for i in zero:
+                c.vc[c.table[b, i]], c.vs[c.table[b, i]] = 0, 1.0
+        c.d_vc, c.d_vs = torch.from_numpy(c.vc).cuda(), torch.from_numpy(c.vs).float().cuda()
+        q, cu, d_cu = pu.queries(counts, G, D, seed=G, pad=1)
+        run_attend(c, q, cu, d_cu, what=f"2^-{down}")
+        sel = np.tile(np.array([3, 0, 5, 1, 4]), (4, 1, 1))
+        run_attend(c, q, cu, d_cu, sel, np.full((4, 1), 5), what=f"2^-{down}, selected")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_small_values_beside_one_large_value_that_is_hardly_seen(D):
+    """A page's scale may come from a token that some queries hardly attend to, while the page's other tokens
+    are rounded to 0 beside it."""
+    c = pu.Cache([600, 330], 2, 16, D, seed=D)
+    c.vs *= 2.0 ** -24
+    q, cu, d_cu = pu.queries([1, 1], 2, D, seed=1)
+    for b in range(2):
+        for h in range(2):
+            for i in (2, 9):
+                pg = c.table[b, i]
+                c.vc[pg, h], c.vs[pg, h] = 0, 1.0
+                c.vc[pg, h, 7] = 0x7E                                 # 448 in every column,
+                x = pu.f64(q[b, h])
+                c.kc[pg, h, 7] = pu.to_e4m3(-x * (64 * D ** 0.5 / (x @ x)) / c.ks[pg, h])  # against the query, as far as codes reach
+    c.d_kc, c.d_vc, c.d_vs = torch.from_numpy(c.kc).cuda(), torch.from_numpy(c.vc).cuda(), torch.from_numpy(c.vs).float().cuda()
+    o, lse = (pu.f64(x) for x in fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages))
+    # A weight w = 2^(x - m + 8) is rounded to fp16: by 2^-11 of itself, or, as a subnormal number, by 2^-25, or by no
+    # more than itself.  m is at most the largest score plus the largest value scale so far, and value scales are
+    # within 2^4 of that (others are rounded against a maximum of their own), so that 2^-25 of w is at most
+    # 2^(-25 - 8 + 4) = 2^-29 of the row's largest softmax weight.  The other terms are check_attend's.
+    for b, L in enumerate(c.lens):
+        at = c.table[b, :-(-L // 16)]
+        for r in range(2):
+            h = r
+            K, V = ((pu.E4M3[x[at, h]] * s[at, h][:, None, None]).reshape(-1, D)[:L] for x, s in ((c.kc, c.ks), (c.vc, c.vs)))
+            s = K @ pu.f64(q[b, r]) * D ** -0.5
+            p = np.exp(s - s.max())
+            ro, rl, size = p @ V / p.sum(), s.max() + np.log(p.sum()), p @ np.abs(V) / p.sum()
+            rounded = np.minimum(p, np.maximum(2.0 ** -11 * p, 2.0 ** -29)) @ np.abs(V) / p.sum()
+            x = (1 + np.abs(s).max() * 1.4427) * 2.0 ** -20
+            assert (np.abs(o[b, r] - ro) <= 2.0 ** -8 * np.abs(ro) + (rounded + 2 * x * size) * (1 + 2.0 ** -7)).all(), (b, r)
+            assert abs(lse[b, r] - rl) <= x + 2.0 ** -22 * abs(rl)
+
+
 def test_attend_tiny_and_huge_queries():
     c = pu.Cache([200, 90], 1, 64, 64, seed=11)
     q, cu, d_cu = pu.queries([1, 1], 4, 64, seed=11)
