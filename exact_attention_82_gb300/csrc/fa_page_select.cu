@@ -419,7 +419,8 @@ cudaError_t launch_page_select(int D, const SelectParams &p, cudaStream_t stream
     void (*const f)(SelectParams) = D == 64 ? fa_page_select_kernel<64> : fa_page_select_kernel<128>;
     const size_t smem = p.max_pages * sizeof(uint32_t);
     if (smem > 32 * 1024) {  // beyond what a kernel may have, beside its own arrays, without asking
-        const cudaError_t e = cudaFuncSetAttribute((const void *)f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // always the most: the limit is the function's, and another thread's call would lower one set to this call's size
+        const cudaError_t e = cudaFuncSetAttribute((const void *)f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectMaxPages * (int)sizeof(uint32_t));
         if (e != cudaSuccess) return e;
     }
     return launch_early(f, dim3(size, p.Hkv, p.B), kSelThreads, smem, stream, size, p);

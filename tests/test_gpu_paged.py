@@ -2,6 +2,8 @@
 fa_page_select, fa_fwd_paged) against plain 64-bit implementations of their
 definitions, at the sizes and contents where they can go wrong, and a run of them
 together as a serving loop uses them."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -221,6 +223,47 @@ def test_select_wide_tables(width, G, D):
     c.ms[:] = np.linspace(0.5, 2, 5).astype(np.float32)[np.arange(c.num_pages) % 5, None]   # five values: many ties
     c.d_mean, c.d_ms = torch.from_numpy(c.mean).cuda(), torch.from_numpy(c.ms).cuda()
     run_select(c, q, cu, d_cu, 64, 0, 0)
+
+
+def two_threads(*calls, times=3000):
+    """Makes the calls again and again, each in a thread and on a stream of its own; what they raise is raised."""
+    failed = []
+
+    def loop(call):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(times):
+                    call()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=loop, args=(call,)) for call in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if failed:
+        raise failed[0]
+
+
+def test_select_in_two_threads():
+    """Tables of different widths, all of which need more shared memory than a kernel has without asking."""
+    calls, checks = [], []
+    for width in (49152, 8300):
+        c = pu.Cache([40], 1, 16, 64, seed=1)
+        table, lens = torch.zeros((1, width), dtype=torch.int32, device="cuda"), i32([16 * 40])
+        table[0, :40] = i32([int(p) for p in np.arange(40) % c.num_pages])
+        q, cu, d_cu = pu.queries([1], 2, 64, seed=1)
+        args = (q, d_cu, lens, table, c.d_mean, c.d_ms, 16, 5)
+        want, _ = fa.fa_page_select(*args)
+        out = dict(sel=torch.empty_like(want), sel_count=torch.empty((1, 1), dtype=torch.int32, device="cuda"))
+        calls.append(lambda args=args, out=out: fa.fa_page_select(*args, **out))
+        checks.append((out["sel"], want))
+    two_threads(*calls)
+    for got, want in checks:
+        assert torch.equal(got, want)
 
 
 def test_select_pages_outside_the_cache_come_last():
