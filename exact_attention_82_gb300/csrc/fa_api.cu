@@ -502,7 +502,7 @@ constexpr int kMostCounted = 1 << 30;
 
 // What the cache's entry points share; FA_OK when the sizes are in range.
 int check_cache(int B, int T, int Hkv, int D, int max_pages, int num_pages, int page_size) {
-    if (B < 1 || B > 8192 || T < 1 || T > kMostCounted || Hkv < 1 || Hkv > 1024 || max_pages < 1 || num_pages < 1)
+    if (B < 1 || B > fa::kMaxSequences || T < 1 || T > kMostCounted || Hkv < 1 || Hkv > 1024 || max_pages < 1 || num_pages < 1)
         return FA_ERR_BAD_SHAPE;
     if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED_D;
     if (page_log2_of(page_size) < 0) return FA_ERR_BAD_PAGE;
@@ -640,7 +640,7 @@ extern "C" int fa_page_select(const void *q, const int *cu_q, const int *seq_len
 }
 
 static bool paged_shape_ok(int B, int T, int Hq, int Hkv, int D) {
-    return B >= 1 && B <= 8192 && T >= 1 && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
+    return B >= 1 && B <= fa::kMaxSequences && T >= 1 && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
            (D == 64 || D == 128);
 }
 

@@ -157,7 +157,9 @@ cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream
     if (grid > 4ll * num_sms) grid = 4ll * num_sms;
     const int smem = 2 * (p.B + 1) * (int)sizeof(int);
     if (smem > 48 * 1024) {  // beyond what a kernel may have without asking
-        const cudaError_t e = cudaFuncSetAttribute(fa_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // always the most: the limit is the function's, and another thread's call would lower one set to this call's size
+        const cudaError_t e = cudaFuncSetAttribute(fa_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   2 * (kMaxSequences + 1) * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
     return launch_early(fa_kv_plan_kernel, dim3((unsigned)grid), kPlanThreads, smem, stream, 1, p);

@@ -7,6 +7,8 @@
 
 namespace fa {
 
+constexpr int kMaxSequences = 8192;  // of a call; fa_kv_plan's sums of that many stay in shared memory
+
 struct PlanParams {
     const int *cached, *fresh;   // [B] tokens in the cache, tokens of this step
     const int *free_pages, *free_count;

@@ -63,6 +63,22 @@ def test_plan_invalid_requests():
     run_plan([big, 0, 1], [big, big, 5], [1, 2], 2, np.full((3, 2), 0), 12, 4, 64)  # sums past 32 bits
 
 
+def test_plan_in_two_threads():
+    """Batches of different sizes, all of which need more shared memory than a kernel has without asking."""
+    calls, checks = [], []
+    for B in (8192, 6200):
+        one = torch.ones(B, dtype=torch.int32, device="cuda")
+        table = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+        out = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B + 1, B, B, 1)]
+        args = (one, one.clone(), i32([0]), i32([0]), table, B, 16, *out)
+        calls.append(lambda args=args: fa.fa_kv_plan(*args))
+        checks.append(out)
+    two_threads(*calls)
+    for cu, lens, slots, left in checks:
+        assert torch.equal(cu, torch.arange(cu.numel(), device="cuda", dtype=torch.int32)) and int(left) == 0
+        assert bool((lens == 2).all()) and bool((slots == 1).all())
+
+
 # ------------------------------------------------------------------ append
 def run_append(lens, new, Hkv, page, D, seed, pad=0, means=True, change=None, gap=False):
     """Appends `new` tokens behind `lens` cached ones and compares every page and scale."""
