@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
                     for (int j = 0; j < 8; ++j) {
                         const float x = y[j];
                         y[j] = x * inv_scale;
-                        y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
+                        if (fabsf(x) < INFINITY) y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
                     }
                 }
                 const uint2 c = encode8(y);

@@ -178,6 +178,24 @@ def test_append_beside_scales_that_are_no_powers_of_two():
         assert np.array_equal(pu.codes_of(got), codes)
 
 
+def test_append_infinities_beside_scales_that_are_no_powers_of_two():
+    """Infinities become the largest codes, whatever scale the page has."""
+    for page, D in ((16, 64), (128, 128)):
+        c = pu.Cache([page + 7, page + 3], 2, page, D, seed=19)
+        c.ks *= 1.5
+        c.vs *= 1.25
+        c.d_ks, c.d_vs = torch.from_numpy(c.ks).float().cuda(), torch.from_numpy(c.vs).float().cuda()
+        x = torch.randn((3, 2, D), generator=torch.Generator().manual_seed(19)).to(torch.bfloat16) * 0.5
+        x[0, :, 3], x[0, :, 4], x[1, 1, 5], x[2, :, 9] = float("inf"), float("-inf"), float("nan"), float("-inf")
+        slots = np.array([int(c.table[0, 1]) * page + 5 + i for i in range(2)] + [int(c.table[1, 1]) * page + 2], np.int32)
+        fa.fa_kv_append(x.cuda(), x.cuda(), torch.from_numpy(slots).cuda(), *c.pages)
+        for codes, scale, got, got_scale in ((c.kc, c.ks, c.d_kc, c.d_ks), (c.vc, c.vs, c.d_vc, c.d_vs)):
+            pu.append(pu.f64(x), slots, codes, scale, page)
+            got = pu.codes_of(got)
+            assert np.array_equal(pu.f64(got_scale), scale)
+            assert ((got == codes) | (np.isnan(pu.E4M3[got]) & np.isnan(pu.E4M3[codes]))).all()
+
+
 def test_append_bad_slots_are_skipped_and_reported():
     c = pu.Cache([20], 2, 16, 64, seed=9)
     before = [t.clone() for t in c.pages]
