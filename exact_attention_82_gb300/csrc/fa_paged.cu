@@ -6,7 +6,7 @@
 // scales ks_j, vs_j, in base 2 (c = scale log2 e):
 //   x_rj = c ks_j (q_r . k_j) + log2 vs_j,
 //   w_rj = 2^(x_rj - m_r + 8)                    (the weight of the CODES v_j)
-//   O_r  = sum_j w_rj v_j / l_r,   l_r = sum_j w_rj / vs_j,
+//   O_r  = sum_j w_rj v_j / l_r,   l_r = sum_j w_rj / vs_j  (kept as 2^-12 of it),
 //   LSE_r = ln2 (m_r - 8 + log2 l_r),
 // for any m_r.  m_r is the largest x_rj so far when it was last taken, and is taken
 // again when some x_rj exceeds it by more than 7, so w is at most 2^15 however
@@ -79,6 +79,10 @@ constexpr int kPgMaxLen = 0x7fffff00;
 constexpr float kPgShift = 8.f;    // exponent of a weight at x = m
 constexpr float kPgMost = 15.f;    // and the largest one
 constexpr float kPgNone = -3e38f;  // m before any key
+// What l is kept scaled by, 2^-12: beside the smallest value scale of 2^-100 a weight of 2^15 adds 2^115 to
+// it, and 8192 keys would pass the largest float; now 2^25 (2^32 of a weight of 2^8).  At the other end, 2^120, l is
+// still 2^-124 or more.
+constexpr float kPgDown = 12.f;
 // log2 of how far value scales may lie apart before weights are rounded apart (see above).  Scales of pages
 // that hold like values differ by 1 or 2.  Where one page in 64 is zeros beside small values, 8 sequences of 16384
 // keys take 50.4 us for 49.6, drafts of 16 to 40 rows 92 for 75; every second page 51.1 and 85.
@@ -390,16 +394,20 @@ __device__ __forceinline__ float *slot_of(float *ws, int blocks, int worker, int
     return ws + (long long)blocks * (sizeof(Tail) / 4) + (2ll * worker + slot) * nr * (D + 2);
 }
 
-// m - 8 + log2 l in base e.  l's exponent is added to m before its mantissa's
+// m - 8 + 12 + log2 l in base e.  l's exponent is added to m before its mantissa's
 // logarithm: both are near what LSE is not, and would cost it their rounding.
 __device__ __forceinline__ float lse_of(float m, float l) {
     const uint32_t u = __float_as_uint(l);
-    const float whole = (float)((int)(u >> 23) - 127) - kPgShift;
+    const float whole = (float)((int)(u >> 23) - 127) + (kPgDown - kPgShift);
     const float frac = log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
     if (l == 0.f) return -INFINITY;
     if (!(l < INFINITY)) return m + l;
     return ((m + whole) + frac) * 0.69314718055994531f;
 }
+
+// What O's sums are multiplied with.
+__device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : 0x1p-12f / l; }
+static_assert(kPgDown == 12.f, "");
 
 // The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
 // The token of a sequence that a row belongs to.
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                 for (int half = 0; half < HB; ++half) {  // the value scale's logarithm, exact for powers of two, and its inverse
                     const int u = __float_as_int(meta[half].z);
                     meta[half].z = fmaxf((float)((u >> 23) - 127) + lg2_approx(__int_as_float((u & 0x7fffff) | 0x3f800000)), -100.f);
-                    meta[half].w = ex2_approx(-meta[half].z);
+                    meta[half].w = ex2_approx(-meta[half].z) * 0x1p-12f;
                     if (key[half] != kPgMaxLen) z_top = fmaxf(z_top, meta[half].z);
                 }
                 bool apart = false;  // whether some keys' value scale is far below one before
@@ -816,7 +824,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll
                                 for (int e = j; e < 4; e += 2) {
                                     w[e] = ex2_approx(yh[e] - x);
-                                    l[nt][j] = fmaf(w[e], back[half][nt][j] * meta[half].w, l[nt][j]);
+                                    l[nt][j] = fmaf(w[e] * back[half][nt][j], meta[half].w, l[nt][j]);
                                 }
                             }
                             wf[half][nt][0] = movmatrix_trans(pack_f16x2(w[0], w[1]));
@@ -934,7 +942,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 #pragma unroll 4
                         for (int w = lead; w <= last; ++w) L = fmaf(join_l[w][lane], ex2_approx(join_m[w][lane] - M), L);
                         join_f[warp][lane] = ex2_approx(join_m[warp][lane] - M);
-                        inv_of[warp][lane] = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+                        inv_of[warp][lane] = whole ? inverse_of(L) : 1.f;
                         if (warp == lead) {
                             if (!whole)
                                 part[NR * D + lane] = M, part[NR * D + NR + lane] = L;
@@ -979,7 +987,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                         for (int c = 0; c < C::CHUNKS; ++c) o[8 * c] = make_float2(acc[c][nt][j], acc[c][nt][j + 2]);
                         if (g == 0) part[NR * D + r] = m[nt][j], part[NR * D + NR + r] = l[nt][j];
                     } else if (it->row0 + r < it->rows) {
-                        const float inv = l[nt][j] == 0.f ? 0.f : 1.f / l[nt][j];
+                        const float inv = inverse_of(l[nt][j]);
                         const long long at = out_row(p, it->q0, it->nq, it->h, it->row0 + r);
                         uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + pg;
 #pragma unroll
@@ -1069,7 +1077,7 @@ struct JoinRow {
     }
     __device__ __forceinline__ void write(const PagedParams &p, long long at) {
         const int lane = threadIdx.x & 31;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = inverse_of(L);
         uint32_t *const o = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + at * D) + lane * (E / 2);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) o[e] = pack_bf16x2(O[2 * e] * inv, O[2 * e + 1] * inv);

@@ -268,7 +268,9 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * each key/value head, in e4m3 codes with one fp32 scale per page and head:
  *
  *   k_pages, v_pages   e4m3 [num_pages, Hkv, page_size, D]   value = code * scale
- *   k_scale, v_scale   fp32 [num_pages, Hkv], finite and > 0
+ *   k_scale, v_scale   fp32 [num_pages, Hkv], finite and > 0; v_scale of 2^-100 to
+ *                      2^120 (as fa_kv_append gives it), those of one sequence's pages
+ *                      within a factor of 2^100 of one another
  *   k_mean             int8 [num_pages, Hkv, D]  and
  *   k_mean_scale       fp32 [num_pages, Hkv]: the page's mean key, m * scale
  *                      (only fa_page_select reads them)

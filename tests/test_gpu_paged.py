@@ -595,6 +595,23 @@ def test_attend_small_values_beside_one_large_value_that_is_hardly_seen(D):
             assert abs(lse[b, r] - rl) <= x + 2.0 ** -22 * abs(rl)
 
 
+@pytest.mark.parametrize("e", [-100, 112])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
+def test_attend_millions_of_extreme_values(D, page, e):
+    """The smallest value scale that fa_kv_append gives, 2^-100, at 2^21 keys of one score (the sum of weights
+    divided by it passes 2^128), and one near the largest.  O is the mean of the values, LSE is ln 2^21."""
+    n = 2 ** 21 // page
+    codes = (8 + torch.arange(page, device="cuda") % 100).to(torch.uint8).view(1, 1, page, 1).expand(1, 1, page, D).contiguous()
+    q, table = torch.zeros((1, 1, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, n), dtype=torch.int32, device="cuda")
+    o, lse = fa.fa_fwd_paged(q, i32([0, 1]), i32([2 ** 21]), table, codes, codes.clone(), torch.ones((1, 1), device="cuda"),
+                             torch.full((1, 1), 2.0 ** e, device="cuda"))
+    mean = pu.E4M3[8 + np.arange(page) % 100].mean() * 2.0 ** e
+    # Scores of 0 give every key the same weight, a power of two, which fp16 holds: what is left are O's rounding to
+    # bf16 and fp32 sums, of up to 2^21 / 152 / 8 keys by one warp (2^-24 each at worst, where all round one way)
+    assert np.abs(pu.f64(o) / mean - 1).max() <= 2.0 ** -8 + 2.0 ** -24 * 2 ** 21 / 152 / 8
+    assert abs(float(lse) - 21 * np.log(2)) <= 2.0 ** -24 * 2 ** 21 / 152 / 8 + 2.0 ** -22 * 15
+
+
 def test_attend_tiny_and_huge_queries():
     c = pu.Cache([200, 90], 1, 64, 64, seed=11)
     q, cu, d_cu = pu.queries([1, 1], 4, 64, seed=11)
