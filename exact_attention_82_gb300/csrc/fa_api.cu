@@ -608,7 +608,7 @@ extern "C" int fa_page_select(const void *q, const int *cu_q, const int *seq_len
     const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
     if (st != FA_OK) return st;
     if (Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || !stride_ok(q_stride, Hq, D) || max_pages > fa::kSelectMaxPages ||
-        top_k < 1 || top_k > kMostCounted || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > top_k)
+        (long long)T * Hq > 0x7fffffff || top_k < 1 || top_k > kMostCounted || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > top_k)
         return FA_ERR_BAD_SHAPE;
     const Span outs[2] = {{sel, (size_t)B * Hkv * top_k * 4}, {sel_count, (size_t)B * Hkv * 4}};
     const Span ins[6] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},

@@ -378,7 +378,7 @@ int fa_kv_append(const void *k, const void *v, const int *slot_map, void *k_page
  * keep_first and the last keep_last pages come before all others, then higher
  * scores, and the lower position among equals; pages outside the cache last.
  * 1 <= top_k <= 2^30, keep_first, keep_last >= 0, keep_first + keep_last <= top_k.
- * max_pages <= 49152.
+ * max_pages <= 49152, T * Hq < 2^31.
  * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE,
  * FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
  */

@@ -88,6 +88,12 @@ def test_counts_that_an_int_cannot_step_past(call, name):
         assert call(**{**kw, name: n}) == fa.FA_ERR_BAD_SHAPE
 
 
+@pytest.mark.parametrize("call", [select, attend])
+@pytest.mark.parametrize("T,Hq", [(1 << 30, 2), (1 << 20, 1 << 15), (1 << 25, 64)])
+def test_query_rows_that_an_int_does_not_count(call, T, Hq):
+    assert call(T=T, Hq=Hq, Hkv=1, qs=64 * Hq) == fa.FA_ERR_BAD_SHAPE
+
+
 @pytest.mark.parametrize("scale", [float("nan"), float("inf"), 0.0, -0.5, 3e38])
 def test_attend_scale(scale):
     assert attend(scale=scale) == fa.FA_ERR_BAD_SCALE
