@@ -640,8 +640,8 @@ extern "C" int fa_page_select(const void *q, const int *cu_q, const int *seq_len
 }
 
 static bool paged_shape_ok(int B, int T, int Hq, int Hkv, int D) {
-    return B >= 1 && B <= fa::kMaxSequences && T >= 1 && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
-           (D == 64 || D == 128);
+    return B >= 1 && B <= fa::kMaxSequences && T >= 1 && T <= kMostCounted && Hkv >= 1 && Hkv <= 1024 && Hq >= 1 && Hq <= 65535 &&
+           Hq % Hkv == 0 && (long long)T * Hq <= 0x7fffffff && (D == 64 || D == 128);
 }
 
 extern "C" size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
@@ -663,9 +663,7 @@ extern "C" int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens,
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o)) return FA_ERR_MISALIGNED;
     const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
     if (st != FA_OK) return st;
-    if (!paged_shape_ok(B, T, Hq, Hkv, D) || !stride_ok(q_stride, Hq, D) || (sel && sel_width < 1) ||
-        (long long)T * Hq > 0x7fffffff)
-        return FA_ERR_BAD_SHAPE;
+    if (!paged_shape_ok(B, T, Hq, Hkv, D) || !stride_ok(q_stride, Hq, D) || (sel && sel_width < 1)) return FA_ERR_BAD_SHAPE;
     const float scale_log2 = scale * 1.4426950408889634f;
     if (!isfinite(scale) || !(scale > 0.f) || !isfinite(scale_log2)) return FA_ERR_BAD_SCALE;
     const size_t need = fa::paged_workspace_bytes(B, T, Hq, Hkv, D, sm_count());

@@ -109,6 +109,13 @@ def test_attend_workspace():
         assert fa.fa_fwd_paged_workspace_bytes(*bad) == 0
 
 
+@pytest.mark.parametrize("B,T,Hq,Hkv,D", [(2, 2 ** 30 + 1, 1, 1, 64), (2, 2 ** 31 - 1, 1, 1, 128), (2, 1 << 30, 2, 1, 64),
+                                          (2, 1 << 16, 1 << 15, 1, 64)])
+def test_no_workspace_for_sizes_that_are_refused(B, T, Hq, Hkv, D):
+    assert attend(B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, qs=Hq * D) == fa.FA_ERR_BAD_SHAPE
+    assert fa.fa_fwd_paged_workspace_bytes(B, T, Hq, Hkv, D) == 0
+
+
 def test_aliases():
     p = list(A[:9])
     p[8] = p[3]  # free_left over free_count
