@@ -411,6 +411,7 @@ def _binding():
         lib()
         with _lock:
             if _binding_module is None:
+                _build.build_binding()
                 loader = importlib.machinery.ExtensionFileLoader("fa_binding", _build.BINDING_PATH)
                 module = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_binding", loader))
                 loader.exec_module(module)

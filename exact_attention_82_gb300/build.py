@@ -3,7 +3,8 @@ extension machinery): each .cu is compiled in parallel, then linked with the
 static CUDA runtime into ``_build/libfa_gb300.so``.  The driver's tensor-map
 encoder is looked up at run time, so the library does not link libcuda.  The
 paged cache's calls for torch tensors are a small CPython extension beside it
-(``fa_binding.cpp``, compiled with g++ against torch's headers).
+(``fa_binding.cpp``, compiled with g++ against torch's headers).  Only those
+calls need it: the library is built and loaded without torch or g++.
 """
 from __future__ import annotations
 
@@ -38,18 +39,34 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the library")
 
 
+def _gxx() -> str:
+    path = shutil.which("g++")
+    if path is None:
+        raise RuntimeError("g++ not found: the paged cache's calls on tensors need it (their *_raw forms do not)")
+    return path
+
+
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + [BINDING_SOURCE]]
+    files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "fa.h"))
     return files
 
 
+def _binding_inputs():
+    return [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "fa.h")]
+
+
+def _newer(path: str, inputs) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _newer(LIB_PATH, _inputs())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING_PATH, _binding_inputs())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -62,34 +79,38 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     def compile_one(src):
         obj = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *ARCH, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr, file=sys.stderr)
+        _run([cc, *ARCH, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc on {src}", verbose)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding, verbose)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([cc, *ARCH, "-shared", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"],
+         "linking the library", verbose)
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj)
     return LIB_PATH
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link the calls on torch tensors, and the library that they need; returns their path."""
+    if not force and binding_up_to_date() and up_to_date():
+        return BINDING_PATH
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=2) as ex:
+        lib = ex.submit(build, force, verbose)
+        binding = ex.submit(_compile_binding, verbose)
+        lib.result()  # whatever becomes of the binding, the library is in its place
+        _link_binding(binding.result(), verbose)
+    return BINDING_PATH
 
 
 def _torch_dir() -> str:
     import importlib.util
 
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed: the paged cache's calls on tensors need it (their *_raw forms do not)")
+    return os.path.dirname(spec.origin)
 
 
 def _run(cmd, what: str, verbose: bool = False):
@@ -98,25 +119,27 @@ def _run(cmd, what: str, verbose: bool = False):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr, file=sys.stderr)
 
 
 def _compile_binding(verbose: bool) -> str:
     obj = os.path.join(OUT_DIR, "fa_binding.o")
     inc = os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_path("include"), "-isystem", inc,
+    _run([_gxx(), "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_path("include"), "-isystem", inc,
           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-c",
           os.path.join(CSRC, BINDING_SOURCE), "-o", obj], f"g++ on {BINDING_SOURCE}", verbose)
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(obj: str, verbose: bool) -> None:
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     libs = os.path.join(_torch_dir(), "lib")
-    _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, LIB_PATH, "-L", libs, "-ltorch_python", "-lc10_cuda", "-lc10",
-          "-ltorch_cpu", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], "linking the binding")
+    _run([_gxx(), "-shared", "-o", tmp, obj, LIB_PATH, "-L", libs, "-ltorch_python", "-lc10_cuda", "-lc10",
+          "-ltorch_cpu", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], "linking the binding", verbose)
     os.replace(tmp, BINDING_PATH)
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_binding(force="--force" in sys.argv, verbose="-v" in sys.argv))
