@@ -49,12 +49,26 @@ def _gxx() -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files.append(os.path.join(INCLUDE, "fa.h"))
+    files += [os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)]
     return files
 
 
 def _binding_inputs():
-    return [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "fa.h")]
+    return [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)]
+
+
+def _binding_key() -> str:
+    """What the binding's binary interface depends on: torch's build and Python's."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('EXT_SUFFIX')}\n{_torch_dir()}\n{f.read()}"
+
+
+def _binding_key_was() -> str | None:
+    try:
+        with open(BINDING_PATH + ".key") as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _newer(path: str, inputs) -> bool:
@@ -66,7 +80,7 @@ def up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    return _newer(BINDING_PATH, _binding_inputs())
+    return _newer(BINDING_PATH, _binding_inputs()) and _binding_key_was() == _binding_key()
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -138,7 +152,10 @@ def _link_binding(obj: str, verbose: bool) -> None:
     libs = os.path.join(_torch_dir(), "lib")
     _run([_gxx(), "-shared", "-o", tmp, obj, LIB_PATH, "-L", libs, "-ltorch_python", "-lc10_cuda", "-lc10",
           "-ltorch_cpu", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], "linking the binding", verbose)
+    with open(tmp + ".key", "w") as f:
+        f.write(_binding_key())
     os.replace(tmp, BINDING_PATH)
+    os.replace(tmp + ".key", BINDING_PATH + ".key")
 
 
 if __name__ == "__main__":

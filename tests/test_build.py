@@ -72,3 +72,31 @@ def test_a_binding_that_does_not_compile_leaves_the_library(commands, monkeypatc
     with pytest.raises(RuntimeError, match="no such header"):
         b.build_binding()
     assert os.path.exists(b.LIB_PATH) and not os.path.exists(b.BINDING_PATH)
+
+
+@pytest.mark.parametrize("changed", ["torch", "python", "build.py"])
+def test_the_binding_is_built_anew_after_a_change_of(changed, commands, monkeypatch, tmp_path):
+    """It holds torch's and Python's binary interfaces, whose change leaves the sources' times alone."""
+    torch_dir = tmp_path / "torch"
+    torch_dir.mkdir()
+    (torch_dir / "version.py").write_text("__version__ = '1.0'")
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: type("Spec", (), {"origin": str(torch_dir / "__init__.py")})
+                        if name == "torch" else find(name, *a))
+    b.build_binding()
+    n = len(commands)
+    b.build_binding()
+    assert len(commands) == n, "built again without a change"
+    if changed == "torch":
+        (torch_dir / "version.py").write_text("__version__ = '1.1'")
+    elif changed == "python":
+        get = b.sysconfig.get_config_var
+        monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: ".cpython-999.so" if name == "EXT_SUFFIX" else get(name))
+    else:
+        later = os.path.getmtime(b.LIB_PATH) + 100
+        mtime = os.path.getmtime
+        monkeypatch.setattr(os.path, "getmtime", lambda p: later if os.path.basename(p) == "build.py" else mtime(p))
+    assert not b.binding_up_to_date()
+    assert b.up_to_date() == (changed != "build.py")
+    b.build_binding()
+    assert len(commands) > n
