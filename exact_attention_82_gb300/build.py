@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -89,19 +90,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
-    objs = []
+    # Objects lie in a folder of this build's own: another process may build at the same time.
+    with tempfile.TemporaryDirectory(dir=OUT_DIR) as work:
 
-    def compile_one(src):
-        obj = os.path.join(OUT_DIR, os.path.splitext(src)[0] + ".o")
-        _run([cc, *ARCH, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc on {src}", verbose)
-        return obj
+        def compile_one(src):
+            obj = os.path.join(work, os.path.splitext(src)[0] + ".o")
+            _run([cc, *ARCH, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc on {src}", verbose)
+            return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    _run([cc, *ARCH, "-shared", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"],
-         "linking the library", verbose)
-    os.replace(tmp, LIB_PATH)
+        with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+            objs = list(ex.map(compile_one, SOURCES))
+        tmp = os.path.join(work, LIB_NAME)
+        _run([cc, *ARCH, "-shared", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"],
+             "linking the library", verbose)
+        os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
 
@@ -110,11 +112,12 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if not force and binding_up_to_date() and up_to_date():
         return BINDING_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=2) as ex:
-        lib = ex.submit(build, force, verbose)
-        binding = ex.submit(_compile_binding, verbose)
-        lib.result()  # whatever becomes of the binding, the library is in its place
-        _link_binding(binding.result(), verbose)
+    with tempfile.TemporaryDirectory(dir=OUT_DIR) as work:
+        with cf.ThreadPoolExecutor(max_workers=2) as ex:
+            lib = ex.submit(build, force, verbose)
+            binding = ex.submit(_compile_binding, work, verbose)
+            lib.result()  # whatever becomes of the binding, the library is in its place
+            _link_binding(binding.result(), work, verbose)
     return BINDING_PATH
 
 
@@ -137,8 +140,8 @@ def _run(cmd, what: str, verbose: bool = False):
         print(r.stdout + r.stderr, file=sys.stderr)
 
 
-def _compile_binding(verbose: bool) -> str:
-    obj = os.path.join(OUT_DIR, "fa_binding.o")
+def _compile_binding(work: str, verbose: bool) -> str:
+    obj = os.path.join(work, "fa_binding.o")
     inc = os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     _run([_gxx(), "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_path("include"), "-isystem", inc,
@@ -147,8 +150,8 @@ def _compile_binding(verbose: bool) -> str:
     return obj
 
 
-def _link_binding(obj: str, verbose: bool) -> None:
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+def _link_binding(obj: str, work: str, verbose: bool) -> None:
+    tmp = os.path.join(work, "fa_binding.so")
     libs = os.path.join(_torch_dir(), "lib")
     _run([_gxx(), "-shared", "-o", tmp, obj, LIB_PATH, "-L", libs, "-ltorch_python", "-lc10_cuda", "-lc10",
           "-ltorch_cpu", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"], "linking the binding", verbose)

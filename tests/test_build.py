@@ -100,3 +100,14 @@ def test_the_binding_is_built_anew_after_a_change_of(changed, commands, monkeypa
     assert b.up_to_date() == (changed != "build.py")
     b.build_binding()
     assert len(commands) > n
+
+
+def test_builds_at_the_same_time_write_files_of_their_own(commands):
+    """Nothing that one build compiles lies where another one compiles the same source."""
+    written = []
+    for _ in range(2):
+        b.build_binding(force=True)
+        written.append({c[c.index("-o") + 1] for c in commands})
+        commands.clear()
+    assert len(written[0]) == len(b.SOURCES) + 3 and not written[0] & written[1]
+    assert sorted(os.listdir(b.OUT_DIR)) == ["fa_binding.so", "fa_binding.so.key", b.LIB_NAME]
