@@ -300,6 +300,21 @@ def test_select_in_two_threads():
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("n", [8193, 16385, 16400, 40001, 49152])
+def test_select_widest_tables(n):
+    """Tables beyond what a kernel's shared memory holds without asking, and lists of more than 32 positions a
+    thread; many entries of the table are the same page, so that scores tie all along."""
+    rng = np.random.default_rng(n)
+    c = pu.Cache([16 * 300], 1, 16, 64, seed=n)
+    c.table = rng.integers(0, c.num_pages, size=(2, n)).astype(np.int32)
+    c.table[1] = np.arange(n) % 3
+    c.lens = [16 * n, 16 * n - 9]
+    c.d_table, c.d_lens = torch.from_numpy(c.table).cuda(), i32(c.lens)
+    q, cu, d_cu = pu.queries([1, 2], 3, 64, seed=n)
+    for top in (7, n // 2, n - 1):
+        run_select(c, q, cu, d_cu, top, 1, 2)
+
+
 def test_select_pages_outside_the_cache_come_last():
     c = pu.Cache([800], 1, 16, 64, seed=5)
     q, cu, d_cu = pu.queries([1], 2, 64, seed=6)
@@ -649,6 +664,27 @@ def test_attend_lengths_past_the_table_are_held_to_it():
     o, lse = fa.fa_fwd_paged(q, d_cu, c.d_lens, c.d_table, *c.pages)
     ref = pu.attend(pu.f64(q), np.array([0, 2, 2]), [64, 0], c.table, c.kc, c.vc, c.ks, c.vs, 0.125, 16)
     pu.check_attend(o, lse, ref)
+
+
+@pytest.mark.parametrize("selected", [False, True])
+def test_attend_refuses_tokens_that_pass_their_number_many_times(selected):
+    """cu_q that does not ascend, so that every other sequence has all tokens and their work, laid end to end,
+    passes what 32 bits count: nothing is written, and the status word says so."""
+    B, T, Hkv, page, W = 4000, 600, 8, 128, 9000
+    q = torch.zeros((T, Hkv, 64), dtype=torch.bfloat16, device="cuda")
+    codes, ones = torch.zeros((1, Hkv, page, 64), dtype=torch.uint8, device="cuda"), torch.ones((1, Hkv), device="cuda")
+    o, lse = torch.full_like(q, 777.0), torch.full((T, Hkv), 777.0, device="cuda")
+    cu = i32([0, T] * (B // 2) + [0])
+    if selected:
+        table, sel = torch.zeros((B, 1), dtype=torch.int32, device="cuda"), torch.zeros((B, Hkv, W // 4), dtype=torch.int32, device="cuda")
+        extra = dict(sel=sel, sel_count=torch.full((B, Hkv), W // 4, dtype=torch.int32, device="cuda"))
+        lens = torch.full((B,), page, dtype=torch.int32, device="cuda")
+    else:
+        table, extra = torch.zeros((B, W // 4), dtype=torch.int32, device="cuda"), {}
+        lens = torch.full((B,), W // 4 * page, dtype=torch.int32, device="cuda")
+    fa.fa_fwd_paged(q, cu, lens, table, codes, codes.clone(), ones, ones.clone(), o=o, lse=lse, **extra)
+    assert fa.fa_device_status() == fa.FA_ERR_BAD_SHAPE
+    assert bool((o == 777).all()) and bool((lse == 777).all())
 
 
 def test_offsets_past_32_bits():
