@@ -261,8 +261,11 @@ struct AppendCfg {
     static constexpr int PASSES = PAGE / ROWS;
     // Blocks an SM that the registers are held to.  A team waits for memory three times
     // (slots, rows, and to be written), so more of them side by side is faster, until they
-    // spill (much): a 16384-token prompt with 7, 8, 9 and 10 blocks 18.4, 18.1, 17.8 and 17.3 us;
-    // ragged prompts at 16 rows a page, D = 64, with 8, 9, 10 and 12 blocks 15.0, 14.3, 13.7 and 14.1.
+    // spill much.  At 10 all forms have 48 registers and spill 140 to 244 bytes, but for D = 64 with
+    // pages of 16.  A 16384-token prompt with 8, 9, 10 and 12 blocks, pages of 16, 32, 64, 128:
+    //   D = 128  18.2 18.6 18.1 20.3,  18.4 18.7 17.7 20.3,  18.6 18.8 17.4 19.1,  20.3 20.6 20.5 21.5 us;
+    //   D = 64   12.3 12.0 12.1 11.7,  12.2 11.9 11.9 11.6,  11.8 11.6 11.6 11.2,  11.9 12.3 12.4 12.6;
+    // ragged prompts at 16 rows a page, D = 64, 14.5, 14.3, 13.7 and 14.1.
     static constexpr int BLOCKS = 10 * 128 / THREADS;
 };
 

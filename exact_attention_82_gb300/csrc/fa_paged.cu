@@ -25,12 +25,15 @@
 // for each query row, so for a few rows (grouped heads, drafts) the HBM stream.
 // The products are computed transposed, S^T = K Q^T and O^T = V^T W^T, so that
 // the long side of the MMA tile (16) lies along the keys or the head dimension
-// and the short one (8) along the few query rows; the tensor cores' 128-row
-// tcgen05 tiles would be filled to a sixteenth, wait on TMEM for every tile, and
-// need the softmax's row sums across lanes.  Here each warp streams its own
+// and the short one (8) along the few query rows.  Each warp streams its own
 // tiles of 32 keys through a private ring of asynchronous copies and keeps its own
 // running maximum and sums: nothing waits for another warp before the end of an
-// item.
+// item.  tcgen05's tiles would lie the same way, 128 keys or D by 8 or more rows, but
+// take their operands from shared memory: codes converted to fp16 would be written
+// back there (its 8-bit kinds take them as they are, and would need queries and weights
+// as several 8-bit terms), and scores and weights would pass through TMEM and shared memory
+// between the products.  Up to 8 rows there is nothing to gain, the stream runs at the copy
+// rate; beyond, where this kernel is bound by its own instructions, it is not built.
 //
 // Split.  The tiles of all items (sequence, key/value head, 8 to 32 query rows)
 // are laid end to end, each item behind a few places that stand for its fixed
@@ -44,11 +47,12 @@
 // result a block in the workspace, which a second kernel joins.
 //
 // Measured (back to back, other inputs in turn, of 6,705 GB/s that a copy reaches): 8 sequences
-// of 65536 keys, 8 of 32 heads, D = 128, 163 us, 6,570 GB/s; of 16384 keys 50.4 us; with 16 query
-// rows 59 us; at D = 64 88 us for 65536; 64 ragged sequences of 50 to 8000 keys 44.8 us; one of 1000 keys,
-// 32 heads, 13.3 us, which is what a call takes without the stream: launch, lengths and shares 2.5,
-// pages and first keys 2, a block's join, the second kernel 1 to 2.  Beyond 8 rows it is bound by
-// its own instructions: 16 sequences with 16 to 40 rows each 74 us, 30.7 at the copy rate.
+// of 65536 keys, 8 of 32 heads, D = 128, 162 us, 6,600 GB/s; of 16384 keys 49.5 us, 81% of the copy rate;
+// with 16 query rows 59 us; at D = 64 87 us for 65536; 64 ragged sequences of 50 to 8000 keys 42.8 us.
+// What a call takes without the stream: 8.3 us for one sequence of 32 keys (two launches, lengths and
+// shares 2.5, one tile, the stores), 9.6 for one tile on every SM, 13.4 for one of 1000 keys and 32
+// heads, whose items are joined.  Beyond 8 rows it is bound by its own instructions: 16 sequences with
+// 16 to 40 rows each 75 us, 30.7 at the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -68,10 +72,10 @@ static __device__ int g_status_paged = 0;
 constexpr int kPgTile = 32;         // keys a tile; two halves of 16, each in one page
 constexpr int kPgFixed = 2;         // places of the line that an item's fixed cost takes
 constexpr int kPgMinShare = 36;     // places of a block: three tiles a warp
-// An item of an eighth of a share is not cut (16 sequences of 2000 to 16000 keys: 88 us
-// with half a share, whose blocks have up to one and a half of it, 80 us with an eighth or
-// less), nor is one of 8 places (256 sequences of 100 keys: 27 us without this, 23 us with
-// it).  What is not cut between warps must not be between blocks: else a warp's end
+// An item of an eighth of a share is not cut (16 sequences of 2000 to 16000 keys with 2 to 5
+// tokens: 84 us with half a share, whose blocks have up to one and a half of it, 73 with a quarter,
+// 74.5 with an eighth; 64 ragged sequences 44.2, 43.6 and 42.6), nor is one of 8 places (256 sequences
+// of 100 keys: 24.4 us without this, 21.2 with it).  What is not cut between warps must not be between blocks: else a warp's end
 // could be moved past its block's.
 constexpr int kPgSmall = 8;
 constexpr int kPgWhole = 8;
@@ -409,10 +413,10 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 __device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : 0x1p-12f / l; }
 static_assert(kPgDown == 12.f, "");
 
-// The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
 // The token of a sequence that a row belongs to.
 __device__ __forceinline__ int token_of(const PagedParams &p, int nq, int row) { return nq > 1 ? row / p.G : 0; }
 
+// The place of a row of (sequence, head) among the T * Hq rows of O and LSE.
 __device__ __forceinline__ long long out_row(const PagedParams &p, int q0, int nq, int h, int row) {
     const int tok = token_of(p, nq, row);
     return (long long)(q0 + tok) * (p.Hkv * p.G) + h * p.G + (row - tok * p.G);
@@ -1006,7 +1010,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
 // Joins the partial results of the items that cross blocks: each block of this kernel
 // takes every fourth row of the item that one of them left off, a warp a row, or the
 // whole block where there are many parts.  Bound by latency: 1 to 2 us behind the kernel
-// above (8 x 16384 keys: 51.4 us without it, 54.0 with it; reading the first parts before it
+// above (8 x 16384 keys at an earlier step: 51.4 us without it, 54.0 with it; reading the first parts before it
 // is known how many there are took off a third: ragged sequences 45.2 -> 44.1 us).
 constexpr int kJoinWarps = 4;
 constexpr int kJoinMany = 8;  // parts
@@ -1154,10 +1158,12 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
 
 // Rows of an item: 8 or 16 while a sequence's query rows are no more (by the mean
 // number of its tokens, padding rounded off).  Beyond, 32 at D = 64 (16 sequences of 16384
-// keys, 32 rows: 98 us, 118 us in two items of 16).  At D = 128 the sums of 32 rows leave
+// keys, 32 rows: 100 us, 119 us in two items of 16).  At D = 128 the sums of 32 rows leave
 // few registers, and items of 32 pay from more than 32 rows on: 8 sequences of 16384 keys with
-// 64 rows take 154 us, 174 us in items of 16; with 32 rows 97 and 100 us; but 16 ragged ones
-// with 16 to 40 rows 89 and 77 us.
+// 64 rows take 154 us, 172 us in items of 16; with 32 rows 97 and 98 us; but 16 ragged ones
+// with 16 to 40 rows 90 and 75 us.  The mean is all that the host knows, and batches of mixed
+// kinds pay for it: 63 sequences with one token beside one with 512 take 706 us, 96 and 443 in
+// two calls; 64 with one token each and T = 512 take 167 us, 98 with T = 64.
 static int item_rows(int D, const PagedParams &p) {
     const long long tokens = (2ll * p.T + p.B) / (2ll * p.B), rows = (tokens > 1 ? tokens : 1) * p.G;
     return rows <= 8 ? 8 : rows <= (D == 128 ? 32 : 16) ? 16 : 32;

@@ -298,7 +298,9 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * D is 64 or 128; q, k and v may be strided over tokens (strides in elements,
  * multiples of 8, each token's heads contiguous).  Tensors of codes and bf16 are
  * 16-byte aligned, int32 and fp32 arrays 4-byte aligned (FA_ERR_MISALIGNED).
- * num_pages * page_size and num_pages * Hkv < 2^31, B <= 8192, T <= 2^30, Hkv <= 1024, Hq a multiple of Hkv.
+ * num_pages * page_size, max_pages * page_size and num_pages * Hkv < 2^31, num_pages * Hkv *
+ * page_size < 2^32, strides < 2^40, B <= 8192, T <= 2^30, Hkv <= 1024, Hq <= 65535 and a multiple
+ * of Hkv.
  * These operations have no counterpart in the pages.
  */
 
@@ -324,7 +326,8 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * (a request that does not fit thus keeps later ones from taking pages).  One
  * that is not served keeps its row of block_table, gets slots of -1 and
  * seq_lens[b] = 0 (attention writes O = 0, LSE = -inf for its rows); its rows of
- * q, k and v stay counted in cu_q.  A slot whose page is outside the cache is -1.
+ * q, k and v stay counted in cu_q.  Where the new tokens are more than T, those behind
+ * T get no slot, though seq_lens counts them: give T at least their sum.  A slot whose page is outside the cache is -1.
  * Outputs may not overlap inputs or one another (free_left is not free_count).
  * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_BAD_SHAPE (B, T, max_pages,
  * num_free or num_pages < 1, or out of range: num_free <= 2^30), FA_ERR_BAD_PAGE, FA_ERR_ALIAS.
@@ -411,6 +414,8 @@ int fa_page_select(const void *q, const int *cu_q, const int *seq_lens, const in
  * the row's largest), O once to bf16.  Any number of query
  * tokens a sequence is taken; the kernel is made for a few (decode, drafts): 8 to 32
  * rows (query tokens times heads of the group) share a pass over the keys.
+ * How many is told from T / B, so T much above the tokens that there are, or one long
+ * run of tokens beside many single ones, costs time (a call for each kind is faster).
  * T * Hq < 2^31, and so is, at most, (T * Hq / Hkv / 8 + B) * Hkv times the 32-key
  * tiles of a full table row, plus 3 (FA_ERR_BAD_SHAPE).  Deterministic; no atomics on
  * results.
