@@ -8,8 +8,9 @@
 //   w_rj = 2^(x_rj - m_r + 8)                    (the weight of the CODES v_j)
 //   O_r  = sum_j w_rj v_j / l_r,   l_r = sum_j w_rj / vs_j  (kept as 2^-12 of it),
 //   LSE_r = ln2 (m_r - 8 + log2 l_r),
-// for any m_r.  m_r is the largest x_rj so far when it was last taken, and is taken
-// again when some x_rj exceeds it by more than 7, so w is at most 2^15 however
+// for any m_r.  m_r is the largest x_rj so far when it was last taken, rounded down to a
+// whole number (sums are then scaled exactly, and x - m loses nothing to a value scale's large
+// logarithm), and is taken again when some x_rj exceeds it by more than 7, so w is at most 2^15 however
 // unevenly the pages are scaled and can be rounded to fp16 (to 2^-11 of each; bf16 would
 // keep three bits less).  fp16's subnormal numbers end at 2^-24, which is 2^-32 of the largest
 // 2^x so far.  That may be a key's whose values are 0, for a page of zeros has scale 1, so
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(PgCfg<D, NT>::THREADS, 1) fa_fwd_paged_kernel(
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            x = fmaxf(x, m[nt][j]);
+                            x = fmaxf(floorf(x), m[nt][j]);
                             const float f = ex2_approx(m[nt][j] - x);
                             m[nt][j] = x;
                             l[nt][j] *= f;
@@ -1160,7 +1161,7 @@ static cudaError_t launch_paged(const PagedParams &p, int num_sms, cudaStream_t 
 // number of its tokens, padding rounded off).  Beyond, 32 at D = 64 (16 sequences of 16384
 // keys, 32 rows: 100 us, 119 us in two items of 16).  At D = 128 the sums of 32 rows leave
 // few registers, and items of 32 pay from more than 32 rows on: 8 sequences of 16384 keys with
-// 64 rows take 154 us, 172 us in items of 16; with 32 rows 97 and 98 us; but 16 ragged ones
+// 64 rows take 156 us, 172 us in items of 16; with 32 rows 97 and 98 us; but 16 ragged ones
 // with 16 to 40 rows 90 and 75 us.  The mean is all that the host knows, and batches of mixed
 // kinds pay for it: 63 sequences with one token beside one with 512 take 706 us, 96 and 443 in
 // two calls; 64 with one token each and T = 512 take 167 us, 98 with T = 64.

@@ -610,6 +610,20 @@ def test_attend_small_values_beside_one_large_value_that_is_hardly_seen(D):
             assert abs(lse[b, r] - rl) <= x + 2.0 ** -22 * abs(rl)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [8, 16, 40])
+@pytest.mark.parametrize("e", [-90, -58, 0, 60, 110])
+def test_attend_lse_does_not_depend_on_the_values_size(D, G, e):
+    """LSE is of the scores alone: a value scale's large logarithm takes nothing from it.  All keys are alike, so
+    that a row's LSE is its score and the logarithm of how many there are."""
+    c = pu.Cache([333, 1], 1, 32, D, seed=G)
+    c.kc[:], c.ks[:], c.vs[:] = 0x38, 1.0, 2.0 ** e       # 1.0
+    c.d_kc, c.d_ks, c.d_vs = torch.from_numpy(c.kc).cuda(), torch.from_numpy(c.ks).float().cuda(), torch.from_numpy(c.vs).float().cuda()
+    q, cu, d_cu = pu.queries([1, 1], G, D, seed=e)
+    q[:, :, 1:] = 0.0
+    run_attend(c, q, cu, d_cu)
+
+
 @pytest.mark.parametrize("e", [-100, 112])
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 128)])
 def test_attend_millions_of_extreme_values(D, page, e):
