@@ -24,7 +24,10 @@ __all__ = ["fa_fwd", "fa_fwd_raw", "fa_fwd_window", "fa_fwd_window_raw", "fa_str
            "fa_bwd", "fa_bwd_raw", "fa_fwd_fp8", "fa_fwd_fp8_raw",
            "fa_fwd_blockmask", "fa_fwd_blockmask_raw", "FA_ERR_BAD_MASK", "FA_BLOCK_M", "FA_BLOCK_N",
            "fa_kv_plan", "fa_kv_plan_raw", "fa_kv_append", "fa_kv_append_raw", "fa_page_select", "fa_page_select_raw",
-           "fa_fwd_paged", "fa_fwd_paged_raw", "fa_fwd_paged_workspace_bytes", "FA_ERR_BAD_PAGE", "FA_PAGE_SIZES"]
+           "fa_fwd_paged", "fa_fwd_paged_raw", "fa_fwd_paged_workspace_bytes", "FA_ERR_BAD_PAGE", "FA_PAGE_SIZES",
+           "fa_kv_plan_positions_raw", "fa_kv_append_rope", "fa_kv_append_rope_raw",
+           "fa_fwd_paged_chunk", "fa_fwd_paged_chunk_raw", "fa_fwd_paged_chunk_workspace_bytes",
+           "fa_rope", "fa_rope_raw", "fa_rope_bwd", "fa_rope_bwd_raw", "fa_rope_phases", "FA_ROPE_SCALINGS"]
 
 FA_OK = 0
 FA_ERR_NULLPTR = -1
@@ -44,6 +47,7 @@ FA_ERR_BAD_PAGE = -14
 FA_BLOCK_M = 128  # query rows per block-mask row
 FA_BLOCK_N = 128  # keys per block-mask column
 FA_PAGE_SIZES = (16, 32, 64, 128)  # tokens per page of the paged cache
+FA_ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}  # how fa_rope_phases stretches frequencies
 
 _lock = threading.Lock()
 _lib = None
@@ -51,6 +55,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _ll = ctypes.c_longlong
+_d = ctypes.c_double
 
 # name -> (restype, argtypes), mirroring include/fa.h
 _SIGNATURES = {
@@ -73,6 +78,13 @@ _SIGNATURES = {
     "fa_page_select": (_i, [_vp] * 8 + [_i] * 5 + [_ll] + [_i] * 6 + [_vp]),
     "fa_fwd_paged": (_i, [_vp] * 12 + [_i] * 5 + [ctypes.c_float, _ll] + [_i] * 4 + [_vp, ctypes.c_size_t, _vp]),
     "fa_fwd_paged_workspace_bytes": (ctypes.c_size_t, [_i] * 5),
+    "fa_kv_plan_positions": (_i, [_vp] * 10 + [_i] * 6 + [_vp]),
+    "fa_kv_append_rope": (_i, [_vp] * 13 + [_i] * 6 + [ctypes.c_float] + [_ll] * 4 + [_i] * 2 + [_vp]),
+    "fa_fwd_paged_chunk": (_i, [_vp] * 10 + [_i] * 5 + [ctypes.c_float, _ll] + [_i] * 3 + [_vp, ctypes.c_size_t, _vp]),
+    "fa_fwd_paged_chunk_workspace_bytes": (ctypes.c_size_t, [_i] * 5),
+    "fa_rope": (_i, [_vp] * 6 + [_i] * 6 + [_vp, _ll, _i, ctypes.c_float, _vp]),
+    "fa_rope_bwd": (_i, [_vp] * 6 + [_i] * 6 + [_vp, _ll, _i, ctypes.c_float, _vp]),
+    "fa_rope_phases": (_i, [_vp, _vp, _i, _d, _i, _d, _d, _d, _d, _vp]),
     "fa_strerror": (ctypes.c_char_p, [_i]),
     "fa_device_status": (_i, [_vp]),
     "fa_selftest_bounded_wait": (_i, [_i, _vp]),
@@ -396,6 +408,36 @@ def fa_fwd_paged_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> i
     return lib().fa_fwd_paged_workspace_bytes(B, T, Hq, Hkv, D)
 
 
+def fa_kv_plan_positions_raw(cached_ptr, new_ptr, free_ptr, count_ptr, table_ptr, cu_q_ptr, lens_ptr, slots_ptr, positions_ptr,
+                             left_ptr, B, T, max_pages, num_free, num_pages, page_size, stream_ptr) -> int:
+    """The plan C call that writes positions too, with raw device pointers; returns the status code."""
+    return lib().fa_kv_plan_positions(cached_ptr, new_ptr, free_ptr, count_ptr, table_ptr, cu_q_ptr, lens_ptr, slots_ptr,
+                                      positions_ptr, left_ptr, B, T, max_pages, num_free, num_pages, page_size, stream_ptr)
+
+
+def fa_kv_append_rope_raw(k_ptr, v_ptr, positions_ptr, phases_ptr, slots_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr,
+                          k_mean_ptr, k_mean_scale_ptr, q_ptr, q_out_ptr, T, Hkv, Hq, D, rot_dim, interleaved, amplitude, k_stride,
+                          v_stride, q_stride, q_out_stride, num_pages, page_size, stream_ptr) -> int:
+    """The rotating append C call with raw device pointers; returns the status code."""
+    return lib().fa_kv_append_rope(k_ptr, v_ptr, positions_ptr, phases_ptr, slots_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr,
+                                   v_scale_ptr, k_mean_ptr, k_mean_scale_ptr, q_ptr, q_out_ptr, T, Hkv, Hq, D, rot_dim,
+                                   int(interleaved), float(amplitude), k_stride, v_stride, q_stride, q_out_stride, num_pages,
+                                   page_size, stream_ptr)
+
+
+def fa_fwd_paged_chunk_raw(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr, o_ptr, lse_ptr,
+                           B, T, Hq, Hkv, D, scale, q_stride, max_pages, num_pages, page_size, ws_ptr, ws_bytes, stream_ptr) -> int:
+    """The paged attention of chunks C call with raw device pointers; returns the status code."""
+    return lib().fa_fwd_paged_chunk(q_ptr, cu_q_ptr, lens_ptr, table_ptr, k_pages_ptr, v_pages_ptr, k_scale_ptr, v_scale_ptr, o_ptr,
+                                    lse_ptr, B, T, Hq, Hkv, D, scale, q_stride, max_pages, num_pages, page_size, ws_ptr, ws_bytes,
+                                    stream_ptr)
+
+
+def fa_fwd_paged_chunk_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of workspace that fa_fwd_paged_chunk needs for these sizes on the current device."""
+    return lib().fa_fwd_paged_chunk_workspace_bytes(B, T, Hq, Hkv, D)
+
+
 _binding_module = None
 
 
@@ -444,14 +486,16 @@ def _allocating(device, stream):
 
 
 def fa_kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_pages: int, page_size: int, cu_q=None,
-               seq_lens=None, slot_map=None, free_left=None, num_tokens: int | None = None, stream=None):
+               seq_lens=None, slot_map=None, free_left=None, num_tokens: int | None = None, stream=None, positions=None):
     """Block tables and slot maps from request lengths, first come, first served.
 
     cached_lens, new_lens: int32 [B]; free_pages: int32 [num_free], of which the first free_count
     (int32 [1]) are free and are taken from the end; block_table: int32 [B, max_pages], to which the
     new pages are added.  slot_map (int32 [T]) or num_tokens says how many tokens there are room for.
     Returns (cu_q [B+1], seq_lens [B], slot_map [T], free_left [1]), all int32, without synchronising;
-    a request that is not served gets seq_lens 0 and slots of -1."""
+    a request that is not served gets seq_lens 0 and slots of -1.  positions (int32 [T], if given) is
+    written too: each token's position in its sequence, for fa_rope and fa_kv_append_rope, -1 behind the
+    last token."""
     if cu_q is None or seq_lens is None or slot_map is None or free_left is None:
         import torch
 
@@ -464,7 +508,7 @@ def fa_kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_p
             slot_map = torch.empty(num_tokens, dtype=torch.int32, device=dev) if slot_map is None else slot_map
             free_left = torch.empty(1, dtype=torch.int32, device=dev) if free_left is None else free_left
     rc = _binding().kv_plan(cached_lens, new_lens, free_pages, free_count, block_table, num_pages, page_size, cu_q, seq_lens,
-                            slot_map, free_left, stream if stream is None else _stream_of(stream, cached_lens.device))
+                            slot_map, free_left, positions, stream if stream is None else _stream_of(stream, cached_lens.device))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv_plan")
     return cu_q, seq_lens, slot_map, free_left
@@ -481,6 +525,26 @@ def fa_kv_append(k, v, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean=None
                               stream if stream is None else _stream_of(stream, k.device))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv_append")
+
+
+def fa_kv_append_rope(k, v, positions, phases, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean=None, k_mean_scale=None, q=None,
+                      q_out=None, interleaved: bool = False, amplitude: float = 1.0, stream=None):
+    """fa_kv_append with the keys rotated on the way (in fp32, rounded once, to codes), and, where q is
+    given, the step's queries rotated beside.
+
+    positions: int32 [T] (fa_kv_plan's); phases, interleaved, amplitude: as in fa_rope; q: bf16 [T, Hq, D],
+    strided over tokens or contiguous; q_out: the same shape (allocated if not given; may be q itself).
+    Other arguments are fa_kv_append's.  Returns q_out (None without q); does not synchronise."""
+    if q is not None and q_out is None:
+        import torch
+
+        with _allocating(q.device, stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    rc = _binding().kv_append_rope(k, v, positions, phases, slot_map, k_pages, v_pages, k_scale, v_scale, k_mean, k_mean_scale, q, q_out,
+                                   interleaved, amplitude, stream if stream is None else _stream_of(stream, k.device))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_kv_append_rope")
+    return q_out
 
 
 def fa_page_select(q, cu_q, seq_lens, block_table, k_mean, k_mean_scale, page_size: int, top_k: int, keep_first: int = 1,
@@ -534,6 +598,110 @@ def fa_fwd_paged(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_sc
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_paged")
     return o, lse
+
+
+def fa_fwd_paged_chunk(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, o=None, lse=None, scale: float | None = None,
+                       workspace=None, stream=None):
+    """fa_fwd_paged (over all pages) made for many query tokens a sequence: prompts, or chunks of them behind
+    what is cached, beside sequences with a single token.
+
+    Arguments and results are fa_fwd_paged's, but workspace has at least fa_fwd_paged_chunk_workspace_bytes(...)
+    bytes.  Returns (o, lse) without synchronising."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if o is None or lse is None or workspace is None:
+        import torch
+
+        dev = q.device
+        with _allocating(dev, stream):
+            o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if o is None else o
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev) if lse is None else lse
+            if workspace is None:
+                with torch.cuda.device(dev):
+                    need = fa_fwd_paged_chunk_workspace_bytes(seq_lens.shape[0], q.shape[0], q.shape[1], k_pages.shape[1], q.shape[-1])
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    rc = _binding().fwd_paged_chunk(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, o, lse, scale, workspace,
+                                    stream if stream is None else _stream_of(stream, q.device))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_fwd_paged_chunk")
+    return o, lse
+
+
+# ------------------------------------------------------------ rotary positions
+def fa_rope_raw(q_ptr, k_ptr, q_out_ptr, k_out_ptr, positions_ptr, phases_ptr, B, S, Hq, Hk, D, rot_dim, strides, positions_stride,
+                interleaved, amplitude, stream_ptr) -> int:
+    """The rotation C call with raw device pointers and 12 strides (a sequence of integers, or None); returns the status code."""
+    array = None if strides is None else (_ll * 12)(*strides)
+    return lib().fa_rope(q_ptr, k_ptr, q_out_ptr, k_out_ptr, positions_ptr, phases_ptr, B, S, Hq, Hk, D, rot_dim, array,
+                         positions_stride, int(interleaved), float(amplitude), stream_ptr)
+
+
+def fa_rope_bwd_raw(dq_out_ptr, dk_out_ptr, dq_ptr, dk_ptr, positions_ptr, phases_ptr, B, S, Hq, Hk, D, rot_dim, strides,
+                    positions_stride, interleaved, amplitude, stream_ptr) -> int:
+    """The rotation's gradient C call with raw device pointers and 12 strides; returns the status code."""
+    array = None if strides is None else (_ll * 12)(*strides)
+    return lib().fa_rope_bwd(dq_out_ptr, dk_out_ptr, dq_ptr, dk_ptr, positions_ptr, phases_ptr, B, S, Hq, Hk, D, rot_dim, array,
+                             positions_stride, int(interleaved), float(amplitude), stream_ptr)
+
+
+def fa_rope_phases(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0, span: float = 0.0,
+                   fast: float = 32.0, slow: float = 1.0, frequencies=None, device="cuda"):
+    """The frequencies of rotary positions as fa_rope takes them: (phases, amplitude), phases an int64 tensor
+    [rot_dim / 2] on ``device`` in units of 2^-64 turns a position, amplitude a float.
+
+    Pair i turns by base^(-2 i / rot_dim) radians a position, or by frequencies[i]; scaling "linear" divides
+    by factor, "ntk" stretches the base by factor, "yarn" divides the pairs that make fewer than ``slow``
+    turns in ``span`` positions by factor, keeps those with more than ``fast`` and mixes between (the
+    amplitude is then 0.1 ln(factor) + 1).  Computed on the host; meant to be called once."""
+    import torch
+
+    if scaling not in FA_ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {tuple(FA_ROPE_SCALINGS)}")
+    if frequencies is not None:
+        frequencies = [float(f) for f in frequencies]
+        if len(frequencies) != rot_dim // 2:
+            raise ValueError("frequencies must have rot_dim / 2 elements")
+    phases = (ctypes.c_ulonglong * max(1, rot_dim // 2))()
+    amplitude = ctypes.c_float()
+    st = lib().fa_rope_phases(phases, ctypes.byref(amplitude), rot_dim, base, FA_ROPE_SCALINGS[scaling], factor, span, fast, slow,
+                              None if frequencies is None else (_d * len(frequencies))(*frequencies))
+    if st != FA_OK:
+        raise FAError(st, "fa_rope_phases")
+    signed = [x - (1 << 64) if x >= 1 << 63 else x for x in phases]
+    return torch.tensor(signed, dtype=torch.int64, device=device), amplitude.value
+
+
+def _rope(name, inverse, q, k, phases, positions, interleaved, amplitude, q_out, k_out, stream):
+    if q_out is None or (k is not None and k_out is None):
+        import torch
+
+        with _allocating(q.device, stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device) if k is not None and k_out is None else k_out
+    rc = _binding().rope(q, k, phases, positions, interleaved, amplitude, q_out, k_out, inverse,
+                         stream if stream is None else _stream_of(stream, q.device))
+    if rc != FA_OK:
+        raise FAError(rc, name)
+    return q_out, k_out
+
+
+def fa_rope(q, k, phases, positions=None, interleaved: bool = False, amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions of queries and keys.
+
+    q: bf16 [B, Hq, S, D] or [T, Hq, D], k: the same with Hk heads, or None; any strides but a contiguous
+    last dimension (views of a fused projection); positions: int32 [S] or [B, S] ([T] for packed tokens),
+    or None: 0, 1, ..; phases, amplitude: fa_rope_phases'.  The first 2 * len(phases) elements of each head
+    are rotated, in pairs i and i + len(phases), or, ``interleaved``, 2 i and 2 i + 1; the others are copied.
+    q_out and k_out (allocated contiguous if not given) may be q and k, or views of a fused tensor.
+    Returns (q_out, k_out) without synchronising."""
+    return _rope("fa_rope", False, q, k, phases, positions, interleaved, amplitude, q_out, k_out, stream)
+
+
+def fa_rope_bwd(dq_out, dk_out, phases, positions=None, interleaved: bool = False, amplitude: float = 1.0, q_out=None, k_out=None,
+                stream=None):
+    """Gradients (dq, dk) of fa_rope for the gradients of its outputs, written to q_out and k_out (allocated if
+    not given); other arguments as for fa_rope."""
+    return _rope("fa_rope_bwd", True, dq_out, dk_out, phases, positions, interleaved, amplitude, q_out, k_out, stream)
 
 
 def fa_device_status(stream=None) -> int:

@@ -522,19 +522,20 @@ size_t strided_bytes(int T, long long stride, int H, int D) {
 
 }  // namespace
 
-extern "C" int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_count,
-                          int *block_table, int *cu_q, int *seq_lens, int *slot_map, int *free_left, int B, int T,
-                          int max_pages, int num_free, int num_pages, int page_size, void *stream) {
+static int plan_checked(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_count,
+                        int *block_table, int *cu_q, int *seq_lens, int *slot_map, int *positions, int *free_left, int B,
+                        int T, int max_pages, int num_free, int num_pages, int page_size, void *stream) {
     const void *ptrs[9] = {cached_lens, new_lens, free_pages, free_count, block_table, cu_q, seq_lens, slot_map, free_left};
     for (const void *ptr : ptrs)
         if (!ptr) return FA_ERR_NULLPTR;
     for (const void *ptr : ptrs)
         if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
+    if (!aligned4(positions)) return FA_ERR_MISALIGNED;
     if (num_free < 1 || num_free > kMostCounted) return FA_ERR_BAD_SHAPE;
     const int st = check_cache(B, T, 1, 64, max_pages, num_pages, page_size);
     if (st != FA_OK) return st;
-    const Span outs[5] = {{block_table, (size_t)B * max_pages * 4}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
-                          {slot_map, (size_t)T * 4}, {free_left, 4}};
+    const Span outs[6] = {{block_table, (size_t)B * max_pages * 4}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
+                          {slot_map, (size_t)T * 4}, {free_left, 4}, {positions, (size_t)T * 4}};
     const Span ins[4] = {{cached_lens, (size_t)B * 4}, {new_lens, (size_t)B * 4}, {free_pages, (size_t)num_free * 4}, {free_count, 4}};
     if (any_alias(outs, ins)) return FA_ERR_ALIAS;
     fa::PlanParams p;
@@ -546,6 +547,7 @@ extern "C" int fa_kv_plan(const int *cached_lens, const int *new_lens, const int
     p.cu_q = cu_q;
     p.seq_lens = seq_lens;
     p.slots = slot_map;
+    p.positions = positions;
     p.free_left = free_left;
     p.B = B;
     p.T = T;
@@ -555,6 +557,22 @@ extern "C" int fa_kv_plan(const int *cached_lens, const int *new_lens, const int
     p.page_log2 = page_log2_of(page_size);
     const cudaError_t e = fa::launch_kv_plan(p, sm_count(), (cudaStream_t)stream);
     return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+extern "C" int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_count,
+                          int *block_table, int *cu_q, int *seq_lens, int *slot_map, int *free_left, int B, int T,
+                          int max_pages, int num_free, int num_pages, int page_size, void *stream) {
+    return plan_checked(cached_lens, new_lens, free_pages, free_count, block_table, cu_q, seq_lens, slot_map, nullptr, free_left, B, T,
+                        max_pages, num_free, num_pages, page_size, stream);
+}
+
+extern "C" int fa_kv_plan_positions(const int *cached_lens, const int *new_lens, const int *free_pages,
+                                    const int *free_count, int *block_table, int *cu_q, int *seq_lens, int *slot_map,
+                                    int *positions, int *free_left, int B, int T, int max_pages, int num_free,
+                                    int num_pages, int page_size, void *stream) {
+    if (!positions) return FA_ERR_NULLPTR;
+    return plan_checked(cached_lens, new_lens, free_pages, free_count, block_table, cu_q, seq_lens, slot_map, positions, free_left, B,
+                        T, max_pages, num_free, num_pages, page_size, stream);
 }
 
 extern "C" int fa_kv_append(const void *k, const void *v, const int *slot_map, void *k_pages, void *v_pages,
@@ -575,7 +593,7 @@ extern "C" int fa_kv_append(const void *k, const void *v, const int *slot_map, v
     const Span ins[3] = {{k, strided_bytes(T, k_stride, Hkv, D)}, {v, strided_bytes(T, v_stride, Hkv, D)},
                          {slot_map, (size_t)T * 4}};
     if (any_alias(outs, ins)) return FA_ERR_ALIAS;
-    fa::AppendParams p;
+    fa::AppendParams p{};
     p.x[0] = k;
     p.x[1] = v;
     p.stride[0] = k_stride;
@@ -591,6 +609,254 @@ extern "C" int fa_kv_append(const void *k, const void *v, const int *slot_map, v
     p.Hkv = Hkv;
     p.num_pages = num_pages;
     p.page_log2 = page_log2_of(page_size);
+    const cudaError_t e = fa::launch_kv_append(D, p, sm_count(), (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+// ------------------------------------------------------------- rotary positions
+namespace {
+
+// A tensor [B, H, S, D] of bf16 with strides (elements) between sequences, tokens and
+// heads; its elements within a head are contiguous.
+struct Strided {
+    const void *ptr;
+    long long stride[3];
+    int B, S, H, D;
+
+    uintptr_t begin() const { return (uintptr_t)ptr; }
+    uintptr_t end() const {
+        return begin() + 2 * (size_t)((B - 1) * stride[0] + (S - 1) * stride[1] + (H - 1) * stride[2] + D);
+    }
+    bool strides_ok() const {
+        const int n[3] = {B, S, H};
+        double past = D;  // an address counts bytes in 63 bits
+        for (int d = 0; d < 3; ++d) {
+            if (stride[d] < 0 || stride[d] % 8 != 0 || stride[d] >= (1ll << 40)) return false;
+            past += (double)stride[d] * (n[d] - 1);
+        }
+        return past < 0x1p60;
+    }
+    // Whether no two of its elements are the same memory: each dimension, in the order
+    // of their strides, steps past all of the smaller ones.
+    bool distinct() const {
+        int n[3] = {B, S, H}, order[3] = {0, 1, 2};
+        for (int i = 0; i < 3; ++i)
+            for (int j = i + 1; j < 3; ++j)
+                if (stride[order[j]] < stride[order[i]]) {
+                    const int x = order[i];
+                    order[i] = order[j];
+                    order[j] = x;
+                }
+        long long past = D;
+        for (const int d : order) {
+            if (n[d] == 1) continue;
+            if (stride[d] < past) return false;
+            past += stride[d] * (n[d] - 1);
+        }
+        return true;
+    }
+    bool same(const Strided &o) const {
+        return ptr == o.ptr && B == o.B && S == o.S && H == o.H && D == o.D && (B == 1 || stride[0] == o.stride[0]) &&
+               (S == 1 || stride[1] == o.stride[1]) && (H == 1 || stride[2] == o.stride[2]);
+    }
+};
+
+// Whether two tensors share memory.  Those whose spans do may still be columns of one
+// fused tensor: with the same strides between tokens and between sequences, the latter
+// a multiple of the former, each lies within its own part of every token's row.
+bool shares(const Strided &a, const Strided &b) {
+    if (a.end() <= b.begin() || b.end() <= a.begin()) return false;
+    const int step = a.S > 1 ? 1 : 0;  // sequences of one token: their stride is the row's
+    const long long row = a.stride[step];
+    if (a.B != b.B || a.S != b.S || row <= 0 || b.stride[step] != row) return true;
+    if (a.S > 1 && a.B > 1 && (a.stride[0] != b.stride[0] || a.stride[0] % row != 0)) return true;
+    const long long na = (a.H - 1) * a.stride[2] + a.D, nb = (b.H - 1) * b.stride[2] + b.D;
+    const long long bytes = (long long)(b.begin() - a.begin());  // (wraps around where b is lower)
+    if (bytes % 2 != 0) return true;
+    const long long at = ((bytes / 2) % row + row) % row;  // b's place in a's rows
+    return at < na || at + nb > row;
+}
+
+// A rotated tensor and its output: the very same tensor, or no memory in common.
+bool turned_in_place_or_apart(const Strided &x, const Strided &y) { return x.same(y) || !shares(x, y); }
+
+int check_rotation(const unsigned long long *phases, const int *positions, int rot_dim, int D, int interleaved, float amplitude) {
+    if (!phases) return FA_ERR_NULLPTR;
+    if (((uintptr_t)phases & 7u) != 0 || !aligned4(positions)) return FA_ERR_MISALIGNED;
+    if (rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > D || (interleaved != 0 && interleaved != 1)) return FA_ERR_BAD_SHAPE;
+    if (!isfinite(amplitude) || !(amplitude > 0.f)) return FA_ERR_BAD_SCALE;
+    return FA_OK;
+}
+
+int rope_checked(const void *q, const void *k, void *q_out, void *k_out, const int *positions, const unsigned long long *phases,
+                 int B, int S, int Hq, int Hk, int D, int rot_dim, const long long *strides, long long positions_stride,
+                 int interleaved, float amplitude, int inverse, void *stream) {
+    if (!q || !q_out || !phases || !strides || (Hk > 0 && (!k || !k_out))) return FA_ERR_NULLPTR;
+    if (!aligned16(q) || !aligned16(q_out) || (Hk > 0 && (!aligned16(k) || !aligned16(k_out)))) return FA_ERR_MISALIGNED;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED_D;
+    if (B < 1 || S < 1 || (long long)B * S > kMostCounted || Hq < 1 || Hq > 65535 || Hk < 0 || Hk > 65535) return FA_ERR_BAD_SHAPE;
+    const int st = check_rotation(phases, positions, rot_dim, D, interleaved, amplitude);
+    if (st != FA_OK) return st;
+    if (positions && (positions_stride < 0 || positions_stride >= (1ll << 31) || (positions_stride != 0 && positions_stride < S && B > 1)))
+        return FA_ERR_BAD_SHAPE;
+    Strided t[4];  // q, k, q_out, k_out
+    const void *ptr[4] = {q, k, q_out, k_out};
+    for (int i = 0; i < 4; ++i) {
+        t[i] = Strided{ptr[i], {strides[3 * i], strides[3 * i + 1], strides[3 * i + 2]}, B, S, i % 2 ? Hk : Hq, D};
+        if (i % 2 && Hk == 0) continue;
+        if (!t[i].strides_ok() || (i >= 2 && !t[i].distinct())) return FA_ERR_BAD_SHAPE;
+    }
+    if (!turned_in_place_or_apart(t[0], t[2])) return FA_ERR_ALIAS;
+    if (Hk > 0 && (!turned_in_place_or_apart(t[1], t[3]) || shares(t[0], t[3]) || shares(t[1], t[2]) || shares(t[2], t[3])))
+        return FA_ERR_ALIAS;
+    // the other inputs, which may lie in no gap of an output either
+    const size_t np = positions ? ((size_t)(B - 1) * (size_t)positions_stride + (size_t)S) * 4 : 0;
+    for (int i = 2; i < (Hk > 0 ? 4 : 3); ++i) {
+        const size_t n = t[i].end() - t[i].begin();
+        if ((positions && overlaps(t[i].ptr, n, positions, np)) || overlaps(t[i].ptr, n, phases, (size_t)rot_dim * 4)) return FA_ERR_ALIAS;
+    }
+    fa::RopeParams p{};
+    for (int i = 0; i < 2; ++i) {
+        p.x[i] = ptr[i];
+        p.y[i] = const_cast<void *>(ptr[i + 2]);
+        for (int d = 0; d < 3; ++d) {
+            p.x_stride[i][d] = strides[3 * i + d];
+            p.y_stride[i][d] = strides[3 * (i + 2) + d];
+        }
+    }
+    p.H[0] = Hq;
+    p.H[1] = Hk;
+    p.positions = positions;
+    p.positions_stride = positions_stride;
+    p.phases = phases;
+    p.B = B;
+    p.S = S;
+    p.D = D;
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.inverse = inverse;
+    p.amplitude = amplitude;
+    const cudaError_t e = fa::launch_rope(p, sm_count(), (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+}  // namespace
+
+extern "C" int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *positions,
+                       const unsigned long long *phases, int B, int S, int Hq, int Hk, int D, int rot_dim,
+                       const long long *strides, long long positions_stride, int interleaved, float amplitude,
+                       void *stream) {
+    return rope_checked(q, k, q_out, k_out, positions, phases, B, S, Hq, Hk, D, rot_dim, strides, positions_stride, interleaved,
+                        amplitude, 0, stream);
+}
+
+extern "C" int fa_rope_bwd(const void *dq_out, const void *dk_out, void *dq, void *dk, const int *positions,
+                           const unsigned long long *phases, int B, int S, int Hq, int Hk, int D, int rot_dim,
+                           const long long *strides, long long positions_stride, int interleaved, float amplitude,
+                           void *stream) {
+    return rope_checked(dq_out, dk_out, dq, dk, positions, phases, B, S, Hq, Hk, D, rot_dim, strides, positions_stride, interleaved,
+                        amplitude, 1, stream);
+}
+
+extern "C" int fa_rope_phases(unsigned long long *phases, float *amplitude, int rot_dim, double base, int scaling,
+                              double factor, double span, double fast, double slow, const double *frequencies) {
+    if (!phases || !amplitude) return FA_ERR_NULLPTR;
+    if (rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > 128) return FA_ERR_BAD_SHAPE;
+    if (scaling < FA_ROPE_PLAIN || scaling > FA_ROPE_YARN) return FA_ERR_BAD_SHAPE;
+    const double two_pi = 6.283185307179586476925;
+    if (!frequencies && (!isfinite(base) || !(base > 1.0))) return FA_ERR_BAD_SCALE;
+    if (scaling != FA_ROPE_PLAIN && (!isfinite(factor) || !(factor >= 1.0))) return FA_ERR_BAD_SCALE;
+    if (scaling == FA_ROPE_NTK && frequencies) return FA_ERR_BAD_SHAPE;
+    if (scaling == FA_ROPE_YARN && (!isfinite(span) || !(span >= 1.0) || !isfinite(fast) || !(slow > 0.0) || !(fast >= slow)))
+        return FA_ERR_BAD_SCALE;
+    if (scaling == FA_ROPE_YARN && frequencies) return FA_ERR_BAD_SHAPE;
+    *amplitude = 1.f;
+    double lo = 0.0, hi = 0.0;
+    if (scaling == FA_ROPE_NTK) base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    if (scaling == FA_ROPE_YARN) {
+        // the pairs that make `fast` and `slow` turns over the span
+        lo = floor(rot_dim * log(span / (fast * two_pi)) / (2.0 * log(base)));
+        hi = ceil(rot_dim * log(span / (slow * two_pi)) / (2.0 * log(base)));
+        lo = lo > 0.0 ? lo : 0.0;
+        hi = hi < rot_dim - 1 ? hi : rot_dim - 1;
+        *amplitude = (float)(0.1 * log(factor) + 1.0);
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = frequencies ? frequencies[i] : pow(base, -2.0 * i / rot_dim);
+        if (!isfinite(f)) return FA_ERR_BAD_SCALE;
+        if (scaling == FA_ROPE_LINEAR) f /= factor;
+        if (scaling == FA_ROPE_YARN) {
+            const double width = hi - lo > 0.001 ? hi - lo : 0.001;
+            const double ramp = fmin(1.0, fmax(0.0, (i - lo) / width));
+            f = f * (1.0 - ramp) + f / factor * ramp;
+        }
+        double turns = f / two_pi;
+        turns -= floor(turns);  // in [0, 1], and 1 is no turn at all
+        phases[i] = turns < 1.0 ? (unsigned long long)(turns * 18446744073709551616.0) : 0ull;
+    }
+    return FA_OK;
+}
+
+extern "C" int fa_kv_append_rope(const void *k, const void *v, const int *positions, const unsigned long long *phases,
+                                 const int *slot_map, void *k_pages, void *v_pages, float *k_scale, float *v_scale,
+                                 signed char *k_mean, float *k_mean_scale, const void *q, void *q_out, int T, int Hkv,
+                                 int Hq, int D, int rot_dim, int interleaved, float amplitude, long long k_stride,
+                                 long long v_stride, long long q_stride, long long q_out_stride, int num_pages,
+                                 int page_size, void *stream) {
+    if (!k || !v || !positions || !phases || !slot_map || !k_pages || !v_pages || !k_scale || !v_scale || (!k_mean != !k_mean_scale) ||
+        (!q != !q_out))
+        return FA_ERR_NULLPTR;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_mean) || !aligned16(q) ||
+        !aligned16(q_out) || !aligned4(slot_map) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(k_mean_scale))
+        return FA_ERR_MISALIGNED;
+    int st = check_cache(1, T, Hkv, D, 1, num_pages, page_size);
+    if (st != FA_OK) return st;
+    st = check_rotation(phases, positions, rot_dim, D, interleaved, amplitude);
+    if (st != FA_OK) return st;
+    if (!stride_ok(k_stride, Hkv, D) || !stride_ok(v_stride, Hkv, D)) return FA_ERR_BAD_SHAPE;
+    if (q && (Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || !stride_ok(q_stride, Hq, D) || !stride_ok(q_out_stride, Hq, D))) return FA_ERR_BAD_SHAPE;
+    const size_t heads = (size_t)num_pages * Hkv, codes = heads * page_size * D;
+    const size_t k_bytes = strided_bytes(T, k_stride, Hkv, D), v_bytes = strided_bytes(T, v_stride, Hkv, D);
+    const size_t q_bytes = q ? strided_bytes(T, q_stride, Hq, D) : 0, q_out_bytes = q ? strided_bytes(T, q_out_stride, Hq, D) : 0;
+    const Span outs[6] = {{k_pages, codes}, {v_pages, codes}, {k_scale, heads * 4}, {v_scale, heads * 4},
+                          {k_mean, heads * D}, {k_mean_scale, heads * 4}};
+    const Span ins[7] = {{k, k_bytes}, {v, v_bytes}, {slot_map, (size_t)T * 4}, {positions, (size_t)T * 4}, {phases, (size_t)rot_dim * 4},
+                         {q, q_bytes}, {q_out, q_out_bytes}};
+    if (any_alias(outs, ins)) return FA_ERR_ALIAS;
+    if (q) {  // rotated queries may lie in the same fused tensor
+        const Strided a{k, {0, k_stride, D}, 1, T, Hkv, D}, b{v, {0, v_stride, D}, 1, T, Hkv, D};
+        const Strided x{q, {0, q_stride, D}, 1, T, Hq, D}, y{q_out, {0, q_out_stride, D}, 1, T, Hq, D};
+        if (!x.strides_ok() || !y.strides_ok() || !a.strides_ok() || !b.strides_ok()) return FA_ERR_BAD_SHAPE;
+        if (!turned_in_place_or_apart(x, y) || shares(a, y) || shares(b, y)) return FA_ERR_ALIAS;
+        for (int i = 2; i < 5; ++i)
+            if (overlaps(q_out, q_out_bytes, ins[i].ptr, ins[i].bytes)) return FA_ERR_ALIAS;
+    }
+    fa::AppendParams p{};
+    p.x[0] = k;
+    p.x[1] = v;
+    p.stride[0] = k_stride;
+    p.stride[1] = v_stride;
+    p.slots = slot_map;
+    p.pages[0] = static_cast<uint8_t *>(k_pages);
+    p.pages[1] = static_cast<uint8_t *>(v_pages);
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.mean = reinterpret_cast<int8_t *>(k_mean);
+    p.mean_scale = k_mean_scale;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.num_pages = num_pages;
+    p.page_log2 = page_log2_of(page_size);
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.amplitude = amplitude;
+    p.positions = positions;
+    p.phases = phases;
+    p.q = q;
+    p.q_out = q_out;
+    p.q_stride = q_stride;
+    p.q_out_stride = q_out_stride;
+    p.G = q ? Hq / Hkv : 0;
     const cudaError_t e = fa::launch_kv_append(D, p, sm_count(), (cudaStream_t)stream);
     return e == cudaSuccess ? FA_OK : fail_cuda(e);
 }
@@ -705,15 +971,71 @@ extern "C" int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens,
     return e == cudaSuccess ? FA_OK : fail_cuda(e);
 }
 
+extern "C" size_t fa_fwd_paged_chunk_workspace_bytes(int B, int T, int Hq, int Hkv, int D) {
+    if (!paged_shape_ok(B, T, Hq, Hkv, D)) return 0;
+    return fa::paged_chunk_workspace_bytes(D, sm_count());
+}
+
+extern "C" int fa_fwd_paged_chunk(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                                  const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                                  void *o, float *lse, int B, int T, int Hq, int Hkv, int D, float scale,
+                                  long long q_stride, int max_pages, int num_pages, int page_size, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    if (!q || !cu_q || !seq_lens || !block_table || !k_pages || !v_pages || !k_scale || !v_scale || !o || !lse) return FA_ERR_NULLPTR;
+    const void *ints[6] = {cu_q, seq_lens, block_table, k_scale, v_scale, lse};
+    for (const void *ptr : ints)
+        if (!aligned4(ptr)) return FA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o)) return FA_ERR_MISALIGNED;
+    const int st = check_cache(B, T, Hkv, D, max_pages, num_pages, page_size);
+    if (st != FA_OK) return st;
+    if (!paged_shape_ok(B, T, Hq, Hkv, D) || !stride_ok(q_stride, Hq, D)) return FA_ERR_BAD_SHAPE;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!isfinite(scale) || !(scale > 0.f) || !isfinite(scale_log2)) return FA_ERR_BAD_SCALE;
+    const size_t need = fa::paged_chunk_workspace_bytes(D, sm_count());
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need) return FA_ERR_WORKSPACE;
+    const size_t heads = (size_t)num_pages * Hkv, codes = heads * page_size * D;
+    if (heads * page_size > 0xffffffffull) return FA_ERR_BAD_SHAPE;  // rows of a cache: more than memory holds
+    const Span outs[3] = {{o, (size_t)T * Hq * D * 2}, {lse, (size_t)T * Hq * 4}, {workspace, need}};
+    const Span ins[8] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
+                         {block_table, (size_t)B * max_pages * 4}, {k_pages, codes}, {v_pages, codes},
+                         {k_scale, heads * 4}, {v_scale, heads * 4}};
+    if (any_alias(outs, ins)) return FA_ERR_ALIAS;
+    fa::ChunkParams p{};
+    p.q = q;
+    p.q_stride = q_stride;
+    p.cu_q = cu_q;
+    p.seq_lens = seq_lens;
+    p.table = block_table;
+    p.k_pages = static_cast<const uint8_t *>(k_pages);
+    p.v_pages = static_cast<const uint8_t *>(v_pages);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.o = o;
+    p.lse = lse;
+    p.ws = static_cast<float *>(workspace);
+    p.B = B;
+    p.T = T;
+    p.G = Hq / Hkv;
+    p.Hkv = Hkv;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.page_log2 = page_log2_of(page_size);
+    p.scale_log2 = scale_log2;
+    p.timeout_ns = kWaitLimitNs;
+    const cudaError_t e = fa::launch_fwd_paged_chunk(D, p, sm_count(), (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
 extern "C" int fa_device_status(void *stream) {
     int v = 0, w = 0, x = 0;
     cudaError_t e = fa::status_read_and_clear(&v, (cudaStream_t)stream);
     if (e == cudaSuccess) e = fa::splitkv_status_read_and_clear(&w);
     if (e == cudaSuccess) e = fa::bwd_status_read_and_clear(&x);
-    int cache[3] = {0, 0, 0};  // the paged cache's kernels
+    int cache[4] = {0, 0, 0, 0};  // the paged cache's kernels
     if (e == cudaSuccess) e = fa::kv_cache_status_read_and_clear(&cache[0]);
     if (e == cudaSuccess) e = fa::page_select_status_read_and_clear(&cache[1]);
     if (e == cudaSuccess) e = fa::paged_status_read_and_clear(&cache[2]);
+    if (e == cudaSuccess) e = fa::paged_chunk_status_read_and_clear(&cache[3]);
     if (e != cudaSuccess) return fail_cuda(e);
     for (int c : cache)
         if (x == FA_OK) x = c;

@@ -1,6 +1,7 @@
 // fa_kv_cache.cu -- what fills the paged 8-bit key/value cache on GB300
 // (sm_103a): fa_kv_plan (block tables and slot maps from request lengths) and
-// fa_kv_append (rounds a step's keys and values into pages).
+// fa_kv_append (rounds a step's keys and values into pages), with the keys' rotation on
+// the way in fa_kv_append_rope.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -12,6 +13,7 @@
 
 #include "../../include/fa.h"
 #include "fa_paged.h"
+#include "fa_rope.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -124,10 +126,11 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const __grid_c
     }
     const int page = 1 << p.page_log2;
     for (int i = me; i < p.T; i += step) {
-        int slot = -1;
+        int slot = -1, position = -1;
         if (i < cu[p.B]) {
             const int b = count_le(cu + 1, p.B, i);
             const Request r = plan_request(p, b);
+            position = (int)((uint32_t)r.cached + (uint32_t)(i - cu[b]));
             if (r.valid && (r.need == 0 || (long long)pc[b] + r.need <= free_count)) {
                 const int pos = r.cached + (i - cu[b]), ord = pos >> p.page_log2;
                 // (in range, unless the caller changes the lengths during the call)
@@ -141,6 +144,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const __grid_c
             }
         }
         p.slots[i] = slot;
+        if (p.positions) p.positions[i] = position;
     }
     for (int i = me; i < min(pc[p.B], free_count); i += step) {
         const int b = count_le(pc + 1, p.B, i);
@@ -249,9 +253,10 @@ __device__ __forceinline__ float pow2_scale(float amax) {
     return __uint_as_float((uint32_t)(max(-100, min(120, e)) + 127) << 23);
 }
 
-template <int D, int PAGE>
+// PER: elements a thread holds at most
+template <int D, int PAGE, int PER = 64>
 struct AppendCfg {
-    static constexpr int TEAM = PAGE * D < 2048 ? 1 : PAGE * D / 2048;  // warps
+    static constexpr int TEAM = PAGE * D < 32 * PER ? 1 : PAGE * D / (32 * PER);  // warps
     static constexpr int WARPS = TEAM > 4 ? TEAM : 4;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int TEAMS = WARPS / TEAM;
@@ -269,17 +274,26 @@ struct AppendCfg {
     static constexpr int BLOCKS = 10 * 128 / THREADS;
 };
 
-template <int D, int PAGE>
-__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE>::BLOCKS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
-    using C = AppendCfg<D, PAGE>;
-    grid_wait();
-    __shared__ int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
-    __shared__ uint32_t starts[kWindow / 32];
-    __shared__ uint32_t amax_sm[2][C::WARPS];
-    __shared__ int sums[C::WARPS][D];
+template <int D, int PAGE, class C>
+struct AppendShared {
+    int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
+    uint32_t starts[kWindow / 32];
+    uint32_t amax[2][C::WARPS];
+    int sums[C::WARPS][D];
+};
+
+enum class Turn { none, halves, pairs };  // whether rows are rotated, and which elements make a pair
+
+// One block's share of the runs of a window, of one head of K (kv = 0) or V.
+template <int D, int PAGE, class C, Turn TURN>
+__device__ __forceinline__ void append_runs(const AppendParams &p, const int share, const int kv, AppendShared<D, PAGE, C> &sm) {
+    int *const slot_of = sm.slot_of;
+    uint32_t *const starts = sm.starts;
+    auto &amax_sm = sm.amax;
+    auto &sums = sm.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
-    const int h = blockIdx.y, kv = blockIdx.z;
+    const int h = blockIdx.y;
     const int win = blockIdx.x / share, part = blockIdx.x % share;
     const int t0 = win * kWindow;
     const int limit = p.num_pages * PAGE;  // fewer than 2^31
@@ -324,6 +338,49 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
             const uint32_t m = __ballot_sync(0xffffffffu, i < PAGE - off && slot_of[i0 + min(i, PAGE - 1)] == slot + i);
             if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
         }
+
+        // the largest of the team's magnitudes
+        auto join_max = [&](uint32_t am) {
+            am = __reduce_max_sync(0xffffffffu, am);
+            if (C::TEAM > 1) {
+                if (lane == 0) amax_sm[0][warp] = am;
+                team_sync();
+#pragma unroll
+                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
+            } else {
+                team_sync();
+            }
+            return am;
+        };
+        // the page's mean of its first `rows` rows, from the warps' sums
+        auto write_mean = [&](long long ph, float scale, int rows) {
+            team_sync();
+            constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
+            int total[PER], a = 0;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int d = tt + c * 32 * C::TEAM;
+                total[c] = 0;
+                if (d < D)
+#pragma unroll
+                    for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
+                a = max(a, abs(total[c]));
+            }
+            a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
+            if (C::TEAM > 1) {
+                if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
+                team_sync();
+#pragma unroll
+                for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
+            }
+            const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int d = tt + c * 32 * C::TEAM;
+                if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
+            }
+            if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * rows);
+        };
 
         // A whole page, the usual run of a prompt, does without what the ends of others need
         // (20.9 -> 18.1 us) and always has a power of two for its scale (17.6 us).
@@ -371,15 +428,7 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
                     }
                 }
             }
-            am = __reduce_max_sync(0xffffffffu, am);
-            if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[0][warp] = am;
-                team_sync();
-#pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
-            } else {
-                team_sync();
-            }
+            am = join_max(am);
             float scale = pow2_scale(__uint_as_float(am << 16));
             if (!W && off > 0) scale = fmaxf(scale, was);
             if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
@@ -442,39 +491,191 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
                     for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
                     if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
                 }
-                team_sync();
-                constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
-                int total[PER], a = 0;
-#pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    const int d = tt + c * 32 * C::TEAM;
-                    total[c] = 0;
-                    if (d < D)
-#pragma unroll
-                        for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
-                    a = max(a, abs(total[c]));
-                }
-                a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
-                if (C::TEAM > 1) {
-                    if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
-                    team_sync();
-#pragma unroll
-                    for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
-                }
-                const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
-#pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    const int d = tt + c * 32 * C::TEAM;
-                    if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
-                }
-                if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (W ? PAGE : off + n));
+                write_mean(ph, scale, W ? PAGE : off + n);
             }
         };
-        if (n == PAGE)
-            append(std::true_type());
-        else
-            append(std::false_type());
+        // Rotated rows: a thread has two pieces of each of its rows, whose elements are one
+        // another's partners, and keeps them in fp32 between the pass that takes the largest
+        // magnitude and the one that writes codes, so that they are rounded once.
+        auto append_turned = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            constexpr int TPT = D / 16, ROWS = 32 * C::TEAM / TPT, PASSES = PAGE / ROWS;
+            static_assert(PASSES * 8 <= 32, "sums of codes are exact in fp32");
+            const int sub = tt % TPT, r0 = tt / TPT;
+            const long long ph = (long long)pg * p.Hkv + h;
+            const float was = W ? 0.f : scale_of[ph];
+            const int2 piece = rope_pieces(sub, p.rot, TURN == Turn::pairs);
+            uint8_t *const codes = pages_of + ph * PAGE * D;
+            const bool mean = p.mean != nullptr, turned = sub < p.rot / 16;
+            unsigned long long phase[8];
+            if (turned) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) phase[j] = __ldg(p.phases + 8 * sub + j);
+            }
+            // ---- what is read, at once: the run's rows, and codes before it for the mean
+            uint4 w[PASSES][2];
+            int position[PASSES];
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * ROWS;
+                position[i] = 0;
+                w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+                if (W || (r >= off && r < off + n)) {
+                    const long long token = (long long)(t0 + i0 - off) + r;
+                    w[i][0] = __ldg(reinterpret_cast<const uint4 *>(x_of + token * stride + 8 * piece.x));
+                    w[i][1] = __ldg(reinterpret_cast<const uint4 *>(x_of + token * stride + 8 * piece.y));
+                    position[i] = __ldg(p.positions + token);
+                } else if (mean && r < off) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(codes + r * D + 8 * piece.x);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(codes + r * D + 8 * piece.y);
+                    w[i][0] = make_uint4(a.x, a.y, b.x, b.y);
+                }
+            }
+            float y[PASSES][16];
+            uint32_t am = 0;  // magnitudes of fp32 compare as integers; infinities and NaN do not count
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * ROWS;
+                if (!W && (r < off || r >= off + n)) continue;
+                bf16x8_to_float(w[i][0], y[i]);
+                bf16x8_to_float(w[i][1], y[i] + 8);
+                if (turned) {
+                    float2 f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = rope_factor(phase[j], position[i], p.amplitude);
+                    rope_turn16<TURN == Turn::pairs>(y[i], f);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t u = __float_as_uint(y[i][j]) & 0x7fffffffu;
+                    am = max(am, u < 0x7f800000u ? u : 0u);
+                }
+            }
+            float scale = pow2_scale(__uint_as_float(join_max(am)));
+            if (!W && off > 0) scale = fmaxf(scale, was);
+            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
+            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+            const float inv_scale = 1.f / scale, shrink = was / scale;
+            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
+            float sum[2][8] = {};
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * ROWS;
+                if (!W && (r < off || r >= off + n)) continue;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = y[i][j];
+                    y[i][j] = x * inv_scale;  // exact for powers of two; the remainder corrects it otherwise
+                    if (!W && !pow2 && fabsf(x) < INFINITY) y[i][j] = fmaf(fmaf(-y[i][j], scale, x), inv_scale, y[i][j]);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float *const v = y[i] + 8 * c;
+                    const uint2 code = make_uint2(pack_e4m3x4(v[0], v[1], v[2], v[3]), pack_e4m3x4(v[4], v[5], v[6], v[7]));
+                    *reinterpret_cast<uint2 *>(codes + r * D + 8 * (c ? piece.y : piece.x)) = code;
+                    if (mean) add8(without_nan(code), sum[c]);
+                }
+            }
+            if (!W && off > 0 && (mean || grown)) {
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) {
+                    const int r = r0 + i * ROWS;
+                    if (r >= off) continue;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint2 *const at = reinterpret_cast<uint2 *>(codes + r * D + 8 * (c ? piece.y : piece.x));
+                        uint2 code = mean ? (c ? make_uint2(w[i][0].z, w[i][0].w) : make_uint2(w[i][0].x, w[i][0].y)) : *at;
+                        float v[8];
+                        if (grown) {
+                            decode8(code, v);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] *= shrink;
+                            code = encode8(v);
+                            *at = code;
+                        }
+                        decode8(without_nan(code), v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[c][j] += v[j];
+                    }
+                }
+            }
+            if (mean) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        int x = (int)(sum[c][j] * 512.f);
+#pragma unroll
+                        for (int d = TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                        if (lane < TPT) sums[warp][8 * (c ? piece.y : piece.x) + j] = x;
+                    }
+                write_mean(ph, scale, W ? PAGE : off + n);
+            }
+        };
+        if constexpr (TURN != Turn::none) {
+            if (n == PAGE)
+                append_turned(std::true_type());
+            else
+                append_turned(std::false_type());
+        } else {
+            if (n == PAGE)
+                append(std::true_type());
+            else
+                append(std::false_type());
+        }
         team_sync();  // the next run overwrites the shared words
+    }
+}
+
+template <int D, int PAGE>
+__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE>::BLOCKS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
+    grid_wait();
+    __shared__ AppendShared<D, PAGE, AppendCfg<D, PAGE>> sm;
+    append_runs<D, PAGE, AppendCfg<D, PAGE>, Turn::none>(p, share, blockIdx.z, sm);
+}
+
+// Keys rotated on the way.  Blocks with z = 0 take keys, z = 1 values, z = 2 rotate the window's
+// queries of the key/value head's group, so that a step has one launch for all three.
+template <int D, int PAGE, bool INTER>
+__global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS) fa_kv_append_rope_kernel(const __grid_constant__ AppendParams p, int share) {
+    using C = AppendCfg<D, PAGE, 32>;
+    grid_wait();
+    __shared__ AppendShared<D, PAGE, C> sm;
+    if (blockIdx.z == 0) {
+        append_runs<D, PAGE, C, INTER ? Turn::pairs : Turn::halves>(p, share, 0, sm);
+    } else if (blockIdx.z == 1) {
+        append_runs<D, PAGE, C, Turn::none>(p, share, 1, sm);
+    } else {
+        constexpr int TPT = D / 16, TOKENS = C::THREADS / TPT;
+        const int win = blockIdx.x / share, part = blockIdx.x % share, sub = threadIdx.x % TPT;
+        const bool turned = sub < p.rot / 16;
+        const int2 piece = rope_pieces(sub, p.rot, INTER);
+        for (int i = part * TOKENS + threadIdx.x / TPT; i < kWindow; i += share * TOKENS) {
+            const int t = win * kWindow + i;
+            if (t >= p.T) break;
+            float2 f[8];
+            if (turned) {
+                const int position = __ldg(p.positions + t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = rope_factor(__ldg(p.phases + 8 * sub + j), position, p.amplitude);
+            }
+            const __nv_bfloat16 *const x = static_cast<const __nv_bfloat16 *>(p.q) + t * p.q_stride + (long long)blockIdx.y * p.G * D;
+            __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(p.q_out) + t * p.q_out_stride + (long long)blockIdx.y * p.G * D;
+#pragma unroll 2
+            for (int g = 0; g < p.G; ++g) {
+                uint4 a = *reinterpret_cast<const uint4 *>(x + g * D + 8 * piece.x), b = *reinterpret_cast<const uint4 *>(x + g * D + 8 * piece.y);
+                if (turned) {
+                    float v[16];
+                    bf16x8_to_float(a, v);
+                    bf16x8_to_float(b, v + 8);
+                    rope_turn16<INTER>(v, f);
+                    a = float_to_bf16x8(v);
+                    b = float_to_bf16x8(v + 8);
+                }
+                *reinterpret_cast<uint4 *>(y + g * D + 8 * piece.x) = a;
+                *reinterpret_cast<uint4 *>(y + g * D + 8 * piece.y) = b;
+            }
+        }
     }
 }
 
@@ -491,8 +692,29 @@ static cudaError_t launch_append(const AppendParams &p, int num_sms, cudaStream_
     return launch_early(fa_kv_append_kernel<D, PAGE>, grid, AppendCfg<D, PAGE>::THREADS, 0, stream, 1, p, (int)share);
 }
 
+template <int D, int PAGE>
+static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaStream_t stream) {
+    using C = AppendCfg<D, PAGE, 32>;
+    const int windows = (p.T + kWindow - 1) / kWindow;
+    const long long per = (long long)windows * p.Hkv * 2;
+    constexpr int most = kWindow / C::TEAMS;
+    long long share = 32ll * num_sms / per;
+    share = share < 1 ? 1 : (share > most ? most : share);
+    const dim3 grid((unsigned)(windows * share), p.Hkv, p.q ? 3 : 2);
+    return p.interleaved ? launch_early(fa_kv_append_rope_kernel<D, PAGE, true>, grid, C::THREADS, 0, stream, 1, p, (int)share)
+                         : launch_early(fa_kv_append_rope_kernel<D, PAGE, false>, grid, C::THREADS, 0, stream, 1, p, (int)share);
+}
+
 template <int D>
 static cudaError_t launch_append_page(const AppendParams &p, int num_sms, cudaStream_t stream) {
+    if (p.rot) {
+        switch (p.page_log2) {
+            case 4: return launch_append_rope<D, 16>(p, num_sms, stream);
+            case 5: return launch_append_rope<D, 32>(p, num_sms, stream);
+            case 6: return launch_append_rope<D, 64>(p, num_sms, stream);
+            default: return launch_append_rope<D, 128>(p, num_sms, stream);
+        }
+    }
     switch (p.page_log2) {
         case 4: return launch_append<D, 16>(p, num_sms, stream);
         case 5: return launch_append<D, 32>(p, num_sms, stream);

@@ -14,6 +14,7 @@ struct PlanParams {
     const int *free_pages, *free_count;
     int *table;                  // [B, max_pages]
     int *cu_q, *seq_lens, *slots, *free_left;
+    int *positions;              // [T], or null
     int B, T, max_pages, num_free, num_pages, page_log2;
 };
 cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream);
@@ -27,6 +28,15 @@ struct AppendParams {
     int8_t *mean;                // null: no means are kept
     float *mean_scale;
     int T, Hkv, num_pages, page_log2;
+    // fa_kv_append_rope (rot = 0: keys are not rotated)
+    int rot, interleaved;        // elements of a head that are rotated; which make a pair
+    float amplitude;
+    const int *positions;        // [T]
+    const unsigned long long *phases;  // [rot / 2]
+    const void *q;               // bf16 [T, Hkv * G, D], or null: no queries
+    void *q_out;
+    long long q_stride, q_out_stride;
+    int G;
 };
 cudaError_t launch_kv_append(int D, const AppendParams &p, int num_sms, cudaStream_t stream);
 
@@ -40,6 +50,19 @@ struct SelectParams {
     int B, T, G, Hkv, max_pages, num_pages, page_log2;
     int top_k, keep_first, keep_last;
 };
+struct RopeParams {
+    const void *x[2];            // queries, keys: bf16 [B, H, S, D] with any strides
+    void *y[2];
+    long long x_stride[2][3], y_stride[2][3];  // batch, token, head
+    int H[2];                    // heads; keys may have none
+    const int *positions;        // null: 0 .. S - 1
+    long long positions_stride;  // between sequences
+    const unsigned long long *phases;
+    int B, S, D, rot, interleaved, inverse;
+    float amplitude;
+};
+cudaError_t launch_rope(const RopeParams &p, int num_sms, cudaStream_t stream);
+
 constexpr int kSelectMaxPages = 49152;  // scores of one (sequence, head) stay in shared memory
 cudaError_t launch_page_select(int D, const SelectParams &p, cudaStream_t stream);
 
@@ -62,10 +85,28 @@ bool paged_fits(int D, const PagedParams &p);
 size_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_fwd_paged(int D, const PagedParams &p, int num_sms, cudaStream_t stream);
 
+struct ChunkParams {
+    const void *q;               // bf16 [T, Hq, D]
+    long long q_stride;
+    const int *cu_q, *seq_lens, *table;
+    const uint8_t *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    void *o;                     // bf16 [T, Hq, D]
+    float *lse;                  // fp32 [T, Hq]
+    float *ws;
+    int B, T, G, Hkv, max_pages, num_pages, page_log2;
+    int max_len;                 // tokens that a table row holds (set by the launch)
+    float scale_log2;            // scale * log2(e)
+    unsigned long long timeout_ns;  // bound of every on-chip wait
+};
+size_t paged_chunk_workspace_bytes(int D, int num_sms);
+cudaError_t launch_fwd_paged_chunk(int D, ChunkParams p, int num_sms, cudaStream_t stream);
+
 // Each translation unit's device status word: read it and reset it.
 cudaError_t kv_cache_status_read_and_clear(int *out);
 cudaError_t page_select_status_read_and_clear(int *out);
 cudaError_t paged_status_read_and_clear(int *out);
+cudaError_t paged_chunk_status_read_and_clear(int *out);
 
 // A launch whose blocks may be made ready while the kernel before it in the stream
 // ends: every kernel of the paged cache begins by waiting for the one before it to have

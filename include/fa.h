@@ -261,8 +261,79 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
            int Sk, int D, float scale, int causal, void *stream);
 
 /*
+ * fa_rope_phases -- the frequencies of rotary positions, for fa_rope, fa_rope_bwd and
+ * fa_kv_append_rope.  A HOST call: it writes host memory and needs no GPU.
+ *
+ * Pair i of rot_dim / 2 turns by the angle position * f_i.  Its phase is f_i in units of
+ * 2^-64 turns, modulo a turn (the low 64 bits of position * phase are the angle, exactly,
+ * for any position and for negative ones):
+ *   f_i = frequencies[i], in radians, or, where frequencies is NULL, base^(-2 i / rot_dim);
+ *   FA_ROPE_PLAIN   as they are
+ *   FA_ROPE_LINEAR  f_i / factor
+ *   FA_ROPE_NTK     from base * factor^(rot_dim / (rot_dim - 2))
+ *   FA_ROPE_YARN    f_i (1 - r_i) + f_i / factor r_i, with a ramp r_i from 0 at the pair that
+ *                   makes `fast` turns in `span` positions to 1 at the one that makes
+ *                   `slow`, and amplitude 0.1 ln(factor) + 1
+ * The phases are then copied to the device by the caller; *amplitude (1 but for
+ * FA_ROPE_YARN) is passed to the calls.
+ *   rot_dim  a multiple of 16, 16 .. 128
+ * span, fast and slow (usually 32 and 1) are read for FA_ROPE_YARN only, factor (>= 1) for all
+ * but FA_ROPE_PLAIN.  frequencies go with FA_ROPE_PLAIN and FA_ROPE_LINEAR.
+ * Errors: FA_ERR_NULLPTR; FA_ERR_BAD_SHAPE for rot_dim, scaling, or frequencies with another
+ * scaling; FA_ERR_BAD_SCALE for numbers that are not finite or out of range.
+ */
+#define FA_ROPE_PLAIN 0
+#define FA_ROPE_LINEAR 1
+#define FA_ROPE_NTK 2
+#define FA_ROPE_YARN 3
+int fa_rope_phases(unsigned long long *phases, float *amplitude, int rot_dim, double base, int scaling,
+                   double factor, double span, double fast, double slow, const double *frequencies);
+
+/*
+ * fa_rope -- rotary positions: turns pairs of each head's elements by angles that
+ * grow with the token's position,
+ *   (y1, y2) = amplitude (x1 cos t - x2 sin t, x1 sin t + x2 cos t),  t = position * f_i,
+ * in fp32, rounded once to bf16.
+ *
+ *   q, k          bf16 [B, H, S, D] with any strides: queries (Hq heads) and keys (Hk heads),
+ *                 read; k and k_out are NULL with Hk = 0
+ *   q_out, k_out  the same shapes, written; each may be its input itself (same pointer and
+ *                 strides), and may be columns of one fused tensor with others: otherwise
+ *                 outputs overlap nothing
+ *   positions     int32 [B, S] with positions_stride between sequences (0: all alike), or NULL:
+ *                 0 .. S - 1 in each
+ *   phases        64-bit [rot_dim / 2] on the device, 8-byte aligned (fa_rope_phases)
+ *   rot_dim       elements of a head that are rotated, a multiple of 16, 16 .. D; those behind
+ *                 them are copied
+ *   strides       HOST array of 12 strides in elements, read during the call: of q, k, q_out and
+ *                 k_out, each between sequences, tokens and heads; multiples of 8, >= 0; an
+ *                 output's must keep its elements apart
+ *   interleaved   0: elements i and i + rot_dim / 2 are a pair; 1: 2 i and 2 i + 1
+ *   amplitude     finite, > 0
+ *   B * S <= 2^30, Hq and Hk <= 65535, D 64 or 128
+ * Packed tokens [T, H, D] are B = 1, S = T.  Deterministic.
+ * Errors: FA_ERR_NULLPTR, FA_ERR_MISALIGNED, FA_ERR_UNSUPPORTED_D, FA_ERR_BAD_SHAPE,
+ * FA_ERR_BAD_SCALE, FA_ERR_ALIAS; FA_ERR_CUDA if the launch fails.
+ */
+int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *positions,
+            const unsigned long long *phases, int B, int S, int Hq, int Hk, int D, int rot_dim,
+            const long long *strides, long long positions_stride, int interleaved, float amplitude,
+            void *stream);
+
+/*
+ * fa_rope_bwd -- the gradients of fa_rope: dq and dk from dq_out and dk_out, by the transposed
+ * rotation, amplitude (g1 cos t + g2 sin t, -g1 sin t + g2 cos t).  Arguments and errors are
+ * fa_rope's, with the gradients of its outputs in the place of its inputs (strides in the same
+ * order: dq_out, dk_out, dq, dk).
+ */
+int fa_rope_bwd(const void *dq_out, const void *dk_out, void *dq, void *dk, const int *positions,
+                const unsigned long long *phases, int B, int S, int Hq, int Hk, int D, int rot_dim,
+                const long long *strides, long long positions_stride, int interleaved, float amplitude,
+                void *stream);
+
+/*
  * ---------------------------------------------------------------------------
- * The paged 8-bit key/value cache: decode serving.
+ * The paged 8-bit key/value cache: decode serving, and prompts in chunks.
  *
  * A cache holds num_pages pages of page_size tokens (16, 32, 64 or 128) for
  * each key/value head, in e4m3 codes with one fp32 scale per page and head:
@@ -285,7 +356,9 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *o, const flo
  * on (padding) are left as they were.  Query head h reads key/value head
  * h / (Hq / Hkv).
  *
- * One step:  fa_kv_plan -> fa_kv_append -> [fa_page_select ->] fa_fwd_paged.
+ * One step:  fa_kv_plan -> fa_kv_append -> [fa_page_select ->] fa_fwd_paged, or, where rotary
+ * positions are applied on the way, fa_kv_plan_positions -> fa_kv_append_rope -> ...; with many
+ * new tokens a sequence (prompts, chunks of them) fa_fwd_paged_chunk in the place of fa_fwd_paged.
  *
  * Lengths and tables are read on the device, so that a step can be captured in
  * a graph and replayed with other lengths.  What they hold is checked there:
@@ -337,6 +410,17 @@ int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_page
                int max_pages, int num_free, int num_pages, int page_size, void *stream);
 
 /*
+ * fa_kv_plan_positions -- fa_kv_plan, which also writes each token's position:
+ *   positions   int32 [T] written: max(cached, 0) + i for the i-th new token of a request, served or
+ *               not; -1 behind the last token
+ * as fa_rope and fa_kv_append_rope take it.  Errors: those of fa_kv_plan.
+ */
+int fa_kv_plan_positions(const int *cached_lens, const int *new_lens, const int *free_pages,
+                         const int *free_count, int *block_table, int *cu_q, int *seq_lens, int *slot_map,
+                         int *positions, int *free_left, int B, int T, int max_pages, int num_free,
+                         int num_pages, int page_size, void *stream);
+
+/*
  * fa_kv_append -- rounds a step's keys and values into the cache.
  *
  *   k, v        bf16 [T, Hkv, D], token strides k_stride, v_stride
@@ -363,6 +447,26 @@ int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_page
 int fa_kv_append(const void *k, const void *v, const int *slot_map, void *k_pages, void *v_pages,
                  float *k_scale, float *v_scale, signed char *k_mean, float *k_mean_scale, int T, int Hkv,
                  int D, long long k_stride, long long v_stride, int num_pages, int page_size, void *stream);
+
+/*
+ * fa_kv_append_rope -- fa_kv_append with the keys rotated on the way, as fa_rope rotates them, but
+ * kept in fp32 until they are rounded to codes (scales come from the rotated keys); and, where
+ * q is given, the step's queries rotated beside, as fa_rope does it.
+ *
+ *   positions   int32 [T]: the tokens' positions (fa_kv_plan_positions)
+ *   phases, rot_dim, interleaved, amplitude   as in fa_rope
+ *   q, q_out    bf16 [T, Hq, D], token strides q_stride and q_out_stride: queries, and where they
+ *               go (all T rows, whatever their slots); q_out may be q itself, and columns of
+ *               the fused tensor that k and v are columns of.  Both NULL: no queries (Hq is not read)
+ * Other arguments, and what a call leaves undefined, are fa_kv_append's.
+ * Errors: those of fa_kv_append and, for the rotation, of fa_rope.
+ */
+int fa_kv_append_rope(const void *k, const void *v, const int *positions, const unsigned long long *phases,
+                      const int *slot_map, void *k_pages, void *v_pages, float *k_scale, float *v_scale,
+                      signed char *k_mean, float *k_mean_scale, const void *q, void *q_out, int T, int Hkv,
+                      int Hq, int D, int rot_dim, int interleaved, float amplitude, long long k_stride,
+                      long long v_stride, long long q_stride, long long q_out_stride, int num_pages,
+                      int page_size, void *stream);
 
 /*
  * fa_page_select -- the pages that a sequence's queries attend to: the top_k
@@ -432,6 +536,34 @@ int fa_fwd_paged(const void *q, const int *cu_q, const int *seq_lens, const int 
 /* fa_fwd_paged_workspace_bytes -- bytes of workspace fa_fwd_paged needs on the
  * current device for these sizes (the same for all lengths); 0 for unsupported sizes. */
 size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
+
+/*
+ * fa_fwd_paged_chunk -- fa_fwd_paged (over all pages) made for many query tokens a sequence:
+ * prompts, or chunks of them behind what is cached, beside sequences with a single token.  The
+ * rows of a sequence and key/value head (query tokens times heads of the group) are taken 256 at
+ * a time, on the tensor cores; where these are few, keys are split over the chip and joined.
+ *
+ * Arguments, layout, checks of what tables hold, and outputs are fa_fwd_paged's.  Scores and sums
+ * are fp32.  q enters the products exactly, and so does K where its pages' scales are powers of two, as
+ * fa_kv_append gives them (otherwise code * scale is rounded to bf16).  Softmax weights are rounded
+ * to fp16 (each by at most 2^-11 of itself, or 2^-28 of the largest among a row's first 128 keys from the
+ * end), but to bf16 (2^-8) for 128 keys whose v_scale are further than a factor of 32 from
+ * those that the pass began with; V is exact where its pages' scales are powers of two, and
+ * otherwise rounded like the weights.  O is rounded once to bf16.
+ * T * Hq < 2^31.  Deterministic; no atomics on results.
+ *   workspace   at least fa_fwd_paged_chunk_workspace_bytes(...) bytes, as for fa_fwd_paged
+ * Errors: those of fa_fwd_paged.  An on-chip wait that gives up sets FA_ERR_TIMEOUT in the status word
+ * (fa_device_status); O and LSE are then undefined.
+ */
+int fa_fwd_paged_chunk(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                       const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                       void *o, float *lse, int B, int T, int Hq, int Hkv, int D, float scale,
+                       long long q_stride, int max_pages, int num_pages, int page_size, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* fa_fwd_paged_chunk_workspace_bytes -- bytes of workspace fa_fwd_paged_chunk needs on the current
+ * device for these sizes (the same for all lengths); 0 for unsupported sizes. */
+size_t fa_fwd_paged_chunk_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
 
 /*
  * fa_strerror -- static English text for a status code.  For FA_ERR_CUDA
