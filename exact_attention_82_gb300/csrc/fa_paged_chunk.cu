@@ -9,11 +9,17 @@
 // for any m_r.  m_r is the largest score of the row's first tile, and is taken again where a
 // half tile's sum of p passes 2^15, so that p fits fp16 (no larger than 2^15, and rounded by half a step, 2^-11
 // of itself, down to 2^-14; steps of 2^-24 below, 2^-28 of a weight at the maximum in use).
-// k_j = code * scale in bf16, exactly where the scale is a power of two, beside q as it is.
-// v_j = code * 2^(e_j - e) in fp16, e the largest exponent of the value scales in the first
-// tile and e_j the page's, exact while |e_j - e| <= 5 (codes are 2^-9 to 448); O's sums are in
-// units of 2^e.  A tile with a page further off, or with a scale that is no power of two, has both P
-// and V in bf16, which has the range of fp32 (and rounds weights to 2^-8).
+// Everything enters the products as fp16, which holds codes exactly (multiples of 2^-9 up to 448):
+//   q_r as bf16 scaled by a power of two to a largest element in [1, 2) (elements below 2^-17 of
+//   it are rounded, to steps of 2^-24 of it);
+//   k_j as code * 2^(e_j - e), e the largest exponent of the key scales in the tile: exactly, to
+//   2^-15 of the largest scale (steps of 2^-24 of it below);
+//   v_j as code * 2^(e_j - e), e the largest exponent of the value scales in the first tile.  O's
+//   sums are in units of 2^e.
+// The powers of two are put back into c (by row and tile) and into O.  A tile with a scale that is no
+// power of two, or a value scale not within 2^-15 to 2^7 of the first tile's, goes another way: scores take
+// the rest of the key scale in fp32, and weights times the value scale go to bf16 (2^-8 of each), which has
+// the range of fp32, beside the codes themselves.
 //
 // What bounds it: 4 D operations for a row and a key on the tensor cores, with enough rows
 // (256 rows share a tile of 128 keys: 2 D bytes a key for 1024 D operations); the conversion
@@ -21,14 +27,17 @@
 // and 256 rows.
 //
 // Roles of a block (one an SM, persistent):
-//   warps 0-3, 4-7   softmax of row sub-tile 0 and 1 (128 rows each): S from tensor memory, P back
-//                    over it, O out of it at the end;
-//   warps 8-11       codes: read from global memory a tile ahead (in registers), converted, and
-//                    written to shared memory in the layout that the MMAs read (128-byte swizzle);
-//   warp 12          issues the MMAs, in the order S0_j, O1 += P1 V_{j+1}, S1_j, O0 += P0 V_j, so
-//                    that one sub-tile's products run while the other's softmax does;
-//   warp 13          the block's work, segment by segment, a ring of four ahead of the others;
-//   warps 14-15      queries into shared memory.
+//   warps 0-3, 4-7   softmax of row sub-tile 0 and 1 (128 rows each): the rows' queries into shared
+//                    memory, S from tensor memory, P back over it, O out of it at the end;
+//   warps 8-15       codes: each takes 16 keys of a tile, reads them from global memory a tile ahead (into
+//                    registers), converts them and writes them to shared memory in the layout
+//                    that the MMAs read (128-byte swizzle).  What they issue is what the others have to
+//                    wait for, so they do nothing else;
+//   warps 16, 19     issue the MMAs of sub-tile 0 and 1: S_j, then O += P V_j as the softmax hands P over, so
+//                    that one sub-tile's products run while the other's softmax does.  (One warp for
+//                    both, in turns, was itself what a tile waited for: 4500 cycles a tile.)
+//   warp 17          the block's work, segment by segment, a ring of four ahead of the others;
+//   warp 18          tiles: pages and scales looked up, a ring of eight ahead of the code warps.
 //
 // Split.  Items (sequence, key/value head, 256 rows) are laid end to end, each as long as its
 // keys and a fixed cost, and the line is cut into equal shares, one a block.  What a block has of
@@ -40,6 +49,7 @@
 #include <cuda_fp16.h>
 #include <limits.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/fa.h"
@@ -50,19 +60,24 @@ namespace fa {
 
 static __device__ int g_status_chunk = 0;
 
-constexpr int kCkThreads = 512;
+constexpr int kCkThreads = 640;
+constexpr int kCkCodeWarps = 8;
 constexpr int kCkRows = 256;        // rows of an item, two sub-tiles of 128
 constexpr int kCkTile = 128;        // keys a tile
 constexpr int kCkFixed = 256;       // keys that an item's fixed cost stands for
 constexpr int kCkMinShare = 768;    // of a block, in keys
 constexpr int kCkSegs = 4;          // segments in the ring
+constexpr int kCkTiles = 8;         // tiles in theirs
 constexpr float kCkShift = 4.f;     // exponent of a weight at the maximum in use
 constexpr float kCkMost = 32768.f;  // of a half tile's sum
-constexpr int kCkApart = 5;         // of value scales' exponents, beyond which a tile takes bf16
+constexpr int kCkUp = 7, kCkDown = 15;  // how far a value scale's exponent may lie above or below the first tile's
 constexpr unsigned long long kCkDrainNs = 20ull * 1000 * 1000;
-// Registers: 512 x 128 at launch; what the last four warps give goes to the others.
-constexpr uint32_t kCkRegsSoftmax = 152, kCkRegsCodes = 136, kCkRegsOther = 72;
-static_assert(256 * kCkRegsSoftmax + 128 * kCkRegsCodes + 128 * kCkRegsOther <= 512 * 128, "register split");
+// Registers: 640 x 96 at launch; what the code warps and the last four give goes to the softmax.  None of
+// the loops may spill: beside this much shared memory the cache that holds spilled registers is small, and
+// they would come from the L2.  (The launch checks that the kernel has as many as the split assumes.)
+constexpr int kCkRegsLaunch = 96;
+constexpr uint32_t kCkRegsSoftmax = 144, kCkRegsCodes = 64, kCkRegsOther = 64;
+static_assert(256 * kCkRegsSoftmax + 256 * kCkRegsCodes + 128 * kCkRegsOther <= kCkThreads * kCkRegsLaunch, "register split");
 
 template <int D>
 struct CkCfg {
@@ -73,41 +88,49 @@ struct CkCfg {
     static constexpr uint32_t OFF_K = 2 * QT_BYTES;
     static constexpr uint32_t OFF_V = OFF_K + ST * KV_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_V + ST * KV_BYTES;
-    static constexpr uint32_t SMEM = OFF_BAR + 1024 + 1024;   // barriers and segments; alignment
+    static constexpr uint32_t SMEM = OFF_BAR + 4096 + 1024;   // barriers, segments, tiles; alignment
     static constexpr uint32_t TM_O = 256;
-    static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, kCkTile, false);
+    static constexpr uint32_t F16 = ~((7u << 7) | (7u << 10));  // fp16 operands: format 0
+    static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, kCkTile, false) & F16;
     static constexpr uint32_t IDESC_PV_BF16 = idesc_bf16_f32(128, D, true);
-    static constexpr uint32_t IDESC_PV = IDESC_PV_BF16 & ~((7u << 7) | (7u << 10));  // fp16 operands: format 0
-    static constexpr int GROUP_LOADS = D / 32;                // 16-byte loads a lane for 16 keys
+    static constexpr uint32_t IDESC_PV = IDESC_PV_BF16 & F16;
+    static constexpr int LOADS = D / 32;                      // 16-byte loads a lane for 16 keys
     static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_BAR % 1024 == 0, "atoms");
     static_assert(SMEM <= 227 * 1024 && SMEM > 114 * 1024, "one block an SM");
 };
 
-// barriers (8 bytes each) in the block's last kilobyte of shared memory
+// barriers (8 bytes each) in the block's last four kilobytes of shared memory
 enum : uint32_t {
     C_Q_FULL = 0,    // + sub-tile
-    C_Q_FREE = 2,
-    C_K_FULL = 4,    // + stage (up to 3)
-    C_K_EMPTY = 7,
-    C_V_FULL = 10,
-    C_V_EMPTY = 13,
-    C_S_FULL = 16,   // + sub-tile
-    C_P_HALF = 18,
-    C_P_FULL = 20,
-    C_PH_DONE = 22,
-    C_O_DONE = 24,
-    C_O_FREE = 26,
-    C_SEG_FULL = 28,  // + ring place
-    C_SEG_FREE = 32,
-    C_DRAIN = 36,
-    C_COUNT = 37
+    C_K_FULL = 2,    // + stage (up to 3)
+    C_K_EMPTY = 5,
+    C_V_FULL = 8,
+    C_V_EMPTY = 11,
+    C_S_FULL = 14,   // + sub-tile
+    C_P_HALF = 16,
+    C_P_FULL = 18,   // C_P_HALF + 2
+    C_PH_DONE = 20,
+    C_O_DONE = 22,
+    C_O_FREE = 24,
+    C_SEG_FULL = 26,  // + ring place
+    C_SEG_FREE = 30,
+    C_TILE_FULL = 34,
+    C_TILE_FREE = 42,
+    C_DRAIN = 50,
+    C_COUNT = 51
 };
-constexpr uint32_t kSlotTmem = 304, kSlotAbort = 308;
-constexpr uint32_t kSlotWide = 320;   // 8 words: a tile's P and V are bf16 (by the tile's number)
-constexpr uint32_t kSlotExp = 352;    // 4 words: e of a segment
-constexpr uint32_t kSlotNan = 368;    // 4 words: number + 1 of a segment with NaN among masked tiles' values
-constexpr uint32_t kSlotSegs = 384;   // 4 segments of 64 bytes
-static_assert(C_COUNT * 8 <= kSlotTmem, "");
+constexpr uint32_t kSlotTmem = 408, kSlotAbort = 412;
+constexpr uint32_t kSlotExp = 416;     // 4 words: e of a segment's values
+constexpr uint32_t kSlotNan = 432;     // 4 words: number + 1 of a segment with NaN among masked tiles' values
+constexpr uint32_t kSlotSegs = 448;    // 4 segments of 64 bytes
+// By the tile's number modulo 16 (the softmax may be ten tiles behind what is looked up):
+constexpr uint32_t kSlotWide = 704;    // whether a tile goes the other way
+constexpr uint32_t kSlotKeyExp = 768;  // 2^e of a tile's keys, negative where it goes the other way
+constexpr uint32_t kSlotRest = 832;    // what key scales are beside powers of two, and value scales, of 8 pieces: 64 bytes a tile
+// and modulo 8: flags, and 16 bytes for each 16 keys
+constexpr uint32_t kSlotFlags = 1856;
+constexpr uint32_t kSlotPieces = 2048;
+static_assert(C_COUNT * 8 <= kSlotTmem && kSlotRest + 16 * 64 <= kSlotFlags && kSlotFlags + kCkTiles * 4 <= kSlotPieces, "");
 
 // What a block does of one item.
 struct __align__(16) Seg {
@@ -117,6 +140,14 @@ struct __align__(16) Seg {
     int slot, end, pad[2];     // partial result: -1 none (the item is whole), 0 begun before, 1 left off; no more work
 };
 static_assert(sizeof(Seg) == 64, "");
+
+// Of 16 keys of a tile: their first row of the cache, how many rows have keys, and the factors in fp16 that
+// K's and V's codes are multiplied with, in both halves of a word (K's: NaN for a page outside the cache).
+struct __align__(16) Piece {
+    uint32_t row;
+    int valid;
+    uint32_t kf, vf;
+};
 
 // ---------------------------------------------------------------- the line
 struct CkSeq {
@@ -155,7 +186,7 @@ struct Cut {
 };
 
 // Moves a cut at the end of item i to the next item.
-__device__ __forceinline__ void ck_next(const ChunkParams &p, Cut &u) {
+__device__ __noinline__ void ck_next(const ChunkParams &p, Cut &u) {
     CkSeq s = ck_sequence(p, u.b);
     const int n = ck_items(p, s.nq), c = s.len - s.nq;
     u.begin += ck_begin(p, u.i + 1, c) - ck_begin(p, u.i, c);
@@ -185,7 +216,7 @@ __device__ __forceinline__ int ck_done(long long pos, long long begin, long long
 }
 
 // The cut at place pos, which lies in sequence b that begins at `base`.
-__device__ Cut ck_cut(const ChunkParams &p, int b, long long base, long long pos, long long share) {
+__device__ __noinline__ Cut ck_cut(const ChunkParams &p, int b, long long base, long long pos, long long share) {
     const CkSeq s = ck_sequence(p, b);
     const int n = ck_items(p, s.nq), c = s.len - s.nq, rows = s.nq * p.G;
     const long long head = max(ck_begin(p, n, c), 1ll);
@@ -223,30 +254,52 @@ __device__ __forceinline__ float *ck_slot(float *ws, int blocks, int block, int 
 }
 
 // ------------------------------------------------------------- conversions
+// Loads that stay where they are written: the compiler would move them down to where their
+// values are used, a whole phase of a code warp later.
+__device__ __forceinline__ uint4 ck_load16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ck_load4(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int ck_load4(const int *p) {
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ uint32_t ck_codes_f16x2(uint32_t two) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
     return h;
 }
-// 16 codes times `scale`, in bf16
-__device__ __forceinline__ void ck_bf16(const uint4 w, float scale, uint32_t (&y)[8]) {
+// 16 codes in bf16
+__device__ __forceinline__ void ck_bf16(const uint4 w, uint32_t (&y)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t h = ck_codes_f16x2(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu);
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        y[i] = pack_bf16x2(f.x * scale, f.y * scale);
+        y[i] = pack_bf16x2(f.x, f.y);
     }
 }
-// 16 codes times a power of two (twice, in halves of a word), in fp16
-__device__ __forceinline__ void ck_f16(const uint4 w, uint32_t scale2, uint32_t (&y)[8]) {
+// 16 codes times a factor (in both halves of a word), in fp16
+__device__ __forceinline__ void ck_f16(const uint4 w, uint32_t factor, uint32_t (&y)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t h = ck_codes_f16x2(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu);
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&scale2));
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&factor));
         y[i] = *reinterpret_cast<const uint32_t *>(&r);
     }
+}
+// 2^e in fp16 (0 below 2^-24), in both halves of a word; e <= 15
+__device__ __forceinline__ uint32_t ck_f16_two_to(int e) {
+    const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : (e >= -24 ? 1u << (e + 24) : 0u);
+    return h | h << 16;
 }
 __device__ __forceinline__ uint32_t ck_nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 // NaN codes as 0; whether there were any
@@ -261,33 +314,113 @@ __device__ __forceinline__ bool ck_without_nan(uint4 &w) {
     }
     return any != 0;
 }
+// registers -> TMEM, 8 consecutive columns per thread, and its wait
+__device__ __forceinline__ void ck_tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t ck_pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ float ck_two_to(int e) { return __uint_as_float((uint32_t)(max(-126, min(127, e)) + 127) << 23); }
+// Words of shared memory by their 32-bit addresses (pointers would be two registers each, in every role).
+__device__ __forceinline__ uint32_t ck_get(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void ck_put(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
 
-// Which columns of a row are NaN because a key that it sees in a masked tile has a NaN value there
-// (the MMA had zeros in their place: another row may not see the key).  Rare.
-template <int D>
-__device__ __noinline__ void ck_nan_columns(const ChunkParams &p, const Seg *g, int limit, uint32_t *mask) {
-    const int from = max(g->t0, max(0, g->c + g->row0 / p.G + 1) / kCkTile) * kCkTile, to = min(min(limit, g->len), g->t1 * kCkTile);
-    for (int j = from; j < to; ++j) {
-        const int pg = p.table[(long long)g->b * p.max_pages + (j >> p.page_log2)];
-        if (pg < 0 || pg >= p.num_pages) continue;
-        const unsigned long long row = ((unsigned long long)((uint32_t)pg * p.Hkv + g->h) << p.page_log2) + (j & ((1 << p.page_log2) - 1));
-        const uint32_t *const v = reinterpret_cast<const uint32_t *>(p.v_pages + row * D);
+// A wait bounded by the number of its tries (a second or more: a try takes some tens of cycles at least), so
+// that the thirty of them are a few instructions each.  One that gives up raises the block's abort flag and the
+// status word, and makes the block's others give up.
+__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, uint32_t tries) {
 #pragma unroll 1
-        for (int i = 0; i < D / 4; ++i) {
-            const uint32_t nan = ck_nan_codes(v[i]) >> 7;  // a bit a byte
-            const uint32_t four = (nan & 1u) | (nan >> 7 & 2u) | (nan >> 14 & 4u) | (nan >> 21 & 8u);
-            mask[i / 8] |= four << (i % 8 * 4);
+    while (!mbar_try_wait(bar, parity)) {
+        if (ck_get(abort_flag) != 0u) return false;
+        if (tries-- == 0u) {
+            ck_put(abort_flag, 1u);
+            atomicExch(&g_status_chunk, (int)FA_ERR_TIMEOUT);
+            return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ float ck_two_to(int e) { return __uint_as_float((uint32_t)(max(-126, min(127, e)) + 127) << 23); }
+
+// Of 32 columns of a row, from column 32 c on, those that are NaN because one of the keys [from, to) has a NaN
+// value there (the MMA had zeros in their place: another row may not see the key).  Rare.
+template <int D>
+__device__ __forceinline__ uint32_t ck_nan_columns(const ChunkParams &p, int b, int h, int from, int to, int c) {
+    uint32_t mask = 0;
+#pragma unroll 1
+    for (int j = from; j < to; ++j) {
+        const int pg = p.table[(long long)b * p.max_pages + (j >> p.page_log2)];
+        if (pg < 0 || pg >= p.num_pages) continue;
+        const unsigned long long row = ((unsigned long long)((uint32_t)pg * p.Hkv + h) << p.page_log2) + (j & ((1 << p.page_log2) - 1));
+        const uint32_t *const v = reinterpret_cast<const uint32_t *>(p.v_pages + row * D + c * 32);
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t nan = ck_nan_codes(v[i]) >> 7;  // a bit a byte
+            mask |= ((nan & 1u) | (nan >> 7 & 2u) | (nan >> 14 & 4u) | (nan >> 21 & 8u)) << (4 * i);
+        }
+    }
+    return mask;
 }
 
-__device__ __forceinline__ void ck_cp_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Several MMAs in a row, issued by one elected lane of a converged warp under one election (one for each, with
+// its operands brought into uniform registers one by one, took twice the instructions, and the issuing warp is
+// on the critical path of every tile).
+// S (128 x 128, fresh) = Q K^T over D = 64 C: C chunks of 64 columns, four steps of 32 bytes each.
+template <int D>
+__device__ __forceinline__ void ck_mma_s(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+            "elect.sync _|p, 0xffffffff;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\tadd.s64 a4, %1, 1024;\n\tadd.s64 a5, %1, 1026;\n\t"
+            "add.s64 a6, %1, 1028;\n\tadd.s64 a7, %1, 1030;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\tadd.s64 b4, %2, 1024;\n\tadd.s64 b5, %2, 1026;\n\t"
+            "add.s64 b6, %2, 1028;\n\tadd.s64 b7, %2, 1030;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, 0;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, 1;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+            "elect.sync _|p, 0xffffffff;\n\t"
+            "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+            "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, 0;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    }
+}
+// O (+)= P V over 64 keys: four steps of 16 keys (8 columns of P, 2048 bytes of V)
+__device__ __forceinline__ void ck_mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // --------------------------------------------------------------- the kernel
@@ -299,21 +432,24 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
     __shared__ long long share_sm;
     __shared__ Cut cut_sm[2];
     const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
-    uint8_t *const gbase = smem_raw + (sbase - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bars = sbase + C::OFF_BAR;
     auto bar = [&](uint32_t i) { return bars + 8u * i; };
-    volatile uint32_t *const words = reinterpret_cast<volatile uint32_t *>(gbase + C::OFF_BAR);
-    volatile uint32_t *const abort_flag = words + kSlotAbort / 4;
-    volatile uint32_t *const wide_of = words + kSlotWide / 4;
-    volatile uint32_t *const exp_of = words + kSlotExp / 4;
-    volatile uint32_t *const nan_of = words + kSlotNan / 4;
-    Seg *const segs = reinterpret_cast<Seg *>(gbase + C::OFF_BAR + kSlotSegs);
+    // words of it: flags and exponents of tiles and segments
+    const uint32_t abort_flag = bars + kSlotAbort;
+    auto wide_at = [&](int tile) { return bars + kSlotWide + (tile & 15) * 4; };
+    auto key_exp_at = [&](int tile) { return bars + kSlotKeyExp + (tile & 15) * 4; };
+    auto rest_at = [&](int tile) { return bars + kSlotRest + (tile & 15) * 64; };  // [k, v][8 pieces]
+    auto flags_at = [&](int tile) { return bars + kSlotFlags + tile % kCkTiles * 4; };
+    auto pieces_at = [&](int tile) { return bars + kSlotPieces + tile % kCkTiles * 128; };
+    auto exp_at = [&](int seg) { return bars + kSlotExp + seg % kCkSegs * 4; };
+    auto nan_at = [&](int seg) { return bars + kSlotNan + seg % kCkSegs * 4; };
+    auto seg_at = [&](int seg) { return bars + kSlotSegs + seg % kCkSegs * (uint32_t)sizeof(Seg); };
+#define CK_SEG(at, field) ((int)ck_get((at) + (uint32_t)offsetof(Seg, field)))
 
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(bar(C_Q_FULL + t), 2);     // a lane of each of two warps
-            mbar_init(bar(C_Q_FREE + t), 1);
+            mbar_init(bar(C_Q_FULL + t), 128);
             mbar_init(bar(C_S_FULL + t), 1);
             mbar_init(bar(C_P_HALF + t), 128);
             mbar_init(bar(C_P_FULL + t), 128);
@@ -322,21 +458,25 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
             mbar_init(bar(C_O_FREE + t), 128);
         }
         for (int s = 0; s < C::ST; ++s) {
-            mbar_init(bar(C_K_FULL + s), 4);     // a lane of each of four warps
-            mbar_init(bar(C_K_EMPTY + s), 1);
-            mbar_init(bar(C_V_FULL + s), 4);
-            mbar_init(bar(C_V_EMPTY + s), 1);
+            mbar_init(bar(C_K_FULL + s), kCkCodeWarps);  // a lane of each warp
+            mbar_init(bar(C_K_EMPTY + s), 2);    // both MMA warps
+            mbar_init(bar(C_V_FULL + s), kCkCodeWarps);
+            mbar_init(bar(C_V_EMPTY + s), 2);
         }
         for (int s = 0; s < kCkSegs; ++s) {
             mbar_init(bar(C_SEG_FULL + s), 1);
-            mbar_init(bar(C_SEG_FREE + s), 15);  // 8 softmax, 4 codes, 1 MMA, 2 query warps
-            nan_of[s] = 0;
+            mbar_init(bar(C_SEG_FREE + s), 8 + 2 + 1);  // softmax, MMA, tiles
+            ck_put(nan_at(s), 0u);
         }
-        mbar_init(bar(C_DRAIN), 1);
-        *abort_flag = 0u;
+        for (int s = 0; s < kCkTiles; ++s) {
+            mbar_init(bar(C_TILE_FULL + s), 1);
+            mbar_init(bar(C_TILE_FREE + s), kCkCodeWarps);
+        }
+        mbar_init(bar(C_DRAIN), 2);
+        ck_put(abort_flag, 0u);
         fence_mbar_init();
     }
-    if (warp == 12) {
+    if (warp == 16) {
         tmem_alloc(bars + kSlotTmem, 512);
         tmem_relinquish();
     }
@@ -386,10 +526,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = words[kSlotTmem / 4];
-    const unsigned long long tlim = p.timeout_ns;
+    const uint32_t tmem = ck_get(bars + kSlotTmem);
+    const uint32_t tries = p.tries;
     auto wait = [&](uint32_t b, uint32_t parity) {
-        return mbar_wait(bar(b), parity, abort_flag, tlim, &g_status_chunk, FA_ERR_TIMEOUT);
+        return ck_wait(bar(b), parity, abort_flag, tries);
     };
     auto wait_all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
     // segment n of the block, once it is there
@@ -399,9 +539,9 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
         if (lane == 0) mbar_arrive(bar(C_SEG_FREE + n % kCkSegs));
     };
 
-    if (warp >= 12) {
+    if (warp >= 16) {
         regs_decrease<kCkRegsOther>();
-        if (warp == 13) {
+        if (warp == 17) {
             // ================================================= segments
             Cut at = cut_sm[0];
             const Cut end = cut_sm[1];
@@ -460,341 +600,265 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                         ck_next(p, at);
                 }
                 if (lane == 0) {
-                    segs[place] = g;
+                    *reinterpret_cast<Seg *>(smem_raw + (seg_at(n) - raw)) = g;
                     mbar_arrive(bar(C_SEG_FULL + place));
                 }
                 __syncwarp();
                 if (!more) break;
             }
-        } else if (warp >= 14) {
-            // ================================================= queries
-            int use[2] = {0, 0};
-            bool ok = true;
-            for (int n = 0; ok; ++n) {
+        } else if (warp == 18) {
+            // ================================================= tiles
+            // Four tiles of a segment at a time, lane 8 j + i for piece i of the j-th.
+            const int j = lane >> 3, i = lane & 7;
+            auto exponent = [](float x) { return max((int)(__float_as_uint(x) >> 23 & 0xffu) - 127, -126); };
+            auto top_of_tile = [](int x) {
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
+                return x;
+            };
+            int tile = 0;
+            bool ok = true, end = false;
+            for (int n = 0; ok && !end; ++n) {
                 ok = segment(n);
                 if (!ok) break;
-                const Seg *const g = segs + n % kCkSegs;
-                const int q0 = g->q0, rows = g->rows, row0 = g->row0, h = g->h, N = g->t1 - g->t0, end = g->end;
-                const int first[2] = {g->first[0], g->first[1]};
+                const uint32_t g = seg_at(n);
+                end = CK_SEG(g, end) != 0;
+                const int N = CK_SEG(g, t1) - CK_SEG(g, t0), t1 = CK_SEG(g, t1), len = CK_SEG(g, len), h = CK_SEG(g, h);
+                const int edge = CK_SEG(g, c) + CK_SEG(g, row0) / p.G + 1;  // keys that the item's first row sees
+                const int *const table = p.table + (long long)CK_SEG(g, b) * p.max_pages;
                 release(n);
-                if (end) break;
-                for (int t = 0; t < 2; ++t) {
-                    if (first[t] >= N) continue;  // the sub-tile sees none of the tiles
-                    const int k = use[t]++;
-                    if (k > 0) ok = wait_all(C_Q_FREE + t, (uint32_t)(k - 1) & 1u);
-                    if (!ok) break;
-                    constexpr int PIECES = D / 8;  // of 16 bytes, a row
-#pragma unroll 4
-                    for (int i = tid - 14 * 32; i < 128 * PIECES; i += 64) {
-                        const int r = i / PIECES, piece = i % PIECES, R = row0 + t * 128 + r;
-                        const int row = min(R, rows - 1), tok = row / p.G;
-                        const __nv_bfloat16 *const src = static_cast<const __nv_bfloat16 *>(p.q) + (long long)(q0 + tok) * p.q_stride +
-                                                         (long long)(h * p.G + row - tok * p.G) * D + piece * 8;
-                        const uint32_t dst = sbase + t * C::QT_BYTES + (piece >> 3) * C::CHUNK + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-                        ck_cp_async16(dst, src, R < rows ? 16 : 0);
+                int e_ref = 0;
+                for (int it = 0; it < N || end; it += 4) {  // (behind the last segment: one more "tile" that says so)
+                    const int some = end ? 1 : min(4, N - it), key = (t1 - 1 - it - j) * kCkTile + 16 * i;
+                    int ph = -2;  // page * Hkv + head; -2: no keys, -1: outside the cache
+                    float ks = 1.f, vs = 1.f;
+                    if (!end && j < some && key < len) {
+                        ph = table[key >> p.page_log2];
+                        if (ph >= 0 && ph < p.num_pages) {
+                            ph = ph * p.Hkv + h;
+                            ks = p.k_scale[ph];
+                            vs = p.v_scale[ph];
+                        } else {
+                            ph = -1;
+                            atomicExch(&g_status_chunk, (int)FA_ERR_BAD_PAGE);
+                        }
                     }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async_smem();
+                    const bool there = ph >= 0;
+                    const int ek = exponent(ks), ev = exponent(vs);
+                    const int e_tile = top_of_tile(there ? ek : -126), v_tile = top_of_tile(there ? ev : -126);
+                    if (it == 0) e_ref = __shfl_sync(0xffffffffu, v_tile, 0);
+                    const float rest = ks * ck_two_to(-ek);
+                    const bool wide = top_of_tile(there && (rest != 1.f || vs * ck_two_to(-ev) != 1.f || ev - e_ref > kCkUp || e_ref - ev > kCkDown)) != 0;
+                    // the tiles' places in the rings
+#pragma unroll 1
+                    for (int k = 0; ok && k < some; ++k)
+                        if (tile + k >= kCkTiles) ok = wait_all(C_TILE_FREE + (tile + k) % kCkTiles, (uint32_t)((tile + k) / kCkTiles - 1) & 1u);
+                    if (!ok) break;
+                    const int m = tile + j;
+                    if (j < some) {
+                        const uint32_t row = ((uint32_t)max(ph, 0) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
+                        const uint32_t kf = ph == -1 ? 0x7e007e00u : ck_f16_two_to(min(ek - e_tile, 0));
+                        st_shared_v4(pieces_at(m) + i * (uint32_t)sizeof(Piece), row, there ? min(len - key, 16) : 0, kf, ck_f16_two_to(min(ev - e_ref, kCkUp)));
+                        if (wide) {
+                            ck_put(rest_at(m) + i * 4, __float_as_uint(rest));
+                            ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(-e_ref) : 1.f));
+                        }
+                        if (i == 0) {
+                            ck_put(wide_at(m), wide);
+                            ck_put(key_exp_at(m), __float_as_uint(wide ? -ck_two_to(e_tile) : ck_two_to(e_tile)));
+                            // 1: no more tiles, 2: a row does not see some of its keys, 4: wide, 8 *: its segment
+                            ck_put(flags_at(m), (end ? 1u : 0u) | (key + kCkTile > edge ? 2u : 0u) | (wide ? 4u : 0u) | (uint32_t)n << 3);
+                            if (it + j == 0) ck_put(exp_at(n), (uint32_t)e_ref);
+                        }
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C_Q_FULL + t));
+                    if (j < some && i == 0) mbar_arrive(bar(C_TILE_FULL + m % kCkTiles));
+                    tile += some;
+                    if (end) break;
                 }
             }
-        } else if (warp == 12) {
-            // ================================================= MMA issuer
-            const uint64_t dq = sw128_desc(sbase, 16, 1024);
+        } else {
+            // ================================================= MMA issuers
+            const int t = warp == 16 ? 0 : 1;
+            const uint64_t dq = sw128_desc(sbase + t * C::QT_BYTES, 16, 1024);
             const uint64_t dk = sw128_desc(sbase + C::OFF_K, 16, 1024);
             const uint64_t dv = sw128_desc(sbase + C::OFF_V, C::CHUNK, 1024);
-            int sk = 0, sv = 0;
-            uint32_t kph = 0, vph = 0;
-            int qn[2] = {0, 0}, npv[2] = {0, 0};
-            int tile = 0;  // tiles so far, over all segments
+            const uint32_t s_tm = tmem + t * 128, o_tm = tmem + C::TM_O + t * D;
+            int items = 0, stage = 0, tile = 0;  // items that the sub-tile took part in; stage of K and V; tiles so far
+            uint32_t phase = 0, pv_phase = 0;
             bool ok = true;
-            auto issue_s = [&](int t, int stage) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4;
-                    tc_mma_ss(tmem + t * 128, dq + ((t * C::QT_BYTES) >> 4) + off, dk + ((stage * C::KV_BYTES) >> 4) + off, C::IDESC_S,
-                              kk > 0 ? 1u : 0u);
-                }
-            };
-            auto issue_half = [&](int t, bool accumulate, int stage, uint32_t idesc, int k0) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + C::TM_O + t * D, tmem + t * 128 + (k0 + kk) * 8,
-                              dv + ((stage * C::KV_BYTES + (k0 + kk) * 16 * 128) >> 4), idesc, (accumulate || kk > 0) ? 1u : 0u);
-            };
             for (int n = 0; ok; ++n) {
                 ok = segment(n);
                 if (!ok) break;
-                const Seg *const g = segs + n % kCkSegs;
-                const int N = g->t1 - g->t0, end = g->end, act1 = g->act1, first0 = g->first[0];
+                const uint32_t g = seg_at(n);
+                const int N = CK_SEG(g, t1) - CK_SEG(g, t0), end = CK_SEG(g, end), first = t ? CK_SEG(g, first[1]) : CK_SEG(g, first[0]);
                 release(n);
                 if (end) break;
-                bool begun0 = false, begun1 = false;
-                // P_t V in two halves of 64 keys, the first as soon as the softmax has written it
-                auto issue_pv = [&](int t, bool begun, int stage, uint32_t phase, int number) -> bool {
-                    const uint32_t idesc = wide_of[number & 7] ? C::IDESC_PV_BF16 : C::IDESC_PV;
-                    if (!wait_all(C_P_HALF + t, (uint32_t)npv[t] & 1u)) return false;
-                    if (!wait_all(C_V_FULL + stage, phase)) return false;
-                    if (!begun && qn[t] > 0 && !wait_all(C_O_FREE + t, (uint32_t)(qn[t] - 1) & 1u)) return false;
-                    tc_fence_after();
-                    issue_half(t, begun, stage, idesc, 0);
-                    tc_commit(bar(C_PH_DONE + t));
-                    if (!wait_all(C_P_FULL + t, (uint32_t)npv[t] & 1u)) return false;
-                    tc_fence_after();
-                    issue_half(t, true, stage, idesc, 4);
-                    ++npv[t];
-                    return true;
-                };
-                int svp = 0;
-                uint32_t vpph = 0;
-                for (int it = 0; it < N; ++it, ++tile) {
-                    ok = wait_all(C_K_FULL + sk, kph);
+                // Tiles that the sub-tile sees nothing of: it waits for both fills, so that its arrivals are for this use.
+                int it = 0;
+#pragma unroll 1
+                for (; it < min(first, N); ++it, ++tile) {
+                    ok = wait_all(C_K_FULL + stage, phase) && wait_all(C_V_FULL + stage, phase);
                     if (!ok) break;
-                    const bool p0 = it >= first0, p1 = act1 != 0;
-                    if (p0) {
-                        if (it == first0) {
-                            ok = wait_all(C_Q_FULL + 0, (uint32_t)qn[0] & 1u);
-                            if (!ok) break;
-                        }
-                        tc_fence_after();
-                        issue_s(0, sk);
-                        tc_commit(bar(C_S_FULL + 0));
-                        if (it == N - 1) tc_commit(bar(C_Q_FREE + 0));
+                    if (lane == 0) {
+                        mbar_arrive(bar(C_K_EMPTY + stage));
+                        mbar_arrive(bar(C_V_EMPTY + stage));
                     }
-                    if (p1 && it > 0) {
-                        ok = issue_pv(1, begun1, svp, vpph, tile - 1);
-                        begun1 = true;
-                        if (!ok) break;
-                        tc_commit(bar(C_V_EMPTY + svp));
-                    }
-                    if (p1) {
-                        if (it == 0) {
-                            ok = wait_all(C_Q_FULL + 1, (uint32_t)qn[1] & 1u);
-                            if (!ok) break;
-                        }
-                        tc_fence_after();
-                        issue_s(1, sk);
-                        tc_commit(bar(C_S_FULL + 1));
-                        if (it == N - 1) tc_commit(bar(C_Q_FREE + 1));
-                    }
-                    tc_commit(bar(C_K_EMPTY + sk));
-                    if (p0) {
-                        ok = issue_pv(0, begun0, sv, vph, tile);
-                        begun0 = true;
-                        if (!ok) break;
-                        if (it == N - 1) tc_commit(bar(C_O_DONE + 0));
-                        if (!p1) tc_commit(bar(C_V_EMPTY + sv));
-                    }
-                    if (++sk == C::ST) sk = 0, kph ^= 1u;
-                    svp = sv;
-                    vpph = vph;
-                    if (++sv == C::ST) sv = 0, vph ^= 1u;
+                    __syncwarp();
+                    if (++stage == C::ST) stage = 0, phase ^= 1u;
                 }
                 if (!ok) break;
-                if (act1 && N > 0) {
-                    ok = issue_pv(1, begun1, svp, vpph, tile - 1);
+                if (it == N) continue;
+                // The others: S of the first; then for each O += P V in two halves of 64 keys, the first as soon as the softmax
+                // has written it, and S of the next right behind the second half.  Whatever else is waited
+                // for is waited for while the softmax works.  (An item's first product overwrites O, which has been
+                // read out.)
+                ok = wait_all(C_K_FULL + stage, phase) && wait_all(C_Q_FULL + t, (uint32_t)items & 1u);
+                if (ok && items > 0) ok = wait_all(C_O_FREE + t, (uint32_t)(items - 1) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+                ck_mma_s<D>(s_tm, dq, dk + ((stage * C::KV_BYTES) >> 4), C::IDESC_S);
+                tc_commit(bar(C_S_FULL + t));
+                tc_commit(bar(C_K_EMPTY + stage));
+                uint32_t more = 0;
+#pragma unroll 1
+                for (; it < N; ++it, ++tile) {
+                    const int next = stage + 1 == C::ST ? 0 : stage + 1;
+                    const uint32_t next_phase = next ? phase : phase ^ 1u;
+                    const bool last = it == N - 1;
+                    const uint32_t idesc = ck_get(wide_at(tile)) ? C::IDESC_PV_BF16 : C::IDESC_PV;
+                    const uint64_t dvs = dv + ((stage * C::KV_BYTES) >> 4), dks = dk + ((next * C::KV_BYTES) >> 4);
+                    ok = wait_all(C_V_FULL + stage, phase) && wait_all(C_P_HALF + t, pv_phase);
                     if (!ok) break;
-                    tc_commit(bar(C_O_DONE + 1));
-                    tc_commit(bar(C_V_EMPTY + svp));
+                    tc_fence_after();
+                    ck_mma_pv(o_tm, s_tm, dvs, idesc, more);
+                    tc_commit(bar(C_PH_DONE + t));
+                    // (the next tile's codes may not be looked up before this one's segment ends: waited for only within it)
+                    if (!last) ok = wait_all(C_K_FULL + next, next_phase);
+                    ok = ok && wait_all(C_P_FULL + t, pv_phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    ck_mma_pv(o_tm, s_tm + 32, dvs + ((64 * 128) >> 4), idesc, 1u);
+                    if (!last) {
+                        ck_mma_s<D>(s_tm, dq, dks, C::IDESC_S);
+                        tc_commit(bar(C_S_FULL + t));
+                        tc_commit(bar(C_K_EMPTY + next));
+                    } else {
+                        tc_commit(bar(C_O_DONE + t));
+                    }
+                    tc_commit(bar(C_V_EMPTY + stage));
+                    pv_phase ^= 1u;
+                    more = 1;
+                    stage = next, phase = next_phase;
                 }
-                if (first0 < N) ++qn[0];
-                if (act1 && N > 0) ++qn[1];
+                if (!ok) break;
+                ++items;
             }
             tc_commit(bar(C_DRAIN));
             mbar_wait_drain(bar(C_DRAIN), 0, kCkDrainNs);
         }
     } else if (warp >= 8) {
         // ===================================================== codes
-        regs_increase<kCkRegsCodes>();
-        const int cw = warp - 8;  // takes the tile's keys 32 cw .. 32 cw + 31: two groups of 16, each in one page
+        regs_decrease<kCkRegsCodes>();
+        const int cw = warp - 8;  // takes the tile's keys 16 cw .. 16 cw + 15, which are in one page
         // A load's lanes: pairs of rows in which eight lanes cover the same 64 columns (four
         // pieces of 16 codes), so that what they write falls into different banks.
         const int ld_row = 2 * (D == 128 ? lane >> 4 : lane >> 3) + ((lane >> 2) & 1);
         const int ld_piece = (lane & 3) + (D == 128 ? (lane >> 3 & 1) * 4 : 0);
         constexpr int LD_ROWS = D == 128 ? 4 : 8;
-        struct Tile {   // of the sequence of tiles over all segments
-            int seg, key0, len, edge, first;  // edge: keys that the item's first row sees; first tile of a segment
-        };
-        int seg_next = 0, it_next = 0;
-        Tile cur{}, nxt{};
-        bool ok = true;
-        int seg_n = 0, seg_t1 = 0, seg_len = 0, seg_edge = 0, seg_b = 0, seg_h = 0;
-        // The next tile, and this lane's group of it (lanes 0-7): its entry of the block table.  Where the
-        // tile's segment is not there yet: to be asked again, or waited for.  (Only once all tiles
-        // before it are handed over: a segment's place in the ring is free when the softmax is
-        // through with the one four before it, and segments without tiles lie between.)
-        int pg_look = -2;  // -2: no keys there
-        Tile look{};
-        int h_look = 0;
-        bool looked = false, end = false;
-        auto look_up = [&](bool may_wait) {
-            if (looked || end) return;
-            while (it_next == seg_n) {
-                if (may_wait)
-                    ok = segment(seg_next);
-                else if (!__all_sync(0xffffffffu, mbar_try_wait(bar(C_SEG_FULL + seg_next % kCkSegs), (uint32_t)(seg_next / kCkSegs) & 1u)))
-                    return;
-                if (!ok) return;
-                const Seg *const g = segs + seg_next % kCkSegs;
-                if (g->end) {
-                    release(seg_next);
-                    end = true;
-                    return;
-                }
-                seg_n = g->t1 - g->t0;
-                seg_t1 = g->t1;
-                seg_len = g->len;
-                seg_edge = g->c + g->row0 / p.G + 1;
-                seg_b = g->b;
-                seg_h = g->h;
-                release(seg_next);
-                ++seg_next;
-                it_next = 0;
-            }
-            look.seg = seg_next - 1;
-            look.key0 = (seg_t1 - 1 - it_next) * kCkTile;
-            look.len = seg_len;
-            look.edge = seg_edge;
-            look.first = it_next == 0;
-            h_look = seg_h;
-            ++it_next;
-            const int key = look.key0 + 16 * (lane & 7);
-            pg_look = -2;
-            if (key < look.len) pg_look = p.table[(long long)seg_b * p.max_pages + (key >> p.page_log2)];
-            looked = true;
-        };
-        // what is known of a tile whose codes are being read: per lane (0-7) its group's page
-        struct Meta {
-            int ph;          // page * Hkv + head; -1: outside the cache, -2: no keys
-            float ks, vs;
-        };
-        auto resolve = [&]() {
-            Meta m{-2, 1.f, 1.f};
-            if (pg_look != -2) {
-                const bool good = pg_look >= 0 && pg_look < p.num_pages;
-                m.ph = good ? pg_look * p.Hkv + h_look : -1;
-                if (good) {
-                    m.ks = __ldg(p.k_scale + m.ph);
-                    m.vs = __ldg(p.v_scale + m.ph);
-                } else {
-                    atomicExch(&g_status_chunk, (int)FA_ERR_BAD_PAGE);
-                }
-            }
-            return m;
-        };
-        uint4 kr[2 * C::GROUP_LOADS], vr[2 * C::GROUP_LOADS];
-        const int page_mask = (1 << p.page_log2) - 1;
-        auto load = [&](const uint8_t *pages, const Tile &x, const Meta &m, uint4 (&r)[2 * C::GROUP_LOADS]) {
+        // (Spilled registers would go to the L2: the cache beside this much shared memory is small.)
+        uint32_t flags = 0, row = 0, kf = 0, vf = 0;   // of the tile being worked on
+        int valid = 0;
+        uint4 kr[C::LOADS], vr[C::LOADS];
+        const uint32_t lane_at = ld_row * D + ld_piece * 16;
+        auto load = [&](const uint8_t *pages, uint4 (&r)[C::LOADS]) {
+            const uint8_t *const src = pages + (unsigned long long)row * D + lane_at;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int key = x.key0 + 16 * (2 * cw + g);
-                const int ph = __shfl_sync(0xffffffffu, m.ph, 2 * cw + g);
-                const unsigned long long row = ((unsigned long long)(uint32_t)max(ph, 0) << p.page_log2) + (key & page_mask);
-                const uint8_t *const src = pages + (row + ld_row) * D + ld_piece * 16;
-#pragma unroll
-                for (int i = 0; i < C::GROUP_LOADS; ++i) {
-                    r[g * C::GROUP_LOADS + i] = make_uint4(0, 0, 0, 0);
-                    if (ph >= 0 && key + i * LD_ROWS + ld_row < x.len)
-                        r[g * C::GROUP_LOADS + i] = __ldg(reinterpret_cast<const uint4 *>(src + i * LD_ROWS * D));
-                }
+            for (int i = 0; i < C::LOADS; ++i) {
+                r[i] = make_uint4(0, 0, 0, 0);
+                if (i * LD_ROWS + ld_row < valid) r[i] = ck_load16(src + i * LD_ROWS * D);
             }
         };
-        auto store = [&](uint32_t base, int g, int i, const uint32_t (&y)[8]) {
-            const int r = 16 * (2 * cw + g) + i * LD_ROWS + ld_row;
-            const uint32_t at = base + (ld_piece >> 2) * C::CHUNK + r * 128, piece = 2 * (ld_piece & 3), sw = r & 7;
-            st_shared_v4(at + ((piece ^ sw) << 4), y[0], y[1], y[2], y[3]);
-            st_shared_v4(at + (((piece + 1) ^ sw) << 4), y[4], y[5], y[6], y[7]);
+        // Where this lane's 32 bytes of a row go: two pieces of 16, swapped within 128 bytes by the row.  Its rows are LD_ROWS
+        // (a multiple of 4) apart, so that their swaps differ in one bit at most.
+        const uint32_t to = (ld_piece >> 2) * C::CHUNK + (16 * cw + ld_row) * 128, piece = 2 * (ld_piece & 3);
+        const uint32_t to0 = to + ((piece ^ (ld_row & 7)) << 4), to1 = to + (((piece + 1) ^ (ld_row & 7)) << 4);
+        auto store = [&](uint32_t base, int i, const uint32_t (&y)[8]) {
+            const uint32_t flip = (i * LD_ROWS & 7) << 4, down = i * LD_ROWS * 128;
+            st_shared_v4(base + (to0 ^ flip) + down, y[0], y[1], y[2], y[3]);
+            st_shared_v4(base + (to1 ^ flip) + down, y[4], y[5], y[6], y[7]);
         };
-        Meta m_cur{-2, 1.f, 1.f}, m_nxt{-2, 1.f, 1.f};
-        look_up(true);
-        bool have = looked;
-        if (have) {
-            looked = false;
-            cur = look;
-            m_cur = resolve();
-            load(p.k_pages, cur, m_cur, kr);
-            look_up(false);
-        }
-        int e_ref = 0;
-        for (int n = 0; ok && have; ++n) {
-            // ---- which operands the tile's second product takes (all four warps find the same)
-            const uint32_t vu = __float_as_uint(m_cur.vs);
-            const int e = (int)(vu >> 23 & 0xffu) - 127;
-            const bool there = lane < 8 && m_cur.ph >= 0;
-            if (cur.first) {
-                const int top = __reduce_max_sync(0xffffffffu, there ? e : -1000);
-                e_ref = top == -1000 ? 0 : top;
-            }
-            const bool wide = __any_sync(0xffffffffu, there && ((vu & 0x7fffffu) != 0 || e - e_ref > kCkApart || e_ref - e > kCkApart));
-            if (cw == 0 && lane == 0) {
-                wide_of[n & 7] = wide;
-                if (cur.first) exp_of[cur.seg % kCkSegs] = (uint32_t)e_ref;
-            }
-            // ---- K of the tile
-            const int st = n % C::ST;
-            const uint32_t use = (uint32_t)(n / C::ST) & 1u;
-            if (n >= C::ST) ok = wait_all(C_K_EMPTY + st, use ^ 1u);
-            if (!ok) break;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float ks = __shfl_sync(0xffffffffu, m_cur.ks, 2 * cw + g);
-                const bool bad = __shfl_sync(0xffffffffu, m_cur.ph, 2 * cw + g) == -1;
-#pragma unroll
-                for (int i = 0; i < C::GROUP_LOADS; ++i) {
-                    uint32_t y[8];
-                    ck_bf16(kr[g * C::GROUP_LOADS + i], bad ? __uint_as_float(0x7fc00000u) : ks, y);
-                    store(sbase + C::OFF_K + st * C::KV_BYTES, g, i, y);
-                }
-            }
+        auto hand_over = [&](uint32_t b) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C_K_FULL + st));
-            // ---- what comes next is asked for: this tile's V, the next one's K, and pages behind it
-            load(p.v_pages, cur, m_cur, vr);
-            auto go_on = [&]() {
-                if (!looked) return false;
-                looked = false;
-                nxt = look;
-                m_nxt = resolve();
-                load(p.k_pages, nxt, m_nxt, kr);
-                look_up(false);
-                return true;
-            };
-            bool more = go_on();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
+        // Takes up tile m, which has been looked up: asks for its K.  Returns whether there is one.
+        auto take_up = [&](int m) {
+            flags = ck_get(flags_at(m));
+            uint32_t some;
+            ld_shared_v4(pieces_at(m) + cw * (uint32_t)sizeof(Piece), row, some, kf, vf);
+            valid = (int)some;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C_TILE_FREE + m % kCkTiles));
+            if (flags & 1u) return false;
+            load(p.k_pages, kr);
+            return true;
+        };
+        bool ok = wait_all(C_TILE_FULL, 0);
+        bool have = ok && take_up(0);
+        if (have) load(p.v_pages, vr);
+        int st = 0;
+        uint32_t use = 1;   // parity of what the stage's last use leaves when it is done (passes at the first)
+#pragma unroll 1
+        for (int n = 0; have; ++n) {
+            // ---- K of the tile; then the next one's is asked for, if it has been looked up (it may not be before this
+            // tile is done: segments' places in the ring are free when the softmax is through with them)
+            ok = wait_all(C_K_EMPTY + st, use);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < C::LOADS; ++i) {
+                uint32_t y[8];
+                ck_f16(kr[i], kf, y);
+                store(sbase + C::OFF_K + st * C::KV_BYTES, i, y);
+            }
+            hand_over(C_K_FULL + st);
+            const uint32_t now = flags, v_factor = vf;
+            const uint32_t next = C_TILE_FULL + (n + 1) % kCkTiles, next_phase = (uint32_t)((n + 1) / kCkTiles) & 1u;
+            const bool early = __all_sync(0xffffffffu, mbar_try_wait(bar(next), next_phase));
+            if (early) have = take_up(n + 1);
             // ---- V of the tile
-            if (n >= C::ST) ok = wait_all(C_V_EMPTY + st, use ^ 1u);
+            ok = wait_all(C_V_EMPTY + st, use);
             if (!ok) break;
-            const bool masked = cur.key0 + kCkTile > cur.edge;  // a row does not see some of its keys: their NaN must not reach it
+            if (__builtin_expect((now & 6u) == 0, 1)) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float vs = __shfl_sync(0xffffffffu, m_cur.vs, 2 * cw + g);
-                const int de = (int)(__float_as_uint(vs) >> 23 & 0xffu) - 127 - e_ref;
-                const uint32_t f16 = (uint32_t)(max(-14, min(15, de)) + 15) << 10, two = f16 | f16 << 16;  // 2^de
-                const float f32 = vs * ck_two_to(-e_ref);
-#pragma unroll
-                for (int i = 0; i < C::GROUP_LOADS; ++i) {
-                    uint4 w = vr[g * C::GROUP_LOADS + i];
-                    if (masked && ck_without_nan(w)) nan_of[cur.seg % kCkSegs] = (uint32_t)cur.seg + 1u;
+                for (int i = 0; i < C::LOADS; ++i) {
                     uint32_t y[8];
-                    if (wide)
-                        ck_bf16(w, f32, y);
-                    else
-                        ck_f16(w, two, y);
-                    store(sbase + C::OFF_V + st * C::KV_BYTES, g, i, y);
+                    ck_f16(vr[i], v_factor, y);
+                    store(sbase + C::OFF_V + st * C::KV_BYTES, i, y);
                 }
+            } else {
+                bool nan = false;
+#pragma unroll
+                for (int i = 0; i < C::LOADS; ++i) {
+                    uint32_t y[8];
+                    if (now & 2u) nan |= ck_without_nan(vr[i]);  // they must not reach the rows that do not see them
+                    if (now & 4u)
+                        ck_bf16(vr[i], y);
+                    else
+                        ck_f16(vr[i], v_factor, y);
+                    store(sbase + C::OFF_V + st * C::KV_BYTES, i, y);
+                }
+                if (nan) ck_put(nan_at(now >> 3), (now >> 3) + 1u);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C_V_FULL + st));
-            if (!more) {
-                look_up(true);
+            hand_over(C_V_FULL + st);
+            if (!early) {
+                ok = wait_all(next, next_phase);
                 if (!ok) break;
-                more = go_on();
+                have = take_up(n + 1);
             }
-            cur = nxt;
-            m_cur = m_nxt;
-            have = more;
+            if (have) load(p.v_pages, vr);
+            if (++st == C::ST) st = 0, use ^= 1u;
         }
     } else {
         // ============================================ softmax warpgroups
@@ -803,172 +867,210 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lane_off + t * 128;
         const uint32_t o_tm = tmem + lane_off + C::TM_O + t * D;
-        const float sl2 = p.scale_log2;
-        const uint64_t c2 = f2_pack(sl2, sl2);
         int ns = 0, od = 0, tile = 0;  // S tiles and items of this sub-tile, tiles of the block so far
         bool ok = true;
         for (int n = 0; ok; ++n) {
             ok = segment(n);
             if (!ok) break;
-            const Seg *const g = segs + n % kCkSegs;  // (released behind the epilogue, which reads it again)
-            if (g->end) {
+            const uint32_t g = seg_at(n);  // (released behind the epilogue, which reads it again)
+            if (CK_SEG(g, end)) {
                 release(n);
                 break;
             }
-            const int N = g->t1 - g->t0, first = t ? g->first[1] : g->first[0];
-            if (t == 1 && !g->act1) {
+            const int N = CK_SEG(g, t1) - CK_SEG(g, t0), first = CK_SEG(g, first[0]) * (1 - t) + CK_SEG(g, first[1]) * t;
+            if (t == 1 && !CK_SEG(g, act1)) {
                 tile += N;
                 release(n);
                 continue;
             }
-            const int limit = g->c + min(g->row0 + t * 128 + row, g->rows - 1) / p.G + 1;  // keys that this row sees
-            const int edge = g->c + (g->row0 + t * 128) / p.G + 1;                         // and the sub-tile's first row
-            const int key1 = g->t1 * kCkTile;
+            const int limit = CK_SEG(g, c) + min(CK_SEG(g, row0) + t * 128 + row, CK_SEG(g, rows) - 1) / p.G + 1;  // keys that this row sees
+            const int edge = CK_SEG(g, c) + (CK_SEG(g, row0) + t * 128) / p.G + 1;                         // and the sub-tile's first row
+            const int key1 = CK_SEG(g, t1) * kCkTile;
             tile += min(first, N);
+            // ---- the row's query, scaled to fp16, into shared memory (the segment before has read what was
+            // there: its last S is complete)
+            float c_row = p.scale_log2;
+            if (first < N) {
+                const int R = CK_SEG(g, row0) + t * 128 + row, tok = min(R, CK_SEG(g, rows) - 1) / p.G;
+                const uint4 *const src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (long long)(CK_SEG(g, q0) + tok) * p.q_stride +
+                                                                         (long long)(CK_SEG(g, h) * p.G + R - tok * p.G) * D);
+                uint4 w[D / 8];
+                uint32_t am = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (R < CK_SEG(g, rows)) w[i] = __ldg(src + i);
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    am = __vmaxu2(am, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+                am = max(am & 0xffffu, am >> 16);
+                const int e = am ? max(-126, min(126, (int)(am >> 7) - 127)) : 0;
+                const float down = ck_two_to(-e);
+                c_row = p.scale_log2 * ck_two_to(e);
+                const uint32_t dst = sbase + t * C::QT_BYTES + row * 128;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = ck_pack_f16(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xffff0000u) * down);
+                    st_shared_v4(dst + (i >> 3) * C::CHUNK + (((i & 7) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(C_Q_FULL + t));
+            }
             float m_used = -INFINITY, l_run = 0.f;
+            bool ready = false;  // every row of the warp has a maximum
             for (int it = first; it < N; ++it, ++tile) {
                 ok = wait_all(C_S_FULL + t, (uint32_t)ns & 1u);
                 if (!ok) break;
                 ++ns;
                 tc_fence_after();
-                const bool wide = wide_of[tile & 7] != 0;
+                // ---- the ordinary tile: no mask, fp16, and a maximum that holds.  S goes through the registers 16
+                // keys at a time, the next two times 16 on their way; P is handed over in halves of 64 keys.
+                // (The loops of all roles have to stay in the instruction cache together, so that this
+                // one has nothing else in it.)
+                const float key_exp = __uint_as_float(ck_get(key_exp_at(tile)));  // negative: the tile goes the other way
                 const int col0 = key1 - (it + 1) * kCkTile;
-                const bool masked = col0 + kCkTile > edge;
-                const int lim = limit - col0;
-                // S goes through the registers 32 keys at a time, the next 32 on their way
-                uint32_t s[2][32];
-                auto mask32 = [&](uint32_t (&x)[32], int c) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (c * 32 + e >= lim) x[e] = __float_as_uint(-INFINITY);
-                };
-                auto scale_o = [&](float f) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t o[16];
-                        tmem_ld16(o_tm + c * 16, o);
-                        tmem_ld_wait16(o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st16(o_tm + c * 16, o);
-                        tmem_st_wait16(o);
-                    }
-                };
-                // the largest of m_used and the scores of chunks [cb, 4)
-                auto max_from = [&](int cb) {
-                    float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = cb; c < 4; ++c) {
-                        tmem_ld32(s_tm + c * 32, s[0]);
-                        tmem_ld_wait(s[0]);
-                        if (masked) mask32(s[0], c);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                mq[q] = max3f(mq[q], __uint_as_float(s[0][e + 2 * q]), __uint_as_float(s[0][e + 2 * q + 1]));
-                    }
-                    return fmaxf(m_used, max3f(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sl2);
-                };
-                // the factor of what was summed so far when the maximum becomes m_new
-                auto raise = [&](float m_new) {
-                    const float f = m_new == -INFINITY ? 1.f : ex2_approx(m_used - m_new);  // 0 on a row's first keys
-                    m_used = m_new;
-                    return f;
-                };
-                uint32_t pk[32];
-                // p of chunks cb and cb + 1, of which the first is already being loaded; returns their sum
-                auto exp_half = [&](int cb) -> float {
-                    const float nm = m_used == -INFINITY ? 0.f : kCkShift - m_used;  // no key yet: p = 0
-                    const uint64_t nm2 = f2_pack(nm, nm);
+                const bool masked = col0 + kCkTile > edge, wide = key_exp < 0.f;
+                const float c_tile = c_row * fabsf(key_exp);
+                int half = 0;
+                if (!(masked || wide) && ready) {
+                    uint32_t s[3][16], pk[32];
+                    const float nm = kCkShift - m_used;
+                    const uint64_t c2 = f2_pack(c_tile, c_tile), nm2 = f2_pack(nm, nm);
                     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                    tmem_ld16(s_tm, s[0]);
+                    half = [&]() {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tmem_ld_wait(s[c]);
-                        if (cb + c < 3) tmem_ld32(s_tm + (cb + c + 1) * 32, s[c ^ 1]);
-                        if (masked) mask32(s[c], cb + c);
-                        if (wide) {
+                        for (int c = 0; c < 8; ++c) {
+                            if (c == 0) tmem_ld16(s_tm + 16, s[1]);
+                            if (c < 6) tmem_ld16(s_tm + (c + 2) * 16, s[(c + 2) % 3]);
+                            tmem_ld_wait16(s[c % 3]);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 8; ++e) {
                                 float x0, x1;
-                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), c2, nm2), x0, x1);
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c % 3][2 * e]), __uint_as_float(s[c % 3][2 * e + 1])), c2, nm2), x0, x1);
                                 const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                                 acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
-                                pk[c * 16 + e] = pack_bf16x2(p0, p1);
+                                pk[c % 4 * 8 + e] = ck_pack_f16(p0, p1);
                             }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float x0, x1;
-                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), c2, nm2), x0, x1);
-                                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                                acc[e & 3] = f2_add(acc[e & 3], f2_pack(p0, p1));
-                                pk[c * 16 + e] = ck_pack_f16(p0, p1);
+                            if (c % 4 == 3) {
+                                float a0, a1, b0, b1;
+                                f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+                                f2_unpack(f2_add(acc[2], acc[3]), b0, b1);
+                                const float sum = (a0 + a1) + (b0 + b1);
+                                // scores have grown past the maximum in use?
+                                if (__any_sync(0xffffffffu, !(sum <= kCkMost))) return c / 4;
+                                l_run += sum;
+                                acc[0] = acc[1] = acc[2] = acc[3] = 0ull;
+                                tmem_st16(s_tm + c / 4 * 32, pk);
+                                tmem_st16(s_tm + c / 4 * 32 + 16, pk + 16);
+                                tmem_st_wait(pk);
+                                tc_fence_before();
+                                mbar_arrive(bar((c == 3 ? C_P_HALF : C_P_FULL) + t));
                             }
                         }
-                    }
-                    float a0, a1, b0, b1;
-                    f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-                    f2_unpack(f2_add(acc[2], acc[3]), b0, b1);
-                    return (a0 + a1) + (b0 + b1);
-                };
-                auto store_half = [&](int half) {
-                    tmem_st16(s_tm + half * 32, pk);
-                    tmem_st16(s_tm + half * 32 + 16, pk + 16);
-                    tmem_st_wait(pk);
-                    tc_fence_before();
-                };
-                const bool took_max = __any_sync(0xffffffffu, m_used == -INFINITY);
-                float alpha = 1.f, beta = 1.f;
-                if (took_max) alpha = raise(max_from(0));
-                tmem_ld32(s_tm, s[0]);
-                float sa = exp_half(0);
-                const bool redo = !took_max && __any_sync(0xffffffffu, !(sa <= kCkMost));
-                if (redo) {  // nothing of this tile is handed over yet: its true maximum
-                    tmem_ld_wait(s[0]);
-                    alpha = raise(max_from(0));
-                    tmem_ld32(s_tm, s[0]);
-                    sa = exp_half(0);
+                        return 2;
+                    }();
+                    if (half == 2) continue;
+                    tmem_ld_wait16(s[0]);
+                    tmem_ld_wait16(s[1]);
+                    tmem_ld_wait16(s[2]);
                 }
-                if (it > first && (redo || took_max)) scale_o(alpha);  // O holds earlier tiles at the old maximum
-                tmem_ld_wait(s[0]);  // (S of chunk 2: P may overwrite chunks 0 and 1, which are read)
-                store_half(0);
-                mbar_arrive(bar(C_P_HALF + t));
-                float sb = exp_half(2);
-                if (!took_max && !redo && __any_sync(0xffffffffu, !(sb <= kCkMost))) {
-                    // the first half's product must be in O before O is rescaled
+                const int lim = limit - col0;
+                // ---- the others, or the second half of one: the maximum first, then P, 16 keys at a time
+                uint32_t x[16];
+                auto piece = [&](int c) {
+                    tmem_ld16(s_tm + c * 16, x);
+                    tmem_ld_wait16(x);
+                    if (wide) {
+                        const float f = __uint_as_float(ck_get(rest_at(tile) + c * 4));
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c * 16 + e >= lim) x[e] = __float_as_uint(-INFINITY);
+                    }
+                };
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 4 * half; c < 8; ++c) {
+                    piece(c);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) top = max3f(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                }
+                const float m_new = fmaxf(m_used, top * c_tile);
+                ready = __all_sync(0xffffffffu, m_new != -INFINITY);
+                const float factor = m_new == -INFINITY ? 1.f : ex2_approx(m_used - m_new);  // 0 on a row's first keys
+                m_used = m_new;
+                l_run *= factor;
+                if (half == 1) {  // the first half's product must be in O before O is rescaled
                     ok = wait_all(C_PH_DONE + t, (uint32_t)(ns - 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    beta = raise(max_from(2));  // chunks 2 and 3 are still there: P is in columns 0-31
-                    scale_o(beta);
-                    tmem_ld32(s_tm + 64, s[0]);
-                    sb = exp_half(2);
                 }
-                store_half(1);
-                l_run = (l_run * alpha + sa) * beta + sb;
+                if ((half == 1 || it > first) && __any_sync(0xffffffffu, factor != 1.f)) {  // O holds what came before at the old maximum
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        tmem_ld16(o_tm + c * 16, x);
+                        tmem_ld_wait16(x);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor);
+                        tmem_st16(o_tm + c * 16, x);
+                        tmem_st_wait16(x);
+                    }
+                }
+                const float nm = m_used == -INFINITY ? 0.f : kCkShift - m_used;  // no key yet: p = 0
+#pragma unroll 1
+                for (int c = 4 * half; c < 8; ++c) {
+                    piece(c);
+                    uint32_t y[8];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c_tile, nm)));
+                        sum += __uint_as_float(x[e]);
+                    }
+                    l_run += sum;
+                    if (wide) {
+                        const float f = __uint_as_float(ck_get(rest_at(tile) + 32 + c * 4));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * f, __uint_as_float(x[2 * e + 1]) * f);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = ck_pack_f16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                    }
+                    ck_tmem_st8(s_tm + c * 8, y);  // (over scores that are read already)
+                    if (c == 3) {
+                        tc_fence_before();
+                        mbar_arrive(bar(C_P_HALF + t));
+                    }
+                }
+                tc_fence_before();
                 mbar_arrive(bar(C_P_FULL + t));
             }
             if (!ok) break;
             // ---- the rows' results, 32 columns at a time
             const bool some = first < N;  // the sub-tile has tiles here
             float unit = 1.f;
-            uint32_t nan_mask[4] = {0, 0, 0, 0};
             bool nan_there = false;
             if (some) {
                 ok = wait_all(C_O_DONE + t, (uint32_t)od & 1u);
                 if (!ok) break;
                 ++od;
                 tc_fence_after();
-                unit = ck_two_to((int)exp_of[n % kCkSegs]);
-                nan_there = nan_of[n % kCkSegs] == (uint32_t)n + 1u;
-                if (nan_there) ck_nan_columns<D>(p, g, limit, nan_mask);
+                unit = ck_two_to((int)ck_get(exp_at(n)));
+                nan_there = ck_get(nan_at(n)) == (uint32_t)n + 1u;
             }
-            const int R = g->row0 + t * 128 + row, slot = g->slot;
-            const bool there = R < g->rows, empty = l_run == 0.f;  // empty: no key
+            const int R = CK_SEG(g, row0) + t * 128 + row, slot = CK_SEG(g, slot);
+            const bool there = R < CK_SEG(g, rows), empty = l_run == 0.f;  // empty: no key
             const float inv = empty ? 0.f : 1.f / l_run;
-            const int tok = min(R, g->rows - 1) / p.G;
-            const long long at = (long long)(g->q0 + tok) * (p.Hkv * p.G) + g->h * p.G + (R - tok * p.G);
+            const int tok = min(R, CK_SEG(g, rows) - 1) / p.G;
+            const long long at = (long long)(CK_SEG(g, q0) + tok) * (p.Hkv * p.G) + CK_SEG(g, h) * p.G + (R - tok * p.G);
             float *const part = ck_slot(p.ws, gridDim.x, blockIdx.x, max(slot, 0), D);
             const int r = t * 128 + row;
 #pragma unroll 1
@@ -978,7 +1080,11 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     tmem_ld32(o_tm + c * 32, o);
                     tmem_ld_wait(o);
                 }
-                const uint32_t nan = nan_there ? (c == 0 ? nan_mask[0] : c == 1 ? nan_mask[1] : c == 2 ? nan_mask[2] : nan_mask[3]) : 0u;
+                uint32_t nan = 0;
+                if (nan_there) {
+                    const int from = max(CK_SEG(g, t0), max(0, CK_SEG(g, c) + CK_SEG(g, row0) / p.G + 1) / kCkTile) * kCkTile;
+                    nan = ck_nan_columns<D>(p, CK_SEG(g, b), CK_SEG(g, h), from, min(min(limit, CK_SEG(g, len)), CK_SEG(g, t1) * kCkTile), c);
+                }
                 if (!there) continue;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -1019,7 +1125,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 16) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1071,6 +1177,12 @@ size_t paged_chunk_workspace_bytes(int D, int num_sms) {
 
 template <int D>
 static cudaError_t launch_chunk(const ChunkParams &p, int num_sms, cudaStream_t stream) {
+    // With fewer registers at launch than the split counts on, the warps that ask for more would wait for ever.
+    static const bool split_holds = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, fa_fwd_paged_chunk_kernel<D>) == cudaSuccess && a.numRegs == kCkRegsLaunch;
+    }();
+    if (!split_holds) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(fa_fwd_paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CkCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     e = launch_early(fa_fwd_paged_chunk_kernel<D>, dim3((unsigned)num_sms), kCkThreads, CkCfg<D>::SMEM, stream, 1, p);

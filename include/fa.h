@@ -544,12 +544,13 @@ size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  * a time, on the tensor cores; where these are few, keys are split over the chip and joined.
  *
  * Arguments, layout, checks of what tables hold, and outputs are fa_fwd_paged's.  Scores and sums
- * are fp32.  q enters the products exactly, and so does K where its pages' scales are powers of two, as
- * fa_kv_append gives them (otherwise code * scale is rounded to bf16).  Softmax weights are rounded
- * to fp16 (each by at most 2^-11 of itself, or 2^-28 of the largest among a row's first 128 keys from the
- * end), but to bf16 (2^-8) for 128 keys whose v_scale are further than a factor of 32 from
- * those that the pass began with; V is exact where its pages' scales are powers of two, and
- * otherwise rounded like the weights.  O is rounded once to bf16.
+ * are fp32.  q and K enter the products exactly (q as bf16 scaled by a power of two to fp16: elements below
+ * 2^-17 of their row's largest are rounded, to steps of 2^-24 of it; K to steps of 2^-24 of the largest
+ * k_scale among the same 128 keys).  Softmax weights are rounded to fp16 (each by at most 2^-11 of itself,
+ * or 2^-29 of the largest among those that the row sees first, from its end), but weights times
+ * v_scale are rounded to bf16 (2^-8 of each) for 128 keys among which a scale is no power of two
+ * (fa_kv_append's are), or a v_scale is not within 2^-15 to 2^7 of the largest that the pass began
+ * with.  O is rounded once to bf16.
  * T * Hq < 2^31.  Deterministic; no atomics on results.
  *   workspace   at least fa_fwd_paged_chunk_workspace_bytes(...) bytes, as for fa_fwd_paged
  * Errors: those of fa_fwd_paged.  An on-chip wait that gives up sets FA_ERR_TIMEOUT in the status word

@@ -23,12 +23,7 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def bf16_round(x):
-    """float64 -> the nearest bf16 value (through fp32, which holds every product of a code and an fp32 scale to 2^-24)."""
-    return torch.from_numpy(np.asarray(x, np.float64)).to(torch.float32).to(torch.bfloat16).double().numpy()
-
-
-def reference(c, q, cu, scale, round_k=False):
+def reference(c, q, cu, scale):
     """(O, LSE, the weights' mean of |v|, the largest |score|) of each row, in 64 bits; NaN rows as fa.h says."""
     T, Hq, D = q.shape
     G, page = Hq // c.Hkv, c.page
@@ -46,8 +41,6 @@ def reference(c, q, cu, scale, round_k=False):
         for h in range(c.Hkv):
             K = (pu.E4M3[c.kc[at, h]] * c.ks[at, h][:, None, None]).reshape(-1, D)[:L]
             V = (pu.E4M3[c.vc[at, h]] * c.vs[at, h][:, None, None]).reshape(-1, D)[:L]
-            if round_k:
-                K = bf16_round(K)
             poison = np.repeat(bad, page)[:L]
             K, V = np.where(poison[:, None], np.nan, K), np.where(poison[:, None], 0.0, V)
             x = q[q0:q0 + n, h * G:(h + 1) * G]
@@ -69,8 +62,7 @@ def reference(c, q, cu, scale, round_k=False):
 
 def check(o, lse, ref, rows, weights=2.0 ** -11, what=""):
     """Tolerances, counted before any run: weights are rounded to fp16, half a step, 2^-11 of each (`weights`: 2^-8 where
-    they are bf16, and as much again where V is rounded too), so O by that share of the weights' mean of |v|, and
-    once to bf16, 2^-8 of itself.  Weights below 2^-14 of 2^4 times the one at the maximum in use are steps of 2^-24, off by 2^-29
+    they are bf16), so O by that share of the weights' mean of |v|, and once to bf16, 2^-8 of itself.  Weights below 2^-14 of 2^4 times the one at the maximum in use are steps of 2^-24, off by 2^-29
     of the largest: less than 2^-15 for all of 10^4 keys, of the largest |v|.  Exponents of magnitude x carry a few
     fp32 roundings (2^-24 each), exp2 two units in the last place, log2 likewise: 2^-20 (1 + x)."""
     ro, rl, size, top = (a[:rows] for a in ref)
@@ -90,7 +82,7 @@ def check(o, lse, ref, rows, weights=2.0 ** -11, what=""):
     assert (el[fine] <= tl[fine]).all(), f"{what}: LSE off by {np.max((el / tl)[fine])} of what is allowed"
 
 
-def run_chunk(c, q, cu, d_cu, scale=None, weights=2.0 ** -11, round_k=False, what="", **kw):
+def run_chunk(c, q, cu, d_cu, scale=None, weights=2.0 ** -11, what="", **kw):
     T, Hq, D = q.shape
     o = torch.full((T, Hq, D), 777.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((T, Hq), 777.0, device="cuda")
@@ -98,7 +90,7 @@ def run_chunk(c, q, cu, d_cu, scale=None, weights=2.0 ** -11, round_k=False, wha
     torch.cuda.synchronize()
     rows = int(cu[-1])
     assert bool((o[rows:] == 777).all()) and bool((lse[rows:] == 777).all()), "padding rows were written"
-    check(o, lse, reference(c, pu.f64(q), cu, scale or D ** -0.5, round_k), rows, weights, what)
+    check(o, lse, reference(c, pu.f64(q), cu, scale or D ** -0.5), rows, weights, what)
     return o, lse
 
 
@@ -204,7 +196,7 @@ def test_value_scales_near_one_another(D):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("spread", [8, 20, 45])
 def test_value_scales_far_apart(D, spread):
-    """Weights and values as bf16 (2^-8 each of the weights)."""
+    """Weights times value scales as bf16 (2^-8 of each)."""
     c = pu.Cache([900, 64, 333, 2000], 1, 32, D, seed=spread)
     c.vs *= 2.0 ** np.random.default_rng(spread).integers(-spread, spread, size=c.vs.shape)
     put_back(c)
@@ -229,13 +221,13 @@ def test_value_scales_at_the_ends(exponent):
 
 
 def test_scales_that_are_no_powers_of_two():
-    """K is rounded to bf16 (the reference rounds it too); V and the weights are rounded to bf16, 2^-8 each."""
+    """Scores take the rest of the key scale in fp32; weights times the value scale are rounded to bf16, 2^-8 of each."""
     c = pu.Cache([900, 64, 333], 2, 32, 128, seed=9)
     c.ks[::3] *= 1.37
     c.vs[1::3] *= 1.1
     put_back(c)
     q, cu, d_cu = pu.queries([140, 60, 7], 4, 128, seed=9)
-    run_chunk(c, q, cu, d_cu, weights=2.0 ** -7, round_k=True)
+    run_chunk(c, q, cu, d_cu, weights=2.0 ** -8)
 
 
 @pytest.mark.parametrize("D", [64, 128])
