@@ -1021,7 +1021,7 @@ extern "C" int fa_fwd_paged_chunk(const void *q, const int *cu_q, const int *seq
     p.num_pages = num_pages;
     p.page_log2 = page_log2_of(page_size);
     p.scale_log2 = scale_log2;
-    p.tries = 1u << 27;
+    p.limit_us = (uint32_t)(kWaitLimitNs / 1000);
     const cudaError_t e = fa::launch_fwd_paged_chunk(D, p, sm_count(), (cudaStream_t)stream);
     return e == cudaSuccess ? FA_OK : fail_cuda(e);
 }

@@ -96,8 +96,9 @@ struct ChunkParams {
     float *ws;
     int B, T, G, Hkv, max_pages, num_pages, page_log2;
     int max_len;                 // tokens that a table row holds (set by the launch)
+    int item_keys;               // keys that an item sees more than the one before it, about (set by the launch)
     float scale_log2;            // scale * log2(e)
-    uint32_t tries;              // bound of every on-chip wait
+    uint32_t limit_us;           // bound of every on-chip wait
 };
 size_t paged_chunk_workspace_bytes(int D, int num_sms);
 cudaError_t launch_fwd_paged_chunk(int D, ChunkParams p, int num_sms, cudaStream_t stream);

@@ -64,7 +64,7 @@ constexpr int kCkThreads = 640;
 constexpr int kCkCodeWarps = 8;
 constexpr int kCkRows = 256;        // rows of an item, two sub-tiles of 128
 constexpr int kCkTile = 128;        // keys a tile
-constexpr int kCkFixed = 256;       // keys that an item's fixed cost stands for
+constexpr int kCkFixed = 640;       // keys that an item's fixed cost stands for
 constexpr int kCkMinShare = 768;    // of a block, in keys
 constexpr int kCkSegs = 4;          // segments in the ring
 constexpr int kCkTiles = 8;         // tiles in theirs
@@ -163,9 +163,9 @@ __device__ __forceinline__ CkSeq ck_sequence(const ChunkParams &p, int b) {
 }
 
 // Where item i of a (sequence, head) begins in it, in keys: an item costs its fixed part, the
-// keys before the step's tokens and those up to its last row's token (256 (i + 1) / G).
+// keys before the step's tokens and those up to its last row's token (about 256 / G more for each item).
 __device__ __forceinline__ long long ck_begin(const ChunkParams &p, long long i, int c) {
-    return i * (kCkFixed + max(c, 0)) + 128 * i * (i + 1) / p.G;
+    return i * (kCkFixed + max(c, 0)) + p.item_keys * (i * (i + 1) >> 1);
 }
 __device__ __forceinline__ int ck_items(const ChunkParams &p, int nq) {
     return (int)(((long long)nq * p.G + kCkRows - 1) / kCkRows);
@@ -186,7 +186,7 @@ struct Cut {
 };
 
 // Moves a cut at the end of item i to the next item.
-__device__ __noinline__ void ck_next(const ChunkParams &p, Cut &u) {
+__device__ __forceinline__ void ck_next(const ChunkParams &p, Cut &u) {
     CkSeq s = ck_sequence(p, u.b);
     const int n = ck_items(p, s.nq), c = s.len - s.nq;
     u.begin += ck_begin(p, u.i + 1, c) - ck_begin(p, u.i, c);
@@ -209,7 +209,7 @@ __device__ __forceinline__ int ck_done(long long pos, long long begin, long long
     const long long in = pos - begin;
     if (in <= kCkFixed) return 0;
     // items of a small part of a share are not cut, nor those a little longer than one
-    const bool whole = w <= share / 4 || tiles <= 3 || (w > share && w <= share + share / 3);
+    const bool whole = w <= share / 4 || tiles <= 3 || (tiles <= 16 && w > share && w <= share + share / 3);
     if (whole) return 2 * in < w ? 0 : tiles;
     const int done = (int)((double)(in - kCkFixed) * tiles / (double)(w - kCkFixed) + 0.5);
     return done < 2 ? 0 : (done > tiles - 2 ? tiles : done);
@@ -332,17 +332,21 @@ __device__ __forceinline__ uint32_t ck_get(uint32_t addr) {
 }
 __device__ __forceinline__ void ck_put(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
 
-// A wait bounded by the number of its tries (a second or more: a try takes some tens of cycles at least), so
-// that the thirty of them are a few instructions each.  One that gives up raises the block's abort flag and the
-// status word, and makes the block's others give up.
-__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, uint32_t tries) {
+// A wait bounded in time.  The clock is read every 64 tries only, so that the thirty of them are a few instructions
+// each.  One that gives up raises the block's abort flag and the status word, and makes the block's others give up.
+__device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, uint32_t limit_us) {
+    uint32_t tries = 0, since = 0;
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
         if (ck_get(abort_flag) != 0u) return false;
-        if (tries-- == 0u) {
-            ck_put(abort_flag, 1u);
-            atomicExch(&g_status_chunk, (int)FA_ERR_TIMEOUT);
-            return false;
+        if ((++tries & 63u) == 0u) {
+            const uint32_t now = (uint32_t)(global_timer_ns() >> 10);  // about microseconds
+            if (tries == 64u) since = now;
+            if (now - since > limit_us) {
+                ck_put(abort_flag, 1u);
+                atomicExch(&g_status_chunk, (int)FA_ERR_TIMEOUT);
+                return false;
+            }
         }
     }
     return true;
@@ -527,9 +531,9 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ck_get(bars + kSlotTmem);
-    const uint32_t tries = p.tries;
+    const uint32_t limit_us = p.limit_us;
     auto wait = [&](uint32_t b, uint32_t parity) {
-        return ck_wait(bar(b), parity, abort_flag, tries);
+        return ck_wait(bar(b), parity, abort_flag, limit_us);
     };
     auto wait_all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
     // segment n of the block, once it is there
@@ -714,12 +718,13 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 // for is waited for while the softmax works.  (An item's first product overwrites O, which has been
                 // read out.)
                 ok = wait_all(C_K_FULL + stage, phase) && wait_all(C_Q_FULL + t, (uint32_t)items & 1u);
-                if (ok && items > 0) ok = wait_all(C_O_FREE + t, (uint32_t)(items - 1) & 1u);
                 if (!ok) break;
                 tc_fence_after();
                 ck_mma_s<D>(s_tm, dq, dk + ((stage * C::KV_BYTES) >> 4), C::IDESC_S);
                 tc_commit(bar(C_S_FULL + t));
                 tc_commit(bar(C_K_EMPTY + stage));
+                if (items > 0) ok = wait_all(C_O_FREE + t, (uint32_t)(items - 1) & 1u);
+                if (!ok) break;
                 uint32_t more = 0;
 #pragma unroll 1
                 for (; it < N; ++it, ++tile) {
@@ -869,57 +874,56 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
         const uint32_t o_tm = tmem + lane_off + C::TM_O + t * D;
         int ns = 0, od = 0, tile = 0;  // S tiles and items of this sub-tile, tiles of the block so far
         bool ok = true;
-        for (int n = 0; ok; ++n) {
-            ok = segment(n);
-            if (!ok) break;
-            const uint32_t g = seg_at(n);  // (released behind the epilogue, which reads it again)
-            if (CK_SEG(g, end)) {
-                release(n);
-                break;
-            }
-            const int N = CK_SEG(g, t1) - CK_SEG(g, t0), first = CK_SEG(g, first[0]) * (1 - t) + CK_SEG(g, first[1]) * t;
-            if (t == 1 && !CK_SEG(g, act1)) {
-                tile += N;
-                release(n);
-                continue;
-            }
-            const int limit = CK_SEG(g, c) + min(CK_SEG(g, row0) + t * 128 + row, CK_SEG(g, rows) - 1) / p.G + 1;  // keys that this row sees
-            const int edge = CK_SEG(g, c) + (CK_SEG(g, row0) + t * 128) / p.G + 1;                         // and the sub-tile's first row
-            const int key1 = CK_SEG(g, t1) * kCkTile;
-            tile += min(first, N);
-            // ---- the row's query, scaled to fp16, into shared memory (the segment before has read what was
-            // there: its last S is complete)
+        // The row's query of segment n, scaled to fp16, into shared memory, where the last S of the segment before (or of
+        // the one before that) has read the one that was there.  Returns the row's factor of the scores.
+        auto load_query = [&](int n) -> float {
             float c_row = p.scale_log2;
-            if (first < N) {
-                const int R = CK_SEG(g, row0) + t * 128 + row, tok = min(R, CK_SEG(g, rows) - 1) / p.G;
-                const uint4 *const src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (long long)(CK_SEG(g, q0) + tok) * p.q_stride +
-                                                                         (long long)(CK_SEG(g, h) * p.G + R - tok * p.G) * D);
-                uint4 w[D / 8];
-                uint32_t am = 0;
+            ok = segment(n);
+            if (!ok) return c_row;
+            const uint32_t g = seg_at(n);
+            const int first = t ? CK_SEG(g, first[1]) : CK_SEG(g, first[0]);
+            if (CK_SEG(g, end) || first >= CK_SEG(g, t1) - CK_SEG(g, t0)) return c_row;
+            const int R = CK_SEG(g, row0) + t * 128 + row, rows = CK_SEG(g, rows), tok = min(R, rows - 1) / p.G;
+            const uint4 *const src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + (long long)(CK_SEG(g, q0) + tok) * p.q_stride +
+                                                                     (long long)(CK_SEG(g, h) * p.G + R - tok * p.G) * D);
+            uint4 w[D / 8];
+            uint32_t am = 0;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (R < CK_SEG(g, rows)) w[i] = __ldg(src + i);
-                }
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    am = __vmaxu2(am, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
-                am = max(am & 0xffffu, am >> 16);
-                const int e = am ? max(-126, min(126, (int)(am >> 7) - 127)) : 0;
-                const float down = ck_two_to(-e);
-                c_row = p.scale_log2 * ck_two_to(e);
-                const uint32_t dst = sbase + t * C::QT_BYTES + row * 128;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t y[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = ck_pack_f16(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xffff0000u) * down);
-                    st_shared_v4(dst + (i >> 3) * C::CHUNK + (((i & 7) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(bar(C_Q_FULL + t));
+            for (int i = 0; i < D / 8; ++i) {
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (R < rows) w[i] = __ldg(src + i);
             }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                am = __vmaxu2(am, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu), __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+            am = max(am & 0xffffu, am >> 16);
+            const int e = am ? max(-126, min(126, (int)(am >> 7) - 127)) : 0;
+            const float down = ck_two_to(-e);
+            c_row *= ck_two_to(e);
+            const uint32_t dst = sbase + t * C::QT_BYTES + row * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = ck_pack_f16(__uint_as_float(u[j] << 16) * down, __uint_as_float(u[j] & 0xffff0000u) * down);
+                st_shared_v4(dst + (i >> 3) * C::CHUNK + (((i & 7) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar(C_Q_FULL + t));
+            return c_row;
+        };
+        float c_row = 0.f, c_next;
+        for (int n = -1; ok; ++n, c_row = c_next) {  // (a first pass takes the first segment's query only)
+            const uint32_t g = seg_at(max(n, 0));    // (released behind the epilogue, which reads it again)
+            const int N = n < 0 ? 0 : CK_SEG(g, t1) - CK_SEG(g, t0), first = n < 0 ? 0 : t ? CK_SEG(g, first[1]) : CK_SEG(g, first[0]);
+            // (What only the rarer paths need is read again there: registers are short in this loop.)
+            auto limit_of_row = [&]() {  // keys that this row sees
+                return CK_SEG(g, c) + min(CK_SEG(g, row0) + t * 128 + row, CK_SEG(g, rows) - 1) / p.G + 1;
+            };
+            // from which tile on every row of the sub-tile sees all keys: those up to its first row's limit
+            const int plain_from = CK_SEG(g, t1) - max(0, CK_SEG(g, c) + (CK_SEG(g, row0) + t * 128) / p.G + 1) / kCkTile;
+            tile += min(first, N);
             float m_used = -INFINITY, l_run = 0.f;
             bool ready = false;  // every row of the warp has a maximum
             for (int it = first; it < N; ++it, ++tile) {
@@ -932,8 +936,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 // (The loops of all roles have to stay in the instruction cache together, so that this
                 // one has nothing else in it.)
                 const float key_exp = __uint_as_float(ck_get(key_exp_at(tile)));  // negative: the tile goes the other way
-                const int col0 = key1 - (it + 1) * kCkTile;
-                const bool masked = col0 + kCkTile > edge, wide = key_exp < 0.f;
+                const bool masked = it < plain_from, wide = key_exp < 0.f;
                 const float c_tile = c_row * fabsf(key_exp);
                 int half = 0;
                 if (!(masked || wide) && ready) {
@@ -979,7 +982,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     tmem_ld_wait16(s[1]);
                     tmem_ld_wait16(s[2]);
                 }
-                const int lim = limit - col0;
+                const int lim = limit_of_row() - (CK_SEG(g, t1) - 1 - it) * kCkTile;
                 // ---- the others, or the second half of one: the maximum first, then P, 16 keys at a time
                 uint32_t x[16];
                 auto piece = [&](int c) {
@@ -1054,6 +1057,12 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 mbar_arrive(bar(C_P_FULL + t));
             }
             if (!ok) break;
+            c_next = load_query(n + 1);  // so that the next segment's first S runs beside what follows
+            if (!ok) break;
+            if (n < 0) {
+                if (CK_SEG(seg_at(0), end)) break;
+                continue;
+            }
             // ---- the rows' results, 32 columns at a time
             const bool some = first < N;  // the sub-tile has tiles here
             float unit = 1.f;
@@ -1083,7 +1092,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 uint32_t nan = 0;
                 if (nan_there) {
                     const int from = max(CK_SEG(g, t0), max(0, CK_SEG(g, c) + CK_SEG(g, row0) / p.G + 1) / kCkTile) * kCkTile;
-                    nan = ck_nan_columns<D>(p, CK_SEG(g, b), CK_SEG(g, h), from, min(min(limit, CK_SEG(g, len)), CK_SEG(g, t1) * kCkTile), c);
+                    nan = ck_nan_columns<D>(p, CK_SEG(g, b), CK_SEG(g, h), from, min(min(limit_of_row(), CK_SEG(g, len)), CK_SEG(g, t1) * kCkTile), c);
                 }
                 if (!there) continue;
 #pragma unroll
@@ -1120,6 +1129,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 }
             }
             release(n);
+            if (CK_SEG(seg_at(n + 1), end)) break;
         }
     }
 
@@ -1192,6 +1202,7 @@ static cudaError_t launch_chunk(const ChunkParams &p, int num_sms, cudaStream_t 
 
 cudaError_t launch_fwd_paged_chunk(int D, ChunkParams p, int num_sms, cudaStream_t stream) {
     p.max_len = p.max_pages << p.page_log2;
+    p.item_keys = (kCkRows + p.G - 1) / p.G;
     return D == 64 ? launch_chunk<64>(p, num_sms, stream) : launch_chunk<128>(p, num_sms, stream);
 }
 
