@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 BINDING_SOURCE = "fa_binding.cpp"
 BINDING_PATH = os.path.join(OUT_DIR, "fa_binding.so")
 
-SOURCES = ["fa_fwd_kernel.cu", "fa_splitkv.cu", "fa_bwd.cu", "fa_kv_cache.cu", "fa_page_select.cu",
+SOURCES = ["fa_fwd_kernel.cu", "fa_splitkv.cu", "fa_bwd.cu", "fa_kv_cache.cu", "fa_kv_append_rope.cu", "fa_page_select.cu",
            "fa_paged.cu", "fa_paged_chunk.cu", "fa_rope.cu", "fa_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -1031,11 +1031,12 @@ extern "C" int fa_device_status(void *stream) {
     cudaError_t e = fa::status_read_and_clear(&v, (cudaStream_t)stream);
     if (e == cudaSuccess) e = fa::splitkv_status_read_and_clear(&w);
     if (e == cudaSuccess) e = fa::bwd_status_read_and_clear(&x);
-    int cache[4] = {0, 0, 0, 0};  // the paged cache's kernels
+    int cache[5] = {0, 0, 0, 0, 0};  // the paged cache's kernels
     if (e == cudaSuccess) e = fa::kv_cache_status_read_and_clear(&cache[0]);
     if (e == cudaSuccess) e = fa::page_select_status_read_and_clear(&cache[1]);
     if (e == cudaSuccess) e = fa::paged_status_read_and_clear(&cache[2]);
     if (e == cudaSuccess) e = fa::paged_chunk_status_read_and_clear(&cache[3]);
+    if (e == cudaSuccess) e = fa::kv_append_rope_status_read_and_clear(&cache[4]);
     if (e != cudaSuccess) return fail_cuda(e);
     for (int c : cache)
         if (x == FA_OK) x = c;

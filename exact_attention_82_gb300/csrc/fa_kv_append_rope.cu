@@ -1,0 +1,508 @@
+// fa_kv_append_rope.cu -- fa_kv_append with the keys rotated on the way, and the step's
+// queries rotated beside, on GB300 (sm_103a).
+//
+// The page's scale comes from the rotated keys, so a run's rows are rotated, their largest
+// magnitude taken, and only then rounded; in between they are kept in fp32, so that a key is
+// rounded once.  Values go the way of fa_kv_append (fa_kv_cache.cu), whose kernel stays apart:
+// with the rotation's instantiations beside it in one function it lost a sixth to registers.
+//
+// Bound by HBM: 4 bytes read and 2 written for a key and a value element, 2 and 2 for a
+// query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 70 us, 5,270
+// GB/s (77% of the copy rate); the queries alone take 44.  Keys alone take 33: a team waits
+// for memory, for the largest magnitude of the page and to be written, head after head, and a quarter
+// of it is sines and cosines.  (A head's rows asked for while the one before is written: no gain.)
+// 64 single tokens 8.4 us.
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "../../include/fa.h"
+#include "fa_kv_append.cuh"
+#include "fa_paged.h"
+#include "fa_rope.cuh"
+
+namespace fa {
+
+static __device__ int g_status_kv_append_rope = 0;
+
+constexpr int kRopeThreadsAnSm = 1024;  // that the kernel's registers are held to (768: 89 us for the prompt, 1536: 96, when it took 78)
+constexpr int kAppendFill = 1024;       // threads an SM, of each kind, below which a block takes fewer heads
+
+template <int D, int PAGE, class C>
+struct AppendShared {
+    int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
+    uint32_t starts[kWindow / 32];
+    uint32_t amax[2][C::WARPS];
+    int sums[C::WARPS][D];
+};
+
+enum class Turn { none, halves, pairs };  // whether rows are rotated, and which elements make a pair
+
+// One block's share of the runs of a window, of heads h0 .. h1 - 1 of K (kv = 0) or V; `turns`: shared memory for the
+// angles of a team's run, which all its heads take.
+template <int D, int PAGE, class C, Turn TURN>
+__device__ __forceinline__ void append_runs(const AppendParams &p, const int share, const int kv, AppendShared<D, PAGE, C> &sm,
+                                            const int block, const int h0, const int h1, float4 *const turns = nullptr) {
+    int *const slot_of = sm.slot_of;
+    uint32_t *const starts = sm.starts;
+    auto &amax_sm = sm.amax;
+    auto &sums = sm.sums;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
+    int h = h0;
+    const int win = block / share, part = block % share;
+    const int t0 = win * kWindow;
+    const int limit = p.num_pages * PAGE;  // fewer than 2^31
+    const __nv_bfloat16 *const x_first = static_cast<const __nv_bfloat16 *>(kv ? p.x[1] : p.x[0]) + h0 * D;
+    const long long stride = kv ? p.stride[1] : p.stride[0];
+    float *const scale_of = kv ? p.scale[1] : p.scale[0];
+    uint8_t *const pages_of = kv ? p.pages[1] : p.pages[0];
+    auto team_sync = [&]() {
+        if (C::TEAM == 1)
+            __syncwarp();
+        else if (C::TEAMS == 1 || team == 0)  // by constant numbers: a block that may mean any of the 16
+            named_bar_sync(1, C::TEAM * 32);  // barriers has them all, and few fit an SM (24.2 -> 14.3 us)
+        else
+            named_bar_sync(2, C::TEAM * 32);
+    };
+
+    // ---- the runs that begin in the window
+    for (int i = tid; i < kWindow + PAGE; i += C::THREADS) slot_of[i] = t0 + i < p.T ? p.slots[t0 + i] : -1;
+    int before = -2;
+    if (tid == 0 && t0 > 0) before = p.slots[t0 - 1];
+    __syncthreads();
+    for (int i = warp * 32; i < kWindow; i += C::THREADS) {
+        const int s = slot_of[i + lane], prev = i + lane > 0 ? slot_of[i + lane - 1] : before;
+        const bool start = s >= 0 && s < limit && (prev != s - 1 || s % PAGE == 0);
+        if (s >= limit) atomicExch(&g_status_kv_append_rope, (int)FA_ERR_BAD_PAGE);
+        const uint32_t m = __ballot_sync(0xffffffffu, start);
+        if (lane == 0) starts[i / 32] = m;
+    }
+    __syncthreads();
+    // this lane's two tokens, and how many runs begin before each
+    const uint32_t s0 = starts[0], s1 = starts[1], lt = (1u << lane) - 1;
+    const int rank0 = (s0 >> lane) & 1u ? __popc(s0 & lt) : -1, rank1 = (s1 >> lane) & 1u ? __popc(s0) + __popc(s1 & lt) : -1;
+    const int runs = __popc(s0) + __popc(s1);
+    for (int run = part * C::TEAMS + team; run < runs; run += share * C::TEAMS) {
+        const uint32_t m0 = __ballot_sync(0xffffffffu, rank0 == run), m1 = __ballot_sync(0xffffffffu, rank1 == run);
+        const int i0 = m0 ? __ffs((int)m0) - 1 : 31 + __ffs((int)m1);
+        const int slot = slot_of[i0], off = slot % PAGE, pg = slot / PAGE;
+        int n = 0;  // tokens of the run
+#pragma unroll
+        for (int w = 0; w < (PAGE + 31) / 32; ++w) {
+            const int i = w * 32 + lane;
+            const uint32_t m = __ballot_sync(0xffffffffu, i < PAGE - off && slot_of[i0 + min(i, PAGE - 1)] == slot + i);
+            if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
+        }
+
+        // the largest of the team's magnitudes
+        auto join_max = [&](uint32_t am) {
+            am = __reduce_max_sync(0xffffffffu, am);
+            if (C::TEAM > 1) {
+                if (lane == 0) amax_sm[0][warp] = am;
+                team_sync();
+#pragma unroll
+                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
+            } else {
+                team_sync();
+            }
+            return am;
+        };
+        // the page's mean of its first `rows` rows, from the warps' sums
+        auto write_mean = [&](long long ph, float scale, int rows) {
+            team_sync();
+            constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
+            int total[PER], a = 0;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int d = tt + c * 32 * C::TEAM;
+                total[c] = 0;
+                if (d < D)
+#pragma unroll
+                    for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
+                a = max(a, abs(total[c]));
+            }
+            a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
+            if (C::TEAM > 1) {
+                if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
+                team_sync();
+#pragma unroll
+                for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
+            }
+            const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
+#pragma unroll
+            for (int c = 0; c < PER; ++c) {
+                const int d = tt + c * 32 * C::TEAM;
+                if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
+            }
+            if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * rows);
+        };
+
+        // A whole page, the usual run of a prompt, does without what the ends of others need
+        // (20.9 -> 18.1 us) and always has a power of two for its scale (17.6 us).
+        auto append = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            const __nv_bfloat16 *const x_of = x_first + (h - h0) * D;
+            // ---- everything that is read, at once: row r0 + i ROWS of the page in slot i
+            const int sub = tt % C::TPT, r0 = tt / C::TPT;
+            const long long ph = (long long)pg * p.Hkv + h;
+            const float was = W ? 0.f : scale_of[ph];
+            uint8_t *const codes = pages_of + ph * PAGE * D + sub * 8;
+            const __nv_bfloat16 *const x = x_of + (long long)(t0 + i0 - off) * stride + sub * 8;  // row 0's token
+            const bool mean = kv == 0 && p.mean != nullptr;
+            uint4 w[C::PASSES];
+#pragma unroll
+            for (int i = 0; i < C::PASSES; ++i) {
+                const int r = r0 + i * C::ROWS;
+                if (!W) w[i] = make_uint4(0, 0, 0, 0);
+                if (W || (r >= off && r < off + n)) {
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(x + r * stride));
+                } else if (mean && r < off) {
+                    const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                    w[i].x = c.x, w[i].y = c.y;
+                }
+            }
+            // magnitudes of bf16 compare as integers, two at a time
+            uint32_t am2 = 0;
+#pragma unroll
+            for (int i = 0; i < C::PASSES; ++i) {
+                uint32_t u = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                if (!W && r0 + i * C::ROWS < off) u = 0;
+                am2 = __vmaxu2(am2, u);
+            }
+            uint32_t am = max(am2 & 0xffffu, am2 >> 16);
+            const bool special = am >= 0x7f80u;
+            if (special) {  // infinities and NaN do not count
+                am = 0;
+#pragma unroll
+                for (int i = 0; i < C::PASSES; ++i) {
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
+                        if (W || r0 + i * C::ROWS >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                    }
+                }
+            }
+            am = join_max(am);
+            float scale = pow2_scale(__uint_as_float(am << 16));
+            if (!W && off > 0) scale = fmaxf(scale, was);
+            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
+            // x / scale is x * (1 / scale) exactly where the scale is a power of two (always,
+            // unless the caller put another one there; the remainder corrects it then)
+            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+            const float inv_scale = 1.f / scale, shrink = was / scale;
+            const uint16_t inv_bf16 = (uint16_t)(__float_as_uint(inv_scale) >> 16);  // exact, where it is used
+            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
+            // the codes' sums: multiples of 2^-9, at most 8 of them of at most 448 a thread, are exact in fp32
+            static_assert(C::PASSES <= 8, "");
+            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < C::PASSES; ++i) {
+                const int r = r0 + i * C::ROWS;
+                if (!W && (r < off || r >= off + n)) continue;
+                float y[8];
+                if (W || pow2) {
+                    scaled8(w[i], inv_bf16, y);
+                } else {
+                    bf16x8(w[i], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float x = y[j];
+                        y[j] = x * inv_scale;
+                        if (fabsf(x) < INFINITY) y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
+                    }
+                }
+                const uint2 c = encode8(y);
+                *reinterpret_cast<uint2 *>(codes + r * D) = c;
+                if (mean) {
+                    add8(special ? without_nan(c) : c, sum);
+                }
+            }
+            if (!W && off > 0 && (mean || grown)) {  // apart, so that prompts' whole pages skip it
+#pragma unroll
+                for (int i = 0; i < C::PASSES; ++i) {
+                    const int r = r0 + i * C::ROWS;
+                    if (r >= off) continue;
+                    uint2 c = make_uint2(w[i].x, w[i].y);
+                    float y[8];
+                    if (grown) {
+                        if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
+                        decode8(c, y);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) y[j] *= shrink;
+                        c = encode8(y);
+                        *reinterpret_cast<uint2 *>(codes + r * D) = c;
+                    }
+                    decode8(without_nan(c), y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += y[j];
+                }
+            }
+            if (mean) {  // integer sums: the same in any order
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    int x = (int)(sum[j] * 512.f);
+#pragma unroll
+                    for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
+                }
+                write_mean(ph, scale, W ? PAGE : off + n);
+            }
+        };
+        // Rotated rows: a thread has two pieces of each of its rows, whose elements are one
+        // another's partners, and keeps them in fp32 between the pass that takes the largest
+        // magnitude and the one that writes codes, so that they are rounded once.
+        auto append_turned = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            const __nv_bfloat16 *const x_of = x_first + (h - h0) * D;
+            constexpr int TPT = D / 16, ROWS = 32 * C::TEAM / TPT, PASSES = PAGE / ROWS;
+            static_assert(PASSES * 8 <= 32, "sums of codes are exact in fp32");
+            const int sub = tt % TPT, r0 = tt / TPT;
+            const long long ph = (long long)pg * p.Hkv + h;
+            const float was = W ? 0.f : scale_of[ph];
+            const int2 piece = rope_pieces(sub, p.rot, TURN == Turn::pairs);
+            uint8_t *const codes = pages_of + ph * PAGE * D;
+            const bool mean = p.mean != nullptr, turned = sub < p.rot / 16;
+            // ---- what is read, at once: the run's rows, and codes before it for the mean
+            uint4 w[PASSES][2];
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * ROWS;
+                w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+                if (W || (r >= off && r < off + n)) {
+                    const long long token = (long long)(t0 + i0 - off) + r;
+                    w[i][0] = __ldg(reinterpret_cast<const uint4 *>(x_of + token * stride + 8 * piece.x));
+                    w[i][1] = __ldg(reinterpret_cast<const uint4 *>(x_of + token * stride + 8 * piece.y));
+                } else if (mean && r < off) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(codes + r * D + 8 * piece.x);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(codes + r * D + 8 * piece.y);
+                    w[i][0] = make_uint4(a.x, a.y, b.x, b.y);
+                }
+            }
+            float y[PASSES][16];
+            uint32_t am = 0;  // magnitudes of fp32 compare as integers; infinities and NaN do not count
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * ROWS;
+                if (!W && (r < off || r >= off + n)) continue;
+                bf16x8_to_float(w[i][0], y[i]);
+                bf16x8_to_float(w[i][1], y[i] + 8);
+                if (turned) {
+                    float2 f[8];
+                    const float4 *const of = turns + (r - off) * (p.rot / 4) + sub;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 two = of[j * (p.rot / 16)];
+                        f[2 * j] = make_float2(two.x, two.y), f[2 * j + 1] = make_float2(two.z, two.w);
+                    }
+                    rope_turn16<TURN == Turn::pairs>(y[i], f);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t u = __float_as_uint(y[i][j]) & 0x7fffffffu;
+                    am = max(am, u < 0x7f800000u ? u : 0u);
+                }
+            }
+            float scale = pow2_scale(__uint_as_float(join_max(am)));
+            if (!W && off > 0) scale = fmaxf(scale, was);
+            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
+            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
+            const float inv_scale = 1.f / scale, shrink = was / scale;
+            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
+            float sum[2][8] = {};
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * ROWS;
+                if (!W && (r < off || r >= off + n)) continue;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = y[i][j];
+                    y[i][j] = x * inv_scale;  // exact for powers of two; the remainder corrects it otherwise
+                    if (!W && !pow2 && fabsf(x) < INFINITY) y[i][j] = fmaf(fmaf(-y[i][j], scale, x), inv_scale, y[i][j]);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float *const v = y[i] + 8 * c;
+                    const uint2 code = make_uint2(pack_e4m3x4(v[0], v[1], v[2], v[3]), pack_e4m3x4(v[4], v[5], v[6], v[7]));
+                    *reinterpret_cast<uint2 *>(codes + r * D + 8 * (c ? piece.y : piece.x)) = code;
+                    if (mean) add8(without_nan(code), sum[c]);
+                }
+            }
+            if (!W && off > 0 && (mean || grown)) {
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i) {
+                    const int r = r0 + i * ROWS;
+                    if (r >= off) continue;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint2 *const at = reinterpret_cast<uint2 *>(codes + r * D + 8 * (c ? piece.y : piece.x));
+                        uint2 code = mean ? (c ? make_uint2(w[i][0].z, w[i][0].w) : make_uint2(w[i][0].x, w[i][0].y)) : *at;
+                        float v[8];
+                        if (grown) {
+                            decode8(code, v);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] *= shrink;
+                            code = encode8(v);
+                            *at = code;
+                        }
+                        decode8(without_nan(code), v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[c][j] += v[j];
+                    }
+                }
+            }
+            if (mean) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        int x = (int)(sum[c][j] * 512.f);
+#pragma unroll
+                        for (int d = TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                        if (lane < TPT) sums[warp][8 * (c ? piece.y : piece.x) + j] = x;
+                    }
+                write_mean(ph, scale, W ? PAGE : off + n);
+            }
+        };
+        if constexpr (TURN != Turn::none) {
+            // The run's angles: pair 8 s + 2 j + e of row r is half e of word (r, j, s), so that the threads of a row read
+            // neighbouring words.
+            const int pairs = p.rot / 2;
+            for (int e = tt; e < n * pairs; e += 32 * C::TEAM) {
+                const int r = e / pairs, pair = e - r * pairs;
+                const float2 f = rope_factor(__ldg(p.phases + pair), __ldg(p.positions + t0 + i0 + r), p.amplitude);
+                reinterpret_cast<float2 *>(turns)[2 * (r * (p.rot / 4) + (pair >> 1 & 3) * (p.rot / 16) + (pair >> 3)) + (pair & 1)] = f;
+            }
+            team_sync();
+        }
+#pragma unroll 1
+        do {
+            if constexpr (TURN != Turn::none) {
+                if (n == PAGE)
+                    append_turned(std::true_type());
+                else
+                    append_turned(std::false_type());
+            } else {
+                if (n == PAGE)
+                    append(std::true_type());
+                else
+                    append(std::false_type());
+            }
+            team_sync();  // the next run overwrites the shared words
+        } while (++h < h1);
+        h = h0;
+    }
+}
+
+// Keys rotated on the way.  Of neighbouring blocks one takes keys, one values, one rotates the window's
+// queries of the same key/value heads' groups, so that a step has one launch for all three and keys, which
+// are bound by what they issue, run beside queries, which are bound by memory.  A sine and cosine
+// is some 50 instructions, and the same for all heads: a block takes `per` heads, and their angles once
+// (a prompt of 16384 tokens, 8 heads of keys, 32 of queries: 109 us with an angle for every head).
+template <int D, int PAGE, bool INTER>
+__global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS, kRopeThreadsAnSm / AppendCfg<D, PAGE, 32>::THREADS) fa_kv_append_rope_kernel(const __grid_constant__ AppendParams p, int share, int per) {
+    using C = AppendCfg<D, PAGE, 32>;
+    grid_wait();
+    extern __shared__ __align__(16) float4 turns_sm[];
+    __shared__ AppendShared<D, PAGE, C> sm;
+    const int kinds = p.q ? 3 : 2, kind = blockIdx.x % kinds, block = blockIdx.x / kinds;
+    const int h0 = blockIdx.y * per, h1 = min(h0 + per, p.Hkv);
+    if (kind == 0) {
+        append_runs<D, PAGE, C, INTER ? Turn::pairs : Turn::halves>(p, share, 0, sm, block, h0, h1,
+                                                                          turns_sm + threadIdx.x / (32 * C::TEAM) * PAGE * (p.rot / 4));
+    } else if (kind == 1) {
+        append_runs<D, PAGE, C, Turn::none>(p, share, 1, sm, block, h0, h1);
+    } else {
+        constexpr int TPT = D / 16, TOKENS = C::THREADS / TPT;
+        const int win = block / share, part = block % share, sub = threadIdx.x % TPT;
+        const bool turned = sub < p.rot / 16;
+        const int2 piece = rope_pieces(sub, p.rot, INTER);
+        for (int i = part * TOKENS + threadIdx.x / TPT; i < kWindow; i += share * TOKENS) {
+            const int t = win * kWindow + i;
+            if (t >= p.T) break;
+            float2 f[8];
+            if (turned) {
+                const int position = __ldg(p.positions + t);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = rope_factor(__ldg(p.phases + 8 * sub + j), position, p.amplitude);
+            }
+            const __nv_bfloat16 *const x = static_cast<const __nv_bfloat16 *>(p.q) + t * p.q_stride + (long long)h0 * p.G * D;
+            __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(p.q_out) + t * p.q_out_stride + (long long)h0 * p.G * D;
+            constexpr int AHEAD = 4;  // heads whose loads are in flight (a store may not pass a load that is written below it)
+#pragma unroll 1
+            for (int g = 0, n = (h1 - h0) * p.G; g < n; g += AHEAD) {
+                uint4 w[AHEAD][2];
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    if (g + k >= n) break;
+                    w[k][0] = *reinterpret_cast<const uint4 *>(x + (g + k) * D + 8 * piece.x);
+                    w[k][1] = *reinterpret_cast<const uint4 *>(x + (g + k) * D + 8 * piece.y);
+                }
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    if (g + k >= n) break;
+                    if (turned) {
+                        float v[16];
+                        bf16x8_to_float(w[k][0], v);
+                        bf16x8_to_float(w[k][1], v + 8);
+                        rope_turn16<INTER>(v, f);
+                        w[k][0] = float_to_bf16x8(v);
+                        w[k][1] = float_to_bf16x8(v + 8);
+                    }
+                    *reinterpret_cast<uint4 *>(y + (g + k) * D + 8 * piece.x) = w[k][0];
+                    *reinterpret_cast<uint4 *>(y + (g + k) * D + 8 * piece.y) = w[k][1];
+                }
+            }
+        }
+    }
+}
+
+template <int D, int PAGE>
+static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaStream_t stream) {
+    using C = AppendCfg<D, PAGE, 32>;
+    const int windows = (p.T + kWindow - 1) / kWindow;
+    constexpr int most = kWindow / C::TEAMS;
+    // Heads a block: all where the windows fill the chip, fewer where they do not; then blocks that share a window's runs.
+    int groups = (int)std::min<long long>((kAppendFill / C::THREADS * (long long)num_sms + windows - 1) / windows, p.Hkv);
+    const int per = (p.Hkv + groups - 1) / groups;
+    groups = (p.Hkv + per - 1) / per;
+    long long share = 32ll * num_sms / ((long long)windows * groups * 2);
+    share = share < 1 ? 1 : (share > most ? most : share);
+    const dim3 grid((unsigned)(windows * share * (p.q ? 3 : 2)), groups);
+    const size_t smem = (size_t)C::TEAMS * PAGE * p.rot * 4;
+    auto *const kernel = p.interleaved ? fa_kv_append_rope_kernel<D, PAGE, true> : fa_kv_append_rope_kernel<D, PAGE, false>;
+    if (smem + sizeof(AppendShared<D, PAGE, C>) > 48 * 1024) {  // beyond what a kernel may have without asking: always the most, as other threads' calls set it too
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TEAMS * PAGE * D * 4);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_early(kernel, grid, C::THREADS, smem, stream, 1, p, (int)share, per);
+}
+
+template <int D>
+static cudaError_t launch_append_rope_page(const AppendParams &p, int num_sms, cudaStream_t stream) {
+    switch (p.page_log2) {
+        case 4: return launch_append_rope<D, 16>(p, num_sms, stream);
+        case 5: return launch_append_rope<D, 32>(p, num_sms, stream);
+        case 6: return launch_append_rope<D, 64>(p, num_sms, stream);
+        default: return launch_append_rope<D, 128>(p, num_sms, stream);
+    }
+}
+
+cudaError_t launch_kv_append_rope(int D, const AppendParams &p, int num_sms, cudaStream_t stream) {
+    return D == 64 ? launch_append_rope_page<64>(p, num_sms, stream) : launch_append_rope_page<128>(p, num_sms, stream);
+}
+
+cudaError_t kv_append_rope_status_read_and_clear(int *out) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_status_kv_append_rope, sizeof(int));
+    if (e != cudaSuccess) return e;
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_status_kv_append_rope, &zero, sizeof(int));
+    *out = v;
+    return e;
+}
+
+}  // namespace fa

@@ -1,7 +1,6 @@
 // fa_kv_cache.cu -- what fills the paged 8-bit key/value cache on GB300
 // (sm_103a): fa_kv_plan (block tables and slot maps from request lengths) and
-// fa_kv_append (rounds a step's keys and values into pages), with the keys' rotation on
-// the way in fa_kv_append_rope.
+// fa_kv_append (rounds a step's keys and values into pages).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -12,8 +11,8 @@
 #include <type_traits>
 
 #include "../../include/fa.h"
+#include "fa_kv_append.cuh"
 #include "fa_paged.h"
-#include "fa_rope.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -84,6 +83,8 @@ __device__ __forceinline__ int count_le(const int *a, int n, int x) {
     return lo;
 }
 
+// POSITIONS: whether the tokens' positions are written too.
+template <bool POSITIONS>
 __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const __grid_constant__ PlanParams p) {
     grid_wait();
     extern __shared__ int sm_plan[];
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const __grid_c
         if (i < cu[p.B]) {
             const int b = count_le(cu + 1, p.B, i);
             const Request r = plan_request(p, b);
-            position = (int)((uint32_t)r.cached + (uint32_t)(i - cu[b]));
+            if (POSITIONS) position = (int)((uint32_t)r.cached + (uint32_t)(i - cu[b]));
             if (r.valid && (r.need == 0 || (long long)pc[b] + r.need <= free_count)) {
                 const int pos = r.cached + (i - cu[b]), ord = pos >> p.page_log2;
                 // (in range, unless the caller changes the lengths during the call)
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv_plan_kernel(const __grid_c
             }
         }
         p.slots[i] = slot;
-        if (p.positions) p.positions[i] = position;
+        if (POSITIONS) p.positions[i] = position;
     }
     for (int i = me; i < min(pc[p.B], free_count); i += step) {
         const int b = count_le(pc + 1, p.B, i);
@@ -160,13 +161,14 @@ cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream
     long long grid = ((most > p.T ? most : p.T) + kPlanThreads - 1) / kPlanThreads;
     if (grid > 4ll * num_sms) grid = 4ll * num_sms;
     const int smem = 2 * (p.B + 1) * (int)sizeof(int);
+    auto *const kernel = p.positions ? fa_kv_plan_kernel<true> : fa_kv_plan_kernel<false>;
     if (smem > 48 * 1024) {  // beyond what a kernel may have without asking
         // always the most: the limit is the function's, and another thread's call would lower one set to this call's size
-        const cudaError_t e = cudaFuncSetAttribute(fa_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    2 * (kMaxSequences + 1) * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
-    return launch_early(fa_kv_plan_kernel, dim3((unsigned)grid), kPlanThreads, smem, stream, 1, p);
+    return launch_early(kernel, dim3((unsigned)grid), kPlanThreads, smem, stream, 1, p);
 }
 
 // ------------------------------------------------------------------ append
@@ -186,114 +188,17 @@ cudaError_t launch_kv_plan(const PlanParams &p, int num_sms, cudaStream_t stream
 // counts: bf16 times the inverse scale and fp16 plus a sum are instructions of mixed
 // precision (22.4 -> 21.4 us with both), NaN among the codes is looked for only where the
 // row had one (20.9 us), and whole pages have a pass of their own.
-constexpr int kWindow = 64;  // tokens whose runs one set of blocks shares
-
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return __half22float2(*reinterpret_cast<__half2 *>(&h));
-}
-
-__device__ __forceinline__ void decode8(const uint2 w, float (&f)[8]) {
-    const float2 a = e4m3x2_to_float2(w.x & 0xffffu), b = e4m3x2_to_float2(w.x >> 16);
-    const float2 c = e4m3x2_to_float2(w.y & 0xffffu), d = e4m3x2_to_float2(w.y >> 16);
-    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
-}
-
-// f += the values of eight codes
-__device__ __forceinline__ void add8(const uint2 w, float (&f)[8]) {
-    const uint32_t u[2] = {w.x, w.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(u[i / 2] >> 16 * (i & 1))));
-        asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; add.rn.f32.f16 %0, lo, %0; add.rn.f32.f16 %1, hi, %1;}"
-            : "+f"(f[2 * i]), "+f"(f[2 * i + 1])
-            : "r"(h));
-    }
-}
-
-// NaN codes (0x7f and 0xff) as 0
-__device__ __forceinline__ uint32_t without_nan(uint32_t c) {
-    const uint32_t nan = ((c & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    return nan ? c & ~((nan >> 7) * 0xffu) : c;
-}
-__device__ __forceinline__ uint2 without_nan(uint2 c) { return make_uint2(without_nan(c.x), without_nan(c.y)); }
-
-__device__ __forceinline__ uint2 encode8(const float (&f)[8]) {
-    return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
-}
-
-__device__ __forceinline__ void bf16x8(const uint4 w, float (&f)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(u[i] << 16);
-        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-
-// eight bf16 numbers times another one, in fp32
-__device__ __forceinline__ void scaled8(const uint4 w, uint16_t by, float (&f)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; fma.rn.f32.bf16 %0, lo, %3, %4; fma.rn.f32.bf16 %1, hi, %3, %4;}"
-            : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
-            : "r"(u[i]), "h"(by), "f"(-0.f));
-    }
-}
-
-// The smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8), its
-// exponent held to [-100, 120]; 1 for amax = 0.  amax is finite.
-__device__ __forceinline__ float pow2_scale(float amax) {
-    if (!(amax > 0.f)) return 1.f;
-    const uint32_t u = __float_as_uint(amax);
-    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return __uint_as_float((uint32_t)(max(-100, min(120, e)) + 127) << 23);
-}
-
-// PER: elements a thread holds at most
-template <int D, int PAGE, int PER = 64>
-struct AppendCfg {
-    static constexpr int TEAM = PAGE * D < 32 * PER ? 1 : PAGE * D / (32 * PER);  // warps
-    static constexpr int WARPS = TEAM > 4 ? TEAM : 4;
-    static constexpr int THREADS = 32 * WARPS;
-    static constexpr int TEAMS = WARPS / TEAM;
-    static_assert(TEAM == 1 || TEAMS <= 2, "");
-    static constexpr int TPT = D / 8;                                 // threads a token
-    static constexpr int ROWS = 32 * TEAM / TPT;                      // tokens a pass
-    static constexpr int PASSES = PAGE / ROWS;
-    // Blocks an SM that the registers are held to.  A team waits for memory three times
-    // (slots, rows, and to be written), so more of them side by side is faster, until they
-    // spill much.  At 10 all forms have 48 registers and spill 140 to 244 bytes, but for D = 64 with
-    // pages of 16.  A 16384-token prompt with 8, 9, 10 and 12 blocks, pages of 16, 32, 64, 128:
-    //   D = 128  18.2 18.6 18.1 20.3,  18.4 18.7 17.7 20.3,  18.6 18.8 17.4 19.1,  20.3 20.6 20.5 21.5 us;
-    //   D = 64   12.3 12.0 12.1 11.7,  12.2 11.9 11.9 11.6,  11.8 11.6 11.6 11.2,  11.9 12.3 12.4 12.6;
-    // ragged prompts at 16 rows a page, D = 64, 14.5, 14.3, 13.7 and 14.1.
-    static constexpr int BLOCKS = 10 * 128 / THREADS;
-};
-
-template <int D, int PAGE, class C>
-struct AppendShared {
-    int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
-    uint32_t starts[kWindow / 32];
-    uint32_t amax[2][C::WARPS];
-    int sums[C::WARPS][D];
-};
-
-enum class Turn { none, halves, pairs };  // whether rows are rotated, and which elements make a pair
-
-// One block's share of the runs of a window, of one head of K (kv = 0) or V.
-template <int D, int PAGE, class C, Turn TURN>
-__device__ __forceinline__ void append_runs(const AppendParams &p, const int share, const int kv, AppendShared<D, PAGE, C> &sm) {
-    int *const slot_of = sm.slot_of;
-    uint32_t *const starts = sm.starts;
-    auto &amax_sm = sm.amax;
-    auto &sums = sm.sums;
+template <int D, int PAGE>
+__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE>::BLOCKS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
+    using C = AppendCfg<D, PAGE>;
+    grid_wait();
+    __shared__ int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
+    __shared__ uint32_t starts[kWindow / 32];
+    __shared__ uint32_t amax_sm[2][C::WARPS];
+    __shared__ int sums[C::WARPS][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
-    const int h = blockIdx.y;
+    const int h = blockIdx.y, kv = blockIdx.z;
     const int win = blockIdx.x / share, part = blockIdx.x % share;
     const int t0 = win * kWindow;
     const int limit = p.num_pages * PAGE;  // fewer than 2^31
@@ -338,49 +243,6 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
             const uint32_t m = __ballot_sync(0xffffffffu, i < PAGE - off && slot_of[i0 + min(i, PAGE - 1)] == slot + i);
             if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
         }
-
-        // the largest of the team's magnitudes
-        auto join_max = [&](uint32_t am) {
-            am = __reduce_max_sync(0xffffffffu, am);
-            if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[0][warp] = am;
-                team_sync();
-#pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
-            } else {
-                team_sync();
-            }
-            return am;
-        };
-        // the page's mean of its first `rows` rows, from the warps' sums
-        auto write_mean = [&](long long ph, float scale, int rows) {
-            team_sync();
-            constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
-            int total[PER], a = 0;
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int d = tt + c * 32 * C::TEAM;
-                total[c] = 0;
-                if (d < D)
-#pragma unroll
-                    for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
-                a = max(a, abs(total[c]));
-            }
-            a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
-            if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
-                team_sync();
-#pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
-            }
-            const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int d = tt + c * 32 * C::TEAM;
-                if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
-            }
-            if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * rows);
-        };
 
         // A whole page, the usual run of a prompt, does without what the ends of others need
         // (20.9 -> 18.1 us) and always has a power of two for its scale (17.6 us).
@@ -428,7 +290,15 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                     }
                 }
             }
-            am = join_max(am);
+            am = __reduce_max_sync(0xffffffffu, am);
+            if (C::TEAM > 1) {
+                if (lane == 0) amax_sm[0][warp] = am;
+                team_sync();
+#pragma unroll
+                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
+            } else {
+                team_sync();
+            }
             float scale = pow2_scale(__uint_as_float(am << 16));
             if (!W && off > 0) scale = fmaxf(scale, was);
             if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
@@ -491,191 +361,39 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                     for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
                     if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
                 }
-                write_mean(ph, scale, W ? PAGE : off + n);
+                team_sync();
+                constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
+                int total[PER], a = 0;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) {
+                    const int d = tt + c * 32 * C::TEAM;
+                    total[c] = 0;
+                    if (d < D)
+#pragma unroll
+                        for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
+                    a = max(a, abs(total[c]));
+                }
+                a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
+                if (C::TEAM > 1) {
+                    if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
+                    team_sync();
+#pragma unroll
+                    for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
+                }
+                const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) {
+                    const int d = tt + c * 32 * C::TEAM;
+                    if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
+                }
+                if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (W ? PAGE : off + n));
             }
         };
-        // Rotated rows: a thread has two pieces of each of its rows, whose elements are one
-        // another's partners, and keeps them in fp32 between the pass that takes the largest
-        // magnitude and the one that writes codes, so that they are rounded once.
-        auto append_turned = [&](auto whole) {
-            constexpr bool W = decltype(whole)::value;
-            constexpr int TPT = D / 16, ROWS = 32 * C::TEAM / TPT, PASSES = PAGE / ROWS;
-            static_assert(PASSES * 8 <= 32, "sums of codes are exact in fp32");
-            const int sub = tt % TPT, r0 = tt / TPT;
-            const long long ph = (long long)pg * p.Hkv + h;
-            const float was = W ? 0.f : scale_of[ph];
-            const int2 piece = rope_pieces(sub, p.rot, TURN == Turn::pairs);
-            uint8_t *const codes = pages_of + ph * PAGE * D;
-            const bool mean = p.mean != nullptr, turned = sub < p.rot / 16;
-            unsigned long long phase[8];
-            if (turned) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) phase[j] = __ldg(p.phases + 8 * sub + j);
-            }
-            // ---- what is read, at once: the run's rows, and codes before it for the mean
-            uint4 w[PASSES][2];
-            int position[PASSES];
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int r = r0 + i * ROWS;
-                position[i] = 0;
-                w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-                if (W || (r >= off && r < off + n)) {
-                    const long long token = (long long)(t0 + i0 - off) + r;
-                    w[i][0] = __ldg(reinterpret_cast<const uint4 *>(x_of + token * stride + 8 * piece.x));
-                    w[i][1] = __ldg(reinterpret_cast<const uint4 *>(x_of + token * stride + 8 * piece.y));
-                    position[i] = __ldg(p.positions + token);
-                } else if (mean && r < off) {
-                    const uint2 a = *reinterpret_cast<const uint2 *>(codes + r * D + 8 * piece.x);
-                    const uint2 b = *reinterpret_cast<const uint2 *>(codes + r * D + 8 * piece.y);
-                    w[i][0] = make_uint4(a.x, a.y, b.x, b.y);
-                }
-            }
-            float y[PASSES][16];
-            uint32_t am = 0;  // magnitudes of fp32 compare as integers; infinities and NaN do not count
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int r = r0 + i * ROWS;
-                if (!W && (r < off || r >= off + n)) continue;
-                bf16x8_to_float(w[i][0], y[i]);
-                bf16x8_to_float(w[i][1], y[i] + 8);
-                if (turned) {
-                    float2 f[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = rope_factor(phase[j], position[i], p.amplitude);
-                    rope_turn16<TURN == Turn::pairs>(y[i], f);
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t u = __float_as_uint(y[i][j]) & 0x7fffffffu;
-                    am = max(am, u < 0x7f800000u ? u : 0u);
-                }
-            }
-            float scale = pow2_scale(__uint_as_float(join_max(am)));
-            if (!W && off > 0) scale = fmaxf(scale, was);
-            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
-            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-            const float inv_scale = 1.f / scale, shrink = was / scale;
-            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
-            float sum[2][8] = {};
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int r = r0 + i * ROWS;
-                if (!W && (r < off || r >= off + n)) continue;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float x = y[i][j];
-                    y[i][j] = x * inv_scale;  // exact for powers of two; the remainder corrects it otherwise
-                    if (!W && !pow2 && fabsf(x) < INFINITY) y[i][j] = fmaf(fmaf(-y[i][j], scale, x), inv_scale, y[i][j]);
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float *const v = y[i] + 8 * c;
-                    const uint2 code = make_uint2(pack_e4m3x4(v[0], v[1], v[2], v[3]), pack_e4m3x4(v[4], v[5], v[6], v[7]));
-                    *reinterpret_cast<uint2 *>(codes + r * D + 8 * (c ? piece.y : piece.x)) = code;
-                    if (mean) add8(without_nan(code), sum[c]);
-                }
-            }
-            if (!W && off > 0 && (mean || grown)) {
-#pragma unroll
-                for (int i = 0; i < PASSES; ++i) {
-                    const int r = r0 + i * ROWS;
-                    if (r >= off) continue;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint2 *const at = reinterpret_cast<uint2 *>(codes + r * D + 8 * (c ? piece.y : piece.x));
-                        uint2 code = mean ? (c ? make_uint2(w[i][0].z, w[i][0].w) : make_uint2(w[i][0].x, w[i][0].y)) : *at;
-                        float v[8];
-                        if (grown) {
-                            decode8(code, v);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) v[j] *= shrink;
-                            code = encode8(v);
-                            *at = code;
-                        }
-                        decode8(without_nan(code), v);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) sum[c][j] += v[j];
-                    }
-                }
-            }
-            if (mean) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        int x = (int)(sum[c][j] * 512.f);
-#pragma unroll
-                        for (int d = TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                        if (lane < TPT) sums[warp][8 * (c ? piece.y : piece.x) + j] = x;
-                    }
-                write_mean(ph, scale, W ? PAGE : off + n);
-            }
-        };
-        if constexpr (TURN != Turn::none) {
-            if (n == PAGE)
-                append_turned(std::true_type());
-            else
-                append_turned(std::false_type());
-        } else {
-            if (n == PAGE)
-                append(std::true_type());
-            else
-                append(std::false_type());
-        }
+        if (n == PAGE)
+            append(std::true_type());
+        else
+            append(std::false_type());
         team_sync();  // the next run overwrites the shared words
-    }
-}
-
-template <int D, int PAGE>
-__global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE>::BLOCKS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
-    grid_wait();
-    __shared__ AppendShared<D, PAGE, AppendCfg<D, PAGE>> sm;
-    append_runs<D, PAGE, AppendCfg<D, PAGE>, Turn::none>(p, share, blockIdx.z, sm);
-}
-
-// Keys rotated on the way.  Blocks with z = 0 take keys, z = 1 values, z = 2 rotate the window's
-// queries of the key/value head's group, so that a step has one launch for all three.
-template <int D, int PAGE, bool INTER>
-__global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS) fa_kv_append_rope_kernel(const __grid_constant__ AppendParams p, int share) {
-    using C = AppendCfg<D, PAGE, 32>;
-    grid_wait();
-    __shared__ AppendShared<D, PAGE, C> sm;
-    if (blockIdx.z == 0) {
-        append_runs<D, PAGE, C, INTER ? Turn::pairs : Turn::halves>(p, share, 0, sm);
-    } else if (blockIdx.z == 1) {
-        append_runs<D, PAGE, C, Turn::none>(p, share, 1, sm);
-    } else {
-        constexpr int TPT = D / 16, TOKENS = C::THREADS / TPT;
-        const int win = blockIdx.x / share, part = blockIdx.x % share, sub = threadIdx.x % TPT;
-        const bool turned = sub < p.rot / 16;
-        const int2 piece = rope_pieces(sub, p.rot, INTER);
-        for (int i = part * TOKENS + threadIdx.x / TPT; i < kWindow; i += share * TOKENS) {
-            const int t = win * kWindow + i;
-            if (t >= p.T) break;
-            float2 f[8];
-            if (turned) {
-                const int position = __ldg(p.positions + t);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = rope_factor(__ldg(p.phases + 8 * sub + j), position, p.amplitude);
-            }
-            const __nv_bfloat16 *const x = static_cast<const __nv_bfloat16 *>(p.q) + t * p.q_stride + (long long)blockIdx.y * p.G * D;
-            __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(p.q_out) + t * p.q_out_stride + (long long)blockIdx.y * p.G * D;
-#pragma unroll 2
-            for (int g = 0; g < p.G; ++g) {
-                uint4 a = *reinterpret_cast<const uint4 *>(x + g * D + 8 * piece.x), b = *reinterpret_cast<const uint4 *>(x + g * D + 8 * piece.y);
-                if (turned) {
-                    float v[16];
-                    bf16x8_to_float(a, v);
-                    bf16x8_to_float(b, v + 8);
-                    rope_turn16<INTER>(v, f);
-                    a = float_to_bf16x8(v);
-                    b = float_to_bf16x8(v + 8);
-                }
-                *reinterpret_cast<uint4 *>(y + g * D + 8 * piece.x) = a;
-                *reinterpret_cast<uint4 *>(y + g * D + 8 * piece.y) = b;
-            }
-        }
     }
 }
 
@@ -692,29 +410,8 @@ static cudaError_t launch_append(const AppendParams &p, int num_sms, cudaStream_
     return launch_early(fa_kv_append_kernel<D, PAGE>, grid, AppendCfg<D, PAGE>::THREADS, 0, stream, 1, p, (int)share);
 }
 
-template <int D, int PAGE>
-static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaStream_t stream) {
-    using C = AppendCfg<D, PAGE, 32>;
-    const int windows = (p.T + kWindow - 1) / kWindow;
-    const long long per = (long long)windows * p.Hkv * 2;
-    constexpr int most = kWindow / C::TEAMS;
-    long long share = 32ll * num_sms / per;
-    share = share < 1 ? 1 : (share > most ? most : share);
-    const dim3 grid((unsigned)(windows * share), p.Hkv, p.q ? 3 : 2);
-    return p.interleaved ? launch_early(fa_kv_append_rope_kernel<D, PAGE, true>, grid, C::THREADS, 0, stream, 1, p, (int)share)
-                         : launch_early(fa_kv_append_rope_kernel<D, PAGE, false>, grid, C::THREADS, 0, stream, 1, p, (int)share);
-}
-
 template <int D>
 static cudaError_t launch_append_page(const AppendParams &p, int num_sms, cudaStream_t stream) {
-    if (p.rot) {
-        switch (p.page_log2) {
-            case 4: return launch_append_rope<D, 16>(p, num_sms, stream);
-            case 5: return launch_append_rope<D, 32>(p, num_sms, stream);
-            case 6: return launch_append_rope<D, 64>(p, num_sms, stream);
-            default: return launch_append_rope<D, 128>(p, num_sms, stream);
-        }
-    }
     switch (p.page_log2) {
         case 4: return launch_append<D, 16>(p, num_sms, stream);
         case 5: return launch_append<D, 32>(p, num_sms, stream);
@@ -724,6 +421,7 @@ static cudaError_t launch_append_page(const AppendParams &p, int num_sms, cudaSt
 }
 
 cudaError_t launch_kv_append(int D, const AppendParams &p, int num_sms, cudaStream_t stream) {
+    if (p.rot) return launch_kv_append_rope(D, p, num_sms, stream);
     return D == 64 ? launch_append_page<64>(p, num_sms, stream) : launch_append_page<128>(p, num_sms, stream);
 }
 

@@ -39,6 +39,7 @@ struct AppendParams {
     int G;
 };
 cudaError_t launch_kv_append(int D, const AppendParams &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_append_rope(int D, const AppendParams &p, int num_sms, cudaStream_t stream);
 
 struct SelectParams {
     const void *q;               // bf16 [T, Hq, D]
@@ -108,6 +109,7 @@ cudaError_t kv_cache_status_read_and_clear(int *out);
 cudaError_t page_select_status_read_and_clear(int *out);
 cudaError_t paged_status_read_and_clear(int *out);
 cudaError_t paged_chunk_status_read_and_clear(int *out);
+cudaError_t kv_append_rope_status_read_and_clear(int *out);
 
 // A launch whose blocks may be made ready while the kernel before it in the stream
 // ends: every kernel of the paged cache begins by waiting for the one before it to have

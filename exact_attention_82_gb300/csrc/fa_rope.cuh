@@ -4,9 +4,11 @@
 // A pair's frequency is a whole number of 2^-64 turns a position (its phase), so the
 // angle at a position is the low 64 bits of position * phase: whole turns drop out of an
 // integer product exactly, however far the position, where fp32 (and at 10^6 positions
-// even the frequency alone in fp32) would lose the angle's leading digits.  The upper
-// 32 bits, a signed number of 2^-31 half turns, then go to fp32: the angle is off by
-// at most 2^-25 half turns, 10^-7 radians.
+// even the frequency alone in fp32) would lose the angle's leading digits.  Of its upper
+// 32 bits the quarter turn that is nearest is taken off, in integers too; what remains, at most
+// an eighth of a turn, goes to fp32 (rounded by 2^-27 of a turn), and its sine and cosine are
+// Taylor sums: behind the terms that are kept (to r^9 and r^8, r in turns) the next are
+// (pi/4)^11 / 11! = 2e-9 and (pi/4)^10 / 10! = 2.5e-8.  The quarter turns swap the two and set their signs.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,10 +21,16 @@ namespace fa {
 
 // amplitude * cos and sin of the angle of `phase` at `position`
 __device__ __forceinline__ float2 rope_factor(unsigned long long phase, int position, float amplitude) {
-    const unsigned long long turns = phase * (unsigned long long)(long long)position;
-    float s, c;
-    sincospif((float)(int)(uint32_t)(turns >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c * amplitude, s * amplitude);
+    // bits 32-63 of phase * position (a negative position counts 2^32 too many, so phase's lower half comes off)
+    const uint32_t lo = (uint32_t)phase, hi = (uint32_t)(phase >> 32);
+    const uint32_t turns = __umulhi(lo, (uint32_t)position) + hi * (uint32_t)position - (position < 0 ? lo : 0u);
+    const uint32_t quarter = (turns + 0x20000000u) >> 30;
+    const float r = (float)(int)(turns - (quarter << 30)) * 0x1p-32f, u = r * r;
+    const float s = r * fmaf(u, fmaf(u, fmaf(u, fmaf(u, 42.05869394f, -76.70585975f), 81.60524928f), -41.34170224f), 6.283185307f);
+    const float c = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 60.24464137f, -85.45681721f), 64.93939402f), -19.7392088f), 1.f);
+    const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;  // cos and sin of r + quarter, but for their signs
+    const uint32_t flip_x = (quarter + 1u) << 30 & 0x80000000u, flip_y = quarter << 30 & 0x80000000u;
+    return make_float2(__uint_as_float(__float_as_uint(x) ^ flip_x) * amplitude, __uint_as_float(__float_as_uint(y) ^ flip_y) * amplitude);
 }
 
 // (a, b) rotated: a c - b s, a s + b c
