@@ -15,7 +15,8 @@ import threading
 from . import build as _build
 
 __all__ = ["fa_fwd", "fa_fwd_raw", "fa_fwd_window", "fa_fwd_window_raw", "fa_strerror", "fa_device_status",
-           "fa_selftest_bounded_wait", "fa_selftest_fwd_timeout", "fa_selftest_bwd_timeout", "fa_selftest_splitkv_timeout", "fa_version", "FAError", "lib", "library_path",
+           "fa_selftest_bounded_wait", "fa_selftest_fwd_timeout", "fa_selftest_bwd_timeout", "fa_selftest_splitkv_timeout",
+           "fa_selftest_paged_chunk_timeout", "fa_version", "FAError", "lib", "library_path",
            "FA_OK", "FA_ERR_NULLPTR", "FA_ERR_BAD_SHAPE", "FA_ERR_UNSUPPORTED_D",
            "FA_ERR_UNSUPPORTED_CAUSAL", "FA_ERR_MISALIGNED", "FA_ERR_BAD_SCALE", "FA_ERR_CUDA",
            "FA_ERR_TIMEOUT", "FA_ERR_ALIAS", "FA_ERR_BAD_WINDOW", "FA_ERR_WORKSPACE",
@@ -94,6 +95,8 @@ _SIGNATURES = {
                                                   _vp]),
     "fa_selftest_splitkv_timeout": (_i, [_vp] * 5 + [_i] * 5 + [ctypes.c_float, _i, _vp, ctypes.c_size_t,
                                                                ctypes.c_ulonglong, _vp]),
+    "fa_selftest_paged_chunk_timeout": (_i, [_vp] * 10 + [_i] * 5 + [ctypes.c_float, _ll] + [_i] * 3 +
+                                        [_vp, ctypes.c_size_t, ctypes.c_ulonglong, _vp]),
     "fa_version": (_i, []),
 }
 
@@ -748,3 +751,17 @@ def fa_selftest_splitkv_timeout(q, k, v, o, lse, workspace, scale, timeout_ns: i
                                              lse.data_ptr(), B, H, Sq, Sk, D, float(scale), int(num_splits),
                                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                              int(timeout_ns), _stream_ptr(stream))
+
+
+def fa_selftest_paged_chunk_timeout(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, o, lse, workspace, scale,
+                                    timeout_ns: int, stream=None) -> int:
+    """fa_fwd_paged_chunk with every on-chip wait bounded by `timeout_ns` (tests of the give-up path); returns
+    the launch status.  All arguments are tensors as for fa_fwd_paged_chunk, none of them optional."""
+    T, Hq, D = q.shape
+    num_pages, Hkv, page, _ = k_pages.shape
+    return lib().fa_selftest_paged_chunk_timeout(q.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                                                 k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                                 o.data_ptr(), lse.data_ptr(), seq_lens.shape[0], T, Hq, Hkv, D, float(scale),
+                                                 q.stride(0) if T > 1 else Hq * D, block_table.shape[1], num_pages, page,
+                                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                                 int(timeout_ns), _stream_ptr(stream))

@@ -976,11 +976,10 @@ extern "C" size_t fa_fwd_paged_chunk_workspace_bytes(int B, int T, int Hq, int H
     return fa::paged_chunk_workspace_bytes(D, sm_count());
 }
 
-extern "C" int fa_fwd_paged_chunk(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
-                                  const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
-                                  void *o, float *lse, int B, int T, int Hq, int Hkv, int D, float scale,
-                                  long long q_stride, int max_pages, int num_pages, int page_size, void *workspace,
-                                  size_t workspace_bytes, void *stream) {
+static int chunk_checked(const void *q, const int *cu_q, const int *seq_lens, const int *block_table, const void *k_pages,
+                         const void *v_pages, const float *k_scale, const float *v_scale, void *o, float *lse, int B, int T, int Hq,
+                         int Hkv, int D, float scale, long long q_stride, int max_pages, int num_pages, int page_size,
+                         void *workspace, size_t workspace_bytes, unsigned long long timeout_ns, void *stream) {
     if (!q || !cu_q || !seq_lens || !block_table || !k_pages || !v_pages || !k_scale || !v_scale || !o || !lse) return FA_ERR_NULLPTR;
     const void *ints[6] = {cu_q, seq_lens, block_table, k_scale, v_scale, lse};
     for (const void *ptr : ints)
@@ -1021,9 +1020,29 @@ extern "C" int fa_fwd_paged_chunk(const void *q, const int *cu_q, const int *seq
     p.num_pages = num_pages;
     p.page_log2 = page_log2_of(page_size);
     p.scale_log2 = scale_log2;
-    p.limit_us = (uint32_t)(kWaitLimitNs / 1000);
+    p.limit_us = (uint32_t)(timeout_ns / 1000);
     const cudaError_t e = fa::launch_fwd_paged_chunk(D, p, sm_count(), (cudaStream_t)stream);
     return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+extern "C" int fa_fwd_paged_chunk(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                                  const void *k_pages, const void *v_pages, const float *k_scale, const float *v_scale,
+                                  void *o, float *lse, int B, int T, int Hq, int Hkv, int D, float scale,
+                                  long long q_stride, int max_pages, int num_pages, int page_size, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    return chunk_checked(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, o, lse, B, T, Hq, Hkv, D, scale, q_stride,
+                         max_pages, num_pages, page_size, workspace, workspace_bytes, kWaitLimitNs, stream);
+}
+
+extern "C" int fa_selftest_paged_chunk_timeout(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                                               const void *k_pages, const void *v_pages, const float *k_scale,
+                                               const float *v_scale, void *o, float *lse, int B, int T, int Hq, int Hkv,
+                                               int D, float scale, long long q_stride, int max_pages, int num_pages,
+                                               int page_size, void *workspace, size_t workspace_bytes,
+                                               unsigned long long timeout_ns, void *stream) {
+    if (timeout_ns > kWaitLimitNs) return FA_ERR_BAD_SHAPE;
+    return chunk_checked(q, cu_q, seq_lens, block_table, k_pages, v_pages, k_scale, v_scale, o, lse, B, T, Hq, Hkv, D, scale, q_stride,
+                         max_pages, num_pages, page_size, workspace, workspace_bytes, timeout_ns, stream);
 }
 
 extern "C" int fa_device_status(void *stream) {

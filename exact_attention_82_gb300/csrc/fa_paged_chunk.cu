@@ -296,6 +296,13 @@ __device__ __forceinline__ void ck_f16(const uint4 w, uint32_t factor, uint32_t 
         y[i] = *reinterpret_cast<const uint32_t *>(&r);
     }
 }
+// 16 codes times 1: half of the conversion's instructions less
+__device__ __forceinline__ void ck_f16(const uint4 w, uint32_t (&y)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = ck_codes_f16x2(i & 1 ? u[i / 2] >> 16 : u[i / 2] & 0xffffu);
+}
+constexpr uint32_t kCkOnes = 0x3c003c00u;
 // 2^e in fp16 (0 below 2^-24), in both halves of a word; e <= 15
 __device__ __forceinline__ uint32_t ck_f16_two_to(int e) {
     const uint32_t h = e >= -14 ? (uint32_t)(e + 15) << 10 : (e >= -24 ? 1u << (e + 24) : 0u);
@@ -333,13 +340,13 @@ __device__ __forceinline__ uint32_t ck_get(uint32_t addr) {
 __device__ __forceinline__ void ck_put(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
 
 // A wait bounded in time.  The clock is read every 64 tries only, so that the thirty of them are a few instructions
-// each.  One that gives up raises the block's abort flag and the status word, and makes the block's others give up.
+// each; no limit at all ends with the first try.  One that gives up raises the block's abort flag and the status word, and makes the block's others give up.
 __device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, uint32_t limit_us) {
     uint32_t tries = 0, since = 0;
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
         if (ck_get(abort_flag) != 0u) return false;
-        if ((++tries & 63u) == 0u) {
+        if ((++tries & 63u) == 0u || limit_us == 0u) {
             const uint32_t now = (uint32_t)(global_timer_ns() >> 10);  // about microseconds
             if (tries == 64u) since = now;
             if (now - since > limit_us) {
@@ -524,8 +531,12 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 if (pos < base + w) break;
                 base += w;
             }
-            cut_sm[e] = ck_cut(p, b, base, pos, share);
+            cut_sm[e].b = b;
+            cut_sm[e].begin = base;
         }
+        __syncthreads();
+        if (lane == 0 && warp < 2 && cut_sm[warp].begin != LLONG_MAX)
+            cut_sm[warp] = ck_cut(p, cut_sm[warp].b, cut_sm[warp].begin, ((long long)blockIdx.x + warp) * share, share);
     }
     tc_fence_before();
     __syncthreads();
@@ -556,6 +567,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 if (n >= kCkSegs) ok = wait_all(C_SEG_FREE + place, (uint32_t)(n / kCkSegs - 1) & 1u);
                 if (!ok) break;
                 const bool more = at.begin < end.begin || (at.begin == end.begin && at.begin != LLONG_MAX && at.done < end.done);
+                const long long begin = at.begin;
                 Seg g{};
                 g.end = !more;
                 if (more) {
@@ -577,27 +589,6 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     g.first[0] = g.t1 - min(g.t1, see0);
                     g.first[1] = g.act1 ? 0 : g.t1 - g.t0;
                     g.slot = at.done > 0 ? 0 : (done1 < tiles ? 1 : -1);
-                    if (g.slot == 1) {  // how many blocks have a part of it
-                        const long long w = ck_begin(p, at.i + 1, g.c) - ck_begin(p, at.i, g.c);
-                        int parts = 0;
-                        for (int j0 = 1; parts == 0; j0 += 32) {
-                            const int j = j0 + lane;  // the j-th block behind has its last part, if its end is not in it
-                            const long long pos = ((long long)blockIdx.x + j + 1) * share;
-                            const bool last_one = pos >= at.begin + w || (int)blockIdx.x + j + 1 >= (int)gridDim.x ||
-                                                  ck_done(pos, at.begin, w, tiles, share) >= tiles;
-                            const uint32_t some = __ballot_sync(0xffffffffu, last_one);
-                            if (some) parts = j0 + __ffs((int)some);
-                        }
-                        if (lane == 0) {
-                            CkTail tail{};
-                            tail.parts = parts;
-                            tail.q0 = g.q0;
-                            tail.rows = g.rows;
-                            tail.row0 = g.row0;
-                            tail.h = g.h;
-                            *ck_tail(p.ws, blockIdx.x) = tail;
-                        }
-                    }
                     if (at.begin == end.begin)
                         at = end;
                     else
@@ -608,13 +599,38 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     mbar_arrive(bar(C_SEG_FULL + place));
                 }
                 __syncwarp();
+                if (more && g.slot == 1) {  // how many blocks have a part of it
+                    const int i = g.row0 / kCkRows, tiles = ck_tiles(p, g.c, min(g.rows, g.row0 + kCkRows) - 1);
+                    const long long w = ck_begin(p, i + 1, g.c) - ck_begin(p, i, g.c);
+                    int parts = 0;
+                    for (int j0 = 1; parts == 0; j0 += 32) {
+                        const int j = j0 + lane;  // the j-th block behind has its last part, if its end is not in it
+                        const long long pos = ((long long)blockIdx.x + j + 1) * share;
+                        const bool last_one = pos >= begin + w || (int)blockIdx.x + j + 1 >= (int)gridDim.x ||
+                                              ck_done(pos, begin, w, tiles, share) >= tiles;
+                        const uint32_t some = __ballot_sync(0xffffffffu, last_one);
+                        if (some) parts = j0 + __ffs((int)some);
+                    }
+                    if (lane == 0) {
+                        CkTail tail{};
+                        tail.parts = parts;
+                        tail.q0 = g.q0;
+                        tail.rows = g.rows;
+                        tail.row0 = g.row0;
+                        tail.h = g.h;
+                        *ck_tail(p.ws, blockIdx.x) = tail;
+                    }
+                }
                 if (!more) break;
             }
         } else if (warp == 18) {
             // ================================================= tiles
             // Four tiles of a segment at a time, lane 8 j + i for piece i of the j-th.
             const int j = lane >> 3, i = lane & 7;
-            auto exponent = [](float x) { return max((int)(__float_as_uint(x) >> 23 & 0xffu) - 127, -126); };
+            auto exponent = [](float x) {  // (one that is not finite must not be what its tile's others are measured by)
+                const int e = (int)(__float_as_uint(x) >> 23 & 0xffu) - 127;
+                return e == 128 ? -126 : max(e, -126);
+            };
             auto top_of_tile = [](int x) {
 #pragma unroll
                 for (int d = 1; d < 8; d <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -824,7 +840,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
 #pragma unroll
             for (int i = 0; i < C::LOADS; ++i) {
                 uint32_t y[8];
-                ck_f16(kr[i], kf, y);
+                if (kf == kCkOnes)  // (the tile's largest scale, as mostly: 744 us instead of 754 for 1,024 tokens behind 65,536 keys)
+                    ck_f16(kr[i], y);
+                else
+                    ck_f16(kr[i], kf, y);
                 store(sbase + C::OFF_K + st * C::KV_BYTES, i, y);
             }
             hand_over(C_K_FULL + st);
@@ -1042,7 +1061,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     if (wide) {
                         const float f = __uint_as_float(ck_get(rest_at(tile) + 32 + c * 4));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * f, __uint_as_float(x[2 * e + 1]) * f);
+                        for (int e = 0; e < 16; ++e)  // (keys that the row does not see: 0, whatever their scale)
+                            x[e] = c * 16 + e >= lim ? 0u : __float_as_uint(__uint_as_float(x[e]) * f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = ck_pack_f16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
@@ -1145,40 +1167,44 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
 // ---------------------------------------------------------------- the join
 // O = sum_s w_s o_s / sum_s w_s with w_s = l_s 2^(m_s - max m), LSE = ln2 (max m - 4 + log2 sum_s w_s), the
 // parts in order: a warp a row, D / 32 columns a lane.
-constexpr int kCkJoinRows = 8;
+constexpr int kCkJoinWarps = 8, kCkJoinBlocks = 16;  // blocks an item, of 8 warps: two rows each (with 8 blocks the chunk of 512 tokens took 7 us more)
 template <int D>
-__global__ void __launch_bounds__(32 * kCkJoinRows) fa_fwd_paged_chunk_join(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(32 * kCkJoinWarps) fa_fwd_paged_chunk_join(const __grid_constant__ ChunkParams p) {
     grid_wait();
     const CkTail tail = *ck_tail(p.ws, blockIdx.x);
-    const int r = blockIdx.y * kCkJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31, row = tail.row0 + r;
-    if (tail.parts == 0 || row >= tail.rows) return;
+    const int lane = threadIdx.x & 31;
+    if (tail.parts == 0) return;
     auto part = [&](int j) { return ck_slot(p.ws, gridDim.x, (int)blockIdx.x + j, j == 0 ? 1 : 0, D); };
-    float top = -INFINITY;
-    for (int j = lane; j < tail.parts; j += 32) {
-        const float *const s = part(j);
-        if (s[(size_t)kCkRows * (D + 1) + r] != 0.f) top = fmaxf(top, s[(size_t)kCkRows * D + r]);
-    }
+#pragma unroll 1
+    for (int r = blockIdx.y * kCkJoinWarps + (threadIdx.x >> 5), row = tail.row0 + r; r < kCkRows && row < tail.rows;
+         r += kCkJoinWarps * kCkJoinBlocks, row += kCkJoinWarps * kCkJoinBlocks) {
+        float top = -INFINITY;
+        for (int j = lane; j < tail.parts; j += 32) {
+            const float *const s = part(j);
+            if (s[(size_t)kCkRows * (D + 1) + r] != 0.f) top = fmaxf(top, s[(size_t)kCkRows * D + r]);
+        }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    constexpr int PER = D / 32;
-    float acc[PER] = {}, sum = 0.f;
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        constexpr int PER = D / 32;
+        float acc[PER] = {}, sum = 0.f;
 #pragma unroll 2
-    for (int j = 0; j < tail.parts; ++j) {
-        const float *const s = part(j);
-        const float l = s[(size_t)kCkRows * (D + 1) + r], m = s[(size_t)kCkRows * D + r];
-        if (l == 0.f) continue;
-        const float w = l * exp2f(m == top ? 0.f : m - top);
-        sum += w;
+        for (int j = 0; j < tail.parts; ++j) {
+            const float *const s = part(j);
+            const float l = s[(size_t)kCkRows * (D + 1) + r], m = s[(size_t)kCkRows * D + r];
+            if (l == 0.f) continue;
+            const float w = l * exp2f(m == top ? 0.f : m - top);
+            sum += w;
 #pragma unroll
-        for (int c = 0; c < PER; ++c) acc[c] = fmaf(w, s[(size_t)r * D + lane * PER + c], acc[c]);
+            for (int c = 0; c < PER; ++c) acc[c] = fmaf(w, s[(size_t)r * D + lane * PER + c], acc[c]);
+        }
+        const int tok = row / p.G;
+        const long long at = (long long)(tail.q0 + tok) * (p.Hkv * p.G) + tail.h * p.G + (row - tok * p.G);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint32_t *const dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + at * D) + lane * (PER / 2);
+#pragma unroll
+        for (int c = 0; c < PER / 2; ++c) dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+        if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : ((top - kCkShift) + log2f(sum)) * 0.69314718055994531f;
     }
-    const int tok = row / p.G;
-    const long long at = (long long)(tail.q0 + tok) * (p.Hkv * p.G) + tail.h * p.G + (row - tok * p.G);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t *const dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + at * D) + lane * (PER / 2);
-#pragma unroll
-    for (int c = 0; c < PER / 2; ++c) dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-    if (lane == 0) p.lse[at] = sum == 0.f ? -INFINITY : ((top - kCkShift) + log2f(sum)) * 0.69314718055994531f;
 }
 
 size_t paged_chunk_workspace_bytes(int D, int num_sms) {
@@ -1197,7 +1223,7 @@ static cudaError_t launch_chunk(const ChunkParams &p, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     e = launch_early(fa_fwd_paged_chunk_kernel<D>, dim3((unsigned)num_sms), kCkThreads, CkCfg<D>::SMEM, stream, 1, p);
     if (e != cudaSuccess) return e;
-    return launch_early(fa_fwd_paged_chunk_join<D>, dim3((unsigned)num_sms, kCkRows / kCkJoinRows), 32 * kCkJoinRows, 0, stream, 1, p);
+    return launch_early(fa_fwd_paged_chunk_join<D>, dim3((unsigned)num_sms, kCkJoinBlocks), 32 * kCkJoinWarps, 0, stream, 1, p);
 }
 
 cudaError_t launch_fwd_paged_chunk(int D, ChunkParams p, int num_sms, cudaStream_t stream) {

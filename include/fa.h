@@ -550,7 +550,8 @@ size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  * or 2^-29 of the largest among those that the row sees first, from its end), but weights times
  * v_scale are rounded to bf16 (2^-8 of each) for 128 keys among which a scale is no power of two
  * (fa_kv_append's are), or a v_scale is not within 2^-15 to 2^7 of the largest that the pass began
- * with.  O is rounded once to bf16.
+ * with.  O is rounded once to bf16.  A scale that is not finite makes the rows that see its keys NaN or
+ * infinite, and no others.
  * T * Hq < 2^31.  Deterministic; no atomics on results.
  *   workspace   at least fa_fwd_paged_chunk_workspace_bytes(...) bytes, as for fa_fwd_paged
  * Errors: those of fa_fwd_paged.  An on-chip wait that gives up sets FA_ERR_TIMEOUT in the status word
@@ -645,6 +646,21 @@ int fa_selftest_bwd_timeout(const void *q, const void *k, const void *v, const v
 int fa_selftest_splitkv_timeout(const void *q, const void *k, const void *v, void *o, float *lse, int B,
                                 int H, int Sq, int Sk, int D, float scale, int num_splits, void *workspace,
                                 size_t workspace_bytes, unsigned long long timeout_ns, void *stream);
+
+/*
+ * fa_selftest_paged_chunk_timeout -- fa_fwd_paged_chunk with every on-chip wait bounded by `timeout_ns`
+ * (0 .. 2e9, counted in microseconds) instead of 2 s.  With a limit shorter than the first tile's way
+ * through the kernel its own give-up path runs, as for fa_selftest_fwd_timeout: the block's abort flag is
+ * raised and FA_ERR_TIMEOUT recorded in the status word, the other roles stop at their next wait, MMAs in
+ * flight are waited for (bounded), TMEM is freed and the block returns.  O and LSE are then undefined.
+ * Arguments, checks and errors are fa_fwd_paged_chunk's, plus FA_ERR_BAD_SHAPE for timeout_ns above 2e9.
+ */
+int fa_selftest_paged_chunk_timeout(const void *q, const int *cu_q, const int *seq_lens, const int *block_table,
+                                    const void *k_pages, const void *v_pages, const float *k_scale,
+                                    const float *v_scale, void *o, float *lse, int B, int T, int Hq, int Hkv, int D,
+                                    float scale, long long q_stride, int max_pages, int num_pages, int page_size,
+                                    void *workspace, size_t workspace_bytes, unsigned long long timeout_ns,
+                                    void *stream);
 
 /* fa_version -- library version, major*10000 + minor*100 + patch. */
 int fa_version(void);

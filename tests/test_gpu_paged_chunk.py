@@ -249,6 +249,28 @@ def test_masked_nan_never_touches_a_row(D, G):
     run_chunk(c, q, cu, d_cu)
 
 
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("scale", [math.nan, math.inf])
+def test_scales_that_are_not_finite(what, scale):
+    """Only the rows that see a key of such a page are other than finite; the page is in a tile that the mask cuts."""
+    c = pu.Cache([300, 200], 2, 16, 128, seed=14)
+    page = c.table[0, 15]  # keys 240 .. 255
+    (c.ks if what == "k" else c.vs)[page, 1] = scale
+    put_back(c)
+    q, cu, d_cu = pu.queries([120, 100], 8, 128, seed=14)
+    o, lse = fa.fa_fwd_paged_chunk(q, d_cu, c.d_lens, c.d_table, *c.pages)
+    (c.ks if what == "k" else c.vs)[page, 1] = math.nan  # (where an infinity ends up as NaN, where not, is not looked at)
+    with np.errstate(invalid="ignore"):
+        ro, rl, size, top = reference(c, pu.f64(q), cu, 128 ** -0.5)
+    keep = np.ones((220, 8), bool)
+    keep[60:120, 4:] = False
+    assert np.array_equal(np.isnan(ro).all(2), ~keep) and not bool(torch.isfinite(o[60:120, 4:]).any())
+    got = np.where(keep[..., None], pu.f64(o), 0), np.where(keep, pu.f64(lse), 0)
+    want = np.where(keep[..., None], ro, 0), np.where(keep, rl, 0), np.where(keep[..., None], size, 0), np.where(keep, top, 0)
+    # weights are bf16 in the tile with the page
+    check(*(torch.from_numpy(a) for a in got), want, 220, 2.0 ** -8)
+
+
 def test_nan_values_in_items_that_are_cut():
     c = pu.Cache([20000], 1, 64, 128, seed=3)
     for t, d in ((19990, 7), (19800, 64), (12345, 100)):
@@ -383,6 +405,49 @@ def test_agrees_with_the_kernel_for_few_tokens():
     _, _, size, _ = reference(c, pu.f64(q), cu, 128 ** -0.5)
     assert (np.abs(pu.f64(a) - pu.f64(b)) <= 2.0 ** -7 * np.abs(pu.f64(a)) + 2.0 ** -9 * size).all()
     assert float((la - lb).abs().max()) < 1e-4
+
+
+def test_most_sequences():
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 9, size=8192).tolist()
+    c = pu.Cache(lens, 1, 16, 64, seed=2)
+    q, cu, d_cu = pu.queries([min(L, 1) for L in lens], 1, 64, seed=2)
+    run_chunk(c, q, cu, d_cu)
+
+
+def test_more_heads_in_a_group_than_an_item_has_rows():
+    c = pu.Cache([700, 130], 1, 32, 64, seed=2)
+    q, cu, d_cu = pu.queries([3, 2], 300, 64, seed=2)
+    run_chunk(c, q, cu, d_cu)
+
+
+def test_caches_past_32_bits():
+    """Pages behind 4 GB of codes."""
+    c = pu.Cache([500, 300], 1, 128, 128, seed=12)
+    much = 2 ** 32 // (128 * 128) + 50
+    first = much - c.num_pages
+    big = [torch.zeros((much, 1, 128, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones((much, 1), device="cuda") for _ in range(2)]
+    for b, s in zip(big + scales, c.pages):
+        b[first:] = s
+    q, cu, d_cu = pu.queries([100, 50], 4, 128, seed=12)
+    want = run_chunk(c, q, cu, d_cu)
+    got = fa.fa_fwd_paged_chunk(q, d_cu, c.d_lens, torch.where(c.d_table >= 0, c.d_table + first, c.d_table), *big, *scales)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_waits_that_give_up():
+    """The kernel winds down where its waits run out at once, says so, and the next call is as good as any."""
+    c = pu.Cache([3000, 900], 2, 32, 128, seed=8)
+    q, cu, d_cu = pu.queries([100, 70], 8, 128, seed=8)
+    o, lse = run_chunk(c, q, cu, d_cu)
+    ws = torch.empty(fa.fa_fwd_paged_chunk_workspace_bytes(2, 170, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    args = (q, d_cu, c.d_lens, c.d_table, *c.pages, torch.empty_like(o), torch.empty_like(lse), ws, 128 ** -0.5)
+    assert fa.fa_selftest_paged_chunk_timeout(*args, 0) == fa.FA_OK
+    assert fa.fa_device_status() == fa.FA_ERR_TIMEOUT
+    assert fa.fa_selftest_paged_chunk_timeout(*args, 2_000_000_001) == fa.FA_ERR_BAD_SHAPE
+    o2, lse2 = run_chunk(c, q, cu, d_cu)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 # ------------------------------------------------------------- the step
