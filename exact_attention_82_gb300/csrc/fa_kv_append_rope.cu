@@ -7,11 +7,11 @@
 // with the rotation's instantiations beside it in one function it lost a sixth to registers.
 //
 // Bound by HBM: 4 bytes read and 2 written for a key and a value element, 2 and 2 for a
-// query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 70 us, 5,270
-// GB/s (77% of the copy rate); the queries alone take 44.  Keys alone take 33: a team waits
+// query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 64.3 us, 5,740
+// GB/s (84% of the copy rate); the queries alone take 44.  Keys alone take 33: a team waits
 // for memory, for the largest magnitude of the page and to be written, head after head, and a quarter
 // of it is sines and cosines.  (A head's rows asked for while the one before is written: no gain.)
-// 64 single tokens 8.4 us.
+// 64 single tokens 7.5 us.
 #include <math.h>
 
 #include <algorithm>
@@ -397,9 +397,9 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
     }
 }
 
-// Keys rotated on the way.  Of neighbouring blocks one takes keys, one values, one rotates the window's
-// queries of the same key/value heads' groups, so that a step has one launch for all three and keys, which
-// are bound by what they issue, run beside queries, which are bound by memory.  A sine and cosine
+// Keys rotated on the way.  Blocks of a third kind rotate queries, of the key/value heads' groups, so that a step has
+// one launch for keys, values and queries.  The keys' blocks, which wait for most, are the first to begin (neighbouring
+// blocks of different kinds instead: three prompts of 5000 tokens 64 for 60 us, 16384 tokens in pages of 128 73 for 70).  A sine and cosine
 // is some 50 instructions, and the same for all heads: a block takes `per` heads, and their angles once
 // (a prompt of 16384 tokens, 8 heads of keys, 32 of queries: 109 us with an angle for every head).
 template <int D, int PAGE, bool INTER>
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS, kRopeThreadsA
     grid_wait();
     extern __shared__ __align__(16) float4 turns_sm[];
     __shared__ AppendShared<D, PAGE, C> sm;
-    const int kinds = p.q ? 3 : 2, kind = blockIdx.x % kinds, block = blockIdx.x / kinds;
+    const int kinds = p.q ? 3 : 2, each = gridDim.x / kinds, kind = blockIdx.x / each, block = blockIdx.x % each;
     const int h0 = blockIdx.y * per, h1 = min(h0 + per, p.Hkv);
     if (kind == 0) {
         append_runs<D, PAGE, C, INTER ? Turn::pairs : Turn::halves>(p, share, 0, sm, block, h0, h1,
@@ -471,6 +471,10 @@ static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaSt
     groups = (p.Hkv + per - 1) / per;
     long long share = 32ll * num_sms / ((long long)windows * groups * 2);
     share = share < 1 ? 1 : (share > most ? most : share);
+    // With a window for each SM the tokens are prompts', whose windows have no more runs than this; further blocks would
+    // look for runs and find none (16384 tokens, 8 and 32 heads, D = 128, pages of 64: 70.6 -> 64.9 us; pages of 128: 83.9 -> 73.2).
+    constexpr int prompt = std::max(1, (kWindow / PAGE + (C::TEAMS > 1 ? C::TEAMS : 0)) / C::TEAMS);
+    if (windows >= num_sms) share = std::min<long long>(share, prompt);
     const dim3 grid((unsigned)(windows * share * (p.q ? 3 : 2)), groups);
     const size_t smem = (size_t)C::TEAMS * PAGE * p.rot * 4;
     auto *const kernel = p.interleaved ? fa_kv_append_rope_kernel<D, PAGE, true> : fa_kv_append_rope_kernel<D, PAGE, false>;
