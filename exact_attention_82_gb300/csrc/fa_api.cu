@@ -994,6 +994,7 @@ static int chunk_checked(const void *q, const int *cu_q, const int *seq_lens, co
     if (!workspace || !aligned16(workspace) || workspace_bytes < need) return FA_ERR_WORKSPACE;
     const size_t heads = (size_t)num_pages * Hkv, codes = heads * page_size * D;
     if (heads * page_size > 0xffffffffull) return FA_ERR_BAD_SHAPE;  // rows of a cache: more than memory holds
+    if ((long long)max_pages * page_size > 0x7fffffffll - 1024) return FA_ERR_BAD_SHAPE;  // a length, a tile and an item's fixed cost are one int
     const Span outs[3] = {{o, (size_t)T * Hq * D * 2}, {lse, (size_t)T * Hq * 4}, {workspace, need}};
     const Span ins[8] = {{q, strided_bytes(T, q_stride, Hq, D)}, {cu_q, ((size_t)B + 1) * 4}, {seq_lens, (size_t)B * 4},
                          {block_table, (size_t)B * max_pages * 4}, {k_pages, codes}, {v_pages, codes},

@@ -552,7 +552,7 @@ size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  * (fa_kv_append's are), or a v_scale is not within 2^-15 to 2^7 of the largest that the pass began
  * with.  O is rounded once to bf16.  A scale that is not finite makes the rows that see its keys NaN or
  * infinite, and no others.
- * T * Hq < 2^31.  Deterministic; no atomics on results.
+ * T * Hq < 2^31, max_pages * page_size < 2^31 - 1023.  Deterministic; no atomics on results.
  *   workspace   at least fa_fwd_paged_chunk_workspace_bytes(...) bytes, as for fa_fwd_paged
  * Errors: those of fa_fwd_paged.  An on-chip wait that gives up sets FA_ERR_TIMEOUT in the status word
  * (fa_device_status); O and LSE are then undefined.

@@ -307,6 +307,12 @@ def test_append_shapes():
     run_append([3, 40, 0, 11, 16, 20] * 4, [1] * 24, 2, 32, 64, 64, seed=6, gap=True, means=True)
 
 
+def test_append_a_window_for_each_sm():
+    """As many tokens as make a block look after all runs of its tokens: prompts, and a few tokens each of many requests."""
+    run_append([50, 0], [6000, 4100], 1, 128, 128, 128, seed=11, G=2)
+    run_append([i * 7 % 40 for i in range(2600)], [4] * 2600, 1, 16, 64, 64, seed=12, G=1, pad=9, means=True)
+
+
 def test_append_agrees_with_append_where_nothing_turns():
     """At position 0 a rotation is the identity: the very same codes, scales and means."""
     c1, c2 = pu.Cache([40, 200, 3], 2, 32, 128, seed=9), pu.Cache([40, 200, 3], 2, 32, 128, seed=9)

@@ -188,7 +188,8 @@ def test_page_sizes(call, page):
     (append, dict(strides=(120, 128, 256, 256))), (append, dict(strides=(128, 132, 256, 256))), (append, dict(strides=(128, 128, 248, 256))),
     (append, dict(strides=(128, 128, 256, 255))), (append, dict(num_pages=1 << 27)),
     (chunk, dict(Hq=3)), (chunk, dict(B=0)), (chunk, dict(T=0)), (chunk, dict(qs=255)), (chunk, dict(Hkv=0)), (chunk, dict(max_pages=0)),
-    (chunk, dict(T=2 ** 30 + 1, Hq=1, Hkv=1)), (chunk, dict(T=1 << 25, Hq=64, Hkv=1, qs=4096)), (chunk, dict(B=8193))])
+    (chunk, dict(T=2 ** 30 + 1, Hq=1, Hkv=1)), (chunk, dict(T=1 << 25, Hq=64, Hkv=1, qs=4096)), (chunk, dict(B=8193)),
+    (chunk, dict(max_pages=(2 ** 31 - 1) // 16 - 63))])
 def test_bad_shapes(call, kw):
     assert call(**kw) == fa.FA_ERR_BAD_SHAPE
 
