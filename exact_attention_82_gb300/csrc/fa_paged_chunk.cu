@@ -45,6 +45,12 @@
 // in the workspace, and a second kernel joins them in order.  Lengths are read on the device.
 //
 // Every wait is bounded in time; one that gives up records a status code and the block winds down.
+//
+// Measured, D = 128: 1024 tokens behind 65536, 8 of 32 heads 793 us, 1,397 TFLOP/s (73% of the measured bf16 rate); 512 behind
+// 16384 131 us, 55%; 4 prompts of 4096, 16 heads 309 us, 46%; 32 sequences of 1 to 1024 tokens behind 50 to 8000, 8 of 64 heads, pages
+// of 16 579 us, 45%.  A tile takes 3,260 cycles, of which the tensor pipe has work for 2,140 and the exponentials take
+// 2,050; the rest is the way from S through the softmax to the next S.  An item's ends cost about five tiles more, the cut and first
+// tile 6 to 11 us, the join 2.5 to 6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
