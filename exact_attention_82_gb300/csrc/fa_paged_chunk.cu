@@ -46,10 +46,10 @@
 //
 // Every wait is bounded in time; one that gives up records a status code and the block winds down.
 //
-// Measured, D = 128: 1024 tokens behind 65536, 8 of 32 heads 793 us, 1,397 TFLOP/s (73% of the measured bf16 rate); 512 behind
-// 16384 131 us, 55%; 4 prompts of 4096, 16 heads 309 us, 46%; 32 sequences of 1 to 1024 tokens behind 50 to 8000, 8 of 64 heads, pages
-// of 16 579 us, 45%.  A tile takes 3,260 cycles, of which the tensor pipe has work for 2,140 and the exponentials take
-// 2,050; the rest is the way from S through the softmax to the next S.  An item's ends cost about five tiles more, the cut and first
+// Measured, D = 128: 1024 tokens behind 65536, 8 of 32 heads 810 us, 1,368 TFLOP/s (71% of the measured bf16 rate); 512 behind
+// 16384 128 us, 57%; 4 prompts of 4096, 16 heads 296 us, 48%; 32 sequences of 1 to 1024 tokens behind 50 to 8000, 8 of 64 heads, pages
+// of 16 567 us, 46%.  A tile takes 3,260 cycles, of which the tensor pipe has work for 2,140 and the exponentials take
+// 2,050; the rest is the way from S through the softmax to the next S.  An item's ends cost four to five tiles more, the cut and first
 // tile 6 to 11 us, the join 2.5 to 6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -70,7 +70,7 @@ constexpr int kCkThreads = 640;
 constexpr int kCkCodeWarps = 8;
 constexpr int kCkRows = 256;        // rows of an item, two sub-tiles of 128
 constexpr int kCkTile = 128;        // keys a tile
-constexpr int kCkFixed = 576;       // keys that an item's fixed cost stands for
+constexpr int kCkFixed = 576;       // keys that an item's fixed cost stands for (512: the mixed batch above 582 us instead of 567; 640: the prompts 303 instead of 296)
 constexpr int kCkMinShare = 768;    // of a block, in keys
 constexpr int kCkSegs = 4;          // segments in the ring
 constexpr int kCkTiles = 8;         // tiles in theirs
