@@ -8,10 +8,10 @@
 //
 // Bound by HBM: 4 bytes read and 2 written for a key and a value element, 2 and 2 for a
 // query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 64.3 us, 5,740
-// GB/s (84% of the copy rate); the queries alone take 44.  Keys alone take 33: a team waits
+// GB/s (85% of the copy rate); the queries alone take 44.  Keys alone take 33: a team waits
 // for memory, for the largest magnitude of the page and to be written, head after head, and a quarter
 // of it is sines and cosines.  (A head's rows asked for while the one before is written: no gain.)
-// 64 single tokens 7.5 us.
+// 64 single tokens 5.7 us, 256 15.6 us.
 #include <math.h>
 
 #include <algorithm>
@@ -27,7 +27,7 @@ namespace fa {
 static __device__ int g_status_kv_append_rope = 0;
 
 constexpr int kRopeThreadsAnSm = 1024;  // that the kernel's registers are held to (768: 89 us for the prompt, 1536: 96, when it took 78)
-constexpr int kAppendFill = 1024;       // threads an SM, of each kind, below which a block takes fewer heads
+constexpr int kAppendFill = 1024;       // threads an SM, of each kind, that the windows' blocks are to make up
 
 template <int D, int PAGE, class C>
 struct AppendShared {
@@ -39,19 +39,18 @@ struct AppendShared {
 
 enum class Turn { none, halves, pairs };  // whether rows are rotated, and which elements make a pair
 
-// One block's share of the runs of a window, of heads h0 .. h1 - 1 of K (kv = 0) or V; `turns`: shared memory for the
-// angles of a team's run, which all its heads take.
-template <int D, int PAGE, class C, Turn TURN>
-__device__ __forceinline__ void append_runs(const AppendParams &p, const int share, const int kv, AppendShared<D, PAGE, C> &sm,
-                                            const int block, const int h0, const int h1, float4 *const turns = nullptr) {
+// One of `share` blocks' part of the runs of a window, of heads h0 .. h0 + heads - 1 of K (kv = 0) or V; `turns`: shared memory for the
+// angles of a team's run, which all its heads take.  Its teams take run after run, or (EVEN) as many (run, head) each, one run's heads in a
+// row, so that single tokens (many runs) and prompts (few) keep the same blocks busy.
+template <int D, int PAGE, class C, Turn TURN, bool EVEN>
+__device__ __forceinline__ void append_runs(const AppendParams &p, const int share, const int h0, const int heads, const int kv, AppendShared<D, PAGE, C> &sm,
+                                            const int win, const int part, float4 *const turns = nullptr) {
     int *const slot_of = sm.slot_of;
     uint32_t *const starts = sm.starts;
     auto &amax_sm = sm.amax;
     auto &sums = sm.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
-    int h = h0;
-    const int win = block / share, part = block % share;
     const int t0 = win * kWindow;
     const int limit = p.num_pages * PAGE;  // fewer than 2^31
     const __nv_bfloat16 *const x_first = static_cast<const __nv_bfloat16 *>(kv ? p.x[1] : p.x[0]) + h0 * D;
@@ -84,7 +83,19 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
     const uint32_t s0 = starts[0], s1 = starts[1], lt = (1u << lane) - 1;
     const int rank0 = (s0 >> lane) & 1u ? __popc(s0 & lt) : -1, rank1 = (s1 >> lane) & 1u ? __popc(s0) + __popc(s1 & lt) : -1;
     const int runs = __popc(s0) + __popc(s1);
-    for (int run = part * C::TEAMS + team; run < runs; run += share * C::TEAMS) {
+    const int each = (runs * heads + share * C::TEAMS - 1) / (share * C::TEAMS);
+    int item = (part * C::TEAMS + team) * (EVEN ? each : 1);
+    const int last = EVEN ? min(item + each, runs * heads) : runs;
+    while (item < last) {
+        int run = item, h = h0, h1 = h0 + heads;
+        if constexpr (EVEN) {
+            run = item / heads;
+            h += item - run * heads;
+            h1 = min(h1, h + last - item);
+            item += h1 - h;
+        } else {
+            item += share * C::TEAMS;
+        }
         const uint32_t m0 = __ballot_sync(0xffffffffu, rank0 == run), m1 = __ballot_sync(0xffffffffu, rank1 == run);
         const int i0 = m0 ? __ffs((int)m0) - 1 : 31 + __ffs((int)m1);
         const int slot = slot_of[i0], off = slot % PAGE, pg = slot / PAGE;
@@ -393,7 +404,6 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
             }
             team_sync();  // the next run overwrites the shared words
         } while (++h < h1);
-        h = h0;
     }
 }
 
@@ -402,25 +412,27 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
 // blocks of different kinds instead: three prompts of 5000 tokens 64 for 60 us, 16384 tokens in pages of 128 73 for 70).  A sine and cosine
 // is some 50 instructions, and the same for all heads: a block takes `per` heads, and their angles once
 // (a prompt of 16384 tokens, 8 heads of keys, 32 of queries: 109 us with an angle for every head).
-template <int D, int PAGE, bool INTER>
-__global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS, kRopeThreadsAnSm / AppendCfg<D, PAGE, 32>::THREADS) fa_kv_append_rope_kernel(const __grid_constant__ AppendParams p, int share, int per) {
+template <int D, int PAGE, bool INTER, bool EVEN>
+__global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS, kRopeThreadsAnSm / AppendCfg<D, PAGE, 32>::THREADS) fa_kv_append_rope_kernel(const __grid_constant__ AppendParams p, int share, int per, int q_tokens, int q_groups) {
     using C = AppendCfg<D, PAGE, 32>;
     grid_wait();
     extern __shared__ __align__(16) float4 turns_sm[];
     __shared__ AppendShared<D, PAGE, C> sm;
-    const int kinds = p.q ? 3 : 2, each = gridDim.x / kinds, kind = blockIdx.x / each, block = blockIdx.x % each;
-    const int h0 = blockIdx.y * per, h1 = min(h0 + per, p.Hkv);
+    const int windows = (p.T + kWindow - 1) / kWindow, each = windows * share, kind = min((int)blockIdx.x / each, 2);
+    const int block = (int)blockIdx.x - kind * each, n = kind < 2 ? share : q_tokens * q_groups, win = block / n, part = block % n;
+    const int h0 = EVEN ? 0 : blockIdx.y * per, heads = EVEN ? p.Hkv : min(per, p.Hkv - h0);
     if (kind == 0) {
-        append_runs<D, PAGE, C, INTER ? Turn::pairs : Turn::halves>(p, share, 0, sm, block, h0, h1,
+        append_runs<D, PAGE, C, INTER ? Turn::pairs : Turn::halves, EVEN>(p, share, h0, heads, 0, sm, win, part,
                                                                           turns_sm + threadIdx.x / (32 * C::TEAM) * PAGE * (p.rot / 4));
     } else if (kind == 1) {
-        append_runs<D, PAGE, C, Turn::none>(p, share, 1, sm, block, h0, h1);
+        append_runs<D, PAGE, C, Turn::none, EVEN>(p, share, h0, heads, 1, sm, win, part);
     } else {
         constexpr int TPT = D / 16, TOKENS = C::THREADS / TPT;
-        const int win = block / share, part = block % share, sub = threadIdx.x % TPT;
+        const int sub = threadIdx.x % TPT, group = part / q_tokens;
+        const int all = heads * p.G, a_group = (all + q_groups - 1) / q_groups, q0 = h0 * p.G + min(group * a_group, all), q_heads = min(a_group, h0 * p.G + all - q0);
         const bool turned = sub < p.rot / 16;
         const int2 piece = rope_pieces(sub, p.rot, INTER);
-        for (int i = part * TOKENS + threadIdx.x / TPT; i < kWindow; i += share * TOKENS) {
+        for (int i = part % q_tokens * TOKENS + threadIdx.x / TPT; i < kWindow; i += q_tokens * TOKENS) {
             const int t = win * kWindow + i;
             if (t >= p.T) break;
             float2 f[8];
@@ -429,11 +441,11 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE, 32>::THREADS, kRopeThreadsA
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = rope_factor(__ldg(p.phases + 8 * sub + j), position, p.amplitude);
             }
-            const __nv_bfloat16 *const x = static_cast<const __nv_bfloat16 *>(p.q) + t * p.q_stride + (long long)h0 * p.G * D;
-            __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(p.q_out) + t * p.q_out_stride + (long long)h0 * p.G * D;
+            const __nv_bfloat16 *const x = static_cast<const __nv_bfloat16 *>(p.q) + t * p.q_stride + (long long)q0 * D;
+            __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(p.q_out) + t * p.q_out_stride + (long long)q0 * D;
             constexpr int AHEAD = 4;  // heads whose loads are in flight (a store may not pass a load that is written below it)
 #pragma unroll 1
-            for (int g = 0, n = (h1 - h0) * p.G; g < n; g += AHEAD) {
+            for (int g = 0, n = q_heads; g < n; g += AHEAD) {
                 uint4 w[AHEAD][2];
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k) {
@@ -464,25 +476,35 @@ template <int D, int PAGE>
 static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaStream_t stream) {
     using C = AppendCfg<D, PAGE, 32>;
     const int windows = (p.T + kWindow - 1) / kWindow;
-    constexpr int most = kWindow / C::TEAMS;
-    // Heads a block: all where the windows fill the chip, fewer where they do not; then blocks that share a window's runs.
-    int groups = (int)std::min<long long>((kAppendFill / C::THREADS * (long long)num_sms + windows - 1) / windows, p.Hkv);
-    const int per = (p.Hkv + groups - 1) / groups;
-    groups = (p.Hkv + per - 1) / per;
-    long long share = 32ll * num_sms / ((long long)windows * groups * 2);
-    share = share < 1 ? 1 : (share > most ? most : share);
-    // With a window for each SM the tokens are prompts', whose windows have no more runs than this; further blocks would
-    // look for runs and find none (16384 tokens, 8 and 32 heads, D = 128, pages of 64: 70.6 -> 64.9 us; pages of 128: 83.9 -> 73.2).
-    constexpr int prompt = std::max(1, (kWindow / PAGE + (C::TEAMS > 1 ? C::TEAMS : 0)) / C::TEAMS);
-    if (windows >= num_sms) share = std::min<long long>(share, prompt);
-    const dim3 grid((unsigned)(windows * share * (p.q ? 3 : 2)), groups);
+    int share, groups = 1, per = 0, q_tokens = 0, q_groups = 0;  // blocks of each kind for a window (and group of heads)
+    const bool even = windows < num_sms;
+    if (!even) {
+        // With a window for each SM the tokens are prompts': groups of heads, as many as fill the chip, and no more blocks than a prompt's
+        // window has runs for (others would find none: 16384 tokens, 8 and 32 heads, D = 128, pages of 64 70.6 -> 64.9 us, of 128 83.9 -> 73.2).
+        constexpr int prompt = std::max(1, (kWindow / PAGE + (C::TEAMS > 1 ? C::TEAMS : 0)) / C::TEAMS);
+        groups = std::min((kAppendFill / C::THREADS * num_sms + windows - 1) / windows, p.Hkv);
+        per = (p.Hkv + groups - 1) / groups;
+        groups = (p.Hkv + per - 1) / per;
+        share = prompt;
+        if (p.q) q_tokens = prompt, q_groups = 1;
+    } else {
+        // Fewer may be of single tokens, each a run, or of prompts: shared out evenly.  (With groups of heads, as above, of whose
+        // blocks many have no run, 256 single tokens of 8 heads, queries of 32, took 23.3 us for 15.6, a prompt of 700 18.6 for 9.5.)  Teams that are a whole
+        // block do better with half of the threads (64 single tokens 7.9 -> 6.5), those of a warp with all (the ragged prompts 24.2 -> 21.4).
+        const int tokens = std::min(p.T, kWindow), fill = ((C::TEAMS > 1 ? kAppendFill : kAppendFill / 2) / C::THREADS * num_sms + windows - 1) / windows;
+        constexpr int at_once = C::THREADS / (D / 16);
+        share = std::min(fill, (tokens * p.Hkv + C::TEAMS - 1) / C::TEAMS);
+        if (p.q) q_tokens = std::min(fill, (tokens + at_once - 1) / at_once), q_groups = std::max(1, std::min(fill / q_tokens, p.Hkv * p.G));
+    }
+    const dim3 grid((unsigned)(windows * (2 * share + q_tokens * q_groups)), groups);
     const size_t smem = (size_t)C::TEAMS * PAGE * p.rot * 4;
-    auto *const kernel = p.interleaved ? fa_kv_append_rope_kernel<D, PAGE, true> : fa_kv_append_rope_kernel<D, PAGE, false>;
+    auto *const kernel = even ? (p.interleaved ? fa_kv_append_rope_kernel<D, PAGE, true, true> : fa_kv_append_rope_kernel<D, PAGE, false, true>)
+                              : (p.interleaved ? fa_kv_append_rope_kernel<D, PAGE, true, false> : fa_kv_append_rope_kernel<D, PAGE, false, false>);
     if (smem + sizeof(AppendShared<D, PAGE, C>) > 48 * 1024) {  // beyond what a kernel may have without asking: always the most, as other threads' calls set it too
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::TEAMS * PAGE * D * 4);
         if (e != cudaSuccess) return e;
     }
-    return launch_early(kernel, grid, C::THREADS, smem, stream, 1, p, (int)share, per);
+    return launch_early(kernel, grid, C::THREADS, smem, stream, 1, p, share, per, q_tokens, q_groups);
 }
 
 template <int D>

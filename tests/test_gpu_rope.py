@@ -310,6 +310,8 @@ def test_append_shapes():
 def test_append_a_window_for_each_sm():
     """As many tokens as make a block look after all runs of its tokens: prompts, and a few tokens each of many requests."""
     run_append([50, 0], [6000, 4100], 1, 128, 128, 128, seed=11, G=2)
+    run_append([0, 7], [6000, 4100], 5, 64, 64, 32, seed=13, G=1, interleaved=True)
+    run_append([33], [10000], 1, 32, 128, 64, seed=14, G=0)
     run_append([i * 7 % 40 for i in range(2600)], [4] * 2600, 1, 16, 64, 64, seed=12, G=1, pad=9, means=True)
 
 
