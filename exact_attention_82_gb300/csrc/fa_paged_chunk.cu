@@ -41,8 +41,8 @@
 //
 // Split.  Items (sequence, key/value head, 256 rows) are laid end to end, each as long as its
 // keys and a fixed cost, and the line is cut into equal shares, one a block.  What a block has of
-// an item is a segment of its tiles.  An item that is cut leaves its parts (normalised sums, m, l)
-// in the workspace, and a second kernel joins them in order.  Lengths are read on the device.
+// an item is a segment of its tiles.  An item that is cut leaves its parts (normalised sums, m, l; l = 0
+// of a block whose share is less than a tile) in the workspace, and a second kernel joins them in order.  Lengths are read on the device.
 //
 // Every wait is bounded in time; one that gives up records a status code and the block winds down.
 //
@@ -572,6 +572,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
             Cut at = cut_sm[0];
             const Cut end = cut_sm[1];
             const long long share = share_sm;
+            // Both cuts before the same tile inside an item (the line weighs rows that see no key too, so that a share may be less
+            // than a tile): the join counts this block's part all the same, and is to find that it holds nothing.
+            if (at.begin == end.begin && at.done > 0 && at.done == end.done)
+                for (int r = lane; r < kCkRows; r += 32) ck_slot(p.ws, gridDim.x, blockIdx.x, 0, D)[(size_t)kCkRows * (D + 1) + r] = 0.f;
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 const int place = n % kCkSegs;
