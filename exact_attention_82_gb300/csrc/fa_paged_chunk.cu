@@ -14,8 +14,9 @@
 //   it are rounded, to steps of 2^-24 of it);
 //   k_j as code * 2^(e_j - e), e the largest exponent of the key scales in the tile: exactly, to
 //   2^-15 of the largest scale (steps of 2^-24 of it below);
-//   v_j as code * 2^(e_j - e), e the largest exponent of the value scales in the first tile.  O's
-//   sums are in units of 2^e.
+//   v_j as code * 2^(e_j - e), e the largest exponent of the value scales in the first tile that has a finite one
+//   (rows that see the tiles before it are NaN; others do not, and must not be measured by them).  O's sums are in
+//   units of 2^e.
 // The powers of two are put back into c (by row and tile) and into O.  A tile with a scale that is no
 // power of two, or a value scale not within 2^-15 to 2^7 of the first tile's, goes another way: scores take
 // the rest of the key scale in fp32, and weights times the value scale go to bf16 (2^-8 of each), which has
@@ -126,7 +127,7 @@ enum : uint32_t {
     C_COUNT = 51
 };
 constexpr uint32_t kSlotTmem = 408, kSlotAbort = 412;
-constexpr uint32_t kSlotExp = 416;     // 4 words: e of a segment's values
+constexpr uint32_t kSlotExp = 416;     // 4 words: e of a segment's values, behind its last tile
 constexpr uint32_t kSlotNan = 432;     // 4 words: number + 1 of a segment with NaN among masked tiles' values
 constexpr uint32_t kSlotSegs = 448;    // 4 segments of 64 bytes
 // By the tile's number modulo 16 (the softmax may be ten tiles behind what is looked up):
@@ -646,6 +647,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 const int e = (int)(__float_as_uint(x) >> 23 & 0xffu) - 127;
                 return e == 128 ? -126 : max(e, -126);
             };
+            constexpr int kNone = -127;  // below every exponent
             auto top_of_tile = [](int x) {
 #pragma unroll
                 for (int d = 1; d < 8; d <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 const int edge = CK_SEG(g, c) + CK_SEG(g, row0) / p.G + 1;  // keys that the item's first row sees
                 const int *const table = p.table + (long long)CK_SEG(g, b) * p.max_pages;
                 release(n);
-                int e_ref = 0;
+                int e_ref = kNone;
                 for (int it = 0; it < N || end; it += 4) {  // (behind the last segment: one more "tile" that says so)
                     const int some = end ? 1 : min(4, N - it), key = (t1 - 1 - it - j) * kCkTile + 16 * i;
                     int ph = -2;  // page * Hkv + head; -2: no keys, -1: outside the cache
@@ -680,10 +682,14 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     }
                     const bool there = ph >= 0;
                     const int ek = exponent(ks), ev = exponent(vs);
-                    const int e_tile = top_of_tile(there ? ek : -126), v_tile = top_of_tile(there ? ev : -126);
-                    if (it == 0) e_ref = __shfl_sync(0xffffffffu, v_tile, 0);
+                    const int e_tile = top_of_tile(there ? ek : -126), v_tile = top_of_tile(there && vs > 0.f && vs < INFINITY ? ev : kNone);
+                    if (e_ref == kNone) {
+                        const uint32_t has = __ballot_sync(0xffffffffu, v_tile != kNone);
+                        if (has) e_ref = __shfl_sync(0xffffffffu, v_tile, __ffs((int)has) - 1);
+                    }
+                    const int unit = e_ref == kNone ? 0 : e_ref;
                     const float rest = ks * ck_two_to(-ek);
-                    const bool wide = top_of_tile(there && (rest != 1.f || vs * ck_two_to(-ev) != 1.f || ev - e_ref > kCkUp || e_ref - ev > kCkDown)) != 0;
+                    const bool wide = top_of_tile(there && (rest != 1.f || vs * ck_two_to(-ev) != 1.f || ev - unit > kCkUp || unit - ev > kCkDown)) != 0;
                     // the tiles' places in the rings
 #pragma unroll 1
                     for (int k = 0; ok && k < some; ++k)
@@ -693,17 +699,17 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     if (j < some) {
                         const uint32_t row = ((uint32_t)max(ph, 0) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
                         const uint32_t kf = ph == -1 ? 0x7e007e00u : ck_f16_two_to(min(ek - e_tile, 0));
-                        st_shared_v4(pieces_at(m) + i * (uint32_t)sizeof(Piece), row, there ? min(len - key, 16) : 0, kf, ck_f16_two_to(min(ev - e_ref, kCkUp)));
+                        st_shared_v4(pieces_at(m) + i * (uint32_t)sizeof(Piece), row, there ? min(len - key, 16) : 0, kf, ck_f16_two_to(min(ev - unit, kCkUp)));
                         if (wide) {
                             ck_put(rest_at(m) + i * 4, __float_as_uint(rest));
-                            ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(-e_ref) : 1.f));
+                            ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(-unit) : 1.f));
                         }
                         if (i == 0) {
                             ck_put(wide_at(m), wide);
                             ck_put(key_exp_at(m), __float_as_uint(wide ? -ck_two_to(e_tile) : ck_two_to(e_tile)));
                             // 1: no more tiles, 2: a row does not see some of its keys, 4: wide, 8 *: its segment
                             ck_put(flags_at(m), (end ? 1u : 0u) | (key + kCkTile > edge ? 2u : 0u) | (wide ? 4u : 0u) | (uint32_t)n << 3);
-                            if (it + j == 0) ck_put(exp_at(n), (uint32_t)e_ref);
+                            if (j == 0) ck_put(exp_at(n), (uint32_t)unit);  // (read when the segment's last tile is through)
                         }
                     }
                     __syncwarp();

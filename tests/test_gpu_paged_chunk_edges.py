@@ -30,5 +30,66 @@ def test_thousands_of_tokens_more_than_keys(n, L, Hkv, D):
     run_chunk(c, q, cu, d_cu, workspace=ws)
 
 
+def reached(c, q, cu, d_cu, hidden_from, heads, weights):
+    """Rows of sequence 0 from token hidden_from on and of `heads` are other than finite; all others are as the definition has them."""
+    o, lse = fa.fa_fwd_paged_chunk(q, d_cu, c.d_lens, c.d_table, *c.pages)
+    T, Hq, _ = q.shape
+    with np.errstate(invalid="ignore"):
+        ref = reference(c, pu.f64(q), cu, q.shape[2] ** -0.5)
+    keep = np.ones((T, Hq), bool)
+    keep[hidden_from:int(cu[1]), heads] = False
+    assert np.array_equal(np.isnan(ref[0]).all(2), ~keep), "the test's own definition"
+    assert not np.isfinite(pu.f64(o))[~keep].any(), "rows that see the page"
+    got = np.where(keep[..., None], pu.f64(o), 0), np.where(keep, pu.f64(lse), 0)
+    want = [np.where(keep[..., None] if a.ndim == 3 else keep, a, 0) for a in ref]
+    check(*(torch.from_numpy(a) for a in got), want, T, weights)
+
+
 # The last tile's only page: pages of a whole tile, and sequences whose last tile has one page.
 ONLY_PAGES = [(128, 300), (64, 300), (16, 260), (32, 385), (16, 513)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,L", ONLY_PAGES)
+@pytest.mark.parametrize("bad", [-1, 10 ** 9])
+def test_a_last_tile_without_a_page(page, L, D, bad):
+    """Rows that would read the page are NaN; earlier ones of the same 256 rows do not see it and are as ever."""
+    for G, n in ((1, 250), (4, 60)):
+        c = pu.Cache([L, 200], 2, page, D, seed=L + G)
+        last = (L - 1) // page
+        c.table[0, last] = bad
+        put_back(c)
+        q, cu, d_cu = pu.queries([n, 100], 2 * G, D, seed=L)
+        reached(c, q, cu, d_cu, last * page - (L - n), slice(None), 2.0 ** -11)
+        assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,L", ONLY_PAGES)
+@pytest.mark.parametrize("what,scale", [("k", math.nan), ("v", math.nan), ("v", math.inf)])
+def test_a_last_tile_whose_scale_is_not_finite(page, L, what, scale, D):
+    last_scale(page, L, what, scale, D)
+
+
+def last_scale(page, L, what, scale, D):
+    for G, n in ((1, 250), (4, 60)):
+        c = pu.Cache([L, 200], 2, page, D, seed=L + G)
+        last = (L - 1) // page
+        scales = c.ks if what == "k" else c.vs
+        scales[c.table[0, last], 1] = scale
+        put_back(c)
+        q, cu, d_cu = pu.queries([n, 100], 2 * G, D, seed=L)
+        scales = c.ks if what == "k" else c.vs
+        scales[c.table[0, last], 1] = math.nan  # (where an infinity ends up as NaN, where not, is not looked at)
+        reached(c, q, cu, d_cu, last * page - (L - n), slice(G, 2 * G), 2.0 ** -11)
+
+
+def test_no_page_at_all():
+    """Every page of a sequence lies outside the cache: its rows are NaN, its neighbour's are not."""
+    c = pu.Cache([700, 300], 1, 128, 128, seed=3)
+    c.table[0, :] = -1
+    put_back(c)
+    q, cu, d_cu = pu.queries([200, 200], 2, 128, seed=3)
+    o, _ = run_chunk(c, q, cu, d_cu)
+    assert bool(torch.isnan(o[:200]).all()) and not bool(torch.isnan(o[200:]).any())
+    assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
