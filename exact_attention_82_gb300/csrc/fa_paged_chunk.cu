@@ -149,7 +149,7 @@ struct __align__(16) Seg {
 static_assert(sizeof(Seg) == 64, "");
 
 // Of 16 keys of a tile: their first row of the cache, how many rows have keys, and the factors in fp16 that
-// K's and V's codes are multiplied with, in both halves of a word (K's: NaN for a page outside the cache).
+// K's and V's codes are multiplied with, in both halves of a word (K's: NaN for a page outside the cache or with a scale that is not finite).
 struct __align__(16) Piece {
     uint32_t row;
     int valid;
@@ -643,10 +643,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
             // ================================================= tiles
             // Four tiles of a segment at a time, lane 8 j + i for piece i of the j-th.
             const int j = lane >> 3, i = lane & 7;
-            auto exponent = [](float x) {  // (one that is not finite must not be what its tile's others are measured by)
-                const int e = (int)(__float_as_uint(x) >> 23 & 0xffu) - 127;
-                return e == 128 ? -126 : max(e, -126);
-            };
+            auto exponent = [](float x) { return max((int)(__float_as_uint(x) >> 23 & 0xffu) - 127, -126); };
             constexpr int kNone = -127;  // below every exponent
             auto top_of_tile = [](int x) {
 #pragma unroll
@@ -668,6 +665,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 for (int it = 0; it < N || end; it += 4) {  // (behind the last segment: one more "tile" that says so)
                     const int some = end ? 1 : min(4, N - it), key = (t1 - 1 - it - j) * kCkTile + 16 * i;
                     int ph = -2;  // page * Hkv + head; -2: no keys, -1: outside the cache
+                    bool nan = false;  // keys that make the rows that see them NaN
                     float ks = 1.f, vs = 1.f;
                     if (!end && j < some && key < len) {
                         ph = table[key >> p.page_log2];
@@ -675,14 +673,16 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                             ph = ph * p.Hkv + h;
                             ks = p.k_scale[ph];
                             vs = p.v_scale[ph];
+                            nan = !(fabsf(ks) < INFINITY);
+                            if (nan) ks = 1.f;
                         } else {
-                            ph = -1;
+                            ph = -1, nan = true;
                             atomicExch(&g_status_chunk, (int)FA_ERR_BAD_PAGE);
                         }
                     }
                     const bool there = ph >= 0;
                     const int ek = exponent(ks), ev = exponent(vs);
-                    const int e_tile = top_of_tile(there ? ek : -126), v_tile = top_of_tile(there && vs > 0.f && vs < INFINITY ? ev : kNone);
+                    const int e_tile = top_of_tile(there && !nan ? ek : -126), v_tile = top_of_tile(there && vs > 0.f && vs < INFINITY ? ev : kNone);
                     if (e_ref == kNone) {
                         const uint32_t has = __ballot_sync(0xffffffffu, v_tile != kNone);
                         if (has) e_ref = __shfl_sync(0xffffffffu, v_tile, __ffs((int)has) - 1);
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     const int m = tile + j;
                     if (j < some) {
                         const uint32_t row = ((uint32_t)max(ph, 0) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
-                        const uint32_t kf = ph == -1 ? 0x7e007e00u : ck_f16_two_to(min(ek - e_tile, 0));
+                        const uint32_t kf = nan ? 0x7e007e00u : ck_f16_two_to(min(ek - e_tile, 0));
                         st_shared_v4(pieces_at(m) + i * (uint32_t)sizeof(Piece), row, there ? min(len - key, 16) : 0, kf, ck_f16_two_to(min(ev - unit, kCkUp)));
                         if (wide) {
                             ck_put(rest_at(m) + i * 4, __float_as_uint(rest));

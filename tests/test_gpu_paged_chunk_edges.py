@@ -84,6 +84,13 @@ def last_scale(page, L, what, scale, D):
         reached(c, q, cu, d_cu, last * page - (L - n), slice(G, 2 * G), 2.0 ** -11)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,L", ONLY_PAGES)
+def test_keys_whose_scale_is_infinite(page, L, D):
+    """A row that sees such keys is other than finite whatever the sign of its products with their codes."""
+    last_scale(page, L, "k", math.inf, D)
+
+
 def test_no_page_at_all():
     """Every page of a sequence lies outside the cache: its rows are NaN, its neighbour's are not."""
     c = pu.Cache([700, 300], 1, 128, 128, seed=3)
