@@ -54,6 +54,7 @@
 // tile 6 to 11 us, the join 2.5 to 6.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stddef.h>
@@ -990,7 +991,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 // one has nothing else in it.)
                 const float key_exp = __uint_as_float(ck_get(key_exp_at(tile)));  // negative: the tile goes the other way
                 const bool masked = it < plain_from, wide = key_exp < 0.f;
-                const float c_tile = c_row * fabsf(key_exp);
+                float c_tile = c_row * fabsf(key_exp);
                 int half = 0;
                 if (!(masked || wide) && ready) {
                     uint32_t s[3][16], pk[32];
@@ -1037,6 +1038,8 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 }
                 const int lim = limit_of_row() - (CK_SEG(g, t1) - 1 - it) * kCkTile;
                 // ---- the others, or the second half of one: the maximum first, then P, 16 keys at a time
+                // (A factor of 0 would make NaN of masked keys' -infinity.  The sum is another than c_tile only where scores are 0 either way.)
+                c_tile += FLT_MIN;
                 uint32_t x[16];
                 auto piece = [&](int c) {
                     tmem_ld16(s_tm + c * 16, x);

@@ -100,3 +100,14 @@ def test_no_page_at_all():
     o, _ = run_chunk(c, q, cu, d_cu)
     assert bool(torch.isnan(o[:200]).all()) and not bool(torch.isnan(o[200:]).any())
     assert fa.fa_device_status() == fa.FA_ERR_BAD_PAGE
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_exponent,k_exponent", [(-60, -100), (-120, -20), (-126, -126), (0, -126)])
+def test_scores_that_vanish(q_exponent, k_exponent, D):
+    """Queries times key scales below fp32: all scores are 0, and a row is the mean of the values that it sees."""
+    c = pu.Cache([400, 90], 2, 32, D, seed=D)
+    c.ks[:] = 2.0 ** k_exponent
+    put_back(c)
+    q, cu, d_cu = pu.queries([300, 90], 4, D, seed=D, mult=2.0 ** q_exponent)
+    run_chunk(c, q, cu, d_cu)
