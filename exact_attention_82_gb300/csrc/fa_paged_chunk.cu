@@ -16,7 +16,8 @@
 //   2^-15 of the largest scale (steps of 2^-24 of it below);
 //   v_j as code * 2^(e_j - e), e the largest exponent of the value scales in the first tile that has a finite one
 //   (rows that see the tiles before it are NaN; others do not, and must not be measured by them).  O's sums are in
-//   units of 2^e.
+//   units of 2^e; a tile with a scale more than 2^kCkLift units takes e up to its own, and O is rescaled, so that sums of any
+//   number of keys stay finite.
 // The powers of two are put back into c (by row and tile) and into O.  A tile with a scale that is no
 // power of two, or a value scale not within 2^-15 to 2^7 of the first tile's, goes another way: scores take
 // the rest of the key scale in fp32, and weights times the value scale go to bf16 (2^-8 of each), which has
@@ -79,6 +80,7 @@ constexpr int kCkTiles = 8;         // tiles in theirs
 constexpr float kCkShift = 4.f;     // exponent of a weight at the maximum in use
 constexpr float kCkMost = 32768.f;  // of a half tile's sum
 constexpr int kCkUp = 7, kCkDown = 15;  // how far a value scale's exponent may lie above or below the first tile's
+constexpr int kCkLift = 40;         // how far above it takes the unit up
 constexpr unsigned long long kCkDrainNs = 20ull * 1000 * 1000;
 // Registers: 640 x 96 at launch; what the code warps and the last four give goes to the softmax.  None of
 // the loops may spill: beside this much shared memory the cache that holds spilled registers is small, and
@@ -138,7 +140,9 @@ constexpr uint32_t kSlotRest = 832;    // what key scales are beside powers of t
 // and modulo 8: flags, and 16 bytes for each 16 keys
 constexpr uint32_t kSlotFlags = 1856;
 constexpr uint32_t kSlotPieces = 2048;
-static_assert(C_COUNT * 8 <= kSlotTmem && kSlotRest + 16 * 64 <= kSlotFlags && kSlotFlags + kCkTiles * 4 <= kSlotPieces, "");
+// and modulo 16 again, of a tile that goes the other way: what O is multiplied with before it, where the unit goes up
+constexpr uint32_t kSlotLift = kSlotPieces + kCkTiles * 128;
+static_assert(C_COUNT * 8 <= kSlotTmem && kSlotRest + 16 * 64 <= kSlotFlags && kSlotFlags + kCkTiles * 4 <= kSlotPieces && kSlotLift + 16 * 4 <= 4096, "");
 
 // What a block does of one item.
 struct __align__(16) Seg {
@@ -464,6 +468,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
     auto wide_at = [&](int tile) { return bars + kSlotWide + (tile & 15) * 4; };
     auto key_exp_at = [&](int tile) { return bars + kSlotKeyExp + (tile & 15) * 4; };
     auto rest_at = [&](int tile) { return bars + kSlotRest + (tile & 15) * 64; };  // [k, v][8 pieces]
+    auto lift_at = [&](int tile) { return bars + kSlotLift + (tile & 15) * 4; };
     auto flags_at = [&](int tile) { return bars + kSlotFlags + tile % kCkTiles * 4; };
     auto pieces_at = [&](int tile) { return bars + kSlotPieces + tile % kCkTiles * 128; };
     auto exp_at = [&](int seg) { return bars + kSlotExp + seg % kCkSegs * 4; };
@@ -688,9 +693,17 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                         const uint32_t has = __ballot_sync(0xffffffffu, v_tile != kNone);
                         if (has) e_ref = __shfl_sync(0xffffffffu, v_tile, __ffs((int)has) - 1);
                     }
-                    const int unit = e_ref == kNone ? 0 : e_ref;
+                    int unit = e_ref == kNone ? 0 : e_ref, before = unit;  // of this lane's tile, and of the one before it
+                    if (__any_sync(0xffffffffu, e_ref != kNone && v_tile - e_ref > kCkLift)) {
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            const int last = e_ref, top = __shfl_sync(0xffffffffu, v_tile, 8 * k);
+                            if (top - e_ref > kCkLift) e_ref = top;
+                            if (k == j) unit = e_ref, before = last;
+                        }
+                    }
                     const float rest = ks * ck_two_to(-ek);
-                    const bool wide = top_of_tile(there && (rest != 1.f || vs * ck_two_to(-ev) != 1.f || ev - unit > kCkUp || unit - ev > kCkDown)) != 0;
+                    const bool wide = top_of_tile(there && (rest != 1.f || vs * ck_two_to(-ev) != 1.f || ev - unit > kCkUp || unit - ev > kCkDown || before != unit)) != 0;
                     // the tiles' places in the rings
 #pragma unroll 1
                     for (int k = 0; ok && k < some; ++k)
@@ -704,13 +717,14 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                         if (wide) {
                             ck_put(rest_at(m) + i * 4, __float_as_uint(rest));
                             ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(-unit) : 1.f));
+                            if (i == 0) ck_put(lift_at(m), __float_as_uint(ck_two_to(before - unit)));
                         }
                         if (i == 0) {
                             ck_put(wide_at(m), wide);
                             ck_put(key_exp_at(m), __float_as_uint(wide ? -ck_two_to(e_tile) : ck_two_to(e_tile)));
                             // 1: no more tiles, 2: a row does not see some of its keys, 4: wide, 8 *: its segment
                             ck_put(flags_at(m), (end ? 1u : 0u) | (key + kCkTile > edge ? 2u : 0u) | (wide ? 4u : 0u) | (uint32_t)n << 3);
-                            if (j == 0) ck_put(exp_at(n), (uint32_t)unit);  // (read when the segment's last tile is through)
+                            if (j == 0) ck_put(exp_at(n), e_ref == kNone ? 0u : (uint32_t)e_ref);  // (read when the segment's last tile is through)
                         }
                     }
                     __syncwarp();
@@ -1067,18 +1081,19 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 const float factor = m_new == -INFINITY ? 1.f : ex2_approx(m_used - m_new);  // 0 on a row's first keys
                 m_used = m_new;
                 l_run *= factor;
+                const float factor_o = wide ? factor * __uint_as_float(ck_get(lift_at(tile))) : factor;
                 if (half == 1) {  // the first half's product must be in O before O is rescaled
                     ok = wait_all(C_PH_DONE + t, (uint32_t)(ns - 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                 }
-                if ((half == 1 || it > first) && __any_sync(0xffffffffu, factor != 1.f)) {  // O holds what came before at the old maximum
+                if ((half == 1 || it > first) && __any_sync(0xffffffffu, factor_o != 1.f)) {  // O holds what came before at the old maximum and in the old unit
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         tmem_ld16(o_tm + c * 16, x);
                         tmem_ld_wait16(x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor);
+                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor_o);
                         tmem_st16(o_tm + c * 16, x);
                         tmem_st_wait16(x);
                     }

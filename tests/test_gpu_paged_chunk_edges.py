@@ -111,3 +111,32 @@ def test_scores_that_vanish(q_exponent, k_exponent, D):
     put_back(c)
     q, cu, d_cu = pu.queries([300, 90], 4, D, seed=D, mult=2.0 ** q_exponent)
     run_chunk(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("first", ["small", "large"])
+def test_value_scales_apart_by_all_that_is_allowed(first):
+    """Pages whose value scales differ by 2^100, the pass beginning at either end, behind 60,000 equally weighted keys: in fp32 the
+    largest's sum in units of the smallest is infinite.  160 items, so that most are a block's from end to end."""
+    L, page, Hkv, G, D, B, n = 60000, 128, 32, 32, 64, 5, 8
+    pages = -(-L // page)
+    near, far = (2.0 ** -60, 2.0 ** 40) if first == "small" else (2.0 ** 40, 2.0 ** -60)
+    codes = torch.full((pages, Hkv, page, D), 0x7E, dtype=torch.uint8, device="cuda")  # 448
+    codes[:, :, :, 1::2] = 0xFE  # -448
+    k_pages = torch.zeros_like(codes)
+    scale = torch.full((pages, Hkv), far, device="cuda")
+    scale[-1] = near  # the pass begins with it
+    if first == "large":
+        codes[-1] = 0  # (else nothing of the others would be seen)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1).contiguous()
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+    q = torch.zeros((B * n, Hkv * G, D), dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.fa_fwd_paged_chunk(q, cu, lens, table, k_pages, codes, torch.ones_like(scale), scale)
+    # all weights alike: the mean over the keys that a row sees, of which those in the last page count for nothing
+    keys = L - n + 1 + torch.arange(n, device="cuda", dtype=torch.float64)
+    want = (448.0 * far * (pages - 1) * page / keys).repeat(B)[:, None, None] * torch.tensor([1.0, -1.0], device="cuda").double().repeat(D // 2)
+    assert bool(torch.isfinite(o).all())
+    # weights are powers of two and sums of 448 times fewer than 2^16 keys are exact, so O has its one rounding, 2^-8, and a division's
+    # and a product's in fp32
+    assert float(((o.double() - want).abs() / want.abs()).max()) <= 2.0 ** -8 + 2.0 ** -20
+    assert float((lse.double() - torch.log(keys).repeat(B)[:, None]).abs().max()) <= 2.0 ** -20 * 12
