@@ -351,21 +351,22 @@ __device__ __forceinline__ uint32_t ck_get(uint32_t addr) {
 }
 __device__ __forceinline__ void ck_put(uint32_t addr, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
 
-// A wait bounded in time.  The clock is read every 64 tries only, so that the thirty of them are a few instructions
-// each; no limit at all ends with the first try.  One that gives up raises the block's abort flag and the status word, and makes the block's others give up.
+// Raises the block's abort flag, which makes its other waits give up, and the status word.
+__device__ __forceinline__ bool ck_give_up(uint32_t abort_flag) {
+    ck_put(abort_flag, 1u);
+    atomicExch(&g_status_chunk, (int)FA_ERR_TIMEOUT);
+    return false;
+}
+// A wait bounded in time.  The clock is read every 64 tries only, so that the thirty of them are a few instructions each.
 __device__ __forceinline__ bool ck_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, uint32_t limit_us) {
     uint32_t tries = 0, since = 0;
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
         if (ck_get(abort_flag) != 0u) return false;
-        if ((++tries & 63u) == 0u || limit_us == 0u) {
+        if ((++tries & 63u) == 0u) {
             const uint32_t now = (uint32_t)(global_timer_ns() >> 10);  // about microseconds
             if (tries == 64u) since = now;
-            if (now - since > limit_us) {
-                ck_put(abort_flag, 1u);
-                atomicExch(&g_status_chunk, (int)FA_ERR_TIMEOUT);
-                return false;
-            }
+            if (now - since > limit_us) return ck_give_up(abort_flag);
         }
     }
     return true;
@@ -565,8 +566,12 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
         return ck_wait(bar(b), parity, abort_flag, limit_us);
     };
     auto wait_all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
-    // segment n of the block, once it is there
-    auto segment = [&](int n) { return wait_all(C_SEG_FULL + n % kCkSegs, (uint32_t)(n / kCkSegs) & 1u); };
+    // Segment n of the block, once it is there.  With a limit of 0 nobody waits for one, whatever has happened by then (a single
+    // try may itself wait, so that whether it fails says little; all roles come by here, and not in their loops over tiles).
+    auto segment = [&](int n) -> int {
+        if (limit_us == 0u) return ck_give_up(abort_flag);
+        return wait_all(C_SEG_FULL + n % kCkSegs, (uint32_t)(n / kCkSegs) & 1u);
+    };
     auto release = [&](int n) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C_SEG_FREE + n % kCkSegs));

@@ -140,3 +140,19 @@ def test_value_scales_apart_by_all_that_is_allowed(first):
     # and a product's in fp32
     assert float(((o.double() - want).abs() / want.abs()).max()) <= 2.0 ** -8 + 2.0 ** -20
     assert float((lse.double() - torch.log(keys).repeat(B)[:, None]).abs().max()) <= 2.0 ** -20 * 12
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,counts", [([3000, 900], [100, 70]), ([1], [1]), ([20000], [1])])
+def test_no_time_at_all(lens, counts, D):
+    """With a limit of 0 no wait is tried, so that the kernel winds down whatever the hardware's waits do, every time."""
+    c = pu.Cache(lens, 2, 32, D, seed=8)
+    q, cu, d_cu = pu.queries(counts, 8, D, seed=8)
+    o, lse = run_chunk(c, q, cu, d_cu)
+    ws = torch.empty(fa.fa_fwd_paged_chunk_workspace_bytes(len(lens), sum(counts), 8, 2, D), dtype=torch.uint8, device="cuda")
+    args = (q, d_cu, c.d_lens, c.d_table, *c.pages, torch.empty_like(o), torch.empty_like(lse), ws, D ** -0.5)
+    for _ in range(20):
+        assert fa.fa_selftest_paged_chunk_timeout(*args, 0) == fa.FA_OK
+        assert fa.fa_device_status() == fa.FA_ERR_TIMEOUT
+    o2, lse2 = run_chunk(c, q, cu, d_cu)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
