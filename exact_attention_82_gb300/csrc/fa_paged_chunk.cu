@@ -61,6 +61,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/fa.h"
 #include "fa_paged.h"
 #include "sm103_ptx.cuh"
@@ -1270,13 +1272,18 @@ size_t paged_chunk_workspace_bytes(int D, int num_sms) {
 
 template <int D>
 static cudaError_t launch_chunk(const ChunkParams &p, int num_sms, cudaStream_t stream) {
-    // With fewer registers at launch than the split counts on, the warps that ask for more would wait for ever.
-    static const bool split_holds = [] {
+    // With fewer registers at launch than the split counts on, the warps that ask for more would wait for ever.  (What was found once
+    // holds: the kernel is compiled for one architecture.  A look-up that failed says nothing of the next call's.)
+    static std::atomic<bool> split_holds{false};
+    cudaError_t e;
+    if (!split_holds.load(std::memory_order_relaxed)) {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, fa_fwd_paged_chunk_kernel<D>) == cudaSuccess && a.numRegs == kCkRegsLaunch;
-    }();
-    if (!split_holds) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(fa_fwd_paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CkCfg<D>::SMEM);
+        e = cudaFuncGetAttributes(&a, fa_fwd_paged_chunk_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs != kCkRegsLaunch) return cudaErrorLaunchOutOfResources;
+        split_holds.store(true, std::memory_order_relaxed);
+    }
+    e = cudaFuncSetAttribute(fa_fwd_paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CkCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     e = launch_early(fa_fwd_paged_chunk_kernel<D>, dim3((unsigned)num_sms), kCkThreads, CkCfg<D>::SMEM, stream, 1, p);
     if (e != cudaSuccess) return e;
