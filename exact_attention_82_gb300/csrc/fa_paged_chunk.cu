@@ -19,9 +19,9 @@
 //   units of 2^e; a tile with a scale more than 2^kCkLift units takes e up to its own, and O is rescaled, so that sums of any
 //   number of keys stay finite.
 // The powers of two are put back into c (by row and tile) and into O.  A tile with a scale that is no
-// power of two, or a value scale not within 2^-15 to 2^7 of the first tile's, goes another way: scores take
-// the rest of the key scale in fp32, and weights times the value scale go to bf16 (2^-8 of each), which has
-// the range of fp32, beside the codes themselves.
+// power of two goes another way: scores take the rest of the key scale in fp32, and so do weights that of the value scale, before
+// they go to fp16.  In one with a value scale not within 2^-15 to 2^7 units weights times the value scale go to bf16
+// (2^-8 of each), which has the range of fp32, beside the codes themselves.
 //
 // What bounds it: 4 D operations for a row and a key on the tensor cores, with enough rows
 // (256 rows share a tile of 128 keys: 2 D bytes a key for 1024 D operations); the conversion
@@ -136,7 +136,7 @@ constexpr uint32_t kSlotExp = 416;     // 4 words: e of a segment's values, behi
 constexpr uint32_t kSlotNan = 432;     // 4 words: number + 1 of a segment with NaN among masked tiles' values
 constexpr uint32_t kSlotSegs = 448;    // 4 segments of 64 bytes
 // By the tile's number modulo 16 (the softmax may be ten tiles behind what is looked up):
-constexpr uint32_t kSlotWide = 704;    // whether a tile goes the other way
+constexpr uint32_t kSlotWide = 704;    // whether a tile's weights are bf16
 constexpr uint32_t kSlotKeyExp = 768;  // 2^e of a tile's keys, negative where it goes the other way
 constexpr uint32_t kSlotRest = 832;    // what key scales are beside powers of two, and value scales, of 8 pieces: 64 bytes a tile
 // and modulo 8: flags, and 16 bytes for each 16 keys
@@ -710,7 +710,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                         }
                     }
                     const float rest = ks * ck_two_to(-ek);
-                    const bool wide = top_of_tile(there && (rest != 1.f || vs * ck_two_to(-ev) != 1.f || ev - unit > kCkUp || unit - ev > kCkDown || before != unit)) != 0;
+                    // 2: weights times value scales need bf16's range, 1: other than powers of two, or a unit that goes up
+                    const int other = top_of_tile(!there ? 0 : ev - unit > kCkUp || unit - ev > kCkDown || !(vs < INFINITY) ? 2 :
+                                                  rest != 1.f || vs * ck_two_to(-ev) != 1.f || before != unit ? 1 : 0);
+                    const bool wide = other == 2;
                     // the tiles' places in the rings
 #pragma unroll 1
                     for (int k = 0; ok && k < some; ++k)
@@ -721,15 +724,15 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                         const uint32_t row = ((uint32_t)max(ph, 0) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
                         const uint32_t kf = nan ? 0x7e007e00u : ck_f16_two_to(min(ek - e_tile, 0));
                         st_shared_v4(pieces_at(m) + i * (uint32_t)sizeof(Piece), row, there ? min(len - key, 16) : 0, kf, ck_f16_two_to(min(ev - unit, kCkUp)));
-                        if (wide) {
+                        if (other) {
                             ck_put(rest_at(m) + i * 4, __float_as_uint(rest));
-                            ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(-unit) : 1.f));
+                            ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(wide ? -unit : -ev) : 1.f));
                             if (i == 0) ck_put(lift_at(m), __float_as_uint(ck_two_to(before - unit)));
                         }
                         if (i == 0) {
                             ck_put(wide_at(m), wide);
-                            ck_put(key_exp_at(m), __float_as_uint(wide ? -ck_two_to(e_tile) : ck_two_to(e_tile)));
-                            // 1: no more tiles, 2: a row does not see some of its keys, 4: wide, 8 *: its segment
+                            ck_put(key_exp_at(m), __float_as_uint(other ? -ck_two_to(e_tile) : ck_two_to(e_tile)));
+                            // 1: no more tiles, 2: a row does not see some of its keys, 4: values as they are, 8 *: its segment
                             ck_put(flags_at(m), (end ? 1u : 0u) | (key + kCkTile > edge ? 2u : 0u) | (wide ? 4u : 0u) | (uint32_t)n << 3);
                             if (j == 0) ck_put(exp_at(n), e_ref == kNone ? 0u : (uint32_t)e_ref);  // (read when the segment's last tile is through)
                         }
@@ -1011,10 +1014,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 // (The loops of all roles have to stay in the instruction cache together, so that this
                 // one has nothing else in it.)
                 const float key_exp = __uint_as_float(ck_get(key_exp_at(tile)));  // negative: the tile goes the other way
-                const bool masked = it < plain_from, wide = key_exp < 0.f;
+                const bool masked = it < plain_from, other = key_exp < 0.f;
                 float c_tile = c_row * fabsf(key_exp);
                 int half = 0;
-                if (!(masked || wide) && ready) {
+                if (!(masked || other) && ready) {
                     uint32_t s[3][16], pk[32];
                     const float nm = kCkShift - m_used;
                     const uint64_t c2 = f2_pack(c_tile, c_tile), nm2 = f2_pack(nm, nm);
@@ -1065,7 +1068,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 auto piece = [&](int c) {
                     tmem_ld16(s_tm + c * 16, x);
                     tmem_ld_wait16(x);
-                    if (wide) {
+                    if (other) {
                         const float f = __uint_as_float(ck_get(rest_at(tile) + c * 4));
 #pragma unroll
                         for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
@@ -1088,7 +1091,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                 const float factor = m_new == -INFINITY ? 1.f : ex2_approx(m_used - m_new);  // 0 on a row's first keys
                 m_used = m_new;
                 l_run *= factor;
-                const float factor_o = wide ? factor * __uint_as_float(ck_get(lift_at(tile))) : factor;
+                const float factor_o = other ? factor * __uint_as_float(ck_get(lift_at(tile))) : factor;
                 if (half == 1) {  // the first half's product must be in O before O is rescaled
                     ok = wait_all(C_PH_DONE + t, (uint32_t)(ns - 1) & 1u);
                     if (!ok) break;
@@ -1117,11 +1120,13 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                         sum += __uint_as_float(x[e]);
                     }
                     l_run += sum;
-                    if (wide) {
+                    if (other) {
                         const float f = __uint_as_float(ck_get(rest_at(tile) + 32 + c * 4));
 #pragma unroll
                         for (int e = 0; e < 16; ++e)  // (keys that the row does not see: 0, whatever their scale)
                             x[e] = c * 16 + e >= lim ? 0u : __float_as_uint(__uint_as_float(x[e]) * f);
+                    }
+                    if (other && ck_get(wide_at(tile))) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                     } else {

@@ -143,6 +143,18 @@ def test_value_scales_apart_by_all_that_is_allowed(first):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+def test_weights_keep_their_bits_where_scales_are_no_powers_of_two(D):
+    """A quantiser that divides by its largest / 448: weights are rounded to fp16 as ever."""
+    c = pu.Cache([900, 64, 333, 5000], 2, 32, D, seed=9)
+    rng = np.random.default_rng(D)
+    c.ks *= rng.uniform(1, 2, size=c.ks.shape)
+    c.vs *= rng.uniform(1, 2, size=c.vs.shape)
+    put_back(c)
+    q, cu, d_cu = pu.queries([140, 60, 7, 20], 4, D, seed=9)
+    run_chunk(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lens,counts", [([3000, 900], [100, 70]), ([1], [1]), ([20000], [1])])
 def test_no_time_at_all(lens, counts, D):
     """With a limit of 0 no wait is tried, so that the kernel winds down whatever the hardware's waits do, every time."""
