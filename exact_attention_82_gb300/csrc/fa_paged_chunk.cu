@@ -12,15 +12,15 @@
 // Everything enters the products as fp16, which holds codes exactly (multiples of 2^-9 up to 448):
 //   q_r as bf16 scaled by a power of two to a largest element in [1, 2) (elements below 2^-17 of
 //   it are rounded, to steps of 2^-24 of it);
-//   k_j as code * 2^(e_j - e), e the largest exponent of the key scales in the tile: exactly, to
-//   2^-15 of the largest scale (steps of 2^-24 of it below);
+//   k_j as code * 2^(e_j - e), e the largest exponent of the key scales in the tile, which is exact to
+//   2^-15 of the largest scale;
 //   v_j as code * 2^(e_j - e), e the largest exponent of the value scales in the first tile that has a finite one
 //   (rows that see the tiles before it are NaN; others do not, and must not be measured by them).  O's sums are in
 //   units of 2^e; a tile with a scale more than 2^kCkLift units takes e up to its own, and O is rescaled, so that sums of any
 //   number of keys stay finite.
 // The powers of two are put back into c (by row and tile) and into O.  A tile with a scale that is no
-// power of two goes another way: scores take the rest of the key scale in fp32, and so do weights that of the value scale, before
-// they go to fp16.  In one with a value scale not within 2^-15 to 2^7 units weights times the value scale go to bf16
+// power of two, or a key scale below 2^-15 of its largest, goes another way: the codes of keys are taken as they are and scores take
+// the key scale over 2^e in fp32, and weights take the rest of the value scale in fp32, before they go to fp16.  In one with a value scale not within 2^-15 to 2^7 units weights times the value scale go to bf16
 // (2^-8 of each), which has the range of fp32, beside the codes themselves.
 //
 // What bounds it: 4 D operations for a row and a key on the tensor cores, with enough rows
@@ -81,7 +81,7 @@ constexpr int kCkSegs = 4;          // segments in the ring
 constexpr int kCkTiles = 8;         // tiles in theirs
 constexpr float kCkShift = 4.f;     // exponent of a weight at the maximum in use
 constexpr float kCkMost = 32768.f;  // of a half tile's sum
-constexpr int kCkUp = 7, kCkDown = 15;  // how far a value scale's exponent may lie above or below the first tile's
+constexpr int kCkUp = 7, kCkDown = 15;  // how far a scale's exponent may lie above or below the unit for fp16 beside codes
 constexpr int kCkLift = 40;         // how far above it takes the unit up
 constexpr unsigned long long kCkDrainNs = 20ull * 1000 * 1000;
 // Registers: 640 x 96 at launch; what the code warps and the last four give goes to the softmax.  None of
@@ -138,7 +138,7 @@ constexpr uint32_t kSlotSegs = 448;    // 4 segments of 64 bytes
 // By the tile's number modulo 16 (the softmax may be ten tiles behind what is looked up):
 constexpr uint32_t kSlotWide = 704;    // whether a tile's weights are bf16
 constexpr uint32_t kSlotKeyExp = 768;  // 2^e of a tile's keys, negative where it goes the other way
-constexpr uint32_t kSlotRest = 832;    // what key scales are beside powers of two, and value scales, of 8 pieces: 64 bytes a tile
+constexpr uint32_t kSlotRest = 832;    // what scores and weights are multiplied with in fp32, of 8 pieces: 64 bytes a tile
 // and modulo 8: flags, and 16 bytes for each 16 keys
 constexpr uint32_t kSlotFlags = 1856;
 constexpr uint32_t kSlotPieces = 2048;
@@ -709,10 +709,9 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                             if (k == j) unit = e_ref, before = last;
                         }
                     }
-                    const float rest = ks * ck_two_to(-ek);
-                    // 2: weights times value scales need bf16's range, 1: other than powers of two, or a unit that goes up
+                    // 2: weights times value scales need bf16's range, 1: other than powers of two, keys' far apart, or a unit that goes up
                     const int other = top_of_tile(!there ? 0 : ev - unit > kCkUp || unit - ev > kCkDown || !(vs < INFINITY) ? 2 :
-                                                  rest != 1.f || vs * ck_two_to(-ev) != 1.f || before != unit ? 1 : 0);
+                                                  ks * ck_two_to(-ek) != 1.f || e_tile - ek > kCkDown || vs * ck_two_to(-ev) != 1.f || before != unit ? 1 : 0);
                     const bool wide = other == 2;
                     // the tiles' places in the rings
 #pragma unroll 1
@@ -722,10 +721,10 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     const int m = tile + j;
                     if (j < some) {
                         const uint32_t row = ((uint32_t)max(ph, 0) << p.page_log2) + (key & ((1 << p.page_log2) - 1));
-                        const uint32_t kf = nan ? 0x7e007e00u : ck_f16_two_to(min(ek - e_tile, 0));
+                        const uint32_t kf = nan ? 0x7e007e00u : other ? kCkOnes : ck_f16_two_to(min(ek - e_tile, 0));
                         st_shared_v4(pieces_at(m) + i * (uint32_t)sizeof(Piece), row, there ? min(len - key, 16) : 0, kf, ck_f16_two_to(min(ev - unit, kCkUp)));
                         if (other) {
-                            ck_put(rest_at(m) + i * 4, __float_as_uint(rest));
+                            ck_put(rest_at(m) + i * 4, __float_as_uint(ks * ck_two_to(-e_tile)));
                             ck_put(rest_at(m) + 32 + i * 4, __float_as_uint(there ? vs * ck_two_to(wide ? -unit : -ev) : 1.f));
                             if (i == 0) ck_put(lift_at(m), __float_as_uint(ck_two_to(before - unit)));
                         }

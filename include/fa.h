@@ -545,13 +545,12 @@ size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  *
  * Arguments, layout, checks of what tables hold, and outputs are fa_fwd_paged's.  Scores and sums
  * are fp32.  q and K enter the products exactly (q as bf16 scaled by a power of two to fp16: elements below
- * 2^-17 of their row's largest are rounded, to steps of 2^-24 of it; K to steps of 2^-24 of the largest
- * k_scale among the same 128 keys).  Softmax weights are rounded to fp16 (each by at most 2^-11 of itself,
- * or 2^-29 of the largest among those that the row sees first, from its end; where a v_scale is no power of
- * two, the weight times what it is beside one), but weights times v_scale are rounded to bf16 (2^-8 of each) for
- * 128 keys among which a v_scale is not within 2^-15 to 2^7 of the largest that the pass began with.  O is
- * rounded once to bf16.  A scale that is not finite makes the rows that see its keys NaN or
- * infinite, and no others.
+ * 2^-17 of their row's largest are rounded, to steps of 2^-24 of it).  Softmax weights are rounded to fp16
+ * (each by at most 2^-11 of itself, or 2^-29 of the largest among those that the row sees first, from its
+ * end; where a v_scale is no power of two, the weight times what it is beside one), but weights times v_scale
+ * are rounded to bf16 (2^-8 of each) for 128 keys among which a v_scale is not within 2^-15 to 2^7 of the
+ * largest that the pass began with.  O is rounded once to bf16.  A scale that is not finite makes the rows
+ * that see its keys NaN or infinite, and no others.
  * T * Hq < 2^31, max_pages * page_size < 2^31 - 1023.  Deterministic; no atomics on results.
  *   workspace   at least fa_fwd_paged_chunk_workspace_bytes(...) bytes, as for fa_fwd_paged
  * Errors: those of fa_fwd_paged.  An on-chip wait that gives up sets FA_ERR_TIMEOUT in the status word

@@ -155,6 +155,20 @@ def test_weights_keep_their_bits_where_scales_are_no_powers_of_two(D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("spread", [16, 30, 60])
+def test_keys_keep_their_bits_beside_larger_ones(spread, D):
+    """Pages of keys 2^spread below others of the same tile, and queries that make their scores count: what a row's later keys
+    are must not show in its scores."""
+    c = pu.Cache([400, 300], 1, 16, D, seed=spread)
+    c.ks[:] = 2.0 ** (-7 - spread)
+    big = c.table[0, 22]  # keys 352 .. 367: of zeros, so that rows that see them have a score of 0 there
+    c.ks[big], c.kc[big] = 2.0 ** -7, 0
+    put_back(c)
+    q, cu, d_cu = pu.queries([120, 100], 2, D, seed=D, mult=2.0 ** spread)
+    run_chunk(c, q, cu, d_cu)
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lens,counts", [([3000, 900], [100, 70]), ([1], [1]), ([20000], [1])])
 def test_no_time_at_all(lens, counts, D):
     """With a limit of 0 no wait is tried, so that the kernel winds down whatever the hardware's waits do, every time."""
