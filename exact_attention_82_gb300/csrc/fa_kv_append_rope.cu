@@ -3,8 +3,8 @@
 //
 // The page's scale comes from the rotated keys, so a run's rows are rotated, their largest
 // magnitude taken, and only then rounded; in between they are kept in fp32, so that a key is
-// rounded once.  Values go the way of fa_kv_append (fa_kv_cache.cu), whose kernel stays apart:
-// with the rotation's instantiations beside it in one function it lost a sixth to registers.
+// rounded once.  Values go the way of fa_kv_append, by the same function (fa_kv_append.cuh); its
+// kernel (fa_kv_cache.cu) stays apart: with the rotation's instantiations beside it in one kernel it lost a sixth to registers.
 //
 // Bound by HBM: 4 bytes read and 2 written for a key and a value element, 2 and 2 for a
 // query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 64.3 us, 5,740
@@ -29,14 +29,6 @@ static __device__ int g_status_kv_append_rope = 0;
 constexpr int kRopeThreadsAnSm = 1024;  // that the kernel's registers are held to (768: 89 us for the prompt, 1536: 96, when it took 78)
 constexpr int kAppendFill = 1024;       // threads an SM, of each kind, that the windows' blocks are to make up
 
-template <int D, int PAGE, class C>
-struct AppendShared {
-    int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
-    uint32_t starts[kWindow / 32];
-    uint32_t amax[2][C::WARPS];
-    int sums[C::WARPS][D];
-};
-
 enum class Turn { none, halves, pairs };  // whether rows are rotated, and which elements make a pair
 
 // One of `share` blocks' part of the runs of a window, of heads h0 .. h0 + heads - 1 of K (kv = 0) or V; `turns`: shared memory for the
@@ -47,24 +39,15 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                                             const int win, const int part, float4 *const turns = nullptr) {
     int *const slot_of = sm.slot_of;
     uint32_t *const starts = sm.starts;
-    auto &amax_sm = sm.amax;
-    auto &sums = sm.sums;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
+    const int team = C::TEAMS == 1 ? 0 : warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
     const int t0 = win * kWindow;
     const int limit = p.num_pages * PAGE;  // fewer than 2^31
     const __nv_bfloat16 *const x_first = static_cast<const __nv_bfloat16 *>(kv ? p.x[1] : p.x[0]) + h0 * D;
     const long long stride = kv ? p.stride[1] : p.stride[0];
     float *const scale_of = kv ? p.scale[1] : p.scale[0];
     uint8_t *const pages_of = kv ? p.pages[1] : p.pages[0];
-    auto team_sync = [&]() {
-        if (C::TEAM == 1)
-            __syncwarp();
-        else if (C::TEAMS == 1 || team == 0)  // by constant numbers: a block that may mean any of the 16
-            named_bar_sync(1, C::TEAM * 32);  // barriers has them all, and few fit an SM (24.2 -> 14.3 us)
-        else
-            named_bar_sync(2, C::TEAM * 32);
-    };
+    const AppendTeam<D, PAGE, C> me{p, sm, lane, warp, team, first_warp, tt, t0};
 
     // ---- the runs that begin in the window
     for (int i = tid; i < kWindow + PAGE; i += C::THREADS) slot_of[i] = t0 + i < p.T ? p.slots[t0 + i] : -1;
@@ -107,162 +90,7 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
             if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
         }
 
-        // the largest of the team's magnitudes
-        auto join_max = [&](uint32_t am) {
-            am = __reduce_max_sync(0xffffffffu, am);
-            if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[0][warp] = am;
-                team_sync();
-#pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
-            } else {
-                team_sync();
-            }
-            return am;
-        };
-        // the page's mean of its first `rows` rows, from the warps' sums
-        auto write_mean = [&](long long ph, float scale, int rows) {
-            team_sync();
-            constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
-            int total[PER], a = 0;
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int d = tt + c * 32 * C::TEAM;
-                total[c] = 0;
-                if (d < D)
-#pragma unroll
-                    for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
-                a = max(a, abs(total[c]));
-            }
-            a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
-            if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
-                team_sync();
-#pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
-            }
-            const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
-#pragma unroll
-            for (int c = 0; c < PER; ++c) {
-                const int d = tt + c * 32 * C::TEAM;
-                if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
-            }
-            if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * rows);
-        };
-
-        // A whole page, the usual run of a prompt, does without what the ends of others need
-        // (20.9 -> 18.1 us) and always has a power of two for its scale (17.6 us).
-        auto append = [&](auto whole) {
-            constexpr bool W = decltype(whole)::value;
-            const __nv_bfloat16 *const x_of = x_first + (h - h0) * D;
-            // ---- everything that is read, at once: row r0 + i ROWS of the page in slot i
-            const int sub = tt % C::TPT, r0 = tt / C::TPT;
-            const long long ph = (long long)pg * p.Hkv + h;
-            const float was = W ? 0.f : scale_of[ph];
-            uint8_t *const codes = pages_of + ph * PAGE * D + sub * 8;
-            const __nv_bfloat16 *const x = x_of + (long long)(t0 + i0 - off) * stride + sub * 8;  // row 0's token
-            const bool mean = kv == 0 && p.mean != nullptr;
-            uint4 w[C::PASSES];
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                const int r = r0 + i * C::ROWS;
-                if (!W) w[i] = make_uint4(0, 0, 0, 0);
-                if (W || (r >= off && r < off + n)) {
-                    w[i] = __ldg(reinterpret_cast<const uint4 *>(x + r * stride));
-                } else if (mean && r < off) {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                    w[i].x = c.x, w[i].y = c.y;
-                }
-            }
-            // magnitudes of bf16 compare as integers, two at a time
-            uint32_t am2 = 0;
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                uint32_t u = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-                if (!W && r0 + i * C::ROWS < off) u = 0;
-                am2 = __vmaxu2(am2, u);
-            }
-            uint32_t am = max(am2 & 0xffffu, am2 >> 16);
-            const bool special = am >= 0x7f80u;
-            if (special) {  // infinities and NaN do not count
-                am = 0;
-#pragma unroll
-                for (int i = 0; i < C::PASSES; ++i) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
-                        if (W || r0 + i * C::ROWS >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                    }
-                }
-            }
-            am = join_max(am);
-            float scale = pow2_scale(__uint_as_float(am << 16));
-            if (!W && off > 0) scale = fmaxf(scale, was);
-            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
-            // x / scale is x * (1 / scale) exactly where the scale is a power of two (always,
-            // unless the caller put another one there; the remainder corrects it then)
-            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-            const float inv_scale = 1.f / scale, shrink = was / scale;
-            const uint16_t inv_bf16 = (uint16_t)(__float_as_uint(inv_scale) >> 16);  // exact, where it is used
-            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
-            // the codes' sums: multiples of 2^-9, at most 8 of them of at most 448 a thread, are exact in fp32
-            static_assert(C::PASSES <= 8, "");
-            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                const int r = r0 + i * C::ROWS;
-                if (!W && (r < off || r >= off + n)) continue;
-                float y[8];
-                if (W || pow2) {
-                    scaled8(w[i], inv_bf16, y);
-                } else {
-                    bf16x8(w[i], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float x = y[j];
-                        y[j] = x * inv_scale;
-                        if (fabsf(x) < INFINITY) y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
-                    }
-                }
-                const uint2 c = encode8(y);
-                *reinterpret_cast<uint2 *>(codes + r * D) = c;
-                if (mean) {
-                    add8(special ? without_nan(c) : c, sum);
-                }
-            }
-            if (!W && off > 0 && (mean || grown)) {  // apart, so that prompts' whole pages skip it
-#pragma unroll
-                for (int i = 0; i < C::PASSES; ++i) {
-                    const int r = r0 + i * C::ROWS;
-                    if (r >= off) continue;
-                    uint2 c = make_uint2(w[i].x, w[i].y);
-                    float y[8];
-                    if (grown) {
-                        if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                        decode8(c, y);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) y[j] *= shrink;
-                        c = encode8(y);
-                        *reinterpret_cast<uint2 *>(codes + r * D) = c;
-                    }
-                    decode8(without_nan(c), y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += y[j];
-                }
-            }
-            if (mean) {  // integer sums: the same in any order
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    int x = (int)(sum[j] * 512.f);
-#pragma unroll
-                    for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                    if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
-                }
-                write_mean(ph, scale, W ? PAGE : off + n);
-            }
-        };
+        const AppendRun of{i0, slot, n};
         // Rotated rows: a thread has two pieces of each of its rows, whose elements are one
         // another's partners, and keeps them in fp32 between the pass that takes the largest
         // magnitude and the one that writes codes, so that they are rounded once.
@@ -303,10 +131,10 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                 bf16x8_to_float(w[i][1], y[i] + 8);
                 if (turned) {
                     float2 f[8];
-                    const float4 *const of = turns + (r - off) * (p.rot / 4) + sub;
+                    const float4 *const from = turns + (r - off) * (p.rot / 4) + sub;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 two = of[j * (p.rot / 16)];
+                        const float4 two = from[j * (p.rot / 16)];
                         f[2 * j] = make_float2(two.x, two.y), f[2 * j + 1] = make_float2(two.z, two.w);
                     }
                     rope_turn16<TURN == Turn::pairs>(y[i], f);
@@ -317,7 +145,7 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                     am = max(am, u < 0x7f800000u ? u : 0u);
                 }
             }
-            float scale = pow2_scale(__uint_as_float(join_max(am)));
+            float scale = pow2_scale(__uint_as_float(me.join_max(am)));
             if (!W && off > 0) scale = fmaxf(scale, was);
             if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
             const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
@@ -373,9 +201,9 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                         int x = (int)(sum[c][j] * 512.f);
 #pragma unroll
                         for (int d = TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                        if (lane < TPT) sums[warp][8 * (c ? piece.y : piece.x) + j] = x;
+                        if (lane < TPT) sm.sums[warp][8 * (c ? piece.y : piece.x) + j] = x;
                     }
-                write_mean(ph, scale, W ? PAGE : off + n);
+                me.write_mean(ph, scale, W ? PAGE : off + n);
             }
         };
         if constexpr (TURN != Turn::none) {
@@ -387,7 +215,7 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                 const float2 f = rope_factor(__ldg(p.phases + pair), __ldg(p.positions + t0 + i0 + r), p.amplitude);
                 reinterpret_cast<float2 *>(turns)[2 * (r * (p.rot / 4) + (pair >> 1 & 3) * (p.rot / 16) + (pair >> 3)) + (pair & 1)] = f;
             }
-            team_sync();
+            me.sync();
         }
 #pragma unroll 1
         do {
@@ -397,12 +225,13 @@ __device__ __forceinline__ void append_runs(const AppendParams &p, const int sha
                 else
                     append_turned(std::false_type());
             } else {
+                const __nv_bfloat16 *const x_of = x_first + (h - h0) * D;
                 if (n == PAGE)
-                    append(std::true_type());
+                    me.template append<true, false>(of, h, false, x_of, stride, pages_of, scale_of);
                 else
-                    append(std::false_type());
+                    me.template append<false, false>(of, h, false, x_of, stride, pages_of, scale_of);
             }
-            team_sync();  // the next run overwrites the shared words
+            me.sync();  // the next run overwrites the shared words
         } while (++h < h1);
     }
 }

@@ -192,10 +192,9 @@ template <int D, int PAGE>
 __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE>::BLOCKS) fa_kv_append_kernel(const __grid_constant__ AppendParams p, int share) {
     using C = AppendCfg<D, PAGE>;
     grid_wait();
-    __shared__ int slot_of[kWindow + PAGE];   // the window's slots and those that its last run may reach
-    __shared__ uint32_t starts[kWindow / 32];
-    __shared__ uint32_t amax_sm[2][C::WARPS];
-    __shared__ int sums[C::WARPS][D];
+    __shared__ AppendShared<D, PAGE, C> sm;
+    int *const slot_of = sm.slot_of;
+    uint32_t *const starts = sm.starts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int team = warp / C::TEAM, first_warp = team * C::TEAM, tt = tid - first_warp * 32;
     const int h = blockIdx.y, kv = blockIdx.z;
@@ -206,14 +205,7 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
     const long long stride = kv ? p.stride[1] : p.stride[0];
     float *const scale_of = kv ? p.scale[1] : p.scale[0];
     uint8_t *const pages_of = kv ? p.pages[1] : p.pages[0];
-    auto team_sync = [&]() {
-        if (C::TEAM == 1)
-            __syncwarp();
-        else if (C::TEAMS == 1 || team == 0)  // by constant numbers: a block that may mean any of the 16
-            named_bar_sync(1, C::TEAM * 32);  // barriers has them all, and few fit an SM (24.2 -> 14.3 us)
-        else
-            named_bar_sync(2, C::TEAM * 32);
-    };
+    const AppendTeam<D, PAGE, C> me{p, sm, lane, warp, team, first_warp, tt, t0};
 
     // ---- the runs that begin in the window
     for (int i = tid; i < kWindow + PAGE; i += C::THREADS) slot_of[i] = t0 + i < p.T ? p.slots[t0 + i] : -1;
@@ -235,7 +227,7 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
     for (int run = part * C::TEAMS + team; run < runs; run += share * C::TEAMS) {
         const uint32_t m0 = __ballot_sync(0xffffffffu, rank0 == run), m1 = __ballot_sync(0xffffffffu, rank1 == run);
         const int i0 = m0 ? __ffs((int)m0) - 1 : 31 + __ffs((int)m1);
-        const int slot = slot_of[i0], off = slot % PAGE, pg = slot / PAGE;
+        const int slot = slot_of[i0], off = slot % PAGE;
         int n = 0;  // tokens of the run
 #pragma unroll
         for (int w = 0; w < (PAGE + 31) / 32; ++w) {
@@ -244,156 +236,12 @@ __global__ void __launch_bounds__(AppendCfg<D, PAGE>::THREADS, AppendCfg<D, PAGE
             if (n == 32 * w) n += m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
         }
 
-        // A whole page, the usual run of a prompt, does without what the ends of others need
-        // (20.9 -> 18.1 us) and always has a power of two for its scale (17.6 us).
-        auto append = [&](auto whole) {
-            constexpr bool W = decltype(whole)::value;
-            // ---- everything that is read, at once: row r0 + i ROWS of the page in slot i
-            const int sub = tt % C::TPT, r0 = tt / C::TPT;
-            const long long ph = (long long)pg * p.Hkv + h;
-            const float was = W ? 0.f : scale_of[ph];
-            uint8_t *const codes = pages_of + ph * PAGE * D + sub * 8;
-            const __nv_bfloat16 *const x = x_of + (long long)(t0 + i0 - off) * stride + sub * 8;  // row 0's token
-            const bool mean = kv == 0 && p.mean != nullptr;
-            uint4 w[C::PASSES];
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                const int r = r0 + i * C::ROWS;
-                if (!W) w[i] = make_uint4(0, 0, 0, 0);
-                if (W || (r >= off && r < off + n)) {
-                    w[i] = __ldg(reinterpret_cast<const uint4 *>(x + r * stride));
-                } else if (mean && r < off) {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                    w[i].x = c.x, w[i].y = c.y;
-                }
-            }
-            // magnitudes of bf16 compare as integers, two at a time
-            uint32_t am2 = 0;
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                uint32_t u = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                      __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-                if (!W && r0 + i * C::ROWS < off) u = 0;
-                am2 = __vmaxu2(am2, u);
-            }
-            uint32_t am = max(am2 & 0xffffu, am2 >> 16);
-            const bool special = am >= 0x7f80u;
-            if (special) {  // infinities and NaN do not count
-                am = 0;
-#pragma unroll
-                for (int i = 0; i < C::PASSES; ++i) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t lo = u[c] & 0x7fffu, hi = (u[c] >> 16) & 0x7fffu;
-                        if (W || r0 + i * C::ROWS >= off) am = max(am, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-                    }
-                }
-            }
-            am = __reduce_max_sync(0xffffffffu, am);
-            if (C::TEAM > 1) {
-                if (lane == 0) amax_sm[0][warp] = am;
-                team_sync();
-#pragma unroll
-                for (int v = 0; v < C::TEAM; ++v) am = max(am, amax_sm[0][first_warp + v]);
-            } else {
-                team_sync();
-            }
-            float scale = pow2_scale(__uint_as_float(am << 16));
-            if (!W && off > 0) scale = fmaxf(scale, was);
-            if (tt == 0) scale_of[ph] = scale;  // every thread has read it (the barrier above)
-            // x / scale is x * (1 / scale) exactly where the scale is a power of two (always,
-            // unless the caller put another one there; the remainder corrects it then)
-            const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
-            const float inv_scale = 1.f / scale, shrink = was / scale;
-            const uint16_t inv_bf16 = (uint16_t)(__float_as_uint(inv_scale) >> 16);  // exact, where it is used
-            const bool grown = !W && off > 0 && scale != was;  // the rows before the run are rounded again
-            // the codes' sums: multiples of 2^-9, at most 8 of them of at most 448 a thread, are exact in fp32
-            static_assert(C::PASSES <= 8, "");
-            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < C::PASSES; ++i) {
-                const int r = r0 + i * C::ROWS;
-                if (!W && (r < off || r >= off + n)) continue;
-                float y[8];
-                if (W || pow2) {
-                    scaled8(w[i], inv_bf16, y);
-                } else {
-                    bf16x8(w[i], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float x = y[j];
-                        y[j] = x * inv_scale;
-                        if (fabsf(x) < INFINITY) y[j] = fmaf(fmaf(-y[j], scale, x), inv_scale, y[j]);
-                    }
-                }
-                const uint2 c = encode8(y);
-                *reinterpret_cast<uint2 *>(codes + r * D) = c;
-                if (mean) {
-                    add8(special ? without_nan(c) : c, sum);
-                }
-            }
-            if (!W && off > 0 && (mean || grown)) {  // apart, so that prompts' whole pages skip it
-#pragma unroll
-                for (int i = 0; i < C::PASSES; ++i) {
-                    const int r = r0 + i * C::ROWS;
-                    if (r >= off) continue;
-                    uint2 c = make_uint2(w[i].x, w[i].y);
-                    float y[8];
-                    if (grown) {
-                        if (!mean) c = *reinterpret_cast<const uint2 *>(codes + r * D);
-                        decode8(c, y);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) y[j] *= shrink;
-                        c = encode8(y);
-                        *reinterpret_cast<uint2 *>(codes + r * D) = c;
-                    }
-                    decode8(without_nan(c), y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += y[j];
-                }
-            }
-            if (mean) {  // integer sums: the same in any order
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    int x = (int)(sum[j] * 512.f);
-#pragma unroll
-                    for (int d = C::TPT; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                    if (lane < C::TPT) sums[warp][lane * 8 + j] = x;
-                }
-                team_sync();
-                constexpr int PER = D > 32 * C::TEAM ? D / (32 * C::TEAM) : 1;  // columns a thread
-                int total[PER], a = 0;
-#pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    const int d = tt + c * 32 * C::TEAM;
-                    total[c] = 0;
-                    if (d < D)
-#pragma unroll
-                        for (int v = 0; v < C::TEAM; ++v) total[c] += sums[first_warp + v][d];
-                    a = max(a, abs(total[c]));
-                }
-                a = (int)__reduce_max_sync(0xffffffffu, (unsigned)a);
-                if (C::TEAM > 1) {
-                    if (lane == 0) amax_sm[1][warp] = (uint32_t)a;
-                    team_sync();
-#pragma unroll
-                    for (int v = 0; v < C::TEAM; ++v) a = max(a, (int)amax_sm[1][first_warp + v]);
-                }
-                const float af = (float)a, inv = a > 0 ? 127.f / af : 0.f;
-#pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    const int d = tt + c * 32 * C::TEAM;
-                    if (d < D) p.mean[ph * D + d] = (int8_t)__float2int_rn((float)total[c] * inv);
-                }
-                if (tt == 0) p.mean_scale[ph] = (af * (scale * 0.001953125f)) / (float)(127 * (W ? PAGE : off + n));
-            }
-        };
+        const AppendRun of{i0, slot, n};
         if (n == PAGE)
-            append(std::true_type());
+            me.template append<true, true>(of, h, kv == 0, x_of, stride, pages_of, scale_of);
         else
-            append(std::false_type());
-        team_sync();  // the next run overwrites the shared words
+            me.template append<false, true>(of, h, kv == 0, x_of, stride, pages_of, scale_of);
+        me.sync();  // the next run overwrites the shared words
     }
 }
 
