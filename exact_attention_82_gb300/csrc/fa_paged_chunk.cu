@@ -62,6 +62,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "fa_paged.h"
@@ -1060,86 +1061,97 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
                     tmem_ld_wait16(s[2]);
                 }
                 const int lim = limit_of_row() - (CK_SEG(g, t1) - 1 - it) * kCkTile;
-                // ---- the others, or the second half of one: the maximum first, then P, 16 keys at a time
+                // ---- the others, or the second half of one: the maximum first, then P, 16 keys at a time.  Tiles that go the other
+                // way have this code to themselves (with both in one, branches at every 16 keys: prompts 301 us instead of 295, and 697 instead
+                // of 518 with scales that are no powers of two).
                 // (A factor of 0 would make NaN of masked keys' -infinity.  The sum is another than c_tile only where scores are 0 either way.)
                 c_tile += FLT_MIN;
-                uint32_t x[16];
-                auto piece = [&](int c) {
-                    tmem_ld16(s_tm + c * 16, x);
-                    tmem_ld_wait16(x);
-                    if (other) {
-                        const float f = __uint_as_float(ck_get(rest_at(tile) + c * 4));
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c * 16 + e >= lim) x[e] = __float_as_uint(-INFINITY);
-                    }
-                };
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int c = 4 * half; c < 8; ++c) {
-                    piece(c);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) top = max3f(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                }
-                const float m_new = fmaxf(m_used, top * c_tile);
-                ready = __all_sync(0xffffffffu, m_new != -INFINITY);
-                const float factor = m_new == -INFINITY ? 1.f : ex2_approx(m_used - m_new);  // 0 on a row's first keys
-                m_used = m_new;
-                l_run *= factor;
-                const float factor_o = other ? factor * __uint_as_float(ck_get(lift_at(tile))) : factor;
-                if (half == 1) {  // the first half's product must be in O before O is rescaled
-                    ok = wait_all(C_PH_DONE + t, (uint32_t)(ns - 1) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                if ((half == 1 || it > first) && __any_sync(0xffffffffu, factor_o != 1.f)) {  // O holds what came before at the old maximum and in the old unit
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        tmem_ld16(o_tm + c * 16, x);
+                auto slowly = [&](auto tag) {
+                    constexpr bool OTHER = decltype(tag)::value;
+                    uint32_t x[16];
+                    auto piece = [&](int c) {
+                        tmem_ld16(s_tm + c * 16, x);
                         tmem_ld_wait16(x);
+                        if constexpr (OTHER) {
+                            const float f = __uint_as_float(ck_get(rest_at(tile) + c * 4));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor_o);
-                        tmem_st16(o_tm + c * 16, x);
-                        tmem_st_wait16(x);
-                    }
-                }
-                const float nm = m_used == -INFINITY ? 0.f : kCkShift - m_used;  // no key yet: p = 0
+                            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (c * 16 + e >= lim) x[e] = __float_as_uint(-INFINITY);
+                        }
+                    };
+                    float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 4 * half; c < 8; ++c) {
-                    piece(c);
-                    uint32_t y[8];
-                    float sum = 0.f;
+                    for (int c = OTHER ? 0 : 4 * half; c < 8; ++c) {
+                        piece(c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c_tile, nm)));
-                        sum += __uint_as_float(x[e]);
+                        for (int e = 0; e < 16; e += 2) top = max3f(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                     }
-                    l_run += sum;
-                    if (other) {
-                        const float f = __uint_as_float(ck_get(rest_at(tile) + 32 + c * 4));
+                    const float m_new = fmaxf(m_used, top * c_tile);
+                    ready = __all_sync(0xffffffffu, m_new != -INFINITY);
+                    const float factor = m_new == -INFINITY ? 1.f : ex2_approx(m_used - m_new);  // 0 on a row's first keys
+                    m_used = m_new;
+                    l_run *= factor;
+                    const float factor_o = OTHER ? factor * __uint_as_float(ck_get(lift_at(tile))) : factor;
+                    if (!OTHER && half == 1) {  // the first half's product must be in O before O is rescaled
+                        ok = wait_all(C_PH_DONE + t, (uint32_t)(ns - 1) & 1u);
+                        if (!ok) return false;
+                        tc_fence_after();
+                    }
+                    if (((!OTHER && half == 1) || it > first) && __any_sync(0xffffffffu, factor_o != 1.f)) {  // O holds what came before at the old maximum and in the old unit
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            tmem_ld16(o_tm + c * 16, x);
+                            tmem_ld_wait16(x);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)  // (keys that the row does not see: 0, whatever their scale)
-                            x[e] = c * 16 + e >= lim ? 0u : __float_as_uint(__uint_as_float(x[e]) * f);
+                            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor_o);
+                            tmem_st16(o_tm + c * 16, x);
+                            tmem_st_wait16(x);
+                        }
                     }
-                    if (other && ck_get(wide_at(tile))) {
+                    const float nm = m_used == -INFINITY ? 0.f : kCkShift - m_used;  // no key yet: p = 0
+#pragma unroll 1
+                    for (int c = OTHER ? 0 : 4 * half; c < 8; ++c) {
+                        piece(c);
+                        uint32_t y[8];
+                        float sum = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                    } else {
+                        for (int e = 0; e < 16; ++e) {
+                            x[e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(x[e]), c_tile, nm)));
+                            sum += __uint_as_float(x[e]);
+                        }
+                        l_run += sum;
+                        if constexpr (OTHER) {
+                            const float f = __uint_as_float(ck_get(rest_at(tile) + 32 + c * 4));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = ck_pack_f16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                            if (!(fabsf(f) < INFINITY)) {  // keys that the row does not see: 0, whatever their scale
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (c * 16 + e >= lim) x[e] = 0u;
+                            }
+                        }
+                        if (OTHER && ck_get(wide_at(tile))) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = ck_pack_f16(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                        }
+                        ck_tmem_st8(s_tm + c * 8, y);  // (over scores that are read already)
+                        if (c == 3) {
+                            tc_fence_before();
+                            mbar_arrive(bar(C_P_HALF + t));
+                        }
                     }
-                    ck_tmem_st8(s_tm + c * 8, y);  // (over scores that are read already)
-                    if (c == 3) {
-                        tc_fence_before();
-                        mbar_arrive(bar(C_P_HALF + t));
-                    }
-                }
-                tc_fence_before();
-                mbar_arrive(bar(C_P_FULL + t));
+                    tc_fence_before();
+                    mbar_arrive(bar(C_P_FULL + t));
+                    return true;
+                };
+                if (!(other ? slowly(std::true_type()) : slowly(std::false_type()))) break;
             }
             if (!ok) break;
             c_next = load_query(n + 1);  // so that the next segment's first S runs beside what follows
