@@ -7,11 +7,13 @@
 // kernel (fa_kv_cache.cu) stays apart: with the rotation's instantiations beside it in one kernel it lost a sixth to registers.
 //
 // Bound by HBM: 4 bytes read and 2 written for a key and a value element, 2 and 2 for a
-// query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 64.3 us, 5,740
-// GB/s (85% of the copy rate); the queries alone take 44.  Keys alone take 33: a team waits
+// query's.  A prompt of 16384 tokens, 8 heads of keys, 32 of queries, D = 128: 62.3 us, 5,920
+// GB/s (87% of the copy rate), with means 63.6; without queries 28.8, where fa_kv_append takes 17.4: a team waits
 // for memory, for the largest magnitude of the page and to be written, head after head, and a quarter
-// of it is sines and cosines.  (A head's rows asked for while the one before is written: no gain.)
-// 64 single tokens 5.7 us, 256 15.6 us.
+// of the keys' time is sines and cosines.  (A head's rows asked for while the one before is written: no gain.)
+// 64 single tokens 5.5 us (with means 7.6), 256 14.4 us.  16 ragged prompts of 30 to 1000 tokens, 32 heads, D = 64, pages of 16: 21.2 us
+// (with means 28.6), where fa_kv_append takes 12.8 on the same runs: the values' path has the registers of the rotation's kernel here, and so fewer
+// threads, and every instantiation spills 208 to 424 bytes.
 #include <math.h>
 
 #include <algorithm>
@@ -310,6 +312,8 @@ static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaSt
     if (!even) {
         // With a window for each SM the tokens are prompts': groups of heads, as many as fill the chip, and no more blocks than a prompt's
         // window has runs for (others would find none: 16384 tokens, 8 and 32 heads, D = 128, pages of 64 70.6 -> 64.9 us, of 128 83.9 -> 73.2).
+        // Many short runs instead are a block's one after another: 4,096 sequences of three tokens 245 us, shared out as below 235; the
+        // prompt of 16384 62.4 and 67.7.
         constexpr int prompt = std::max(1, (kWindow / PAGE + (C::TEAMS > 1 ? C::TEAMS : 0)) / C::TEAMS);
         groups = std::min((kAppendFill / C::THREADS * num_sms + windows - 1) / windows, p.Hkv);
         per = (p.Hkv + groups - 1) / groups;
@@ -318,7 +322,7 @@ static cudaError_t launch_append_rope(const AppendParams &p, int num_sms, cudaSt
         if (p.q) q_tokens = prompt, q_groups = 1;
     } else {
         // Fewer may be of single tokens, each a run, or of prompts: shared out evenly.  (With groups of heads, as above, of whose
-        // blocks many have no run, 256 single tokens of 8 heads, queries of 32, took 23.3 us for 15.6, a prompt of 700 18.6 for 9.5.)  Teams that are a whole
+        // blocks many have no run, 256 single tokens of 8 heads, queries of 32, took 23.3 us for 15.6, a prompt of 700 18.6 for 9.5; now 14.4 and 8.1.)  Teams that are a whole
         // block do better with half of the threads (64 single tokens 7.9 -> 6.5), those of a warp with all (the ragged prompts 24.2 -> 21.4).
         const int tokens = std::min(p.T, kWindow), fill = ((C::TEAMS > 1 ? kAppendFill : kAppendFill / 2) / C::THREADS * num_sms + windows - 1) / windows;
         constexpr int at_once = C::THREADS / (D / 16);

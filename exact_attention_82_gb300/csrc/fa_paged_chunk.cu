@@ -48,11 +48,13 @@
 //
 // Every wait is bounded in time; one that gives up records a status code and the block winds down.
 //
-// Measured, D = 128: 1024 tokens behind 65536, 8 of 32 heads 810 us, 1,368 TFLOP/s (71% of the measured bf16 rate); 512 behind
-// 16384 128 us, 57%; 4 prompts of 4096, 16 heads 296 us, 48%; 32 sequences of 1 to 1024 tokens behind 50 to 8000, 8 of 64 heads, pages
-// of 16 567 us, 46%.  A tile takes 3,260 cycles, of which the tensor pipe has work for 2,140 and the exponentials take
-// 2,050; the rest is the way from S through the softmax to the next S.  An item's ends cost four to five tiles more, the cut and first
-// tile 6 to 11 us, the join 2.5 to 6.
+// Measured, D = 128: 1024 tokens behind 65536, 8 of 32 heads 770 to 800 us, 1,440 to 1,385 TFLOP/s (75 to 72% of the measured bf16 rate); 512 behind
+// 16384 129 us, 56%; 4 prompts of 4096, 16 heads 295 us, 48%; 32 sequences of 1 to 1024 tokens behind 50 to 8000, 8 of 64 heads, pages
+// of 16 570 us, 46%.  D = 64: 4 prompts of 2048, 16 heads 86 to 92 us, a fifth of the rate.  A tile takes 3,160 to 3,500 cycles, of which the tensor pipe has
+// work for 2,050 (64 for each of 32 steps) and the exponentials take 1,024 (32 a cycle, measured); the rest is the way from S
+// through the softmax to the next S: 1,630 cycles from S to the second half of P, 1,070 more until the softmax waits for the next S no longer.  (A copy
+// with a multiply-add in the place of each exponential was no faster.)  An item's ends cost four to five tiles more, the cut and first
+// tile 6 to 11 us, the join 2.5 to 7.  Where scales are no powers of two every tile takes its maximum again: 1.8 to 2.0 times these times.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -76,7 +78,7 @@ constexpr int kCkThreads = 640;
 constexpr int kCkCodeWarps = 8;
 constexpr int kCkRows = 256;        // rows of an item, two sub-tiles of 128
 constexpr int kCkTile = 128;        // keys a tile
-constexpr int kCkFixed = 576;       // keys that an item's fixed cost stands for (512: the mixed batch above 582 us instead of 567; 640: the prompts 303 instead of 296)
+constexpr int kCkFixed = 576;       // keys that an item's fixed cost stands for (512: the mixed batch above 582 us when this took 567; 640: the prompts 303 when this took 296)
 constexpr int kCkMinShare = 768;    // of a block, in keys
 constexpr int kCkSegs = 4;          // segments in the ring
 constexpr int kCkTiles = 8;         // tiles in theirs
@@ -86,7 +88,7 @@ constexpr int kCkUp = 7, kCkDown = 15;  // how far a scale's exponent may lie ab
 constexpr int kCkLift = 40;         // how far above it takes the unit up
 constexpr unsigned long long kCkDrainNs = 20ull * 1000 * 1000;
 // Registers: 640 x 96 at launch; what the code warps and the last four give goes to the softmax.  None of
-// the loops may spill: beside this much shared memory the cache that holds spilled registers is small, and
+// the loops may spill much (D = 128 does not, D = 64 a word): beside this much shared memory the cache that holds spilled registers is small, and
 // they would come from the L2.  (The launch checks that the kernel has as many as the split assumes.)
 constexpr int kCkRegsLaunch = 96;
 constexpr uint32_t kCkRegsSoftmax = 144, kCkRegsCodes = 64, kCkRegsOther = 64;
