@@ -20,7 +20,8 @@
 //   number of keys stay finite.
 // The powers of two are put back into c (by row and tile) and into O.  A tile with a scale that is no
 // power of two, or a key scale below 2^-15 of its largest, goes another way: the codes of keys are taken as they are and scores take
-// the key scale over 2^e in fp32, and weights take the rest of the value scale in fp32, before they go to fp16.  In one with a value scale not within 2^-15 to 2^7 units weights times the value scale go to bf16
+// the key scale over 2^e in fp32, and weights take the rest of the value scale in fp32, before they go to fp16.
+// In one with a value scale not within 2^-15 to 2^7 units weights times the value scale go to bf16
 // (2^-8 of each), which has the range of fp32, beside the codes themselves.
 //
 // What bounds it: 4 D operations for a row and a key on the tensor cores, with enough rows
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) fa_fwd_paged_chunk_kernel(const
             const long long share = share_sm;
             // Both cuts before the same tile inside an item (the line weighs rows that see no key too, so that a share may be less
             // than a tile): the join counts this block's part all the same, and is to find that it holds nothing.
-            if (at.begin == end.begin && at.done > 0 && at.done == end.done)
+            if (at.begin == end.begin && at.begin != LLONG_MAX && at.done > 0 && at.done == end.done)
                 for (int r = lane; r < kCkRows; r += 32) ck_slot(p.ws, gridDim.x, blockIdx.x, 0, D)[(size_t)kCkRows * (D + 1) + r] = 0.f;
             bool ok = true;
             for (int n = 0; ok; ++n) {

@@ -549,8 +549,8 @@ size_t fa_fwd_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D);
  * (each by at most 2^-11 of itself, or 2^-29 of the largest among those that the row sees first, from its
  * end; where a v_scale is no power of two, the weight times what it is beside one), but weights times v_scale
  * are rounded to bf16 (2^-8 of each) for 128 keys among which a v_scale is not within 2^-15 to 2^7 of the
- * largest that the pass began with.  O is rounded once to bf16.  A scale that is not finite makes the rows
- * that see its keys NaN or infinite, and no others.
+ * largest that the pass began with (or met since, more than 2^40 above it).  O is rounded once to bf16.  A
+ * scale that is not finite makes the rows that see its keys NaN or infinite, and no others.
  * T * Hq < 2^31, max_pages * page_size < 2^31 - 1023.  Deterministic; no atomics on results.
  *   workspace   at least fa_fwd_paged_chunk_workspace_bytes(...) bytes, as for fa_fwd_paged
  * Errors: those of fa_fwd_paged.  An on-chip wait that gives up sets FA_ERR_TIMEOUT in the status word
@@ -649,7 +649,7 @@ int fa_selftest_splitkv_timeout(const void *q, const void *k, const void *v, voi
 /*
  * fa_selftest_paged_chunk_timeout -- fa_fwd_paged_chunk with every on-chip wait bounded by `timeout_ns`
  * (0 .. 2e9, counted in microseconds) instead of 2 s.  With a limit shorter than the first tile's way
- * through the kernel its own give-up path runs, as for fa_selftest_fwd_timeout: the block's abort flag is
+ * through the kernel, and always with 0, its own give-up path runs, as for fa_selftest_fwd_timeout: the block's abort flag is
  * raised and FA_ERR_TIMEOUT recorded in the status word, the other roles stop at their next wait, MMAs in
  * flight are waited for (bounded), TMEM is freed and the block returns.  O and LSE are then undefined.
  * Arguments, checks and errors are fa_fwd_paged_chunk's, plus FA_ERR_BAD_SHAPE for timeout_ns above 2e9.
